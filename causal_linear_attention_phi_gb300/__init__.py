@@ -19,12 +19,15 @@ from . import build as _build
 
 __all__ = [
     "LaError", "noncausal_fwd", "noncausal_bwd", "causal_fwd", "causal_bwd", "causal_step_host", "host_step_bytes",
-    "recurrent_step", "retention_fwd", "retention_step", "selftest_bounded_wait", "workspace_bytes",
+    "recurrent_step", "retention_fwd", "retention_step", "gated_delta_fwd", "gated_delta_bwd", "gated_delta_step",
+    "layer_norm_fwd", "layer_norm_bwd", "layer_norm_workspace_bytes", "selftest_bounded_wait", "workspace_bytes",
     "last_error", "clear_error", "timing_enable", "timing_reset", "timing_read", "library", "version",
     "OP_NONCAUSAL_FWD", "OP_CAUSAL_FWD", "OP_CAUSAL_BWD", "OP_NONCAUSAL_BWD", "OP_RETENTION_FWD",
+    "OP_GATED_DELTA_FWD", "OP_GATED_DELTA_BWD",
 ]
 
 OP_NONCAUSAL_FWD, OP_CAUSAL_FWD, OP_CAUSAL_BWD, OP_NONCAUSAL_BWD, OP_RETENTION_FWD = 0, 1, 2, 3, 4
+OP_GATED_DELTA_FWD, OP_GATED_DELTA_BWD = 5, 6
 LA_F32, LA_BF16 = 0, 1
 _STATUS = {0: "LA_OK", 1: "LA_ERR_INVALID_ARG", 2: "LA_ERR_UNSUPPORTED", 3: "LA_ERR_WORKSPACE",
            4: "LA_ERR_CUDA", 5: "LA_ERR_TIMEOUT", 6: "LA_ERR_BOUNDS"}
@@ -40,6 +43,10 @@ class LaError(RuntimeError):
 class Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("N", ctypes.c_int), ("Dk", ctypes.c_int),
                 ("Dv", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("C", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
 class KernelTime(ctypes.Structure):
@@ -67,11 +74,19 @@ def _declare(lib):
     lib.la_recurrent_step.argtypes = [_vp] * 6 + [Shape, _vp]
     lib.la_retention_fwd.argtypes = [_vp] * 6 + [Shape, _vp, ctypes.c_size_t, _vp]
     lib.la_retention_step.argtypes = [_vp] * 6 + [Shape, _vp]
+    lib.la_gated_delta_fwd.argtypes = [_vp] * 8 + [Shape, _vp, ctypes.c_size_t, _vp]
+    lib.la_gated_delta_bwd.argtypes = [_vp] * 11 + [Shape, _vp, ctypes.c_size_t, _vp]
+    lib.la_gated_delta_step.argtypes = [_vp] * 7 + [Shape, _vp]
+    lib.la_layer_norm_fwd.argtypes = [_vp] * 6 + [NormShape, ctypes.c_float, _vp]
+    lib.la_layer_norm_workspace_bytes.argtypes = [NormShape]
+    lib.la_layer_norm_workspace_bytes.restype = ctypes.c_size_t
+    lib.la_layer_norm_bwd.argtypes = [_vp] * 8 + [NormShape, _vp, ctypes.c_size_t, _vp]
     lib.la_selftest_bounded_wait.argtypes = [_vp]
     lib.la_selftest_lookback_timeout.argtypes = [_vp] * 4 + [Shape, _vp, ctypes.c_size_t, _vp]
     for f in ("la_causal_step_host", "la_noncausal_fwd", "la_noncausal_bwd", "la_causal_fwd",
               "la_causal_fwd_with_state", "la_causal_bwd", "la_causal_bwd_after_fwd", "la_recurrent_step",
-              "la_retention_fwd", "la_retention_step", "la_selftest_bounded_wait", "la_selftest_lookback_timeout",
+              "la_retention_fwd", "la_retention_step", "la_gated_delta_fwd", "la_gated_delta_bwd",
+              "la_gated_delta_step", "la_layer_norm_fwd", "la_layer_norm_bwd", "la_selftest_bounded_wait", "la_selftest_lookback_timeout",
               "la_last_error", "la_causal_fwd_fused",
               "la_clear_error", "la_timing_enable", "la_timing_reset"):
         getattr(lib, f).restype = ctypes.c_int
@@ -341,6 +356,163 @@ def retention_step(q, k, v, gamma, S, out=None, stream=None):
     _check(library().la_retention_step(_ptr(q), _ptr(k), _ptr(v), _ptr(gamma), _ptr(S), _ptr(out), s,
                                        _stream_ptr(stream)), "la_retention_step")
     return out
+
+
+def _result(t, like, what):
+    """A caller's output tensor, checked against what it receives; a new one if None."""
+    if t is None:
+        return torch.empty_like(like)
+    _need_cuda(t)
+    if t.shape != like.shape or t.dtype != like.dtype:
+        raise ValueError("%s must be %s of shape %s" % (what, like.dtype, tuple(like.shape)))
+    return t
+
+
+def _gates(g, beta, lead, dtype):
+    _need_cuda(g, beta)
+    if g.shape != lead or beta.shape != lead or g.dtype != dtype or beta.dtype != dtype:
+        raise ValueError("g and beta must be %s of the dtype of q" % ("[B,H,N]" if len(lead) == 3 else "[B,H]"))
+
+
+def _state(S, B, H, Dk, Dv, what):
+    _need_cuda(S)
+    if S.dtype != torch.float32 or S.shape != (B, H, Dk, Dv):
+        raise ValueError("%s must be fp32 [B,H,Dk,Dv]" % what)
+
+
+def gated_delta_fwd(q, k, v, g, beta, S0=None, out=None, workspace=None, stream=None, return_state=False):
+    """The gated delta rule: S_t = a_t S_(t-1) + k_t u_t^T with a_t = exp(g_t) and
+    u_t = beta_t (v_t - a_t S_(t-1)^T k_t); returns o_t = S_t^T q_t, [B,H,N,Dv].
+
+    q, k [B,H,N,Dk], v [B,H,N,Dv], g (log decays) and beta (write strengths) [B,H,N], one dtype.  A g of
+    -inf starts the state anew (packed sequences).  S0: the fp32 [B,H,Dk,Dv] state before the first
+    position (zero if None).  With return_state, returns (o, S): the fp32 state after the last position, from
+    which gated_delta_step or another gated_delta_fwd continues.
+    """
+    _need_cuda(q, k, v)
+    s = _shape4(q, k, v)
+    B, H, N, Dk = q.shape
+    _gates(g, beta, (B, H, N), q.dtype)
+    if S0 is not None:
+        _state(S0, B, H, Dk, s.Dv, "S0")
+    out = _result(out, v, "out")
+    S = torch.empty(B, H, Dk, s.Dv, dtype=torch.float32, device=q.device) if return_state else None
+    ws, nb = _workspace(OP_GATED_DELTA_FWD, s, q.device, workspace)
+    _check(library().la_gated_delta_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(out), _ptr(S),
+                                        s, _ptr(ws), nb, _stream_ptr(stream)), "la_gated_delta_fwd")
+    return (out, S) if return_state else out
+
+
+def gated_delta_bwd(q, k, v, g, beta, dout, dq=None, dk=None, dv=None, dg=None, dbeta=None, workspace=None,
+                    stream=None):
+    """Gradients (dq, dk, dv, dg, dbeta) of gated_delta_fwd (from the zero state) for upstream gradient dout."""
+    _need_cuda(q, k, v, dout)
+    s = _shape4(q, k, v)
+    _gates(g, beta, tuple(q.shape[:3]), q.dtype)
+    if dout.shape != v.shape or dout.dtype != v.dtype:
+        raise ValueError("dout must match v in shape and dtype")
+    dq = _result(dq, q, "dq")
+    dk = _result(dk, k, "dk")
+    dv = _result(dv, v, "dv")
+    dg = _result(dg, g, "dg")
+    dbeta = _result(dbeta, beta, "dbeta")
+    ws, nb = _workspace(OP_GATED_DELTA_BWD, s, q.device, workspace)
+    _check(library().la_gated_delta_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(dout), _ptr(dq),
+                                        _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), s, _ptr(ws), nb,
+                                        _stream_ptr(stream)), "la_gated_delta_bwd")
+    return dq, dk, dv, dg, dbeta
+
+
+def gated_delta_step(q, k, v, g, beta, S, out=None, stream=None):
+    """One decode step of the gated delta rule: u = beta (v - a S^T k), S <- a S + k u^T (in place),
+    out = S^T q, with a = exp(g).  q, k [B,H,Dk], v [B,H,Dv], g, beta [B,H], S fp32 [B,H,Dk,Dv]."""
+    _need_cuda(q, k, v)
+    if q.dim() != 3 or k.shape != q.shape or v.dim() != 3 or v.shape[:2] != q.shape[:2]:
+        raise ValueError("expected q, k [B,H,Dk] and v [B,H,Dv]")
+    if not (q.dtype == k.dtype == v.dtype):
+        raise TypeError("q, k, v must share a dtype")
+    B, H, Dk = q.shape
+    Dv = v.shape[2]
+    _gates(g, beta, (B, H), q.dtype)
+    _state(S, B, H, Dk, Dv, "S")
+    out = _result(out, v, "out")
+    s = Shape(B, H, 1, Dk, Dv, _dtype_code(q))
+    _check(library().la_gated_delta_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S), _ptr(out), s,
+                                         _stream_ptr(stream)), "la_gated_delta_step")
+    return out
+
+
+def _norm_shape(x):
+    if x.dim() < 1:
+        raise ValueError("expected x of shape [..., C]")
+    C = x.shape[-1]
+    return NormShape(x.numel() // C if C else 0, C, _dtype_code(x))
+
+
+def _norm_param(p, x, what):
+    if p is None:
+        return
+    _need_cuda(p)
+    if p.shape != x.shape[-1:] or p.dtype != x.dtype:
+        raise ValueError("%s must be [C] of the dtype of x" % what)
+
+
+def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, stream=None, return_stats=False):
+    """Layer norm over the last dimension of x: (x - mean) rstd weight + bias.
+
+    weight and bias are [C] of x's dtype, or None (1 and 0).  With return_stats, returns
+    (y, mean, rstd): the fp32 statistics of shape x.shape[:-1] that layer_norm_bwd takes.
+    """
+    _need_cuda(x)
+    s = _norm_shape(x)
+    _norm_param(weight, x, "weight")
+    _norm_param(bias, x, "bias")
+    out = _result(out, x, "out")
+    mean = rstd = None
+    if return_stats:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+    _check(library().la_layer_norm_fwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(out), _ptr(mean), _ptr(rstd), s, eps,
+                                       _stream_ptr(stream)), "la_layer_norm_fwd")
+    return (out, mean, rstd) if return_stats else out
+
+
+def layer_norm_workspace_bytes(rows: int, C: int, dtype: torch.dtype) -> int:
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dtype)
+    code = LA_BF16 if dtype == torch.bfloat16 else LA_F32
+    return int(library().la_layer_norm_workspace_bytes(NormShape(rows, C, code)))
+
+
+def layer_norm_bwd(x, weight, mean, rstd, dout, dx=None, dweight=None, dbias=None, workspace=None, stream=None):
+    """Gradients (dx, dweight, dbias) of layer_norm_fwd for upstream gradient dout, from its
+    statistics.  With weight None there is no weight or bias: dweight and dbias are None."""
+    _need_cuda(x, mean, rstd, dout)
+    s = _norm_shape(x)
+    _norm_param(weight, x, "weight")
+    if dout.shape != x.shape or dout.dtype != x.dtype:
+        raise ValueError("dout must match x in shape and dtype")
+    for t in (mean, rstd):
+        if t.dtype != torch.float32 or t.shape != x.shape[:-1]:
+            raise ValueError("mean and rstd must be fp32 of shape x.shape[:-1]")
+    dx = _result(dx, x, "dx")
+    ws, nb = None, 0
+    if weight is not None:
+        dweight = _result(dweight, weight, "dweight")
+        dbias = _result(dbias, weight, "dbias")
+        nb = int(library().la_layer_norm_workspace_bytes(s))
+        if workspace is not None:
+            if not workspace.is_cuda:
+                raise ValueError("workspace must be a device tensor")
+            ws, nb = workspace, workspace.numel() * workspace.element_size()
+        else:
+            ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
+    else:
+        dweight = dbias = None
+    _check(library().la_layer_norm_bwd(_ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dout), _ptr(dx),
+                                       _ptr(dweight), _ptr(dbias), s, _ptr(ws), nb, _stream_ptr(stream)),
+           "la_layer_norm_bwd")
+    return dx, dweight, dbias
 
 
 def selftest_bounded_wait(stream=None):

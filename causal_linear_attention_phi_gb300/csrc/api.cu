@@ -9,7 +9,9 @@
 #include <string>
 #include <vector>
 
+#include "gated_delta.cuh"
 #include "la_internal.cuh"
+#include "layer_norm.cuh"
 
 namespace la {
 
@@ -415,8 +417,9 @@ static la_status causal_fwd_impl(const void* q, const void* k, const void* v, vo
 extern "C" {
 
 size_t la_workspace_bytes(int op, la_shape s) {
-    if (op < LA_OP_NONCAUSAL_FWD || op > LA_OP_RETENTION_FWD) return 0;
+    if (op < LA_OP_NONCAUSAL_FWD || op > LA_OP_GATED_DELTA_BWD) return 0;
     if (check_shape(s) != LA_OK || empty(s)) return 0;
+    if (op >= LA_OP_GATED_DELTA_FWD) return gd::layout(s, op == LA_OP_GATED_DELTA_BWD).bytes;
     const Plan p = make_plan(s, op);
     return make_ws_layout(s, op, p).bytes;
 }
@@ -645,6 +648,131 @@ la_status la_retention_step(const void* q, const void* k, const void* v, const f
     return LA_OK;
 }
 
+la_status la_gated_delta_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                             const float* S0, void* o, float* S, la_shape s, void* ws, size_t ws_bytes,
+                             la_stream_t stream) {
+    t_detail.clear();
+    LA_TRY(check_shape(s));
+    if (s.B == 0 || s.H == 0) return LA_OK;
+    if (s.N == 0 && !S) return LA_OK;
+    LA_TRY(check_device());
+    if (S0) LA_TRY(check_ptr(S0, "S0"));
+    if (S) LA_TRY(check_ptr(S, "S"));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (s.N == 0) {  // no position: the state stays what it was
+        const size_t bytes = (size_t)s.B * s.H * s.Dk * s.Dv * sizeof(float);
+        if (S0 == S) return LA_OK;
+        return cuda_status(S0 ? cudaMemcpyAsync(S, S0, bytes, cudaMemcpyDeviceToDevice, st)
+                              : cudaMemsetAsync(S, 0, bytes, st),
+                           "state copy");
+    }
+    LA_TRY(check_ptr(q, "q"));
+    LA_TRY(check_ptr(k, "k"));
+    LA_TRY(check_ptr(v, "v"));
+    LA_TRY(check_ptr(o, "o"));
+    const uintptr_t elem = s.dtype == LA_BF16 ? 2 : 4;
+    LA_TRY(check_ptr(g, "g", elem));
+    LA_TRY(check_ptr(beta, "beta", elem));
+    LA_TRY(check_ws(ws, ws_bytes, gd::layout(s, false).bytes));
+    const gd::FwdArgs a{q, k, v, g, beta, S0, o, S};
+    return cuda_status(gd::simt_fwd(a, s, static_cast<char*>(ws), st), "gated delta forward");
+}
+
+la_status la_gated_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                             const void* dout, void* dq, void* dk, void* dv, void* dg, void* dbeta, la_shape s,
+                             void* ws, size_t ws_bytes, la_stream_t stream) {
+    t_detail.clear();
+    LA_TRY(check_shape(s));
+    if (empty(s)) return LA_OK;
+    LA_TRY(check_bwd_args(q, k, v, dout, dq, dk, dv));
+    const uintptr_t elem = s.dtype == LA_BF16 ? 2 : 4;
+    LA_TRY(check_ptr(g, "g", elem));
+    LA_TRY(check_ptr(beta, "beta", elem));
+    LA_TRY(check_ptr(dg, "dg", elem));
+    LA_TRY(check_ptr(dbeta, "dbeta", elem));
+    LA_TRY(check_ws(ws, ws_bytes, gd::layout(s, true).bytes));
+    const gd::BwdArgs a{q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta};
+    return cuda_status(gd::simt_bwd(a, s, static_cast<char*>(ws), reinterpret_cast<cudaStream_t>(stream)),
+                       "gated delta backward");
+}
+
+la_status la_gated_delta_step(const void* q, const void* k, const void* v, const void* g, const void* beta, float* S,
+                              void* out, la_shape s, la_stream_t stream) {
+    t_detail.clear();
+    la_shape s1 = s;
+    s1.N = 1;  // N is ignored by the step
+    LA_TRY(check_shape(s1));
+    if (empty(s1)) return LA_OK;
+    LA_TRY(check_device());
+    const uintptr_t elem = s.dtype == LA_BF16 ? 2 : 4;
+    LA_TRY(check_ptr(q, "q"));
+    LA_TRY(check_ptr(k, "k"));
+    LA_TRY(check_ptr(v, "v"));
+    LA_TRY(check_ptr(g, "g", elem));
+    LA_TRY(check_ptr(beta, "beta", elem));
+    LA_TRY(check_ptr(S, "S"));
+    LA_TRY(check_ptr(out, "out"));
+    return cuda_status(gd::step(q, k, v, g, beta, S, out, s1, reinterpret_cast<cudaStream_t>(stream)),
+                       "gated delta step");
+}
+
+static la_status check_norm(const la_norm_shape& s) {
+    if (s.rows < 0 || s.C < 1) return fail(LA_ERR_INVALID_ARG, "bad size rows=%lld C=%d", s.rows, s.C);
+    if (s.dtype != LA_F32 && s.dtype != LA_BF16) return fail(LA_ERR_INVALID_ARG, "bad dtype %d", s.dtype);
+    if (s.C > ln::kMaxC) return fail(LA_ERR_UNSUPPORTED, "C=%d exceeds %d", s.C, ln::kMaxC);
+    if ((double)s.rows * s.C >= 1099511627776.0) return fail(LA_ERR_INVALID_ARG, "problem too large");
+    return LA_OK;
+}
+
+la_status la_layer_norm_fwd(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
+                            la_norm_shape s, float eps, la_stream_t stream) {
+    t_detail.clear();
+    LA_TRY(check_norm(s));
+    if (!(eps >= 0.f)) return fail(LA_ERR_INVALID_ARG, "eps must not be negative");
+    if (s.rows == 0) return LA_OK;
+    LA_TRY(check_device());
+    LA_TRY(check_ptr(x, "x"));
+    LA_TRY(check_ptr(y, "y"));
+    if (w) LA_TRY(check_ptr(w, "w"));
+    if (b) LA_TRY(check_ptr(b, "b"));
+    if (mean) LA_TRY(check_ptr(mean, "mean", 4));
+    if (rstd) LA_TRY(check_ptr(rstd, "rstd", 4));
+    return cuda_status(ln::fwd(x, w, b, y, mean, rstd, s, eps, reinterpret_cast<cudaStream_t>(stream)),
+                       "layer norm forward");
+}
+
+size_t la_layer_norm_workspace_bytes(la_norm_shape s) {
+    if (check_norm(s) != LA_OK || s.rows == 0) return 0;
+    return align256((size_t)ln::bwd_blocks(s.rows, s.C) * 2 * s.C * sizeof(float));
+}
+
+la_status la_layer_norm_bwd(const void* x, const void* w, const float* mean, const float* rstd, const void* dy,
+                            void* dx, void* dw, void* db, la_norm_shape s, void* ws, size_t ws_bytes,
+                            la_stream_t stream) {
+    t_detail.clear();
+    LA_TRY(check_norm(s));
+    if (s.rows == 0 && !dw && !db) return LA_OK;
+    LA_TRY(check_device());
+    if (dw) LA_TRY(check_ptr(dw, "dw"));
+    if (db) LA_TRY(check_ptr(db, "db"));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (s.rows == 0) {  // sums over no row
+        const size_t bytes = (size_t)s.C * (s.dtype == LA_BF16 ? 2 : 4);
+        if (dw) LA_TRY(cuda_status(cudaMemsetAsync(dw, 0, bytes, st), "gradient clear"));
+        if (db) LA_TRY(cuda_status(cudaMemsetAsync(db, 0, bytes, st), "gradient clear"));
+        return LA_OK;
+    }
+    LA_TRY(check_ptr(x, "x"));
+    if (w) LA_TRY(check_ptr(w, "w"));
+    LA_TRY(check_ptr(mean, "mean", 4));
+    LA_TRY(check_ptr(rstd, "rstd", 4));
+    LA_TRY(check_ptr(dy, "dy"));
+    LA_TRY(check_ptr(dx, "dx"));
+    if (dw || db) LA_TRY(check_ws(ws, ws_bytes, la_layer_norm_workspace_bytes(s)));
+    return cuda_status(ln::bwd(x, w, mean, rstd, dy, dx, dw, db, static_cast<float*>(ws), s, st),
+                       "layer norm backward");
+}
+
 la_status la_last_error(void) {
     int v = 0;
     if (cudaMemcpyFromSymbol(&v, g_error_word, sizeof(int)) != cudaSuccess)
@@ -653,7 +781,9 @@ la_status la_last_error(void) {
     if (v == LA_ERR_BOUNDS) {
         unsigned site = 0;
         if (cudaMemcpyFromSymbol(&site, g_debug_site, sizeof(site)) == cudaSuccess) {
-            static const char* const kFiles[] = {"api.cu", "decode.cu", "host_step.cu", "noalloc.cu", "retention.cu",
+            static const char* const kFiles[] = {"api.cu", "decode.cu", "gated_delta.cu", "gated_delta_step.cu",
+                                                 "gated_delta.cuh", "host_step.cu", "layer_norm.cu", "noalloc.cu",
+                                                 "retention.cu",
                                                  "selftest.cu", "simt_kernels.cu", "tc_apply.cu", "tc_bwd.cu",
                                                  "tc_fwd.cu", "tc_noncausal_bwd.cu", "tc_retention.cu",
                                                  "la_internal.cuh", "simt_common.cuh", "tc_common.cuh", "sm100.cuh"};

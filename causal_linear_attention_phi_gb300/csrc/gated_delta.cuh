@@ -1,0 +1,179 @@
+// gated_delta.cuh -- the gated delta rule (itwiki 선형 어텐션, 발전: 감쇠, 게이트, 델타 규칙: a decaying
+// state whose write replaces what the key already holds).  Per head, with S a Dk x Dv state:
+//   a_t = exp(g_t),  u_t = beta_t (v_t - a_t S_(t-1)^T k_t),  S_t = a_t S_(t-1) + k_t u_t^T,  o_t = S_t^T q_t.
+//
+// Chunked form, for a chunk of C = 64 positions entered with the state S.  With G_i the sum of g over the
+// chunk's positions up to i, gam_i = exp(G_i), tail_j = exp(G_C - G_j), and Gam_ij = exp(G_i - G_j) for i >= j:
+//   A = tril(K K^T, -1) . Gam                        what earlier keys of the chunk hold of key i
+//   R = V - gam K S,   u = beta X,   X = R - A u     (X is v minus what the state before t holds of k_t)
+//     =>  X = R + t (beta R)  with  t = -A (I + beta A)^-1, strictly lower triangular
+//   O  = gam Q S + P u,   P = tril(Q K^T) . Gam
+//   S' = gam_C S + K^T (tail u)
+// Gradient, with dS' the gradient with respect to the state after the chunk:
+//   dU = P^T dO + tail K dS',   Y = dU + t^T (beta dU),   dV = dR = beta Y,   dbeta_i = X_i . Y_i
+//   dS = gam_C dS' + Q^T (gam dO) - K^T (gam dR)
+//   F = tril(dO u^T) . Gam,   E = -tril(dR u^T, -1) . Gam
+//   dQ = gam dO S^T + F K
+//   dK = tail u dS'^T + F^T Q + E K + E^T K - gam dR S^T
+//   dG_i: every product that a decay enters counted at its later end and taken off at its earlier one;
+//   dg = the reverse cumulative sum of dG.
+// t is kept apart from the identity, so neither beta nor a decay is ever divided by: beta = 0 and
+// a = 0 are ordinary values.
+#pragma once
+
+#include "la_internal.cuh"
+
+namespace la {
+namespace gd {
+
+constexpr int kC = 64;
+
+// The gates of one chunk, fp32, one record per (head, chunk) in the workspace.  The sum of log decays is
+// formed in fp64 and kept as hi + lo, so that differences of long sums keep fp32's precision; a decay
+// below exp(-100) (under fp32's normal range; -inf among them) is counted in kSeg instead of entering the sum,
+// and a product across it is 0.  Positions past the sequence's end have g = 0 and beta = 0.
+constexpr int kGam = 0, kTail = kC, kBeta = 2 * kC, kGhi = 3 * kC, kGlo = 4 * kC, kSeg = 5 * kC;
+constexpr int kRec = 6 * kC;
+constexpr float kReset = -100.f;
+
+// exp(hi + lo) for |lo| at most half a step of hi.
+__device__ __forceinline__ float exp_hilo(float hi, float lo) {
+    const float e = expf(hi);
+    return fmaf(e, lo, e);
+}
+
+// Gam_ij for i >= j (0 across a reset).
+__device__ __forceinline__ float pair_decay(const float* rec, int i, int j) {
+    return rec[kSeg + i] == rec[kSeg + j]
+               ? exp_hilo(rec[kGhi + i] - rec[kGhi + j], rec[kGlo + i] - rec[kGlo + j])
+               : 0.f;
+}
+
+// One warp forms the record of the chunk at c0 (n positions) in rec (shared memory).
+template <typename T>
+__device__ __forceinline__ void gate_record(const T* __restrict__ g, const T* __restrict__ beta, int c0, int n,
+                                            float* rec, int lane) {
+    double v[2];
+    int r[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int i = 2 * lane + e;
+        const float x = i < n ? to_f32(g[c0 + i]) : 0.f;
+        rec[kBeta + i] = i < n ? to_f32(beta[c0 + i]) : 0.f;
+        const bool reset = x < kReset;
+        v[e] = reset ? 0.0 : (double)x;
+        r[e] = reset ? 1 : 0;
+    }
+    v[1] += v[0];
+    r[1] += r[0];
+    double sv = v[1];
+    int sr = r[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double pv = __shfl_up_sync(0xffffffffu, sv, o);
+        const int pr = __shfl_up_sync(0xffffffffu, sr, o);
+        if (lane >= o) {
+            sv += pv;
+            sr += pr;
+        }
+    }
+    const double tot = __shfl_sync(0xffffffffu, sv, 31);
+    const int rtot = __shfl_sync(0xffffffffu, sr, 31);
+    const double base = sv - v[1];
+    const int rbase = sr - r[1];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int i = 2 * lane + e;
+        const double G = base + v[e], D = tot - G;
+        const int seg = rbase + r[e];
+        const float hi = (float)G, lo = (float)(G - (double)hi);
+        const float dhi = (float)D, dlo = (float)(D - (double)dhi);
+        rec[kGhi + i] = hi;
+        rec[kGlo + i] = lo;
+        rec[kSeg + i] = (float)seg;
+        rec[kGam + i] = seg == 0 ? exp_hilo(hi, lo) : 0.f;
+        rec[kTail + i] = seg == rtot ? exp_hilo(dhi, dlo) : 0.f;
+    }
+}
+
+// t = -A (I + beta A)^-1 for a strictly lower triangular A (zero on and above the diagonal), 64 x 64 fp32
+// in shared memory with row pitch ld, by 256 threads.  Row by row t_i = -(A_i + sum_(j<i) A_ij beta_j t_j)
+// (forward substitution) in blocks of 16: the diagonal blocks column by column, then the block rows below
+// them as products.  Every thread calls it; A is complete before and t after it.
+__device__ __forceinline__ void solve_t(const float* A, float* t, const float* beta, int ld, int tid) {
+    for (int i = tid; i < kC * kC; i += 256) {
+        const int r = i >> 6, c = i & 63;
+        if ((r >> 4) <= (c >> 4)) t[r * ld + c] = 0.f;  // the block rows below the diagonal are all written
+    }
+    __syncthreads();
+    if (tid < kC) {
+        const int b0 = tid & 48, c = tid & 15;
+        float x[16];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) {
+            float s = A[(b0 + r) * ld + b0 + c];
+#pragma unroll
+            for (int j = 1; j < r; ++j)
+                if (j > c) s = fmaf(A[(b0 + r) * ld + b0 + j] * beta[b0 + j], x[j], s);
+            x[r] = -s;
+            if (r > c) t[(b0 + r) * ld + b0 + c] = x[r];
+        }
+    }
+    __syncthreads();
+    const int rr = tid >> 4, cc = tid & 15;
+#pragma unroll
+    for (int I = 1; I < 4; ++I) {
+        const int i = 16 * I + rr;
+        float rhs[3];
+#pragma unroll
+        for (int J = 0; J < I; ++J) {
+            float s = A[i * ld + 16 * J + cc];
+            for (int k = 16 * J; k < 16 * I; ++k) s = fmaf(A[i * ld + k] * beta[k], t[k * ld + 16 * J + cc], s);
+            rhs[J] = s;
+        }
+#pragma unroll
+        for (int J = 0; J < I; ++J) t[i * ld + 16 * J + cc] = rhs[J];
+        __syncthreads();
+#pragma unroll
+        for (int J = 0; J < I; ++J) {
+            float s = rhs[J];
+#pragma unroll 4
+            for (int j = 0; j < 15; ++j)  // t is 0 from the diagonal on
+                s = fmaf(t[i * ld + 16 * I + j] * beta[16 * I + j], t[(16 * I + j) * ld + 16 * J + cc], s);
+            rhs[J] = -s;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int J = 0; J < I; ++J) t[i * ld + 16 * J + cc] = rhs[J];
+        __syncthreads();
+    }
+}
+
+// Byte offsets of the workspace regions of one call (256-byte aligned).
+struct Layout {
+    size_t rec;     // [BH][M][kRec] fp32 gate records
+    size_t t, P;    // [BH][M][64][64] fp32
+    size_t X, Y;    // [BH][M * 64][Dv] fp32 (gradient)
+    size_t S, dS;   // [BH][M][Dk][Dv] fp32: the state entering each chunk, the gradient leaving it (gradient)
+    size_t bytes;
+};
+Layout layout(const la_shape& s, bool bwd);
+
+struct FwdArgs {
+    const void *q, *k, *v, *g, *beta;
+    const float* S0;
+    void* o;
+    float* S;
+};
+struct BwdArgs {
+    const void *q, *k, *v, *g, *beta, *dout;
+    void *dq, *dk, *dv, *dg, *dbeta;
+};
+// Any dtype and head size, on the CUDA cores.
+cudaError_t simt_fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st);
+cudaError_t simt_bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st);
+cudaError_t step(const void* q, const void* k, const void* v, const void* g, const void* beta, float* S, void* out,
+                 const la_shape& s, cudaStream_t st);
+
+}  // namespace gd
+}  // namespace la

@@ -71,7 +71,9 @@ typedef enum {
     LA_OP_CAUSAL_FWD = 1,
     LA_OP_CAUSAL_BWD = 2,
     LA_OP_NONCAUSAL_BWD = 3,
-    LA_OP_RETENTION_FWD = 4
+    LA_OP_RETENTION_FWD = 4,
+    LA_OP_GATED_DELTA_FWD = 5,
+    LA_OP_GATED_DELTA_BWD = 6
 } la_op;
 
 /* Problem shape.  dtype is an la_dtype value. */
@@ -264,6 +266,77 @@ la_status la_retention_fwd(const void* q, const void* k, const void* v, const fl
  */
 la_status la_retention_step(const void* q, const void* k, const void* v, const float* gamma,
                             float* S, void* out, la_shape s, la_stream_t stream);
+
+/*
+ * The gated delta rule (itwiki 선형 어텐션, 발전: 감쇠, 게이트, 델타 규칙): linear attention whose state
+ * decays by a gate per position and whose write replaces what the key already holds.  With
+ * a_t = exp(g_t), S_(-1) = S0 (or 0):
+ *   u_t = beta_t (v_t - a_t S_(t-1)^T k_t),  S_t = a_t S_(t-1) + k_t u_t^T,  o_t = S_t^T q_t.
+ * The feature map is the identity, there is no normaliser and no scale; the method intends keys of unit
+ * length, g <= 0 and 0 <= beta <= 1, any real value is computed as written (with |k| > 1 or g > 0 the state
+ * may grow without bound).  g below -100 (-inf among them) is a decay of exactly 0: the state starts anew, so
+ * sequences packed one after another are separated by a g of -inf at each one's first position.
+ * Computed in chunks of 64 positions: inside a chunk the writes are solved for together (a triangular system),
+ * the state is carried from chunk to chunk.
+ * q, k: [B,H,N,Dk]; v, o: [B,H,N,Dv]; g, beta: [B,H,N], all in s.dtype; o written.  g and beta need the
+ * alignment of their elements only.
+ * S0: NULL, or a DEVICE fp32 [B,H,Dk,Dv]: the state before the first position.
+ * S: NULL, or a DEVICE fp32 [B,H,Dk,Dv] that receives the state after the last position (written; S0, or zero,
+ *   for N = 0), from which la_gated_delta_step or another la_gated_delta_fwd continues.  It may be S0 itself.
+ * Workspace: la_workspace_bytes(LA_OP_GATED_DELTA_FWD, s).
+ */
+la_status la_gated_delta_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                             const float* S0, void* o, float* S, la_shape s,
+                             void* ws, size_t ws_bytes, la_stream_t stream);
+
+/*
+ * Gradient of la_gated_delta_fwd (from the zero state) for an upstream gradient dout = dL/do:
+ * dq, dk: [B,H,N,Dk]; dv: [B,H,N,Dv]; dg, dbeta: [B,H,N], all in s.dtype and written.  dg is the gradient with
+ * respect to g (the log of the decay); it is 0 where g is below -100.  Everything is recomputed from the
+ * inputs; the workspace holds one state and one state gradient for each chunk of 64 positions, so memory is linear in N.
+ * Workspace: la_workspace_bytes(LA_OP_GATED_DELTA_BWD, s).
+ */
+la_status la_gated_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                             const void* dout, void* dq, void* dk, void* dv, void* dg, void* dbeta, la_shape s,
+                             void* ws, size_t ws_bytes, la_stream_t stream);
+
+/*
+ * One decode step of the gated delta rule for every head:
+ *   u = beta (v - a S^T k),  S <- a S + k u^T,  out = S^T q   with a = exp(g).
+ * q, k: [B,H,Dk]; v, out: [B,H,Dv]; g, beta: [B,H], in s.dtype; S: [B,H,Dk,Dv] fp32, read and updated
+ * in place (zero before the first step, or the S of la_gated_delta_fwd).  s.N is ignored.  No workspace.
+ */
+la_status la_gated_delta_step(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                              float* S, void* out, la_shape s, la_stream_t stream);
+
+/*
+ * Layer norm over the last dimension of a dense [rows, C] array (the heads' outputs with C = Dv, or the model
+ * width):  y = (x - mean) rstd w + b,  mean and variance over the C elements of a row (the variance divided by C),
+ * rstd = 1 / sqrt(variance + eps).  Statistics and sums are fp32.
+ * x, y: [rows, C]; w, b: [C], each may be NULL (1 and 0); all in `dtype`, 16-byte aligned.  mean, rstd: NULL, or
+ * DEVICE fp32 [rows] that receive the statistics for la_layer_norm_bwd.  y may be x itself.
+ * rows >= 0, 1 <= C <= 16384 (else LA_ERR_UNSUPPORTED), rows * C < 2^40.  No workspace.
+ */
+typedef struct {
+    long long rows;
+    int C;
+    int dtype;
+} la_norm_shape;
+
+la_status la_layer_norm_fwd(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
+                            la_norm_shape s, float eps, la_stream_t stream);
+
+/*
+ * Gradient of la_layer_norm_fwd for dy = dL/dy, from the saved statistics.  With h = (x - mean) rstd and d = dy w:
+ *   dx = rstd (d - sum(d) / C - h sum(d h) / C),  dw = sum over rows of dy h,  db = sum over rows of dy.
+ * w may be NULL (1).  dw, db: [C] in s.dtype, each may be NULL (not wanted).  dx may be dy or x itself.  The sums
+ * over rows are fp32 in a fixed order: the same inputs give the same bits.  For rows = 0, dw and db are zero.
+ * Workspace: la_layer_norm_workspace_bytes(s), needed where dw or db is wanted.
+ */
+size_t la_layer_norm_workspace_bytes(la_norm_shape s);
+la_status la_layer_norm_bwd(const void* x, const void* w, const float* mean, const float* rstd, const void* dy,
+                            void* dx, void* dw, void* db, la_norm_shape s,
+                            void* ws, size_t ws_bytes, la_stream_t stream);
 
 /*
  * la_causal_fwd with no workspace argument: the same causal forward, with its

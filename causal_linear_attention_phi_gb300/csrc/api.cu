@@ -675,7 +675,9 @@ la_status la_gated_delta_fwd(const void* q, const void* k, const void* v, const 
     LA_TRY(check_ptr(beta, "beta", elem));
     LA_TRY(check_ws(ws, ws_bytes, gd::layout(s, false).bytes));
     const gd::FwdArgs a{q, k, v, g, beta, S0, o, S};
-    return cuda_status(gd::simt_fwd(a, s, static_cast<char*>(ws), st), "gated delta forward");
+    return cuda_status(gd::tc_ok(s) ? gd::tc_fwd(a, s, static_cast<char*>(ws), st)
+                                    : gd::simt_fwd(a, s, static_cast<char*>(ws), st),
+                       "gated delta forward");
 }
 
 la_status la_gated_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
@@ -784,7 +786,7 @@ la_status la_last_error(void) {
             static const char* const kFiles[] = {"api.cu", "decode.cu", "gated_delta.cu", "gated_delta_step.cu",
                                                  "gated_delta.cuh", "host_step.cu", "layer_norm.cu", "noalloc.cu",
                                                  "retention.cu",
-                                                 "selftest.cu", "simt_kernels.cu", "tc_apply.cu", "tc_bwd.cu",
+                                                 "selftest.cu", "simt_kernels.cu", "tc_gated_delta.cu", "tc_apply.cu", "tc_bwd.cu",
                                                  "tc_fwd.cu", "tc_noncausal_bwd.cu", "tc_retention.cu",
                                                  "la_internal.cuh", "simt_common.cuh", "tc_common.cuh", "sm100.cuh"};
             const char* file = "unknown file";

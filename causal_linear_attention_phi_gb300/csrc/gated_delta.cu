@@ -562,8 +562,8 @@ Layout layout(const la_shape& s, bool bwd) {
         return at;
     };
     L.rec = take(chunks * kRec);
-    L.t = take(chunks * kC * kC);
-    L.P = take(chunks * kC * kC);
+    L.t = take(2 * chunks * kC * kC);
+    L.P = L.t + chunks * kC * kC * sizeof(float);
     if (bwd) {
         L.X = take(chunks * kC * s.Dv);
         L.Y = take(chunks * kC * s.Dv);

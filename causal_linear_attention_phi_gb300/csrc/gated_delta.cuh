@@ -152,7 +152,7 @@ __device__ __forceinline__ void solve_t(const float* A, float* t, const float* b
 // Byte offsets of the workspace regions of one call (256-byte aligned).
 struct Layout {
     size_t rec;     // [BH][M][kRec] fp32 gate records
-    size_t t, P;    // [BH][M][64][64] fp32
+    size_t t, P;    // [BH][M][64][64] fp32 (tensor cores: t hi, t lo, P hi, P lo as bf16 in the bytes of t and P)
     size_t X, Y;    // [BH][M * 64][Dv] fp32 (gradient)
     size_t S, dS;   // [BH][M][Dk][Dv] fp32: the state entering each chunk, the gradient leaving it (gradient)
     size_t bytes;
@@ -172,6 +172,9 @@ struct BwdArgs {
 // Any dtype and head size, on the CUDA cores.
 cudaError_t simt_fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st);
 cudaError_t simt_bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st);
+// bf16 heads with Dk = Dv = 64 or 128, on the tensor cores.
+bool tc_ok(const la_shape& s);
+cudaError_t tc_fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st);
 cudaError_t step(const void* q, const void* k, const void* v, const void* g, const void* beta, float* S, void* out,
                  const la_shape& s, cudaStream_t st);
 

@@ -1,0 +1,539 @@
+// tc_gated_delta.cu -- tensor-core (tcgen05 / TMEM / TMA) kernels of the gated delta rule for bf16 heads with
+// Dk = Dv = 128 or 64 (formulas in gated_delta.cuh), chunks of 64 positions.
+//
+// tc_gd_prepare (one block per chunk): [Q; K] K^T as one 128 x 64 product, the decays applied, t solved for in fp32;
+// t and P go to the workspace as bf16 hi + lo tiles in the swizzled layout that the products read.
+//
+// tc_gd_states (one block per head and segment of chunks): the recurrence with the state transposed, S^T
+// [Dv lanes x Dk], so that every product has 128 rows and its left operand comes from TMEM, written there by the
+// thread that owns the row:
+//   Y^T  = S^T K^T                       R^T = V^T - gam Y^T          (a column is a position)
+//   X^T  = R^T + (beta R)^T t^T          u^T = beta X^T
+//   S^T <- gam_C S^T + (tail u)^T K      O^T = gam (S^T Q^T) + u^T P^T
+// The fp32 state stays in registers (half a row to a thread).  Inputs K, Q are bf16 already; what is formed
+// here (S, beta R, u, t, P) enters the products as hi + lo bf16 parts, x = hi + lo to 2^-17, except the S of
+// S^T Q^T, which meets one rounding only (it adds 0.5e-3 to the 1.7e-3 of rounding o itself; with
+// single parts throughout, correlated keys lift o's error to 7e-3 and the state's to 4e-3).
+//
+// Roles (320 threads): warp 0 issues TMA, warp 1 tcgen05.mma, warps 2-9 compute: warp w serves TMEM lanes
+// 32 (w % 4) .. +31 (value columns r), warps 2-5 positions 0-31 and state columns 0 .. D/2 - 1, warps 6-9 the others.
+// Every wait is bounded: one that runs out records LA_ERR_TIMEOUT and its thread waits no more, so every role ends.
+#include <cudaTypedefs.h>
+
+#include "gated_delta.cuh"
+#include "tc_common.cuh"
+
+namespace la {
+namespace gd {
+namespace {
+using namespace sm100;
+using tc::bf_hi;
+using tc::bf_lo;
+
+constexpr int kBlk = kC * 128;          // 64 rows x 64 bf16 columns, 128-byte swizzle
+constexpr int kMats = 4 * kBlk;         // t hi, t lo, P hi, P lo of a chunk
+constexpr int kTHi = 0, kTLo = kBlk, kPHi = 2 * kBlk, kPLo = 3 * kBlk;
+constexpr int kGateBytes = 3 * kC * 4;  // gam, tail, beta of the record
+
+// Contiguous global -> shared copy (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+// Operands of 64-row tiles: K-major (rows are M or N) and MN-major (rows are K), K step kk of 16.
+__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int kk) {
+    return smem_desc_sw128(tile + (kk >> 2) * kBlk + (kk & 3) * 32, 16, 1024);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int kk) {
+    return smem_desc_sw128(tile + kk * 2048, kBlk, 1024);
+}
+// Byte offset of (row, column c) in 64-column blocks of kC rows.
+__device__ __forceinline__ int elem_off(int row, int c) {
+    return (c >> 6) * kBlk + row * 128 + ((((c >> 3) & 7) ^ (row & 7)) << 4) + (c & 7) * 2;
+}
+// Every kernel here starts so: wait for the previous grid, take the TMEM columns, and only then let the next
+// grid's blocks be scheduled.  Blocks of several of these kernels fit on one SM: none holds columns while it
+// waits for a grid, and none is still to take its columns when a block that waits for it can arrive.
+__device__ __forceinline__ uint32_t enter(uint32_t* slot, uint32_t cols, int warp) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 1) {
+        tmem_alloc(slot, cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    return *slot;
+}
+// a, b -> packed bf16 hi and lo parts.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16x2(a, b);
+    lo = pack_bf16x2(a - bf_lo(hi), b - bf_hi(hi));
+}
+
+// ------------------------------------------------------------------ t and P of every chunk
+constexpr int kPrepThreads = 256;
+struct PrepSmem {
+    // offset 0: blocks of [Q rows 0-63; K rows 64-127] x 64 columns, then (once the product has read them) fp32 A
+    static constexpr int A = 0;
+    static constexpr int T = A + kC * (kC + 1) * 4;
+    static constexpr int rec = T + kC * (kC + 1) * 4;  // beyond the tiles (32768 bytes)
+    static constexpr int bar = rec + kRec * 4;
+    static constexpr int total = bar + 32;
+};
+static_assert(PrepSmem::rec >= 4 * kBlk, "the gate record lies beyond the tiles");
+constexpr size_t kPrepBytes = PrepSmem::total + 1024;
+
+template <int D>
+__global__ void __launch_bounds__(kPrepThreads, 4)
+tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+              const __nv_bfloat16* __restrict__ g, const __nv_bfloat16* __restrict__ beta, float* __restrict__ recs,
+              uint8_t* __restrict__ mats, int N, int M, int* err) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* rec = reinterpret_cast<float*>(base + PrepSmem::rec);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(base + PrepSmem::bar);  // loads, product
+    uint32_t* slot = reinterpret_cast<uint32_t*>(bar + 2);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, m = blockIdx.x;
+    const size_t bh = blockIdx.y, at = bh * M + m;
+    const int c0 = m * kC, n = min(kC, N - c0);
+    LA_DCHECK(n >= 1 && m < M && (int)gridDim.x == M);
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        mbar_init(bar + 1, 1);
+        fence_mbar_init();
+    }
+    const uint32_t tmem = enter(slot, 64, warp);
+    if (tid == 0) {
+        mbar_arrive_expect_tx(bar, 2 * (D / 64) * kBlk);
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b) {
+            tma_load_3d(base + 2 * b * kBlk, &tm_q, 64 * b, c0, (int)bh, bar);
+            tma_load_3d(base + (2 * b + 1) * kBlk, &tm_k, 64 * b, c0, (int)bh, bar);
+        }
+    }
+    if (warp == 1) gate_record(g + bh * N, beta + bh * N, c0, n, rec, lane);
+    if (tid == 0 && mbar_wait(bar, 0, err, LA_ERR_TIMEOUT)) {
+        tc_fence_after();
+        constexpr uint32_t id = idesc_bf16_f32(128, kC, 0, 0);
+        const uint32_t a = smem_u32(base);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t t = a + (kk >> 2) * 2 * kBlk + (kk & 3) * 32;
+            mma_ss(tmem, smem_desc_sw128(t, 16, 1024), smem_desc_sw128(t + kBlk, 16, 1024), id, kk > 0);
+        }
+        mma_commit(bar + 1);
+    }
+    const bool ok = mbar_wait(bar + 1, 0, err, LA_ERR_TIMEOUT);
+    __syncthreads();  // the gates
+    tc_fence_after();
+    float* A = reinterpret_cast<float*>(base + PrepSmem::A);
+    float* T = reinterpret_cast<float*>(base + PrepSmem::T);
+    uint8_t* mat = mats + at * (size_t)kMats;
+    {
+        // lanes 0-63 hold Q K^T, 64-127 K K^T; this thread row i, positions 32 h .. +31
+        const int quarter = warp & 3, h = warp >> 2, i = 32 * (quarter & 1) + lane, j0 = 32 * h;
+        uint32_t w[32];
+        tmem_ld32(tmem + ((uint32_t)(32 * quarter) << 16) + j0, w);
+        tmem_ld_wait();
+        const float seg = rec[kSeg + i], hi = rec[kGhi + i], lo = rec[kGlo + i];
+        const bool isP = quarter < 2;
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+            const int j = j0 + x;
+            const bool in = (isP ? j <= i : j < i) && rec[kSeg + j] == seg;
+            w[x] = in ? __float_as_uint(__uint_as_float(w[x]) * exp_hilo(hi - rec[kGhi + j], lo - rec[kGlo + j])) : 0u;
+        }
+        if (isP) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint4 a, b;
+                split2(__uint_as_float(w[8 * c]), __uint_as_float(w[8 * c + 1]), a.x, b.x);
+                split2(__uint_as_float(w[8 * c + 2]), __uint_as_float(w[8 * c + 3]), a.y, b.y);
+                split2(__uint_as_float(w[8 * c + 4]), __uint_as_float(w[8 * c + 5]), a.z, b.z);
+                split2(__uint_as_float(w[8 * c + 6]), __uint_as_float(w[8 * c + 7]), a.w, b.w);
+                const int off = elem_off(i, j0 + 8 * c);
+                *reinterpret_cast<uint4*>(mat + kPHi + off) = a;
+                *reinterpret_cast<uint4*>(mat + kPLo + off) = b;
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) A[i * (kC + 1) + j0 + x] = __uint_as_float(w[x]);
+        }
+    }
+    __syncthreads();
+    solve_t(A, T, rec + kBeta, kC + 1, tid);
+    {
+        const int i = tid >> 2, j0 = 16 * (tid & 3);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const float* s = T + i * (kC + 1) + j0 + 8 * c;
+            uint4 a, b;
+            split2(s[0], s[1], a.x, b.x);
+            split2(s[2], s[3], a.y, b.y);
+            split2(s[4], s[5], a.z, b.z);
+            split2(s[6], s[7], a.w, b.w);
+            const int off = elem_off(i, j0 + 8 * c);
+            *reinterpret_cast<uint4*>(mat + kTHi + off) = a;
+            *reinterpret_cast<uint4*>(mat + kTLo + off) = b;
+        }
+    }
+    for (int i = tid; i < kRec; i += kPrepThreads) recs[at * kRec + i] = rec[i];
+    if (!ok && tid == 0) mbar_wait(bar, 0, err, LA_ERR_TIMEOUT);  // never leave with copies in flight
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 64);
+    }
+}
+
+// ------------------------------------------------------------------ the recurrence
+constexpr int kThreads = 320;
+constexpr int kWarps = 8;  // compute warps
+
+struct __align__(8) Bars {
+    uint64_t full[2], empty[2];
+    uint64_t s_ready, y_done, r_ready, x_done, u_ready, s_done, o_ready, o_done, o_free, final_mma;
+};
+
+template <int D>
+struct FwdSmem {
+    static constexpr int tile = D / 64 * kBlk;
+    static constexpr int K = 0, Q = tile, V = 2 * tile, mats = 3 * tile, gates = mats + kMats;
+    static constexpr int stage = gates + 1024;
+    static constexpr int O = 2 * stage;  // o tile for its TMA store
+    static constexpr int bars = O + tile;
+    static constexpr int slot = bars + 256;
+    static constexpr int total = slot + 16;
+    static constexpr size_t bytes = total + 1024;
+};
+static_assert(FwdSmem<128>::bytes <= 232448, "shared memory");
+
+// TMEM columns
+template <int D>
+struct Tm {
+    static constexpr uint32_t SHi = 0, SLo = D / 2, Y = D, R = D + 64, U = D + 128, dS = D + 192, O = 2 * D + 192;
+    static_assert(O + 64 <= 512, "TMEM");
+};
+
+// Chunks [p cps, (p + 1) cps) of a head.  S0 / S_out: fp32 [BH][D][D] (null: zero / not wanted).
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+             const float* __restrict__ recs, const uint8_t* __restrict__ mats, const float* S0, float* S_out, int M,
+             int cps, int* err) {
+    using L = FwdSmem<D>;
+    using T = Tm<D>;
+    constexpr int kSc = D / 2;  // state columns of a thread
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Bars* bar = reinterpret_cast<Bars*>(base + L::bars);
+    uint32_t* slot = reinterpret_cast<uint32_t*>(base + L::slot);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int p = blockIdx.x, bh = blockIdx.y, cbeg = p * cps, nloc = min(M, cbeg + cps) - cbeg;
+    LA_DCHECK(nloc >= 1);
+
+    if (tid == 0) {
+        mbar_init(&bar->full[0], 1);
+        mbar_init(&bar->full[1], 1);
+        mbar_init(&bar->empty[0], 1 + kWarps);
+        mbar_init(&bar->empty[1], 1 + kWarps);
+        mbar_init(&bar->s_ready, kWarps);
+        mbar_init(&bar->y_done, 1);
+        mbar_init(&bar->r_ready, kWarps);
+        mbar_init(&bar->x_done, 1);
+        mbar_init(&bar->u_ready, kWarps);
+        mbar_init(&bar->s_done, 1);
+        mbar_init(&bar->o_ready, kWarps);
+        mbar_init(&bar->o_done, 1);
+        mbar_init(&bar->o_free, kWarps);
+        mbar_init(&bar->final_mma, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_o);
+    }
+    const uint32_t tmem = enter(slot, 512, warp);
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int armed[2] = {-1, -1};
+            for (int i = 0; i < nloc; ++i) {
+                const int s = i & 1, c = cbeg + i, t0 = c * kC;
+                uint8_t* st = base + s * L::stage;
+                if (!mbar_wait(&bar->empty[s], ((i >> 1) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
+                mbar_arrive_expect_tx(&bar->full[s], 3 * L::tile + kMats + kGateBytes);
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b) {
+                    tma_load_3d(st + L::K + b * kBlk, &tm_k, 64 * b, t0, bh, &bar->full[s]);
+                    tma_load_3d(st + L::V + b * kBlk, &tm_v, 64 * b, t0, bh, &bar->full[s]);
+                    tma_load_3d(st + L::Q + b * kBlk, &tm_q, 64 * b, t0, bh, &bar->full[s]);
+                }
+                const size_t at = (size_t)bh * M + c;
+                bulk_load(st + L::mats, mats + at * kMats, kMats, &bar->full[s]);
+                bulk_load(st + L::gates, recs + at * kRec, kGateBytes, &bar->full[s]);
+                armed[s] = i;
+            }
+            // never leave with copies in flight: wait for the last armed phase of each stage
+            for (int s = 0; s < 2; ++s)
+                if (armed[s] >= 0) mbar_wait(&bar->full[s], (armed[s] >> 1) & 1, err, LA_ERR_TIMEOUT);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t id_k = idesc_bf16_f32(128, kC, 0, 0);   // [128 x 64], B K-major
+            constexpr uint32_t id_mn = idesc_bf16_f32(128, D, 0, 1);  // [128 x D], B MN-major
+            bool ok = true;
+            auto wait = [&](uint64_t* b, int parity) {
+                ok = ok && mbar_wait(b, parity, err, LA_ERR_TIMEOUT);
+                tc_fence_after();
+            };
+            for (int i = 0; i < nloc; ++i) {
+                const int s = i & 1, ph = i & 1;
+                const uint32_t st = smem_u32(base + s * L::stage);
+                const uint32_t aK = st + L::K, aQ = st + L::Q, aM = st + L::mats;
+                wait(&bar->full[s], (i >> 1) & 1);
+                wait(&bar->s_ready, ph);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)  // Y = S K^T
+                    mma_ts(tmem + T::Y, tmem + T::SHi + 8 * kk, desc_k(aK, kk), id_k, kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ts(tmem + T::Y, tmem + T::SLo + 8 * kk, desc_k(aK, kk), id_k, 1);
+                mma_commit(&bar->y_done);
+                if (i > 0) wait(&bar->o_free, ph ^ 1);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)  // O = S Q^T
+                    mma_ts(tmem + T::O, tmem + T::SHi + 8 * kk, desc_k(aQ, kk), id_k, kk > 0);
+                wait(&bar->r_ready, ph);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)  // X - R = (beta R) t^T, over the consumed Y
+                    mma_ts(tmem + T::Y, tmem + T::R + 8 * kk, desc_k(aM + kTHi, kk), id_k, kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts(tmem + T::Y, tmem + T::R + 32 + 8 * kk, desc_k(aM + kTHi, kk), id_k, 1);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts(tmem + T::Y, tmem + T::R + 8 * kk, desc_k(aM + kTLo, kk), id_k, 1);
+                mma_commit(&bar->x_done);
+                wait(&bar->u_ready, ph);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)  // the chunk's writes (tail u) K
+                    mma_ts(tmem + T::dS, tmem + T::R + 8 * kk, desc_mn(aK, kk), id_mn, kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts(tmem + T::dS, tmem + T::R + 32 + 8 * kk, desc_mn(aK, kk), id_mn, 1);
+                mma_commit(&bar->s_done);
+                wait(&bar->o_ready, ph);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)  // O (scaled by gam) += u P^T
+                    mma_ts(tmem + T::O, tmem + T::U + 8 * kk, desc_k(aM + kPHi, kk), id_k, 1);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts(tmem + T::O, tmem + T::U + 32 + 8 * kk, desc_k(aM + kPHi, kk), id_k, 1);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts(tmem + T::O, tmem + T::U + 8 * kk, desc_k(aM + kPLo, kk), id_k, 1);
+                mma_commit(&bar->o_done);
+                mma_commit(&bar->empty[s]);
+            }
+            // drain: every MMA this thread issued has completed before TMEM is released
+            mma_commit(&bar->final_mma);
+            mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
+        }
+    } else {
+        // ------------------------------------------------------------ compute warps
+        const int ct = tid - 64, h = ct >> 7;        // half: positions 32 h .., state columns kSc h ..
+        const int r = 32 * (warp & 3) + lane;        // TMEM lane: value column
+        const uint32_t lb = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        bool ok = true;
+        auto wait = [&](uint64_t* b, int parity) {
+            ok = ok && mbar_wait(b, parity, err, LA_ERR_TIMEOUT);
+            __syncwarp();
+            tc_fence_after();
+        };
+        auto arrive = [&](uint64_t* b) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b);
+        };
+        float S[kSc];
+#pragma unroll
+        for (int x = 0; x < kSc; ++x)
+            S[x] = S0 && r < D ? S0[((size_t)bh * D + kSc * h + x) * D + r] : 0.f;
+        auto put_state = [&]() {  // the state's hi and lo parts, and the signal that they are there
+            constexpr int kW = kSc / 2;
+            uint32_t hi[kW], lo[kW];
+#pragma unroll
+            for (int x = 0; x < kW; ++x) split2(S[2 * x], S[2 * x + 1], hi[x], lo[x]);
+            if constexpr (kW == 32) {
+                tmem_st32(lb + T::SHi + kW * h, hi);
+                tmem_st32(lb + T::SLo + kW * h, lo);
+            } else {
+                tmem_st16(lb + T::SHi + kW * h, hi);
+                tmem_st16(lb + T::SLo + kW * h, lo);
+            }
+            tmem_st_wait();
+            arrive(&bar->s_ready);
+        };
+        put_state();
+        uint8_t* sO = base + L::O;
+        for (int i = 0; i < nloc; ++i) {
+            const int s = i & 1, ph = i & 1, t0 = (cbeg + i) * kC;
+            uint8_t* st = base + s * L::stage;
+            const float* gam = reinterpret_cast<const float*>(st + L::gates) + 32 * h;
+            const float* tail = gam + kC;
+            const float* beta = gam + 2 * kC;
+            float R[32];
+            uint32_t w[32], hi[16], lo[16];
+            wait(&bar->full[s], (i >> 1) & 1);
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+                R[x] = r < D ? __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(
+                                                   st + L::V + elem_off(32 * h + x, r))
+                                               << 16)
+                             : 0.f;
+            wait(&bar->y_done, ph);
+            tmem_ld32(lb + T::Y + 32 * h, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+                R[x] = fmaf(-gam[x], __uint_as_float(w[x]), R[x]);
+                R[x + 1] = fmaf(-gam[x + 1], __uint_as_float(w[x + 1]), R[x + 1]);
+                split2(beta[x] * R[x], beta[x + 1] * R[x + 1], hi[x / 2], lo[x / 2]);
+            }
+            tmem_st16(lb + T::R + 16 * h, hi);
+            tmem_st16(lb + T::R + 32 + 16 * h, lo);
+            tmem_st_wait();
+            arrive(&bar->r_ready);
+            wait(&bar->x_done, ph);
+            tmem_ld32(lb + T::Y + 32 * h, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+                R[x] = beta[x] * (R[x] + __uint_as_float(w[x]));  // u
+                R[x + 1] = beta[x + 1] * (R[x + 1] + __uint_as_float(w[x + 1]));
+                split2(tail[x] * R[x], tail[x + 1] * R[x + 1], hi[x / 2], lo[x / 2]);
+            }
+            tmem_st16(lb + T::R + 16 * h, hi);
+            tmem_st16(lb + T::R + 32 + 16 * h, lo);
+            tmem_st_wait();
+            arrive(&bar->u_ready);
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) split2(R[x], R[x + 1], hi[x / 2], lo[x / 2]);
+            tmem_st16(lb + T::U + 16 * h, hi);
+            tmem_st16(lb + T::U + 32 + 16 * h, lo);
+            tmem_ld32(lb + T::O + 32 * h, w);  // S Q^T is complete: it was issued before X
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) w[x] = __float_as_uint(gam[x] * __uint_as_float(w[x]));
+            tmem_st32(lb + T::O + 32 * h, w);
+            tmem_st_wait();
+            arrive(&bar->o_ready);
+            const float gc = (gam - 32 * h)[kC - 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar->empty[s]);  // this warp is done with V and the gates
+            wait(&bar->s_done, ph);
+#pragma unroll
+            for (int cb = 0; cb < kSc / 32; ++cb) {
+                tmem_ld32(lb + T::dS + kSc * h + 32 * cb, w);
+                tmem_ld_wait();
+#pragma unroll
+                for (int x = 0; x < 32; ++x) S[32 * cb + x] = fmaf(gc, S[32 * cb + x], __uint_as_float(w[x]));
+            }
+            put_state();
+            // o: the tile is free once the previous store has read it
+            if (ct == 0) bulk_wait_read_all();
+            named_barrier(1, 32 * kWarps);
+            wait(&bar->o_done, ph);
+            tmem_ld32(lb + T::O + 32 * h, w);
+            tmem_ld_wait();
+            arrive(&bar->o_free);
+            if (r < D) {
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                    *reinterpret_cast<__nv_bfloat16*>(sO + elem_off(32 * h + x, r)) =
+                        __float2bfloat16_rn(__uint_as_float(w[x]));
+            }
+            fence_proxy_async_smem();
+            named_barrier(1, 32 * kWarps);
+            if (ct == 0) {
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b) tma_store_3d(&tm_o, sO + b * kBlk, 64 * b, t0, bh);
+                bulk_commit();
+            }
+        }
+        if (ct == 0) bulk_wait_all();
+        if (S_out && r < D) {
+#pragma unroll
+            for (int x = 0; x < kSc; ++x) S_out[((size_t)bh * D + kSc * h + x) * D + r] = S[x];
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes) {
+    return cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+#define GD_TRY(x)                         \
+    do {                                  \
+        const cudaError_t _e = (x);       \
+        if (_e != cudaSuccess) return _e; \
+    } while (0)
+
+template <int D>
+cudaError_t prepare(const CUtensorMap& tq, const CUtensorMap& tk, const void* g, const void* beta, float* recs,
+                    uint8_t* mats, const la_shape& s, int M, int* err, cudaStream_t st) {
+    GD_TRY(allow_smem(tc_gd_prepare<D>, kPrepBytes));
+    launch_begin("tc_gd_prepare", st);
+    const cudaError_t e =
+        launch_pdl(tc_gd_prepare<D>, dim3(M, s.B * s.H), dim3(kPrepThreads), kPrepBytes, st, tq, tk,
+                   (const __nv_bfloat16*)g, (const __nv_bfloat16*)beta, recs, mats, s.N, M, err);
+    const cudaError_t e2 = launch_end("tc_gd_prepare", st);
+    return e != cudaSuccess ? e : e2;
+}
+
+template <int D>
+cudaError_t fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) {
+    const int BH = s.B * s.H, M = (s.N + kC - 1) / kC;
+    CUtensorMap tq, tk, tv, to;
+    if (!make_tmap_bf16_rows(&tq, a.q, BH, s.N, D, kC) || !make_tmap_bf16_rows(&tk, a.k, BH, s.N, D, kC) ||
+        !make_tmap_bf16_rows(&tv, a.v, BH, s.N, D, kC) || !make_tmap_bf16_rows(&to, a.o, BH, s.N, D, kC))
+        return cudaErrorInvalidValue;
+    int* err = device_error_word();
+    const Layout L = layout(s, false);
+    float* recs = (float*)(ws + L.rec);
+    uint8_t* mats = (uint8_t*)(ws + L.t);
+    GD_TRY(prepare<D>(tq, tk, a.g, a.beta, recs, mats, s, M, err, st));
+    auto kern = tc_gd_states<D>;
+    GD_TRY(allow_smem(kern, FwdSmem<D>::bytes));
+    launch_begin("tc_gd_states", st);
+    const cudaError_t e = launch_pdl(kern, dim3(1, BH), dim3(kThreads), FwdSmem<D>::bytes, st, tq, tk, tv, to,
+                                     (const float*)recs, (const uint8_t*)mats, a.S0, a.S, M, M, err);
+    const cudaError_t e2 = launch_end("tc_gd_states", st);
+    return e != cudaSuccess ? e : e2;
+}
+
+}  // namespace
+
+bool tc_ok(const la_shape& s) { return s.dtype == LA_BF16 && s.Dk == s.Dv && (s.Dk == 64 || s.Dk == 128); }
+
+cudaError_t tc_fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) {
+    return s.Dk == 128 ? fwd<128>(a, s, ws, st) : fwd<64>(a, s, ws, st);
+}
+
+}  // namespace gd
+}  // namespace la

@@ -32,8 +32,9 @@ constexpr int kC = 64;
 // formed in fp64 and kept as hi + lo, so that differences of long sums keep fp32's precision; a decay
 // below exp(-100) (under fp32's normal range; -inf among them) is counted in kSeg instead of entering the sum,
 // and a product across it is 0.  Positions past the sequence's end have g = 0 and beta = 0.
-constexpr int kGam = 0, kTail = kC, kBeta = 2 * kC, kGhi = 3 * kC, kGlo = 4 * kC, kSeg = 5 * kC;
-constexpr int kRec = 6 * kC;
+constexpr int kGam = 0, kTail = kC, kBeta = 2 * kC, kBg = 3 * kC, kTb = 4 * kC;  // kBg = beta gam, kTb = tail beta
+constexpr int kGhi = 5 * kC, kGlo = 6 * kC, kSeg = 7 * kC;
+constexpr int kRec = 8 * kC;
 constexpr float kReset = -100.f;
 
 // exp(hi + lo) for |lo| at most half a step of hi.
@@ -59,7 +60,6 @@ __device__ __forceinline__ void gate_record(const T* __restrict__ g, const T* __
     for (int e = 0; e < 2; ++e) {
         const int i = 2 * lane + e;
         const float x = i < n ? to_f32(g[c0 + i]) : 0.f;
-        rec[kBeta + i] = i < n ? to_f32(beta[c0 + i]) : 0.f;
         const bool reset = x < kReset;
         v[e] = reset ? 0.0 : (double)x;
         r[e] = reset ? 1 : 0;
@@ -91,62 +91,89 @@ __device__ __forceinline__ void gate_record(const T* __restrict__ g, const T* __
         rec[kGhi + i] = hi;
         rec[kGlo + i] = lo;
         rec[kSeg + i] = (float)seg;
-        rec[kGam + i] = seg == 0 ? exp_hilo(hi, lo) : 0.f;
-        rec[kTail + i] = seg == rtot ? exp_hilo(dhi, dlo) : 0.f;
+        const float gam = seg == 0 ? exp_hilo(hi, lo) : 0.f, tail = seg == rtot ? exp_hilo(dhi, dlo) : 0.f;
+        const float b = i < n ? to_f32(beta[c0 + i]) : 0.f;
+        rec[kGam + i] = gam;
+        rec[kTail + i] = tail;
+        rec[kBeta + i] = b;
+        rec[kBg + i] = b * gam;
+        rec[kTb + i] = tail * b;
     }
 }
 
-// t = -A (I + beta A)^-1 for a strictly lower triangular A (zero on and above the diagonal), 64 x 64 fp32
-// in shared memory with row pitch ld, by 256 threads.  Row by row t_i = -(A_i + sum_(j<i) A_ij beta_j t_j)
-// (forward substitution) in blocks of 16: the diagonal blocks column by column, then the block rows below
-// them as products.  Every thread calls it; A is complete before and t after it.
-__device__ __forceinline__ void solve_t(const float* A, float* t, const float* beta, int ld, int tid) {
-    for (int i = tid; i < kC * kC; i += 256) {
-        const int r = i >> 6, c = i & 63;
-        if ((r >> 4) <= (c >> 4)) t[r * ld + c] = 0.f;  // the block rows below the diagonal are all written
+// t = -A (I + beta A)^-1 for a strictly lower triangular A (zero on and above the diagonal), 64 x 64 fp32 in
+// shared memory with row pitch kLd, by 256 threads.  Two diagonal blocks of 32 by forward substitution,
+// t_i = -(A_i + sum_(j<i) A_ij beta_j t_j), one column to a lane of one warp each, the column in registers; then
+// the block below them, t21 = -(I + t22 beta) A21 (I + beta t11), as two 32 x 32 x 32 products.  Every thread calls it; A (overwritten) is complete
+// before, t after.
+constexpr int kLd = kC + 4;
+
+__device__ __forceinline__ float4 ld_f4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
+__device__ __forceinline__ void solve_t(float* A, float* t, const float* beta, int tid) {
+    constexpr int kH = kC / 2;
+    if (tid < 64) {
+        const int b0 = tid & 32, c = tid & 31;
+        float y[kH];  // beta_j t_j of this column
+        t[b0 * kLd + b0 + c] = 0.f;
+        y[0] = 0.f;
+#pragma unroll
+        for (int r = 1; r < kH; ++r) {
+            const float* a = A + (b0 + r) * kLd + b0;
+            float s0 = a[c], s1 = 0.f;
+#pragma unroll
+            for (int j = 0; j < r; j += 4) {
+                const float4 v = ld_f4(a + j);  // broadcast; zero from the diagonal on
+                s0 = fmaf(v.x, y[j], s0);
+                if (j + 1 < r) s1 = fmaf(v.y, y[j + 1], s1);
+                if (j + 2 < r) s0 = fmaf(v.z, y[j + 2], s0);
+                if (j + 3 < r) s1 = fmaf(v.w, y[j + 3], s1);
+            }
+            const float x = r > c ? -(s0 + s1) : 0.f;
+            t[(b0 + r) * kLd + b0 + c] = x;
+            y[r] = beta[b0 + r] * x;
+        }
+    } else {
+        for (int i = tid - 64; i < kH * kH; i += 192) t[(i >> 5) * kLd + kH + (i & 31)] = 0.f;
     }
     __syncthreads();
-    if (tid < kC) {
-        const int b0 = tid & 48, c = tid & 15;
-        float x[16];
+    // this thread: row kH + r, columns c .. c + 3 of the lower left block
+    const int r = tid >> 3, c = 4 * (tid & 7);
+    float* row = A + (kH + r) * kLd;
+    float4 z = ld_f4(row + c);
 #pragma unroll
-        for (int r = 1; r < 16; ++r) {
-            float s = A[(b0 + r) * ld + b0 + c];
+    for (int k = 0; k < kH; k += 4) {
+        const float4 a = ld_f4(row + k);
+        const float av[4] = {a.x * beta[k], a.y * beta[k + 1], a.z * beta[k + 2], a.w * beta[k + 3]};
 #pragma unroll
-            for (int j = 1; j < r; ++j)
-                if (j > c) s = fmaf(A[(b0 + r) * ld + b0 + j] * beta[b0 + j], x[j], s);
-            x[r] = -s;
-            if (r > c) t[(b0 + r) * ld + b0 + c] = x[r];
+        for (int e = 0; e < 4; ++e) {
+            const float4 b = ld_f4(t + (k + e) * kLd + c);
+            z.x = fmaf(av[e], b.x, z.x);
+            z.y = fmaf(av[e], b.y, z.y);
+            z.z = fmaf(av[e], b.z, z.z);
+            z.w = fmaf(av[e], b.w, z.w);
         }
     }
     __syncthreads();
-    const int rr = tid >> 4, cc = tid & 15;
+    *reinterpret_cast<float4*>(row + c) = z;
+    __syncthreads();
+    const float* tr = t + (kH + r) * kLd + kH;
 #pragma unroll
-    for (int I = 1; I < 4; ++I) {
-        const int i = 16 * I + rr;
-        float rhs[3];
+    for (int k = 0; k < kH; k += 4) {
+        const float4 a = ld_f4(tr + k);
+        const float av[4] = {a.x * beta[kH + k], a.y * beta[kH + k + 1], a.z * beta[kH + k + 2],
+                             a.w * beta[kH + k + 3]};
 #pragma unroll
-        for (int J = 0; J < I; ++J) {
-            float s = A[i * ld + 16 * J + cc];
-            for (int k = 16 * J; k < 16 * I; ++k) s = fmaf(A[i * ld + k] * beta[k], t[k * ld + 16 * J + cc], s);
-            rhs[J] = s;
+        for (int e = 0; e < 4; ++e) {
+            const float4 b = ld_f4(A + (kH + k + e) * kLd + c);
+            z.x = fmaf(av[e], b.x, z.x);
+            z.y = fmaf(av[e], b.y, z.y);
+            z.z = fmaf(av[e], b.z, z.z);
+            z.w = fmaf(av[e], b.w, z.w);
         }
-#pragma unroll
-        for (int J = 0; J < I; ++J) t[i * ld + 16 * J + cc] = rhs[J];
-        __syncthreads();
-#pragma unroll
-        for (int J = 0; J < I; ++J) {
-            float s = rhs[J];
-#pragma unroll 4
-            for (int j = 0; j < 15; ++j)  // t is 0 from the diagonal on
-                s = fmaf(t[i * ld + 16 * I + j] * beta[16 * I + j], t[(16 * I + j) * ld + 16 * J + cc], s);
-            rhs[J] = -s;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int J = 0; J < I; ++J) t[i * ld + 16 * J + cc] = rhs[J];
-        __syncthreads();
     }
+    *reinterpret_cast<float4*>(t + (kH + r) * kLd + c) = make_float4(-z.x, -z.y, -z.z, -z.w);
+    __syncthreads();
 }
 
 // Byte offsets of the workspace regions of one call (256-byte aligned).

@@ -15,8 +15,8 @@
 // S^T Q^T, which meets one rounding only (it adds 0.5e-3 to the 1.7e-3 of rounding o itself; with
 // single parts throughout, correlated keys lift o's error to 7e-3 and the state's to 4e-3).
 //
-// Roles (320 threads): warp 0 issues TMA, warp 1 tcgen05.mma, warps 2-9 compute: warp w serves TMEM lanes
-// 32 (w % 4) .. +31 (value columns r), warps 2-5 positions 0-31 and state columns 0 .. D/2 - 1, warps 6-9 the others.
+// Roles (576 threads): warp 0 issues TMA, warp 1 tcgen05.mma, warps 2-17 compute: warp w serves TMEM lanes
+// 32 (w % 4) .. +31 (value columns r) and, by its group of four, 16 positions and D / 4 state columns of them.
 // Every wait is bounded: one that runs out records LA_ERR_TIMEOUT and its thread waits no more, so every role ends.
 #include <cudaTypedefs.h>
 
@@ -33,7 +33,7 @@ using tc::bf_lo;
 constexpr int kBlk = kC * 128;          // 64 rows x 64 bf16 columns, 128-byte swizzle
 constexpr int kMats = 4 * kBlk;         // t hi, t lo, P hi, P lo of a chunk
 constexpr int kTHi = 0, kTLo = kBlk, kPHi = 2 * kBlk, kPLo = 3 * kBlk;
-constexpr int kGateBytes = 3 * kC * 4;  // gam, tail, beta of the record
+constexpr int kGateBytes = 5 * kC * 4;  // gam, tail, beta, beta gam, tail beta of the record
 
 // Contiguous global -> shared copy (16-byte aligned, a multiple of 16 bytes).
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -79,8 +79,8 @@ constexpr int kPrepThreads = 256;
 struct PrepSmem {
     // offset 0: blocks of [Q rows 0-63; K rows 64-127] x 64 columns, then (once the product has read them) fp32 A
     static constexpr int A = 0;
-    static constexpr int T = A + kC * (kC + 1) * 4;
-    static constexpr int rec = T + kC * (kC + 1) * 4;  // beyond the tiles (32768 bytes)
+    static constexpr int T = A + kC * kLd * 4;
+    static constexpr int rec = T + kC * kLd * 4;  // beyond the tiles (32768 bytes)
     static constexpr int bar = rec + kRec * 4;
     static constexpr int total = bar + 32;
 };
@@ -145,7 +145,8 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         for (int x = 0; x < 32; ++x) {
             const int j = j0 + x;
             const bool in = (isP ? j <= i : j < i) && rec[kSeg + j] == seg;
-            w[x] = in ? __float_as_uint(__uint_as_float(w[x]) * exp_hilo(hi - rec[kGhi + j], lo - rec[kGlo + j])) : 0u;
+            const float d = (hi - rec[kGhi + j]) + (lo - rec[kGlo + j]);
+            w[x] = in ? __float_as_uint(__uint_as_float(w[x]) * ex2_approx(d * 1.4426950408889634f)) : 0u;
         }
         if (isP) {
 #pragma unroll
@@ -161,16 +162,17 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             }
         } else {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) A[i * (kC + 1) + j0 + x] = __uint_as_float(w[x]);
+            for (int x = 0; x < 32; x += 4)
+                *reinterpret_cast<uint4*>(A + i * kLd + j0 + x) = make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
         }
     }
     __syncthreads();
-    solve_t(A, T, rec + kBeta, kC + 1, tid);
+    solve_t(A, T, rec + kBeta, tid);
     {
         const int i = tid >> 2, j0 = 16 * (tid & 3);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const float* s = T + i * (kC + 1) + j0 + 8 * c;
+            const float* s = T + i * kLd + j0 + 8 * c;
             uint4 a, b;
             split2(s[0], s[1], a.x, b.x);
             split2(s[2], s[3], a.y, b.y);
@@ -192,8 +194,25 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 }
 
 // ------------------------------------------------------------------ the recurrence
-constexpr int kThreads = 320;
-constexpr int kWarps = 8;  // compute warps
+constexpr int kWarps = 16;  // compute warps
+constexpr int kThreads = 64 + 32 * kWarps;
+constexpr int kHs = kWarps / 4;   // column groups: a thread owns one row of one group
+constexpr int kTok = kC / kHs;    // positions of a thread
+
+template <int N>
+__device__ __forceinline__ void ld(uint32_t a, uint32_t (&r)[N]) {
+    static_assert(N == 8 || N == 16 || N == 32, "columns");
+    if constexpr (N == 8) tmem_ld8(a, r);
+    if constexpr (N == 16) tmem_ld16(a, r);
+    if constexpr (N == 32) tmem_ld32(a, r);
+}
+template <int N>
+__device__ __forceinline__ void st(uint32_t a, const uint32_t (&r)[N]) {
+    static_assert(N == 8 || N == 16 || N == 32, "columns");
+    if constexpr (N == 8) tmem_st8(a, r);
+    if constexpr (N == 16) tmem_st16(a, r);
+    if constexpr (N == 32) tmem_st32(a, r);
+}
 
 struct __align__(8) Bars {
     uint64_t full[2], empty[2];
@@ -204,7 +223,8 @@ template <int D>
 struct FwdSmem {
     static constexpr int tile = D / 64 * kBlk;
     static constexpr int K = 0, Q = tile, V = 2 * tile, mats = 3 * tile, gates = mats + kMats;
-    static constexpr int stage = gates + 1024;
+    static constexpr int stage = gates + 2048;
+    static_assert(kGateBytes <= 2048, "gates");
     static constexpr int O = 2 * stage;  // o tile for its TMA store
     static constexpr int bars = O + tile;
     static constexpr int slot = bars + 256;
@@ -216,8 +236,9 @@ static_assert(FwdSmem<128>::bytes <= 232448, "shared memory");
 // TMEM columns
 template <int D>
 struct Tm {
-    static constexpr uint32_t SHi = 0, SLo = D / 2, Y = D, R = D + 64, U = D + 128, dS = D + 192, O = 2 * D + 192;
-    static_assert(O + 64 <= 512, "TMEM");
+    static constexpr uint32_t SHi = 0, SLo = D / 2, Y = D, R = D + 64, U = D + 128, O = D + 192, dS = D + 256;
+    static constexpr uint32_t X = dS;  // two products of 64 columns, read before dS is written
+    static_assert(dS + 128 <= 512, "TMEM");
 };
 
 // Chunks [p cps, (p + 1) cps) of a head.  S0 / S_out: fp32 [BH][D][D] (null: zero / not wanted).
@@ -229,7 +250,7 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
              int cps, int* err) {
     using L = FwdSmem<D>;
     using T = Tm<D>;
-    constexpr int kSc = D / 2;  // state columns of a thread
+    constexpr int kSc = D / kHs;  // state columns of a thread
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Bars* bar = reinterpret_cast<Bars*>(base + L::bars);
@@ -289,16 +310,33 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0) {
             constexpr uint32_t id_k = idesc_bf16_f32(128, kC, 0, 0);   // [128 x 64], B K-major
+            constexpr uint32_t id_k2 = idesc_bf16_f32(128, 2 * kC, 0, 0);  // [128 x 128]
             constexpr uint32_t id_mn = idesc_bf16_f32(128, D, 0, 1);  // [128 x D], B MN-major
             bool ok = true;
             auto wait = [&](uint64_t* b, int parity) {
                 ok = ok && mbar_wait(b, parity, err, LA_ERR_TIMEOUT);
                 tc_fence_after();
             };
+            // O += u P^T of chunk j, issued while the next chunk's R is formed
+            auto outputs = [&](int j) {
+                const uint32_t aM = smem_u32(base + (j & 1) * L::stage) + L::mats;
+                wait(&bar->o_ready, j & 1);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts(tmem + T::O, tmem + T::U + 8 * kk, desc_k(aM + kPHi, kk), id_k, 1);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts(tmem + T::O, tmem + T::U + 32 + 8 * kk, desc_k(aM + kPHi, kk), id_k, 1);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts(tmem + T::O, tmem + T::U + 8 * kk, desc_k(aM + kPLo, kk), id_k, 1);
+                mma_commit(&bar->o_done);
+                mma_commit(&bar->empty[j & 1]);
+            };
             for (int i = 0; i < nloc; ++i) {
                 const int s = i & 1, ph = i & 1;
-                const uint32_t st = smem_u32(base + s * L::stage);
-                const uint32_t aK = st + L::K, aQ = st + L::Q, aM = st + L::mats;
+                const uint32_t sg = smem_u32(base + s * L::stage);
+                const uint32_t aK = sg + L::K, aQ = sg + L::Q, aM = sg + L::mats;
                 wait(&bar->full[s], (i >> 1) & 1);
                 wait(&bar->s_ready, ph);
 #pragma unroll
@@ -308,21 +346,19 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 for (int kk = 0; kk < D / 16; ++kk)
                     mma_ts(tmem + T::Y, tmem + T::SLo + 8 * kk, desc_k(aK, kk), id_k, 1);
                 mma_commit(&bar->y_done);
+                if (i > 0) outputs(i - 1);
+                wait(&bar->r_ready, ph);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)  // (beta R)_hi [t_hi; t_lo]^T: two products of 64 columns
+                    mma_ts(tmem + T::X, tmem + T::R + 8 * kk, desc_k(aM + kTHi, kk), id_k2, kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts(tmem + T::X, tmem + T::R + 32 + 8 * kk, desc_k(aM + kTHi, kk), id_k, 1);
+                mma_commit(&bar->x_done);
                 if (i > 0) wait(&bar->o_free, ph ^ 1);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)  // O = S Q^T
                     mma_ts(tmem + T::O, tmem + T::SHi + 8 * kk, desc_k(aQ, kk), id_k, kk > 0);
-                wait(&bar->r_ready, ph);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)  // X - R = (beta R) t^T, over the consumed Y
-                    mma_ts(tmem + T::Y, tmem + T::R + 8 * kk, desc_k(aM + kTHi, kk), id_k, kk > 0);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_ts(tmem + T::Y, tmem + T::R + 32 + 8 * kk, desc_k(aM + kTHi, kk), id_k, 1);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_ts(tmem + T::Y, tmem + T::R + 8 * kk, desc_k(aM + kTLo, kk), id_k, 1);
-                mma_commit(&bar->x_done);
                 wait(&bar->u_ready, ph);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)  // the chunk's writes (tail u) K
@@ -331,26 +367,15 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 for (int kk = 0; kk < 4; ++kk)
                     mma_ts(tmem + T::dS, tmem + T::R + 32 + 8 * kk, desc_mn(aK, kk), id_mn, 1);
                 mma_commit(&bar->s_done);
-                wait(&bar->o_ready, ph);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)  // O (scaled by gam) += u P^T
-                    mma_ts(tmem + T::O, tmem + T::U + 8 * kk, desc_k(aM + kPHi, kk), id_k, 1);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_ts(tmem + T::O, tmem + T::U + 32 + 8 * kk, desc_k(aM + kPHi, kk), id_k, 1);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_ts(tmem + T::O, tmem + T::U + 8 * kk, desc_k(aM + kPLo, kk), id_k, 1);
-                mma_commit(&bar->o_done);
-                mma_commit(&bar->empty[s]);
             }
+            outputs(nloc - 1);
             // drain: every MMA this thread issued has completed before TMEM is released
             mma_commit(&bar->final_mma);
             mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
         }
     } else {
         // ------------------------------------------------------------ compute warps
-        const int ct = tid - 64, h = ct >> 7;        // half: positions 32 h .., state columns kSc h ..
+        const int ct = tid - 64, h = ct >> 7;        // group: positions kTok h .., state columns kSc h ..
         const int r = 32 * (warp & 3) + lane;        // TMEM lane: value column
         const uint32_t lb = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         bool ok = true;
@@ -369,107 +394,138 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         for (int x = 0; x < kSc; ++x)
             S[x] = S0 && r < D ? S0[((size_t)bh * D + kSc * h + x) * D + r] : 0.f;
         auto put_state = [&]() {  // the state's hi and lo parts, and the signal that they are there
-            constexpr int kW = kSc / 2;
-            uint32_t hi[kW], lo[kW];
+            uint32_t hi[kSc / 2], lo[kSc / 2];
 #pragma unroll
-            for (int x = 0; x < kW; ++x) split2(S[2 * x], S[2 * x + 1], hi[x], lo[x]);
-            if constexpr (kW == 32) {
-                tmem_st32(lb + T::SHi + kW * h, hi);
-                tmem_st32(lb + T::SLo + kW * h, lo);
-            } else {
-                tmem_st16(lb + T::SHi + kW * h, hi);
-                tmem_st16(lb + T::SLo + kW * h, lo);
-            }
+            for (int x = 0; x < kSc / 2; ++x) split2(S[2 * x], S[2 * x + 1], hi[x], lo[x]);
+            st(lb + T::SHi + kSc / 2 * h, hi);
+            st(lb + T::SLo + kSc / 2 * h, lo);
             tmem_st_wait();
             arrive(&bar->s_ready);
         };
         put_state();
         uint8_t* sO = base + L::O;
-        for (int i = 0; i < nloc; ++i) {
-            const int s = i & 1, ph = i & 1, t0 = (cbeg + i) * kC;
-            uint8_t* st = base + s * L::stage;
-            const float* gam = reinterpret_cast<const float*>(st + L::gates) + 32 * h;
-            const float* tail = gam + kC;
-            const float* beta = gam + 2 * kC;
-            float R[32];
-            uint32_t w[32], hi[16], lo[16];
-            wait(&bar->full[s], (i >> 1) & 1);
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-                R[x] = r < D ? __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(
-                                                   st + L::V + elem_off(32 * h + x, r))
-                                               << 16)
-                             : 0.f;
-            wait(&bar->y_done, ph);
-            tmem_ld32(lb + T::Y + 32 * h, w);
-            tmem_ld_wait();
-#pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-                R[x] = fmaf(-gam[x], __uint_as_float(w[x]), R[x]);
-                R[x + 1] = fmaf(-gam[x + 1], __uint_as_float(w[x + 1]), R[x + 1]);
-                split2(beta[x] * R[x], beta[x + 1] * R[x + 1], hi[x / 2], lo[x / 2]);
-            }
-            tmem_st16(lb + T::R + 16 * h, hi);
-            tmem_st16(lb + T::R + 32 + 16 * h, lo);
-            tmem_st_wait();
-            arrive(&bar->r_ready);
-            wait(&bar->x_done, ph);
-            tmem_ld32(lb + T::Y + 32 * h, w);
-            tmem_ld_wait();
-#pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-                R[x] = beta[x] * (R[x] + __uint_as_float(w[x]));  // u
-                R[x + 1] = beta[x + 1] * (R[x + 1] + __uint_as_float(w[x + 1]));
-                split2(tail[x] * R[x], tail[x + 1] * R[x + 1], hi[x / 2], lo[x / 2]);
-            }
-            tmem_st16(lb + T::R + 16 * h, hi);
-            tmem_st16(lb + T::R + 32 + 16 * h, lo);
-            tmem_st_wait();
-            arrive(&bar->u_ready);
-#pragma unroll
-            for (int x = 0; x < 32; x += 2) split2(R[x], R[x + 1], hi[x / 2], lo[x / 2]);
-            tmem_st16(lb + T::U + 16 * h, hi);
-            tmem_st16(lb + T::U + 32 + 16 * h, lo);
-            tmem_ld32(lb + T::O + 32 * h, w);  // S Q^T is complete: it was issued before X
-            tmem_ld_wait();
-#pragma unroll
-            for (int x = 0; x < 32; ++x) w[x] = __float_as_uint(gam[x] * __uint_as_float(w[x]));
-            tmem_st32(lb + T::O + 32 * h, w);
-            tmem_st_wait();
-            arrive(&bar->o_ready);
-            const float gc = (gam - 32 * h)[kC - 1];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar->empty[s]);  // this warp is done with V and the gates
-            wait(&bar->s_done, ph);
-#pragma unroll
-            for (int cb = 0; cb < kSc / 32; ++cb) {
-                tmem_ld32(lb + T::dS + kSc * h + 32 * cb, w);
-                tmem_ld_wait();
-#pragma unroll
-                for (int x = 0; x < 32; ++x) S[32 * cb + x] = fmaf(gc, S[32 * cb + x], __uint_as_float(w[x]));
-            }
-            put_state();
-            // o: the tile is free once the previous store has read it
+        auto output = [&](int j) {  // o of chunk j
+            // the tile is free once the previous store has read it
             if (ct == 0) bulk_wait_read_all();
             named_barrier(1, 32 * kWarps);
-            wait(&bar->o_done, ph);
-            tmem_ld32(lb + T::O + 32 * h, w);
+            wait(&bar->o_done, j & 1);
+            uint32_t w[kTok];
+            ld(lb + T::O + kTok * h, w);
             tmem_ld_wait();
             arrive(&bar->o_free);
             if (r < D) {
 #pragma unroll
-                for (int x = 0; x < 32; ++x)
-                    *reinterpret_cast<__nv_bfloat16*>(sO + elem_off(32 * h + x, r)) =
+                for (int x = 0; x < kTok; ++x)
+                    *reinterpret_cast<__nv_bfloat16*>(sO + elem_off(kTok * h + x, r)) =
                         __float2bfloat16_rn(__uint_as_float(w[x]));
             }
             fence_proxy_async_smem();
             named_barrier(1, 32 * kWarps);
             if (ct == 0) {
 #pragma unroll
-                for (int b = 0; b < D / 64; ++b) tma_store_3d(&tm_o, sO + b * kBlk, 64 * b, t0, bh);
+                for (int b = 0; b < D / 64; ++b) tma_store_3d(&tm_o, sO + b * kBlk, 64 * b, (cbeg + j) * kC, bh);
                 bulk_commit();
             }
+        };
+        for (int i = 0; i < nloc; ++i) {
+            const int s = i & 1, ph = i & 1;
+            uint8_t* sg = base + s * L::stage;
+            const float* gates = reinterpret_cast<const float*>(sg + L::gates);
+            // a gate of this thread's positions x .. x + 3
+            auto gate = [&](int which, int x) { return ld_f4(gates + which + kTok * h + x); };
+            float R[kTok];  // beta V, beta R, then tail beta R
+            uint32_t w[kTok], hi[kTok / 2], lo[kTok / 2];
+            wait(&bar->full[s], (i >> 1) & 1);
+#pragma unroll
+            for (int x = 0; x < kTok; x += 4) {
+                const float4 b = gate(kBeta, x);
+                const float bb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    R[x + e] = r < D ? bb[e] * __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(
+                                                                   sg + L::V + elem_off(kTok * h + x + e, r))
+                                                               << 16)
+                                     : 0.f;
+            }
+            wait(&bar->y_done, ph);
+            ld(lb + T::Y + kTok * h, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < kTok; x += 4) {
+                const float4 b = gate(kBg, x);
+                R[x] = fmaf(-b.x, __uint_as_float(w[x]), R[x]);
+                R[x + 1] = fmaf(-b.y, __uint_as_float(w[x + 1]), R[x + 1]);
+                R[x + 2] = fmaf(-b.z, __uint_as_float(w[x + 2]), R[x + 2]);
+                R[x + 3] = fmaf(-b.w, __uint_as_float(w[x + 3]), R[x + 3]);
+                split2(R[x], R[x + 1], hi[x / 2], lo[x / 2]);
+                split2(R[x + 2], R[x + 3], hi[x / 2 + 1], lo[x / 2 + 1]);
+            }
+            st(lb + T::R + kTok / 2 * h, hi);
+            st(lb + T::R + 32 + kTok / 2 * h, lo);
+            tmem_st_wait();
+            arrive(&bar->r_ready);
+            if (i > 0) output(i - 1);
+            wait(&bar->x_done, ph);
+            {
+                uint32_t w2[kTok];
+                ld(lb + T::X + kTok * h, w);
+                ld(lb + T::X + kC + kTok * h, w2);
+                tmem_ld_wait();
+#pragma unroll
+                for (int x = 0; x < kTok; x += 4) {
+                    const float4 tb = gate(kTb, x), tl = gate(kTail, x);
+                    const float tbv[4] = {tb.x, tb.y, tb.z, tb.w}, tlv[4] = {tl.x, tl.y, tl.z, tl.w};
+                    float u[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float d = __uint_as_float(w[x + e]) + __uint_as_float(w2[x + e]);
+                        w[x + e] = __float_as_uint(d);
+                        u[e] = fmaf(tbv[e], d, tlv[e] * R[x + e]);
+                    }
+                    split2(u[0], u[1], hi[x / 2], lo[x / 2]);
+                    split2(u[2], u[3], hi[x / 2 + 1], lo[x / 2 + 1]);
+                }
+            }
+            st(lb + T::R + kTok / 2 * h, hi);
+            st(lb + T::R + 32 + kTok / 2 * h, lo);
+            tmem_st_wait();
+            arrive(&bar->u_ready);
+#pragma unroll
+            for (int x = 0; x < kTok; x += 4) {
+                const float4 b = gate(kBeta, x);
+                split2(fmaf(b.x, __uint_as_float(w[x]), R[x]), fmaf(b.y, __uint_as_float(w[x + 1]), R[x + 1]),
+                       hi[x / 2], lo[x / 2]);
+                split2(fmaf(b.z, __uint_as_float(w[x + 2]), R[x + 2]), fmaf(b.w, __uint_as_float(w[x + 3]), R[x + 3]),
+                       hi[x / 2 + 1], lo[x / 2 + 1]);
+            }
+            st(lb + T::U + kTok / 2 * h, hi);
+            st(lb + T::U + 32 + kTok / 2 * h, lo);
+            const float gc = gates[kGam + kC - 1];
+            wait(&bar->s_done, ph);
+            {
+                uint32_t d[kSc];
+                ld(lb + T::dS + kSc * h, d);
+                tmem_ld_wait();
+#pragma unroll
+                for (int x = 0; x < kSc; ++x) S[x] = fmaf(gc, S[x], __uint_as_float(d[x]));
+            }
+            put_state();
+            ld(lb + T::O + kTok * h, w);  // S Q^T is complete: it was issued before dS
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < kTok; x += 4) {
+                const float4 g = gate(kGam, x);
+                w[x] = __float_as_uint(g.x * __uint_as_float(w[x]));
+                w[x + 1] = __float_as_uint(g.y * __uint_as_float(w[x + 1]));
+                w[x + 2] = __float_as_uint(g.z * __uint_as_float(w[x + 2]));
+                w[x + 3] = __float_as_uint(g.w * __uint_as_float(w[x + 3]));
+            }
+            st(lb + T::O + kTok * h, w);
+            tmem_st_wait();
+            arrive(&bar->o_ready);
+            if (lane == 0) mbar_arrive(&bar->empty[s]);  // this warp is done with V and the gates
         }
+        output(nloc - 1);
         if (ct == 0) bulk_wait_all();
         if (S_out && r < D) {
 #pragma unroll

@@ -42,12 +42,52 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
         "l"(src), "r"(bytes), "r"(smem_u32(bar))
         : "memory");
 }
-// Operands of 64-row tiles: K-major (rows are M or N) and MN-major (rows are K), K step kk of 16.
-__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int kk) {
-    return smem_desc_sw128(tile + (kk >> 2) * kBlk + (kk & 3) * 32, 16, 1024);
+// Shared-memory operands, as the low word of their descriptors (address and leading offset, in units of 16 bytes;
+// the high word is the same for all): K-major (rows are M or N) and MN-major (rows are K) tiles, K step kk of 16.  A
+// whole warp runs the issuing role and one elected lane issues, so that these words stay in uniform registers: with the
+// role in a one-lane branch an instruction cost about 90 cycles to issue, more than it takes to run.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+template <int kLead = 16>
+__device__ __forceinline__ uint32_t tile_desc(uint32_t addr) {
+    return ((addr & 0x3FFFFu) >> 4) | ((uint32_t)(kLead >> 4) << 16);
 }
-__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int kk) {
-    return smem_desc_sw128(tile + kk * 2048, kBlk, 1024);
+__device__ __forceinline__ constexpr uint32_t step_k(int kk, int blk = kBlk) { return ((kk >> 2) * blk + (kk & 3) * 32) >> 4; }
+__device__ __forceinline__ constexpr uint32_t step_mn(int kk) { return (kk * 2048) >> 4; }
+
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p;
+}
+// D[tmem] (+)= A[tmem] B[smem], and with both in shared memory, by the elected lane of a converged warp.
+__device__ __forceinline__ void mma_ts1(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 bd;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 bd, {%2, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"(lead), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ss1(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 ad, bd;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 ad, {%1, %4};\n\tmov.b64 bd, {%2, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"(lead), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void commit1(uint32_t lead, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
 }
 // Byte offset of (row, column c) in 64-column blocks of kC rows.
 __device__ __forceinline__ int elem_off(int row, int c) {
@@ -308,69 +348,72 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        {
+            const uint32_t lead = elect_one();
             constexpr uint32_t id_k = idesc_bf16_f32(128, kC, 0, 0);   // [128 x 64], B K-major
             constexpr uint32_t id_k2 = idesc_bf16_f32(128, 2 * kC, 0, 0);  // [128 x 128]
             constexpr uint32_t id_mn = idesc_bf16_f32(128, D, 0, 1);  // [128 x D], B MN-major
             bool ok = true;
             auto wait = [&](uint64_t* b, int parity) {
                 ok = ok && mbar_wait(b, parity, err, LA_ERR_TIMEOUT);
+                __syncwarp();
                 tc_fence_after();
             };
             // O += u P^T of chunk j, issued while the next chunk's R is formed
             auto outputs = [&](int j) {
-                const uint32_t aM = smem_u32(base + (j & 1) * L::stage) + L::mats;
+                const uint32_t dM = tile_desc(smem_u32(base + (j & 1) * L::stage) + L::mats);
                 wait(&bar->o_ready, j & 1);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_ts(tmem + T::O, tmem + T::U + 8 * kk, desc_k(aM + kPHi, kk), id_k, 1);
+                    mma_ts1(lead, tmem + T::O, tmem + T::U + 8 * kk, dM + (kPHi >> 4) + step_k(kk), id_k, 1);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_ts(tmem + T::O, tmem + T::U + 32 + 8 * kk, desc_k(aM + kPHi, kk), id_k, 1);
+                    mma_ts1(lead, tmem + T::O, tmem + T::U + 32 + 8 * kk, dM + (kPHi >> 4) + step_k(kk), id_k, 1);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_ts(tmem + T::O, tmem + T::U + 8 * kk, desc_k(aM + kPLo, kk), id_k, 1);
-                mma_commit(&bar->o_done);
-                mma_commit(&bar->empty[j & 1]);
+                    mma_ts1(lead, tmem + T::O, tmem + T::U + 8 * kk, dM + (kPLo >> 4) + step_k(kk), id_k, 1);
+                commit1(lead, &bar->o_done);
+                commit1(lead, &bar->empty[j & 1]);
             };
             for (int i = 0; i < nloc; ++i) {
                 const int s = i & 1, ph = i & 1;
                 const uint32_t sg = smem_u32(base + s * L::stage);
-                const uint32_t aK = sg + L::K, aQ = sg + L::Q, aM = sg + L::mats;
+                const uint32_t dK = tile_desc(sg + L::K), dQ = tile_desc(sg + L::Q), dM = tile_desc(sg + L::mats);
+                const uint32_t dKmn = tile_desc<kBlk>(sg + L::K);
                 wait(&bar->full[s], (i >> 1) & 1);
                 wait(&bar->s_ready, ph);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)  // Y = S K^T
-                    mma_ts(tmem + T::Y, tmem + T::SHi + 8 * kk, desc_k(aK, kk), id_k, kk > 0);
+                    mma_ts1(lead, tmem + T::Y, tmem + T::SHi + 8 * kk, dK + step_k(kk), id_k, kk > 0);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_ts(tmem + T::Y, tmem + T::SLo + 8 * kk, desc_k(aK, kk), id_k, 1);
-                mma_commit(&bar->y_done);
+                    mma_ts1(lead, tmem + T::Y, tmem + T::SLo + 8 * kk, dK + step_k(kk), id_k, 1);
+                commit1(lead, &bar->y_done);
                 if (i > 0) outputs(i - 1);
                 wait(&bar->r_ready, ph);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)  // (beta R)_hi [t_hi; t_lo]^T: two products of 64 columns
-                    mma_ts(tmem + T::X, tmem + T::R + 8 * kk, desc_k(aM + kTHi, kk), id_k2, kk > 0);
+                    mma_ts1(lead, tmem + T::X, tmem + T::R + 8 * kk, dM + step_k(kk), id_k2, kk > 0);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_ts(tmem + T::X, tmem + T::R + 32 + 8 * kk, desc_k(aM + kTHi, kk), id_k, 1);
-                mma_commit(&bar->x_done);
+                    mma_ts1(lead, tmem + T::X, tmem + T::R + 32 + 8 * kk, dM + step_k(kk), id_k, 1);
+                commit1(lead, &bar->x_done);
                 if (i > 0) wait(&bar->o_free, ph ^ 1);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)  // O = S Q^T
-                    mma_ts(tmem + T::O, tmem + T::SHi + 8 * kk, desc_k(aQ, kk), id_k, kk > 0);
+                    mma_ts1(lead, tmem + T::O, tmem + T::SHi + 8 * kk, dQ + step_k(kk), id_k, kk > 0);
                 wait(&bar->u_ready, ph);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)  // the chunk's writes (tail u) K
-                    mma_ts(tmem + T::dS, tmem + T::R + 8 * kk, desc_mn(aK, kk), id_mn, kk > 0);
+                    mma_ts1(lead, tmem + T::dS, tmem + T::R + 8 * kk, dKmn + step_mn(kk), id_mn, kk > 0);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_ts(tmem + T::dS, tmem + T::R + 32 + 8 * kk, desc_mn(aK, kk), id_mn, 1);
-                mma_commit(&bar->s_done);
+                    mma_ts1(lead, tmem + T::dS, tmem + T::R + 32 + 8 * kk, dKmn + step_mn(kk), id_mn, 1);
+                commit1(lead, &bar->s_done);
             }
             outputs(nloc - 1);
             // drain: every MMA this thread issued has completed before TMEM is released
-            mma_commit(&bar->final_mma);
+            commit1(lead, &bar->final_mma);
             mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
         }
     } else {

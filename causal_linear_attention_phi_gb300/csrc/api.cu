@@ -694,7 +694,9 @@ la_status la_gated_delta_bwd(const void* q, const void* k, const void* v, const 
     LA_TRY(check_ptr(dbeta, "dbeta", elem));
     LA_TRY(check_ws(ws, ws_bytes, gd::layout(s, true).bytes));
     const gd::BwdArgs a{q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta};
-    return cuda_status(gd::simt_bwd(a, s, static_cast<char*>(ws), reinterpret_cast<cudaStream_t>(stream)),
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return cuda_status(gd::tc_ok(s) ? gd::tc_bwd(a, s, static_cast<char*>(ws), st)
+                                    : gd::simt_bwd(a, s, static_cast<char*>(ws), st),
                        "gated delta backward");
 }
 
@@ -786,7 +788,7 @@ la_status la_last_error(void) {
             static const char* const kFiles[] = {"api.cu", "decode.cu", "gated_delta.cu", "gated_delta_step.cu",
                                                  "gated_delta.cuh", "host_step.cu", "layer_norm.cu", "noalloc.cu",
                                                  "retention.cu",
-                                                 "selftest.cu", "simt_kernels.cu", "tc_gated_delta.cu", "tc_apply.cu", "tc_bwd.cu",
+                                                 "selftest.cu", "simt_kernels.cu", "tc_gated_delta.cu", "tc_gated_delta_bwd.cu", "tc_gated_delta.cuh", "tc_apply.cu", "tc_bwd.cu",
                                                  "tc_fwd.cu", "tc_noncausal_bwd.cu", "tc_retention.cu",
                                                  "la_internal.cuh", "simt_common.cuh", "tc_common.cuh", "sm100.cuh"};
             const char* file = "unknown file";

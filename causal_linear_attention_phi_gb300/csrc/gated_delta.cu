@@ -566,9 +566,10 @@ Layout layout(const la_shape& s, bool bwd) {
     L.P = L.t + chunks * kC * kC * sizeof(float);
     if (bwd) {
         L.X = take(chunks * kC * s.Dv);
+        const size_t half = tc_ok(s) ? 2 : 1;  // the states in bf16
         L.Y = take(chunks * kC * s.Dv);
-        L.S = take(chunks * s.Dk * s.Dv);
-        L.dS = take(chunks * s.Dk * s.Dv);
+        L.S = take(chunks * s.Dk * s.Dv / half);
+        L.dS = take(chunks * s.Dk * s.Dv / half);
     }
     L.bytes = off;
     return L;

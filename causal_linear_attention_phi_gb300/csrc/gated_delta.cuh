@@ -180,8 +180,9 @@ __device__ __forceinline__ void solve_t(float* A, float* t, const float* beta, i
 struct Layout {
     size_t rec;     // [BH][M][kRec] fp32 gate records
     size_t t, P;    // [BH][M][64][64] fp32 (tensor cores: t hi, t lo, P hi, P lo as bf16 in the bytes of t and P)
-    size_t X, Y;    // [BH][M * 64][Dv] fp32 (gradient)
-    size_t S, dS;   // [BH][M][Dk][Dv] fp32: the state entering each chunk, the gradient leaving it (gradient)
+    // The gradient's, fp32 (tensor cores: bf16 tiles of transposed matrices, X and Y as lo and hi parts):
+    size_t X, Y;    // [BH][M * 64][Dv]
+    size_t S, dS;   // [BH][M][Dk][Dv]: the state entering each chunk, the gradient leaving it
     size_t bytes;
 };
 Layout layout(const la_shape& s, bool bwd);
@@ -202,6 +203,7 @@ cudaError_t simt_bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t
 // bf16 heads with Dk = Dv = 64 or 128, on the tensor cores.
 bool tc_ok(const la_shape& s);
 cudaError_t tc_fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st);
+cudaError_t tc_bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st);
 cudaError_t step(const void* q, const void* k, const void* v, const void* g, const void* beta, float* S, void* out,
                  const la_shape& s, cudaStream_t st);
 

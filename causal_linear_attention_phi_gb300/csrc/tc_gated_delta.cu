@@ -20,99 +20,13 @@
 // Every wait is bounded: one that runs out records LA_ERR_TIMEOUT and its thread waits no more, so every role ends.
 #include <cudaTypedefs.h>
 
-#include "gated_delta.cuh"
-#include "tc_common.cuh"
+#include "tc_gated_delta.cuh"
 
 namespace la {
 namespace gd {
 namespace {
 using namespace sm100;
-using tc::bf_hi;
-using tc::bf_lo;
-
-constexpr int kBlk = kC * 128;          // 64 rows x 64 bf16 columns, 128-byte swizzle
-constexpr int kMats = 4 * kBlk;         // t hi, t lo, P hi, P lo of a chunk
-constexpr int kTHi = 0, kTLo = kBlk, kPHi = 2 * kBlk, kPLo = 3 * kBlk;
-constexpr int kGateBytes = 5 * kC * 4;  // gam, tail, beta, beta gam, tail beta of the record
-
-// Contiguous global -> shared copy (16-byte aligned, a multiple of 16 bytes).
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar))
-        : "memory");
-}
-// Shared-memory operands, as the low word of their descriptors (address and leading offset, in units of 16 bytes;
-// the high word is the same for all): K-major (rows are M or N) and MN-major (rows are K) tiles, K step kk of 16.  A
-// whole warp runs the issuing role and one elected lane issues, so that these words stay in uniform registers: with the
-// role in a one-lane branch an instruction cost about 90 cycles to issue, more than it takes to run.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-template <int kLead = 16>
-__device__ __forceinline__ uint32_t tile_desc(uint32_t addr) {
-    return ((addr & 0x3FFFFu) >> 4) | ((uint32_t)(kLead >> 4) << 16);
-}
-__device__ __forceinline__ constexpr uint32_t step_k(int kk, int blk = kBlk) { return ((kk >> 2) * blk + (kk & 3) * 32) >> 4; }
-__device__ __forceinline__ constexpr uint32_t step_mn(int kk) { return (kk * 2048) >> 4; }
-
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t p;
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "elect.sync _|q, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(p));
-    return p;
-}
-// D[tmem] (+)= A[tmem] B[smem], and with both in shared memory, by the elected lane of a converged warp.
-__device__ __forceinline__ void mma_ts1(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 bd;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "mov.b64 bd, {%2, %4};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"(lead), "r"(acc)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ss1(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 ad, bd;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "mov.b64 ad, {%1, %4};\n\tmov.b64 bd, {%2, %4};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"(lead), "r"(acc)
-        : "memory");
-}
-__device__ __forceinline__ void commit1(uint32_t lead, uint64_t* bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-        "r"(lead)
-        : "memory");
-}
-// Byte offset of (row, column c) in 64-column blocks of kC rows.
-__device__ __forceinline__ int elem_off(int row, int c) {
-    return (c >> 6) * kBlk + row * 128 + ((((c >> 3) & 7) ^ (row & 7)) << 4) + (c & 7) * 2;
-}
-// Every kernel here starts so: wait for the previous grid, take the TMEM columns, and only then let the next
-// grid's blocks be scheduled.  Blocks of several of these kernels fit on one SM: none holds columns while it
-// waits for a grid, and none is still to take its columns when a block that waits for it can arrive.
-__device__ __forceinline__ uint32_t enter(uint32_t* slot, uint32_t cols, int warp) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (warp == 1) {
-        tmem_alloc(slot, cols);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    return *slot;
-}
-// a, b -> packed bf16 hi and lo parts.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = pack_bf16x2(a, b);
-    lo = pack_bf16x2(a - bf_lo(hi), b - bf_hi(hi));
-}
+using namespace tcgd;
 
 // ------------------------------------------------------------------ t and P of every chunk
 constexpr int kPrepThreads = 256;
@@ -234,44 +148,30 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 }
 
 // ------------------------------------------------------------------ the recurrence
-constexpr int kWarps = 16;  // compute warps
-constexpr int kThreads = 64 + 32 * kWarps;
-constexpr int kHs = kWarps / 4;   // column groups: a thread owns one row of one group
-constexpr int kTok = kC / kHs;    // positions of a thread
-
-template <int N>
-__device__ __forceinline__ void ld(uint32_t a, uint32_t (&r)[N]) {
-    static_assert(N == 8 || N == 16 || N == 32, "columns");
-    if constexpr (N == 8) tmem_ld8(a, r);
-    if constexpr (N == 16) tmem_ld16(a, r);
-    if constexpr (N == 32) tmem_ld32(a, r);
-}
-template <int N>
-__device__ __forceinline__ void st(uint32_t a, const uint32_t (&r)[N]) {
-    static_assert(N == 8 || N == 16 || N == 32, "columns");
-    if constexpr (N == 8) tmem_st8(a, r);
-    if constexpr (N == 16) tmem_st16(a, r);
-    if constexpr (N == 32) tmem_st32(a, r);
-}
-
 struct __align__(8) Bars {
     uint64_t full[2], empty[2];
     uint64_t s_ready, y_done, r_ready, x_done, u_ready, s_done, o_ready, o_done, o_free, final_mma;
 };
 
-template <int D>
+// kOut: outputs.  kGrad: the gradient's records instead, for each chunk the state entering it (s_tiles, S^T as
+// [Dv rows x Dk] bf16 tiles of 64 columns) and X (x_tiles, lo then hi, X^T as [Dv rows x 64 positions]).
+enum Mode { kOut, kGrad };
+
+template <int D, int kMode>
 struct FwdSmem {
-    static constexpr int tile = D / 64 * kBlk;
-    static constexpr int K = 0, Q = tile, V = 2 * tile, mats = 3 * tile, gates = mats + kMats;
+    static constexpr int tile = D / 64 * kBlk, nmats = kMode == kOut ? kMats : 2 * kBlk;
+    // a stage: K, V, t (and P), Q, gates
+    static constexpr int K = 0, V = tile, mats = 2 * tile, Q = mats + nmats, gates = Q + (kMode == kOut ? tile : 0);
     static constexpr int stage = gates + 2048;
     static_assert(kGateBytes <= 2048, "gates");
-    static constexpr int O = 2 * stage;  // o tile for its TMA store
-    static constexpr int bars = O + tile;
+    static constexpr int out = 2 * stage;  // kOut: the o tile; kGrad: the state's tile and X lo, X hi
+    static constexpr int sbytes = D * D * 2, xbytes = 2 * D * 128;
+    static constexpr int bars = out + (kMode == kOut ? tile : sbytes + xbytes);
     static constexpr int slot = bars + 256;
     static constexpr int total = slot + 16;
     static constexpr size_t bytes = total + 1024;
+    static_assert(bytes <= 232448, "shared memory");
 };
-static_assert(FwdSmem<128>::bytes <= 232448, "shared memory");
 
 // TMEM columns
 template <int D>
@@ -282,13 +182,13 @@ struct Tm {
 };
 
 // Chunks [p cps, (p + 1) cps) of a head.  S0 / S_out: fp32 [BH][D][D] (null: zero / not wanted).
-template <int D>
+template <int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-             const float* __restrict__ recs, const uint8_t* __restrict__ mats, const float* S0, float* S_out, int M,
-             int cps, int* err) {
-    using L = FwdSmem<D>;
+             const float* __restrict__ recs, const uint8_t* __restrict__ mats, const float* S0, float* S_out,
+             uint8_t* __restrict__ x_tiles, uint8_t* __restrict__ s_tiles, int M, int cps, int* err) {
+    using L = FwdSmem<D, kMode>;
     using T = Tm<D>;
     constexpr int kSc = D / kHs;  // state columns of a thread
     extern __shared__ uint8_t smem_raw[];
@@ -330,15 +230,15 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 const int s = i & 1, c = cbeg + i, t0 = c * kC;
                 uint8_t* st = base + s * L::stage;
                 if (!mbar_wait(&bar->empty[s], ((i >> 1) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
-                mbar_arrive_expect_tx(&bar->full[s], 3 * L::tile + kMats + kGateBytes);
+                mbar_arrive_expect_tx(&bar->full[s], (kMode == kOut ? 3 * L::tile + kMats : 2 * L::tile + 2 * kBlk) + kGateBytes);
 #pragma unroll
                 for (int b = 0; b < D / 64; ++b) {
                     tma_load_3d(st + L::K + b * kBlk, &tm_k, 64 * b, t0, bh, &bar->full[s]);
                     tma_load_3d(st + L::V + b * kBlk, &tm_v, 64 * b, t0, bh, &bar->full[s]);
-                    tma_load_3d(st + L::Q + b * kBlk, &tm_q, 64 * b, t0, bh, &bar->full[s]);
+                    if (kMode == kOut) tma_load_3d(st + L::Q + b * kBlk, &tm_q, 64 * b, t0, bh, &bar->full[s]);
                 }
                 const size_t at = (size_t)bh * M + c;
-                bulk_load(st + L::mats, mats + at * kMats, kMats, &bar->full[s]);
+                bulk_load(st + L::mats, mats + at * kMats, kMode == kOut ? kMats : 2 * kBlk, &bar->full[s]);
                 bulk_load(st + L::gates, recs + at * kRec, kGateBytes, &bar->full[s]);
                 armed[s] = i;
             }
@@ -389,7 +289,7 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 for (int kk = 0; kk < D / 16; ++kk)
                     mma_ts1(lead, tmem + T::Y, tmem + T::SLo + 8 * kk, dK + step_k(kk), id_k, 1);
                 commit1(lead, &bar->y_done);
-                if (i > 0) outputs(i - 1);
+                if (kMode == kOut && i > 0) outputs(i - 1);
                 wait(&bar->r_ready, ph);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)  // (beta R)_hi [t_hi; t_lo]^T: two products of 64 columns
@@ -398,9 +298,9 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 for (int kk = 0; kk < 4; ++kk)
                     mma_ts1(lead, tmem + T::X, tmem + T::R + 32 + 8 * kk, dM + step_k(kk), id_k, 1);
                 commit1(lead, &bar->x_done);
-                if (i > 0) wait(&bar->o_free, ph ^ 1);
+                if (kMode == kOut && i > 0) wait(&bar->o_free, ph ^ 1);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)  // O = S Q^T
+                for (int kk = 0; kk < (kMode == kOut ? D / 16 : 0); ++kk)  // O = S Q^T
                     mma_ts1(lead, tmem + T::O, tmem + T::SHi + 8 * kk, dQ + step_k(kk), id_k, kk > 0);
                 wait(&bar->u_ready, ph);
 #pragma unroll
@@ -410,8 +310,9 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 for (int kk = 0; kk < 4; ++kk)
                     mma_ts1(lead, tmem + T::dS, tmem + T::R + 32 + 8 * kk, dKmn + step_mn(kk), id_mn, 1);
                 commit1(lead, &bar->s_done);
+                if (kMode != kOut) commit1(lead, &bar->empty[s]);
             }
-            outputs(nloc - 1);
+            if (kMode == kOut) outputs(nloc - 1);
             // drain: every MMA this thread issued has completed before TMEM is released
             commit1(lead, &bar->final_mma);
             mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
@@ -446,7 +347,7 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             arrive(&bar->s_ready);
         };
         put_state();
-        uint8_t* sO = base + L::O;
+        uint8_t* sO = base + L::out;
         auto output = [&](int j) {  // o of chunk j
             // the tile is free once the previous store has read it
             if (ct == 0) bulk_wait_read_all();
@@ -476,7 +377,8 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             const float* gates = reinterpret_cast<const float*>(sg + L::gates);
             // a gate of this thread's positions x .. x + 3
             auto gate = [&](int which, int x) { return ld_f4(gates + which + kTok * h + x); };
-            float R[kTok];  // beta V, beta R, then tail beta R
+            float R[kTok];  // beta V, then beta R
+            float Rp[kMode == kGrad ? kTok : 1];  // V, R, then X
             uint32_t w[kTok], hi[kTok / 2], lo[kTok / 2];
             wait(&bar->full[s], (i >> 1) & 1);
 #pragma unroll
@@ -484,11 +386,14 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 const float4 b = gate(kBeta, x);
                 const float bb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    R[x + e] = r < D ? bb[e] * __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(
-                                                                   sg + L::V + elem_off(kTok * h + x + e, r))
-                                                               << 16)
-                                     : 0.f;
+                for (int e = 0; e < 4; ++e) {
+                    const float v = r < D ? __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(
+                                                                sg + L::V + elem_off(kTok * h + x + e, r))
+                                                            << 16)
+                                          : 0.f;
+                    if constexpr (kMode == kGrad) Rp[x + e] = v;
+                    R[x + e] = bb[e] * v;
+                }
             }
             wait(&bar->y_done, ph);
             ld(lb + T::Y + kTok * h, w);
@@ -507,7 +412,17 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             st(lb + T::R + 32 + kTok / 2 * h, lo);
             tmem_st_wait();
             arrive(&bar->r_ready);
-            if (i > 0) output(i - 1);
+            if constexpr (kMode == kGrad) {
+#pragma unroll
+                for (int x = 0; x < kTok; x += 4) {
+                    const float4 g = gate(kGam, x);
+                    Rp[x] = fmaf(-g.x, __uint_as_float(w[x]), Rp[x]);
+                    Rp[x + 1] = fmaf(-g.y, __uint_as_float(w[x + 1]), Rp[x + 1]);
+                    Rp[x + 2] = fmaf(-g.z, __uint_as_float(w[x + 2]), Rp[x + 2]);
+                    Rp[x + 3] = fmaf(-g.w, __uint_as_float(w[x + 3]), Rp[x + 3]);
+                }
+            }
+            if (kMode == kOut && i > 0) output(i - 1);
             wait(&bar->x_done, ph);
             {
                 uint32_t w2[kTok];
@@ -533,16 +448,50 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             st(lb + T::R + 32 + kTok / 2 * h, lo);
             tmem_st_wait();
             arrive(&bar->u_ready);
+            if constexpr (kMode == kOut) {
 #pragma unroll
-            for (int x = 0; x < kTok; x += 4) {
-                const float4 b = gate(kBeta, x);
-                split2(fmaf(b.x, __uint_as_float(w[x]), R[x]), fmaf(b.y, __uint_as_float(w[x + 1]), R[x + 1]),
-                       hi[x / 2], lo[x / 2]);
-                split2(fmaf(b.z, __uint_as_float(w[x + 2]), R[x + 2]), fmaf(b.w, __uint_as_float(w[x + 3]), R[x + 3]),
-                       hi[x / 2 + 1], lo[x / 2 + 1]);
+                for (int x = 0; x < kTok; x += 4) {
+                    const float4 b = gate(kBeta, x);
+                    split2(fmaf(b.x, __uint_as_float(w[x]), R[x]), fmaf(b.y, __uint_as_float(w[x + 1]), R[x + 1]),
+                           hi[x / 2], lo[x / 2]);
+                    split2(fmaf(b.z, __uint_as_float(w[x + 2]), R[x + 2]),
+                           fmaf(b.w, __uint_as_float(w[x + 3]), R[x + 3]), hi[x / 2 + 1], lo[x / 2 + 1]);
+                }
+                st(lb + T::U + kTok / 2 * h, hi);
+                st(lb + T::U + 32 + kTok / 2 * h, lo);
+            } else {  // this thread's row of the state's tile (the state entering the chunk) and of X's tiles
+                if (ct == 0) bulk_wait_read_all();  // the previous chunk's stores have read the tiles
+                named_barrier(1, 32 * kWarps);
+                if (r < D) {
+                    uint8_t *sS = base + L::out, *sX = sS + L::sbytes;
+#pragma unroll
+                    for (int x = 0; x < kSc; x += 8) {
+                        const int c = kSc * h + x;
+                        *reinterpret_cast<uint4*>(sS + (c >> 6) * (D * 128) + row_off(r, c >> 3)) =
+                            make_uint4(pack_bf16x2(S[x], S[x + 1]), pack_bf16x2(S[x + 2], S[x + 3]),
+                                       pack_bf16x2(S[x + 4], S[x + 5]), pack_bf16x2(S[x + 6], S[x + 7]));
+                    }
+#pragma unroll
+                    for (int x = 0; x < kTok; x += 8) {
+                        uint4 a, b;
+                        split2(Rp[x] + __uint_as_float(w[x]), Rp[x + 1] + __uint_as_float(w[x + 1]), a.x, b.x);
+                        split2(Rp[x + 2] + __uint_as_float(w[x + 2]), Rp[x + 3] + __uint_as_float(w[x + 3]), a.y, b.y);
+                        split2(Rp[x + 4] + __uint_as_float(w[x + 4]), Rp[x + 5] + __uint_as_float(w[x + 5]), a.z, b.z);
+                        split2(Rp[x + 6] + __uint_as_float(w[x + 6]), Rp[x + 7] + __uint_as_float(w[x + 7]), a.w, b.w);
+                        const int off = row_off(r, (kTok * h + x) >> 3);
+                        *reinterpret_cast<uint4*>(sX + off) = b;
+                        *reinterpret_cast<uint4*>(sX + D * 128 + off) = a;
+                    }
+                }
+                fence_proxy_async_smem();
+                named_barrier(1, 32 * kWarps);
+                if (ct == 0) {
+                    const size_t at = (size_t)bh * M + cbeg + i;
+                    bulk_store(s_tiles + at * L::sbytes, base + L::out, L::sbytes);
+                    bulk_store(x_tiles + at * L::xbytes, base + L::out + L::sbytes, L::xbytes);
+                    bulk_commit();
+                }
             }
-            st(lb + T::U + kTok / 2 * h, hi);
-            st(lb + T::U + 32 + kTok / 2 * h, lo);
             const float gc = gates[kGam + kC - 1];
             wait(&bar->s_done, ph);
             {
@@ -553,22 +502,25 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 for (int x = 0; x < kSc; ++x) S[x] = fmaf(gc, S[x], __uint_as_float(d[x]));
             }
             put_state();
-            ld(lb + T::O + kTok * h, w);  // S Q^T is complete: it was issued before dS
-            tmem_ld_wait();
+            if constexpr (kMode == kOut) {
+                ld(lb + T::O + kTok * h, w);  // S Q^T is complete: it was issued before dS
+                tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < kTok; x += 4) {
-                const float4 g = gate(kGam, x);
-                w[x] = __float_as_uint(g.x * __uint_as_float(w[x]));
-                w[x + 1] = __float_as_uint(g.y * __uint_as_float(w[x + 1]));
-                w[x + 2] = __float_as_uint(g.z * __uint_as_float(w[x + 2]));
-                w[x + 3] = __float_as_uint(g.w * __uint_as_float(w[x + 3]));
+                for (int x = 0; x < kTok; x += 4) {
+                    const float4 g = gate(kGam, x);
+                    w[x] = __float_as_uint(g.x * __uint_as_float(w[x]));
+                    w[x + 1] = __float_as_uint(g.y * __uint_as_float(w[x + 1]));
+                    w[x + 2] = __float_as_uint(g.z * __uint_as_float(w[x + 2]));
+                    w[x + 3] = __float_as_uint(g.w * __uint_as_float(w[x + 3]));
+                }
+                st(lb + T::O + kTok * h, w);
+                tmem_st_wait();
+                arrive(&bar->o_ready);
             }
-            st(lb + T::O + kTok * h, w);
-            tmem_st_wait();
-            arrive(&bar->o_ready);
+            __syncwarp();
             if (lane == 0) mbar_arrive(&bar->empty[s]);  // this warp is done with V and the gates
         }
-        output(nloc - 1);
+        if (kMode == kOut) output(nloc - 1);
         if (ct == 0) bulk_wait_all();
         if (S_out && r < D) {
 #pragma unroll
@@ -583,15 +535,9 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     }
 }
 
-template <typename K>
-cudaError_t allow_smem(K kern, size_t bytes) {
-    return cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-#define GD_TRY(x)                         \
-    do {                                  \
-        const cudaError_t _e = (x);       \
-        if (_e != cudaSuccess) return _e; \
-    } while (0)
+}  // namespace
+
+namespace tcgd {
 
 template <int D>
 cudaError_t prepare(const CUtensorMap& tq, const CUtensorMap& tk, const void* g, const void* beta, float* recs,
@@ -604,6 +550,36 @@ cudaError_t prepare(const CUtensorMap& tq, const CUtensorMap& tk, const void* g,
     const cudaError_t e2 = launch_end("tc_gd_prepare", st);
     return e != cudaSuccess ? e : e2;
 }
+template cudaError_t prepare<64>(const CUtensorMap&, const CUtensorMap&, const void*, const void*, float*, uint8_t*,
+                                 const la_shape&, int, int*, cudaStream_t);
+template cudaError_t prepare<128>(const CUtensorMap&, const CUtensorMap&, const void*, const void*, float*, uint8_t*,
+                                  const la_shape&, int, int*, cudaStream_t);
+
+template <int D>
+cudaError_t states(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
+                   const float* recs, const uint8_t* mats, const float* S0, float* S_out, uint8_t* x_tiles,
+                   uint8_t* s_tiles, int BH, int M, int* err, cudaStream_t st) {
+    const bool grad = x_tiles != nullptr;
+    auto kern = grad ? tc_gd_states<D, kGrad> : tc_gd_states<D, kOut>;
+    const size_t smem = grad ? FwdSmem<D, kGrad>::bytes : FwdSmem<D, kOut>::bytes;
+    GD_TRY(allow_smem(kern, smem));
+    const char* name = grad ? "tc_gd_states_grad" : "tc_gd_states";
+    launch_begin(name, st);
+    const cudaError_t e = launch_pdl(kern, dim3(1, BH), dim3(kThreads), smem, st, tq, tk, tv, to, recs, mats, S0, S_out,
+                                     x_tiles, s_tiles, M, M, err);
+    const cudaError_t e2 = launch_end(name, st);
+    return e != cudaSuccess ? e : e2;
+}
+template cudaError_t states<64>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                                const float*, const uint8_t*, const float*, float*, uint8_t*, uint8_t*, int, int, int*,
+                                cudaStream_t);
+template cudaError_t states<128>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                                 const float*, const uint8_t*, const float*, float*, uint8_t*, uint8_t*, int, int,
+                                 int*, cudaStream_t);
+
+}  // namespace tcgd
+
+namespace {
 
 template <int D>
 cudaError_t fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) {
@@ -617,13 +593,7 @@ cudaError_t fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
     float* recs = (float*)(ws + L.rec);
     uint8_t* mats = (uint8_t*)(ws + L.t);
     GD_TRY(prepare<D>(tq, tk, a.g, a.beta, recs, mats, s, M, err, st));
-    auto kern = tc_gd_states<D>;
-    GD_TRY(allow_smem(kern, FwdSmem<D>::bytes));
-    launch_begin("tc_gd_states", st);
-    const cudaError_t e = launch_pdl(kern, dim3(1, BH), dim3(kThreads), FwdSmem<D>::bytes, st, tq, tk, tv, to,
-                                     (const float*)recs, (const uint8_t*)mats, a.S0, a.S, M, M, err);
-    const cudaError_t e2 = launch_end("tc_gd_states", st);
-    return e != cudaSuccess ? e : e2;
+    return states<D>(tq, tk, tv, to, recs, mats, a.S0, a.S, nullptr, nullptr, BH, M, err, st);
 }
 
 }  // namespace

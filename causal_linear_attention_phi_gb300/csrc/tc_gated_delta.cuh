@@ -1,0 +1,149 @@
+// tc_gated_delta.cuh -- pieces shared by the tensor-core kernels of the gated delta rule: tile layouts and their
+// descriptors, products issued from a converged warp, hi + lo splitting, the kernels' entry.
+#pragma once
+
+#include "gated_delta.cuh"
+#include "tc_common.cuh"
+
+namespace la {
+namespace gd {
+namespace tcgd {
+using namespace sm100;
+using tc::bf_hi;
+using tc::bf_lo;
+
+constexpr int kBlk = kC * 128;          // 64 rows x 64 bf16 columns, 128-byte swizzle
+constexpr int kMats = 4 * kBlk;         // t hi, t lo, P hi, P lo of a chunk
+constexpr int kTHi = 0, kTLo = kBlk, kPHi = 2 * kBlk, kPLo = 3 * kBlk;
+constexpr int kGateBytes = 5 * kC * 4;  // gam, tail, beta, beta gam, tail beta of the record
+
+// Contiguous global -> shared copy (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+// Contiguous shared -> global copy, tracked by the issuing thread's bulk groups.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
+// Shared-memory operands, as the low word of their descriptors (address and leading offset, in units of 16 bytes;
+// the high word is the same for all): K-major (rows are M or N) and MN-major (rows are K) tiles, K step kk of 16.  A
+// whole warp runs the issuing role and one elected lane issues, so that these words stay in uniform registers: with the
+// role in a one-lane branch an instruction cost about 90 cycles to issue, more than it takes to run.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+template <int kLead = 16>
+__device__ __forceinline__ uint32_t tile_desc(uint32_t addr) {
+    return ((addr & 0x3FFFFu) >> 4) | ((uint32_t)(kLead >> 4) << 16);
+}
+__device__ __forceinline__ constexpr uint32_t step_k(int kk, int blk = kBlk) { return ((kk >> 2) * blk + (kk & 3) * 32) >> 4; }
+__device__ __forceinline__ constexpr uint32_t step_mn(int kk) { return (kk * 2048) >> 4; }
+
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p;
+}
+// D[tmem] (+)= A[tmem] B[smem], and with both in shared memory, by the elected lane of a converged warp.
+__device__ __forceinline__ void mma_ts1(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 bd;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 bd, {%2, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"(lead), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ss1(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 ad, bd;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 ad, {%1, %4};\n\tmov.b64 bd, {%2, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"(lead), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void commit1(uint32_t lead, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+// Byte offset of (row, column c) in 64-column blocks of kC rows.
+__device__ __forceinline__ int elem_off(int row, int c) {
+    return (c >> 6) * kBlk + row * 128 + ((((c >> 3) & 7) ^ (row & 7)) << 4) + (c & 7) * 2;
+}
+// Every kernel here starts so: wait for the previous grid, take the TMEM columns, and only then let the next
+// grid's blocks be scheduled.  Blocks of several of these kernels fit on one SM: none holds columns while it
+// waits for a grid, and none is still to take its columns when a block that waits for it can arrive.
+__device__ __forceinline__ uint32_t enter(uint32_t* slot, uint32_t cols, int warp) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 1) {
+        tmem_alloc(slot, cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    return *slot;
+}
+// Byte offset of 16-byte chunk c of row r in rows of 64 columns.
+__device__ __forceinline__ int row_off(int r, int c) { return r * 128 + (((c & 7) ^ (r & 7)) << 4); }
+// a, b -> packed bf16 hi and lo parts.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16x2(a, b);
+    lo = pack_bf16x2(a - bf_lo(hi), b - bf_hi(hi));
+}
+
+constexpr int kWarps = 16;  // compute warps
+constexpr int kThreads = 64 + 32 * kWarps;
+constexpr int kHs = kWarps / 4;   // column groups: a thread owns one row of one group
+constexpr int kTok = kC / kHs;    // positions of a thread
+
+template <int N>
+__device__ __forceinline__ void ld(uint32_t a, uint32_t (&r)[N]) {
+    static_assert(N == 8 || N == 16 || N == 32, "columns");
+    if constexpr (N == 8) tmem_ld8(a, r);
+    if constexpr (N == 16) tmem_ld16(a, r);
+    if constexpr (N == 32) tmem_ld32(a, r);
+}
+template <int N>
+__device__ __forceinline__ void st(uint32_t a, const uint32_t (&r)[N]) {
+    static_assert(N == 8 || N == 16 || N == 32, "columns");
+    if constexpr (N == 8) tmem_st8(a, r);
+    if constexpr (N == 16) tmem_st16(a, r);
+    if constexpr (N == 32) tmem_st32(a, r);
+}
+
+
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes) {
+    return cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+#define GD_TRY(x)                         \
+    do {                                  \
+        const cudaError_t _e = (x);       \
+        if (_e != cudaSuccess) return _e; \
+    } while (0)
+
+// t and P of every chunk (tc_gated_delta.cu).
+template <int D>
+cudaError_t prepare(const CUtensorMap& tq, const CUtensorMap& tk, const void* g, const void* beta, float* recs,
+                    uint8_t* mats, const la_shape& s, int M, int* err, cudaStream_t st);
+// The recurrence; `x_tiles` and `s_tiles` given: the gradient's records instead of outputs.
+template <int D>
+cudaError_t states(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
+                   const float* recs, const uint8_t* mats, const float* S0, float* S_out, uint8_t* x_tiles,
+                   uint8_t* s_tiles, int BH, int M, int* err, cudaStream_t st);
+
+}  // namespace tcgd
+}  // namespace gd
+}  // namespace la

@@ -1,0 +1,714 @@
+// tc_gated_delta_bwd.cu -- tensor-core gradient of the gated delta rule for bf16 heads with Dk = Dv = 128 or 64
+// (formulas in gated_delta.cuh, layouts in tc_gated_delta.cuh).
+//
+// tc_gd_reverse (one block per head and segment): the adjoint recurrence from the last chunk back, transposed like the
+// forward one, with dS'^T [Dv lanes x Dk] in registers:
+//   dU^T = tail (dS'^T K^T) + dO^T P        Y^T = dU^T + (beta dU)^T t      dV^T = beta Y^T
+//   dS^T = gam_C dS'^T + (gam dO)^T Q - (beta gam Y)^T K
+// What is formed here enters the products as hi + lo bf16 parts, as in the forward kernel.  It writes dV and,
+// for tc_gd_grads, the tiles of Y^T [Dv rows x 64 positions], lo and hi, and of dS'^T [Dv rows x Dk], rounded to bf16
+// once like S (a relative error of 2^-9 of each term of the products with the states, none of which cancel by much).
+//
+// tc_gd_grads (one block per chunk): with G = Y X^T, F^T = X dO^T, all products with 128 rows,
+//   F_ij = (dO_i . X_j) beta_j Gam_ij (i >= j),  E_ij = -beta_i beta_j Gam_ij G_ij (i > j),  dbeta_i = G_ii
+//   dQ^T = gam S dO^T + K^T F^T              dK^T = -beta gam S Y^T + tail beta dS' X^T + Q^T F + K^T (E + E^T)^T
+// F and E enter as hi + lo parts: dg is a difference of sums over them.  Lanes 0-63 hold E's rows, 64-127 F^T's.
+#include <cudaTypedefs.h>
+
+#include "tc_gated_delta.cuh"
+
+namespace la {
+namespace gd {
+namespace {
+using namespace sm100;
+using namespace tcgd;
+
+// ------------------------------------------------------------------ the adjoint recurrence
+struct __align__(8) RBars {
+    uint64_t full[2], empty[2];
+    uint64_t s_ready, a_done, g_ready, b_ready, y_done, r_ready, s_done, final_mma;
+};
+
+template <int D>
+struct RevSmem {
+    static constexpr int tile = D / 64 * kBlk;
+    static constexpr int K = 0, Q = tile, dO = 2 * tile, mats = 3 * tile, gates = mats + kMats;
+    static constexpr int stage = gates + 2048;
+    static constexpr int out = 2 * stage;  // dS' tile; then dV tile and Y's lo and hi tiles
+    static constexpr int sbytes = D * D * 2, ybytes = 2 * D * 128;
+    static constexpr int bars = out + (sbytes > tile + ybytes ? sbytes : tile + ybytes);
+    static constexpr int slot = bars + 256;
+    static constexpr int total = slot + 16;
+    static constexpr size_t bytes = total + 1024;
+    static_assert(bytes <= 232448, "shared memory");
+};
+
+template <int D>
+struct RTm {
+    static constexpr uint32_t SHi = 0, SLo = D / 2, A1 = D, A2 = D + 64, B = D + 128, G = D + 192, dS = D + 256;
+    static constexpr uint32_t Y = A1;  // two products of 64 columns over A1 and A2, read before
+    static_assert(dS + 128 <= 512, "TMEM");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+              const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dv,
+              const float* __restrict__ recs, const uint8_t* __restrict__ mats, uint8_t* __restrict__ y_tiles,
+              uint8_t* __restrict__ ds_tiles, int M, int cps, int* err) {
+    using L = RevSmem<D>;
+    using T = RTm<D>;
+    constexpr int kSc = D / kHs;  // state columns of a thread
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    RBars* bar = reinterpret_cast<RBars*>(base + L::bars);
+    uint32_t* slot = reinterpret_cast<uint32_t*>(base + L::slot);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int p = blockIdx.x, bh = blockIdx.y, cbeg = p * cps, cend = min(M, cbeg + cps), nloc = cend - cbeg;
+    LA_DCHECK(nloc >= 1);
+    if (tid == 0) {
+        mbar_init(&bar->full[0], 1);
+        mbar_init(&bar->full[1], 1);
+        mbar_init(&bar->empty[0], 1 + kWarps);
+        mbar_init(&bar->empty[1], 1 + kWarps);
+        mbar_init(&bar->s_ready, kWarps);
+        mbar_init(&bar->a_done, 1);
+        mbar_init(&bar->g_ready, kWarps);
+        mbar_init(&bar->b_ready, kWarps);
+        mbar_init(&bar->y_done, 1);
+        mbar_init(&bar->r_ready, kWarps);
+        mbar_init(&bar->s_done, 1);
+        mbar_init(&bar->final_mma, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_do);
+        tma_prefetch_desc(&tm_dv);
+    }
+    const uint32_t tmem = enter(slot, 512, warp);
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int armed[2] = {-1, -1};
+            for (int i = 0; i < nloc; ++i) {
+                const int s = i & 1, c = cend - 1 - i, t0 = c * kC;
+                uint8_t* st = base + s * L::stage;
+                if (!mbar_wait(&bar->empty[s], ((i >> 1) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
+                mbar_arrive_expect_tx(&bar->full[s], 3 * L::tile + kMats + kGateBytes);
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b) {
+                    tma_load_3d(st + L::dO + b * kBlk, &tm_do, 64 * b, t0, bh, &bar->full[s]);
+                    tma_load_3d(st + L::K + b * kBlk, &tm_k, 64 * b, t0, bh, &bar->full[s]);
+                    tma_load_3d(st + L::Q + b * kBlk, &tm_q, 64 * b, t0, bh, &bar->full[s]);
+                }
+                const size_t at = (size_t)bh * M + c;
+                bulk_load(st + L::mats, mats + at * kMats, kMats, &bar->full[s]);
+                bulk_load(st + L::gates, recs + at * kRec, kGateBytes, &bar->full[s]);
+                armed[s] = i;
+            }
+            // never leave with copies in flight: wait for the last armed phase of each stage
+            for (int s = 0; s < 2; ++s)
+                if (armed[s] >= 0) mbar_wait(&bar->full[s], (armed[s] >> 1) & 1, err, LA_ERR_TIMEOUT);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        const uint32_t lead = elect_one();
+        constexpr uint32_t id_k = idesc_bf16_f32(128, kC, 0, 0);        // [128 x 64], B K-major
+        constexpr uint32_t id_amn = idesc_bf16_f32(128, kC, 1, 1);      // A (smem) and B MN-major
+        constexpr uint32_t id_mn = idesc_bf16_f32(128, kC, 0, 1);       // [128 x 64], B MN-major
+        constexpr uint32_t id_mn2 = idesc_bf16_f32(128, 2 * kC, 0, 1);  // [128 x 128]
+        constexpr uint32_t id_mnD = idesc_bf16_f32(128, D, 0, 1);       // [128 x D]
+        bool ok = true;
+        auto wait = [&](uint64_t* b, int parity) {
+            ok = ok && mbar_wait(b, parity, err, LA_ERR_TIMEOUT);
+            __syncwarp();
+            tc_fence_after();
+        };
+        for (int i = 0; i < nloc; ++i) {
+            const int s = i & 1, ph = i & 1;
+            const uint32_t sg = smem_u32(base + s * L::stage);
+            const uint32_t dK = tile_desc(sg + L::K), dKmn = tile_desc<kBlk>(sg + L::K), dQmn = tile_desc<kBlk>(sg + L::Q);
+            const uint32_t dO = tile_desc<kBlk>(sg + L::dO), dM = tile_desc<kBlk>(sg + L::mats);
+            wait(&bar->full[s], (i >> 1) & 1);
+            if (i > 0) wait(&bar->r_ready, ph ^ 1);  // Y, over A1 and A2, has been read
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // dO^T P
+                mma_ss1(lead, tmem + T::A2, dO + step_mn(kk), dM + (kPHi >> 4) + step_mn(kk), id_amn, kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_ss1(lead, tmem + T::A2, dO + step_mn(kk), dM + (kPLo >> 4) + step_mn(kk), id_amn, 1);
+            wait(&bar->s_ready, ph);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)  // dS'^T K^T
+                mma_ts1(lead, tmem + T::A1, tmem + T::SHi + 8 * kk, dK + step_k(kk), id_k, kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                mma_ts1(lead, tmem + T::A1, tmem + T::SLo + 8 * kk, dK + step_k(kk), id_k, 1);
+            commit1(lead, &bar->a_done);
+            wait(&bar->g_ready, ph);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // (gam dO)^T Q
+                mma_ts1(lead, tmem + T::dS, tmem + T::G + 8 * kk, dQmn + step_mn(kk), id_mnD, kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_ts1(lead, tmem + T::dS, tmem + T::G + 32 + 8 * kk, dQmn + step_mn(kk), id_mnD, 1);
+            wait(&bar->b_ready, ph);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // (beta dU)_hi^T [t_hi | t_lo]: two products of 64 columns
+                mma_ts1(lead, tmem + T::Y, tmem + T::B + 8 * kk, dM + step_mn(kk), id_mn2, kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_ts1(lead, tmem + T::Y, tmem + T::B + 32 + 8 * kk, dM + step_mn(kk), id_mn, 1);
+            commit1(lead, &bar->y_done);
+            wait(&bar->r_ready, ph);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // -(beta gam Y)^T K
+                mma_ts1(lead, tmem + T::dS, tmem + T::B + 8 * kk, dKmn + step_mn(kk), id_mnD, 1);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_ts1(lead, tmem + T::dS, tmem + T::B + 32 + 8 * kk, dKmn + step_mn(kk), id_mnD, 1);
+            commit1(lead, &bar->s_done);
+            commit1(lead, &bar->empty[s]);
+        }
+        // drain: every MMA issued has completed before TMEM is released
+        commit1(lead, &bar->final_mma);
+        mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
+    } else {
+        // ------------------------------------------------------------ compute warps
+        const int ct = tid - 64, h = ct >> 7;  // group: positions kTok h .., state columns kSc h ..
+        const int r = 32 * (warp & 3) + lane;  // TMEM lane: value column
+        const uint32_t lb = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        bool ok = true;
+        auto wait = [&](uint64_t* b, int parity) {
+            ok = ok && mbar_wait(b, parity, err, LA_ERR_TIMEOUT);
+            __syncwarp();
+            tc_fence_after();
+        };
+        auto arrive = [&](uint64_t* b) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b);
+        };
+        float S[kSc];
+#pragma unroll
+        for (int x = 0; x < kSc; ++x) S[x] = 0.f;
+        uint8_t* out = base + L::out;
+        for (int i = 0; i < nloc; ++i) {
+            const int s = i & 1, ph = i & 1, c = cend - 1 - i;
+            const size_t at = (size_t)bh * M + c;
+            uint8_t* sg = base + s * L::stage;
+            const float* gates = reinterpret_cast<const float*>(sg + L::gates);
+            auto gate = [&](int which, int x) { return ld_f4(gates + which + kTok * h + x); };
+            {  // the state gradient's parts, and the signal that they are there
+                uint32_t hi[kSc / 2], lo[kSc / 2];
+#pragma unroll
+                for (int x = 0; x < kSc / 2; ++x) split2(S[2 * x], S[2 * x + 1], hi[x], lo[x]);
+                st(lb + T::SHi + kSc / 2 * h, hi);
+                st(lb + T::SLo + kSc / 2 * h, lo);
+                tmem_st_wait();
+                arrive(&bar->s_ready);
+                // its tile: the gradient leaving this chunk
+                if (ct == 0) bulk_wait_read_all();
+                named_barrier(1, 32 * kWarps);
+                if (r < D) {
+#pragma unroll
+                    for (int x = 0; x < kSc; x += 8) {
+                        const int cc = kSc * h + x;
+                        *reinterpret_cast<uint4*>(out + (cc >> 6) * (D * 128) + row_off(r, cc >> 3)) =
+                            make_uint4(hi[x / 2], hi[x / 2 + 1], hi[x / 2 + 2], hi[x / 2 + 3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                named_barrier(1, 32 * kWarps);
+                if (ct == 0) {
+                    bulk_store(ds_tiles + at * L::sbytes, out, L::sbytes);
+                    bulk_commit();
+                }
+            }
+            uint32_t w[kTok], hi[kTok / 2], lo[kTok / 2];
+            wait(&bar->full[s], (i >> 1) & 1);
+#pragma unroll
+            for (int x = 0; x < kTok; x += 4) {
+                const float4 g = gate(kGam, x);
+                const float gg[4] = {g.x, g.y, g.z, g.w};
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = r < D ? gg[e] * __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(
+                                                               sg + L::dO + elem_off(kTok * h + x + e, r))
+                                                           << 16)
+                                 : 0.f;
+                split2(v[0], v[1], hi[x / 2], lo[x / 2]);
+                split2(v[2], v[3], hi[x / 2 + 1], lo[x / 2 + 1]);
+            }
+            st(lb + T::G + kTok / 2 * h, hi);  // free: the previous chunk's products are complete
+            st(lb + T::G + 32 + kTok / 2 * h, lo);
+            tmem_st_wait();
+            arrive(&bar->g_ready);
+            float dU[kTok];
+            wait(&bar->a_done, ph);
+            {
+                uint32_t w2[kTok];
+                ld(lb + T::A1 + kTok * h, w);
+                ld(lb + T::A2 + kTok * h, w2);
+                tmem_ld_wait();
+#pragma unroll
+                for (int x = 0; x < kTok; x += 4) {
+                    const float4 t = gate(kTail, x), b = gate(kBeta, x);
+                    const float tt[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        dU[x + e] = fmaf(tt[e], __uint_as_float(w[x + e]), __uint_as_float(w2[x + e]));
+                    split2(b.x * dU[x], b.y * dU[x + 1], hi[x / 2], lo[x / 2]);
+                    split2(b.z * dU[x + 2], b.w * dU[x + 3], hi[x / 2 + 1], lo[x / 2 + 1]);
+                }
+            }
+            st(lb + T::B + kTok / 2 * h, hi);
+            st(lb + T::B + 32 + kTok / 2 * h, lo);
+            tmem_st_wait();
+            arrive(&bar->b_ready);
+            wait(&bar->y_done, ph);
+            {
+                uint32_t w2[kTok];
+                ld(lb + T::Y + kTok * h, w);
+                ld(lb + T::Y + kC + kTok * h, w2);
+                tmem_ld_wait();
+#pragma unroll
+                for (int x = 0; x < kTok; x += 4) {
+                    const float4 b = gate(kBg, x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        dU[x + e] += __uint_as_float(w[x + e]) + __uint_as_float(w2[x + e]);  // Y
+                    split2(-b.x * dU[x], -b.y * dU[x + 1], hi[x / 2], lo[x / 2]);
+                    split2(-b.z * dU[x + 2], -b.w * dU[x + 3], hi[x / 2 + 1], lo[x / 2 + 1]);
+                }
+            }
+            st(lb + T::B + kTok / 2 * h, hi);
+            st(lb + T::B + 32 + kTok / 2 * h, lo);
+            tmem_st_wait();
+            arrive(&bar->r_ready);
+            const float gc = gates[kGam + kC - 1];
+            // dV's tile [positions][value columns] and Y's [value columns][positions]
+            if (ct == 0) bulk_wait_read_all();
+            named_barrier(1, 32 * kWarps);
+            if (r < D) {
+#pragma unroll
+                for (int x = 0; x < kTok; x += 4) {
+                    const float4 b = gate(kBeta, x);
+                    const float bb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<__nv_bfloat16*>(out + elem_off(kTok * h + x + e, r)) =
+                            __float2bfloat16_rn(bb[e] * dU[x + e]);
+                }
+#pragma unroll
+                for (int x = 0; x < kTok; x += 8) {
+                    uint4 a, b;
+                    split2(dU[x], dU[x + 1], a.x, b.x);
+                    split2(dU[x + 2], dU[x + 3], a.y, b.y);
+                    split2(dU[x + 4], dU[x + 5], a.z, b.z);
+                    split2(dU[x + 6], dU[x + 7], a.w, b.w);
+                    uint8_t* y = out + L::tile + row_off(r, (kTok * h + x) >> 3);
+                    *reinterpret_cast<uint4*>(y) = b;
+                    *reinterpret_cast<uint4*>(y + D * 128) = a;
+                }
+            }
+            fence_proxy_async_smem();
+            named_barrier(1, 32 * kWarps);
+            if (ct == 0) {
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b) tma_store_3d(&tm_dv, out + b * kBlk, 64 * b, c * kC, bh);
+                bulk_store(y_tiles + at * L::ybytes, out + L::tile, L::ybytes);
+                bulk_commit();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar->empty[s]);  // this warp is done with dO and the gates
+            wait(&bar->s_done, ph);
+            {
+                uint32_t d[kSc];
+                ld(lb + T::dS + kSc * h, d);
+                tmem_ld_wait();
+#pragma unroll
+                for (int x = 0; x < kSc; ++x) S[x] = fmaf(gc, S[x], __uint_as_float(d[x]));
+            }
+        }
+        if (ct == 0) bulk_wait_all();
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ dq, dk, dg, dbeta of a chunk
+template <int D>
+struct GradSmem {
+    static constexpr int TS = D * 128;  // a tile of D rows x 64 columns
+    static constexpr int S = 0, XLo = S + D * D * 2, XHi = XLo + TS, YLo = XHi + TS, Y = YLo + TS, dS = Y + TS;
+    static constexpr int QK = dS + D * D * 2;  // blocks of [Q rows; K rows] x 64 columns
+    static constexpr int dO = QK + 2 * (D / 64) * kBlk;
+    static constexpr int FHi = dO + (D / 64) * kBlk, FLo = FHi + kBlk, EHi = FLo + kBlk, ELo = EHi + kBlk;
+    static constexpr int out = XLo;  // dq and dk tiles, once the products have read X and Y
+    static_assert(2 * (D / 64) * kBlk <= 4 * TS, "output tiles");
+    static constexpr int rec = ELo + kBlk;
+    static constexpr int part = rec + kRec * 4;  // fp32 partial sums, below
+    static constexpr int pRow = 0, pCol = pRow + 4 * 128, pTok = pCol + 4 * kC, pSum = pTok + 4 * kC,
+                         dBeta = pSum + 2 * kWarps, pEnd = dBeta + kC;
+    static constexpr int bars = part + pEnd * 4;
+    static constexpr int slot = bars + 64;
+    static constexpr int total = slot + 16;
+    static constexpr size_t bytes = total + 1024;
+    static_assert(bytes <= 232448, "shared memory");
+};
+struct GTm {
+    static constexpr uint32_t q1 = 0, k1 = 64, k3 = 128;          // S dO^T; S Y^T; dS' X^T as two halves
+    static constexpr uint32_t G = 256, FT = 320, kk = 384, qk = 448;
+    static constexpr uint32_t q2 = 256, k2 = 384;                 // over the four above, two halves each
+};
+
+// v[x] (x < 16) summed over the 32 lanes; lane l (even ones suffice) gets the total of column (l >> 1) & 15.
+__device__ __forceinline__ float reduce16(float (&v)[16], int lane) {
+#pragma unroll
+    for (int o = 16, n = 8; n >= 1; o >>= 1, n >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int x = 0; x < n; ++x) {
+            const float send = up ? v[x] : v[x + n];
+            const float keep = up ? v[x + n] : v[x];
+            v[x] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+            const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dq,
+            const __grid_constant__ CUtensorMap tm_dk, const __nv_bfloat16* __restrict__ g,
+            const float* __restrict__ recs, const uint8_t* __restrict__ x_tiles, const uint8_t* __restrict__ y_tiles,
+            const uint8_t* __restrict__ s_tiles, const uint8_t* __restrict__ ds_tiles, __nv_bfloat16* __restrict__ dg,
+            __nv_bfloat16* __restrict__ dbeta, int N, int M, int* err) {
+    using L = GradSmem<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bar = reinterpret_cast<uint64_t*>(base + L::bars);  // loads, first products, pairs ready, second products
+    uint32_t* slot = reinterpret_cast<uint32_t*>(base + L::slot);
+    float* rec = reinterpret_cast<float*>(base + L::rec);
+    float* part = reinterpret_cast<float*>(base + L::part);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, m = blockIdx.x, bh = blockIdx.y;
+    const size_t at = (size_t)bh * M + m;
+    const int c0 = m * kC, n = min(kC, N - c0);
+    LA_DCHECK(n >= 1 && m < M);
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        mbar_init(bar + 1, 1);
+        mbar_init(bar + 2, kWarps);
+        mbar_init(bar + 3, 1);
+        mbar_init(bar + 4, 1);
+        fence_mbar_init();
+    }
+    const uint32_t tmem = enter(slot, 512, warp);
+    if (warp == 0) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar, 2 * D * D * 2 + 4 * L::TS + 3 * (D / 64) * kBlk + kRec * 4);
+#pragma unroll
+            for (int b = 0; b < D / 64; ++b) {
+                tma_load_3d(base + L::QK + 2 * b * kBlk, &tm_q, 64 * b, c0, bh, bar);
+                tma_load_3d(base + L::QK + (2 * b + 1) * kBlk, &tm_k, 64 * b, c0, bh, bar);
+                tma_load_3d(base + L::dO + b * kBlk, &tm_do, 64 * b, c0, bh, bar);
+            }
+            bulk_load(base + L::XLo, x_tiles + at * (2 * L::TS), 2 * L::TS, bar);
+            bulk_load(base + L::YLo, y_tiles + at * (2 * L::TS), 2 * L::TS, bar);
+            bulk_load(base + L::S, s_tiles + at * (D * D * 2), D * D * 2, bar);
+            bulk_load(base + L::dS, ds_tiles + at * (D * D * 2), D * D * 2, bar);
+            bulk_load(rec, recs + at * kRec, kRec * 4, bar);
+            mbar_wait(bar, 0, err, LA_ERR_TIMEOUT);  // never leave with copies in flight
+        }
+    } else if (warp == 1) {
+        const uint32_t lead = elect_one();
+        bool ok = true;
+        auto wait = [&](uint64_t* b, int parity) {
+            ok = ok && mbar_wait(b, parity, err, LA_ERR_TIMEOUT);
+            __syncwarp();
+            tc_fence_after();
+        };
+        constexpr uint32_t id_kk = idesc_bf16_f32(128, kC, 0, 0), id_mk = idesc_bf16_f32(128, kC, 1, 0),
+                           id_mm = idesc_bf16_f32(128, kC, 1, 1), id_mm2 = idesc_bf16_f32(128, 2 * kC, 1, 1),
+                           id_mk2 = idesc_bf16_f32(128, 2 * kC, 1, 0);
+        const uint32_t b0 = smem_u32(base);
+        constexpr int TS = L::TS, kSteps = D / 16;
+        const uint32_t dQ = tile_desc(b0 + L::QK), dK = tile_desc(b0 + L::QK + kBlk), dO = tile_desc(b0 + L::dO);
+        // MN-major left operands: blocks of 64 rows (of M) one tile apart
+        const uint32_t aBelow = tile_desc<TS>(b0 + L::XLo - TS), aLo = tile_desc<TS>(b0 + L::XLo),
+                       aY = tile_desc<TS>(b0 + L::Y), aS = tile_desc<TS>(b0 + L::S), adS = tile_desc<TS>(b0 + L::dS);
+        wait(bar, 0);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)  // lanes 64-127: X dO^T
+            mma_ss1(lead, tmem + GTm::FT, aBelow + step_mn(k), dO + step_k(k), id_mk, k > 0);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+            mma_ss1(lead, tmem + GTm::FT, aLo + step_mn(k), dO + step_k(k), id_mk, 1);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)  // lanes 0-63: Y X^T
+            mma_ss1(lead, tmem + GTm::G, aY + step_mn(k), tile_desc<TS>(b0 + L::XHi) + step_mn(k), id_mm, k > 0);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+            mma_ss1(lead, tmem + GTm::G, aY + step_mn(k), aLo + step_mn(k), id_mm, 1);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+            mma_ss1(lead, tmem + GTm::G, tile_desc<TS>(b0 + L::YLo) + step_mn(k),
+                    tile_desc<TS>(b0 + L::XHi) + step_mn(k), id_mm, 1);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)  // lanes 64-127: K Q^T
+            mma_ss1(lead, tmem + GTm::qk, dQ + step_k(k, 2 * kBlk), dQ + step_k(k, 2 * kBlk), id_kk, k > 0);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)  // lanes 0-63: K K^T
+            mma_ss1(lead, tmem + GTm::kk, dK + step_k(k, 2 * kBlk), dK + step_k(k, 2 * kBlk), id_kk, k > 0);
+        commit1(lead, bar + 1);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)  // S dO^T
+            mma_ss1(lead, tmem + GTm::q1, aS + step_mn(k), dO + step_k(k), id_mk, k > 0);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)  // S Y^T
+            mma_ss1(lead, tmem + GTm::k1, aS + step_mn(k), aY + step_mn(k), id_mm, k > 0);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)  // dS' [X_lo | X_hi]^T
+            mma_ss1(lead, tmem + GTm::k3, adS + step_mn(k), aLo + step_mn(k), id_mm2, k > 0);
+        wait(bar + 2, 0);  // F and E are in their tiles, their products have been read
+        const uint32_t mQ = tile_desc<2 * kBlk>(b0 + L::QK), mK = tile_desc<2 * kBlk>(b0 + L::QK + kBlk);
+        const uint32_t fMn = tile_desc<kBlk>(b0 + L::FHi), eMn = tile_desc<kBlk>(b0 + L::EHi);
+        const uint32_t fK = tile_desc(b0 + L::FHi), eK = tile_desc(b0 + L::EHi);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // K^T F^T, with [F_hi | F_lo]
+            mma_ss1(lead, tmem + GTm::q2, mK + step_mn(k), fMn + step_mn(k), id_mm2, k > 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // Q^T F
+            mma_ss1(lead, tmem + GTm::k2, mQ + step_mn(k), fK + step_k(k), id_mk2, k > 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // K^T E^T
+            mma_ss1(lead, tmem + GTm::k2, mK + step_mn(k), eK + step_k(k), id_mk2, 1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // K^T E
+            mma_ss1(lead, tmem + GTm::k2, mK + step_mn(k), eMn + step_mn(k), id_mm2, 1);
+        commit1(lead, bar + 3);
+        mbar_wait(bar + 3, 0, err, LA_ERR_TIMEOUT);
+        __syncwarp();
+    } else {
+        const int ct = tid - 64, h = ct >> 7, r = 32 * (warp & 3) + lane, q4 = warp & 3;
+        const uint32_t lb = tmem + ((uint32_t)(32 * q4) << 16);
+        bool ok = true;
+        auto wait = [&](uint64_t* b, int parity) {
+            ok = ok && mbar_wait(b, parity, err, LA_ERR_TIMEOUT);
+            __syncwarp();
+            tc_fence_after();
+        };
+        wait(bar, 0);
+        float kept = 0.f;  // <dS', S>
+        for (int x = ct; x < D * D / 8; x += 32 * kWarps) {
+            const uint4 a = *reinterpret_cast<const uint4*>(base + L::S + 16 * x);
+            const uint4 b = *reinterpret_cast<const uint4*>(base + L::dS + 16 * x);
+            kept = fmaf(bf_lo(a.x), bf_lo(b.x), fmaf(bf_hi(a.x), bf_hi(b.x), kept));
+            kept = fmaf(bf_lo(a.y), bf_lo(b.y), fmaf(bf_hi(a.y), bf_hi(b.y), kept));
+            kept = fmaf(bf_lo(a.z), bf_lo(b.z), fmaf(bf_hi(a.z), bf_hi(b.z), kept));
+            kept = fmaf(bf_lo(a.w), bf_lo(b.w), fmaf(bf_hi(a.w), bf_hi(b.w), kept));
+        }
+        wait(bar + 1, 0);
+        {  // F^T (row j, columns i) or E (row i, columns j): this thread's 16 columns
+            const bool isF = r >= kC;
+            const int row = r & (kC - 1), col0 = 16 * h;
+            uint32_t v[16], pq[16];
+            ld(lb + (isF ? GTm::FT : GTm::G) + col0, v);
+            ld(lb + (isF ? GTm::qk : GTm::kk) + col0, pq);
+            tmem_ld_wait();
+            const float seg = rec[kSeg + row], hi = rec[kGhi + row], lo = rec[kGlo + row], br = rec[kBeta + row];
+            float pr[16], rsum = 0.f;
+            uint4 ph[2], pl[2];
+            uint32_t* eh = reinterpret_cast<uint32_t*>(ph);
+            uint32_t* el = reinterpret_cast<uint32_t*>(pl);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                const int col = col0 + x;
+                const float raw = __uint_as_float(v[x]);
+                if (!isF && col == row) part[L::dBeta + row] = raw;
+                float d = (hi - rec[kGhi + col]) + (lo - rec[kGlo + col]);  // G_row - G_col
+                if (isF) d = -d;
+                const bool in = (isF ? col >= row : col < row) && rec[kSeg + col] == seg;
+                const float s = isF ? br : -br * rec[kBeta + col];
+                const float val = in ? raw * (s * ex2_approx(d * 1.4426950408889634f)) : 0.f;
+                v[x] = __float_as_uint(val);
+                pr[x] = col != row ? val * __uint_as_float(pq[x]) : 0.f;
+                pr[x] = in ? pr[x] : 0.f;
+                rsum += pr[x];
+            }
+#pragma unroll
+            for (int x = 0; x < 16; x += 2)
+                split2(__uint_as_float(v[x]), __uint_as_float(v[x + 1]), eh[x / 2], el[x / 2]);
+            uint8_t* tile = base + (isF ? L::FHi : L::EHi);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int off = row_off(row, (col0 >> 3) + x);
+                *reinterpret_cast<uint4*>(tile + off) = ph[x];
+                *reinterpret_cast<uint4*>(tile + kBlk + off) = pl[x];
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + 2);
+            // shares of dG: a row of E adds to its position, its columns are taken off theirs; F^T the other way round
+            part[L::pRow + h * 128 + r] = isF ? -rsum : rsum;
+            const float cs = reduce16(pr, lane);
+            if ((lane & 1) == 0) part[L::pCol + q4 * kC + col0 + (lane >> 1)] = isF ? cs : -cs;
+        }
+        wait(bar + 3, 0);
+        {  // row r = dk, positions 16 h ..
+            const int t0 = 16 * h;
+            float tok[16], outs = 0.f;
+            uint8_t *sq = base + L::out, *sk = sq + (D / 64) * kBlk;
+#pragma unroll
+            for (int x0 = 0; x0 < 16; x0 += 8) {
+                uint32_t q1[8], k1[8], ka[8], kb[8], qa[8], qb[8], ea[8], eb[8];
+                ld(lb + GTm::q1 + t0 + x0, q1);
+                ld(lb + GTm::k1 + t0 + x0, k1);
+                ld(lb + GTm::k3 + t0 + x0, ka);
+                ld(lb + GTm::k3 + kC + t0 + x0, kb);
+                ld(lb + GTm::q2 + t0 + x0, qa);
+                ld(lb + GTm::q2 + kC + t0 + x0, qb);
+                ld(lb + GTm::k2 + t0 + x0, ea);
+                ld(lb + GTm::k2 + kC + t0 + x0, eb);
+                tmem_ld_wait();
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const int t = t0 + x0 + x;
+                    const float dqi = rec[kGam + t] * __uint_as_float(q1[x]);
+                    const float dki = -rec[kBg + t] * __uint_as_float(k1[x]);
+                    const float dko = rec[kTb + t] * (__uint_as_float(ka[x]) + __uint_as_float(kb[x]));
+                    const float dqv = dqi + (__uint_as_float(qa[x]) + __uint_as_float(qb[x]));
+                    const float dkv = (dki + dko) + (__uint_as_float(ea[x]) + __uint_as_float(eb[x]));
+                    float s = 0.f;
+                    if (r < D) {
+                        const int eo = (r >> 6) * 2 * kBlk + (elem_off(t, r) - (r >> 6) * kBlk);  // [Q; K] blocks
+                        const float qv = __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(base + L::QK + eo) << 16);
+                        const float kv =
+                            __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(base + L::QK + kBlk + eo) << 16);
+                        const float o = kv * dko;
+                        s = fmaf(qv, dqi, fmaf(kv, dki, -o));
+                        outs += o;
+                        const int off = elem_off(t, r);
+                        *reinterpret_cast<__nv_bfloat16*>(sq + off) = __float2bfloat16_rn(dqv);
+                        *reinterpret_cast<__nv_bfloat16*>(sk + off) = __float2bfloat16_rn(dkv);
+                    }
+                    tok[x0 + x] = s;
+                }
+            }
+            const float ts = reduce16(tok, lane);
+            if ((lane & 1) == 0) part[L::pTok + q4 * kC + t0 + (lane >> 1)] = ts;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                outs += __shfl_xor_sync(0xffffffffu, outs, o);
+                kept += __shfl_xor_sync(0xffffffffu, kept, o);
+            }
+            if (lane == 0) {
+                part[L::pSum + (warp - 2)] = outs;
+                part[L::pSum + kWarps + (warp - 2)] = kept;
+            }
+        }
+        fence_proxy_async_smem();
+        named_barrier(1, 32 * kWarps);
+        if (ct == 0) {
+#pragma unroll
+            for (int b = 0; b < D / 64; ++b) {
+                tma_store_3d(&tm_dq, base + L::out + b * kBlk, 64 * b, c0, bh);
+                tma_store_3d(&tm_dk, base + L::out + (D / 64 + b) * kBlk, 64 * b, c0, bh);
+            }
+            bulk_commit();
+        }
+        if (warp == 3) {  // dg: the reverse cumulative sum, in fp64 (its terms cancel); two positions to a lane
+            double v[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * lane + e;
+                double a = 0.0;
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    a += (double)part[L::pRow + y * 128 + i] + (double)part[L::pRow + y * 128 + kC + i] +
+                         (double)part[L::pCol + y * kC + i] + (double)part[L::pTok + y * kC + i];
+                v[e] = a;
+            }
+            double tail = 0.0, os = 0.0;
+#pragma unroll
+            for (int y = 0; y < kWarps; ++y) {
+                os += (double)part[L::pSum + y];
+                tail += (double)part[L::pSum + kWarps + y];
+            }
+            tail = tail * (double)rec[kGam + kC - 1] + os;
+            const double both = v[0] + v[1];
+            double run = both;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double x = __shfl_down_sync(0xffffffffu, run, o);
+                if (lane + o < 32) run += x;
+            }
+            const double after = run - both;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * lane + e;
+                if (i >= n) continue;
+                const size_t pos = (size_t)bh * N + c0 + i;
+                const double d = after + (e ? v[1] : both) + tail;
+                dg[pos] = __float2bfloat16_rn(__bfloat162float(g[pos]) < kReset ? 0.f : (float)d);
+                dbeta[pos] = __float2bfloat16_rn(part[L::dBeta + i]);
+            }
+        }
+        if (ct == 0) bulk_wait_all();
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+cudaError_t bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) {
+    const int BH = s.B * s.H, M = (s.N + kC - 1) / kC;
+    CUtensorMap tq, tk, tv, tdo, tdq, tdk, tdv;
+    if (!make_tmap_bf16_rows(&tq, a.q, BH, s.N, D, kC) || !make_tmap_bf16_rows(&tk, a.k, BH, s.N, D, kC) ||
+        !make_tmap_bf16_rows(&tv, a.v, BH, s.N, D, kC) || !make_tmap_bf16_rows(&tdo, a.dout, BH, s.N, D, kC) ||
+        !make_tmap_bf16_rows(&tdq, a.dq, BH, s.N, D, kC) || !make_tmap_bf16_rows(&tdk, a.dk, BH, s.N, D, kC) ||
+        !make_tmap_bf16_rows(&tdv, a.dv, BH, s.N, D, kC))
+        return cudaErrorInvalidValue;
+    int* err = device_error_word();
+    const Layout L = layout(s, true);
+    float* recs = (float*)(ws + L.rec);
+    uint8_t *mats = (uint8_t*)(ws + L.t), *X = (uint8_t*)(ws + L.X), *Y = (uint8_t*)(ws + L.Y), *S = (uint8_t*)(ws + L.S),
+            *dS = (uint8_t*)(ws + L.dS);
+    GD_TRY(prepare<D>(tq, tk, a.g, a.beta, recs, mats, s, M, err, st));
+    GD_TRY(states<D>(tq, tk, tv, tv, recs, mats, nullptr, nullptr, X, S, BH, M, err, st));
+    GD_TRY(allow_smem(tc_gd_reverse<D>, RevSmem<D>::bytes));
+    launch_begin("tc_gd_reverse", st);
+    cudaError_t e = launch_pdl(tc_gd_reverse<D>, dim3(1, BH), dim3(kThreads), RevSmem<D>::bytes, st, tq, tk, tdo, tdv,
+                               (const float*)recs, (const uint8_t*)mats, Y, dS, M, M, err);
+    cudaError_t e2 = launch_end("tc_gd_reverse", st);
+    if (e != cudaSuccess || e2 != cudaSuccess) return e != cudaSuccess ? e : e2;
+    GD_TRY(allow_smem(tc_gd_grads<D>, GradSmem<D>::bytes));
+    launch_begin("tc_gd_grads", st);
+    e = launch_pdl(tc_gd_grads<D>, dim3(M, BH), dim3(kThreads), GradSmem<D>::bytes, st, tq, tk, tdo, tdq, tdk,
+                   (const __nv_bfloat16*)a.g, (const float*)recs, (const uint8_t*)X, (const uint8_t*)Y,
+                   (const uint8_t*)S, (const uint8_t*)dS, (__nv_bfloat16*)a.dg, (__nv_bfloat16*)a.dbeta, s.N, M, err);
+    e2 = launch_end("tc_gd_grads", st);
+    return e != cudaSuccess ? e : e2;
+}
+
+}  // namespace
+
+cudaError_t tc_bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) {
+    return s.Dk == 128 ? bwd<128>(a, s, ws, st) : bwd<64>(a, s, ws, st);
+}
+
+}  // namespace gd
+}  // namespace la

@@ -111,6 +111,8 @@ def library(path: str | None = None):
     With LA_DEBUG=1 in the environment the debug build (device-side index checks,
     _lib/libla_debug.so) is loaded instead of the regular one."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or _build.lib_path(os.environ.get("LA_DEBUG", "0") == "1")
@@ -146,9 +148,18 @@ def _need_cuda(*ts):
             raise ValueError("expected contiguous tensors")
 
 
+# The handle of the current stream without building a torch.cuda.Stream for it (3 us of a 20 us call), where
+# this PyTorch has that entry.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream_ptr(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return int(s.cuda_stream)
+    if stream is not None:
+        return int(stream.cuda_stream)
+    if _raw_stream is not None and _get_device is not None:
+        return _raw_stream(_get_device())
+    return int(torch.cuda.current_stream().cuda_stream)
 
 
 def _ptr(t):
@@ -358,6 +369,15 @@ def retention_step(q, k, v, gamma, S, out=None, stream=None):
     return out
 
 
+# The entry points below are called once per decoded token, where the time of the call itself counts: the checks
+# are written out over plain attributes, pointers go to ctypes as integers.
+_DTYPE_CODE = {torch.float32: LA_F32, torch.bfloat16: LA_BF16}
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
 def _result(t, like, what):
     """A caller's output tensor, checked against what it receives; a new one if None."""
     if t is None:
@@ -368,15 +388,27 @@ def _result(t, like, what):
     return t
 
 
-def _gates(g, beta, lead, dtype):
-    _need_cuda(g, beta)
-    if g.shape != lead or beta.shape != lead or g.dtype != dtype or beta.dtype != dtype:
-        raise ValueError("g and beta must be %s of the dtype of q" % ("[B,H,N]" if len(lead) == 3 else "[B,H]"))
+def _delta_args(q, k, v, g, beta):
+    """Checks the inputs of a gated delta call; returns their leading sizes, Dk, Dv and the dtype code."""
+    _need_cuda(q, k, v, g, beta)
+    qs, vs, dt = q.shape, v.shape, q.dtype
+    lead = qs[:-1]
+    if k.shape != qs or len(vs) != len(qs) or vs[:-1] != lead:
+        raise ValueError("expected q, k [..., Dk] and v [..., Dv]; got %s %s %s" %
+                         (tuple(qs), tuple(k.shape), tuple(vs)))
+    if k.dtype != dt or v.dtype != dt:
+        raise TypeError("q, k, v must share a dtype")
+    if g.shape != lead or beta.shape != lead or g.dtype != dt or beta.dtype != dt:
+        raise ValueError("g and beta must have the leading sizes %s and the dtype of q" % (tuple(lead),))
+    code = _DTYPE_CODE.get(dt)
+    if code is None:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dt)
+    return lead, qs[-1], vs[-1], code
 
 
-def _state(S, B, H, Dk, Dv, what):
+def _state(S, shape, what):
     _need_cuda(S)
-    if S.dtype != torch.float32 or S.shape != (B, H, Dk, Dv):
+    if S.dtype != torch.float32 or S.shape != shape:
         raise ValueError("%s must be fp32 [B,H,Dk,Dv]" % what)
 
 
@@ -389,72 +421,72 @@ def gated_delta_fwd(q, k, v, g, beta, S0=None, out=None, workspace=None, stream=
     position (zero if None).  With return_state, returns (o, S): the fp32 state after the last position, from
     which gated_delta_step or another gated_delta_fwd continues.
     """
-    _need_cuda(q, k, v)
-    s = _shape4(q, k, v)
-    B, H, N, Dk = q.shape
-    _gates(g, beta, (B, H, N), q.dtype)
+    lead, Dk, Dv, code = _delta_args(q, k, v, g, beta)
+    if len(lead) != 3:
+        raise ValueError("expected q, k [B,H,N,Dk] and v [B,H,N,Dv]")
+    B, H, N = lead
+    s = Shape(B, H, N, Dk, Dv, code)
     if S0 is not None:
-        _state(S0, B, H, Dk, s.Dv, "S0")
+        _state(S0, (B, H, Dk, Dv), "S0")
     out = _result(out, v, "out")
-    S = torch.empty(B, H, Dk, s.Dv, dtype=torch.float32, device=q.device) if return_state else None
+    S = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device) if return_state else None
     ws, nb = _workspace(OP_GATED_DELTA_FWD, s, q.device, workspace)
-    _check(library().la_gated_delta_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(out), _ptr(S),
-                                        s, _ptr(ws), nb, _stream_ptr(stream)), "la_gated_delta_fwd")
+    _check(library().la_gated_delta_fwd(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(S0), _p(out), _p(S), s, _p(ws), nb,
+                                        _stream_ptr(stream)), "la_gated_delta_fwd")
     return (out, S) if return_state else out
 
 
 def gated_delta_bwd(q, k, v, g, beta, dout, dq=None, dk=None, dv=None, dg=None, dbeta=None, workspace=None,
                     stream=None):
     """Gradients (dq, dk, dv, dg, dbeta) of gated_delta_fwd (from the zero state) for upstream gradient dout."""
-    _need_cuda(q, k, v, dout)
-    s = _shape4(q, k, v)
-    _gates(g, beta, tuple(q.shape[:3]), q.dtype)
+    lead, Dk, Dv, code = _delta_args(q, k, v, g, beta)
+    if len(lead) != 3:
+        raise ValueError("expected q, k [B,H,N,Dk] and v [B,H,N,Dv]")
+    _need_cuda(dout)
     if dout.shape != v.shape or dout.dtype != v.dtype:
         raise ValueError("dout must match v in shape and dtype")
+    s = Shape(*lead, Dk, Dv, code)
     dq = _result(dq, q, "dq")
     dk = _result(dk, k, "dk")
     dv = _result(dv, v, "dv")
     dg = _result(dg, g, "dg")
     dbeta = _result(dbeta, beta, "dbeta")
     ws, nb = _workspace(OP_GATED_DELTA_BWD, s, q.device, workspace)
-    _check(library().la_gated_delta_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(dout), _ptr(dq),
-                                        _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), s, _ptr(ws), nb,
-                                        _stream_ptr(stream)), "la_gated_delta_bwd")
+    _check(library().la_gated_delta_bwd(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(dout), _p(dq), _p(dk), _p(dv), _p(dg),
+                                        _p(dbeta), s, _p(ws), nb, _stream_ptr(stream)), "la_gated_delta_bwd")
     return dq, dk, dv, dg, dbeta
 
 
 def gated_delta_step(q, k, v, g, beta, S, out=None, stream=None):
     """One decode step of the gated delta rule: u = beta (v - a S^T k), S <- a S + k u^T (in place),
     out = S^T q, with a = exp(g).  q, k [B,H,Dk], v [B,H,Dv], g, beta [B,H], S fp32 [B,H,Dk,Dv]."""
-    _need_cuda(q, k, v)
-    if q.dim() != 3 or k.shape != q.shape or v.dim() != 3 or v.shape[:2] != q.shape[:2]:
+    lead, Dk, Dv, code = _delta_args(q, k, v, g, beta)
+    if len(lead) != 2:
         raise ValueError("expected q, k [B,H,Dk] and v [B,H,Dv]")
-    if not (q.dtype == k.dtype == v.dtype):
-        raise TypeError("q, k, v must share a dtype")
-    B, H, Dk = q.shape
-    Dv = v.shape[2]
-    _gates(g, beta, (B, H), q.dtype)
-    _state(S, B, H, Dk, Dv, "S")
+    B, H = lead
+    _state(S, (B, H, Dk, Dv), "S")
     out = _result(out, v, "out")
-    s = Shape(B, H, 1, Dk, Dv, _dtype_code(q))
-    _check(library().la_gated_delta_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S), _ptr(out), s,
-                                         _stream_ptr(stream)), "la_gated_delta_step")
+    _check(library().la_gated_delta_step(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(S), _p(out),
+                                         Shape(B, H, 1, Dk, Dv, code), _stream_ptr(stream)), "la_gated_delta_step")
     return out
 
 
-def _norm_shape(x):
-    if x.dim() < 1:
+def _norm_args(x, *params):
+    """Checks x and its [C] parameters (None: not given); returns the call's shape."""
+    _need_cuda(x)
+    xs, dt = x.shape, x.dtype
+    if not xs:
         raise ValueError("expected x of shape [..., C]")
-    C = x.shape[-1]
-    return NormShape(x.numel() // C if C else 0, C, _dtype_code(x))
-
-
-def _norm_param(p, x, what):
-    if p is None:
-        return
-    _need_cuda(p)
-    if p.shape != x.shape[-1:] or p.dtype != x.dtype:
-        raise ValueError("%s must be [C] of the dtype of x" % what)
+    code = _DTYPE_CODE.get(dt)
+    if code is None:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dt)
+    C = xs[-1]
+    for p in params:
+        if p is not None:
+            _need_cuda(p)
+            if p.shape != xs[-1:] or p.dtype != dt:
+                raise ValueError("weight and bias must be [C] of the dtype of x")
+    return NormShape(x.numel() // C if C else 0, C, code)
 
 
 def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, stream=None, return_stats=False):
@@ -463,55 +495,50 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, stream=None, r
     weight and bias are [C] of x's dtype, or None (1 and 0).  With return_stats, returns
     (y, mean, rstd): the fp32 statistics of shape x.shape[:-1] that layer_norm_bwd takes.
     """
-    _need_cuda(x)
-    s = _norm_shape(x)
-    _norm_param(weight, x, "weight")
-    _norm_param(bias, x, "bias")
+    s = _norm_args(x, weight, bias)
     out = _result(out, x, "out")
     mean = rstd = None
     if return_stats:
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         rstd = torch.empty_like(mean)
-    _check(library().la_layer_norm_fwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(out), _ptr(mean), _ptr(rstd), s, eps,
+    _check(library().la_layer_norm_fwd(_p(x), _p(weight), _p(bias), _p(out), _p(mean), _p(rstd), s, eps,
                                        _stream_ptr(stream)), "la_layer_norm_fwd")
     return (out, mean, rstd) if return_stats else out
 
 
 def layer_norm_workspace_bytes(rows: int, C: int, dtype: torch.dtype) -> int:
-    if dtype not in (torch.float32, torch.bfloat16):
+    if dtype not in _DTYPE_CODE:
         raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dtype)
-    code = LA_BF16 if dtype == torch.bfloat16 else LA_F32
-    return int(library().la_layer_norm_workspace_bytes(NormShape(rows, C, code)))
+    return int(library().la_layer_norm_workspace_bytes(NormShape(rows, C, _DTYPE_CODE[dtype])))
 
 
 def layer_norm_bwd(x, weight, mean, rstd, dout, dx=None, dweight=None, dbias=None, workspace=None, stream=None):
     """Gradients (dx, dweight, dbias) of layer_norm_fwd for upstream gradient dout, from its
     statistics.  With weight None there is no weight or bias: dweight and dbias are None."""
-    _need_cuda(x, mean, rstd, dout)
-    s = _norm_shape(x)
-    _norm_param(weight, x, "weight")
+    s = _norm_args(x, weight)
+    _need_cuda(mean, rstd, dout)
     if dout.shape != x.shape or dout.dtype != x.dtype:
         raise ValueError("dout must match x in shape and dtype")
-    for t in (mean, rstd):
-        if t.dtype != torch.float32 or t.shape != x.shape[:-1]:
-            raise ValueError("mean and rstd must be fp32 of shape x.shape[:-1]")
+    stats = x.shape[:-1]
+    if mean.dtype != torch.float32 or rstd.dtype != torch.float32 or mean.shape != stats or rstd.shape != stats:
+        raise ValueError("mean and rstd must be fp32 of shape x.shape[:-1]")
     dx = _result(dx, x, "dx")
+    lib = library()
     ws, nb = None, 0
     if weight is not None:
         dweight = _result(dweight, weight, "dweight")
         dbias = _result(dbias, weight, "dbias")
-        nb = int(library().la_layer_norm_workspace_bytes(s))
         if workspace is not None:
             if not workspace.is_cuda:
                 raise ValueError("workspace must be a device tensor")
             ws, nb = workspace, workspace.numel() * workspace.element_size()
         else:
+            nb = int(lib.la_layer_norm_workspace_bytes(s))
             ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
     else:
         dweight = dbias = None
-    _check(library().la_layer_norm_bwd(_ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dout), _ptr(dx),
-                                       _ptr(dweight), _ptr(dbias), s, _ptr(ws), nb, _stream_ptr(stream)),
-           "la_layer_norm_bwd")
+    _check(lib.la_layer_norm_bwd(_p(x), _p(weight), _p(mean), _p(rstd), _p(dout), _p(dx), _p(dweight), _p(dbias), s,
+                                 _p(ws), nb, _stream_ptr(stream)), "la_layer_norm_bwd")
     return dx, dweight, dbias
 
 

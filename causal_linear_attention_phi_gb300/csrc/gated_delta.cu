@@ -571,6 +571,20 @@ Layout layout(const la_shape& s, bool bwd) {
         L.S = take(chunks * s.Dk * s.Dv / half);
         L.dS = take(chunks * s.Dk * s.Dv / half);
     }
+    const int M = (s.N + kC - 1) / kC;
+    L.segs = tc_ok(s) ? tc_segments(s, bwd) : 1;
+    L.cps = (M + L.segs - 1) / L.segs;
+    L.segs = (M + L.cps - 1) / L.cps;  // no empty segment
+    if (L.segs > 1) {
+        const size_t seg = (size_t)s.B * s.H * L.segs * s.Dk * s.Dv;
+        L.segB = take(seg);
+        L.segM = take(seg);
+        L.segS = take(seg);
+        if (bwd) {
+            L.segB2 = take(seg);
+            L.segdS = take(seg);
+        }
+    }
     L.bytes = off;
     return L;
 }

@@ -183,6 +183,11 @@ struct Layout {
     // The gradient's, fp32 (tensor cores: bf16 tiles of transposed matrices, X and Y as lo and hi parts):
     size_t X, Y;    // [BH][M * 64][Dv]
     size_t S, dS;   // [BH][M][Dk][Dv]: the state entering each chunk, the gradient leaving it
+    // Tensor cores, segs > 1 segments of cps chunks to a head (fp32 Dk x Dv records [BH][segs]): the state that a
+    // segment adds (B) and the map that it applies to the state entering it (M); the states entering the segments; and
+    // for the gradient, what a segment adds to the state's gradient (B2) and the gradients leaving the segments.
+    int segs, cps;
+    size_t segB, segM, segS, segB2, segdS;
     size_t bytes;
 };
 Layout layout(const la_shape& s, bool bwd);
@@ -202,6 +207,8 @@ cudaError_t simt_fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t
 cudaError_t simt_bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st);
 // bf16 heads with Dk = Dv = 64 or 128, on the tensor cores.
 bool tc_ok(const la_shape& s);
+// Segments of a head for M chunks (a function of the sizes alone).
+int tc_segments(const la_shape& s, bool bwd);
 cudaError_t tc_fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st);
 cudaError_t tc_bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st);
 cudaError_t step(const void* q, const void* k, const void* v, const void* g, const void* beta, float* S, void* out,

@@ -153,10 +153,6 @@ struct __align__(8) Bars {
     uint64_t s_ready, y_done, r_ready, x_done, u_ready, s_done, o_ready, o_done, o_free, final_mma;
 };
 
-// kOut: outputs.  kGrad: the gradient's records instead, for each chunk the state entering it (s_tiles, S^T as
-// [Dv rows x Dk] bf16 tiles of 64 columns) and X (x_tiles, lo then hi, X^T as [Dv rows x 64 positions]).
-enum Mode { kOut, kGrad };
-
 template <int D, int kMode>
 struct FwdSmem {
     static constexpr int tile = D / 64 * kBlk, nmats = kMode == kOut ? kMats : 2 * kBlk;
@@ -166,7 +162,7 @@ struct FwdSmem {
     static_assert(kGateBytes <= 2048, "gates");
     static constexpr int out = 2 * stage;  // kOut: the o tile; kGrad: the state's tile and X lo, X hi
     static constexpr int sbytes = D * D * 2, xbytes = 2 * D * 128;
-    static constexpr int bars = out + (kMode == kOut ? tile : sbytes + xbytes);
+    static constexpr int bars = out + (kMode == kOut ? tile : kMode == kGrad ? sbytes + xbytes : 0);
     static constexpr int slot = bars + 256;
     static constexpr int total = slot + 16;
     static constexpr size_t bytes = total + 1024;
@@ -181,13 +177,12 @@ struct Tm {
     static_assert(dS + 128 <= 512, "TMEM");
 };
 
-// Chunks [p cps, (p + 1) cps) of a head.  S0 / S_out: fp32 [BH][D][D] (null: zero / not wanted).
+// One block per (segment, head); kSum with D = 128 has a third grid dimension: 0 the sum, 1 the map (with D = 64 the
+// upper lanes, which have no value columns, carry the map).
 template <int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-             const float* __restrict__ recs, const uint8_t* __restrict__ mats, const float* S0, float* S_out,
-             uint8_t* __restrict__ x_tiles, uint8_t* __restrict__ s_tiles, int M, int cps, int* err) {
+             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, StateArgs a, int* err) {
     using L = FwdSmem<D, kMode>;
     using T = Tm<D>;
     constexpr int kSc = D / kHs;  // state columns of a thread
@@ -196,8 +191,10 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     Bars* bar = reinterpret_cast<Bars*>(base + L::bars);
     uint32_t* slot = reinterpret_cast<uint32_t*>(base + L::slot);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int p = blockIdx.x, bh = blockIdx.y, cbeg = p * cps, nloc = min(M, cbeg + cps) - cbeg;
+    const int p = blockIdx.x, bh = blockIdx.y, M = a.M, cbeg = p * a.cps, nloc = min(M, cbeg + a.cps) - cbeg;
+    const bool map = kMode == kSum && blockIdx.z == 1;  // D = 128: this block forms the segment's map
     LA_DCHECK(nloc >= 1);
+    if (kMode == kSum && D == 128 && !map && p >= a.nsum) return;
 
     if (tid == 0) {
         mbar_init(&bar->full[0], 1);
@@ -238,8 +235,8 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     if (kMode == kOut) tma_load_3d(st + L::Q + b * kBlk, &tm_q, 64 * b, t0, bh, &bar->full[s]);
                 }
                 const size_t at = (size_t)bh * M + c;
-                bulk_load(st + L::mats, mats + at * kMats, kMode == kOut ? kMats : 2 * kBlk, &bar->full[s]);
-                bulk_load(st + L::gates, recs + at * kRec, kGateBytes, &bar->full[s]);
+                bulk_load(st + L::mats, a.mats + at * kMats, kMode == kOut ? kMats : 2 * kBlk, &bar->full[s]);
+                bulk_load(st + L::gates, a.recs + at * kRec, kGateBytes, &bar->full[s]);
                 armed[s] = i;
             }
             // never leave with copies in flight: wait for the last armed phase of each stage
@@ -336,7 +333,9 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         float S[kSc];
 #pragma unroll
         for (int x = 0; x < kSc; ++x)
-            S[x] = S0 && r < D ? S0[((size_t)bh * D + kSc * h + x) * D + r] : 0.f;
+            S[x] = kMode == kSum ? ((map && kSc * h + x == r) || (D == 64 && kSc * h + x == r - D) ? 1.f : 0.f)
+                   : a.S0 && r < D ? a.S0[(((size_t)bh * a.P + p) * D + kSc * h + x) * D + r]
+                                   : 0.f;
         auto put_state = [&]() {  // the state's hi and lo parts, and the signal that they are there
             uint32_t hi[kSc / 2], lo[kSc / 2];
 #pragma unroll
@@ -387,7 +386,7 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 const float bb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float v = r < D ? __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(
+                    const float v = r < D && !map ? __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(
                                                                 sg + L::V + elem_off(kTok * h + x + e, r))
                                                             << 16)
                                           : 0.f;
@@ -459,7 +458,7 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 }
                 st(lb + T::U + kTok / 2 * h, hi);
                 st(lb + T::U + 32 + kTok / 2 * h, lo);
-            } else {  // this thread's row of the state's tile (the state entering the chunk) and of X's tiles
+            } else if constexpr (kMode == kGrad) {  // this thread's row of the state's tile (the state entering the chunk) and of X's tiles
                 if (ct == 0) bulk_wait_read_all();  // the previous chunk's stores have read the tiles
                 named_barrier(1, 32 * kWarps);
                 if (r < D) {
@@ -487,8 +486,8 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 named_barrier(1, 32 * kWarps);
                 if (ct == 0) {
                     const size_t at = (size_t)bh * M + cbeg + i;
-                    bulk_store(s_tiles + at * L::sbytes, base + L::out, L::sbytes);
-                    bulk_store(x_tiles + at * L::xbytes, base + L::out + L::sbytes, L::xbytes);
+                    bulk_store(a.s_tiles + at * L::sbytes, base + L::out, L::sbytes);
+                    bulk_store(a.x_tiles + at * L::xbytes, base + L::out + L::sbytes, L::xbytes);
                     bulk_commit();
                 }
             }
@@ -522,9 +521,13 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         }
         if (kMode == kOut) output(nloc - 1);
         if (ct == 0) bulk_wait_all();
-        if (S_out && r < D) {
+        if (kMode == kSum) {
+            float* rec = (map || r >= D ? a.segM : a.segB) + ((size_t)bh * a.P + p) * (D * D) + (r & (D - 1));
 #pragma unroll
-            for (int x = 0; x < kSc; ++x) S_out[((size_t)bh * D + kSc * h + x) * D + r] = S[x];
+            for (int x = 0; x < kSc; ++x) rec[(kSc * h + x) * D] = S[x];
+        } else if (kMode == kOut && a.S_out && p == a.P - 1 && r < D) {
+#pragma unroll
+            for (int x = 0; x < kSc; ++x) a.S_out[((size_t)bh * D + kSc * h + x) * D + r] = S[x];
         }
         tc_fence_before();
     }
@@ -532,6 +535,105 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ joining the segments
+// Block (slice, head): kJoinCols value columns of the state, carried through the segments' maps in fp32:
+// out[p + 1] = B[p] + M[p] out[p], or in reverse out[p - 1] = B[p] + M[p]^T out[p].  A map (64 KB for D = 128) is copied to
+// shared memory while the previous one is applied; rows are padded by 16 bytes against bank conflicts.
+constexpr int kJoinCols = 16, kJoinThreads = 256;
+template <int D>
+struct JoinSmem {
+    static constexpr int pitch = D + 4;  // floats
+    static constexpr int map = D * pitch * 4;
+    static constexpr int S = 2 * map;    // [D][kJoinCols]
+    static constexpr int bars = S + D * kJoinCols * 4;
+    static constexpr size_t bytes = bars + 32;
+};
+
+template <int D, bool kReverse>
+__global__ void __launch_bounds__(kJoinThreads)
+tc_gd_join(const float* __restrict__ B, const float* __restrict__ Mx, const float* __restrict__ first,
+           float* __restrict__ out, int P, int* err) {
+    using L = JoinSmem<D>;
+    constexpr int kThr = kJoinThreads / D;          // threads of a row: 2 (D = 128) or 4
+    constexpr int kCols = kJoinCols / kThr;         // columns of a thread: 8 or 4
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* S = reinterpret_cast<float*>(smem + L::S);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::bars);
+    const int tid = threadIdx.x, row = tid / kThr, c0 = tid % kThr * kCols, col = blockIdx.x * kJoinCols + c0;
+    const size_t bh = blockIdx.y, rec = (size_t)D * D;
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        mbar_init(bar + 1, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_enter();  // launched with programmatic dependent launch
+    // the i-th map applied: segment i, or from the last one back
+    auto seg = [&](int i) { return bh * P + (kReverse ? P - 1 - i : i); };
+    auto load = [&](int i) {
+        if (tid >= 32) return;
+        if (tid == 0) mbar_arrive_expect_tx(bar + (i & 1), D * D * 4);
+        __syncwarp();
+        for (int r = tid; r < D; r += 32)
+            bulk_load(smem + (i & 1) * L::map + r * L::pitch * 4, Mx + seg(i) * rec + r * D, D * 4, bar + (i & 1));
+    };
+    float s[kCols];
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) s[x] = !kReverse && first ? first[bh * rec + row * D + col + x] : 0.f;
+    load(0);
+    bool ok = true;
+    for (int i = 0; i < P; ++i) {
+        float* o = out + seg(i) * rec + row * D + col;
+#pragma unroll
+        for (int x = 0; x < kCols; x += 4) {
+            *reinterpret_cast<float4*>(o + x) = make_float4(s[x], s[x + 1], s[x + 2], s[x + 3]);
+            *reinterpret_cast<float4*>(S + row * kJoinCols + c0 + x) = make_float4(s[x], s[x + 1], s[x + 2], s[x + 3]);
+        }
+        if (i == P - 1) break;
+        if (i + 1 < P - 1) load(i + 1);  // its buffer was last read before the previous barrier
+        const float* b = B + seg(i) * rec + row * D + col;
+        float acc[kCols];
+#pragma unroll
+        for (int x = 0; x < kCols; x += 4) {
+            const float4 v = ld_f4(b + x);
+            acc[x] = v.x;
+            acc[x + 1] = v.y;
+            acc[x + 2] = v.z;
+            acc[x + 3] = v.w;
+        }
+        ok = ok && mbar_wait(bar + (i & 1), (i >> 1) & 1, err, LA_ERR_TIMEOUT);
+        __syncthreads();
+        const float* m = reinterpret_cast<const float*>(smem + (i & 1) * L::map);
+#pragma unroll 4
+        for (int k = 0; k < D; k += 4) {
+            float mv[4];
+            if (kReverse) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mv[e] = m[(k + e) * L::pitch + row];
+            } else {
+                const float4 v = ld_f4(m + row * L::pitch + k);
+                mv[0] = v.x;
+                mv[1] = v.y;
+                mv[2] = v.z;
+                mv[3] = v.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int x = 0; x < kCols; x += 4) {
+                    const float4 v = ld_f4(S + (k + e) * kJoinCols + c0 + x);
+                    acc[x] = fmaf(mv[e], v.x, acc[x]);
+                    acc[x + 1] = fmaf(mv[e], v.y, acc[x + 1]);
+                    acc[x + 2] = fmaf(mv[e], v.z, acc[x + 2]);
+                    acc[x + 3] = fmaf(mv[e], v.w, acc[x + 3]);
+                }
+        }
+        __syncthreads();  // S and the map have been read
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) s[x] = acc[x];
     }
 }
 
@@ -557,25 +659,40 @@ template cudaError_t prepare<128>(const CUtensorMap&, const CUtensorMap&, const 
 
 template <int D>
 cudaError_t states(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
-                   const float* recs, const uint8_t* mats, const float* S0, float* S_out, uint8_t* x_tiles,
-                   uint8_t* s_tiles, int BH, int M, int* err, cudaStream_t st) {
-    const bool grad = x_tiles != nullptr;
-    auto kern = grad ? tc_gd_states<D, kGrad> : tc_gd_states<D, kOut>;
-    const size_t smem = grad ? FwdSmem<D, kGrad>::bytes : FwdSmem<D, kOut>::bytes;
+                   const StateArgs& a, Mode mode, int BH, int segments, int* err, cudaStream_t st) {
+    auto kern = mode == kOut ? tc_gd_states<D, kOut> : mode == kGrad ? tc_gd_states<D, kGrad> : tc_gd_states<D, kSum>;
+    const size_t smem = mode == kOut    ? FwdSmem<D, kOut>::bytes
+                        : mode == kGrad ? FwdSmem<D, kGrad>::bytes
+                                        : FwdSmem<D, kSum>::bytes;
     GD_TRY(allow_smem(kern, smem));
-    const char* name = grad ? "tc_gd_states_grad" : "tc_gd_states";
+    const char* name = mode == kOut ? "tc_gd_states" : mode == kGrad ? "tc_gd_states_grad" : "tc_gd_segments";
     launch_begin(name, st);
-    const cudaError_t e = launch_pdl(kern, dim3(1, BH), dim3(kThreads), smem, st, tq, tk, tv, to, recs, mats, S0, S_out,
-                                     x_tiles, s_tiles, M, M, err);
+    const cudaError_t e = launch_pdl(kern, dim3(segments, BH, mode == kSum && D == 128 ? 2 : 1), dim3(kThreads), smem, st,
+                                     tq, tk, tv, to, a, err);
     const cudaError_t e2 = launch_end(name, st);
     return e != cudaSuccess ? e : e2;
 }
-template cudaError_t states<64>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
-                                const float*, const uint8_t*, const float*, float*, uint8_t*, uint8_t*, int, int, int*,
-                                cudaStream_t);
-template cudaError_t states<128>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
-                                 const float*, const uint8_t*, const float*, float*, uint8_t*, uint8_t*, int, int,
-                                 int*, cudaStream_t);
+
+template <int D>
+cudaError_t join(const float* B, const float* Mx, const float* first, float* out, int BH, int P, bool reverse, int* err,
+                 cudaStream_t st) {
+    auto kern = reverse ? tc_gd_join<D, true> : tc_gd_join<D, false>;
+    GD_TRY(allow_smem(kern, JoinSmem<D>::bytes));
+    const char* name = reverse ? "tc_gd_join_reverse" : "tc_gd_join";
+    launch_begin(name, st);
+    const cudaError_t e =
+        launch_pdl(kern, dim3(D / kJoinCols, BH), dim3(kJoinThreads), JoinSmem<D>::bytes, st, B, Mx, first, out, P, err);
+    const cudaError_t e2 = launch_end(name, st);
+    return e != cudaSuccess ? e : e2;
+}
+
+#define GD_INSTANCE(D)                                                                                              \
+    template cudaError_t states<D>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, \
+                                   const StateArgs&, Mode, int, int, int*, cudaStream_t);                          \
+    template cudaError_t join<D>(const float*, const float*, const float*, float*, int, int, bool, int*, cudaStream_t);
+GD_INSTANCE(64)
+GD_INSTANCE(128)
+#undef GD_INSTANCE
 
 }  // namespace tcgd
 
@@ -593,10 +710,52 @@ cudaError_t fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
     float* recs = (float*)(ws + L.rec);
     uint8_t* mats = (uint8_t*)(ws + L.t);
     GD_TRY(prepare<D>(tq, tk, a.g, a.beta, recs, mats, s, M, err, st));
-    return states<D>(tq, tk, tv, to, recs, mats, a.S0, a.S, nullptr, nullptr, BH, M, err, st);
+    StateArgs sa{};
+    sa.recs = recs;
+    sa.mats = mats;
+    sa.M = M;
+    sa.P = L.segs;
+    sa.cps = L.cps;
+    if (L.segs > 1) {
+        float *B = (float*)(ws + L.segB), *Mx = (float*)(ws + L.segM), *S = (float*)(ws + L.segS);
+        sa.segB = B;
+        sa.segM = Mx;
+        sa.nsum = L.segs - 1;
+        GD_TRY(states<D>(tq, tk, tv, to, sa, kSum, BH, L.segs - 1, err, st));
+        GD_TRY(join<D>(B, Mx, a.S0, S, BH, L.segs, false, err, st));
+        sa.S0 = S;
+    } else {
+        sa.S0 = a.S0;
+    }
+    sa.S_out = a.S;
+    return states<D>(tq, tk, tv, to, sa, kOut, BH, L.segs, err, st);
 }
 
 }  // namespace
+
+// More segments fill more of the 152 SMs and shorten the chain of chunks, but with P > 1 every segment but the last
+// is walked once more for its sum and once for its map (twice the blocks for D = 128), and the segments are joined one
+// after another.  The costs below are the measured microseconds of a chunk in each kernel.
+int tc_segments(const la_shape& s, bool bwd) {
+    constexpr int kSms = 152;
+    const int BH = s.B * s.H, M = (s.N + kC - 1) / kC;
+    const double main = bwd ? 7.9 : 3.0, sum = bwd ? 2.2 : 2.2, join = bwd ? 2.6 : 1.3;
+    auto waves = [](long long blocks) { return (double)((blocks + kSms - 1) / kSms); };
+    int best = 1;
+    double best_t = waves(BH) * M * main;
+    for (int P = 2; P <= M && P <= 64; ++P) {
+        const int cps = (M + P - 1) / P;
+        if ((M + cps - 1) / cps != P) continue;
+        double t = waves((long long)BH * P) * cps * main + 10.0 + P * join;
+        t += waves((long long)BH * (P - 1) * (s.Dk == 128 ? 2 : 1)) * cps * sum;
+        if (bwd) t += waves((long long)BH * (P - 1)) * cps * 3.8;
+        if (t < 0.95 * best_t) {
+            best_t = t;
+            best = P;
+        }
+    }
+    return best;
+}
 
 bool tc_ok(const la_shape& s) { return s.dtype == LA_BF16 && s.Dk == s.Dv && (s.Dk == 64 || s.Dk == 128); }
 

@@ -138,11 +138,29 @@ cudaError_t allow_smem(K kern, size_t bytes) {
 template <int D>
 cudaError_t prepare(const CUtensorMap& tq, const CUtensorMap& tk, const void* g, const void* beta, float* recs,
                     uint8_t* mats, const la_shape& s, int M, int* err, cudaStream_t st);
-// The recurrence; `x_tiles` and `s_tiles` given: the gradient's records instead of outputs.
+// The recurrence's modes.  kOut: outputs.  kGrad: the gradient's records instead, for each chunk the state entering it
+// (s_tiles, S^T as [Dv rows x Dk] bf16 tiles of 64 columns) and X (x_tiles, lo then hi, X^T as [Dv rows x 64
+// positions]).  kSum: only the segment's last state, from a zero state (segB) and, with no values, from the identity
+// (segM): the state after a segment is segB + segM (the state before it).
+enum Mode { kOut, kGrad, kSum };
+struct StateArgs {
+    const float* recs;
+    const uint8_t* mats;
+    const float* S0;   // [BH][P] records: the states entering the segments; null: zero
+    float* S_out;      // kOut: [BH] records, the state after the last position, or null
+    uint8_t *x_tiles, *s_tiles;   // kGrad
+    float *segB, *segM;           // kSum: [BH][P] records
+    int M, P, cps;                // chunks, segments, chunks of a segment
+    int nsum;                     // kSum: segments whose B is wanted (the first nsum)
+};
 template <int D>
 cudaError_t states(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
-                   const float* recs, const uint8_t* mats, const float* S0, float* S_out, uint8_t* x_tiles,
-                   uint8_t* s_tiles, int BH, int M, int* err, cudaStream_t st);
+                   const StateArgs& a, Mode mode, int BH, int segments, int* err, cudaStream_t st);
+// Joins the segments' sums: out[p + 1] = B[p] + M[p] out[p] from out[0] = first (or zero); reverse: out[P - 1] = 0,
+// out[p - 1] = B[p] + M[p]^T out[p].
+template <int D>
+cudaError_t join(const float* B, const float* Mx, const float* first, float* out, int BH, int P, bool reverse, int* err,
+                 cudaStream_t st);
 
 }  // namespace tcgd
 }  // namespace gd

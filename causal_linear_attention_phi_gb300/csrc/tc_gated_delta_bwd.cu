@@ -50,12 +50,14 @@ struct RTm {
     static_assert(dS + 128 <= 512, "TMEM");
 };
 
-template <int D>
+// kSums: only the gradient that a segment adds to that of the state before it (segB2), from a zero gradient after it.
+template <int D, bool kSums>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dv,
               const float* __restrict__ recs, const uint8_t* __restrict__ mats, uint8_t* __restrict__ y_tiles,
-              uint8_t* __restrict__ ds_tiles, int M, int cps, int* err) {
+              uint8_t* __restrict__ ds_tiles, const float* __restrict__ segdS, float* __restrict__ segB2, int M, int P,
+              int cps, int* err) {
     using L = RevSmem<D>;
     using T = RTm<D>;
     constexpr int kSc = D / kHs;  // state columns of a thread
@@ -64,7 +66,8 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     RBars* bar = reinterpret_cast<RBars*>(base + L::bars);
     uint32_t* slot = reinterpret_cast<uint32_t*>(base + L::slot);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int p = blockIdx.x, bh = blockIdx.y, cbeg = p * cps, cend = min(M, cbeg + cps), nloc = cend - cbeg;
+    const int p = blockIdx.x + (kSums ? 1 : 0);  // the first segment's sum is not needed
+    const int bh = blockIdx.y, cbeg = p * cps, cend = min(M, cbeg + cps), nloc = cend - cbeg;
     LA_DCHECK(nloc >= 1);
     if (tid == 0) {
         mbar_init(&bar->full[0], 1);
@@ -192,7 +195,8 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         };
         float S[kSc];
 #pragma unroll
-        for (int x = 0; x < kSc; ++x) S[x] = 0.f;
+        for (int x = 0; x < kSc; ++x)
+            S[x] = !kSums && segdS && r < D ? segdS[(((size_t)bh * P + p) * D + kSc * h + x) * D + r] : 0.f;
         uint8_t* out = base + L::out;
         for (int i = 0; i < nloc; ++i) {
             const int s = i & 1, ph = i & 1, c = cend - 1 - i;
@@ -208,22 +212,23 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 st(lb + T::SLo + kSc / 2 * h, lo);
                 tmem_st_wait();
                 arrive(&bar->s_ready);
-                // its tile: the gradient leaving this chunk
-                if (ct == 0) bulk_wait_read_all();
-                named_barrier(1, 32 * kWarps);
-                if (r < D) {
+                if constexpr (!kSums) {  // its tile: the gradient leaving this chunk
+                    if (ct == 0) bulk_wait_read_all();
+                    named_barrier(1, 32 * kWarps);
+                    if (r < D) {
 #pragma unroll
-                    for (int x = 0; x < kSc; x += 8) {
-                        const int cc = kSc * h + x;
-                        *reinterpret_cast<uint4*>(out + (cc >> 6) * (D * 128) + row_off(r, cc >> 3)) =
-                            make_uint4(hi[x / 2], hi[x / 2 + 1], hi[x / 2 + 2], hi[x / 2 + 3]);
+                        for (int x = 0; x < kSc; x += 8) {
+                            const int cc = kSc * h + x;
+                            *reinterpret_cast<uint4*>(out + (cc >> 6) * (D * 128) + row_off(r, cc >> 3)) =
+                                make_uint4(hi[x / 2], hi[x / 2 + 1], hi[x / 2 + 2], hi[x / 2 + 3]);
+                        }
                     }
-                }
-                fence_proxy_async_smem();
-                named_barrier(1, 32 * kWarps);
-                if (ct == 0) {
-                    bulk_store(ds_tiles + at * L::sbytes, out, L::sbytes);
-                    bulk_commit();
+                    fence_proxy_async_smem();
+                    named_barrier(1, 32 * kWarps);
+                    if (ct == 0) {
+                        bulk_store(ds_tiles + at * L::sbytes, out, L::sbytes);
+                        bulk_commit();
+                    }
                 }
             }
             uint32_t w[kTok], hi[kTok / 2], lo[kTok / 2];
@@ -289,38 +294,40 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             tmem_st_wait();
             arrive(&bar->r_ready);
             const float gc = gates[kGam + kC - 1];
-            // dV's tile [positions][value columns] and Y's [value columns][positions]
-            if (ct == 0) bulk_wait_read_all();
-            named_barrier(1, 32 * kWarps);
-            if (r < D) {
+            if constexpr (!kSums) {
+                // dV's tile [positions][value columns] and Y's [value columns][positions]
+                if (ct == 0) bulk_wait_read_all();
+                named_barrier(1, 32 * kWarps);
+                if (r < D) {
 #pragma unroll
-                for (int x = 0; x < kTok; x += 4) {
-                    const float4 b = gate(kBeta, x);
-                    const float bb[4] = {b.x, b.y, b.z, b.w};
+                    for (int x = 0; x < kTok; x += 4) {
+                        const float4 b = gate(kBeta, x);
+                        const float bb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<__nv_bfloat16*>(out + elem_off(kTok * h + x + e, r)) =
-                            __float2bfloat16_rn(bb[e] * dU[x + e]);
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<__nv_bfloat16*>(out + elem_off(kTok * h + x + e, r)) =
+                                __float2bfloat16_rn(bb[e] * dU[x + e]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < kTok; x += 8) {
+                        uint4 a, b;
+                        split2(dU[x], dU[x + 1], a.x, b.x);
+                        split2(dU[x + 2], dU[x + 3], a.y, b.y);
+                        split2(dU[x + 4], dU[x + 5], a.z, b.z);
+                        split2(dU[x + 6], dU[x + 7], a.w, b.w);
+                        uint8_t* y = out + L::tile + row_off(r, (kTok * h + x) >> 3);
+                        *reinterpret_cast<uint4*>(y) = b;
+                        *reinterpret_cast<uint4*>(y + D * 128) = a;
+                    }
                 }
+                fence_proxy_async_smem();
+                named_barrier(1, 32 * kWarps);
+                if (ct == 0) {
 #pragma unroll
-                for (int x = 0; x < kTok; x += 8) {
-                    uint4 a, b;
-                    split2(dU[x], dU[x + 1], a.x, b.x);
-                    split2(dU[x + 2], dU[x + 3], a.y, b.y);
-                    split2(dU[x + 4], dU[x + 5], a.z, b.z);
-                    split2(dU[x + 6], dU[x + 7], a.w, b.w);
-                    uint8_t* y = out + L::tile + row_off(r, (kTok * h + x) >> 3);
-                    *reinterpret_cast<uint4*>(y) = b;
-                    *reinterpret_cast<uint4*>(y + D * 128) = a;
+                    for (int b = 0; b < D / 64; ++b) tma_store_3d(&tm_dv, out + b * kBlk, 64 * b, c * kC, bh);
+                    bulk_store(y_tiles + at * L::ybytes, out + L::tile, L::ybytes);
+                    bulk_commit();
                 }
-            }
-            fence_proxy_async_smem();
-            named_barrier(1, 32 * kWarps);
-            if (ct == 0) {
-#pragma unroll
-                for (int b = 0; b < D / 64; ++b) tma_store_3d(&tm_dv, out + b * kBlk, 64 * b, c * kC, bh);
-                bulk_store(y_tiles + at * L::ybytes, out + L::tile, L::ybytes);
-                bulk_commit();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar->empty[s]);  // this warp is done with dO and the gates
@@ -334,6 +341,10 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             }
         }
         if (ct == 0) bulk_wait_all();
+        if (kSums && r < D) {
+#pragma unroll
+            for (int x = 0; x < kSc; ++x) segB2[(((size_t)bh * P + p) * D + kSc * h + x) * D + r] = S[x];
+        }
         tc_fence_before();
     }
     __syncthreads();
@@ -688,19 +699,45 @@ cudaError_t bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
     uint8_t *mats = (uint8_t*)(ws + L.t), *X = (uint8_t*)(ws + L.X), *Y = (uint8_t*)(ws + L.Y), *S = (uint8_t*)(ws + L.S),
             *dS = (uint8_t*)(ws + L.dS);
     GD_TRY(prepare<D>(tq, tk, a.g, a.beta, recs, mats, s, M, err, st));
-    GD_TRY(states<D>(tq, tk, tv, tv, recs, mats, nullptr, nullptr, X, S, BH, M, err, st));
-    GD_TRY(allow_smem(tc_gd_reverse<D>, RevSmem<D>::bytes));
-    launch_begin("tc_gd_reverse", st);
-    cudaError_t e = launch_pdl(tc_gd_reverse<D>, dim3(1, BH), dim3(kThreads), RevSmem<D>::bytes, st, tq, tk, tdo, tdv,
-                               (const float*)recs, (const uint8_t*)mats, Y, dS, M, M, err);
-    cudaError_t e2 = launch_end("tc_gd_reverse", st);
-    if (e != cudaSuccess || e2 != cudaSuccess) return e != cudaSuccess ? e : e2;
+    StateArgs sa{};
+    sa.recs = recs;
+    sa.mats = mats;
+    sa.x_tiles = X;
+    sa.s_tiles = S;
+    sa.M = M;
+    sa.P = L.segs;
+    sa.cps = L.cps;
+    auto reverse = [&](bool sums, const float* segdS, float* segB2) {
+        auto kern = sums ? tc_gd_reverse<D, true> : tc_gd_reverse<D, false>;
+        GD_TRY(allow_smem(kern, RevSmem<D>::bytes));
+        const char* name = sums ? "tc_gd_reverse_segments" : "tc_gd_reverse";
+        launch_begin(name, st);
+        const cudaError_t e =
+            launch_pdl(kern, dim3(sums ? L.segs - 1 : L.segs, BH), dim3(kThreads), RevSmem<D>::bytes, st, tq, tk, tdo, tdv,
+                       (const float*)recs, (const uint8_t*)mats, Y, dS, segdS, segB2, M, L.segs, L.cps, err);
+        const cudaError_t e2 = launch_end(name, st);
+        return e != cudaSuccess ? e : e2;
+    };
+    const float* segdS = nullptr;
+    if (L.segs > 1) {
+        sa.segB = (float*)(ws + L.segB);
+        sa.segM = (float*)(ws + L.segM);
+        sa.nsum = L.segs - 1;  // the maps of all segments are wanted: the first for the states, the last for their gradients
+        GD_TRY(states<D>(tq, tk, tv, tv, sa, kSum, BH, L.segs, err, st));
+        GD_TRY(reverse(true, nullptr, (float*)(ws + L.segB2)));
+        GD_TRY(join<D>(sa.segB, sa.segM, nullptr, (float*)(ws + L.segS), BH, L.segs, false, err, st));
+        GD_TRY(join<D>((float*)(ws + L.segB2), sa.segM, nullptr, (float*)(ws + L.segdS), BH, L.segs, true, err, st));
+        sa.S0 = (float*)(ws + L.segS);
+        segdS = (float*)(ws + L.segdS);
+    }
+    GD_TRY(states<D>(tq, tk, tv, tv, sa, kGrad, BH, L.segs, err, st));
+    GD_TRY(reverse(false, segdS, nullptr));
     GD_TRY(allow_smem(tc_gd_grads<D>, GradSmem<D>::bytes));
     launch_begin("tc_gd_grads", st);
-    e = launch_pdl(tc_gd_grads<D>, dim3(M, BH), dim3(kThreads), GradSmem<D>::bytes, st, tq, tk, tdo, tdq, tdk,
+    const cudaError_t e = launch_pdl(tc_gd_grads<D>, dim3(M, BH), dim3(kThreads), GradSmem<D>::bytes, st, tq, tk, tdo, tdq, tdk,
                    (const __nv_bfloat16*)a.g, (const float*)recs, (const uint8_t*)X, (const uint8_t*)Y,
                    (const uint8_t*)S, (const uint8_t*)dS, (__nv_bfloat16*)a.dg, (__nv_bfloat16*)a.dbeta, s.N, M, err);
-    e2 = launch_end("tc_gd_grads", st);
+    const cudaError_t e2 = launch_end("tc_gd_grads", st);
     return e != cudaSuccess ? e : e2;
 }
 

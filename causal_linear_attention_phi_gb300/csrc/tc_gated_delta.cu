@@ -177,6 +177,13 @@ struct Tm {
     static_assert(dS + 128 <= 512, "TMEM");
 };
 
+// Element (row, c) of a segment's map: vectors of four along a row, permuted by the row so that the join's reads of
+// eight rows at once meet no bank twice.
+template <int D>
+__device__ __forceinline__ int map_at(int row, int c) {
+    return row * D + ((((c >> 2) ^ ((row >> 1) & 7)) << 2) | (c & 3));
+}
+
 // One block per (segment, head); kSum with D = 128 has a third grid dimension: 0 the sum, 1 the map (with D = 64 the
 // upper lanes, which have no value columns, carry the map).
 template <int D, int kMode>
@@ -522,9 +529,16 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         if (kMode == kOut) output(nloc - 1);
         if (ct == 0) bulk_wait_all();
         if (kMode == kSum) {
-            float* rec = (map || r >= D ? a.segM : a.segB) + ((size_t)bh * a.P + p) * (D * D) + (r & (D - 1));
+            const size_t at = ((size_t)bh * a.P + p) * (D * D);
+            const int c = r & (D - 1);
 #pragma unroll
-            for (int x = 0; x < kSc; ++x) rec[(kSc * h + x) * D] = S[x];
+            for (int x = 0; x < kSc; ++x) {
+                const int d = kSc * h + x;
+                if (map || r >= D)
+                    a.segM[at + map_at<D>(d, c)] = S[x];
+                else
+                    a.segB[at + d * D + c] = S[x];
+            }
         } else if (kMode == kOut && a.S_out && p == a.P - 1 && r < D) {
 #pragma unroll
             for (int x = 0; x < kSc; ++x) a.S_out[((size_t)bh * D + kSc * h + x) * D + r] = S[x];
@@ -541,28 +555,35 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 // ------------------------------------------------------------------ joining the segments
 // Block (slice, head): kJoinCols value columns of the state, carried through the segments' maps in fp32:
 // out[p + 1] = B[p] + M[p] out[p], or in reverse out[p - 1] = B[p] + M[p]^T out[p].  A map (64 KB for D = 128) is copied to
-// shared memory while the previous one is applied; rows are padded by 16 bytes against bank conflicts.
-constexpr int kJoinCols = 16, kJoinThreads = 256;
+// shared memory while the previous one is applied.  A thread forms 2 rows x 4 columns with packed multiply-adds: per
+// four terms 6 vector loads from shared memory to 16 of those.
+constexpr int kJoinCols = 16;
 template <int D>
-struct JoinSmem {
-    static constexpr int pitch = D + 4;  // floats
-    static constexpr int map = D * pitch * 4;
-    static constexpr int S = 2 * map;    // [D][kJoinCols]
+struct JoinCfg {
+    static constexpr int threads = D / 2 * (kJoinCols / 4);
+    static constexpr int map = D * D * 4;
+    static constexpr int S = 2 * map;  // [D][kJoinCols]
     static constexpr int bars = S + D * kJoinCols * 4;
     static constexpr size_t bytes = bars + 32;
 };
 
+// a += m b on two floats at once.
+__device__ __forceinline__ void fma2(float2& a, float m, float2 b) {
+    const float2 mm = make_float2(m, m);
+    asm("fma.rn.f32x2 %0, %1, %2, %0;"
+        : "+l"(reinterpret_cast<uint64_t&>(a))
+        : "l"(reinterpret_cast<const uint64_t&>(mm)), "l"(reinterpret_cast<const uint64_t&>(b)));
+}
+
 template <int D, bool kReverse>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(JoinCfg<D>::threads)
 tc_gd_join(const float* __restrict__ B, const float* __restrict__ Mx, const float* __restrict__ first,
            float* __restrict__ out, int P, int* err) {
-    using L = JoinSmem<D>;
-    constexpr int kThr = kJoinThreads / D;          // threads of a row: 2 (D = 128) or 4
-    constexpr int kCols = kJoinCols / kThr;         // columns of a thread: 8 or 4
-    extern __shared__ __align__(16) uint8_t smem[];
+    using L = JoinCfg<D>;
+    extern __shared__ __align__(128) uint8_t smem[];
     float* S = reinterpret_cast<float*>(smem + L::S);
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::bars);
-    const int tid = threadIdx.x, row = tid / kThr, c0 = tid % kThr * kCols, col = blockIdx.x * kJoinCols + c0;
+    const int tid = threadIdx.x, row = 2 * (tid >> 2), c0 = 4 * (tid & 3), col = blockIdx.x * kJoinCols + c0;
     const size_t bh = blockIdx.y, rec = (size_t)D * D;
     if (tid == 0) {
         mbar_init(bar, 1);
@@ -574,66 +595,67 @@ tc_gd_join(const float* __restrict__ B, const float* __restrict__ Mx, const floa
     // the i-th map applied: segment i, or from the last one back
     auto seg = [&](int i) { return bh * P + (kReverse ? P - 1 - i : i); };
     auto load = [&](int i) {
-        if (tid >= 32) return;
-        if (tid == 0) mbar_arrive_expect_tx(bar + (i & 1), D * D * 4);
-        __syncwarp();
-        for (int r = tid; r < D; r += 32)
-            bulk_load(smem + (i & 1) * L::map + r * L::pitch * 4, Mx + seg(i) * rec + r * D, D * 4, bar + (i & 1));
+        if (tid != 0) return;
+        mbar_arrive_expect_tx(bar + (i & 1), D * D * 4);
+        bulk_load(smem + (i & 1) * L::map, Mx + seg(i) * rec, D * D * 4, bar + (i & 1));
     };
-    float s[kCols];
+    float4 s[2];
 #pragma unroll
-    for (int x = 0; x < kCols; ++x) s[x] = !kReverse && first ? first[bh * rec + row * D + col + x] : 0.f;
+    for (int y = 0; y < 2; ++y)
+        s[y] = !kReverse && first ? ld_f4(first + bh * rec + (row + y) * D + col) : make_float4(0.f, 0.f, 0.f, 0.f);
     load(0);
     bool ok = true;
     for (int i = 0; i < P; ++i) {
-        float* o = out + seg(i) * rec + row * D + col;
+        float2 acc[2][2];
 #pragma unroll
-        for (int x = 0; x < kCols; x += 4) {
-            *reinterpret_cast<float4*>(o + x) = make_float4(s[x], s[x + 1], s[x + 2], s[x + 3]);
-            *reinterpret_cast<float4*>(S + row * kJoinCols + c0 + x) = make_float4(s[x], s[x + 1], s[x + 2], s[x + 3]);
+        for (int y = 0; y < 2; ++y) {
+            const size_t at = seg(i) * rec + (row + y) * D + col;
+            *reinterpret_cast<float4*>(out + at) = s[y];
+            *reinterpret_cast<float4*>(S + (row + y) * kJoinCols + c0) = s[y];
+            if (i < P - 1) {
+                const float4 v = ld_f4(B + at);
+                acc[y][0] = make_float2(v.x, v.y);
+                acc[y][1] = make_float2(v.z, v.w);
+            }
         }
         if (i == P - 1) break;
         if (i + 1 < P - 1) load(i + 1);  // its buffer was last read before the previous barrier
-        const float* b = B + seg(i) * rec + row * D + col;
-        float acc[kCols];
-#pragma unroll
-        for (int x = 0; x < kCols; x += 4) {
-            const float4 v = ld_f4(b + x);
-            acc[x] = v.x;
-            acc[x + 1] = v.y;
-            acc[x + 2] = v.z;
-            acc[x + 3] = v.w;
-        }
         ok = ok && mbar_wait(bar + (i & 1), (i >> 1) & 1, err, LA_ERR_TIMEOUT);
         __syncthreads();
         const float* m = reinterpret_cast<const float*>(smem + (i & 1) * L::map);
 #pragma unroll 4
         for (int k = 0; k < D; k += 4) {
-            float mv[4];
+            float mv[2][4];
             if (kReverse) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mv[e] = m[(k + e) * L::pitch + row];
+                for (int e = 0; e < 4; ++e) {
+                    const float2 v = *reinterpret_cast<const float2*>(m + map_at<D>(k + e, row));
+                    mv[0][e] = v.x;
+                    mv[1][e] = v.y;
+                }
             } else {
-                const float4 v = ld_f4(m + row * L::pitch + k);
-                mv[0] = v.x;
-                mv[1] = v.y;
-                mv[2] = v.z;
-                mv[3] = v.w;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const float4 v = ld_f4(m + map_at<D>(row + y, k));
+                    mv[y][0] = v.x;
+                    mv[y][1] = v.y;
+                    mv[y][2] = v.z;
+                    mv[y][3] = v.w;
+                }
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 4; ++e) {
+                const float4 v = ld_f4(S + (k + e) * kJoinCols + c0);
 #pragma unroll
-                for (int x = 0; x < kCols; x += 4) {
-                    const float4 v = ld_f4(S + (k + e) * kJoinCols + c0 + x);
-                    acc[x] = fmaf(mv[e], v.x, acc[x]);
-                    acc[x + 1] = fmaf(mv[e], v.y, acc[x + 1]);
-                    acc[x + 2] = fmaf(mv[e], v.z, acc[x + 2]);
-                    acc[x + 3] = fmaf(mv[e], v.w, acc[x + 3]);
+                for (int y = 0; y < 2; ++y) {
+                    fma2(acc[y][0], mv[y][e], make_float2(v.x, v.y));
+                    fma2(acc[y][1], mv[y][e], make_float2(v.z, v.w));
                 }
+            }
         }
         __syncthreads();  // S and the map have been read
 #pragma unroll
-        for (int x = 0; x < kCols; ++x) s[x] = acc[x];
+        for (int y = 0; y < 2; ++y) s[y] = make_float4(acc[y][0].x, acc[y][0].y, acc[y][1].x, acc[y][1].y);
     }
 }
 
@@ -677,11 +699,11 @@ template <int D>
 cudaError_t join(const float* B, const float* Mx, const float* first, float* out, int BH, int P, bool reverse, int* err,
                  cudaStream_t st) {
     auto kern = reverse ? tc_gd_join<D, true> : tc_gd_join<D, false>;
-    GD_TRY(allow_smem(kern, JoinSmem<D>::bytes));
+    GD_TRY(allow_smem(kern, JoinCfg<D>::bytes));
     const char* name = reverse ? "tc_gd_join_reverse" : "tc_gd_join";
     launch_begin(name, st);
     const cudaError_t e =
-        launch_pdl(kern, dim3(D / kJoinCols, BH), dim3(kJoinThreads), JoinSmem<D>::bytes, st, B, Mx, first, out, P, err);
+        launch_pdl(kern, dim3(D / kJoinCols, BH), dim3(JoinCfg<D>::threads), JoinCfg<D>::bytes, st, B, Mx, first, out, P, err);
     const cudaError_t e2 = launch_end(name, st);
     return e != cudaSuccess ? e : e2;
 }

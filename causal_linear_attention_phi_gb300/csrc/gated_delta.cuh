@@ -102,23 +102,24 @@ __device__ __forceinline__ void gate_record(const T* __restrict__ g, const T* __
 }
 
 // t = -A (I + beta A)^-1 for a strictly lower triangular A (zero on and above the diagonal), 64 x 64 fp32 in
-// shared memory with row pitch kLd, by 256 threads.  Two diagonal blocks of 32 by forward substitution,
-// t_i = -(A_i + sum_(j<i) A_ij beta_j t_j), one column to a lane of one warp each, the column in registers; then
-// the block below them, t21 = -(I + t22 beta) A21 (I + beta t11), as two 32 x 32 x 32 products.  Every thread calls it; A (overwritten) is complete
-// before, t after.
+// shared memory with row pitch kLd, by 256 threads.  Four diagonal blocks of 16 by forward substitution,
+// t_i = -(A_i + sum_(j<i) A_ij beta_j t_j), one column to a lane, the column in registers; then blocks are joined in
+// pairs, first to 32 and then to 64: t21 = -(I + t22 beta) A21 (I + beta t11), two small products each.  (Diagonal
+// blocks of 32 left six of eight warps waiting for a chain of 31 rows.)  Every thread calls it; A (overwritten) is
+// complete before, t after.
 constexpr int kLd = kC + 4;
 
 __device__ __forceinline__ float4 ld_f4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 __device__ __forceinline__ void solve_t(float* A, float* t, const float* beta, int tid) {
-    constexpr int kH = kC / 2;
-    if (tid < 64) {
-        const int b0 = tid & 32, c = tid & 31;
-        float y[kH];  // beta_j t_j of this column
+    constexpr int kH = kC / 2, kQ = kC / 4;
+    if (tid < kC) {
+        const int b0 = tid & 48, c = tid & 15;
+        float y[kQ];  // beta_j t_j of this column
         t[b0 * kLd + b0 + c] = 0.f;
         y[0] = 0.f;
 #pragma unroll
-        for (int r = 1; r < kH; ++r) {
+        for (int r = 1; r < kQ; ++r) {
             const float* a = A + (b0 + r) * kLd + b0;
             float s0 = a[c], s1 = 0.f;
 #pragma unroll
@@ -133,8 +134,45 @@ __device__ __forceinline__ void solve_t(float* A, float* t, const float* beta, i
             t[(b0 + r) * kLd + b0 + c] = x;
             y[r] = beta[b0 + r] * x;
         }
-    } else {
-        for (int i = tid - 64; i < kH * kH; i += 192) t[(i >> 5) * kLd + kH + (i & 31)] = 0.f;
+    } else {  // what lies above the diagonal blocks
+        for (int i = tid - kC; i < kC * 12; i += 192) {
+            const int r = i / 12, v = i % 12;  // vectors of four columns past this row's diagonal block
+            const int c = 4 * v + 16;
+            if (c >= (r & 48) + 16) *reinterpret_cast<float4*>(t + r * kLd + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    __syncthreads();
+    {  // pair p: rows 32 p + 16 + r, columns 32 p + c, c + 1
+        const int b = kH * (tid >> 7), r = (tid >> 3) & 15, c = 2 * (tid & 7);
+        float* row = A + (b + kQ + r) * kLd + b;
+        float2 z = *reinterpret_cast<const float2*>(row + c);
+#pragma unroll
+        for (int k = 0; k < kQ; k += 4) {
+            const float4 a = ld_f4(row + k), be = ld_f4(beta + b + k);
+            const float av[4] = {a.x * be.x, a.y * be.y, a.z * be.z, a.w * be.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 v = *reinterpret_cast<const float2*>(t + (b + k + e) * kLd + b + c);
+                z.x = fmaf(av[e], v.x, z.x);
+                z.y = fmaf(av[e], v.y, z.y);
+            }
+        }
+        __syncthreads();
+        *reinterpret_cast<float2*>(row + c) = z;
+        __syncthreads();
+        const float* tr = t + (b + kQ + r) * kLd + b + kQ;
+#pragma unroll
+        for (int k = 0; k < kQ; k += 4) {
+            const float4 a = ld_f4(tr + k), be = ld_f4(beta + b + kQ + k);
+            const float av[4] = {a.x * be.x, a.y * be.y, a.z * be.z, a.w * be.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 v = *reinterpret_cast<const float2*>(A + (b + kQ + k + e) * kLd + b + c);
+                z.x = fmaf(av[e], v.x, z.x);
+                z.y = fmaf(av[e], v.y, z.y);
+            }
+        }
+        *reinterpret_cast<float2*>(t + (b + kQ + r) * kLd + b + c) = make_float2(-z.x, -z.y);
     }
     __syncthreads();
     // this thread: row kH + r, columns c .. c + 3 of the lower left block
@@ -143,8 +181,8 @@ __device__ __forceinline__ void solve_t(float* A, float* t, const float* beta, i
     float4 z = ld_f4(row + c);
 #pragma unroll
     for (int k = 0; k < kH; k += 4) {
-        const float4 a = ld_f4(row + k);
-        const float av[4] = {a.x * beta[k], a.y * beta[k + 1], a.z * beta[k + 2], a.w * beta[k + 3]};
+        const float4 a = ld_f4(row + k), be = ld_f4(beta + k);
+        const float av[4] = {a.x * be.x, a.y * be.y, a.z * be.z, a.w * be.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float4 b = ld_f4(t + (k + e) * kLd + c);
@@ -160,9 +198,8 @@ __device__ __forceinline__ void solve_t(float* A, float* t, const float* beta, i
     const float* tr = t + (kH + r) * kLd + kH;
 #pragma unroll
     for (int k = 0; k < kH; k += 4) {
-        const float4 a = ld_f4(tr + k);
-        const float av[4] = {a.x * beta[kH + k], a.y * beta[kH + k + 1], a.z * beta[kH + k + 2],
-                             a.w * beta[kH + k + 3]};
+        const float4 a = ld_f4(tr + k), be = ld_f4(beta + kH + k);
+        const float av[4] = {a.x * be.x, a.y * be.y, a.z * be.z, a.w * be.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float4 b = ld_f4(A + (kH + k + e) * kLd + c);

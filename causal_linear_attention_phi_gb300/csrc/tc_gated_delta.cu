@@ -31,14 +31,16 @@ using namespace tcgd;
 // ------------------------------------------------------------------ t and P of every chunk
 constexpr int kPrepThreads = 256;
 struct PrepSmem {
-    // offset 0: blocks of [Q rows 0-63; K rows 64-127] x 64 columns, then (once the product has read them) fp32 A
+    // offset 0: blocks of [Q rows 0-63; K rows 64-127] x 64 columns, then (once the product has read them) fp32 A, and
+    // last t's tiles over A
     static constexpr int A = 0;
-    static constexpr int T = A + kC * kLd * 4;
-    static constexpr int rec = T + kC * kLd * 4;  // beyond the tiles (32768 bytes)
+    static constexpr int T = 18432;  // A's bytes rounded up to a tile's alignment
+    static constexpr int P = T + 18432;  // P's tiles
+    static constexpr int rec = P + 2 * kBlk;
     static constexpr int bar = rec + kRec * 4;
     static constexpr int total = bar + 32;
 };
-static_assert(PrepSmem::rec >= 4 * kBlk, "the gate record lies beyond the tiles");
+static_assert(PrepSmem::T >= kC * kLd * 4 && PrepSmem::T >= 2 * kBlk && PrepSmem::P >= 4 * kBlk, "regions");
 constexpr size_t kPrepBytes = PrepSmem::total + 1024;
 
 template <int D>
@@ -86,7 +88,6 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     tc_fence_after();
     float* A = reinterpret_cast<float*>(base + PrepSmem::A);
     float* T = reinterpret_cast<float*>(base + PrepSmem::T);
-    uint8_t* mat = mats + at * (size_t)kMats;
     {
         // lanes 0-63 hold Q K^T, 64-127 K K^T; this thread row i, positions 32 h .. +31
         const int quarter = warp & 3, h = warp >> 2, i = 32 * (quarter & 1) + lane, j0 = 32 * h;
@@ -95,12 +96,23 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         tmem_ld_wait();
         const float seg = rec[kSeg + i], hi = rec[kGhi + i], lo = rec[kGlo + i];
         const bool isP = quarter < 2;
+        if (h > (quarter & 1)) {  // above the diagonal
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
-            const int j = j0 + x;
-            const bool in = (isP ? j <= i : j < i) && rec[kSeg + j] == seg;
-            const float d = (hi - rec[kGhi + j]) + (lo - rec[kGlo + j]);
-            w[x] = in ? __float_as_uint(__uint_as_float(w[x]) * ex2_approx(d * 1.4426950408889634f)) : 0u;
+            for (int x = 0; x < 32; ++x) w[x] = 0u;
+        } else {
+#pragma unroll
+            for (int x = 0; x < 32; x += 4) {
+                const float4 gh = ld_f4(rec + kGhi + j0 + x), gl = ld_f4(rec + kGlo + j0 + x), sg = ld_f4(rec + kSeg + j0 + x);
+                const float ghv[4] = {gh.x, gh.y, gh.z, gh.w}, glv[4] = {gl.x, gl.y, gl.z, gl.w},
+                            sgv[4] = {sg.x, sg.y, sg.z, sg.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = j0 + x + e;
+                    const bool in = (isP ? j <= i : j < i) && sgv[e] == seg;
+                    const float d = (hi - ghv[e]) + (lo - glv[e]);
+                    w[x + e] = in ? __float_as_uint(__uint_as_float(w[x + e]) * ex2_approx(d * 1.4426950408889634f)) : 0u;
+                }
+            }
         }
         if (isP) {
 #pragma unroll
@@ -111,8 +123,8 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 split2(__uint_as_float(w[8 * c + 4]), __uint_as_float(w[8 * c + 5]), a.z, b.z);
                 split2(__uint_as_float(w[8 * c + 6]), __uint_as_float(w[8 * c + 7]), a.w, b.w);
                 const int off = elem_off(i, j0 + 8 * c);
-                *reinterpret_cast<uint4*>(mat + kPHi + off) = a;
-                *reinterpret_cast<uint4*>(mat + kPLo + off) = b;
+                *reinterpret_cast<uint4*>(base + PrepSmem::P + off) = a;
+                *reinterpret_cast<uint4*>(base + PrepSmem::P + kBlk + off) = b;
             }
         } else {
 #pragma unroll
@@ -126,18 +138,27 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         const int i = tid >> 2, j0 = 16 * (tid & 3);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const float* s = T + i * kLd + j0 + 8 * c;
+            const float4 s = ld_f4(T + i * kLd + j0 + 8 * c), u = ld_f4(T + i * kLd + j0 + 8 * c + 4);
             uint4 a, b;
-            split2(s[0], s[1], a.x, b.x);
-            split2(s[2], s[3], a.y, b.y);
-            split2(s[4], s[5], a.z, b.z);
-            split2(s[6], s[7], a.w, b.w);
+            split2(s.x, s.y, a.x, b.x);
+            split2(s.z, s.w, a.y, b.y);
+            split2(u.x, u.y, a.z, b.z);
+            split2(u.z, u.w, a.w, b.w);
             const int off = elem_off(i, j0 + 8 * c);
-            *reinterpret_cast<uint4*>(mat + kTHi + off) = a;
-            *reinterpret_cast<uint4*>(mat + kTLo + off) = b;
+            *reinterpret_cast<uint4*>(base + off) = a;
+            *reinterpret_cast<uint4*>(base + kBlk + off) = b;
         }
     }
-    for (int i = tid; i < kRec; i += kPrepThreads) recs[at * kRec + i] = rec[i];
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+        uint8_t* mat = mats + at * (size_t)kMats;
+        bulk_store(mat + kTHi, base, 2 * kBlk);
+        bulk_store(mat + kPHi, base + PrepSmem::P, 2 * kBlk);
+        bulk_store(recs + at * kRec, rec, kRec * 4);
+        bulk_commit();
+        bulk_wait_all();
+    }
     if (!ok && tid == 0) mbar_wait(bar, 0, err, LA_ERR_TIMEOUT);  // never leave with copies in flight
     tc_fence_before();
     __syncthreads();

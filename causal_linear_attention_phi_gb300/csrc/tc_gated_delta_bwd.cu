@@ -9,7 +9,7 @@
 // for tc_gd_grads, the tiles of Y^T [Dv rows x 64 positions], lo and hi, and of dS'^T [Dv rows x Dk], rounded to bf16
 // once like S (a relative error of 2^-9 of each term of the products with the states, none of which cancel by much).
 //
-// tc_gd_grads (one block per chunk): with G = Y X^T, F^T = X dO^T, all products with 128 rows,
+// tc_gd_grads (persistent blocks, a chunk at a time): with G = Y X^T, F^T = X dO^T, all products with 128 rows,
 //   F_ij = (dO_i . X_j) beta_j Gam_ij (i >= j),  E_ij = -beta_i beta_j Gam_ij G_ij (i > j),  dbeta_i = G_ii
 //   dQ^T = gam S dO^T + K^T F^T              dK^T = -beta gam S Y^T + tail beta dS' X^T + Q^T F + K^T (E + E^T)^T
 // F and E enter as hi + lo parts: dg is a difference of sums over them.  Lanes 0-63 hold E's rows, 64-127 F^T's.
@@ -362,17 +362,23 @@ struct GradSmem {
     static constexpr int QK = dS + D * D * 2;  // blocks of [Q rows; K rows] x 64 columns
     static constexpr int dO = QK + 2 * (D / 64) * kBlk;
     static constexpr int FHi = dO + (D / 64) * kBlk, FLo = FHi + kBlk, EHi = FLo + kBlk, ELo = EHi + kBlk;
-    static constexpr int out = XLo;  // dq and dk tiles, once the products have read X and Y
-    static_assert(2 * (D / 64) * kBlk <= 4 * TS, "output tiles");
+    static constexpr int out = FHi;  // dq and dk tiles, once the products have read F and E
+    static_assert(2 * (D / 64) * kBlk <= 4 * kBlk, "output tiles");
     static constexpr int rec = ELo + kBlk;
     static constexpr int part = rec + kRec * 4;  // fp32 partial sums, below
     static constexpr int pRow = 0, pCol = pRow + 4 * 128, pTok = pCol + 4 * kC, pSum = pTok + 4 * kC,
                          dBeta = pSum + 2 * kWarps, pEnd = dBeta + kC;
     static constexpr int bars = part + pEnd * 4;
-    static constexpr int slot = bars + 64;
+    static constexpr int slot = bars + 128;
     static constexpr int total = slot + 16;
     static constexpr size_t bytes = total + 1024;
     static_assert(bytes <= 232448, "shared memory");
+};
+struct __align__(8) GBars {
+    uint64_t a_full, b_full;    // X, Y, S, dS', dO; Q, K and the gates
+    uint64_t a_free, b_free;
+    uint64_t pairs_done, pairs_ready, out_done, acc_free;
+    uint64_t final_mma;
 };
 struct GTm {
     static constexpr uint32_t q1 = 0, k1 = 64, k3 = 128;          // S dO^T; S Y^T; dS' X^T as two halves
@@ -402,44 +408,68 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const __grid_constant__ CUtensorMap tm_dk, const __nv_bfloat16* __restrict__ g,
             const float* __restrict__ recs, const uint8_t* __restrict__ x_tiles, const uint8_t* __restrict__ y_tiles,
             const uint8_t* __restrict__ s_tiles, const uint8_t* __restrict__ ds_tiles, __nv_bfloat16* __restrict__ dg,
-            __nv_bfloat16* __restrict__ dbeta, int N, int M, int* err) {
+            __nv_bfloat16* __restrict__ dbeta, int N, int M, int total, int* err) {
     using L = GradSmem<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* bar = reinterpret_cast<uint64_t*>(base + L::bars);  // loads, first products, pairs ready, second products
+    GBars* bar = reinterpret_cast<GBars*>(base + L::bars);
     uint32_t* slot = reinterpret_cast<uint32_t*>(base + L::slot);
     float* rec = reinterpret_cast<float*>(base + L::rec);
     float* part = reinterpret_cast<float*>(base + L::part);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, m = blockIdx.x, bh = blockIdx.y;
-    const size_t at = (size_t)bh * M + m;
-    const int c0 = m * kC, n = min(kC, N - c0);
-    LA_DCHECK(n >= 1 && m < M);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int nloc = (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // chunks of this block
+    LA_DCHECK(nloc >= 1);
     if (tid == 0) {
-        mbar_init(bar, 1);
-        mbar_init(bar + 1, 1);
-        mbar_init(bar + 2, kWarps);
-        mbar_init(bar + 3, 1);
-        mbar_init(bar + 4, 1);
+        mbar_init(&bar->a_full, 1);
+        mbar_init(&bar->b_full, 1);
+        mbar_init(&bar->a_free, 1 + kWarps);
+        mbar_init(&bar->b_free, kWarps);
+        mbar_init(&bar->pairs_done, 1);
+        mbar_init(&bar->pairs_ready, kWarps);
+        mbar_init(&bar->out_done, 1);
+        mbar_init(&bar->acc_free, kWarps);
+        mbar_init(&bar->final_mma, 1);
         fence_mbar_init();
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_do);
+        tma_prefetch_desc(&tm_dq);
+        tma_prefetch_desc(&tm_dk);
     }
     const uint32_t tmem = enter(slot, 512, warp);
     if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
-            mbar_arrive_expect_tx(bar, 2 * D * D * 2 + 4 * L::TS + 3 * (D / 64) * kBlk + kRec * 4);
+            int a_armed = -1, b_armed = -1;
+            for (int i = 0; i < nloc; ++i) {
+                const size_t at = (size_t)blockIdx.x + (size_t)gridDim.x * i;
+                const int bh = (int)(at / M), c0 = (int)(at % M) * kC;
+                if (!mbar_wait(&bar->a_free, (i & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
+                mbar_arrive_expect_tx(&bar->a_full, 2 * D * D * 2 + 4 * L::TS + (D / 64) * kBlk);
+                bulk_load(base + L::XLo, x_tiles + at * (2 * L::TS), 2 * L::TS, &bar->a_full);
+                bulk_load(base + L::YLo, y_tiles + at * (2 * L::TS), 2 * L::TS, &bar->a_full);
 #pragma unroll
-            for (int b = 0; b < D / 64; ++b) {
-                tma_load_3d(base + L::QK + 2 * b * kBlk, &tm_q, 64 * b, c0, bh, bar);
-                tma_load_3d(base + L::QK + (2 * b + 1) * kBlk, &tm_k, 64 * b, c0, bh, bar);
-                tma_load_3d(base + L::dO + b * kBlk, &tm_do, 64 * b, c0, bh, bar);
+                for (int b = 0; b < D / 64; ++b)
+                    tma_load_3d(base + L::dO + b * kBlk, &tm_do, 64 * b, c0, bh, &bar->a_full);
+                bulk_load(base + L::S, s_tiles + at * (D * D * 2), D * D * 2, &bar->a_full);
+                bulk_load(base + L::dS, ds_tiles + at * (D * D * 2), D * D * 2, &bar->a_full);
+                a_armed = i;
+                if (!mbar_wait(&bar->b_free, (i & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
+                mbar_arrive_expect_tx(&bar->b_full, 2 * (D / 64) * kBlk + kRec * 4);
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b) {
+                    tma_load_3d(base + L::QK + 2 * b * kBlk, &tm_q, 64 * b, c0, bh, &bar->b_full);
+                    tma_load_3d(base + L::QK + (2 * b + 1) * kBlk, &tm_k, 64 * b, c0, bh, &bar->b_full);
+                }
+                bulk_load(rec, recs + at * kRec, kRec * 4, &bar->b_full);
+                b_armed = i;
             }
-            bulk_load(base + L::XLo, x_tiles + at * (2 * L::TS), 2 * L::TS, bar);
-            bulk_load(base + L::YLo, y_tiles + at * (2 * L::TS), 2 * L::TS, bar);
-            bulk_load(base + L::S, s_tiles + at * (D * D * 2), D * D * 2, bar);
-            bulk_load(base + L::dS, ds_tiles + at * (D * D * 2), D * D * 2, bar);
-            bulk_load(rec, recs + at * kRec, kRec * 4, bar);
-            mbar_wait(bar, 0, err, LA_ERR_TIMEOUT);  // never leave with copies in flight
+            // never leave with copies in flight
+            if (a_armed >= 0) mbar_wait(&bar->a_full, a_armed & 1, err, LA_ERR_TIMEOUT);
+            if (b_armed >= 0) mbar_wait(&bar->b_full, b_armed & 1, err, LA_ERR_TIMEOUT);
         }
     } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
         const uint32_t lead = elect_one();
         bool ok = true;
         auto wait = [&](uint64_t* b, int parity) {
@@ -455,60 +485,69 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const uint32_t dQ = tile_desc(b0 + L::QK), dK = tile_desc(b0 + L::QK + kBlk), dO = tile_desc(b0 + L::dO);
         // MN-major left operands: blocks of 64 rows (of M) one tile apart
         const uint32_t aBelow = tile_desc<TS>(b0 + L::XLo - TS), aLo = tile_desc<TS>(b0 + L::XLo),
-                       aY = tile_desc<TS>(b0 + L::Y), aS = tile_desc<TS>(b0 + L::S), adS = tile_desc<TS>(b0 + L::dS);
-        wait(bar, 0);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)  // lanes 64-127: X dO^T
-            mma_ss1(lead, tmem + GTm::FT, aBelow + step_mn(k), dO + step_k(k), id_mk, k > 0);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-            mma_ss1(lead, tmem + GTm::FT, aLo + step_mn(k), dO + step_k(k), id_mk, 1);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)  // lanes 0-63: Y X^T
-            mma_ss1(lead, tmem + GTm::G, aY + step_mn(k), tile_desc<TS>(b0 + L::XHi) + step_mn(k), id_mm, k > 0);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-            mma_ss1(lead, tmem + GTm::G, aY + step_mn(k), aLo + step_mn(k), id_mm, 1);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-            mma_ss1(lead, tmem + GTm::G, tile_desc<TS>(b0 + L::YLo) + step_mn(k),
-                    tile_desc<TS>(b0 + L::XHi) + step_mn(k), id_mm, 1);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)  // lanes 64-127: K Q^T
-            mma_ss1(lead, tmem + GTm::qk, dQ + step_k(k, 2 * kBlk), dQ + step_k(k, 2 * kBlk), id_kk, k > 0);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)  // lanes 0-63: K K^T
-            mma_ss1(lead, tmem + GTm::kk, dK + step_k(k, 2 * kBlk), dK + step_k(k, 2 * kBlk), id_kk, k > 0);
-        commit1(lead, bar + 1);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)  // S dO^T
-            mma_ss1(lead, tmem + GTm::q1, aS + step_mn(k), dO + step_k(k), id_mk, k > 0);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)  // S Y^T
-            mma_ss1(lead, tmem + GTm::k1, aS + step_mn(k), aY + step_mn(k), id_mm, k > 0);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)  // dS' [X_lo | X_hi]^T
-            mma_ss1(lead, tmem + GTm::k3, adS + step_mn(k), aLo + step_mn(k), id_mm2, k > 0);
-        wait(bar + 2, 0);  // F and E are in their tiles, their products have been read
+                       aHi = tile_desc<TS>(b0 + L::XHi), aYLo = tile_desc<TS>(b0 + L::YLo), aY = tile_desc<TS>(b0 + L::Y),
+                       aS = tile_desc<TS>(b0 + L::S), adS = tile_desc<TS>(b0 + L::dS);
         const uint32_t mQ = tile_desc<2 * kBlk>(b0 + L::QK), mK = tile_desc<2 * kBlk>(b0 + L::QK + kBlk);
         const uint32_t fMn = tile_desc<kBlk>(b0 + L::FHi), eMn = tile_desc<kBlk>(b0 + L::EHi);
         const uint32_t fK = tile_desc(b0 + L::FHi), eK = tile_desc(b0 + L::EHi);
+        for (int i = 0; i < nloc; ++i) {
+            const int ph = i & 1;
+            wait(&bar->a_full, ph);
+            if (i > 0) wait(&bar->acc_free, ph ^ 1);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)  // K^T F^T, with [F_hi | F_lo]
-            mma_ss1(lead, tmem + GTm::q2, mK + step_mn(k), fMn + step_mn(k), id_mm2, k > 0);
+            for (int k = 0; k < kSteps; ++k)  // lanes 64-127: X dO^T
+                mma_ss1(lead, tmem + GTm::FT, aBelow + step_mn(k), dO + step_k(k), id_mk, k > 0);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)  // Q^T F
-            mma_ss1(lead, tmem + GTm::k2, mQ + step_mn(k), fK + step_k(k), id_mk2, k > 0);
+            for (int k = 0; k < kSteps; ++k)
+                mma_ss1(lead, tmem + GTm::FT, aLo + step_mn(k), dO + step_k(k), id_mk, 1);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)  // K^T E^T
-            mma_ss1(lead, tmem + GTm::k2, mK + step_mn(k), eK + step_k(k), id_mk2, 1);
+            for (int k = 0; k < kSteps; ++k)  // lanes 0-63: Y X^T
+                mma_ss1(lead, tmem + GTm::G, aY + step_mn(k), aHi + step_mn(k), id_mm, k > 0);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)  // K^T E
-            mma_ss1(lead, tmem + GTm::k2, mK + step_mn(k), eMn + step_mn(k), id_mm2, 1);
-        commit1(lead, bar + 3);
-        mbar_wait(bar + 3, 0, err, LA_ERR_TIMEOUT);
+            for (int k = 0; k < kSteps; ++k)
+                mma_ss1(lead, tmem + GTm::G, aY + step_mn(k), aLo + step_mn(k), id_mm, 1);
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
+                mma_ss1(lead, tmem + GTm::G, aYLo + step_mn(k), aHi + step_mn(k), id_mm, 1);
+            wait(&bar->b_full, ph);
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)  // lanes 64-127: K Q^T
+                mma_ss1(lead, tmem + GTm::qk, dQ + step_k(k, 2 * kBlk), dQ + step_k(k, 2 * kBlk), id_kk, k > 0);
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)  // lanes 0-63: K K^T
+                mma_ss1(lead, tmem + GTm::kk, dK + step_k(k, 2 * kBlk), dK + step_k(k, 2 * kBlk), id_kk, k > 0);
+            commit1(lead, &bar->pairs_done);
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)  // S dO^T
+                mma_ss1(lead, tmem + GTm::q1, aS + step_mn(k), dO + step_k(k), id_mk, k > 0);
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)  // S Y^T
+                mma_ss1(lead, tmem + GTm::k1, aS + step_mn(k), aY + step_mn(k), id_mm, k > 0);
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)  // dS' [X_lo | X_hi]^T
+                mma_ss1(lead, tmem + GTm::k3, adS + step_mn(k), aLo + step_mn(k), id_mm2, k > 0);
+            commit1(lead, &bar->a_free);
+            wait(&bar->pairs_ready, ph);  // F and E are in their tiles, their products have been read
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // K^T F^T, with [F_hi | F_lo]
+                mma_ss1(lead, tmem + GTm::q2, mK + step_mn(k), fMn + step_mn(k), id_mm2, k > 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // Q^T F
+                mma_ss1(lead, tmem + GTm::k2, mQ + step_mn(k), fK + step_k(k), id_mk2, k > 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // K^T E^T
+                mma_ss1(lead, tmem + GTm::k2, mK + step_mn(k), eK + step_k(k), id_mk2, 1);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // K^T E
+                mma_ss1(lead, tmem + GTm::k2, mK + step_mn(k), eMn + step_mn(k), id_mm2, 1);
+            commit1(lead, &bar->out_done);
+        }
+        // drain: every MMA issued has completed before TMEM is released
+        commit1(lead, &bar->final_mma);
+        mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
         __syncwarp();
     } else {
+        // ------------------------------------------------------------ compute warps
         const int ct = tid - 64, h = ct >> 7, r = 32 * (warp & 3) + lane, q4 = warp & 3;
         const uint32_t lb = tmem + ((uint32_t)(32 * q4) << 16);
         bool ok = true;
@@ -517,106 +556,144 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             __syncwarp();
             tc_fence_after();
         };
-        wait(bar, 0);
-        float kept = 0.f;  // <dS', S>
-        for (int x = ct; x < D * D / 8; x += 32 * kWarps) {
-            const uint4 a = *reinterpret_cast<const uint4*>(base + L::S + 16 * x);
-            const uint4 b = *reinterpret_cast<const uint4*>(base + L::dS + 16 * x);
-            kept = fmaf(bf_lo(a.x), bf_lo(b.x), fmaf(bf_hi(a.x), bf_hi(b.x), kept));
-            kept = fmaf(bf_lo(a.y), bf_lo(b.y), fmaf(bf_hi(a.y), bf_hi(b.y), kept));
-            kept = fmaf(bf_lo(a.z), bf_lo(b.z), fmaf(bf_hi(a.z), bf_hi(b.z), kept));
-            kept = fmaf(bf_lo(a.w), bf_lo(b.w), fmaf(bf_hi(a.w), bf_hi(b.w), kept));
-        }
-        wait(bar + 1, 0);
-        {  // F^T (row j, columns i) or E (row i, columns j): this thread's 16 columns
-            const bool isF = r >= kC;
-            const int row = r & (kC - 1), col0 = 16 * h;
-            uint32_t v[16], pq[16];
-            ld(lb + (isF ? GTm::FT : GTm::G) + col0, v);
-            ld(lb + (isF ? GTm::qk : GTm::kk) + col0, pq);
-            tmem_ld_wait();
-            const float seg = rec[kSeg + row], hi = rec[kGhi + row], lo = rec[kGlo + row], br = rec[kBeta + row];
-            float pr[16], rsum = 0.f;
-            uint4 ph[2], pl[2];
-            uint32_t* eh = reinterpret_cast<uint32_t*>(ph);
-            uint32_t* el = reinterpret_cast<uint32_t*>(pl);
+        auto arrive = [&](uint64_t* b) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b);
+        };
+        const bool isF = r >= kC;
+        const int row = r & (kC - 1), col0 = 16 * h;
+        for (int i = 0; i < nloc; ++i) {
+            const int ph = i & 1;
+            const size_t at = (size_t)blockIdx.x + (size_t)gridDim.x * i;
+            const int bh = (int)(at / M), c0 = (int)(at % M) * kC, n = min(kC, N - c0);
+            wait(&bar->a_full, ph);
+            float kept = 0.f;  // <dS', S>
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                const int col = col0 + x;
-                const float raw = __uint_as_float(v[x]);
-                if (!isF && col == row) part[L::dBeta + row] = raw;
-                float d = (hi - rec[kGhi + col]) + (lo - rec[kGlo + col]);  // G_row - G_col
-                if (isF) d = -d;
-                const bool in = (isF ? col >= row : col < row) && rec[kSeg + col] == seg;
-                const float s = isF ? br : -br * rec[kBeta + col];
-                const float val = in ? raw * (s * ex2_approx(d * 1.4426950408889634f)) : 0.f;
-                v[x] = __float_as_uint(val);
-                pr[x] = col != row ? val * __uint_as_float(pq[x]) : 0.f;
-                pr[x] = in ? pr[x] : 0.f;
-                rsum += pr[x];
+            for (int x = 0; x < D * D / 8 / (32 * kWarps); ++x) {
+                const int o = 16 * (ct + 32 * kWarps * x);
+                const uint4 a = *reinterpret_cast<const uint4*>(base + L::S + o);
+                const uint4 b = *reinterpret_cast<const uint4*>(base + L::dS + o);
+                kept = fmaf(bf_lo(a.x), bf_lo(b.x), fmaf(bf_hi(a.x), bf_hi(b.x), kept));
+                kept = fmaf(bf_lo(a.y), bf_lo(b.y), fmaf(bf_hi(a.y), bf_hi(b.y), kept));
+                kept = fmaf(bf_lo(a.z), bf_lo(b.z), fmaf(bf_hi(a.z), bf_hi(b.z), kept));
+                kept = fmaf(bf_lo(a.w), bf_lo(b.w), fmaf(bf_hi(a.w), bf_hi(b.w), kept));
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar->a_free);
+            // the F and E tiles are free once the previous chunk's stores have read dq and dk out of them, the
+            // partial sums once its dg is formed
+            if (ct == 0) bulk_wait_read_all();
+            named_barrier(1, 32 * kWarps);
+            wait(&bar->b_full, ph);
+            wait(&bar->pairs_done, ph);
+            // F^T (row j, columns i >= j) or E (row i, columns j < i): this thread's 16 columns; none in a block
+            // on the other side of the diagonal
+            float pr[16], rsum = 0.f;
+            uint4 phi[2], plo[2];
+            uint32_t* eh = reinterpret_cast<uint32_t*>(phi);
+            uint32_t* el = reinterpret_cast<uint32_t*>(plo);
+            const int row0 = 32 * (q4 & 1);  // the warp's rows are row0 .. +31
+            if (isF ? col0 + 15 >= row0 : col0 <= row0 + 31) {
+                uint32_t v[16], pq[16];
+                ld(lb + (isF ? GTm::FT : GTm::G) + col0, v);
+                ld(lb + (isF ? GTm::qk : GTm::kk) + col0, pq);
+                tmem_ld_wait();
+                const float seg = rec[kSeg + row], hi = rec[kGhi + row], lo = rec[kGlo + row], br = rec[kBeta + row];
+                const float sgn = isF ? -1.4426950408889634f : 1.4426950408889634f;
 #pragma unroll
-            for (int x = 0; x < 16; x += 2)
-                split2(__uint_as_float(v[x]), __uint_as_float(v[x + 1]), eh[x / 2], el[x / 2]);
+                for (int x0 = 0; x0 < 16; x0 += 4) {
+                    const float4 gh = ld_f4(rec + kGhi + col0 + x0), gl = ld_f4(rec + kGlo + col0 + x0),
+                                 sg = ld_f4(rec + kSeg + col0 + x0), be = ld_f4(rec + kBeta + col0 + x0);
+                    const float ghv[4] = {gh.x, gh.y, gh.z, gh.w}, glv[4] = {gl.x, gl.y, gl.z, gl.w},
+                                sgv[4] = {sg.x, sg.y, sg.z, sg.w}, bev[4] = {be.x, be.y, be.z, be.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int x = x0 + e, col = col0 + x;
+                        const float raw = __uint_as_float(v[x]);
+                        if (!isF && col == row) part[L::dBeta + row] = raw;
+                        const float d = (hi - ghv[e]) + (lo - glv[e]);  // G_row - G_col
+                        const bool in = (isF ? col >= row : col < row) && sgv[e] == seg;
+                        const float s = isF ? br : -br * bev[e];
+                        const float val = in ? raw * (s * ex2_approx(d * sgn)) : 0.f;
+                        v[x] = __float_as_uint(val);
+                        pr[x] = in && col != row ? val * __uint_as_float(pq[x]) : 0.f;
+                        rsum += pr[x];
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < 16; x += 2)
+                    split2(__uint_as_float(v[x]), __uint_as_float(v[x + 1]), eh[x / 2], el[x / 2]);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 16; ++x) pr[x] = 0.f;
+                phi[0] = phi[1] = plo[0] = plo[1] = make_uint4(0u, 0u, 0u, 0u);
+            }
             uint8_t* tile = base + (isF ? L::FHi : L::EHi);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int off = row_off(row, (col0 >> 3) + x);
-                *reinterpret_cast<uint4*>(tile + off) = ph[x];
-                *reinterpret_cast<uint4*>(tile + kBlk + off) = pl[x];
+                *reinterpret_cast<uint4*>(tile + off) = phi[x];
+                *reinterpret_cast<uint4*>(tile + kBlk + off) = plo[x];
             }
             fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar + 2);
+            arrive(&bar->pairs_ready);
             // shares of dG: a row of E adds to its position, its columns are taken off theirs; F^T the other way round
             part[L::pRow + h * 128 + r] = isF ? -rsum : rsum;
             const float cs = reduce16(pr, lane);
             if ((lane & 1) == 0) part[L::pCol + q4 * kC + col0 + (lane >> 1)] = isF ? cs : -cs;
-        }
-        wait(bar + 3, 0);
-        {  // row r = dk, positions 16 h ..
-            const int t0 = 16 * h;
+            wait(&bar->out_done, ph);
+            // row r = dk, positions 16 h ..
             float tok[16], outs = 0.f;
             uint8_t *sq = base + L::out, *sk = sq + (D / 64) * kBlk;
 #pragma unroll
             for (int x0 = 0; x0 < 16; x0 += 8) {
+                const int t0 = col0 + x0;
                 uint32_t q1[8], k1[8], ka[8], kb[8], qa[8], qb[8], ea[8], eb[8];
-                ld(lb + GTm::q1 + t0 + x0, q1);
-                ld(lb + GTm::k1 + t0 + x0, k1);
-                ld(lb + GTm::k3 + t0 + x0, ka);
-                ld(lb + GTm::k3 + kC + t0 + x0, kb);
-                ld(lb + GTm::q2 + t0 + x0, qa);
-                ld(lb + GTm::q2 + kC + t0 + x0, qb);
-                ld(lb + GTm::k2 + t0 + x0, ea);
-                ld(lb + GTm::k2 + kC + t0 + x0, eb);
+                ld(lb + GTm::q1 + t0, q1);
+                ld(lb + GTm::k1 + t0, k1);
+                ld(lb + GTm::k3 + t0, ka);
+                ld(lb + GTm::k3 + kC + t0, kb);
+                ld(lb + GTm::q2 + t0, qa);
+                ld(lb + GTm::q2 + kC + t0, qb);
+                ld(lb + GTm::k2 + t0, ea);
+                ld(lb + GTm::k2 + kC + t0, eb);
                 tmem_ld_wait();
+                if (x0 == 8) arrive(&bar->acc_free);
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    const int t = t0 + x0 + x;
-                    const float dqi = rec[kGam + t] * __uint_as_float(q1[x]);
-                    const float dki = -rec[kBg + t] * __uint_as_float(k1[x]);
-                    const float dko = rec[kTb + t] * (__uint_as_float(ka[x]) + __uint_as_float(kb[x]));
-                    const float dqv = dqi + (__uint_as_float(qa[x]) + __uint_as_float(qb[x]));
-                    const float dkv = (dki + dko) + (__uint_as_float(ea[x]) + __uint_as_float(eb[x]));
-                    float s = 0.f;
-                    if (r < D) {
-                        const int eo = (r >> 6) * 2 * kBlk + (elem_off(t, r) - (r >> 6) * kBlk);  // [Q; K] blocks
-                        const float qv = __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(base + L::QK + eo) << 16);
-                        const float kv =
-                            __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(base + L::QK + kBlk + eo) << 16);
-                        const float o = kv * dko;
-                        s = fmaf(qv, dqi, fmaf(kv, dki, -o));
-                        outs += o;
-                        const int off = elem_off(t, r);
-                        *reinterpret_cast<__nv_bfloat16*>(sq + off) = __float2bfloat16_rn(dqv);
-                        *reinterpret_cast<__nv_bfloat16*>(sk + off) = __float2bfloat16_rn(dkv);
+                for (int y = 0; y < 8; y += 4) {
+                    const float4 ga = ld_f4(rec + kGam + t0 + y), bg = ld_f4(rec + kBg + t0 + y),
+                                 tb = ld_f4(rec + kTb + t0 + y);
+                    const float gav[4] = {ga.x, ga.y, ga.z, ga.w}, bgv[4] = {bg.x, bg.y, bg.z, bg.w},
+                                tbv[4] = {tb.x, tb.y, tb.z, tb.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int x = y + e, t = t0 + x;
+                        const float dqi = gav[e] * __uint_as_float(q1[x]);
+                        const float dki = -bgv[e] * __uint_as_float(k1[x]);
+                        const float dko = tbv[e] * (__uint_as_float(ka[x]) + __uint_as_float(kb[x]));
+                        const float dqv = dqi + (__uint_as_float(qa[x]) + __uint_as_float(qb[x]));
+                        const float dkv = (dki + dko) + (__uint_as_float(ea[x]) + __uint_as_float(eb[x]));
+                        float s = 0.f;
+                        if (r < D) {
+                            const int off = elem_off(t, r);
+                            const int eo = off + (r >> 6) * kBlk;  // [Q; K] blocks
+                            const float qv =
+                                __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(base + L::QK + eo) << 16);
+                            const float kv = __uint_as_float(
+                                (uint32_t) * reinterpret_cast<const uint16_t*>(base + L::QK + kBlk + eo) << 16);
+                            const float o = kv * dko;
+                            s = fmaf(qv, dqi, fmaf(kv, dki, -o));
+                            outs += o;
+                            *reinterpret_cast<__nv_bfloat16*>(sq + off) = __float2bfloat16_rn(dqv);
+                            *reinterpret_cast<__nv_bfloat16*>(sk + off) = __float2bfloat16_rn(dkv);
+                        }
+                        tok[x0 + x] = s;
                     }
-                    tok[x0 + x] = s;
                 }
             }
             const float ts = reduce16(tok, lane);
-            if ((lane & 1) == 0) part[L::pTok + q4 * kC + t0 + (lane >> 1)] = ts;
+            if ((lane & 1) == 0) part[L::pTok + q4 * kC + col0 + (lane >> 1)] = ts;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 outs += __shfl_xor_sync(0xffffffffu, outs, o);
@@ -626,53 +703,55 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 part[L::pSum + (warp - 2)] = outs;
                 part[L::pSum + kWarps + (warp - 2)] = kept;
             }
-        }
-        fence_proxy_async_smem();
-        named_barrier(1, 32 * kWarps);
-        if (ct == 0) {
+            fence_proxy_async_smem();
+            named_barrier(1, 32 * kWarps);
+            if (ct == 0) {
 #pragma unroll
-            for (int b = 0; b < D / 64; ++b) {
-                tma_store_3d(&tm_dq, base + L::out + b * kBlk, 64 * b, c0, bh);
-                tma_store_3d(&tm_dk, base + L::out + (D / 64 + b) * kBlk, 64 * b, c0, bh);
+                for (int b = 0; b < D / 64; ++b) {
+                    tma_store_3d(&tm_dq, base + L::out + b * kBlk, 64 * b, c0, bh);
+                    tma_store_3d(&tm_dk, base + L::out + (D / 64 + b) * kBlk, 64 * b, c0, bh);
+                }
+                bulk_commit();
             }
-            bulk_commit();
-        }
-        if (warp == 3) {  // dg: the reverse cumulative sum, in fp64 (its terms cancel); two positions to a lane
-            double v[2];
+            if (warp == 3) {  // dg: the reverse cumulative sum, in fp64 (its terms cancel); two positions to a lane
+                double v[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = 2 * lane + e;
-                double a = 0.0;
+                for (int e = 0; e < 2; ++e) {
+                    const int j = 2 * lane + e;
+                    double a = 0.0;
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    a += (double)part[L::pRow + y * 128 + i] + (double)part[L::pRow + y * 128 + kC + i] +
-                         (double)part[L::pCol + y * kC + i] + (double)part[L::pTok + y * kC + i];
-                v[e] = a;
+                    for (int y = 0; y < 4; ++y)
+                        a += (double)((part[L::pRow + y * 128 + j] + part[L::pRow + y * 128 + kC + j]) +
+                                      (part[L::pCol + y * kC + j] + part[L::pTok + y * kC + j]));
+                    v[e] = a;
+                }
+                float tail = part[L::pSum + kWarps + (lane & (kWarps - 1))], os = part[L::pSum + (lane & (kWarps - 1))];
+#pragma unroll
+                for (int o = kWarps / 2; o > 0; o >>= 1) {
+                    tail += __shfl_xor_sync(0xffffffffu, tail, o);
+                    os += __shfl_xor_sync(0xffffffffu, os, o);
+                }
+                const double all = (double)tail * (double)rec[kGam + kC - 1] + (double)os;
+                const double both = v[0] + v[1];
+                double run = both;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const double x = __shfl_down_sync(0xffffffffu, run, o);
+                    if (lane + o < 32) run += x;
+                }
+                const double after = run - both;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int j = 2 * lane + e;
+                    if (j >= n) continue;
+                    const size_t pos = (size_t)bh * N + c0 + j;
+                    const double d = after + (e ? v[1] : both) + all;
+                    dg[pos] = __float2bfloat16_rn(__bfloat162float(g[pos]) < kReset ? 0.f : (float)d);
+                    dbeta[pos] = __float2bfloat16_rn(part[L::dBeta + j]);
+                }
             }
-            double tail = 0.0, os = 0.0;
-#pragma unroll
-            for (int y = 0; y < kWarps; ++y) {
-                os += (double)part[L::pSum + y];
-                tail += (double)part[L::pSum + kWarps + y];
-            }
-            tail = tail * (double)rec[kGam + kC - 1] + os;
-            const double both = v[0] + v[1];
-            double run = both;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double x = __shfl_down_sync(0xffffffffu, run, o);
-                if (lane + o < 32) run += x;
-            }
-            const double after = run - both;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = 2 * lane + e;
-                if (i >= n) continue;
-                const size_t pos = (size_t)bh * N + c0 + i;
-                const double d = after + (e ? v[1] : both) + tail;
-                dg[pos] = __float2bfloat16_rn(__bfloat162float(g[pos]) < kReset ? 0.f : (float)d);
-                dbeta[pos] = __float2bfloat16_rn(part[L::dBeta + i]);
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar->b_free);  // this warp is done with Q, K and the gates
         }
         if (ct == 0) bulk_wait_all();
         tc_fence_before();
@@ -734,9 +813,10 @@ cudaError_t bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
     GD_TRY(reverse(false, segdS, nullptr));
     GD_TRY(allow_smem(tc_gd_grads<D>, GradSmem<D>::bytes));
     launch_begin("tc_gd_grads", st);
-    const cudaError_t e = launch_pdl(tc_gd_grads<D>, dim3(M, BH), dim3(kThreads), GradSmem<D>::bytes, st, tq, tk, tdo, tdq, tdk,
+    const int total = BH * M;
+    const cudaError_t e = launch_pdl(tc_gd_grads<D>, dim3(total < 152 ? total : 152), dim3(kThreads), GradSmem<D>::bytes, st, tq, tk, tdo, tdq, tdk,
                    (const __nv_bfloat16*)a.g, (const float*)recs, (const uint8_t*)X, (const uint8_t*)Y,
-                   (const uint8_t*)S, (const uint8_t*)dS, (__nv_bfloat16*)a.dg, (__nv_bfloat16*)a.dbeta, s.N, M, err);
+                   (const uint8_t*)S, (const uint8_t*)dS, (__nv_bfloat16*)a.dg, (__nv_bfloat16*)a.dbeta, s.N, M, total, err);
     const cudaError_t e2 = launch_end("tc_gd_grads", st);
     return e != cudaSuccess ? e : e2;
 }

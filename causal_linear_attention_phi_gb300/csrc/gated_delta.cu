@@ -68,7 +68,6 @@ gd_prepare(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict
     float* ks = sm.take(kC * (Dk + 1));
     float* qs = sm.take(kC * (Dk + 1));
     float* As = sm.take(kC * kLd);
-    float* tt = sm.take(kC * kLd);
     float* rec = sm.take(kRec);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, m = blockIdx.x;
     const size_t bh = blockIdx.y;
@@ -96,8 +95,8 @@ gd_prepare(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict
             Ps[at * kC * kC + r * kC + c] = d != 0.f ? qk[i][j] * d : 0.f;
         }
     __syncthreads();
-    solve_t(As, tt, rec + kBeta, tid);
-    for (int i = tid; i < kC * kC; i += kThreads) ts[at * kC * kC + i] = tt[(i >> 6) * kLd + (i & 63)];
+    solve_t(As, rec + kBeta, tid);
+    for (int i = tid; i < kC * kC; i += kThreads) ts[at * kC * kC + i] = As[(i >> 6) * kLd + (i & 63)];
     for (int i = tid; i < kRec; i += kThreads) recs[at * kRec + i] = rec[i];
 }
 
@@ -473,7 +472,7 @@ gd_grads(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__
 }
 
 int f4(int n) { return (n + 3) / 4 * 4; }
-size_t smem_prepare(int Dk) { return 4 * (size_t)(2 * f4(kC * (Dk + 1)) + 2 * kC * kLd + kRec); }
+size_t smem_prepare(int Dk) { return 4 * (size_t)(2 * f4(kC * (Dk + 1)) + kC * kLd + kRec); }
 size_t smem_states(int Dk) {
     return 4 * (size_t)(2 * f4(kC * (Dk + 1)) + 2 * f4(kC * kLc) + f4(Dk * kLw) + 2 * f4(kC * kLw) + kRec);
 }

@@ -28,8 +28,8 @@ namespace gd {
 
 constexpr int kC = 64;
 
-// The gates of one chunk, fp32, one record per (head, chunk) in the workspace.  The sum of log decays is
-// formed in fp64 and kept as hi + lo, so that differences of long sums keep fp32's precision; a decay
+// The gates of one chunk, fp32, one record per (head, chunk) in the workspace.  The sum of log decays (to the base
+// 2 here) is formed in fp64 and kept as hi + lo, so that differences of long sums keep fp32's precision; a decay
 // below exp(-100) (under fp32's normal range; -inf among them) is counted in kSeg instead of entering the sum,
 // and a product across it is 0.  Positions past the sequence's end have g = 0 and beta = 0.
 constexpr int kGam = 0, kTail = kC, kBeta = 2 * kC, kBg = 3 * kC, kTb = 4 * kC;  // kBg = beta gam, kTb = tail beta
@@ -37,16 +37,16 @@ constexpr int kGhi = 5 * kC, kGlo = 6 * kC, kSeg = 7 * kC;
 constexpr int kRec = 8 * kC;
 constexpr float kReset = -100.f;
 
-// exp(hi + lo) for |lo| at most half a step of hi.
-__device__ __forceinline__ float exp_hilo(float hi, float lo) {
-    const float e = expf(hi);
-    return fmaf(e, lo, e);
+// 2^(hi + lo) for |lo| at most half a step of hi.
+__device__ __forceinline__ float exp2_hilo(float hi, float lo) {
+    const float e = exp2f(hi);
+    return fmaf(e, lo * 0.6931471805599453f, e);
 }
 
 // Gam_ij for i >= j (0 across a reset).
 __device__ __forceinline__ float pair_decay(const float* rec, int i, int j) {
     return rec[kSeg + i] == rec[kSeg + j]
-               ? exp_hilo(rec[kGhi + i] - rec[kGhi + j], rec[kGlo + i] - rec[kGlo + j])
+               ? exp2_hilo(rec[kGhi + i] - rec[kGhi + j], rec[kGlo + i] - rec[kGlo + j])
                : 0.f;
 }
 
@@ -61,7 +61,7 @@ __device__ __forceinline__ void gate_record(const T* __restrict__ g, const T* __
         const int i = 2 * lane + e;
         const float x = i < n ? to_f32(g[c0 + i]) : 0.f;
         const bool reset = x < kReset;
-        v[e] = reset ? 0.0 : (double)x;
+        v[e] = reset ? 0.0 : (double)x * 1.4426950408889634074;
         r[e] = reset ? 1 : 0;
     }
     v[1] += v[0];
@@ -91,7 +91,7 @@ __device__ __forceinline__ void gate_record(const T* __restrict__ g, const T* __
         rec[kGhi + i] = hi;
         rec[kGlo + i] = lo;
         rec[kSeg + i] = (float)seg;
-        const float gam = seg == 0 ? exp_hilo(hi, lo) : 0.f, tail = seg == rtot ? exp_hilo(dhi, dlo) : 0.f;
+        const float gam = seg == 0 ? exp2_hilo(hi, lo) : 0.f, tail = seg == rtot ? exp2_hilo(dhi, dlo) : 0.f;
         const float b = i < n ? to_f32(beta[c0 + i]) : 0.f;
         rec[kGam + i] = gam;
         rec[kTail + i] = tail;
@@ -101,26 +101,59 @@ __device__ __forceinline__ void gate_record(const T* __restrict__ g, const T* __
     }
 }
 
-// t = -A (I + beta A)^-1 for a strictly lower triangular A (zero on and above the diagonal), 64 x 64 fp32 in
-// shared memory with row pitch kLd, by 256 threads.  Four diagonal blocks of 16 by forward substitution,
-// t_i = -(A_i + sum_(j<i) A_ij beta_j t_j), one column to a lane, the column in registers; then blocks are joined in
-// pairs, first to 32 and then to 64: t21 = -(I + t22 beta) A21 (I + beta t11), two small products each.  (Diagonal
-// blocks of 32 left six of eight warps waiting for a chain of 31 rows.)  Every thread calls it; A (overwritten) is
-// complete before, t after.
-constexpr int kLd = kC + 4;
+constexpr int kLd = kC + 4;  // row pitch of A
 
 __device__ __forceinline__ float4 ld_f4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-__device__ __forceinline__ void solve_t(float* A, float* t, const float* beta, int tid) {
+// a += m b on two floats at once.
+__device__ __forceinline__ void fma2(float2& a, float m, float2 b) {
+    const float2 mm = make_float2(m, m);
+    asm("fma.rn.f32x2 %0, %1, %2, %0;"
+        : "+l"(reinterpret_cast<uint64_t&>(a))
+        : "l"(reinterpret_cast<const uint64_t&>(mm)), "l"(reinterpret_cast<const uint64_t&>(b)));
+}
+struct F4 {
+    float2 a, b;
+};
+__device__ __forceinline__ void fma4(F4& z, float m, float4 v) {
+    fma2(z.a, m, make_float2(v.x, v.y));
+    fma2(z.b, m, make_float2(v.z, v.w));
+}
+__device__ __forceinline__ F4 get4(const float* p) {
+    const float4 v = ld_f4(p);
+    return {make_float2(v.x, v.y), make_float2(v.z, v.w)};
+}
+__device__ __forceinline__ void put4(float* p, const F4& z, float s = 1.f) {
+    *reinterpret_cast<float4*>(p) = make_float4(s * z.a.x, s * z.a.y, s * z.b.x, s * z.b.y);
+}
+// z += sum_(k0 <= k < k1) row[k] beta[k] m[k][0..3], m's rows kLd apart; k0 and k1 multiples of 4.
+__device__ __forceinline__ void acc_rows(F4& z, const float* row, const float* beta, const float* m, int k0, int k1) {
+#pragma unroll 4
+    for (int k = k0; k < k1; k += 4) {
+        const float4 a = ld_f4(row + k), be = ld_f4(beta + k);
+        fma4(z, a.x * be.x, ld_f4(m + k * kLd));
+        fma4(z, a.y * be.y, ld_f4(m + (k + 1) * kLd));
+        fma4(z, a.z * be.z, ld_f4(m + (k + 2) * kLd));
+        fma4(z, a.w * be.w, ld_f4(m + (k + 3) * kLd));
+    }
+}
+
+// t = -A (I + beta A)^-1 in place of a strictly lower triangular A (zero on and above the diagonal), 64 x 64 fp32 in
+// shared memory with row pitch kLd.  Four diagonal blocks of 16 by forward substitution,
+// t_i = -(A_i + sum_(j<i) A_ij beta_j t_j), one column to a lane, the column in registers; then blocks are joined in
+// pairs, first to 32 and then to 64: t21 = -(I + t22 beta) A21 (I + beta t11), two small products each.  (Diagonal
+// blocks of 32 left all but two warps waiting for a chain of 31 rows.)  The first 128 threads do the work, all threads
+// call it; A is complete before, t after.
+__device__ __forceinline__ void solve_t(float* A, const float* beta, int tid) {
     constexpr int kH = kC / 2, kQ = kC / 4;
+    const bool work = tid < 128;
     if (tid < kC) {
         const int b0 = tid & 48, c = tid & 15;
         float y[kQ];  // beta_j t_j of this column
-        t[b0 * kLd + b0 + c] = 0.f;
         y[0] = 0.f;
 #pragma unroll
         for (int r = 1; r < kQ; ++r) {
-            const float* a = A + (b0 + r) * kLd + b0;
+            float* a = A + (b0 + r) * kLd + b0;
             float s0 = a[c], s1 = 0.f;
 #pragma unroll
             for (int j = 0; j < r; j += 4) {
@@ -131,86 +164,56 @@ __device__ __forceinline__ void solve_t(float* A, float* t, const float* beta, i
                 if (j + 3 < r) s1 = fmaf(v.w, y[j + 3], s1);
             }
             const float x = r > c ? -(s0 + s1) : 0.f;
-            t[(b0 + r) * kLd + b0 + c] = x;
+            __syncwarp();  // the row has been read
+            a[c] = x;
             y[r] = beta[b0 + r] * x;
         }
-    } else {  // what lies above the diagonal blocks
-        for (int i = tid - kC; i < kC * 12; i += 192) {
-            const int r = i / 12, v = i % 12;  // vectors of four columns past this row's diagonal block
-            const int c = 4 * v + 16;
-            if (c >= (r & 48) + 16) *reinterpret_cast<float4*>(t + r * kLd + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
     }
     __syncthreads();
-    {  // pair p: rows 32 p + 16 + r, columns 32 p + c, c + 1
-        const int b = kH * (tid >> 7), r = (tid >> 3) & 15, c = 2 * (tid & 7);
+    {  // pair p: rows 32 p + 16 + r, columns 32 p + c .. c + 3
+        const int b = kH * ((tid >> 6) & 1), r = (tid >> 2) & 15, c = 4 * (tid & 3);
         float* row = A + (b + kQ + r) * kLd + b;
-        float2 z = *reinterpret_cast<const float2*>(row + c);
-#pragma unroll
-        for (int k = 0; k < kQ; k += 4) {
-            const float4 a = ld_f4(row + k), be = ld_f4(beta + b + k);
-            const float av[4] = {a.x * be.x, a.y * be.y, a.z * be.z, a.w * be.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 v = *reinterpret_cast<const float2*>(t + (b + k + e) * kLd + b + c);
-                z.x = fmaf(av[e], v.x, z.x);
-                z.y = fmaf(av[e], v.y, z.y);
-            }
+        F4 z;
+        if (work) {
+            z = get4(row + c);
+            acc_rows(z, row, beta + b, A + b * kLd + b + c, 0, kQ);
         }
         __syncthreads();
-        *reinterpret_cast<float2*>(row + c) = z;
+        if (work) put4(row + c, z);
         __syncthreads();
-        const float* tr = t + (b + kQ + r) * kLd + b + kQ;
-#pragma unroll
-        for (int k = 0; k < kQ; k += 4) {
-            const float4 a = ld_f4(tr + k), be = ld_f4(beta + b + kQ + k);
-            const float av[4] = {a.x * be.x, a.y * be.y, a.z * be.z, a.w * be.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 v = *reinterpret_cast<const float2*>(A + (b + kQ + k + e) * kLd + b + c);
-                z.x = fmaf(av[e], v.x, z.x);
-                z.y = fmaf(av[e], v.y, z.y);
-            }
-        }
-        *reinterpret_cast<float2*>(t + (b + kQ + r) * kLd + b + c) = make_float2(-z.x, -z.y);
+        if (work) acc_rows(z, row + kQ, beta + b + kQ, A + (b + kQ) * kLd + b + c, 0, kQ);
+        __syncthreads();
+        if (work) put4(row + c, z, -1.f);
+        __syncthreads();
     }
-    __syncthreads();
-    // this thread: row kH + r, columns c .. c + 3 of the lower left block
-    const int r = tid >> 3, c = 4 * (tid & 7);
-    float* row = A + (kH + r) * kLd;
-    float4 z = ld_f4(row + c);
-#pragma unroll
-    for (int k = 0; k < kH; k += 4) {
-        const float4 a = ld_f4(row + k), be = ld_f4(beta + k);
-        const float av[4] = {a.x * be.x, a.y * be.y, a.z * be.z, a.w * be.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float4 b = ld_f4(t + (k + e) * kLd + c);
-            z.x = fmaf(av[e], b.x, z.x);
-            z.y = fmaf(av[e], b.y, z.y);
-            z.z = fmaf(av[e], b.z, z.z);
-            z.w = fmaf(av[e], b.w, z.w);
+    {  // row 32 + r, columns c .. c + 3 and 16 + c .. 16 + c + 3; t11 and t22 are lower triangular
+        const int r = (tid >> 2) & 31, c = 4 * (tid & 3);
+        float* row = A + (kH + r) * kLd;
+        F4 z0, z1;
+        if (work) {
+            z0 = get4(row + c);
+            z1 = get4(row + kQ + c);
+            acc_rows(z0, row, beta, A + c, 0, kH);
+            acc_rows(z1, row, beta, A + kQ + c, kQ, kH);
         }
-    }
-    __syncthreads();
-    *reinterpret_cast<float4*>(row + c) = z;
-    __syncthreads();
-    const float* tr = t + (kH + r) * kLd + kH;
-#pragma unroll
-    for (int k = 0; k < kH; k += 4) {
-        const float4 a = ld_f4(tr + k), be = ld_f4(beta + kH + k);
-        const float av[4] = {a.x * be.x, a.y * be.y, a.z * be.z, a.w * be.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float4 b = ld_f4(A + (kH + k + e) * kLd + c);
-            z.x = fmaf(av[e], b.x, z.x);
-            z.y = fmaf(av[e], b.y, z.y);
-            z.z = fmaf(av[e], b.z, z.z);
-            z.w = fmaf(av[e], b.w, z.w);
+        __syncthreads();
+        if (work) {
+            put4(row + c, z0);
+            put4(row + kQ + c, z1);
         }
+        __syncthreads();
+        if (work) {
+            const int k1 = r < kQ ? kQ : kH;  // the same for a whole warp
+            acc_rows(z0, row + kH, beta + kH, A + kH * kLd + c, 0, k1);
+            acc_rows(z1, row + kH, beta + kH, A + kH * kLd + kQ + c, 0, k1);
+        }
+        __syncthreads();
+        if (work) {
+            put4(row + c, z0, -1.f);
+            put4(row + kQ + c, z1, -1.f);
+        }
+        __syncthreads();
     }
-    *reinterpret_cast<float4*>(t + (kH + r) * kLd + c) = make_float4(-z.x, -z.y, -z.z, -z.w);
-    __syncthreads();
 }
 
 // Byte offsets of the workspace regions of one call (256-byte aligned).

@@ -29,22 +29,42 @@ using namespace sm100;
 using namespace tcgd;
 
 // ------------------------------------------------------------------ t and P of every chunk
-constexpr int kPrepThreads = 256;
+// 128 threads, six blocks to an SM: the phases of a chunk are short and each ends in a barrier, so what counts is how many
+// chunks an SM has in hand (256 threads and four blocks: 0.82 ms at B=2 H=16 N=65536 D=128).
+constexpr int kPrepThreads = 128;
 struct PrepSmem {
-    // offset 0: blocks of [Q rows 0-63; K rows 64-127] x 64 columns, then (once the product has read them) fp32 A, and
-    // last t's tiles over A
+    // offset 0: blocks of [Q rows 0-63; K rows 64-127] x 64 columns, then (once the product has read them) fp32 A, which
+    // becomes t, and P's tiles; t's tiles last, in the place of P's once those are stored
     static constexpr int A = 0;
-    static constexpr int T = 18432;  // A's bytes rounded up to a tile's alignment
-    static constexpr int P = T + 18432;  // P's tiles
+    static constexpr int P = 18432;  // A's bytes rounded up to a tile's alignment
     static constexpr int rec = P + 2 * kBlk;
     static constexpr int bar = rec + kRec * 4;
     static constexpr int total = bar + 32;
 };
-static_assert(PrepSmem::T >= kC * kLd * 4 && PrepSmem::T >= 2 * kBlk && PrepSmem::P >= 4 * kBlk, "regions");
+static_assert(PrepSmem::P >= kC * kLd * 4 && PrepSmem::rec >= 4 * kBlk, "regions");
 constexpr size_t kPrepBytes = PrepSmem::total + 1024;
 
+// w[x] (columns j0 .. j0 + 31 of row i) times the decay from j to i, 0 outside j <= i (j < i).
+template <bool kResets>
+__device__ __forceinline__ void decay32(uint32_t (&w)[32], const float* rec, int i, int j0, bool incl) {
+    const float seg = rec[kSeg + i], hi = rec[kGhi + i], lo = rec[kGlo + i];
+    const int last = incl ? i : i - 1;
+#pragma unroll
+    for (int x = 0; x < 32; x += 4) {
+        const float4 gh = ld_f4(rec + kGhi + j0 + x), gl = ld_f4(rec + kGlo + j0 + x);
+        const float4 sg = kResets ? ld_f4(rec + kSeg + j0 + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float ghv[4] = {gh.x, gh.y, gh.z, gh.w}, glv[4] = {gl.x, gl.y, gl.z, gl.w}, sgv[4] = {sg.x, sg.y, sg.z, sg.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool in = j0 + x + e <= last && (!kResets || sgv[e] == seg);
+            const float d = ex2_approx((hi - ghv[e]) + (lo - glv[e]));
+            w[x + e] = in ? __float_as_uint(__uint_as_float(w[x + e]) * d) : 0u;
+        }
+    }
+}
+
 template <int D>
-__global__ void __launch_bounds__(kPrepThreads, 4)
+__global__ void __launch_bounds__(kPrepThreads, 6)
 tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __nv_bfloat16* __restrict__ g, const __nv_bfloat16* __restrict__ beta, float* __restrict__ recs,
               uint8_t* __restrict__ mats, int N, int M, int* err) {
@@ -87,81 +107,78 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     __syncthreads();  // the gates
     tc_fence_after();
     float* A = reinterpret_cast<float*>(base + PrepSmem::A);
-    float* T = reinterpret_cast<float*>(base + PrepSmem::T);
     {
-        // lanes 0-63 hold Q K^T, 64-127 K K^T; this thread row i, positions 32 h .. +31
-        const int quarter = warp & 3, h = warp >> 2, i = 32 * (quarter & 1) + lane, j0 = 32 * h;
-        uint32_t w[32];
-        tmem_ld32(tmem + ((uint32_t)(32 * quarter) << 16) + j0, w);
-        tmem_ld_wait();
-        const float seg = rec[kSeg + i], hi = rec[kGhi + i], lo = rec[kGlo + i];
-        const bool isP = quarter < 2;
-        if (h > (quarter & 1)) {  // above the diagonal
+        // lanes 0-63 hold Q K^T, 64-127 K K^T; this thread's row i, 32 columns at a time
+        const int i = tid & 63;
+        const bool isP = tid < 64, resets = rec[kSeg + kC - 1] != 0.f;
 #pragma unroll
-            for (int x = 0; x < 32; ++x) w[x] = 0u;
-        } else {
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[32];
+            if (h > (warp & 1)) {  // above the diagonal
 #pragma unroll
-            for (int x = 0; x < 32; x += 4) {
-                const float4 gh = ld_f4(rec + kGhi + j0 + x), gl = ld_f4(rec + kGlo + j0 + x), sg = ld_f4(rec + kSeg + j0 + x);
-                const float ghv[4] = {gh.x, gh.y, gh.z, gh.w}, glv[4] = {gl.x, gl.y, gl.z, gl.w},
-                            sgv[4] = {sg.x, sg.y, sg.z, sg.w};
+                for (int x = 0; x < 32; ++x) w[x] = 0u;
+            } else {
+                tmem_ld32(tmem + ((uint32_t)(32 * warp) << 16) + 32 * h, w);
+                tmem_ld_wait();
+                if (resets)
+                    decay32<true>(w, rec, i, 32 * h, isP);
+                else
+                    decay32<false>(w, rec, i, 32 * h, isP);
+            }
+            if (isP) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = j0 + x + e;
-                    const bool in = (isP ? j <= i : j < i) && sgv[e] == seg;
-                    const float d = (hi - ghv[e]) + (lo - glv[e]);
-                    w[x + e] = in ? __float_as_uint(__uint_as_float(w[x + e]) * ex2_approx(d * 1.4426950408889634f)) : 0u;
+                for (int c = 0; c < 4; ++c) {
+                    uint4 a, b;
+                    split2(__uint_as_float(w[8 * c]), __uint_as_float(w[8 * c + 1]), a.x, b.x);
+                    split2(__uint_as_float(w[8 * c + 2]), __uint_as_float(w[8 * c + 3]), a.y, b.y);
+                    split2(__uint_as_float(w[8 * c + 4]), __uint_as_float(w[8 * c + 5]), a.z, b.z);
+                    split2(__uint_as_float(w[8 * c + 6]), __uint_as_float(w[8 * c + 7]), a.w, b.w);
+                    const int off = row_off(i, 4 * h + c);
+                    *reinterpret_cast<uint4*>(base + PrepSmem::P + off) = a;
+                    *reinterpret_cast<uint4*>(base + PrepSmem::P + kBlk + off) = b;
                 }
-            }
-        }
-        if (isP) {
+            } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint4 a, b;
-                split2(__uint_as_float(w[8 * c]), __uint_as_float(w[8 * c + 1]), a.x, b.x);
-                split2(__uint_as_float(w[8 * c + 2]), __uint_as_float(w[8 * c + 3]), a.y, b.y);
-                split2(__uint_as_float(w[8 * c + 4]), __uint_as_float(w[8 * c + 5]), a.z, b.z);
-                split2(__uint_as_float(w[8 * c + 6]), __uint_as_float(w[8 * c + 7]), a.w, b.w);
-                const int off = elem_off(i, j0 + 8 * c);
-                *reinterpret_cast<uint4*>(base + PrepSmem::P + off) = a;
-                *reinterpret_cast<uint4*>(base + PrepSmem::P + kBlk + off) = b;
+                for (int x = 0; x < 32; x += 4)
+                    *reinterpret_cast<uint4*>(A + i * kLd + 32 * h + x) = make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
             }
-        } else {
-#pragma unroll
-            for (int x = 0; x < 32; x += 4)
-                *reinterpret_cast<uint4*>(A + i * kLd + j0 + x) = make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
         }
     }
+    fence_proxy_async_smem();
     __syncthreads();
-    solve_t(A, T, rec + kBeta, tid);
+    uint8_t* mat = mats + at * (size_t)kMats;
+    if (tid == 0) {
+        bulk_store(mat + kPHi, base + PrepSmem::P, 2 * kBlk);
+        bulk_store(recs + at * kRec, rec, kRec * 4);
+        bulk_commit();
+    }
+    solve_t(A, rec + kBeta, tid);
+    if (tid == 0) bulk_wait_read_all();  // P's tiles have been stored: t's go in their place
+    __syncthreads();
     {
-        const int i = tid >> 2, j0 = 16 * (tid & 3);
+        const int i = tid >> 1, j0 = 32 * (tid & 1);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const float4 s = ld_f4(T + i * kLd + j0 + 8 * c), u = ld_f4(T + i * kLd + j0 + 8 * c + 4);
+        for (int c = 0; c < 4; ++c) {
+            const float4 s = ld_f4(A + i * kLd + j0 + 8 * c), u = ld_f4(A + i * kLd + j0 + 8 * c + 4);
             uint4 a, b;
             split2(s.x, s.y, a.x, b.x);
             split2(s.z, s.w, a.y, b.y);
             split2(u.x, u.y, a.z, b.z);
             split2(u.z, u.w, a.w, b.w);
-            const int off = elem_off(i, j0 + 8 * c);
-            *reinterpret_cast<uint4*>(base + off) = a;
-            *reinterpret_cast<uint4*>(base + kBlk + off) = b;
+            const int off = row_off(i, (j0 >> 3) + c);
+            *reinterpret_cast<uint4*>(base + PrepSmem::P + off) = a;
+            *reinterpret_cast<uint4*>(base + PrepSmem::P + kBlk + off) = b;
         }
     }
     fence_proxy_async_smem();
-    __syncthreads();
-    if (tid == 0) {
-        uint8_t* mat = mats + at * (size_t)kMats;
-        bulk_store(mat + kTHi, base, 2 * kBlk);
-        bulk_store(mat + kPHi, base + PrepSmem::P, 2 * kBlk);
-        bulk_store(recs + at * kRec, rec, kRec * 4);
-        bulk_commit();
-        bulk_wait_all();
-    }
-    if (!ok && tid == 0) mbar_wait(bar, 0, err, LA_ERR_TIMEOUT);  // never leave with copies in flight
     tc_fence_before();
     __syncthreads();
+    if (tid == 0) {
+        bulk_store(mat + kTHi, base + PrepSmem::P, 2 * kBlk);
+        bulk_commit();
+        bulk_wait_all();
+        if (!ok) mbar_wait(bar, 0, err, LA_ERR_TIMEOUT);  // never leave with copies in flight
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 64);
@@ -587,14 +604,6 @@ struct JoinCfg {
     static constexpr int bars = S + D * kJoinCols * 4;
     static constexpr size_t bytes = bars + 32;
 };
-
-// a += m b on two floats at once.
-__device__ __forceinline__ void fma2(float2& a, float m, float2 b) {
-    const float2 mm = make_float2(m, m);
-    asm("fma.rn.f32x2 %0, %1, %2, %0;"
-        : "+l"(reinterpret_cast<uint64_t&>(a))
-        : "l"(reinterpret_cast<const uint64_t&>(mm)), "l"(reinterpret_cast<const uint64_t&>(b)));
-}
 
 template <int D, bool kReverse>
 __global__ void __launch_bounds__(JoinCfg<D>::threads)

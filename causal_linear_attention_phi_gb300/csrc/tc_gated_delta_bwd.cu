@@ -600,7 +600,7 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 ld(lb + (isF ? GTm::qk : GTm::kk) + col0, pq);
                 tmem_ld_wait();
                 const float seg = rec[kSeg + row], hi = rec[kGhi + row], lo = rec[kGlo + row], br = rec[kBeta + row];
-                const float sgn = isF ? -1.4426950408889634f : 1.4426950408889634f;
+                const float sgn = isF ? -1.f : 1.f;
 #pragma unroll
                 for (int x0 = 0; x0 < 16; x0 += 4) {
                     const float4 gh = ld_f4(rec + kGhi + col0 + x0), gl = ld_f4(rec + kGlo + col0 + x0),

@@ -188,7 +188,7 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 // ------------------------------------------------------------------ the recurrence
 struct __align__(8) Bars {
     uint64_t full[2], empty[2];
-    uint64_t s_ready, y_done, r_ready, x_done, u_ready, s_done, o_ready, o_done, o_free, final_mma;
+    uint64_t s_hi, s_lo, y_done, r_hi, r_lo, x_done, u_hi, u_lo, s_done, o_ready, o_done, o_free, final_mma;
 };
 
 template <int D, int kMode>
@@ -210,8 +210,9 @@ struct FwdSmem {
 // TMEM columns
 template <int D>
 struct Tm {
-    static constexpr uint32_t SHi = 0, SLo = D / 2, Y = D, R = D + 64, U = D + 128, O = D + 192, dS = D + 256;
-    static constexpr uint32_t X = dS;  // two products of 64 columns, read before dS is written
+    static constexpr uint32_t SHi = 0, SLo = D / 2, R = D, U = D + 64, O = D + 128;
+    // Y, then the two products of X, then dS, each read before the next is written
+    static constexpr uint32_t Y = D + 256, X = Y, dS = Y;
     static_assert(dS + 128 <= 512, "TMEM");
 };
 
@@ -246,11 +247,14 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         mbar_init(&bar->full[1], 1);
         mbar_init(&bar->empty[0], 1 + kWarps);
         mbar_init(&bar->empty[1], 1 + kWarps);
-        mbar_init(&bar->s_ready, kWarps);
+        mbar_init(&bar->s_hi, kWarps);
+        mbar_init(&bar->s_lo, kWarps);
         mbar_init(&bar->y_done, 1);
-        mbar_init(&bar->r_ready, kWarps);
+        mbar_init(&bar->r_hi, kWarps);
+        mbar_init(&bar->r_lo, kWarps);
         mbar_init(&bar->x_done, 1);
-        mbar_init(&bar->u_ready, kWarps);
+        mbar_init(&bar->u_hi, kWarps);
+        mbar_init(&bar->u_lo, kWarps);
         mbar_init(&bar->s_done, 1);
         mbar_init(&bar->o_ready, kWarps);
         mbar_init(&bar->o_done, 1);
@@ -301,19 +305,16 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 __syncwarp();
                 tc_fence_after();
             };
-            // O += u P^T of chunk j, issued while the next chunk's R is formed
+            // u P^T of chunk j, added to O (scaled by gam) in two columns' sets, while the next chunk's R is formed
             auto outputs = [&](int j) {
-                const uint32_t dM = tile_desc(smem_u32(base + (j & 1) * L::stage) + L::mats);
+                const uint32_t dP = tile_desc(smem_u32(base + (j & 1) * L::stage) + L::mats + kPHi);
                 wait(&bar->o_ready, j & 1);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_ts1(lead, tmem + T::O, tmem + T::U + 8 * kk, dM + (kPHi >> 4) + step_k(kk), id_k, 1);
+                for (int kk = 0; kk < 4; ++kk)  // u_hi [P_hi; P_lo]^T
+                    mma_ts1(lead, tmem + T::O, tmem + T::U + 8 * kk, dP + step_k(kk), id_k2, 1);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_ts1(lead, tmem + T::O, tmem + T::U + 32 + 8 * kk, dM + (kPHi >> 4) + step_k(kk), id_k, 1);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_ts1(lead, tmem + T::O, tmem + T::U + 8 * kk, dM + (kPLo >> 4) + step_k(kk), id_k, 1);
+                    mma_ts1(lead, tmem + T::O, tmem + T::U + 32 + 8 * kk, dP + step_k(kk), id_k, 1);
                 commit1(lead, &bar->o_done);
                 commit1(lead, &bar->empty[j & 1]);
             };
@@ -323,31 +324,36 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 const uint32_t dK = tile_desc(sg + L::K), dQ = tile_desc(sg + L::Q), dM = tile_desc(sg + L::mats);
                 const uint32_t dKmn = tile_desc<kBlk>(sg + L::K);
                 wait(&bar->full[s], (i >> 1) & 1);
-                wait(&bar->s_ready, ph);
+                wait(&bar->s_hi, ph);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)  // Y = S K^T
                     mma_ts1(lead, tmem + T::Y, tmem + T::SHi + 8 * kk, dK + step_k(kk), id_k, kk > 0);
+                wait(&bar->s_lo, ph);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     mma_ts1(lead, tmem + T::Y, tmem + T::SLo + 8 * kk, dK + step_k(kk), id_k, 1);
                 commit1(lead, &bar->y_done);
                 if (kMode == kOut && i > 0) outputs(i - 1);
-                wait(&bar->r_ready, ph);
+                wait(&bar->r_hi, ph);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)  // (beta R)_hi [t_hi; t_lo]^T: two products of 64 columns
                     mma_ts1(lead, tmem + T::X, tmem + T::R + 8 * kk, dM + step_k(kk), id_k2, kk > 0);
+                wait(&bar->r_lo, ph);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_ts1(lead, tmem + T::X, tmem + T::R + 32 + 8 * kk, dM + step_k(kk), id_k, 1);
                 commit1(lead, &bar->x_done);
-                if (kMode == kOut && i > 0) wait(&bar->o_free, ph ^ 1);
+                if constexpr (kMode == kOut) {  // O = S Q^T, while u is formed
+                    if (i > 0) wait(&bar->o_free, ph ^ 1);
 #pragma unroll
-                for (int kk = 0; kk < (kMode == kOut ? D / 16 : 0); ++kk)  // O = S Q^T
-                    mma_ts1(lead, tmem + T::O, tmem + T::SHi + 8 * kk, dQ + step_k(kk), id_k, kk > 0);
-                wait(&bar->u_ready, ph);
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_ts1(lead, tmem + T::O, tmem + T::SHi + 8 * kk, dQ + step_k(kk), id_k, kk > 0);
+                }
+                wait(&bar->u_hi, ph);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)  // the chunk's writes (tail u) K
                     mma_ts1(lead, tmem + T::dS, tmem + T::R + 8 * kk, dKmn + step_mn(kk), id_mn, kk > 0);
+                wait(&bar->u_lo, ph);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_ts1(lead, tmem + T::dS, tmem + T::R + 32 + 8 * kk, dKmn + step_mn(kk), id_mn, 1);
@@ -381,14 +387,12 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             S[x] = kMode == kSum ? ((map && kSc * h + x == r) || (D == 64 && kSc * h + x == r - D) ? 1.f : 0.f)
                    : a.S0 && r < D ? a.S0[(((size_t)bh * a.P + p) * D + kSc * h + x) * D + r]
                                    : 0.f;
-        auto put_state = [&]() {  // the state's hi and lo parts, and the signal that they are there
-            uint32_t hi[kSc / 2], lo[kSc / 2];
-#pragma unroll
-            for (int x = 0; x < kSc / 2; ++x) split2(S[2 * x], S[2 * x + 1], hi[x], lo[x]);
-            st(lb + T::SHi + kSc / 2 * h, hi);
-            st(lb + T::SLo + kSc / 2 * h, lo);
-            tmem_st_wait();
-            arrive(&bar->s_ready);
+        auto put_state = [&]() {
+            uint32_t hi[kSc / 2];
+            put_hi(lb + T::SHi + kSc / 2 * h, S, hi);
+            arrive(&bar->s_hi);
+            put_lo(lb + T::SLo + kSc / 2 * h, S, hi);
+            arrive(&bar->s_lo);
         };
         put_state();
         uint8_t* sO = base + L::out;
@@ -397,15 +401,16 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             if (ct == 0) bulk_wait_read_all();
             named_barrier(1, 32 * kWarps);
             wait(&bar->o_done, j & 1);
-            uint32_t w[kTok];
+            uint32_t w[kTok], w2[kTok];
             ld(lb + T::O + kTok * h, w);
+            ld(lb + T::O + kC + kTok * h, w2);
             tmem_ld_wait();
             arrive(&bar->o_free);
             if (r < D) {
 #pragma unroll
                 for (int x = 0; x < kTok; ++x)
                     *reinterpret_cast<__nv_bfloat16*>(sO + elem_off(kTok * h + x, r)) =
-                        __float2bfloat16_rn(__uint_as_float(w[x]));
+                        __float2bfloat16_rn(__uint_as_float(w[x]) + __uint_as_float(w2[x]));
             }
             fence_proxy_async_smem();
             named_barrier(1, 32 * kWarps);
@@ -423,7 +428,7 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             auto gate = [&](int which, int x) { return ld_f4(gates + which + kTok * h + x); };
             float R[kTok];  // beta V, then beta R
             float Rp[kMode == kGrad ? kTok : 1];  // V, R, then X
-            uint32_t w[kTok], hi[kTok / 2], lo[kTok / 2];
+            uint32_t w[kTok], hi[kTok / 2];
             wait(&bar->full[s], (i >> 1) & 1);
 #pragma unroll
             for (int x = 0; x < kTok; x += 4) {
@@ -432,9 +437,9 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float v = r < D && !map ? __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(
-                                                                sg + L::V + elem_off(kTok * h + x + e, r))
-                                                            << 16)
-                                          : 0.f;
+                                                                        sg + L::V + elem_off(kTok * h + x + e, r))
+                                                                    << 16)
+                                                  : 0.f;
                     if constexpr (kMode == kGrad) Rp[x + e] = v;
                     R[x + e] = bb[e] * v;
                 }
@@ -449,13 +454,11 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 R[x + 1] = fmaf(-b.y, __uint_as_float(w[x + 1]), R[x + 1]);
                 R[x + 2] = fmaf(-b.z, __uint_as_float(w[x + 2]), R[x + 2]);
                 R[x + 3] = fmaf(-b.w, __uint_as_float(w[x + 3]), R[x + 3]);
-                split2(R[x], R[x + 1], hi[x / 2], lo[x / 2]);
-                split2(R[x + 2], R[x + 3], hi[x / 2 + 1], lo[x / 2 + 1]);
             }
-            st(lb + T::R + kTok / 2 * h, hi);
-            st(lb + T::R + 32 + kTok / 2 * h, lo);
-            tmem_st_wait();
-            arrive(&bar->r_ready);
+            put_hi(lb + T::R + kTok / 2 * h, R, hi);
+            arrive(&bar->r_hi);
+            put_lo(lb + T::R + 32 + kTok / 2 * h, R, hi);
+            arrive(&bar->r_lo);
             if constexpr (kMode == kGrad) {
 #pragma unroll
                 for (int x = 0; x < kTok; x += 4) {
@@ -469,6 +472,7 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             if (kMode == kOut && i > 0) output(i - 1);
             wait(&bar->x_done, ph);
             {
+                float u[kTok];  // tail u
                 uint32_t w2[kTok];
                 ld(lb + T::X + kTok * h, w);
                 ld(lb + T::X + kC + kTok * h, w2);
@@ -477,22 +481,21 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 for (int x = 0; x < kTok; x += 4) {
                     const float4 tb = gate(kTb, x), tl = gate(kTail, x);
                     const float tbv[4] = {tb.x, tb.y, tb.z, tb.w}, tlv[4] = {tl.x, tl.y, tl.z, tl.w};
-                    float u[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float d = __uint_as_float(w[x + e]) + __uint_as_float(w2[x + e]);
                         w[x + e] = __float_as_uint(d);
-                        u[e] = fmaf(tbv[e], d, tlv[e] * R[x + e]);
+                        u[x + e] = fmaf(tbv[e], d, tlv[e] * R[x + e]);
                     }
-                    split2(u[0], u[1], hi[x / 2], lo[x / 2]);
-                    split2(u[2], u[3], hi[x / 2 + 1], lo[x / 2 + 1]);
                 }
+                put_hi(lb + T::R + kTok / 2 * h, u, hi);
+                arrive(&bar->u_hi);
+                put_lo(lb + T::R + 32 + kTok / 2 * h, u, hi);
+                arrive(&bar->u_lo);
             }
-            st(lb + T::R + kTok / 2 * h, hi);
-            st(lb + T::R + 32 + kTok / 2 * h, lo);
-            tmem_st_wait();
-            arrive(&bar->u_ready);
             if constexpr (kMode == kOut) {
+                // u for the outputs (its columns are free: the previous chunk's output was read)
+                uint32_t lo[kTok / 2];
 #pragma unroll
                 for (int x = 0; x < kTok; x += 4) {
                     const float4 b = gate(kBeta, x);
@@ -546,8 +549,8 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 for (int x = 0; x < kSc; ++x) S[x] = fmaf(gc, S[x], __uint_as_float(d[x]));
             }
             put_state();
-            if constexpr (kMode == kOut) {
-                ld(lb + T::O + kTok * h, w);  // S Q^T is complete: it was issued before dS
+            if constexpr (kMode == kOut) {  // S Q^T (complete: issued before dS) scaled in place, the second columns cleared
+                ld(lb + T::O + kTok * h, w);
                 tmem_ld_wait();
 #pragma unroll
                 for (int x = 0; x < kTok; x += 4) {
@@ -558,6 +561,9 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     w[x + 3] = __float_as_uint(g.w * __uint_as_float(w[x + 3]));
                 }
                 st(lb + T::O + kTok * h, w);
+#pragma unroll
+                for (int x = 0; x < kTok; ++x) w[x] = 0u;
+                st(lb + T::O + kC + kTok * h, w);
                 tmem_st_wait();
                 arrive(&bar->o_ready);
             }

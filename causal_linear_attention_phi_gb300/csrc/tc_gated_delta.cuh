@@ -124,6 +124,24 @@ __device__ __forceinline__ void st(uint32_t a, const uint32_t (&r)[N]) {
 }
 
 
+// What is formed for a product goes to TMEM hi parts first, with a signal of their own: the products of the hi parts run
+// while the lo parts are formed.  put_hi leaves the packed hi parts for put_lo.
+template <int N>
+__device__ __forceinline__ void put_hi(uint32_t a, const float (&v)[N], uint32_t (&hi)[N / 2]) {
+#pragma unroll
+    for (int x = 0; x < N / 2; ++x) hi[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
+    st(a, hi);
+    tmem_st_wait();
+}
+template <int N>
+__device__ __forceinline__ void put_lo(uint32_t a, const float (&v)[N], const uint32_t (&hi)[N / 2]) {
+    uint32_t lo[N / 2];
+#pragma unroll
+    for (int x = 0; x < N / 2; ++x) lo[x] = pack_bf16x2(v[2 * x] - bf_lo(hi[x]), v[2 * x + 1] - bf_hi(hi[x]));
+    st(a, lo);
+    tmem_st_wait();
+}
+
 template <typename K>
 cudaError_t allow_smem(K kern, size_t bytes) {
     return cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);

@@ -26,7 +26,7 @@ using namespace tcgd;
 // ------------------------------------------------------------------ the adjoint recurrence
 struct __align__(8) RBars {
     uint64_t full[2], empty[2];
-    uint64_t s_ready, a_done, g_ready, b_ready, y_done, r_ready, s_done, final_mma;
+    uint64_t s_hi, s_lo, a_done, g_ready, b_hi, b_lo, y_done, r_hi, r_lo, s_done, final_mma;
 };
 
 template <int D>
@@ -74,12 +74,15 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         mbar_init(&bar->full[1], 1);
         mbar_init(&bar->empty[0], 1 + kWarps);
         mbar_init(&bar->empty[1], 1 + kWarps);
-        mbar_init(&bar->s_ready, kWarps);
+        mbar_init(&bar->s_hi, kWarps);
+        mbar_init(&bar->s_lo, kWarps);
         mbar_init(&bar->a_done, 1);
         mbar_init(&bar->g_ready, kWarps);
-        mbar_init(&bar->b_ready, kWarps);
+        mbar_init(&bar->b_hi, kWarps);
+        mbar_init(&bar->b_lo, kWarps);
         mbar_init(&bar->y_done, 1);
-        mbar_init(&bar->r_ready, kWarps);
+        mbar_init(&bar->r_hi, kWarps);
+        mbar_init(&bar->r_lo, kWarps);
         mbar_init(&bar->s_done, 1);
         mbar_init(&bar->final_mma, 1);
         fence_mbar_init();
@@ -134,17 +137,18 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             const uint32_t dK = tile_desc(sg + L::K), dKmn = tile_desc<kBlk>(sg + L::K), dQmn = tile_desc<kBlk>(sg + L::Q);
             const uint32_t dO = tile_desc<kBlk>(sg + L::dO), dM = tile_desc<kBlk>(sg + L::mats);
             wait(&bar->full[s], (i >> 1) & 1);
-            if (i > 0) wait(&bar->r_ready, ph ^ 1);  // Y, over A1 and A2, has been read
+            if (i > 0) wait(&bar->r_lo, ph ^ 1);  // Y, over A1 and A2, has been read
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // dO^T P
                 mma_ss1(lead, tmem + T::A2, dO + step_mn(kk), dM + (kPHi >> 4) + step_mn(kk), id_amn, kk > 0);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
                 mma_ss1(lead, tmem + T::A2, dO + step_mn(kk), dM + (kPLo >> 4) + step_mn(kk), id_amn, 1);
-            wait(&bar->s_ready, ph);
+            wait(&bar->s_hi, ph);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)  // dS'^T K^T
                 mma_ts1(lead, tmem + T::A1, tmem + T::SHi + 8 * kk, dK + step_k(kk), id_k, kk > 0);
+            wait(&bar->s_lo, ph);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
                 mma_ts1(lead, tmem + T::A1, tmem + T::SLo + 8 * kk, dK + step_k(kk), id_k, 1);
@@ -156,18 +160,20 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
                 mma_ts1(lead, tmem + T::dS, tmem + T::G + 32 + 8 * kk, dQmn + step_mn(kk), id_mnD, 1);
-            wait(&bar->b_ready, ph);
+            wait(&bar->b_hi, ph);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // (beta dU)_hi^T [t_hi | t_lo]: two products of 64 columns
                 mma_ts1(lead, tmem + T::Y, tmem + T::B + 8 * kk, dM + step_mn(kk), id_mn2, kk > 0);
+            wait(&bar->b_lo, ph);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
                 mma_ts1(lead, tmem + T::Y, tmem + T::B + 32 + 8 * kk, dM + step_mn(kk), id_mn, 1);
             commit1(lead, &bar->y_done);
-            wait(&bar->r_ready, ph);
+            wait(&bar->r_hi, ph);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // -(beta gam Y)^T K
                 mma_ts1(lead, tmem + T::dS, tmem + T::B + 8 * kk, dKmn + step_mn(kk), id_mnD, 1);
+            wait(&bar->r_lo, ph);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
                 mma_ts1(lead, tmem + T::dS, tmem + T::B + 32 + 8 * kk, dKmn + step_mn(kk), id_mnD, 1);
@@ -205,13 +211,11 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             const float* gates = reinterpret_cast<const float*>(sg + L::gates);
             auto gate = [&](int which, int x) { return ld_f4(gates + which + kTok * h + x); };
             {  // the state gradient's parts, and the signal that they are there
-                uint32_t hi[kSc / 2], lo[kSc / 2];
-#pragma unroll
-                for (int x = 0; x < kSc / 2; ++x) split2(S[2 * x], S[2 * x + 1], hi[x], lo[x]);
-                st(lb + T::SHi + kSc / 2 * h, hi);
-                st(lb + T::SLo + kSc / 2 * h, lo);
-                tmem_st_wait();
-                arrive(&bar->s_ready);
+                uint32_t hi[kSc / 2];
+                put_hi(lb + T::SHi + kSc / 2 * h, S, hi);
+                arrive(&bar->s_hi);
+                put_lo(lb + T::SLo + kSc / 2 * h, S, hi);
+                arrive(&bar->s_lo);
                 if constexpr (!kSums) {  // its tile: the gradient leaving this chunk
                     if (ct == 0) bulk_wait_read_all();
                     named_barrier(1, 32 * kWarps);
@@ -231,8 +235,10 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     }
                 }
             }
-            uint32_t w[kTok], hi[kTok / 2], lo[kTok / 2];
+            uint32_t w[kTok], hi[kTok / 2];
             wait(&bar->full[s], (i >> 1) & 1);
+            {
+            uint32_t lo[kTok / 2];
 #pragma unroll
             for (int x = 0; x < kTok; x += 4) {
                 const float4 g = gate(kGam, x);
@@ -251,48 +257,52 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             st(lb + T::G + 32 + kTok / 2 * h, lo);
             tmem_st_wait();
             arrive(&bar->g_ready);
+            }
             float dU[kTok];
             wait(&bar->a_done, ph);
             {
+                float b[kTok];
                 uint32_t w2[kTok];
                 ld(lb + T::A1 + kTok * h, w);
                 ld(lb + T::A2 + kTok * h, w2);
                 tmem_ld_wait();
 #pragma unroll
                 for (int x = 0; x < kTok; x += 4) {
-                    const float4 t = gate(kTail, x), b = gate(kBeta, x);
-                    const float tt[4] = {t.x, t.y, t.z, t.w};
+                    const float4 t = gate(kTail, x), be = gate(kBeta, x);
+                    const float tt[4] = {t.x, t.y, t.z, t.w}, bv[4] = {be.x, be.y, be.z, be.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < 4; ++e) {
                         dU[x + e] = fmaf(tt[e], __uint_as_float(w[x + e]), __uint_as_float(w2[x + e]));
-                    split2(b.x * dU[x], b.y * dU[x + 1], hi[x / 2], lo[x / 2]);
-                    split2(b.z * dU[x + 2], b.w * dU[x + 3], hi[x / 2 + 1], lo[x / 2 + 1]);
+                        b[x + e] = bv[e] * dU[x + e];
+                    }
                 }
+                put_hi(lb + T::B + kTok / 2 * h, b, hi);
+                arrive(&bar->b_hi);
+                put_lo(lb + T::B + 32 + kTok / 2 * h, b, hi);
+                arrive(&bar->b_lo);
             }
-            st(lb + T::B + kTok / 2 * h, hi);
-            st(lb + T::B + 32 + kTok / 2 * h, lo);
-            tmem_st_wait();
-            arrive(&bar->b_ready);
             wait(&bar->y_done, ph);
             {
+                float b[kTok];
                 uint32_t w2[kTok];
                 ld(lb + T::Y + kTok * h, w);
                 ld(lb + T::Y + kC + kTok * h, w2);
                 tmem_ld_wait();
 #pragma unroll
                 for (int x = 0; x < kTok; x += 4) {
-                    const float4 b = gate(kBg, x);
+                    const float4 bg = gate(kBg, x);
+                    const float bv[4] = {bg.x, bg.y, bg.z, bg.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < 4; ++e) {
                         dU[x + e] += __uint_as_float(w[x + e]) + __uint_as_float(w2[x + e]);  // Y
-                    split2(-b.x * dU[x], -b.y * dU[x + 1], hi[x / 2], lo[x / 2]);
-                    split2(-b.z * dU[x + 2], -b.w * dU[x + 3], hi[x / 2 + 1], lo[x / 2 + 1]);
+                        b[x + e] = -bv[e] * dU[x + e];
+                    }
                 }
+                put_hi(lb + T::B + kTok / 2 * h, b, hi);
+                arrive(&bar->r_hi);
+                put_lo(lb + T::B + 32 + kTok / 2 * h, b, hi);
+                arrive(&bar->r_lo);
             }
-            st(lb + T::B + kTok / 2 * h, hi);
-            st(lb + T::B + 32 + kTok / 2 * h, lo);
-            tmem_st_wait();
-            arrive(&bar->r_ready);
             const float gc = gates[kGam + kC - 1];
             if constexpr (!kSums) {
                 // dV's tile [positions][value columns] and Y's [value columns][positions]

@@ -188,7 +188,7 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 // ------------------------------------------------------------------ the recurrence
 struct __align__(8) Bars {
     uint64_t full[2], empty[2];
-    uint64_t s_hi, s_lo, y_done, r_hi, r_lo, x_done, u_hi, u_lo, s_done, o_ready, o_done, o_free, final_mma;
+    uint64_t s_hi, s_lo, y_done, r_hi, r_lo, x_done, u_ready, s_done, o_ready, o_done, o_free, final_mma;
 };
 
 template <int D, int kMode>
@@ -198,9 +198,9 @@ struct FwdSmem {
     static constexpr int K = 0, V = tile, mats = 2 * tile, Q = mats + nmats, gates = Q + (kMode == kOut ? tile : 0);
     static constexpr int stage = gates + 2048;
     static_assert(kGateBytes <= 2048, "gates");
-    static constexpr int out = 2 * stage;  // kOut: the o tile; kGrad: the state's tile and X lo, X hi
+    static constexpr int out = 2 * stage;  // kGrad: the state's tile and X lo, X hi
     static constexpr int sbytes = D * D * 2, xbytes = 2 * D * 128;
-    static constexpr int bars = out + (kMode == kOut ? tile : kMode == kGrad ? sbytes + xbytes : 0);
+    static constexpr int bars = out + (kMode == kGrad ? sbytes + xbytes : 0);
     static constexpr int slot = bars + 256;
     static constexpr int total = slot + 16;
     static constexpr size_t bytes = total + 1024;
@@ -228,7 +228,7 @@ __device__ __forceinline__ int map_at(int row, int c) {
 template <int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, StateArgs a, int* err) {
+             const __grid_constant__ CUtensorMap tm_v, StateArgs a, int* err) {
     using L = FwdSmem<D, kMode>;
     using T = Tm<D>;
     constexpr int kSc = D / kHs;  // state columns of a thread
@@ -253,8 +253,7 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         mbar_init(&bar->r_hi, kWarps);
         mbar_init(&bar->r_lo, kWarps);
         mbar_init(&bar->x_done, 1);
-        mbar_init(&bar->u_hi, kWarps);
-        mbar_init(&bar->u_lo, kWarps);
+        mbar_init(&bar->u_ready, kWarps);
         mbar_init(&bar->s_done, 1);
         mbar_init(&bar->o_ready, kWarps);
         mbar_init(&bar->o_done, 1);
@@ -264,7 +263,6 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
         tma_prefetch_desc(&tm_q);
-        tma_prefetch_desc(&tm_o);
     }
     const uint32_t tmem = enter(slot, 512, warp);
 
@@ -349,11 +347,10 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     for (int kk = 0; kk < D / 16; ++kk)
                         mma_ts1(lead, tmem + T::O, tmem + T::SHi + 8 * kk, dQ + step_k(kk), id_k, kk > 0);
                 }
-                wait(&bar->u_hi, ph);
+                wait(&bar->u_ready, ph);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)  // the chunk's writes (tail u) K
                     mma_ts1(lead, tmem + T::dS, tmem + T::R + 8 * kk, dKmn + step_mn(kk), id_mn, kk > 0);
-                wait(&bar->u_lo, ph);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_ts1(lead, tmem + T::dS, tmem + T::R + 32 + 8 * kk, dKmn + step_mn(kk), id_mn, 1);
@@ -395,29 +392,21 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             arrive(&bar->s_lo);
         };
         put_state();
-        uint8_t* sO = base + L::out;
-        auto output = [&](int j) {  // o of chunk j
-            // the tile is free once the previous store has read it
-            if (ct == 0) bulk_wait_read_all();
-            named_barrier(1, 32 * kWarps);
+        // o of chunk j: a warp's store of a position is 64 contiguous bytes (staged for a TMA store it took two
+        // barriers of all compute warps in the chain of chunks)
+        auto output = [&](int j) {
             wait(&bar->o_done, j & 1);
             uint32_t w[kTok], w2[kTok];
             ld(lb + T::O + kTok * h, w);
             ld(lb + T::O + kC + kTok * h, w2);
             tmem_ld_wait();
             arrive(&bar->o_free);
+            const int t0 = (cbeg + j) * kC + kTok * h, n = a.N - t0;
+            __nv_bfloat16* o = a.o + ((size_t)bh * a.N + t0) * D + r;
             if (r < D) {
 #pragma unroll
                 for (int x = 0; x < kTok; ++x)
-                    *reinterpret_cast<__nv_bfloat16*>(sO + elem_off(kTok * h + x, r)) =
-                        __float2bfloat16_rn(__uint_as_float(w[x]) + __uint_as_float(w2[x]));
-            }
-            fence_proxy_async_smem();
-            named_barrier(1, 32 * kWarps);
-            if (ct == 0) {
-#pragma unroll
-                for (int b = 0; b < D / 64; ++b) tma_store_3d(&tm_o, sO + b * kBlk, 64 * b, (cbeg + j) * kC, bh);
-                bulk_commit();
+                    if (x < n) o[x * D] = __float2bfloat16_rn(__uint_as_float(w[x]) + __uint_as_float(w2[x]));
             }
         };
         for (int i = 0; i < nloc; ++i) {
@@ -471,39 +460,34 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             }
             if (kMode == kOut && i > 0) output(i - 1);
             wait(&bar->x_done, ph);
+            uint32_t lo[kTok / 2];
             {
-                float u[kTok];  // tail u
                 uint32_t w2[kTok];
                 ld(lb + T::X + kTok * h, w);
                 ld(lb + T::X + kC + kTok * h, w2);
                 tmem_ld_wait();
 #pragma unroll
                 for (int x = 0; x < kTok; x += 4) {
-                    const float4 tb = gate(kTb, x), tl = gate(kTail, x);
-                    const float tbv[4] = {tb.x, tb.y, tb.z, tb.w}, tlv[4] = {tl.x, tl.y, tl.z, tl.w};
+                    const float4 b = gate(kBeta, x), tl = gate(kTail, x);
+                    const float bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float d = __uint_as_float(w[x + e]) + __uint_as_float(w2[x + e]);
-                        w[x + e] = __float_as_uint(d);
-                        u[x + e] = fmaf(tbv[e], d, tlv[e] * R[x + e]);
+                        if constexpr (kMode == kGrad) Rp[x + e] += d;
+                        R[x + e] = fmaf(bv[e], d, R[x + e]);  // u
                     }
+                    split2(tl.x * R[x], tl.y * R[x + 1], hi[x / 2], lo[x / 2]);
+                    split2(tl.z * R[x + 2], tl.w * R[x + 3], hi[x / 2 + 1], lo[x / 2 + 1]);
                 }
-                put_hi(lb + T::R + kTok / 2 * h, u, hi);
-                arrive(&bar->u_hi);
-                put_lo(lb + T::R + 32 + kTok / 2 * h, u, hi);
-                arrive(&bar->u_lo);
             }
+            st(lb + T::R + kTok / 2 * h, hi);
+            st(lb + T::R + 32 + kTok / 2 * h, lo);
+            tmem_st_wait();
+            arrive(&bar->u_ready);
             if constexpr (kMode == kOut) {
                 // u for the outputs (its columns are free: the previous chunk's output was read)
-                uint32_t lo[kTok / 2];
 #pragma unroll
-                for (int x = 0; x < kTok; x += 4) {
-                    const float4 b = gate(kBeta, x);
-                    split2(fmaf(b.x, __uint_as_float(w[x]), R[x]), fmaf(b.y, __uint_as_float(w[x + 1]), R[x + 1]),
-                           hi[x / 2], lo[x / 2]);
-                    split2(fmaf(b.z, __uint_as_float(w[x + 2]), R[x + 2]),
-                           fmaf(b.w, __uint_as_float(w[x + 3]), R[x + 3]), hi[x / 2 + 1], lo[x / 2 + 1]);
-                }
+                for (int x = 0; x < kTok; x += 2) split2(R[x], R[x + 1], hi[x / 2], lo[x / 2]);
                 st(lb + T::U + kTok / 2 * h, hi);
                 st(lb + T::U + 32 + kTok / 2 * h, lo);
             } else if constexpr (kMode == kGrad) {  // this thread's row of the state's tile (the state entering the chunk) and of X's tiles
@@ -521,10 +505,10 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll
                     for (int x = 0; x < kTok; x += 8) {
                         uint4 a, b;
-                        split2(Rp[x] + __uint_as_float(w[x]), Rp[x + 1] + __uint_as_float(w[x + 1]), a.x, b.x);
-                        split2(Rp[x + 2] + __uint_as_float(w[x + 2]), Rp[x + 3] + __uint_as_float(w[x + 3]), a.y, b.y);
-                        split2(Rp[x + 4] + __uint_as_float(w[x + 4]), Rp[x + 5] + __uint_as_float(w[x + 5]), a.z, b.z);
-                        split2(Rp[x + 6] + __uint_as_float(w[x + 6]), Rp[x + 7] + __uint_as_float(w[x + 7]), a.w, b.w);
+                        split2(Rp[x], Rp[x + 1], a.x, b.x);
+                        split2(Rp[x + 2], Rp[x + 3], a.y, b.y);
+                        split2(Rp[x + 4], Rp[x + 5], a.z, b.z);
+                        split2(Rp[x + 6], Rp[x + 7], a.w, b.w);
                         const int off = row_off(r, (kTok * h + x) >> 3);
                         *reinterpret_cast<uint4*>(sX + off) = b;
                         *reinterpret_cast<uint4*>(sX + D * 128 + off) = a;
@@ -716,7 +700,7 @@ template cudaError_t prepare<128>(const CUtensorMap&, const CUtensorMap&, const 
                                   const la_shape&, int, int*, cudaStream_t);
 
 template <int D>
-cudaError_t states(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
+cudaError_t states(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const StateArgs& a, Mode mode, int BH, int segments, int* err, cudaStream_t st) {
     auto kern = mode == kOut ? tc_gd_states<D, kOut> : mode == kGrad ? tc_gd_states<D, kGrad> : tc_gd_states<D, kSum>;
     const size_t smem = mode == kOut    ? FwdSmem<D, kOut>::bytes
@@ -726,7 +710,7 @@ cudaError_t states(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
     const char* name = mode == kOut ? "tc_gd_states" : mode == kGrad ? "tc_gd_states_grad" : "tc_gd_segments";
     launch_begin(name, st);
     const cudaError_t e = launch_pdl(kern, dim3(segments, BH, mode == kSum && D == 128 ? 2 : 1), dim3(kThreads), smem, st,
-                                     tq, tk, tv, to, a, err);
+                                     tq, tk, tv, a, err);
     const cudaError_t e2 = launch_end(name, st);
     return e != cudaSuccess ? e : e2;
 }
@@ -745,8 +729,8 @@ cudaError_t join(const float* B, const float* Mx, const float* first, float* out
 }
 
 #define GD_INSTANCE(D)                                                                                              \
-    template cudaError_t states<D>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, \
-                                   const StateArgs&, Mode, int, int, int*, cudaStream_t);                          \
+    template cudaError_t states<D>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const StateArgs&,    \
+                                   Mode, int, int, int*, cudaStream_t);                                            \
     template cudaError_t join<D>(const float*, const float*, const float*, float*, int, int, bool, int*, cudaStream_t);
 GD_INSTANCE(64)
 GD_INSTANCE(128)
@@ -759,9 +743,9 @@ namespace {
 template <int D>
 cudaError_t fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) {
     const int BH = s.B * s.H, M = (s.N + kC - 1) / kC;
-    CUtensorMap tq, tk, tv, to;
+    CUtensorMap tq, tk, tv;
     if (!make_tmap_bf16_rows(&tq, a.q, BH, s.N, D, kC) || !make_tmap_bf16_rows(&tk, a.k, BH, s.N, D, kC) ||
-        !make_tmap_bf16_rows(&tv, a.v, BH, s.N, D, kC) || !make_tmap_bf16_rows(&to, a.o, BH, s.N, D, kC))
+        !make_tmap_bf16_rows(&tv, a.v, BH, s.N, D, kC))
         return cudaErrorInvalidValue;
     int* err = device_error_word();
     const Layout L = layout(s, false);
@@ -779,14 +763,16 @@ cudaError_t fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
         sa.segB = B;
         sa.segM = Mx;
         sa.nsum = L.segs - 1;
-        GD_TRY(states<D>(tq, tk, tv, to, sa, kSum, BH, L.segs - 1, err, st));
+        GD_TRY(states<D>(tq, tk, tv, sa, kSum, BH, L.segs - 1, err, st));
         GD_TRY(join<D>(B, Mx, a.S0, S, BH, L.segs, false, err, st));
         sa.S0 = S;
     } else {
         sa.S0 = a.S0;
     }
     sa.S_out = a.S;
-    return states<D>(tq, tk, tv, to, sa, kOut, BH, L.segs, err, st);
+    sa.o = (__nv_bfloat16*)a.o;
+    sa.N = s.N;
+    return states<D>(tq, tk, tv, sa, kOut, BH, L.segs, err, st);
 }
 
 }  // namespace

@@ -166,13 +166,15 @@ struct StateArgs {
     const uint8_t* mats;
     const float* S0;   // [BH][P] records: the states entering the segments; null: zero
     float* S_out;      // kOut: [BH] records, the state after the last position, or null
+    __nv_bfloat16* o;  // kOut: [BH][N][D]
+    int N;
     uint8_t *x_tiles, *s_tiles;   // kGrad
     float *segB, *segM;           // kSum: [BH][P] records
     int M, P, cps;                // chunks, segments, chunks of a segment
     int nsum;                     // kSum: segments whose B is wanted (the first nsum)
 };
 template <int D>
-cudaError_t states(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
+cudaError_t states(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const StateArgs& a, Mode mode, int BH, int segments, int* err, cudaStream_t st);
 // Joins the segments' sums: out[p + 1] = B[p] + M[p] out[p] from out[0] = first (or zero); reverse: out[P - 1] = 0,
 // out[p - 1] = B[p] + M[p]^T out[p].

@@ -812,14 +812,14 @@ cudaError_t bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
         sa.segB = (float*)(ws + L.segB);
         sa.segM = (float*)(ws + L.segM);
         sa.nsum = L.segs - 1;  // the maps of all segments are wanted: the first for the states, the last for their gradients
-        GD_TRY(states<D>(tq, tk, tv, tv, sa, kSum, BH, L.segs, err, st));
+        GD_TRY(states<D>(tq, tk, tv, sa, kSum, BH, L.segs, err, st));
         GD_TRY(reverse(true, nullptr, (float*)(ws + L.segB2)));
         GD_TRY(join<D>(sa.segB, sa.segM, nullptr, (float*)(ws + L.segS), BH, L.segs, false, err, st));
         GD_TRY(join<D>((float*)(ws + L.segB2), sa.segM, nullptr, (float*)(ws + L.segdS), BH, L.segs, true, err, st));
         sa.S0 = (float*)(ws + L.segS);
         segdS = (float*)(ws + L.segdS);
     }
-    GD_TRY(states<D>(tq, tk, tv, tv, sa, kGrad, BH, L.segs, err, st));
+    GD_TRY(states<D>(tq, tk, tv, sa, kGrad, BH, L.segs, err, st));
     GD_TRY(reverse(false, segdS, nullptr));
     GD_TRY(allow_smem(tc_gd_grads<D>, GradSmem<D>::bytes));
     launch_begin("tc_gd_grads", st);

@@ -188,7 +188,7 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 // ------------------------------------------------------------------ the recurrence
 struct __align__(8) Bars {
     uint64_t full[2], empty[2];
-    uint64_t s_hi, s_lo, y_done, r_hi, r_lo, x_done, u_ready, s_done, o_ready, o_done, o_free, final_mma;
+    uint64_t s_hi, s_lo, y_done, r_hi, r_lo, x_done, u_hi, u_lo, s_done, o_ready, o_done, o_free, final_mma;
 };
 
 template <int D, int kMode>
@@ -253,7 +253,8 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         mbar_init(&bar->r_hi, kWarps);
         mbar_init(&bar->r_lo, kWarps);
         mbar_init(&bar->x_done, 1);
-        mbar_init(&bar->u_ready, kWarps);
+        mbar_init(&bar->u_hi, kWarps);
+        mbar_init(&bar->u_lo, kWarps);
         mbar_init(&bar->s_done, 1);
         mbar_init(&bar->o_ready, kWarps);
         mbar_init(&bar->o_done, 1);
@@ -347,10 +348,11 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     for (int kk = 0; kk < D / 16; ++kk)
                         mma_ts1(lead, tmem + T::O, tmem + T::SHi + 8 * kk, dQ + step_k(kk), id_k, kk > 0);
                 }
-                wait(&bar->u_ready, ph);
+                wait(&bar->u_hi, ph);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)  // the chunk's writes (tail u) K
                     mma_ts1(lead, tmem + T::dS, tmem + T::R + 8 * kk, dKmn + step_mn(kk), id_mn, kk > 0);
+                wait(&bar->u_lo, ph);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_ts1(lead, tmem + T::dS, tmem + T::R + 32 + 8 * kk, dKmn + step_mn(kk), id_mn, 1);
@@ -476,14 +478,23 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         if constexpr (kMode == kGrad) Rp[x + e] += d;
                         R[x + e] = fmaf(bv[e], d, R[x + e]);  // u
                     }
-                    split2(tl.x * R[x], tl.y * R[x + 1], hi[x / 2], lo[x / 2]);
-                    split2(tl.z * R[x + 2], tl.w * R[x + 3], hi[x / 2 + 1], lo[x / 2 + 1]);
+                    hi[x / 2] = pack_bf16x2(tl.x * R[x], tl.y * R[x + 1]);
+                    hi[x / 2 + 1] = pack_bf16x2(tl.z * R[x + 2], tl.w * R[x + 3]);
                 }
             }
             st(lb + T::R + kTok / 2 * h, hi);
+            tmem_st_wait();
+            arrive(&bar->u_hi);
+#pragma unroll
+            for (int x = 0; x < kTok; x += 4) {
+                const float4 tl = gate(kTail, x);
+                lo[x / 2] = pack_bf16x2(fmaf(tl.x, R[x], -bf_lo(hi[x / 2])), fmaf(tl.y, R[x + 1], -bf_hi(hi[x / 2])));
+                lo[x / 2 + 1] =
+                    pack_bf16x2(fmaf(tl.z, R[x + 2], -bf_lo(hi[x / 2 + 1])), fmaf(tl.w, R[x + 3], -bf_hi(hi[x / 2 + 1])));
+            }
             st(lb + T::R + 32 + kTok / 2 * h, lo);
             tmem_st_wait();
-            arrive(&bar->u_ready);
+            arrive(&bar->u_lo);
             if constexpr (kMode == kOut) {
                 // u for the outputs (its columns are free: the previous chunk's output was read)
 #pragma unroll

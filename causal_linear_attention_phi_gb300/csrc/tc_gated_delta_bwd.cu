@@ -415,8 +415,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
             const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dq,
-            const __grid_constant__ CUtensorMap tm_dk, const __nv_bfloat16* __restrict__ g,
-            const float* __restrict__ recs, const uint8_t* __restrict__ x_tiles, const uint8_t* __restrict__ y_tiles,
+            const __grid_constant__ CUtensorMap tm_dk, const float* __restrict__ recs, const uint8_t* __restrict__ x_tiles, const uint8_t* __restrict__ y_tiles,
             const uint8_t* __restrict__ s_tiles, const uint8_t* __restrict__ ds_tiles, __nv_bfloat16* __restrict__ dg,
             __nv_bfloat16* __restrict__ dbeta, int N, int M, int total, int* err) {
     using L = GradSmem<D>;
@@ -723,16 +722,16 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 }
                 bulk_commit();
             }
-            if (warp == 3) {  // dg: the reverse cumulative sum, in fp64 (its terms cancel); two positions to a lane
-                double v[2];
+            if (warp == 3) {  // dg: the reverse cumulative sum, two positions to a lane (fp32: the result is bf16)
+                float v[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int j = 2 * lane + e;
-                    double a = 0.0;
+                    float a = 0.f;
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
-                        a += (double)((part[L::pRow + y * 128 + j] + part[L::pRow + y * 128 + kC + j]) +
-                                      (part[L::pCol + y * kC + j] + part[L::pTok + y * kC + j]));
+                        a += (part[L::pRow + y * 128 + j] + part[L::pRow + y * 128 + kC + j]) +
+                             (part[L::pCol + y * kC + j] + part[L::pTok + y * kC + j]);
                     v[e] = a;
                 }
                 float tail = part[L::pSum + kWarps + (lane & (kWarps - 1))], os = part[L::pSum + (lane & (kWarps - 1))];
@@ -741,22 +740,23 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     tail += __shfl_xor_sync(0xffffffffu, tail, o);
                     os += __shfl_xor_sync(0xffffffffu, os, o);
                 }
-                const double all = (double)tail * (double)rec[kGam + kC - 1] + (double)os;
-                const double both = v[0] + v[1];
-                double run = both;
+                const float all = fmaf(tail, rec[kGam + kC - 1], os);
+                const float both = v[0] + v[1];
+                float run = both;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const double x = __shfl_down_sync(0xffffffffu, run, o);
+                    const float x = __shfl_down_sync(0xffffffffu, run, o);
                     if (lane + o < 32) run += x;
                 }
-                const double after = run - both;
+                const float after = run - both;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int j = 2 * lane + e;
                     if (j >= n) continue;
                     const size_t pos = (size_t)bh * N + c0 + j;
-                    const double d = after + (e ? v[1] : both) + all;
-                    dg[pos] = __float2bfloat16_rn(__bfloat162float(g[pos]) < kReset ? 0.f : (float)d);
+                    // a reset is where the count of resets goes up
+                    const bool reset = rec[kSeg + j] != (j > 0 ? rec[kSeg + j - 1] : 0.f);
+                    dg[pos] = __float2bfloat16_rn(reset ? 0.f : after + (e ? v[1] : both) + all);
                     dbeta[pos] = __float2bfloat16_rn(part[L::dBeta + j]);
                 }
             }
@@ -825,7 +825,7 @@ cudaError_t bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
     launch_begin("tc_gd_grads", st);
     const int total = BH * M;
     const cudaError_t e = launch_pdl(tc_gd_grads<D>, dim3(total < 152 ? total : 152), dim3(kThreads), GradSmem<D>::bytes, st, tq, tk, tdo, tdq, tdk,
-                   (const __nv_bfloat16*)a.g, (const float*)recs, (const uint8_t*)X, (const uint8_t*)Y,
+                   (const float*)recs, (const uint8_t*)X, (const uint8_t*)Y,
                    (const uint8_t*)S, (const uint8_t*)dS, (__nv_bfloat16*)a.dg, (__nv_bfloat16*)a.dbeta, s.N, M, total, err);
     const cudaError_t e2 = launch_end("tc_gd_grads", st);
     return e != cudaSuccess ? e : e2;

@@ -747,7 +747,7 @@ la_status la_layer_norm_fwd(const void* x, const void* w, const void* b, void* y
 
 size_t la_layer_norm_workspace_bytes(la_norm_shape s) {
     if (check_norm(s) != LA_OK || s.rows == 0) return 0;
-    return align256((size_t)ln::bwd_blocks(s.rows, s.C) * 2 * s.C * sizeof(float));
+    return align256((size_t)ln::bwd_blocks(s) * 2 * s.C * sizeof(float));
 }
 
 la_status la_layer_norm_bwd(const void* x, const void* w, const float* mean, const float* rstd, const void* dy,

@@ -9,7 +9,7 @@ namespace ln {
 constexpr int kMaxC = 16384;  // a row is held in the registers of at most 1024 threads, 16 elements each
 
 // Blocks of the gradient kernel, i.e. partial (dw, db) records of 2 C floats in the workspace.
-int bwd_blocks(long long rows, int C);
+int bwd_blocks(const la_norm_shape& s);
 // w, b, mean, rstd may be null.
 cudaError_t fwd(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd, const la_norm_shape& s,
                 float eps, cudaStream_t st);

@@ -200,10 +200,10 @@ ln_bwd_kernel(const T* x, const T* __restrict__ w, const float* __restrict__ mea
 }
 
 // ------------------------------------------------------------------ streamed rows (16-byte vectors divide a row)
-// Rows are contiguous, so a tile of them is one bulk copy.  A block keeps kStages tiles in flight in shared memory, which
+// Rows are contiguous, so a tile of them is one bulk copy.  A block keeps two or three tiles in flight in shared memory, which
 // is what it takes to keep the memory busy (about 50 KB an SM); rows held in registers instead, with a barrier between
 // load and use, reached 0.74 of the copy rate forward (131072 x 2048 bf16) and 0.68 in the gradient (1048576 x 128).
-constexpr int kStages = 3;
+constexpr int kFwdStages = 2, kBwdStages = 3;
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile(
@@ -307,12 +307,12 @@ ln_fwd_tiles(const T* x, const T* __restrict__ w, const T* __restrict__ b, T* y,
     using P = Pairs<T>;
     constexpr int VEC = 16 / (int)sizeof(T), kRows = kBlock / TPR;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t bar[kStages];
+    __shared__ uint64_t bar[kFwdStages];
     __shared__ float buf[kRows][2][8];
     const int tid = threadIdx.x, t = tid % TPR, sub = tid / TPR, nv = tl.C / VEC;
     const uint32_t tile = tl.row * tl.R;
     if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) sm100::mbar_init(bar + s, 1);
+        for (int s = 0; s < kFwdStages; ++s) sm100::mbar_init(bar + s, 1);
         sm100::fence_mbar_init();
     }
     __syncthreads();
@@ -321,19 +321,19 @@ ln_fwd_tiles(const T* x, const T* __restrict__ w, const T* __restrict__ b, T* y,
     auto load = [&](long long i) {  // the i-th tile of this block
         const long long k = blockIdx.x + i * gridDim.x;
         if (tid != 0 || k >= tl.tiles) return;
-        const int s = (int)(i % kStages);
+        const int s = (int)(i % kFwdStages);
         const uint32_t bytes = rows_of(k) * tl.row;
         sm100::mbar_arrive_expect_tx(bar + s, bytes);
         bulk_load(smem + s * tile, reinterpret_cast<const uint8_t*>(x) + k * tile, bytes, bar + s);
     };
-    for (int i = 0; i < kStages; ++i) load(i);
+    for (int i = 0; i < kFwdStages; ++i) load(i);
     const float inv = 1.f / (float)tl.C;
     int turn = 0;
     bool ok = true;
     long long i = 0;
     for (long long k = blockIdx.x; k < tl.tiles; k += gridDim.x, ++i) {
-        const int s = (int)(i % kStages), n = rows_of(k);
-        ok = ok && sm100::mbar_wait(bar + s, (int)(i / kStages) & 1, err, LA_ERR_TIMEOUT);
+        const int s = (int)(i % kFwdStages), n = rows_of(k);
+        ok = ok && sm100::mbar_wait(bar + s, (int)(i / kFwdStages) & 1, err, LA_ERR_TIMEOUT);
         __syncwarp();
         for (int r0 = 0; r0 < n; r0 += kRows) {
             const int r = r0 + sub;
@@ -385,7 +385,7 @@ ln_fwd_tiles(const T* x, const T* __restrict__ w, const T* __restrict__ b, T* y,
             }
         }
         __syncthreads();  // the tile has been read
-        load(i + kStages);
+        load(i + kFwdStages);
     }
 }
 
@@ -397,12 +397,12 @@ ln_bwd_tiles(const T* x, const T* __restrict__ w, const float* __restrict__ mean
     using P = Pairs<T>;
     constexpr int VEC = 16 / (int)sizeof(T), kRows = kBlock / TPR;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t bar[kStages];
+    __shared__ uint64_t bar[kBwdStages];
     __shared__ float buf[kRows][4][8];
     const int tid = threadIdx.x, t = tid % TPR, sub = tid / TPR, nv = tl.C / VEC;
     const uint32_t tile = tl.row * tl.R;
     if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) sm100::mbar_init(bar + s, 1);
+        for (int s = 0; s < kBwdStages; ++s) sm100::mbar_init(bar + s, 1);
         sm100::fence_mbar_init();
     }
     __syncthreads();
@@ -411,13 +411,13 @@ ln_bwd_tiles(const T* x, const T* __restrict__ w, const float* __restrict__ mean
     auto load = [&](long long i) {
         const long long k = blockIdx.x + i * gridDim.x;
         if (tid != 0 || k >= tl.tiles) return;
-        const int s = (int)(i % kStages);
+        const int s = (int)(i % kBwdStages);
         const uint32_t bytes = rows_of(k) * tl.row;
         sm100::mbar_arrive_expect_tx(bar + s, 2 * bytes);
         bulk_load(smem + 2 * s * tile, reinterpret_cast<const uint8_t*>(x) + k * tile, bytes, bar + s);
         bulk_load(smem + (2 * s + 1) * tile, reinterpret_cast<const uint8_t*>(dy) + k * tile, bytes, bar + s);
     };
-    for (int i = 0; i < kStages; ++i) load(i);
+    for (int i = 0; i < kBwdStages; ++i) load(i);
     float2 wv[VPT][P::n], dw[VPT][P::n], db[VPT][P::n];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -432,18 +432,31 @@ ln_bwd_tiles(const T* x, const T* __restrict__ w, const float* __restrict__ mean
     int turn = 0;
     bool ok = true;
     long long i = 0;
+    // the statistics of this thread's next row, loaded a turn ahead
+    float mu_next = 0.f, rs_next = 0.f;
+    auto stats = [&](long long k, int r) {
+        if (k < tl.tiles && r < rows_of(k)) {
+            mu_next = mean[k * tl.R + r];
+            rs_next = rstd[k * tl.R + r];
+        }
+    };
+    stats(blockIdx.x, sub);
     for (long long k = blockIdx.x; k < tl.tiles; k += gridDim.x, ++i) {
-        const int s = (int)(i % kStages), n = rows_of(k);
-        ok = ok && sm100::mbar_wait(bar + s, (int)(i / kStages) & 1, err, LA_ERR_TIMEOUT);
+        const int s = (int)(i % kBwdStages), n = rows_of(k);
+        ok = ok && sm100::mbar_wait(bar + s, (int)(i / kBwdStages) & 1, err, LA_ERR_TIMEOUT);
         __syncwarp();
         for (int r0 = 0; r0 < n; r0 += kRows) {
             const int r = r0 + sub;
             const bool in = r < n;
+            const float mu = mu_next, rs = rs_next;
+            if (r0 + kRows < n)
+                stats(k, r + kRows);
+            else
+                stats(k + gridDim.x, sub);
             if (TPR > 32 && !in) break;
             const long long row = k * tl.R + (in ? r : 0);
             const uint8_t* xr = smem + 2 * s * tile + (in ? r : 0) * tl.row;
             const uint8_t* dr = xr + tile;
-            const float mu = mean[row], rs = rstd[row];
             float2 s0 = both(0.f), s1 = s0;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
@@ -482,7 +495,7 @@ ln_bwd_tiles(const T* x, const T* __restrict__ w, const float* __restrict__ mean
             }
         }
         __syncthreads();  // the tiles have been read
-        load(i + kStages);
+        load(i + kBwdStages);
     }
     if (!part) return;
     // the rows of a block joined in shared memory (the tiles are done with), then one record per block
@@ -576,7 +589,7 @@ Tiles tiles_of(long long rows, int C, int elem, int threads, int bytes) {
     t.tiles = (rows + t.R - 1) / t.R;
     return t;
 }
-size_t tile_smem(const Tiles& t, int arrays) { return (size_t)kStages * arrays * t.row * t.R; }
+size_t tile_smem(const Tiles& t, int tiles) { return (size_t)tiles * t.row * t.R; }
 int resident(size_t smem) {
     const long long per = 225000 / (long long)(smem + 1536);
     return (int)(per < 1 ? 1 : per > 8 ? 8 : per);
@@ -589,7 +602,7 @@ int bwd_blocks(const la_norm_shape& s) {
     const int elem = s.dtype == LA_BF16 ? 2 : 4;
     if (streamed(s.C, elem, true)) {
         const Tiles t = tiles_of(s.rows, s.C, elem, bwd_threads(s.C), kBwdTile);
-        const long long most = 152LL * resident(tile_smem(t, 2));
+        const long long most = 152LL * resident(tile_smem(t, 2 * kBwdStages));
         return (int)(t.tiles < most ? t.tiles : most);
     }
     const int tpr = row_shape(s.C, elem, kBwdElems).tpr;
@@ -658,7 +671,7 @@ cudaError_t fwd_t(const void* x, const void* w, const void* b, void* y, float* m
     }
     const int threads = fwd_threads(C, sizeof(T));
     const Tiles t = tiles_of(rows, C, sizeof(T), threads, kFwdTile);
-    const size_t smem = tile_smem(t, 1);
+    const size_t smem = tile_smem(t, kFwdStages);
     const long long most = 152LL * resident(smem), blocks = t.tiles < most ? t.tiles : most;
     int* err = device_error_word();
 #define LN_FWD(tpr)                                                                                              \
@@ -690,7 +703,7 @@ cudaError_t bwd_t(const void* x, const void* w, const float* mean, const float* 
     }
     const int threads = bwd_threads(C);
     const Tiles t = tiles_of(rows, C, sizeof(T), threads, kBwdTile);
-    size_t smem = tile_smem(t, 2);
+    size_t smem = tile_smem(t, 2 * kBwdStages);
     const size_t sums = (size_t)(kBlock / threads) * C * 4;
     if (smem < sums) smem = sums;
     int* err = device_error_word();

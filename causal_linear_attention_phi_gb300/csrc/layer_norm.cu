@@ -590,11 +590,11 @@ Tiles tiles_of(long long rows, int C, int elem, int threads, int bytes) {
     return t;
 }
 size_t tile_smem(const Tiles& t, int tiles) { return (size_t)tiles * t.row * t.R; }
-int resident(size_t smem) {
+int resident(size_t smem, int most) {  // blocks of an SM: by shared memory, at most `most` by registers
     const long long per = 225000 / (long long)(smem + 1536);
-    return (int)(per < 1 ? 1 : per > 8 ? 8 : per);
+    return (int)(per < 1 ? 1 : per > most ? most : per);
 }
-constexpr int kFwdTile = 16384, kBwdTile = 8192;
+constexpr int kFwdTile = 16384, kBwdTile = 16384;
 
 }  // namespace
 
@@ -602,7 +602,7 @@ int bwd_blocks(const la_norm_shape& s) {
     const int elem = s.dtype == LA_BF16 ? 2 : 4;
     if (streamed(s.C, elem, true)) {
         const Tiles t = tiles_of(s.rows, s.C, elem, bwd_threads(s.C), kBwdTile);
-        const long long most = 152LL * resident(tile_smem(t, 2 * kBwdStages));
+        const long long most = 152LL * resident(tile_smem(t, 2 * kBwdStages), 2);
         return (int)(t.tiles < most ? t.tiles : most);
     }
     const int tpr = row_shape(s.C, elem, kBwdElems).tpr;
@@ -672,7 +672,7 @@ cudaError_t fwd_t(const void* x, const void* w, const void* b, void* y, float* m
     const int threads = fwd_threads(C, sizeof(T));
     const Tiles t = tiles_of(rows, C, sizeof(T), threads, kFwdTile);
     const size_t smem = tile_smem(t, kFwdStages);
-    const long long most = 152LL * resident(smem), blocks = t.tiles < most ? t.tiles : most;
+    const long long most = 152LL * resident(smem, 4), blocks = t.tiles < most ? t.tiles : most;
     int* err = device_error_word();
 #define LN_FWD(tpr)                                                                                              \
     return launch_tiles("ln_fwd", ln_fwd_tiles<T, tpr>, blocks, smem, st, (const T*)x, (const T*)w, (const T*)b, (T*)y, \

@@ -592,29 +592,33 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 }
 
 // ------------------------------------------------------------------ joining the segments
-// Block (slice, head): kJoinCols value columns of the state, carried through the segments' maps in fp32:
+// Block (slice, head): kCols value columns of the state, carried through the segments' maps in fp32:
 // out[p + 1] = B[p] + M[p] out[p], or in reverse out[p - 1] = B[p] + M[p]^T out[p].  A map (64 KB for D = 128) is copied to
 // shared memory while the previous one is applied.  A thread forms 2 rows x 4 columns with packed multiply-adds: per
 // four terms 6 vector loads from shared memory to 16 of those.
-constexpr int kJoinCols = 16;
-template <int D>
+// 16 columns to a block, with the terms of a product halved between two groups of threads, or 32 columns where that
+// many blocks would not be resident at once (a block's two maps fill most of an SM's shared memory).
+template <int D, int kCols>
 struct JoinCfg {
-    static constexpr int threads = D / 2 * (kJoinCols / 4);
+    static constexpr int group = D / 2 * (kCols / 4), split = 32 / kCols, threads = group * split;
     static constexpr int map = D * D * 4;
-    static constexpr int S = 2 * map;  // [D][kJoinCols]
-    static constexpr int bars = S + D * kJoinCols * 4;
+    static constexpr int S = 2 * map;              // [D][kCols]
+    static constexpr int half = S + D * kCols * 4;  // the second group's sums
+    static constexpr int bars = half + (split > 1 ? D * kCols * 4 : 0);
     static constexpr size_t bytes = bars + 32;
 };
 
-template <int D, bool kReverse>
-__global__ void __launch_bounds__(JoinCfg<D>::threads)
+template <int D, bool kReverse, int kCols>
+__global__ void __launch_bounds__(JoinCfg<D, kCols>::threads)
 tc_gd_join(const float* __restrict__ B, const float* __restrict__ Mx, const float* __restrict__ first,
            float* __restrict__ out, int P, int* err) {
-    using L = JoinCfg<D>;
+    using L = JoinCfg<D, kCols>;
     extern __shared__ __align__(128) uint8_t smem[];
     float* S = reinterpret_cast<float*>(smem + L::S);
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::bars);
-    const int tid = threadIdx.x, row = 2 * (tid >> 2), c0 = 4 * (tid & 3), col = blockIdx.x * kJoinCols + c0;
+    const int tid = threadIdx.x, part = tid / L::group, id = tid % L::group;
+    const int row = 2 * (id / (kCols / 4)), c0 = 4 * (id % (kCols / 4)), col = blockIdx.x * kCols + c0;
+    float4* half = reinterpret_cast<float4*>(smem + L::half) + id;
     const size_t bh = blockIdx.y, rec = (size_t)D * D;
     if (tid == 0) {
         mbar_init(bar, 1);
@@ -630,32 +634,42 @@ tc_gd_join(const float* __restrict__ B, const float* __restrict__ Mx, const floa
         mbar_arrive_expect_tx(bar + (i & 1), D * D * 4);
         bulk_load(smem + (i & 1) * L::map, Mx + seg(i) * rec, D * D * 4, bar + (i & 1));
     };
-    float4 s[2];
+    float4 s[2], b[2];
+    auto load_b = [&](int i) {
 #pragma unroll
-    for (int y = 0; y < 2; ++y)
-        s[y] = !kReverse && first ? ld_f4(first + bh * rec + (row + y) * D + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int y = 0; y < 2; ++y) b[y] = ld_f4(B + seg(i) * rec + (row + y) * D + col);
+    };
     load(0);
+    if (part == 0) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+            s[y] = !kReverse && first ? ld_f4(first + bh * rec + (row + y) * D + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+        load_b(0);
+    }
     bool ok = true;
     for (int i = 0; i < P; ++i) {
-        float2 acc[2][2];
+        F4 acc[2];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-            const size_t at = seg(i) * rec + (row + y) * D + col;
-            *reinterpret_cast<float4*>(out + at) = s[y];
-            *reinterpret_cast<float4*>(S + (row + y) * kJoinCols + c0) = s[y];
-            if (i < P - 1) {
-                const float4 v = ld_f4(B + at);
-                acc[y][0] = make_float2(v.x, v.y);
-                acc[y][1] = make_float2(v.z, v.w);
+            acc[y].a = acc[y].b = make_float2(0.f, 0.f);
+            if (part == 0) {
+                *reinterpret_cast<float4*>(out + seg(i) * rec + (row + y) * D + col) = s[y];
+                *reinterpret_cast<float4*>(S + (row + y) * kCols + c0) = s[y];
+                acc[y] = {make_float2(b[y].x, b[y].y), make_float2(b[y].z, b[y].w)};
             }
         }
         if (i == P - 1) break;
-        if (i + 1 < P - 1) load(i + 1);  // its buffer was last read before the previous barrier
+        if (i + 1 < P - 1) {
+            load(i + 1);  // its buffer was last read before the previous barrier
+            if (part == 0) load_b(i + 1);
+        }
         ok = ok && mbar_wait(bar + (i & 1), (i >> 1) & 1, err, LA_ERR_TIMEOUT);
         __syncthreads();
         const float* m = reinterpret_cast<const float*>(smem + (i & 1) * L::map);
+        const int k0 = part * (D / L::split);
 #pragma unroll 4
-        for (int k = 0; k < D; k += 4) {
+        for (int kk = 0; kk < D / L::split; kk += 4) {
+            const int k = k0 + kk;
             float mv[2][4];
             if (kReverse) {
 #pragma unroll
@@ -676,17 +690,28 @@ tc_gd_join(const float* __restrict__ B, const float* __restrict__ Mx, const floa
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float4 v = ld_f4(S + (k + e) * kJoinCols + c0);
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    fma2(acc[y][0], mv[y][e], make_float2(v.x, v.y));
-                    fma2(acc[y][1], mv[y][e], make_float2(v.z, v.w));
-                }
+                const float4 v = ld_f4(S + (k + e) * kCols + c0);
+                fma4(acc[0], mv[0][e], v);
+                fma4(acc[1], mv[1][e], v);
             }
         }
-        __syncthreads();  // S and the map have been read
+        if (L::split > 1) {
+            if (part == 1) {
 #pragma unroll
-        for (int y = 0; y < 2; ++y) s[y] = make_float4(acc[y][0].x, acc[y][0].y, acc[y][1].x, acc[y][1].y);
+                for (int y = 0; y < 2; ++y)
+                    half[y * L::group] = make_float4(acc[y].a.x, acc[y].a.y, acc[y].b.x, acc[y].b.y);
+            }
+            __syncthreads();  // S and the map have been read, the second sums are there
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            s[y] = make_float4(acc[y].a.x, acc[y].a.y, acc[y].b.x, acc[y].b.y);
+            if (L::split > 1 && part == 0) {
+                const float4 h = half[y * L::group];
+                s[y] = make_float4(s[y].x + h.x, s[y].y + h.y, s[y].z + h.z, s[y].w + h.w);
+            }
+        }
+        if (L::split == 1) __syncthreads();  // S and the map have been read
     }
 }
 
@@ -729,12 +754,16 @@ cudaError_t states(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
 template <int D>
 cudaError_t join(const float* B, const float* Mx, const float* first, float* out, int BH, int P, bool reverse, int* err,
                  cudaStream_t st) {
-    auto kern = reverse ? tc_gd_join<D, true> : tc_gd_join<D, false>;
-    GD_TRY(allow_smem(kern, JoinCfg<D>::bytes));
+    const bool wide = (long long)BH * (D / 16) > 152;
+    auto kern = reverse ? (wide ? tc_gd_join<D, true, 32> : tc_gd_join<D, true, 16>)
+                        : (wide ? tc_gd_join<D, false, 32> : tc_gd_join<D, false, 16>);
+    const size_t smem = wide ? JoinCfg<D, 32>::bytes : JoinCfg<D, 16>::bytes;
+    GD_TRY(allow_smem(kern, smem));
     const char* name = reverse ? "tc_gd_join_reverse" : "tc_gd_join";
     launch_begin(name, st);
     const cudaError_t e =
-        launch_pdl(kern, dim3(D / kJoinCols, BH), dim3(JoinCfg<D>::threads), JoinCfg<D>::bytes, st, B, Mx, first, out, P, err);
+        launch_pdl(kern, dim3(D / (wide ? 32 : 16), BH), dim3(wide ? JoinCfg<D, 32>::threads : JoinCfg<D, 16>::threads), smem,
+                   st, B, Mx, first, out, P, err);
     const cudaError_t e2 = launch_end(name, st);
     return e != cudaSuccess ? e : e2;
 }
@@ -794,17 +823,19 @@ cudaError_t fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
 int tc_segments(const la_shape& s, bool bwd) {
     constexpr int kSms = 152;
     const int BH = s.B * s.H, M = (s.N + kC - 1) / kC;
-    const double main = bwd ? 7.9 : 3.0, sum = bwd ? 2.2 : 2.2, join = bwd ? 2.6 : 1.3;
+    const double main = bwd ? 3.8 + 4.6 : 3.2, sum = 2.6, reverse_sum = 2.8, launch = 6.0;
     auto waves = [](long long blocks) { return (double)((blocks + kSms - 1) / kSms); };
+    const long long slices = (long long)BH * (s.Dk / 16);
+    const double join = (s.Dk == 128 ? 1.9 : 0.8) * (slices > kSms ? 1.6 * waves(slices / 2) : 1.0);
     int best = 1;
     double best_t = waves(BH) * M * main;
     for (int P = 2; P <= M && P <= 64; ++P) {
         const int cps = (M + P - 1) / P;
         if ((M + cps - 1) / cps != P) continue;
-        double t = waves((long long)BH * P) * cps * main + 10.0 + P * join;
+        double t = waves((long long)BH * P) * cps * main + 2 * launch + (bwd ? 2 : 1) * P * join;
         t += waves((long long)BH * (P - 1) * (s.Dk == 128 ? 2 : 1)) * cps * sum;
-        if (bwd) t += waves((long long)BH * (P - 1)) * cps * 3.8;
-        if (t < 0.95 * best_t) {
+        if (bwd) t += waves((long long)BH * (P - 1)) * cps * reverse_sum + 2 * launch;
+        if (t < 0.97 * best_t) {
             best_t = t;
             best = P;
         }

@@ -32,7 +32,7 @@ constexpr int kC = 64;
 // 2 here) is formed in fp64 and kept as hi + lo, so that differences of long sums keep fp32's precision; a decay
 // below exp(-100) (under fp32's normal range; -inf among them) is counted in kSeg instead of entering the sum,
 // and a product across it is 0.  Positions past the sequence's end have g = 0 and beta = 0.
-constexpr int kGam = 0, kTail = kC, kBeta = 2 * kC, kBg = 3 * kC, kTb = 4 * kC;  // kBg = beta gam, kTb = tail beta
+constexpr int kGam = 0, kTail = kC, kBeta = 2 * kC, kBg = 3 * kC, kTb = 4 * kC;  // kBg = -beta gam, kTb = tail beta
 constexpr int kGhi = 5 * kC, kGlo = 6 * kC, kSeg = 7 * kC;
 constexpr int kRec = 8 * kC;
 constexpr float kReset = -100.f;
@@ -96,7 +96,7 @@ __device__ __forceinline__ void gate_record(const T* __restrict__ g, const T* __
         rec[kGam + i] = gam;
         rec[kTail + i] = tail;
         rec[kBeta + i] = b;
-        rec[kBg + i] = b * gam;
+        rec[kBg + i] = -b * gam;
         rec[kTb + i] = tail * b;
     }
 }
@@ -111,6 +111,29 @@ __device__ __forceinline__ void fma2(float2& a, float m, float2 b) {
     asm("fma.rn.f32x2 %0, %1, %2, %0;"
         : "+l"(reinterpret_cast<uint64_t&>(a))
         : "l"(reinterpret_cast<const uint64_t&>(mm)), "l"(reinterpret_cast<const uint64_t&>(b)));
+}
+// a b + c on two floats at once.
+__device__ __forceinline__ float2 fma2v(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+          "l"(reinterpret_cast<const uint64_t&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2v(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2v(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+    return d;
 }
 struct F4 {
     float2 a, b;

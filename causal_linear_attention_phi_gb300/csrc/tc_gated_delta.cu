@@ -380,20 +380,25 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             __syncwarp();
             if (lane == 0) mbar_arrive(b);
         };
-        float S[kSc];
+        float2 S[kSc / 2];
 #pragma unroll
-        for (int x = 0; x < kSc; ++x)
-            S[x] = kMode == kSum ? ((map && kSc * h + x == r) || (D == 64 && kSc * h + x == r - D) ? 1.f : 0.f)
-                   : a.S0 && r < D ? a.S0[(((size_t)bh * a.P + p) * D + kSc * h + x) * D + r]
-                                   : 0.f;
-        auto put_state = [&]() {
+        for (int x = 0; x < kSc / 2; ++x) {
+            const int c = kSc * h + 2 * x;
+            if (kMode == kSum) {
+                const int d = map ? r : D == 64 ? r - D : -1;
+                S[x] = make_float2(c == d ? 1.f : 0.f, c + 1 == d ? 1.f : 0.f);
+            } else {
+                const float* s0 = a.S0 + (((size_t)bh * a.P + p) * D + c) * D + r;
+                S[x] = a.S0 && r < D ? make_float2(s0[0], s0[D]) : make_float2(0.f, 0.f);
+            }
+        }
+        {
             uint32_t hi[kSc / 2];
             put_hi(lb + T::SHi + kSc / 2 * h, S, hi);
             arrive(&bar->s_hi);
             put_lo(lb + T::SLo + kSc / 2 * h, S, hi);
             arrive(&bar->s_lo);
-        };
-        put_state();
+        }
         // o of chunk j: a warp's store of a position is 64 contiguous bytes (staged for a TMA store it took two
         // barriers of all compute warps in the chain of chunks)
         auto output = [&](int j) {
@@ -417,34 +422,39 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             const float* gates = reinterpret_cast<const float*>(sg + L::gates);
             // a gate of this thread's positions x .. x + 3
             auto gate = [&](int which, int x) { return ld_f4(gates + which + kTok * h + x); };
-            float R[kTok];  // beta V, then beta R
-            float Rp[kMode == kGrad ? kTok : 1];  // V, R, then X
-            uint32_t w[kTok], hi[kTok / 2];
+            float2 R[kTok / 2];  // beta V, then beta R, then u; positions in pairs
+            float2 Rp[kMode == kGrad ? kTok / 2 : 1];  // V, R, then X
+            uint32_t w[kTok], hi[kTok / 2], lo[kTok / 2];
             wait(&bar->full[s], (i >> 1) & 1);
+            if (map || 32 * (warp & 3) >= D) {
 #pragma unroll
-            for (int x = 0; x < kTok; x += 4) {
-                const float4 b = gate(kBeta, x);
-                const float bb[4] = {b.x, b.y, b.z, b.w};
+                for (int x = 0; x < kTok / 2; ++x) {
+                    R[x] = make_float2(0.f, 0.f);
+                    if constexpr (kMode == kGrad) Rp[x] = R[x];
+                }
+            } else {
+                const uint32_t vc = col_addr(sg + L::V, r, kTok * h);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float v = r < D && !map ? __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(
-                                                                        sg + L::V + elem_off(kTok * h + x + e, r))
-                                                                    << 16)
-                                                  : 0.f;
-                    if constexpr (kMode == kGrad) Rp[x + e] = v;
-                    R[x + e] = bb[e] * v;
+                for (int x = 0; x < kTok; x += 4) {
+                    const F4 b = get4(gates + kBeta + kTok * h + x);
+                    const float2 v0 = make_float2(col_get(vc, x), col_get(vc, x + 1)),
+                                 v1 = make_float2(col_get(vc, x + 2), col_get(vc, x + 3));
+                    if constexpr (kMode == kGrad) {
+                        Rp[x / 2] = v0;
+                        Rp[x / 2 + 1] = v1;
+                    }
+                    R[x / 2] = mul2v(b.a, v0);
+                    R[x / 2 + 1] = mul2v(b.b, v1);
                 }
             }
             wait(&bar->y_done, ph);
             ld(lb + T::Y + kTok * h, w);
             tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < kTok; x += 4) {
-                const float4 b = gate(kBg, x);
-                R[x] = fmaf(-b.x, __uint_as_float(w[x]), R[x]);
-                R[x + 1] = fmaf(-b.y, __uint_as_float(w[x + 1]), R[x + 1]);
-                R[x + 2] = fmaf(-b.z, __uint_as_float(w[x + 2]), R[x + 2]);
-                R[x + 3] = fmaf(-b.w, __uint_as_float(w[x + 3]), R[x + 3]);
+            for (int x = 0; x < kTok; x += 4) {  // kBg holds -beta gam
+                const F4 b = get4(gates + kBg + kTok * h + x);
+                R[x / 2] = fma2v(b.a, pair(w[x], w[x + 1]), R[x / 2]);
+                R[x / 2 + 1] = fma2v(b.b, pair(w[x + 2], w[x + 3]), R[x / 2 + 1]);
             }
             put_hi(lb + T::R + kTok / 2 * h, R, hi);
             arrive(&bar->r_hi);
@@ -454,43 +464,34 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll
                 for (int x = 0; x < kTok; x += 4) {
                     const float4 g = gate(kGam, x);
-                    Rp[x] = fmaf(-g.x, __uint_as_float(w[x]), Rp[x]);
-                    Rp[x + 1] = fmaf(-g.y, __uint_as_float(w[x + 1]), Rp[x + 1]);
-                    Rp[x + 2] = fmaf(-g.z, __uint_as_float(w[x + 2]), Rp[x + 2]);
-                    Rp[x + 3] = fmaf(-g.w, __uint_as_float(w[x + 3]), Rp[x + 3]);
+                    Rp[x / 2] = fma2v(make_float2(-g.x, -g.y), pair(w[x], w[x + 1]), Rp[x / 2]);
+                    Rp[x / 2 + 1] = fma2v(make_float2(-g.z, -g.w), pair(w[x + 2], w[x + 3]), Rp[x / 2 + 1]);
                 }
             }
             if (kMode == kOut && i > 0) output(i - 1);
             wait(&bar->x_done, ph);
-            uint32_t lo[kTok / 2];
             {
                 uint32_t w2[kTok];
                 ld(lb + T::X + kTok * h, w);
                 ld(lb + T::X + kC + kTok * h, w2);
                 tmem_ld_wait();
 #pragma unroll
-                for (int x = 0; x < kTok; x += 4) {
-                    const float4 b = gate(kBeta, x), tl = gate(kTail, x);
-                    const float bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float d = __uint_as_float(w[x + e]) + __uint_as_float(w2[x + e]);
-                        if constexpr (kMode == kGrad) Rp[x + e] += d;
-                        R[x + e] = fmaf(bv[e], d, R[x + e]);  // u
-                    }
-                    hi[x / 2] = pack_bf16x2(tl.x * R[x], tl.y * R[x + 1]);
-                    hi[x / 2 + 1] = pack_bf16x2(tl.z * R[x + 2], tl.w * R[x + 3]);
+                for (int x = 0; x < kTok; x += 2) {
+                    const float2 d = add2v(pair(w[x], w[x + 1]), pair(w2[x], w2[x + 1]));
+                    const float2 b = *reinterpret_cast<const float2*>(gates + kBeta + kTok * h + x),
+                                 tl = *reinterpret_cast<const float2*>(gates + kTail + kTok * h + x);
+                    if constexpr (kMode == kGrad) Rp[x / 2] = add2v(Rp[x / 2], d);
+                    R[x / 2] = fma2v(b, d, R[x / 2]);  // u
+                    hi[x / 2] = hi2(mul2v(tl, R[x / 2]));
                 }
             }
             st(lb + T::R + kTok / 2 * h, hi);
             tmem_st_wait();
             arrive(&bar->u_hi);
 #pragma unroll
-            for (int x = 0; x < kTok; x += 4) {
-                const float4 tl = gate(kTail, x);
-                lo[x / 2] = pack_bf16x2(fmaf(tl.x, R[x], -bf_lo(hi[x / 2])), fmaf(tl.y, R[x + 1], -bf_hi(hi[x / 2])));
-                lo[x / 2 + 1] =
-                    pack_bf16x2(fmaf(tl.z, R[x + 2], -bf_lo(hi[x / 2 + 1])), fmaf(tl.w, R[x + 3], -bf_hi(hi[x / 2 + 1])));
+            for (int x = 0; x < kTok; x += 2) {
+                const float2 tl = *reinterpret_cast<const float2*>(gates + kTail + kTok * h + x);
+                lo[x / 2] = lo2(mul2v(tl, R[x / 2]), hi[x / 2]);
             }
             st(lb + T::R + 32 + kTok / 2 * h, lo);
             tmem_st_wait();
@@ -498,7 +499,10 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             if constexpr (kMode == kOut) {
                 // u for the outputs (its columns are free: the previous chunk's output was read)
 #pragma unroll
-                for (int x = 0; x < kTok; x += 2) split2(R[x], R[x + 1], hi[x / 2], lo[x / 2]);
+                for (int x = 0; x < kTok / 2; ++x) {
+                    hi[x] = hi2(R[x]);
+                    lo[x] = lo2(R[x], hi[x]);
+                }
                 st(lb + T::U + kTok / 2 * h, hi);
                 st(lb + T::U + 32 + kTok / 2 * h, lo);
             } else if constexpr (kMode == kGrad) {  // this thread's row of the state's tile (the state entering the chunk) and of X's tiles
@@ -507,21 +511,17 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 if (r < D) {
                     uint8_t *sS = base + L::out, *sX = sS + L::sbytes;
 #pragma unroll
-                    for (int x = 0; x < kSc; x += 8) {
-                        const int c = kSc * h + x;
+                    for (int x = 0; x < kSc / 2; x += 4) {
+                        const int c = kSc * h + 2 * x;
                         *reinterpret_cast<uint4*>(sS + (c >> 6) * (D * 128) + row_off(r, c >> 3)) =
-                            make_uint4(pack_bf16x2(S[x], S[x + 1]), pack_bf16x2(S[x + 2], S[x + 3]),
-                                       pack_bf16x2(S[x + 4], S[x + 5]), pack_bf16x2(S[x + 6], S[x + 7]));
+                            make_uint4(hi2(S[x]), hi2(S[x + 1]), hi2(S[x + 2]), hi2(S[x + 3]));
                     }
 #pragma unroll
-                    for (int x = 0; x < kTok; x += 8) {
-                        uint4 a, b;
-                        split2(Rp[x], Rp[x + 1], a.x, b.x);
-                        split2(Rp[x + 2], Rp[x + 3], a.y, b.y);
-                        split2(Rp[x + 4], Rp[x + 5], a.z, b.z);
-                        split2(Rp[x + 6], Rp[x + 7], a.w, b.w);
-                        const int off = row_off(r, (kTok * h + x) >> 3);
-                        *reinterpret_cast<uint4*>(sX + off) = b;
+                    for (int x = 0; x < kTok / 2; x += 4) {
+                        const uint4 a = make_uint4(hi2(Rp[x]), hi2(Rp[x + 1]), hi2(Rp[x + 2]), hi2(Rp[x + 3]));
+                        const int off = row_off(r, (kTok * h + 2 * x) >> 3);
+                        *reinterpret_cast<uint4*>(sX + off) =
+                            make_uint4(lo2(Rp[x], a.x), lo2(Rp[x + 1], a.y), lo2(Rp[x + 2], a.z), lo2(Rp[x + 3], a.w));
                         *reinterpret_cast<uint4*>(sX + D * 128 + off) = a;
                     }
                 }
@@ -537,13 +537,30 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             const float gc = gates[kGam + kC - 1];
             wait(&bar->s_done, ph);
             {
-                uint32_t d[kSc];
-                ld(lb + T::dS + kSc * h, d);
+                // half of the columns are updated while the other half are read
+                constexpr int kH = kSc / 2;
+                uint32_t d0[kH], d1[kH], sh[kH];
+                const float2 g2 = make_float2(gc, gc);
+                ld(lb + T::dS + kSc * h, d0);
+                tmem_ld_wait();
+                ld(lb + T::dS + kSc * h + kH, d1);
+#pragma unroll
+                for (int x = 0; x < kH / 2; ++x) {
+                    S[x] = fma2v(g2, S[x], pair(d0[2 * x], d0[2 * x + 1]));
+                    sh[x] = hi2(S[x]);
+                }
                 tmem_ld_wait();
 #pragma unroll
-                for (int x = 0; x < kSc; ++x) S[x] = fmaf(gc, S[x], __uint_as_float(d[x]));
+                for (int x = 0; x < kH / 2; ++x) {
+                    S[kH / 2 + x] = fma2v(g2, S[kH / 2 + x], pair(d1[2 * x], d1[2 * x + 1]));
+                    sh[kH / 2 + x] = hi2(S[kH / 2 + x]);
+                }
+                st(lb + T::SHi + kH * h, sh);
+                tmem_st_wait();
+                arrive(&bar->s_hi);
+                put_lo(lb + T::SLo + kH * h, S, sh);
+                arrive(&bar->s_lo);
             }
-            put_state();
             if constexpr (kMode == kOut) {  // S Q^T (complete: issued before dS) scaled in place, the second columns cleared
                 ld(lb + T::O + kTok * h, w);
                 tmem_ld_wait();
@@ -574,13 +591,14 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             for (int x = 0; x < kSc; ++x) {
                 const int d = kSc * h + x;
                 if (map || r >= D)
-                    a.segM[at + map_at<D>(d, c)] = S[x];
+                    a.segM[at + map_at<D>(d, c)] = x & 1 ? S[x / 2].y : S[x / 2].x;
                 else
-                    a.segB[at + d * D + c] = S[x];
+                    a.segB[at + d * D + c] = x & 1 ? S[x / 2].y : S[x / 2].x;
             }
         } else if (kMode == kOut && a.S_out && p == a.P - 1 && r < D) {
 #pragma unroll
-            for (int x = 0; x < kSc; ++x) a.S_out[((size_t)bh * D + kSc * h + x) * D + r] = S[x];
+            for (int x = 0; x < kSc; ++x)
+                a.S_out[((size_t)bh * D + kSc * h + x) * D + r] = x & 1 ? S[x / 2].y : S[x / 2].x;
         }
         tc_fence_before();
     }

@@ -76,10 +76,6 @@ __device__ __forceinline__ void commit1(uint32_t lead, uint64_t* bar) {
         "r"(lead)
         : "memory");
 }
-// Byte offset of (row, column c) in 64-column blocks of kC rows.
-__device__ __forceinline__ int elem_off(int row, int c) {
-    return (c >> 6) * kBlk + row * 128 + ((((c >> 3) & 7) ^ (row & 7)) << 4) + (c & 7) * 2;
-}
 // Every kernel here starts so: wait for the previous grid, take the TMEM columns, and only then let the next
 // grid's blocks be scheduled.  Blocks of several of these kernels fit on one SM: none holds columns while it
 // waits for a grid, and none is still to take its columns when a block that waits for it can arrive.
@@ -137,21 +133,54 @@ __device__ __forceinline__ void st(uint32_t a, const uint32_t (&r)[N]) {
 
 
 // What is formed for a product goes to TMEM hi parts first, with a signal of their own: the products of the hi parts run
-// while the lo parts are formed.  put_hi leaves the packed hi parts for put_lo.
+// while the lo parts are formed.  Values in pairs, as the packed arithmetic has them.
+__device__ __forceinline__ float2 pair(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ uint32_t hi2(float2 v) { return pack_bf16x2(v.x, v.y); }
+__device__ __forceinline__ uint32_t lo2(float2 v, uint32_t hi) {
+    const float2 d = fma2v(make_float2(bf_lo(hi), bf_hi(hi)), make_float2(-1.f, -1.f), v);
+    return pack_bf16x2(d.x, d.y);
+}
 template <int N>
-__device__ __forceinline__ void put_hi(uint32_t a, const float (&v)[N], uint32_t (&hi)[N / 2]) {
+__device__ __forceinline__ void put_hi(uint32_t a, const float2 (&v)[N], uint32_t (&hi)[N]) {
 #pragma unroll
-    for (int x = 0; x < N / 2; ++x) hi[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
+    for (int x = 0; x < N; ++x) hi[x] = hi2(v[x]);
     st(a, hi);
     tmem_st_wait();
 }
 template <int N>
-__device__ __forceinline__ void put_lo(uint32_t a, const float (&v)[N], const uint32_t (&hi)[N / 2]) {
-    uint32_t lo[N / 2];
+__device__ __forceinline__ void put_lo(uint32_t a, const float2 (&v)[N], const uint32_t (&hi)[N]) {
+    uint32_t lo[N];
 #pragma unroll
-    for (int x = 0; x < N / 2; ++x) lo[x] = pack_bf16x2(v[2 * x] - bf_lo(hi[x]), v[2 * x + 1] - bf_hi(hi[x]));
+    for (int x = 0; x < N; ++x) lo[x] = lo2(v[x], hi[x]);
     st(a, lo);
     tmem_st_wait();
+}
+
+// One column r of a tile of 64-column blocks (`blk` bytes apart), rows row0 (a multiple of 8) + x for constant x: the
+// swizzle is an exclusive or of the row into bits 4-6 of the address, so an access is that and an immediate offset.
+// Written for the shared address space: generic addressing took a dozen instructions an element, more than the rest of
+// the phase.
+__device__ __forceinline__ uint32_t col_addr(const void* tile, int r, int row0, int blk = kBlk) {
+    return smem_u32(tile) + (r >> 6) * blk + row0 * 128 + ((r >> 3) & 7) * 16 + (r & 7) * 2;
+}
+__device__ __forceinline__ float col_get(uint32_t col, int x) {  // a bf16
+    uint32_t v;
+    asm volatile(
+        "{\n\t.reg .b16 h, z;\n\tmov.b16 z, 0;\n\t"
+        "ld.shared.b16 h, [%1];\n\tmov.b32 %0, {z, h};\n\t}"
+        : "=r"(v)
+        : "r"((col ^ ((x & 7) << 4)) + x * 128)
+        : "memory");
+    return __uint_as_float(v);
+}
+__device__ __forceinline__ void col_put(uint32_t col, int x, uint16_t v) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"((col ^ ((x & 7) << 4)) + x * 128), "h"(v) : "memory");
+}
+// Two bf16 of rows x and x + 1.
+__device__ __forceinline__ void col_put2(uint32_t col, int x, float a, float b) {
+    const uint32_t w = pack_bf16x2(a, b);
+    col_put(col, x, (uint16_t)w);
+    col_put(col, x + 1, (uint16_t)(w >> 16));
 }
 
 template <typename K>

@@ -199,17 +199,19 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             __syncwarp();
             if (lane == 0) mbar_arrive(b);
         };
-        float S[kSc];
+        float2 S[kSc / 2];
 #pragma unroll
-        for (int x = 0; x < kSc; ++x)
-            S[x] = !kSums && segdS && r < D ? segdS[(((size_t)bh * P + p) * D + kSc * h + x) * D + r] : 0.f;
+        for (int x = 0; x < kSc / 2; ++x) {
+            const float* s0 = segdS + (((size_t)bh * P + p) * D + kSc * h + 2 * x) * D + r;
+            S[x] = !kSums && segdS && r < D ? make_float2(s0[0], s0[D]) : make_float2(0.f, 0.f);
+        }
         uint8_t* out = base + L::out;
         for (int i = 0; i < nloc; ++i) {
             const int s = i & 1, ph = i & 1, c = cend - 1 - i;
             const size_t at = (size_t)bh * M + c;
             uint8_t* sg = base + s * L::stage;
             const float* gates = reinterpret_cast<const float*>(sg + L::gates);
-            auto gate = [&](int which, int x) { return ld_f4(gates + which + kTok * h + x); };
+            auto gate = [&](int which, int x) { return get4(gates + which + kTok * h + x); };
             {  // the state gradient's parts, and the signal that they are there
                 uint32_t hi[kSc / 2];
                 put_hi(lb + T::SHi + kSc / 2 * h, S, hi);
@@ -235,98 +237,84 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     }
                 }
             }
-            uint32_t w[kTok], hi[kTok / 2];
+            uint32_t w[kTok], w2[kTok], hi[kTok / 2];
             wait(&bar->full[s], (i >> 1) & 1);
             {
-            uint32_t lo[kTok / 2];
+                uint32_t lo[kTok / 2];
+                if (32 * (warp & 3) >= D) {
+#pragma unroll
+                    for (int x = 0; x < kTok / 2; ++x) hi[x] = lo[x] = 0u;
+                } else {
+                    const uint32_t dc = col_addr(sg + L::dO, r, kTok * h);
+#pragma unroll
+                    for (int x = 0; x < kTok; x += 4) {
+                        const F4 g = gate(kGam, x);
+                        const float2 v0 = mul2v(g.a, make_float2(col_get(dc, x), col_get(dc, x + 1))),
+                                     v1 = mul2v(g.b, make_float2(col_get(dc, x + 2), col_get(dc, x + 3)));
+                        hi[x / 2] = hi2(v0);
+                        lo[x / 2] = lo2(v0, hi[x / 2]);
+                        hi[x / 2 + 1] = hi2(v1);
+                        lo[x / 2 + 1] = lo2(v1, hi[x / 2 + 1]);
+                    }
+                }
+                st(lb + T::G + kTok / 2 * h, hi);  // free: the previous chunk's products are complete
+                st(lb + T::G + 32 + kTok / 2 * h, lo);
+                tmem_st_wait();
+                arrive(&bar->g_ready);
+            }
+            float2 dU[kTok / 2], b[kTok / 2];  // dU, then Y; positions in pairs
+            wait(&bar->a_done, ph);
+            ld(lb + T::A1 + kTok * h, w);
+            ld(lb + T::A2 + kTok * h, w2);
+            tmem_ld_wait();
 #pragma unroll
             for (int x = 0; x < kTok; x += 4) {
-                const float4 g = gate(kGam, x);
-                const float gg[4] = {g.x, g.y, g.z, g.w};
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] = r < D ? gg[e] * __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(
-                                                               sg + L::dO + elem_off(kTok * h + x + e, r))
-                                                           << 16)
-                                 : 0.f;
-                split2(v[0], v[1], hi[x / 2], lo[x / 2]);
-                split2(v[2], v[3], hi[x / 2 + 1], lo[x / 2 + 1]);
+                const F4 t = gate(kTail, x), be = gate(kBeta, x);
+                dU[x / 2] = fma2v(t.a, pair(w[x], w[x + 1]), pair(w2[x], w2[x + 1]));
+                dU[x / 2 + 1] = fma2v(t.b, pair(w[x + 2], w[x + 3]), pair(w2[x + 2], w2[x + 3]));
+                b[x / 2] = mul2v(be.a, dU[x / 2]);
+                b[x / 2 + 1] = mul2v(be.b, dU[x / 2 + 1]);
             }
-            st(lb + T::G + kTok / 2 * h, hi);  // free: the previous chunk's products are complete
-            st(lb + T::G + 32 + kTok / 2 * h, lo);
-            tmem_st_wait();
-            arrive(&bar->g_ready);
-            }
-            float dU[kTok];
-            wait(&bar->a_done, ph);
-            {
-                float b[kTok];
-                uint32_t w2[kTok];
-                ld(lb + T::A1 + kTok * h, w);
-                ld(lb + T::A2 + kTok * h, w2);
-                tmem_ld_wait();
-#pragma unroll
-                for (int x = 0; x < kTok; x += 4) {
-                    const float4 t = gate(kTail, x), be = gate(kBeta, x);
-                    const float tt[4] = {t.x, t.y, t.z, t.w}, bv[4] = {be.x, be.y, be.z, be.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        dU[x + e] = fmaf(tt[e], __uint_as_float(w[x + e]), __uint_as_float(w2[x + e]));
-                        b[x + e] = bv[e] * dU[x + e];
-                    }
-                }
-                put_hi(lb + T::B + kTok / 2 * h, b, hi);
-                arrive(&bar->b_hi);
-                put_lo(lb + T::B + 32 + kTok / 2 * h, b, hi);
-                arrive(&bar->b_lo);
-            }
+            put_hi(lb + T::B + kTok / 2 * h, b, hi);
+            arrive(&bar->b_hi);
+            put_lo(lb + T::B + 32 + kTok / 2 * h, b, hi);
+            arrive(&bar->b_lo);
             wait(&bar->y_done, ph);
-            {
-                float b[kTok];
-                uint32_t w2[kTok];
-                ld(lb + T::Y + kTok * h, w);
-                ld(lb + T::Y + kC + kTok * h, w2);
-                tmem_ld_wait();
+            ld(lb + T::Y + kTok * h, w);
+            ld(lb + T::Y + kC + kTok * h, w2);
+            tmem_ld_wait();
 #pragma unroll
-                for (int x = 0; x < kTok; x += 4) {
-                    const float4 bg = gate(kBg, x);
-                    const float bv[4] = {bg.x, bg.y, bg.z, bg.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        dU[x + e] += __uint_as_float(w[x + e]) + __uint_as_float(w2[x + e]);  // Y
-                        b[x + e] = -bv[e] * dU[x + e];
-                    }
-                }
-                put_hi(lb + T::B + kTok / 2 * h, b, hi);
-                arrive(&bar->r_hi);
-                put_lo(lb + T::B + 32 + kTok / 2 * h, b, hi);
-                arrive(&bar->r_lo);
+            for (int x = 0; x < kTok; x += 4) {
+                const F4 bg = gate(kBg, x);  // -beta gam
+                dU[x / 2] = add2v(dU[x / 2], add2v(pair(w[x], w[x + 1]), pair(w2[x], w2[x + 1])));
+                dU[x / 2 + 1] = add2v(dU[x / 2 + 1], add2v(pair(w[x + 2], w[x + 3]), pair(w2[x + 2], w2[x + 3])));
+                b[x / 2] = mul2v(bg.a, dU[x / 2]);
+                b[x / 2 + 1] = mul2v(bg.b, dU[x / 2 + 1]);
             }
+            put_hi(lb + T::B + kTok / 2 * h, b, hi);
+            arrive(&bar->r_hi);
+            put_lo(lb + T::B + 32 + kTok / 2 * h, b, hi);
+            arrive(&bar->r_lo);
             const float gc = gates[kGam + kC - 1];
             if constexpr (!kSums) {
                 // dV's tile [positions][value columns] and Y's [value columns][positions]
                 if (ct == 0) bulk_wait_read_all();
                 named_barrier(1, 32 * kWarps);
                 if (r < D) {
+                    const uint32_t oc = col_addr(out, r, kTok * h);
 #pragma unroll
                     for (int x = 0; x < kTok; x += 4) {
-                        const float4 b = gate(kBeta, x);
-                        const float bb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            *reinterpret_cast<__nv_bfloat16*>(out + elem_off(kTok * h + x + e, r)) =
-                                __float2bfloat16_rn(bb[e] * dU[x + e]);
+                        const F4 be = gate(kBeta, x);
+                        const float2 v0 = mul2v(be.a, dU[x / 2]), v1 = mul2v(be.b, dU[x / 2 + 1]);
+                        col_put2(oc, x, v0.x, v0.y);
+                        col_put2(oc, x + 2, v1.x, v1.y);
                     }
 #pragma unroll
-                    for (int x = 0; x < kTok; x += 8) {
-                        uint4 a, b;
-                        split2(dU[x], dU[x + 1], a.x, b.x);
-                        split2(dU[x + 2], dU[x + 3], a.y, b.y);
-                        split2(dU[x + 4], dU[x + 5], a.z, b.z);
-                        split2(dU[x + 6], dU[x + 7], a.w, b.w);
-                        uint8_t* y = out + L::tile + row_off(r, (kTok * h + x) >> 3);
-                        *reinterpret_cast<uint4*>(y) = b;
+                    for (int x = 0; x < kTok / 2; x += 4) {
+                        const uint4 a = make_uint4(hi2(dU[x]), hi2(dU[x + 1]), hi2(dU[x + 2]), hi2(dU[x + 3]));
+                        uint8_t* y = out + L::tile + row_off(r, (kTok * h + 2 * x) >> 3);
+                        *reinterpret_cast<uint4*>(y) =
+                            make_uint4(lo2(dU[x], a.x), lo2(dU[x + 1], a.y), lo2(dU[x + 2], a.z), lo2(dU[x + 3], a.w));
                         *reinterpret_cast<uint4*>(y + D * 128) = a;
                     }
                 }
@@ -344,16 +332,18 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             wait(&bar->s_done, ph);
             {
                 uint32_t d[kSc];
+                const float2 g2 = make_float2(gc, gc);
                 ld(lb + T::dS + kSc * h, d);
                 tmem_ld_wait();
 #pragma unroll
-                for (int x = 0; x < kSc; ++x) S[x] = fmaf(gc, S[x], __uint_as_float(d[x]));
+                for (int x = 0; x < kSc / 2; ++x) S[x] = fma2v(g2, S[x], pair(d[2 * x], d[2 * x + 1]));
             }
         }
         if (ct == 0) bulk_wait_all();
         if (kSums && r < D) {
 #pragma unroll
-            for (int x = 0; x < kSc; ++x) segB2[(((size_t)bh * P + p) * D + kSc * h + x) * D + r] = S[x];
+            for (int x = 0; x < kSc; ++x)
+                segB2[(((size_t)bh * P + p) * D + kSc * h + x) * D + r] = x & 1 ? S[x / 2].y : S[x / 2].x;
         }
         tc_fence_before();
     }
@@ -653,8 +643,9 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if ((lane & 1) == 0) part[L::pCol + q4 * kC + col0 + (lane >> 1)] = isF ? cs : -cs;
             wait(&bar->out_done, ph);
             // row r = dk, positions 16 h ..
-            float tok[16], outs = 0.f;
-            uint8_t *sq = base + L::out, *sk = sq + (D / 64) * kBlk;
+            float tok[16], outs = 0.f, dq_even = 0.f, dk_even = 0.f;
+            const uint32_t sq = col_addr(base + L::out, r & (D - 1), col0), sk = sq + (D / 64) * kBlk;
+            const uint32_t qc = col_addr(base + L::QK, r & (D - 1), col0, 2 * kBlk), kc = qc + kBlk;  // [Q; K] blocks
 #pragma unroll
             for (int x0 = 0; x0 < 16; x0 += 8) {
                 const int t0 = col0 + x0;
@@ -677,25 +668,23 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                                 tbv[4] = {tb.x, tb.y, tb.z, tb.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int x = y + e, t = t0 + x;
+                        const int x = y + e;
                         const float dqi = gav[e] * __uint_as_float(q1[x]);
-                        const float dki = -bgv[e] * __uint_as_float(k1[x]);
+                        const float dki = bgv[e] * __uint_as_float(k1[x]);
                         const float dko = tbv[e] * (__uint_as_float(ka[x]) + __uint_as_float(kb[x]));
                         const float dqv = dqi + (__uint_as_float(qa[x]) + __uint_as_float(qb[x]));
                         const float dkv = (dki + dko) + (__uint_as_float(ea[x]) + __uint_as_float(eb[x]));
                         float s = 0.f;
                         if (r < D) {
-                            const int off = elem_off(t, r);
-                            const int eo = off + (r >> 6) * kBlk;  // [Q; K] blocks
-                            const float qv =
-                                __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(base + L::QK + eo) << 16);
-                            const float kv = __uint_as_float(
-                                (uint32_t) * reinterpret_cast<const uint16_t*>(base + L::QK + kBlk + eo) << 16);
-                            const float o = kv * dko;
+                            const float qv = col_get(qc, x0 + x), kv = col_get(kc, x0 + x), o = kv * dko;
                             s = fmaf(qv, dqi, fmaf(kv, dki, -o));
                             outs += o;
-                            *reinterpret_cast<__nv_bfloat16*>(sq + off) = __float2bfloat16_rn(dqv);
-                            *reinterpret_cast<__nv_bfloat16*>(sk + off) = __float2bfloat16_rn(dkv);
+                            if (e & 1) {
+                                col_put2(sq, x0 + x - 1, dq_even, dqv);
+                                col_put2(sk, x0 + x - 1, dk_even, dkv);
+                            }
+                            dq_even = dqv;
+                            dk_even = dkv;
                         }
                         tok[x0 + x] = s;
                     }

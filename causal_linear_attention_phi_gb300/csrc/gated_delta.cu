@@ -95,7 +95,9 @@ gd_prepare(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict
             Ps[at * kC * kC + r * kC + c] = d != 0.f ? qk[i][j] * d : 0.f;
         }
     __syncthreads();
-    solve_t(As, rec + kBeta, tid);
+    if (tid < 64) solve_diagonal(As, rec + kBeta, tid >> 5, tid & 31);
+    __syncthreads();
+    solve_joins(As, rec + kBeta, tid);
     for (int i = tid; i < kC * kC; i += kThreads) ts[at * kC * kC + i] = As[(i >> 6) * kLd + (i & 63)];
     for (int i = tid; i < kRec; i += kThreads) recs[at * kRec + i] = rec[i];
 }

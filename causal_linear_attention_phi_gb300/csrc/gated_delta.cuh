@@ -165,34 +165,37 @@ __device__ __forceinline__ void acc_rows(F4& z, const float* row, const float* b
 // shared memory with row pitch kLd.  Four diagonal blocks of 16 by forward substitution,
 // t_i = -(A_i + sum_(j<i) A_ij beta_j t_j), one column to a lane, the column in registers; then blocks are joined in
 // pairs, first to 32 and then to 64: t21 = -(I + t22 beta) A21 (I + beta t11), two small products each.  (Diagonal
-// blocks of 32 left all but two warps waiting for a chain of 31 rows.)  The first 128 threads do the work, all threads
-// call it; A is complete before, t after.
-__device__ __forceinline__ void solve_t(float* A, const float* beta, int tid) {
+// blocks of 32 left all but two warps waiting for a chain of 31 rows.)
+// solve_diagonal: one warp, the two diagonal blocks of rows 32 w .. 32 w + 31, which it needs complete.
+__device__ __forceinline__ void solve_diagonal(float* A, const float* beta, int w, int lane) {
+    constexpr int kQ = kC / 4;
+    const int b0 = 32 * w + (lane & 16), c = lane & 15;
+    float y[kQ];  // beta_j t_j of this column
+    y[0] = 0.f;
+#pragma unroll
+    for (int r = 1; r < kQ; ++r) {
+        float* a = A + (b0 + r) * kLd + b0;
+        float s0 = a[c], s1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < r; j += 4) {
+            const float4 v = ld_f4(a + j);  // broadcast; zero from the diagonal on
+            s0 = fmaf(v.x, y[j], s0);
+            if (j + 1 < r) s1 = fmaf(v.y, y[j + 1], s1);
+            if (j + 2 < r) s0 = fmaf(v.z, y[j + 2], s0);
+            if (j + 3 < r) s1 = fmaf(v.w, y[j + 3], s1);
+        }
+        const float x = r > c ? -(s0 + s1) : 0.f;
+        __syncwarp();  // the row has been read
+        a[c] = x;
+        y[r] = beta[b0 + r] * x;
+    }
+}
+
+// The joins: the first 128 threads do the work, all threads of the block call it; the diagonal blocks and the rest of
+// A are complete before, t after.
+__device__ __forceinline__ void solve_joins(float* A, const float* beta, int tid) {
     constexpr int kH = kC / 2, kQ = kC / 4;
     const bool work = tid < 128;
-    if (tid < kC) {
-        const int b0 = tid & 48, c = tid & 15;
-        float y[kQ];  // beta_j t_j of this column
-        y[0] = 0.f;
-#pragma unroll
-        for (int r = 1; r < kQ; ++r) {
-            float* a = A + (b0 + r) * kLd + b0;
-            float s0 = a[c], s1 = 0.f;
-#pragma unroll
-            for (int j = 0; j < r; j += 4) {
-                const float4 v = ld_f4(a + j);  // broadcast; zero from the diagonal on
-                s0 = fmaf(v.x, y[j], s0);
-                if (j + 1 < r) s1 = fmaf(v.y, y[j + 1], s1);
-                if (j + 2 < r) s0 = fmaf(v.z, y[j + 2], s0);
-                if (j + 3 < r) s1 = fmaf(v.w, y[j + 3], s1);
-            }
-            const float x = r > c ? -(s0 + s1) : 0.f;
-            __syncwarp();  // the row has been read
-            a[c] = x;
-            y[r] = beta[b0 + r] * x;
-        }
-    }
-    __syncthreads();
     {  // pair p: rows 32 p + 16 + r, columns 32 p + c .. c + 3
         const int b = kH * ((tid >> 6) & 1), r = (tid >> 2) & 15, c = 4 * (tid & 3);
         float* row = A + (b + kQ + r) * kLd + b;

@@ -44,22 +44,24 @@ struct PrepSmem {
 static_assert(PrepSmem::P >= kC * kLd * 4 && PrepSmem::rec >= 4 * kBlk, "regions");
 constexpr size_t kPrepBytes = PrepSmem::total + 1024;
 
-// w[x] (columns j0 .. j0 + 31 of row i) times the decay from j to i, 0 outside j <= i (j < i).
-template <bool kResets>
-__device__ __forceinline__ void decay32(uint32_t (&w)[32], const float* rec, int i, int j0, bool incl) {
-    const float seg = rec[kSeg + i], hi = rec[kGhi + i], lo = rec[kGlo + i];
-    const int last = incl ? i : i - 1;
+// w[x] (columns j0 .. j0 + 31 of row i) times the decay from j to i, 0 outside j <= last (kFull: all inside).
+template <bool kResets, bool kFull>
+__device__ __forceinline__ void decay32(uint32_t (&w)[32], const float* rec, int i, int j0, int last) {
+    const float seg = rec[kSeg + i];
+    const float2 hi = make_float2(rec[kGhi + i], rec[kGhi + i]), lo = make_float2(rec[kGlo + i], rec[kGlo + i]);
+    const float2 neg = make_float2(-1.f, -1.f);
 #pragma unroll
     for (int x = 0; x < 32; x += 4) {
-        const float4 gh = ld_f4(rec + kGhi + j0 + x), gl = ld_f4(rec + kGlo + j0 + x);
-        const float4 sg = kResets ? ld_f4(rec + kSeg + j0 + x) : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float ghv[4] = {gh.x, gh.y, gh.z, gh.w}, glv[4] = {gl.x, gl.y, gl.z, gl.w}, sgv[4] = {sg.x, sg.y, sg.z, sg.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bool in = j0 + x + e <= last && (!kResets || sgv[e] == seg);
-            const float d = ex2_approx((hi - ghv[e]) + (lo - glv[e]));
-            w[x + e] = in ? __float_as_uint(__uint_as_float(w[x + e]) * d) : 0u;
-        }
+        const F4 gh = get4(rec + kGhi + j0 + x), gl = get4(rec + kGlo + j0 + x);
+        const float2 d0 = add2v(fma2v(gh.a, neg, hi), fma2v(gl.a, neg, lo)),
+                     d1 = add2v(fma2v(gh.b, neg, hi), fma2v(gl.b, neg, lo));
+        const float2 v0 = mul2v(pair(w[x], w[x + 1]), make_float2(ex2_approx(d0.x), ex2_approx(d0.y))),
+                     v1 = mul2v(pair(w[x + 2], w[x + 3]), make_float2(ex2_approx(d1.x), ex2_approx(d1.y)));
+        const float4 sg = kResets ? ld_f4(rec + kSeg + j0 + x) : make_float4(seg, seg, seg, seg);
+        w[x] = (kFull || j0 + x <= last) && sg.x == seg ? __float_as_uint(v0.x) : 0u;
+        w[x + 1] = (kFull || j0 + x + 1 <= last) && sg.y == seg ? __float_as_uint(v0.y) : 0u;
+        w[x + 2] = (kFull || j0 + x + 2 <= last) && sg.z == seg ? __float_as_uint(v1.x) : 0u;
+        w[x + 3] = (kFull || j0 + x + 3 <= last) && sg.w == seg ? __float_as_uint(v1.y) : 0u;
     }
 }
 
@@ -120,10 +122,13 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             } else {
                 tmem_ld32(tmem + ((uint32_t)(32 * warp) << 16) + 32 * h, w);
                 tmem_ld_wait();
+                const int last = isP ? i : i - 1;
                 if (resets)
-                    decay32<true>(w, rec, i, 32 * h, isP);
+                    decay32<true, false>(w, rec, i, 32 * h, last);
+                else if (h < (warp & 1))
+                    decay32<false, true>(w, rec, i, 32 * h, last);
                 else
-                    decay32<false>(w, rec, i, 32 * h, isP);
+                    decay32<false, false>(w, rec, i, 32 * h, last);
             }
             if (isP) {
 #pragma unroll
@@ -144,6 +149,11 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             }
         }
     }
+    // a warp of A's rows has all that its diagonal blocks need: it goes on while the other two warps form P
+    if (tid >= 64) {
+        __syncwarp();
+        solve_diagonal(A, rec + kBeta, warp & 1, lane);
+    }
     fence_proxy_async_smem();
     __syncthreads();
     uint8_t* mat = mats + at * (size_t)kMats;
@@ -152,7 +162,7 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         bulk_store(recs + at * kRec, rec, kRec * 4);
         bulk_commit();
     }
-    solve_t(A, rec + kBeta, tid);
+    solve_joins(A, rec + kBeta, tid);
     if (tid == 0) bulk_wait_read_all();  // P's tiles have been stored: t's go in their place
     __syncthreads();
     {
@@ -176,7 +186,7 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     if (tid == 0) {
         bulk_store(mat + kTHi, base + PrepSmem::P, 2 * kBlk);
         bulk_commit();
-        bulk_wait_all();
+        bulk_wait_read_all();  // shared memory outlives the copies' reads; the grid's end makes them visible
         if (!ok) mbar_wait(bar, 0, err, LA_ERR_TIMEOUT);  // never leave with copies in flight
     }
     if (warp == 1) {

@@ -563,7 +563,7 @@ Layout layout(const la_shape& s, bool bwd) {
         return at;
     };
     L.rec = take(chunks * kRec);
-    L.t = take(2 * chunks * kC * kC);
+    L.t = take((tc_ok(s) && bwd ? 3 : 2) * chunks * kC * kC);
     L.P = L.t + chunks * kC * kC * sizeof(float);
     if (bwd) {
         L.X = take(chunks * kC * s.Dv);

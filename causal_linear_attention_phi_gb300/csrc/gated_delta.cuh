@@ -32,9 +32,9 @@ constexpr int kC = 64;
 // 2 here) is formed in fp64 and kept as hi + lo, so that differences of long sums keep fp32's precision; a decay
 // below exp(-100) (under fp32's normal range; -inf among them) is counted in kSeg instead of entering the sum,
 // and a product across it is 0.  Positions past the sequence's end have g = 0 and beta = 0.
-constexpr int kGam = 0, kTail = kC, kBeta = 2 * kC, kBg = 3 * kC, kTb = 4 * kC;  // kBg = -beta gam, kTb = tail beta
-constexpr int kGhi = 5 * kC, kGlo = 6 * kC, kSeg = 7 * kC;
-constexpr int kRec = 8 * kC;
+constexpr int kGam = 0, kNg = kC, kTb = 2 * kC, kTail = 3 * kC, kBeta = 4 * kC, kBg = 5 * kC;  // -gam, tail beta, -beta gam
+constexpr int kGhi = 6 * kC, kGlo = 7 * kC, kSeg = 8 * kC;
+constexpr int kRec = 9 * kC;
 constexpr float kReset = -100.f;
 
 // 2^(hi + lo) for |lo| at most half a step of hi.
@@ -94,6 +94,7 @@ __device__ __forceinline__ void gate_record(const T* __restrict__ g, const T* __
         const float gam = seg == 0 ? exp2_hilo(hi, lo) : 0.f, tail = seg == rtot ? exp2_hilo(dhi, dlo) : 0.f;
         const float b = i < n ? to_f32(beta[c0 + i]) : 0.f;
         rec[kGam + i] = gam;
+        rec[kNg + i] = -gam;
         rec[kTail + i] = tail;
         rec[kBeta + i] = b;
         rec[kBg + i] = -b * gam;
@@ -149,15 +150,26 @@ __device__ __forceinline__ F4 get4(const float* p) {
 __device__ __forceinline__ void put4(float* p, const F4& z, float s = 1.f) {
     *reinterpret_cast<float4*>(p) = make_float4(s * z.a.x, s * z.a.y, s * z.b.x, s * z.b.y);
 }
-// z += sum_(k0 <= k < k1) row[k] beta[k] m[k][0..3], m's rows kLd apart; k0 and k1 multiples of 4.
-__device__ __forceinline__ void acc_rows(F4& z, const float* row, const float* beta, const float* m, int k0, int k1) {
-#pragma unroll 4
+// z[j] += sum_(k0 <= k < k1) row[j step kLd + k] beta[k] m[k][0..3] for the J rows from j0 on, m's rows kLd apart; k0 and
+// k1 multiples of 4.  A load from shared memory costs the bytes it returns to registers, broadcast or not (these
+// products are bound by that: 4 x 4 tiles return 2.25 bytes a multiply-add, single rows of 8 columns 5).
+template <int kJ0, int kStep>
+__device__ __forceinline__ void acc_tile(F4 (&z)[4], const float* row, const float* beta, const float* m, int k0, int k1) {
+#pragma unroll 2
     for (int k = k0; k < k1; k += 4) {
-        const float4 a = ld_f4(row + k), be = ld_f4(beta + k);
-        fma4(z, a.x * be.x, ld_f4(m + k * kLd));
-        fma4(z, a.y * be.y, ld_f4(m + (k + 1) * kLd));
-        fma4(z, a.z * be.z, ld_f4(m + (k + 2) * kLd));
-        fma4(z, a.w * be.w, ld_f4(m + (k + 3) * kLd));
+        const float4 be = ld_f4(beta + k);
+        float4 a[4], v[4];
+#pragma unroll
+        for (int j = kJ0; j < 4; ++j) a[j] = ld_f4(row + j * kStep * kLd + k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = ld_f4(m + (k + e) * kLd);
+#pragma unroll
+        for (int j = kJ0; j < 4; ++j) {
+            fma4(z[j], a[j].x * be.x, v[0]);
+            fma4(z[j], a[j].y * be.y, v[1]);
+            fma4(z[j], a[j].z * be.z, v[2]);
+            fma4(z[j], a[j].w * be.w, v[3]);
+        }
     }
 }
 
@@ -191,61 +203,56 @@ __device__ __forceinline__ void solve_diagonal(float* A, const float* beta, int 
     }
 }
 
-// The joins: the first 128 threads do the work, all threads of the block call it; the diagonal blocks and the rest of
-// A are complete before, t after.
+// The joins: the first two warps do the work, all threads of the block call it; the diagonal blocks and the rest of A are
+// complete before, t after.
 __device__ __forceinline__ void solve_joins(float* A, const float* beta, int tid) {
     constexpr int kH = kC / 2, kQ = kC / 4;
-    const bool work = tid < 128;
-    {  // pair p: rows 32 p + 16 + r, columns 32 p + c .. c + 3
-        const int b = kH * ((tid >> 6) & 1), r = (tid >> 2) & 15, c = 4 * (tid & 3);
+    if (tid < 32) {  // pair p: rows 32 p + 16 + r + 4 j, columns 32 p + c .. c + 3
+        const int b = kH * (tid >> 4), r = (tid >> 2) & 3, c = 4 * (tid & 3);
         float* row = A + (b + kQ + r) * kLd + b;
-        F4 z;
-        if (work) {
-            z = get4(row + c);
-            acc_rows(z, row, beta + b, A + b * kLd + b + c, 0, kQ);
-        }
-        __syncthreads();
-        if (work) put4(row + c, z);
-        __syncthreads();
-        if (work) acc_rows(z, row + kQ, beta + b + kQ, A + (b + kQ) * kLd + b + c, 0, kQ);
-        __syncthreads();
-        if (work) put4(row + c, z, -1.f);
-        __syncthreads();
+        F4 z[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] = get4(row + 4 * j * kLd + c);
+        acc_tile<0, 4>(z, row, beta + b, A + b * kLd + b + c, 0, kQ);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) put4(row + 4 * j * kLd + c, z[j]);
+        __syncwarp();
+        acc_tile<0, 4>(z, row + kQ, beta + b + kQ, A + (b + kQ) * kLd + b + c, 0, kQ);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) put4(row + 4 * j * kLd + c, z[j], -1.f);
     }
-    {  // row 32 + r, columns c .. c + 3 and 16 + c .. 16 + c + 3; t11 and t22 are lower triangular
-        const int r = (tid >> 2) & 31, c = 4 * (tid & 3);
-        float* row = A + (kH + r) * kLd;
-        F4 z0, z1;
-        if (work) {
-            z0 = get4(row + c);
-            z1 = get4(row + kQ + c);
-            acc_rows(z0, row, beta, A + c, 0, kH);
-            acc_rows(z1, row, beta, A + kQ + c, kQ, kH);
-        }
-        __syncthreads();
-        if (work) {
-            put4(row + c, z0);
-            put4(row + kQ + c, z1);
-        }
-        __syncthreads();
-        if (work) {
-            const int k1 = r < kQ ? kQ : kH;  // the same for a whole warp
-            acc_rows(z0, row + kH, beta + kH, A + kH * kLd + c, 0, k1);
-            acc_rows(z1, row + kH, beta + kH, A + kH * kLd + kQ + c, 0, k1);
-        }
-        __syncthreads();
-        if (work) {
-            put4(row + c, z0, -1.f);
-            put4(row + kQ + c, z1, -1.f);
-        }
-        __syncthreads();
+    __syncthreads();
+    // rows 32 + r + 8 j, 16 columns to a warp, four to a thread; t11 and t22 are lower triangular
+    const int half = kQ * (tid >> 5), r = (tid >> 2) & 7, c = half + 4 * (tid & 3);
+    float* row = A + (kH + r) * kLd;
+    F4 z[4];
+    if (tid < 64) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] = get4(row + 8 * j * kLd + c);
+        acc_tile<0, 8>(z, row, beta, A + c, half, kH);
     }
+    __syncthreads();
+    if (tid < 64) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) put4(row + 8 * j * kLd + c, z[j]);
+        __syncwarp();  // a warp reads the columns that it wrote
+        acc_tile<0, 8>(z, row + kH, beta + kH, A + kH * kLd + c, 0, kQ);
+        acc_tile<2, 8>(z, row + kH, beta + kH, A + kH * kLd + c, kQ, kH);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) put4(row + 8 * j * kLd + c, z[j], -1.f);
+    }
+    __syncthreads();
 }
 
 // Byte offsets of the workspace regions of one call (256-byte aligned).
 struct Layout {
     size_t rec;     // [BH][M][kRec] fp32 gate records
-    size_t t, P;    // [BH][M][64][64] fp32 (tensor cores: t hi, t lo, P hi, P lo as bf16 in the bytes of t and P)
+    // [BH][M][64][64] fp32; tensor cores: bf16 tiles, hi and lo, of t beta and P beta (columns scaled), for the gradient
+    // of t beta, P and beta t (rows scaled)
+    size_t t, P;
     // The gradient's, fp32 (tensor cores: bf16 tiles of transposed matrices, X and Y as lo and hi parts):
     size_t X, Y;    // [BH][M * 64][Dv]
     size_t S, dS;   // [BH][M][Dk][Dv]: the state entering each chunk, the gradient leaving it

@@ -7,11 +7,11 @@
 // tc_gd_states (one block per head and segment of chunks): the recurrence with the state transposed, S^T
 // [Dv lanes x Dk], so that every product has 128 rows and its left operand comes from TMEM, written there by the
 // thread that owns the row:
-//   Y^T  = S^T K^T                       R^T = V^T - gam Y^T          (a column is a position)
-//   X^T  = R^T + (beta R)^T t^T          u^T = beta X^T
-//   S^T <- gam_C S^T + (tail u)^T K      O^T = gam (S^T Q^T) + u^T P^T
+//   Y^T  = S^T K^T                            R^T = V^T - gam Y^T          (a column is a position)
+//   X^T  = R^T + R^T (t beta)^T               (u = beta X)
+//   S^T <- gam_C S^T + (tail beta X)^T K      O^T = gam (S^T Q^T) + X^T (P beta)^T
 // The fp32 state stays in registers (half a row to a thread).  Inputs K, Q are bf16 already; what is formed
-// here (S, beta R, u, t, P) enters the products as hi + lo bf16 parts, x = hi + lo to 2^-17, except the S of
+// here (S, R, X, t, P) enters the products as hi + lo bf16 parts, x = hi + lo to 2^-17, except the S of
 // S^T Q^T, which meets one rounding only (it adds 0.5e-3 to the 1.7e-3 of rounding o itself; with
 // single parts throughout, correlated keys lift o's error to 7e-3 and the state's to 4e-3).
 //
@@ -34,7 +34,7 @@ using namespace tcgd;
 constexpr int kPrepThreads = 128;
 struct PrepSmem {
     // offset 0: blocks of [Q rows 0-63; K rows 64-127] x 64 columns, then (once the product has read them) fp32 A, which
-    // becomes t, and P's tiles; t's tiles last, in the place of P's once those are stored
+    // becomes t, and P's tiles; t's tiles last, in the place of P's once those are stored (and of A)
     static constexpr int A = 0;
     static constexpr int P = 18432;  // A's bytes rounded up to a tile's alignment
     static constexpr int rec = P + 2 * kBlk;
@@ -65,7 +65,7 @@ __device__ __forceinline__ void decay32(uint32_t (&w)[32], const float* rec, int
     }
 }
 
-template <int D>
+template <int D, bool kBwd>
 __global__ void __launch_bounds__(kPrepThreads, 6)
 tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __nv_bfloat16* __restrict__ g, const __nv_bfloat16* __restrict__ beta, float* __restrict__ recs,
@@ -129,6 +129,16 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     decay32<false, true>(w, rec, i, 32 * h, last);
                 else
                     decay32<false, false>(w, rec, i, 32 * h, last);
+                if (!kBwd && isP) {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4) {
+                        const float4 be = ld_f4(rec + kBeta + 32 * h + x);
+                        w[x] = __float_as_uint(be.x * __uint_as_float(w[x]));
+                        w[x + 1] = __float_as_uint(be.y * __uint_as_float(w[x + 1]));
+                        w[x + 2] = __float_as_uint(be.z * __uint_as_float(w[x + 2]));
+                        w[x + 3] = __float_as_uint(be.w * __uint_as_float(w[x + 3]));
+                    }
+                }
             }
             if (isP) {
 #pragma unroll
@@ -156,35 +166,48 @@ tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     }
     fence_proxy_async_smem();
     __syncthreads();
-    uint8_t* mat = mats + at * (size_t)kMats;
+    uint8_t* mat = mats + at * (size_t)(kBwd ? kMatsBwd : kMatsFwd);
     if (tid == 0) {
-        bulk_store(mat + kPHi, base + PrepSmem::P, 2 * kBlk);
+        bulk_store(mat + kMatP, base + PrepSmem::P, 2 * kBlk);
         bulk_store(recs + at * kRec, rec, kRec * 4);
         bulk_commit();
     }
     solve_joins(A, rec + kBeta, tid);
     if (tid == 0) bulk_wait_read_all();  // P's tiles have been stored: t's go in their place
     __syncthreads();
-    {
-        const int i = tid >> 1, j0 = 32 * (tid & 1);
+    const int i = tid >> 1, j0 = 32 * (tid & 1);
+    float4 tr[8];  // half a row
+#pragma unroll
+    for (int x = 0; x < 8; ++x) tr[x] = ld_f4(A + i * kLd + j0 + 4 * x);
+    auto put = [&](uint8_t* tile, auto scale) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const float4 s = ld_f4(A + i * kLd + j0 + 8 * c), u = ld_f4(A + i * kLd + j0 + 8 * c + 4);
+            const float4 s = scale(2 * c), u = scale(2 * c + 1);
             uint4 a, b;
             split2(s.x, s.y, a.x, b.x);
             split2(s.z, s.w, a.y, b.y);
             split2(u.x, u.y, a.z, b.z);
             split2(u.z, u.w, a.w, b.w);
             const int off = row_off(i, (j0 >> 3) + c);
-            *reinterpret_cast<uint4*>(base + PrepSmem::P + off) = a;
-            *reinterpret_cast<uint4*>(base + PrepSmem::P + kBlk + off) = b;
+            *reinterpret_cast<uint4*>(tile + off) = a;
+            *reinterpret_cast<uint4*>(tile + kBlk + off) = b;
         }
+    };
+    put(base + PrepSmem::P, [&](int x) {
+        const float4 be = ld_f4(rec + kBeta + j0 + 4 * x);
+        return make_float4(tr[x].x * be.x, tr[x].y * be.y, tr[x].z * be.z, tr[x].w * be.w);
+    });
+    if (kBwd) {
+        __syncthreads();  // A has been read
+        const float bi = rec[kBeta + i];
+        put(base + PrepSmem::A, [&](int x) { return make_float4(bi * tr[x].x, bi * tr[x].y, bi * tr[x].z, bi * tr[x].w); });
     }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     if (tid == 0) {
-        bulk_store(mat + kTHi, base + PrepSmem::P, 2 * kBlk);
+        bulk_store(mat + kMatF, base + PrepSmem::P, 2 * kBlk);
+        if (kBwd) bulk_store(mat + kMatR, base + PrepSmem::A, 2 * kBlk);
         bulk_commit();
         bulk_wait_read_all();  // shared memory outlives the copies' reads; the grid's end makes them visible
         if (!ok) mbar_wait(bar, 0, err, LA_ERR_TIMEOUT);  // never leave with copies in flight
@@ -203,11 +226,11 @@ struct __align__(8) Bars {
 
 template <int D, int kMode>
 struct FwdSmem {
-    static constexpr int tile = D / 64 * kBlk, nmats = kMode == kOut ? kMats : 2 * kBlk;
+    static constexpr int tile = D / 64 * kBlk, nmats = kMode == kOut ? kMatsFwd : 2 * kBlk;
     // a stage: K, V, t (and P), Q, gates
     static constexpr int K = 0, V = tile, mats = 2 * tile, Q = mats + nmats, gates = Q + (kMode == kOut ? tile : 0);
     static constexpr int stage = gates + 2048;
-    static_assert(kGateBytes <= 2048, "gates");
+    static_assert(kFwdGates <= 2048, "gates");
     static constexpr int out = 2 * stage;  // kGrad: the state's tile and X lo, X hi
     static constexpr int sbytes = D * D * 2, xbytes = 2 * D * 128;
     static constexpr int bars = out + (kMode == kGrad ? sbytes + xbytes : 0);
@@ -285,7 +308,7 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 const int s = i & 1, c = cbeg + i, t0 = c * kC;
                 uint8_t* st = base + s * L::stage;
                 if (!mbar_wait(&bar->empty[s], ((i >> 1) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
-                mbar_arrive_expect_tx(&bar->full[s], (kMode == kOut ? 3 * L::tile + kMats : 2 * L::tile + 2 * kBlk) + kGateBytes);
+                mbar_arrive_expect_tx(&bar->full[s], (kMode == kOut ? 3 : 2) * L::tile + L::nmats + kFwdGates);
 #pragma unroll
                 for (int b = 0; b < D / 64; ++b) {
                     tma_load_3d(st + L::K + b * kBlk, &tm_k, 64 * b, t0, bh, &bar->full[s]);
@@ -293,8 +316,8 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     if (kMode == kOut) tma_load_3d(st + L::Q + b * kBlk, &tm_q, 64 * b, t0, bh, &bar->full[s]);
                 }
                 const size_t at = (size_t)bh * M + c;
-                bulk_load(st + L::mats, a.mats + at * kMats, kMode == kOut ? kMats : 2 * kBlk, &bar->full[s]);
-                bulk_load(st + L::gates, a.recs + at * kRec, kGateBytes, &bar->full[s]);
+                bulk_load(st + L::mats, a.mats + at * a.mat_bytes, L::nmats, &bar->full[s]);
+                bulk_load(st + L::gates, a.recs + at * kRec, kFwdGates, &bar->full[s]);
                 armed[s] = i;
             }
             // never leave with copies in flight: wait for the last armed phase of each stage
@@ -314,12 +337,12 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 __syncwarp();
                 tc_fence_after();
             };
-            // u P^T of chunk j, added to O (scaled by gam) in two columns' sets, while the next chunk's R is formed
+            // X (P beta)^T of chunk j, added to O (scaled by gam) in two columns' sets, while the next chunk's R is formed
             auto outputs = [&](int j) {
-                const uint32_t dP = tile_desc(smem_u32(base + (j & 1) * L::stage) + L::mats + kPHi);
+                const uint32_t dP = tile_desc(smem_u32(base + (j & 1) * L::stage) + L::mats + kMatP);
                 wait(&bar->o_ready, j & 1);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)  // u_hi [P_hi; P_lo]^T
+                for (int kk = 0; kk < 4; ++kk)  // X_hi [P_hi; P_lo]^T
                     mma_ts1(lead, tmem + T::O, tmem + T::U + 8 * kk, dP + step_k(kk), id_k2, 1);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
@@ -345,14 +368,14 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 if (kMode == kOut && i > 0) outputs(i - 1);
                 wait(&bar->r_hi, ph);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)  // (beta R)_hi [t_hi; t_lo]^T: two products of 64 columns
+                for (int kk = 0; kk < 4; ++kk)  // R_hi [t_hi; t_lo]^T: two products of 64 columns
                     mma_ts1(lead, tmem + T::X, tmem + T::R + 8 * kk, dM + step_k(kk), id_k2, kk > 0);
                 wait(&bar->r_lo, ph);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_ts1(lead, tmem + T::X, tmem + T::R + 32 + 8 * kk, dM + step_k(kk), id_k, 1);
                 commit1(lead, &bar->x_done);
-                if constexpr (kMode == kOut) {  // O = S Q^T, while u is formed
+                if constexpr (kMode == kOut) {  // O = S Q^T, while X is formed
                     if (i > 0) wait(&bar->o_free, ph ^ 1);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
@@ -360,7 +383,7 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 }
                 wait(&bar->u_hi, ph);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)  // the chunk's writes (tail u) K
+                for (int kk = 0; kk < 4; ++kk)  // the chunk's writes (tail beta X) K
                     mma_ts1(lead, tmem + T::dS, tmem + T::R + 8 * kk, dKmn + step_mn(kk), id_mn, kk > 0);
                 wait(&bar->u_lo, ph);
 #pragma unroll
@@ -431,83 +454,58 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             uint8_t* sg = base + s * L::stage;
             const float* gates = reinterpret_cast<const float*>(sg + L::gates);
             // a gate of this thread's positions x .. x + 3
-            auto gate = [&](int which, int x) { return ld_f4(gates + which + kTok * h + x); };
-            float2 R[kTok / 2];  // beta V, then beta R, then u; positions in pairs
-            float2 Rp[kMode == kGrad ? kTok / 2 : 1];  // V, R, then X
-            uint32_t w[kTok], hi[kTok / 2], lo[kTok / 2];
+            auto gate = [&](int which, int x) { return get4(gates + which + kTok * h + x); };
+            float2 R[kTok / 2];  // V, then R, then X; positions in pairs
+            uint32_t w[kTok], hi[kTok / 2];
             wait(&bar->full[s], (i >> 1) & 1);
             if (map || 32 * (warp & 3) >= D) {
 #pragma unroll
-                for (int x = 0; x < kTok / 2; ++x) {
-                    R[x] = make_float2(0.f, 0.f);
-                    if constexpr (kMode == kGrad) Rp[x] = R[x];
-                }
+                for (int x = 0; x < kTok / 2; ++x) R[x] = make_float2(0.f, 0.f);
             } else {
                 const uint32_t vc = col_addr(sg + L::V, r, kTok * h);
 #pragma unroll
-                for (int x = 0; x < kTok; x += 4) {
-                    const F4 b = get4(gates + kBeta + kTok * h + x);
-                    const float2 v0 = make_float2(col_get(vc, x), col_get(vc, x + 1)),
-                                 v1 = make_float2(col_get(vc, x + 2), col_get(vc, x + 3));
-                    if constexpr (kMode == kGrad) {
-                        Rp[x / 2] = v0;
-                        Rp[x / 2 + 1] = v1;
-                    }
-                    R[x / 2] = mul2v(b.a, v0);
-                    R[x / 2 + 1] = mul2v(b.b, v1);
-                }
+                for (int x = 0; x < kTok; x += 2) R[x / 2] = make_float2(col_get(vc, x), col_get(vc, x + 1));
             }
             wait(&bar->y_done, ph);
             ld(lb + T::Y + kTok * h, w);
             tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < kTok; x += 4) {  // kBg holds -beta gam
-                const F4 b = get4(gates + kBg + kTok * h + x);
-                R[x / 2] = fma2v(b.a, pair(w[x], w[x + 1]), R[x / 2]);
-                R[x / 2 + 1] = fma2v(b.b, pair(w[x + 2], w[x + 3]), R[x / 2 + 1]);
+            for (int x = 0; x < kTok; x += 4) {
+                const F4 g = gate(kNg, x);
+                R[x / 2] = fma2v(g.a, pair(w[x], w[x + 1]), R[x / 2]);
+                R[x / 2 + 1] = fma2v(g.b, pair(w[x + 2], w[x + 3]), R[x / 2 + 1]);
             }
             put_hi(lb + T::R + kTok / 2 * h, R, hi);
             arrive(&bar->r_hi);
             put_lo(lb + T::R + 32 + kTok / 2 * h, R, hi);
             arrive(&bar->r_lo);
-            if constexpr (kMode == kGrad) {
-#pragma unroll
-                for (int x = 0; x < kTok; x += 4) {
-                    const float4 g = gate(kGam, x);
-                    Rp[x / 2] = fma2v(make_float2(-g.x, -g.y), pair(w[x], w[x + 1]), Rp[x / 2]);
-                    Rp[x / 2 + 1] = fma2v(make_float2(-g.z, -g.w), pair(w[x + 2], w[x + 3]), Rp[x / 2 + 1]);
-                }
-            }
             if (kMode == kOut && i > 0) output(i - 1);
             wait(&bar->x_done, ph);
             {
-                uint32_t w2[kTok];
-                ld(lb + T::X + kTok * h, w);
-                ld(lb + T::X + kC + kTok * h, w2);
-                tmem_ld_wait();
+                float2 u[kTok / 2];  // tail beta X
+                {
+                    uint32_t w2[kTok];
+                    ld(lb + T::X + kTok * h, w);
+                    ld(lb + T::X + kC + kTok * h, w2);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int x = 0; x < kTok; x += 2) {
-                    const float2 d = add2v(pair(w[x], w[x + 1]), pair(w2[x], w2[x + 1]));
-                    const float2 b = *reinterpret_cast<const float2*>(gates + kBeta + kTok * h + x),
-                                 tl = *reinterpret_cast<const float2*>(gates + kTail + kTok * h + x);
-                    if constexpr (kMode == kGrad) Rp[x / 2] = add2v(Rp[x / 2], d);
-                    R[x / 2] = fma2v(b, d, R[x / 2]);  // u
-                    hi[x / 2] = hi2(mul2v(tl, R[x / 2]));
+                    for (int x = 0; x < kTok; x += 2)
+                        R[x / 2] = add2v(R[x / 2], add2v(pair(w[x], w[x + 1]), pair(w2[x], w2[x + 1])));
                 }
-            }
-            st(lb + T::R + kTok / 2 * h, hi);
-            tmem_st_wait();
-            arrive(&bar->u_hi);
 #pragma unroll
-            for (int x = 0; x < kTok; x += 2) {
-                const float2 tl = *reinterpret_cast<const float2*>(gates + kTail + kTok * h + x);
-                lo[x / 2] = lo2(mul2v(tl, R[x / 2]), hi[x / 2]);
+                for (int x = 0; x < kTok; x += 4) {
+                    const F4 t = gate(kTb, x);
+                    u[x / 2] = mul2v(t.a, R[x / 2]);
+                    u[x / 2 + 1] = mul2v(t.b, R[x / 2 + 1]);
+                }
+                put_hi(lb + T::R + kTok / 2 * h, u, hi);
+                arrive(&bar->u_hi);
+                put_lo(lb + T::R + 32 + kTok / 2 * h, u, hi);
+                arrive(&bar->u_lo);
             }
-            st(lb + T::R + 32 + kTok / 2 * h, lo);
-            tmem_st_wait();
-            arrive(&bar->u_lo);
             if constexpr (kMode == kOut) {
-                // u for the outputs (its columns are free: the previous chunk's output was read)
+                // X for the outputs (its columns are free: the previous chunk's output was read)
+                uint32_t lo[kTok / 2];
 #pragma unroll
                 for (int x = 0; x < kTok / 2; ++x) {
                     hi[x] = hi2(R[x]);
@@ -528,10 +526,10 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     }
 #pragma unroll
                     for (int x = 0; x < kTok / 2; x += 4) {
-                        const uint4 a = make_uint4(hi2(Rp[x]), hi2(Rp[x + 1]), hi2(Rp[x + 2]), hi2(Rp[x + 3]));
+                        const uint4 a = make_uint4(hi2(R[x]), hi2(R[x + 1]), hi2(R[x + 2]), hi2(R[x + 3]));
                         const int off = row_off(r, (kTok * h + 2 * x) >> 3);
                         *reinterpret_cast<uint4*>(sX + off) =
-                            make_uint4(lo2(Rp[x], a.x), lo2(Rp[x + 1], a.y), lo2(Rp[x + 2], a.z), lo2(Rp[x + 3], a.w));
+                            make_uint4(lo2(R[x], a.x), lo2(R[x + 1], a.y), lo2(R[x + 2], a.z), lo2(R[x + 3], a.w));
                         *reinterpret_cast<uint4*>(sX + D * 128 + off) = a;
                     }
                 }
@@ -576,11 +574,12 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 tmem_ld_wait();
 #pragma unroll
                 for (int x = 0; x < kTok; x += 4) {
-                    const float4 g = gate(kGam, x);
-                    w[x] = __float_as_uint(g.x * __uint_as_float(w[x]));
-                    w[x + 1] = __float_as_uint(g.y * __uint_as_float(w[x + 1]));
-                    w[x + 2] = __float_as_uint(g.z * __uint_as_float(w[x + 2]));
-                    w[x + 3] = __float_as_uint(g.w * __uint_as_float(w[x + 3]));
+                    const F4 g = gate(kGam, x);
+                    const float2 v0 = mul2v(g.a, pair(w[x], w[x + 1])), v1 = mul2v(g.b, pair(w[x + 2], w[x + 3]));
+                    w[x] = __float_as_uint(v0.x);
+                    w[x + 1] = __float_as_uint(v0.y);
+                    w[x + 2] = __float_as_uint(v1.x);
+                    w[x + 3] = __float_as_uint(v1.y);
                 }
                 st(lb + T::O + kTok * h, w);
 #pragma unroll
@@ -749,19 +748,20 @@ namespace tcgd {
 
 template <int D>
 cudaError_t prepare(const CUtensorMap& tq, const CUtensorMap& tk, const void* g, const void* beta, float* recs,
-                    uint8_t* mats, const la_shape& s, int M, int* err, cudaStream_t st) {
-    GD_TRY(allow_smem(tc_gd_prepare<D>, kPrepBytes));
+                    uint8_t* mats, const la_shape& s, int M, bool bwd, int* err, cudaStream_t st) {
+    auto kern = bwd ? tc_gd_prepare<D, true> : tc_gd_prepare<D, false>;
+    GD_TRY(allow_smem(kern, kPrepBytes));
     launch_begin("tc_gd_prepare", st);
     const cudaError_t e =
-        launch_pdl(tc_gd_prepare<D>, dim3(M, s.B * s.H), dim3(kPrepThreads), kPrepBytes, st, tq, tk,
+        launch_pdl(kern, dim3(M, s.B * s.H), dim3(kPrepThreads), kPrepBytes, st, tq, tk,
                    (const __nv_bfloat16*)g, (const __nv_bfloat16*)beta, recs, mats, s.N, M, err);
     const cudaError_t e2 = launch_end("tc_gd_prepare", st);
     return e != cudaSuccess ? e : e2;
 }
 template cudaError_t prepare<64>(const CUtensorMap&, const CUtensorMap&, const void*, const void*, float*, uint8_t*,
-                                 const la_shape&, int, int*, cudaStream_t);
+                                 const la_shape&, int, bool, int*, cudaStream_t);
 template cudaError_t prepare<128>(const CUtensorMap&, const CUtensorMap&, const void*, const void*, float*, uint8_t*,
-                                  const la_shape&, int, int*, cudaStream_t);
+                                  const la_shape&, int, bool, int*, cudaStream_t);
 
 template <int D>
 cudaError_t states(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -819,10 +819,11 @@ cudaError_t fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
     const Layout L = layout(s, false);
     float* recs = (float*)(ws + L.rec);
     uint8_t* mats = (uint8_t*)(ws + L.t);
-    GD_TRY(prepare<D>(tq, tk, a.g, a.beta, recs, mats, s, M, err, st));
+    GD_TRY(prepare<D>(tq, tk, a.g, a.beta, recs, mats, s, M, false, err, st));
     StateArgs sa{};
     sa.recs = recs;
     sa.mats = mats;
+    sa.mat_bytes = kMatsFwd;
     sa.M = M;
     sa.P = L.segs;
     sa.cps = L.cps;

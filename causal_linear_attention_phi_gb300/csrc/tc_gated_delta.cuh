@@ -13,9 +13,12 @@ using tc::bf_hi;
 using tc::bf_lo;
 
 constexpr int kBlk = kC * 128;          // 64 rows x 64 bf16 columns, 128-byte swizzle
-constexpr int kMats = 4 * kBlk;         // t hi, t lo, P hi, P lo of a chunk
-constexpr int kTHi = 0, kTLo = kBlk, kPHi = 2 * kBlk, kPLo = 3 * kBlk;
-constexpr int kGateBytes = 5 * kC * 4;  // gam, tail, beta, beta gam, tail beta of the record
+// The 64 x 64 matrices of a chunk, a hi and a lo tile each.  The write strengths are folded into them, so that no
+// recurrence multiplies by beta: t beta and P beta (columns), and in the gradient's records t beta, P and beta t (rows).
+constexpr int kMatF = 0, kMatP = 2 * kBlk, kMatR = 4 * kBlk;
+constexpr int kMatsFwd = 4 * kBlk, kMatsBwd = 6 * kBlk;  // bytes of a chunk
+constexpr int kFwdGates = 3 * kC * 4;  // gam, -gam, tail beta of the record
+constexpr int kRevGates = 6 * kC * 4;  // and tail, beta, -beta gam
 
 // Contiguous global -> shared copy (16-byte aligned, a multiple of 16 bytes).
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -196,7 +199,7 @@ cudaError_t allow_smem(K kern, size_t bytes) {
 // t and P of every chunk (tc_gated_delta.cu).
 template <int D>
 cudaError_t prepare(const CUtensorMap& tq, const CUtensorMap& tk, const void* g, const void* beta, float* recs,
-                    uint8_t* mats, const la_shape& s, int M, int* err, cudaStream_t st);
+                    uint8_t* mats, const la_shape& s, int M, bool bwd, int* err, cudaStream_t st);
 // The recurrence's modes.  kOut: outputs.  kGrad: the gradient's records instead, for each chunk the state entering it
 // (s_tiles, S^T as [Dv rows x Dk] bf16 tiles of 64 columns) and X (x_tiles, lo then hi, X^T as [Dv rows x 64
 // positions]).  kSum: only the segment's last state, from a zero state (segB) and, with no values, from the identity
@@ -205,6 +208,7 @@ enum Mode { kOut, kGrad, kSum };
 struct StateArgs {
     const float* recs;
     const uint8_t* mats;
+    int mat_bytes;     // kMatsFwd or kMatsBwd
     const float* S0;   // [BH][P] records: the states entering the segments; null: zero
     float* S_out;      // kOut: [BH] records, the state after the last position, or null
     __nv_bfloat16* o;  // kOut: [BH][N][D]

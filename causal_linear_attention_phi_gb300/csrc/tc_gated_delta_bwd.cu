@@ -3,7 +3,7 @@
 //
 // tc_gd_reverse (one block per head and segment): the adjoint recurrence from the last chunk back, transposed like the
 // forward one, with dS'^T [Dv lanes x Dk] in registers:
-//   dU^T = tail (dS'^T K^T) + dO^T P        Y^T = dU^T + (beta dU)^T t      dV^T = beta Y^T
+//   dU^T = tail (dS'^T K^T) + dO^T P        Y^T = dU^T + dU^T (beta t)      dV^T = beta Y^T
 //   dS^T = gam_C dS'^T + (gam dO)^T Q - (beta gam Y)^T K
 // What is formed here enters the products as hi + lo bf16 parts, as in the forward kernel.  It writes dV and,
 // for tc_gd_grads, the tiles of Y^T [Dv rows x 64 positions], lo and hi, and of dS'^T [Dv rows x Dk], rounded to bf16
@@ -32,7 +32,8 @@ struct __align__(8) RBars {
 template <int D>
 struct RevSmem {
     static constexpr int tile = D / 64 * kBlk;
-    static constexpr int K = 0, Q = tile, dO = 2 * tile, mats = 3 * tile, gates = mats + kMats;
+    static constexpr int K = 0, Q = tile, dO = 2 * tile, mats = 3 * tile;  // P, then beta t
+    static constexpr int gates = mats + 4 * kBlk;
     static constexpr int stage = gates + 2048;
     static constexpr int out = 2 * stage;  // dS' tile; then dV tile and Y's lo and hi tiles
     static constexpr int sbytes = D * D * 2, ybytes = 2 * D * 128;
@@ -101,7 +102,7 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 const int s = i & 1, c = cend - 1 - i, t0 = c * kC;
                 uint8_t* st = base + s * L::stage;
                 if (!mbar_wait(&bar->empty[s], ((i >> 1) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
-                mbar_arrive_expect_tx(&bar->full[s], 3 * L::tile + kMats + kGateBytes);
+                mbar_arrive_expect_tx(&bar->full[s], 3 * L::tile + 4 * kBlk + kRevGates);
 #pragma unroll
                 for (int b = 0; b < D / 64; ++b) {
                     tma_load_3d(st + L::dO + b * kBlk, &tm_do, 64 * b, t0, bh, &bar->full[s]);
@@ -109,8 +110,8 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     tma_load_3d(st + L::Q + b * kBlk, &tm_q, 64 * b, t0, bh, &bar->full[s]);
                 }
                 const size_t at = (size_t)bh * M + c;
-                bulk_load(st + L::mats, mats + at * kMats, kMats, &bar->full[s]);
-                bulk_load(st + L::gates, recs + at * kRec, kGateBytes, &bar->full[s]);
+                bulk_load(st + L::mats, mats + at * kMatsBwd + kMatP, 4 * kBlk, &bar->full[s]);
+                bulk_load(st + L::gates, recs + at * kRec, kRevGates, &bar->full[s]);
                 armed[s] = i;
             }
             // never leave with copies in flight: wait for the last armed phase of each stage
@@ -135,15 +136,16 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             const int s = i & 1, ph = i & 1;
             const uint32_t sg = smem_u32(base + s * L::stage);
             const uint32_t dK = tile_desc(sg + L::K), dKmn = tile_desc<kBlk>(sg + L::K), dQmn = tile_desc<kBlk>(sg + L::Q);
-            const uint32_t dO = tile_desc<kBlk>(sg + L::dO), dM = tile_desc<kBlk>(sg + L::mats);
+            const uint32_t dO = tile_desc<kBlk>(sg + L::dO), dM = tile_desc<kBlk>(sg + L::mats),
+                           dT = tile_desc<kBlk>(sg + L::mats + 2 * kBlk);
             wait(&bar->full[s], (i >> 1) & 1);
             if (i > 0) wait(&bar->r_lo, ph ^ 1);  // Y, over A1 and A2, has been read
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // dO^T P
-                mma_ss1(lead, tmem + T::A2, dO + step_mn(kk), dM + (kPHi >> 4) + step_mn(kk), id_amn, kk > 0);
+                mma_ss1(lead, tmem + T::A2, dO + step_mn(kk), dM + step_mn(kk), id_amn, kk > 0);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_ss1(lead, tmem + T::A2, dO + step_mn(kk), dM + (kPLo >> 4) + step_mn(kk), id_amn, 1);
+                mma_ss1(lead, tmem + T::A2, dO + step_mn(kk), dM + (kBlk >> 4) + step_mn(kk), id_amn, 1);
             wait(&bar->s_hi, ph);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)  // dS'^T K^T
@@ -162,12 +164,12 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 mma_ts1(lead, tmem + T::dS, tmem + T::G + 32 + 8 * kk, dQmn + step_mn(kk), id_mnD, 1);
             wait(&bar->b_hi, ph);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // (beta dU)_hi^T [t_hi | t_lo]: two products of 64 columns
-                mma_ts1(lead, tmem + T::Y, tmem + T::B + 8 * kk, dM + step_mn(kk), id_mn2, kk > 0);
+            for (int kk = 0; kk < 4; ++kk)  // dU_hi^T [(beta t)_hi | (beta t)_lo]: two products of 64 columns
+                mma_ts1(lead, tmem + T::Y, tmem + T::B + 8 * kk, dT + step_mn(kk), id_mn2, kk > 0);
             wait(&bar->b_lo, ph);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_ts1(lead, tmem + T::Y, tmem + T::B + 32 + 8 * kk, dM + step_mn(kk), id_mn, 1);
+                mma_ts1(lead, tmem + T::Y, tmem + T::B + 32 + 8 * kk, dT + step_mn(kk), id_mn, 1);
             commit1(lead, &bar->y_done);
             wait(&bar->r_hi, ph);
 #pragma unroll
@@ -262,30 +264,29 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 tmem_st_wait();
                 arrive(&bar->g_ready);
             }
-            float2 dU[kTok / 2], b[kTok / 2];  // dU, then Y; positions in pairs
+            float2 dU[kTok / 2];  // dU, then Y; positions in pairs
             wait(&bar->a_done, ph);
             ld(lb + T::A1 + kTok * h, w);
             ld(lb + T::A2 + kTok * h, w2);
             tmem_ld_wait();
 #pragma unroll
             for (int x = 0; x < kTok; x += 4) {
-                const F4 t = gate(kTail, x), be = gate(kBeta, x);
+                const F4 t = gate(kTail, x);
                 dU[x / 2] = fma2v(t.a, pair(w[x], w[x + 1]), pair(w2[x], w2[x + 1]));
                 dU[x / 2 + 1] = fma2v(t.b, pair(w[x + 2], w[x + 3]), pair(w2[x + 2], w2[x + 3]));
-                b[x / 2] = mul2v(be.a, dU[x / 2]);
-                b[x / 2 + 1] = mul2v(be.b, dU[x / 2 + 1]);
             }
-            put_hi(lb + T::B + kTok / 2 * h, b, hi);
+            put_hi(lb + T::B + kTok / 2 * h, dU, hi);
             arrive(&bar->b_hi);
-            put_lo(lb + T::B + 32 + kTok / 2 * h, b, hi);
+            put_lo(lb + T::B + 32 + kTok / 2 * h, dU, hi);
             arrive(&bar->b_lo);
             wait(&bar->y_done, ph);
             ld(lb + T::Y + kTok * h, w);
             ld(lb + T::Y + kC + kTok * h, w2);
             tmem_ld_wait();
+            float2 b[kTok / 2];  // -beta gam Y
 #pragma unroll
             for (int x = 0; x < kTok; x += 4) {
-                const F4 bg = gate(kBg, x);  // -beta gam
+                const F4 bg = gate(kBg, x);
                 dU[x / 2] = add2v(dU[x / 2], add2v(pair(w[x], w[x + 1]), pair(w2[x], w2[x + 1])));
                 dU[x / 2 + 1] = add2v(dU[x / 2 + 1], add2v(pair(w[x + 2], w[x + 3]), pair(w2[x + 2], w2[x + 3])));
                 b[x / 2] = mul2v(bg.a, dU[x / 2]);
@@ -600,10 +601,13 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 tmem_ld_wait();
                 const float seg = rec[kSeg + row], hi = rec[kGhi + row], lo = rec[kGlo + row], br = rec[kBeta + row];
                 const float sgn = isF ? -1.f : 1.f;
+                const bool resets = rec[kSeg + kC - 1] != 0.f;
 #pragma unroll
                 for (int x0 = 0; x0 < 16; x0 += 4) {
-                    const float4 gh = ld_f4(rec + kGhi + col0 + x0), gl = ld_f4(rec + kGlo + col0 + x0),
-                                 sg = ld_f4(rec + kSeg + col0 + x0), be = ld_f4(rec + kBeta + col0 + x0);
+                    const float4 gh = ld_f4(rec + kGhi + col0 + x0), gl = ld_f4(rec + kGlo + col0 + x0);
+                    float4 sg = make_float4(seg, seg, seg, seg), be = make_float4(-1.f, -1.f, -1.f, -1.f);
+                    if (resets) sg = ld_f4(rec + kSeg + col0 + x0);
+                    if (!isF) be = ld_f4(rec + kBeta + col0 + x0);
                     const float ghv[4] = {gh.x, gh.y, gh.z, gh.w}, glv[4] = {gl.x, gl.y, gl.z, gl.w},
                                 sgv[4] = {sg.x, sg.y, sg.z, sg.w}, bev[4] = {be.x, be.y, be.z, be.w};
 #pragma unroll
@@ -613,8 +617,7 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                         if (!isF && col == row) part[L::dBeta + row] = raw;
                         const float d = (hi - ghv[e]) + (lo - glv[e]);  // G_row - G_col
                         const bool in = (isF ? col >= row : col < row) && sgv[e] == seg;
-                        const float s = isF ? br : -br * bev[e];
-                        const float val = in ? raw * (s * ex2_approx(d * sgn)) : 0.f;
+                        const float val = in ? raw * (-br * bev[e] * ex2_approx(d * sgn)) : 0.f;
                         v[x] = __float_as_uint(val);
                         pr[x] = in && col != row ? val * __uint_as_float(pq[x]) : 0.f;
                         rsum += pr[x];
@@ -776,10 +779,11 @@ cudaError_t bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
     float* recs = (float*)(ws + L.rec);
     uint8_t *mats = (uint8_t*)(ws + L.t), *X = (uint8_t*)(ws + L.X), *Y = (uint8_t*)(ws + L.Y), *S = (uint8_t*)(ws + L.S),
             *dS = (uint8_t*)(ws + L.dS);
-    GD_TRY(prepare<D>(tq, tk, a.g, a.beta, recs, mats, s, M, err, st));
+    GD_TRY(prepare<D>(tq, tk, a.g, a.beta, recs, mats, s, M, true, err, st));
     StateArgs sa{};
     sa.recs = recs;
     sa.mats = mats;
+    sa.mat_bytes = kMatsBwd;
     sa.x_tiles = X;
     sa.s_tiles = S;
     sa.M = M;

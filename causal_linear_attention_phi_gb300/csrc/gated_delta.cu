@@ -1,6 +1,6 @@
-// gated_delta.cu -- the gated delta rule on the CUDA cores, any dtype and head size (formulas in gated_delta.cuh).
+// gated_delta.cu -- the gated delta rule in fp32 on the CUDA cores, any head size (formulas in gated_delta.cuh).
 //
-// Forward: gd_prepare (one block per chunk: gates, t, P) and gd_states (one block per head and slice of kW value
+// Forward: gd_prepare (one block per chunk: gates, t, P) and gd_states (one block per head and slice of value
 // columns, which are independent of each other: it walks the chunks with its slice of S in shared memory and
 // writes o).  Gradient: gd_prepare, gd_states (X and the state entering every chunk), gd_reverse (the
 // adjoint recurrence from the last chunk back, sliced alike: dv, Y and the gradient leaving every chunk) and
@@ -12,7 +12,7 @@ namespace gd {
 namespace {
 
 constexpr int kThreads = 256;  // 16 x 16
-constexpr int kW = 16;         // value columns of a slice
+constexpr int kW = 16;         // value columns that gd_grads walks at a time
 constexpr int kLc = kC + 1;    // row pitch of 64 x 64 tiles
 constexpr int kLw = kW + 1;
 
@@ -26,11 +26,10 @@ struct Carve {
 };
 
 // Rows [c0, c0 + n) of a [N][D] matrix as fp32 into dst[kC][D + 1]; the rows past n are 0.
-template <typename T>
-__device__ __forceinline__ void load_rows(float* dst, const T* __restrict__ src, int c0, int n, int D) {
+__device__ __forceinline__ void load_rows(float* dst, const float* __restrict__ src, int c0, int n, int D) {
     for (int i = threadIdx.x; i < kC * D; i += kThreads) {
         const int r = i / D, d = i - r * D;
-        dst[r * (D + 1) + d] = r < n ? to_f32(src[(size_t)(c0 + r) * D + d]) : 0.f;
+        dst[r * (D + 1) + d] = r < n ? src[(size_t)(c0 + r) * D + d] : 0.f;
     }
 }
 
@@ -59,9 +58,9 @@ __device__ __forceinline__ void zero(float (&acc)[RT][CT]) {
 }
 
 // ------------------------------------------------------------------ gates, t and P of every chunk
-template <typename T>
 __global__ void __launch_bounds__(kThreads)
-gd_prepare(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ g, const T* __restrict__ beta,
+gd_prepare(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ g,
+           const float* __restrict__ beta,
            float* __restrict__ recs, float* __restrict__ ts, float* __restrict__ Ps, int N, int M, int Dk) {
     extern __shared__ __align__(16) float smem[];
     Carve sm{smem};
@@ -102,179 +101,247 @@ gd_prepare(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict
     for (int i = tid; i < kRec; i += kThreads) recs[at * kRec + i] = rec[i];
 }
 
-__device__ __forceinline__ void load_square(float* dst, const float* __restrict__ src) {
-    for (int i = threadIdx.x; i < kC * kC; i += kThreads) dst[(i >> 6) * kLc + (i & 63)] = src[i];
+// ------------------------------------------------------------------ products of the recurrences
+// Tiles in shared memory with rows of a multiple of 4 floats.  A thread forms 4 x 4 tiles, so that a multiply-add costs two
+// bytes of shared-memory reads (single columns of four rows cost five and were bound by them).
+// z[j] += sum_(x < K) a[(16 j) lda + x] b[x ldb + 0..3]
+__device__ __forceinline__ void mac_rows(F4 (&z)[4], const float* a, int lda, const float* b, int ldb, int K) {
+#pragma unroll 2
+    for (int x = 0; x < K; x += 4) {
+        float4 av[4], bv[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) av[j] = ld_f4(a + 16 * j * lda + x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bv[e] = ld_f4(b + (x + e) * ldb);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            fma4(z[j], av[j].x, bv[0]);
+            fma4(z[j], av[j].y, bv[1]);
+            fma4(z[j], av[j].z, bv[2]);
+            fma4(z[j], av[j].w, bv[3]);
+        }
+    }
+}
+// z[j] += sum_(x < K) a[x lda + j] b[x ldb + 0..3]: four consecutive columns of a as rows
+__device__ __forceinline__ void mac_cols(F4 (&z)[4], const float* a, int lda, const float* b, int ldb, int K) {
+#pragma unroll 4
+    for (int x = 0; x < K; ++x) {
+        const float4 av = ld_f4(a + x * lda), bv = ld_f4(b + x * ldb);
+        fma4(z[0], av.x, bv);
+        fma4(z[1], av.y, bv);
+        fma4(z[2], av.z, bv);
+        fma4(z[3], av.w, bv);
+    }
+}
+__device__ __forceinline__ void zero(F4 (&z)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z[j].a = z[j].b = make_float2(0.f, 0.f);
+}
+__device__ __forceinline__ F4 scaled(float m, const F4& z) {
+    return {make_float2(m * z.a.x, m * z.a.y), make_float2(m * z.b.x, m * z.b.y)};
+}
+
+constexpr int kLc4 = kC + 4;  // row pitch of the 64 x 64 tiles
+
+// Rows [c0, c0 + n) of a [N][D] matrix into dst, pitch D + 4; the rows past n are 0.
+template <int W>
+__device__ __forceinline__ void load_rows4(float* dst, const float* __restrict__ src, int c0, int n, int D) {
+    const int v = D / 4;
+    for (int i = threadIdx.x; i < kC * v; i += 4 * W) {
+        const int r = i / v, d = i - r * v;
+        const float4 x = r < n ? ld_f4(src + (size_t)(c0 + r) * D + 4 * d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(dst + r * (D + 4) + 4 * d) = x;
+    }
+}
+template <int W>
+__device__ __forceinline__ void load_square4(float* dst, const float* __restrict__ src) {
+    for (int i = threadIdx.x; i < kC * kC / 4; i += 4 * W)
+        *reinterpret_cast<float4*>(dst + (i >> 4) * kLc4 + 4 * (i & 15)) = ld_f4(src + 4 * i);
 }
 
 // ------------------------------------------------------------------ the recurrence over chunks
-// Block (slice, head): value columns [kW slice, +kW).  o, Xs / Ss (the gradient's records) and S_out may be null.
-template <typename T, int NK>  // Dk = 16 NK
-__global__ void __launch_bounds__(kThreads)
-gd_states(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const float* __restrict__ S0,
+// Block (slice, head): value columns [W slice, +W), 4 W threads.  o, Xs / Ss (the gradient's records) and S_out may be null.
+template <int W>
+__global__ void __launch_bounds__(4 * W)
+gd_states(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v, const float* S0,
           const float* __restrict__ recs, const float* __restrict__ ts, const float* __restrict__ Ps,
-          T* __restrict__ o, float* __restrict__ Xs, float* __restrict__ Ss, float* S_out, int N, int M, int Dv) {
-    constexpr int Dk = 16 * NK;
+          float* __restrict__ o, float* __restrict__ Xs, float* __restrict__ Ss, float* S_out, int N, int M, int Dk,
+          int Dv) {
+    constexpr int kLw = W + 4;
     extern __shared__ __align__(16) float smem[];
     Carve sm{smem};
-    float* ks = sm.take(kC * (Dk + 1));
-    float* qs = sm.take(kC * (Dk + 1));
-    float* tt = sm.take(kC * kLc);
-    float* PP = sm.take(kC * kLc);
+    const int ld = Dk + 4;
+    float* ks = sm.take(kC * ld);
+    float* qs = sm.take(kC * ld);
+    float* tt = sm.take(kC * kLc4);
+    float* PP = sm.take(kC * kLc4);
     float* S = sm.take(Dk * kLw);
-    float* Rb = sm.take(kC * kLw);  // beta R, then u = beta X
-    float* Ub = sm.take(kC * kLw);
+    float* Rb = sm.take(kC * kLw);  // beta R, then tail u
+    float* Ub = sm.take(kC * kLw);  // u
     float* rec = sm.take(kRec);
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int tid = threadIdx.x, rg = tid / (W / 4), c = 4 * (tid % (W / 4));
     const size_t bh = blockIdx.y;
-    const int col = blockIdx.x * kW + tx;
-    LA_DCHECK(col < Dv);
-    float s[NK][1];
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-        s[i][0] = S0 ? S0[(bh * Dk + ty + 16 * i) * Dv + col] : 0.f;
-        S[(ty + 16 * i) * kLw + tx] = s[i][0];
-    }
+    const int col = blockIdx.x * W + c;
+    LA_DCHECK(col + 3 < Dv);
+    for (int d = rg; d < Dk; d += 16)
+        *reinterpret_cast<float4*>(S + d * kLw + c) =
+            S0 ? ld_f4(S0 + (bh * Dk + d) * Dv + col) : make_float4(0.f, 0.f, 0.f, 0.f);
     for (int m = 0; m < M; ++m) {
         const int c0 = m * kC, n = min(kC, N - c0);
         const size_t at = bh * M + m;
         __syncthreads();
-        load_rows(ks, k + bh * N * Dk, c0, n, Dk);
-        load_square(tt, ts + at * kC * kC);
-        for (int i = tid; i < kRec; i += kThreads) rec[i] = recs[at * kRec + i];
+        load_rows4<W>(ks, k + bh * N * Dk, c0, n, Dk);
+        load_square4<W>(tt, ts + at * kC * kC);
+        for (int i = tid; i < kRec; i += 4 * W) rec[i] = recs[at * kRec + i];
         if (o) {
-            load_rows(qs, q + bh * N * Dk, c0, n, Dk);
-            load_square(PP, Ps + at * kC * kC);
+            load_rows4<W>(qs, q + bh * N * Dk, c0, n, Dk);
+            load_square4<W>(PP, Ps + at * kC * kC);
         }
-        if (Ss) {
-#pragma unroll
-            for (int i = 0; i < NK; ++i) Ss[(at * Dk + ty + 16 * i) * Dv + col] = s[i][0];
-        }
+        if (Ss)
+            for (int d = rg; d < Dk; d += 16)
+                *reinterpret_cast<float4*>(Ss + (at * Dk + d) * Dv + col) = ld_f4(S + d * kLw + c);
         __syncthreads();
-        float x[4][1], w[4][1];
+        F4 x[4], w[4];
         zero(w);
-        mac(w, Dk, [&](int i, int d) { return ks[(ty + 16 * i) * (Dk + 1) + d]; },
-            [&](int d, int) { return S[d * kLw + tx]; });
+        mac_rows(w, ks + rg * ld, ld, S + c, kLw, Dk);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = ty + 16 * i;
-            const float vv = r < n ? to_f32(v[(bh * N + c0 + r) * (size_t)Dv + col]) : 0.f;
-            x[i][0] = fmaf(-rec[kGam + r], w[i][0], vv);
-            Rb[r * kLw + tx] = rec[kBeta + r] * x[i][0];
+        for (int j = 0; j < 4; ++j) {
+            const int r = rg + 16 * j;
+            x[j] = scaled(-rec[kGam + r], w[j]);
+            if (r < n) {
+                const float4 vv = ld_f4(v + (bh * N + c0 + r) * (size_t)Dv + col);
+                x[j].a.x += vv.x;
+                x[j].a.y += vv.y;
+                x[j].b.x += vv.z;
+                x[j].b.y += vv.w;
+            }
+            put4(Rb + r * kLw + c, x[j], rec[kBeta + r]);
         }
         __syncthreads();
-        mac(x, kC, [&](int i, int j) { return tt[(ty + 16 * i) * kLc + j]; },
-            [&](int j, int) { return Rb[j * kLw + tx]; });
+        mac_rows(x, tt + rg * kLc4, kLc4, Rb + c, kLw, kC);
+        __syncthreads();  // Rb has been read
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = ty + 16 * i;
-            if (Xs) Xs[(at * kC + r) * Dv + col] = x[i][0];
-            Ub[r * kLw + tx] = rec[kBeta + r] * x[i][0];
+        for (int j = 0; j < 4; ++j) {
+            const int r = rg + 16 * j;
+            if (Xs) put4(Xs + (at * kC + r) * Dv + col, x[j]);
+            put4(Ub + r * kLw + c, x[j], rec[kBeta + r]);
+            put4(Rb + r * kLw + c, x[j], rec[kTb + r]);
         }
         __syncthreads();
         if (o) {
             zero(w);
-            mac(w, Dk, [&](int i, int d) { return qs[(ty + 16 * i) * (Dk + 1) + d]; },
-                [&](int d, int) { return S[d * kLw + tx]; });
+            mac_rows(w, qs + rg * ld, ld, S + c, kLw, Dk);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i][0] *= rec[kGam + ty + 16 * i];
-            mac(w, kC, [&](int i, int j) { return PP[(ty + 16 * i) * kLc + j]; },
-                [&](int j, int) { return Ub[j * kLw + tx]; });
+            for (int j = 0; j < 4; ++j) w[j] = scaled(rec[kGam + rg + 16 * j], w[j]);
+            mac_rows(w, PP + rg * kLc4, kLc4, Ub + c, kLw, kC);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = ty + 16 * i;
-                if (r < n) o[(bh * N + c0 + r) * (size_t)Dv + col] = from_f32<T>(w[i][0]);
+            for (int j = 0; j < 4; ++j) {
+                const int r = rg + 16 * j;
+                if (r < n) put4(o + (bh * N + c0 + r) * (size_t)Dv + col, w[j]);
             }
+            __syncthreads();  // the old slice has been read
         }
         const float gc = rec[kGam + kC - 1];
+        for (int g = rg; g < Dk / 4; g += 16) {
 #pragma unroll
-        for (int i = 0; i < NK; ++i) s[i][0] *= gc;
-        mac(s, kC, [&](int i, int j) { return ks[j * (Dk + 1) + ty + 16 * i]; },
-            [&](int j, int) { return rec[kTail + j] * Ub[j * kLw + tx]; });
-        __syncthreads();  // the old slice has been read
+            for (int j = 0; j < 4; ++j) w[j] = scaled(gc, get4(S + (4 * g + j) * kLw + c));
+            mac_cols(w, ks + 4 * g, ld, Rb + c, kLw, kC);
 #pragma unroll
-        for (int i = 0; i < NK; ++i) S[(ty + 16 * i) * kLw + tx] = s[i][0];
+            for (int j = 0; j < 4; ++j) put4(S + (4 * g + j) * kLw + c, w[j]);
+        }
     }
-    if (S_out) {
-#pragma unroll
-        for (int i = 0; i < NK; ++i) S_out[(bh * Dk + ty + 16 * i) * Dv + col] = s[i][0];
-    }
+    __syncthreads();
+    if (S_out)
+        for (int d = rg; d < Dk; d += 16)
+            *reinterpret_cast<float4*>(S_out + (bh * Dk + d) * Dv + col) = ld_f4(S + d * kLw + c);
 }
 
 // ------------------------------------------------------------------ the adjoint recurrence, last chunk first
-template <typename T, int NK>
-__global__ void __launch_bounds__(kThreads)
-gd_reverse(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ dout,
+template <int W>
+__global__ void __launch_bounds__(4 * W)
+gd_reverse(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ dout,
            const float* __restrict__ recs, const float* __restrict__ ts, const float* __restrict__ Ps,
-           T* __restrict__ dv, float* __restrict__ Ys, float* __restrict__ dSs, int N, int M, int Dv) {
-    constexpr int Dk = 16 * NK;
+           float* __restrict__ dv, float* __restrict__ Ys, float* __restrict__ dSs, int N, int M, int Dk, int Dv) {
+    constexpr int kLw = W + 4;
     extern __shared__ __align__(16) float smem[];
     Carve sm{smem};
-    float* ks = sm.take(kC * (Dk + 1));
-    float* qs = sm.take(kC * (Dk + 1));
-    float* tt = sm.take(kC * kLc);
-    float* PP = sm.take(kC * kLc);
+    const int ld = Dk + 4;
+    float* ks = sm.take(kC * ld);
+    float* qs = sm.take(kC * ld);
+    float* tt = sm.take(kC * kLc4);
+    float* PP = sm.take(kC * kLc4);
     float* S = sm.take(Dk * kLw);   // this slice of dS'
-    float* Db = sm.take(kC * kLw);  // dO
+    float* Db = sm.take(kC * kLw);  // dO, then gam dO
     float* Ub = sm.take(kC * kLw);  // beta dU, then -gam dR
     float* rec = sm.take(kRec);
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int tid = threadIdx.x, rg = tid / (W / 4), c = 4 * (tid % (W / 4));
     const size_t bh = blockIdx.y;
-    const int col = blockIdx.x * kW + tx;
-    LA_DCHECK(col < Dv);
-    float s[NK][1];
-    zero(s);
-#pragma unroll
-    for (int i = 0; i < NK; ++i) S[(ty + 16 * i) * kLw + tx] = 0.f;
+    const int col = blockIdx.x * W + c;
+    LA_DCHECK(col + 3 < Dv);
+    for (int d = rg; d < Dk; d += 16) *reinterpret_cast<float4*>(S + d * kLw + c) = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int m = M - 1; m >= 0; --m) {
         const int c0 = m * kC, n = min(kC, N - c0);
         const size_t at = bh * M + m;
         __syncthreads();
-        load_rows(ks, k + bh * N * Dk, c0, n, Dk);
-        load_rows(qs, q + bh * N * Dk, c0, n, Dk);
-        load_square(tt, ts + at * kC * kC);
-        load_square(PP, Ps + at * kC * kC);
-        for (int i = tid; i < kRec; i += kThreads) rec[i] = recs[at * kRec + i];
+        load_rows4<W>(ks, k + bh * N * Dk, c0, n, Dk);
+        load_rows4<W>(qs, q + bh * N * Dk, c0, n, Dk);
+        load_square4<W>(tt, ts + at * kC * kC);
+        load_square4<W>(PP, Ps + at * kC * kC);
+        for (int i = tid; i < kRec; i += 4 * W) rec[i] = recs[at * kRec + i];
+        for (int r = rg; r < kC; r += 16)
+            *reinterpret_cast<float4*>(Db + r * kLw + c) =
+                r < n ? ld_f4(dout + (bh * N + c0 + r) * (size_t)Dv + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int d = rg; d < Dk; d += 16)
+            *reinterpret_cast<float4*>(dSs + (at * Dk + d) * Dv + col) = ld_f4(S + d * kLw + c);
+        __syncthreads();
+        // rows 4 rg .. 4 rg + 3 from here on
+        F4 y[4];
+        zero(y);
+        {
+            const float* kr = ks + 4 * rg * ld;
+#pragma unroll 2
+            for (int x = 0; x < Dk; x += 4) {
+                float4 av[4], bv[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = ty + 16 * i;
-            Db[r * kLw + tx] = r < n ? to_f32(dout[(bh * N + c0 + r) * (size_t)Dv + col]) : 0.f;
+                for (int j = 0; j < 4; ++j) av[j] = ld_f4(kr + j * ld + x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) bv[e] = ld_f4(S + (x + e) * kLw + c);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    fma4(y[j], av[j].x, bv[0]);
+                    fma4(y[j], av[j].y, bv[1]);
+                    fma4(y[j], av[j].z, bv[2]);
+                    fma4(y[j], av[j].w, bv[3]);
+                }
+            }
         }
 #pragma unroll
-        for (int i = 0; i < NK; ++i) dSs[(at * Dk + ty + 16 * i) * Dv + col] = s[i][0];
-        __syncthreads();
-        float y[4][1];
-        zero(y);
-        mac(y, Dk, [&](int i, int d) { return ks[(ty + 16 * i) * (Dk + 1) + d]; },
-            [&](int d, int) { return S[d * kLw + tx]; });
+        for (int j = 0; j < 4; ++j) y[j] = scaled(rec[kTail + 4 * rg + j], y[j]);
+        mac_cols(y, PP + 4 * rg, kLc4, Db + c, kLw, kC);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i][0] *= rec[kTail + ty + 16 * i];
-        mac(y, kC, [&](int i, int j) { return PP[j * kLc + ty + 16 * i]; },
-            [&](int j, int) { return Db[j * kLw + tx]; });
-#pragma unroll
-        for (int i = 0; i < 4; ++i) Ub[(ty + 16 * i) * kLw + tx] = rec[kBeta + ty + 16 * i] * y[i][0];
+        for (int j = 0; j < 4; ++j) put4(Ub + (4 * rg + j) * kLw + c, y[j], rec[kBeta + 4 * rg + j]);
         __syncthreads();
-        mac(y, kC, [&](int i, int j) { return tt[j * kLc + ty + 16 * i]; },
-            [&](int j, int) { return Ub[j * kLw + tx]; });
-        __syncthreads();
+        mac_cols(y, tt + 4 * rg, kLc4, Ub + c, kLw, kC);
+        __syncthreads();  // Ub and Db have been read
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = ty + 16 * i;
-            const float dr = rec[kBeta + r] * y[i][0];
-            Ys[(at * kC + r) * Dv + col] = y[i][0];
-            if (r < n) dv[(bh * N + c0 + r) * (size_t)Dv + col] = from_f32<T>(dr);
-            Ub[r * kLw + tx] = -rec[kGam + r] * dr;
-            Db[r * kLw + tx] *= rec[kGam + r];
+        for (int j = 0; j < 4; ++j) {
+            const int r = 4 * rg + j;
+            put4(Ys + (at * kC + r) * Dv + col, y[j]);
+            if (r < n) put4(dv + (bh * N + c0 + r) * (size_t)Dv + col, y[j], rec[kBeta + r]);
+            put4(Ub + r * kLw + c, y[j], rec[kBg + r]);
+            put4(Db + r * kLw + c, get4(Db + r * kLw + c), rec[kGam + r]);
         }
         __syncthreads();
         const float gc = rec[kGam + kC - 1];
+        for (int g = rg; g < Dk / 4; g += 16) {
+            F4 s[4];
 #pragma unroll
-        for (int i = 0; i < NK; ++i) s[i][0] *= gc;
-        mac(s, kC, [&](int i, int j) { return qs[j * (Dk + 1) + ty + 16 * i]; },
-            [&](int j, int) { return Db[j * kLw + tx]; });
-        mac(s, kC, [&](int i, int j) { return ks[j * (Dk + 1) + ty + 16 * i]; },
-            [&](int j, int) { return Ub[j * kLw + tx]; });
+            for (int j = 0; j < 4; ++j) s[j] = scaled(gc, get4(S + (4 * g + j) * kLw + c));
+            mac_cols(s, qs + 4 * g, ld, Db + c, kLw, kC);
+            mac_cols(s, ks + 4 * g, ld, Ub + c, kLw, kC);
 #pragma unroll
-        for (int i = 0; i < NK; ++i) S[(ty + 16 * i) * kLw + tx] = s[i][0];
+            for (int j = 0; j < 4; ++j) put4(S + (4 * g + j) * kLw + c, s[j]);
+        }
     }
 }
 
@@ -286,12 +353,12 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
-template <typename T, int NK>
+template <int NK>  // Dk = 16 NK
 __global__ void __launch_bounds__(kThreads)
-gd_grads(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ g, const T* __restrict__ dout,
+gd_grads(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ g, const float* __restrict__ dout,
          const float* __restrict__ recs, const float* __restrict__ Xs, const float* __restrict__ Ys,
-         const float* __restrict__ Ss, const float* __restrict__ dSs, T* __restrict__ dq, T* __restrict__ dk,
-         T* __restrict__ dg, T* __restrict__ dbeta, int N, int M, int Dv) {
+         const float* __restrict__ Ss, const float* __restrict__ dSs, float* __restrict__ dq, float* __restrict__ dk,
+         float* __restrict__ dg, float* __restrict__ dbeta, int N, int M, int Dv) {
     constexpr int Dk = 16 * NK;
     constexpr int kSt = 16;  // state columns staged at a time
     extern __shared__ __align__(16) float smem[];
@@ -334,7 +401,7 @@ gd_grads(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__
             const int r = ty + 16 * i, c = w0 + tx;
             const float b = rec[kBeta + r];
             const float x = Xs[(at * kC + r) * Dv + c], y = Ys[(at * kC + r) * Dv + c];
-            ds[r * kLw + tx] = r < n ? to_f32(dout[(bh * N + c0 + r) * (size_t)Dv + c]) : 0.f;
+            ds[r * kLw + tx] = r < n ? dout[(bh * N + c0 + r) * (size_t)Dv + c] : 0.f;
             us[r * kLw + tx] = b * x;
             rs[r * kLw + tx] = b * y;
             const float s = row_sum(x * y);
@@ -433,8 +500,8 @@ gd_grads(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__
         if (r >= n) continue;
 #pragma unroll
         for (int j = 0; j < NK; ++j) {
-            dq[(bh * N + c0 + r) * (size_t)Dk + tx + 16 * j] = from_f32<T>(qi[i][j]);
-            dk[(bh * N + c0 + r) * (size_t)Dk + tx + 16 * j] = from_f32<T>(ki[i][j]);
+            dq[(bh * N + c0 + r) * (size_t)Dk + tx + 16 * j] = qi[i][j];
+            dk[(bh * N + c0 + r) * (size_t)Dk + tx + 16 * j] = ki[i][j];
         }
     }
     if (tid < kC) {
@@ -465,18 +532,18 @@ gd_grads(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__
             const int i = 2 * tid + x;
             if (i >= n) continue;
             const size_t pos = bh * N + c0 + i;
-            const bool reset = to_f32(g[pos]) < kReset;
+            const bool reset = g[pos] < kReset;
             const double d = after + (x ? hi : lo) + tail;
-            dg[pos] = from_f32<T>(reset ? 0.f : (float)d);
-            dbeta[pos] = from_f32<T>(db[i]);
+            dg[pos] = reset ? 0.f : (float)d;
+            dbeta[pos] = db[i];
         }
     }
 }
 
 int f4(int n) { return (n + 3) / 4 * 4; }
 size_t smem_prepare(int Dk) { return 4 * (size_t)(2 * f4(kC * (Dk + 1)) + kC * kLd + kRec); }
-size_t smem_states(int Dk) {
-    return 4 * (size_t)(2 * f4(kC * (Dk + 1)) + 2 * f4(kC * kLc) + f4(Dk * kLw) + 2 * f4(kC * kLw) + kRec);
+size_t smem_states(int Dk, int W) {
+    return 4 * (size_t)(2 * kC * (Dk + 4) + 2 * kC * kLc4 + Dk * (W + 4) + 2 * kC * (W + 4) + kRec);
 }
 size_t smem_grads(int Dk) {
     return 4 * (size_t)(2 * f4(kC * (Dk + 1)) + 2 * f4(kC * kLc) + 3 * f4(kC * kLw) + 2 * f4(Dk * 17) + kRec +
@@ -495,59 +562,65 @@ cudaError_t allow_smem(K kern, size_t bytes) {
         if (_e != cudaSuccess) return _e;      \
     } while (0)
 
-template <typename T>
 cudaError_t prepare(const void* q, const void* k, const void* g, const void* beta, const Layout& L, char* ws,
                     const la_shape& s, int M, cudaStream_t st) {
     const size_t sm = smem_prepare(s.Dk);
-    GD_TRY(allow_smem(gd_prepare<T>, sm));
+    GD_TRY(allow_smem(gd_prepare, sm));
     launch_begin("gd_prepare", st);
-    gd_prepare<T><<<dim3(M, s.B * s.H), kThreads, sm, st>>>(
-        (const T*)q, (const T*)k, (const T*)g, (const T*)beta, (float*)(ws + L.rec), (float*)(ws + L.t),
-        (float*)(ws + L.P), s.N, M, s.Dk);
+    gd_prepare<<<dim3(M, s.B * s.H), kThreads, sm, st>>>((const float*)q, (const float*)k, (const float*)g,
+                                                         (const float*)beta, (float*)(ws + L.rec), (float*)(ws + L.t),
+                                                         (float*)(ws + L.P), s.N, M, s.Dk);
     return launch_end("gd_prepare", st);
 }
 
-template <typename T, int NK>
-cudaError_t fwd_t(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) {
-    const int M = (s.N + kC - 1) / kC;
-    const Layout L = layout(s, false);
-    GD_TRY(prepare<T>(a.q, a.k, a.g, a.beta, L, ws, s, M, st));
-    const size_t sm = smem_states(s.Dk);
-    auto kern = gd_states<T, NK>;
-    GD_TRY(allow_smem(kern, sm));
-    launch_begin("gd_states", st);
-    kern<<<dim3(s.Dv / kW, s.B * s.H), kThreads, sm, st>>>(
-        (const T*)a.q, (const T*)a.k, (const T*)a.v, a.S0, (const float*)(ws + L.rec), (const float*)(ws + L.t),
-        (const float*)(ws + L.P), (T*)a.o, nullptr, nullptr, a.S, s.N, M, s.Dv);
-    return launch_end("gd_states", st);
+// Value columns of a slice: wide ones read K, Q, t and P less often, narrow ones make more blocks where heads are few.
+int slice(const la_shape& s) {
+    int w = s.Dv < 64 ? s.Dv : 64;
+    while (w > 16 && (long long)s.B * s.H * (s.Dv / w) < 152) w /= 2;
+    return w;
 }
 
-template <typename T, int NK>
-cudaError_t bwd_t(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) {
-    const int M = (s.N + kC - 1) / kC, BH = s.B * s.H;
-    const Layout L = layout(s, true);
-    float *rec = (float*)(ws + L.rec), *t = (float*)(ws + L.t), *P = (float*)(ws + L.P);
-    float *X = (float*)(ws + L.X), *Y = (float*)(ws + L.Y), *S = (float*)(ws + L.S), *dS = (float*)(ws + L.dS);
-    GD_TRY(prepare<T>(a.q, a.k, a.g, a.beta, L, ws, s, M, st));
-    const size_t sm = smem_states(s.Dk);
-    auto states = gd_states<T, NK>;
-    GD_TRY(allow_smem(states, sm));
+template <int W>
+cudaError_t launch_states(const void* q, const void* k, const void* v, const float* S0, void* o, float* X, float* S,
+                          float* S_out, const la_shape& s, const Layout& L, char* ws, int M, cudaStream_t st) {
+    const size_t sm = smem_states(s.Dk, W);
+    GD_TRY(allow_smem(gd_states<W>, sm));
     launch_begin("gd_states", st);
-    states<<<dim3(s.Dv / kW, BH), kThreads, sm, st>>>((const T*)a.q, (const T*)a.k, (const T*)a.v, nullptr, rec, t,
-                                                       P, nullptr, X, S, nullptr, s.N, M, s.Dv);
-    GD_TRY(launch_end("gd_states", st));
-    auto reverse = gd_reverse<T, NK>;
-    GD_TRY(allow_smem(reverse, sm));
+    gd_states<W><<<dim3(s.Dv / W, s.B * s.H), 4 * W, sm, st>>>(
+        (const float*)q, (const float*)k, (const float*)v, S0, (const float*)(ws + L.rec), (const float*)(ws + L.t),
+        (const float*)(ws + L.P), (float*)o, X, S, S_out, s.N, M, s.Dk, s.Dv);
+    return launch_end("gd_states", st);
+}
+cudaError_t states(const void* q, const void* k, const void* v, const float* S0, void* o, float* X, float* S,
+                   float* S_out, const la_shape& s, const Layout& L, char* ws, int M, cudaStream_t st) {
+    switch (slice(s)) {
+        case 16: return launch_states<16>(q, k, v, S0, o, X, S, S_out, s, L, ws, M, st);
+        case 32: return launch_states<32>(q, k, v, S0, o, X, S, S_out, s, L, ws, M, st);
+        default: return launch_states<64>(q, k, v, S0, o, X, S, S_out, s, L, ws, M, st);
+    }
+}
+
+template <int W>
+cudaError_t launch_reverse(const BwdArgs& a, const la_shape& s, const Layout& L, char* ws, int M, cudaStream_t st) {
+    const size_t sm = smem_states(s.Dk, W);
+    GD_TRY(allow_smem(gd_reverse<W>, sm));
     launch_begin("gd_reverse", st);
-    reverse<<<dim3(s.Dv / kW, BH), kThreads, sm, st>>>((const T*)a.q, (const T*)a.k, (const T*)a.dout, rec, t, P,
-                                                        (T*)a.dv, Y, dS, s.N, M, s.Dv);
-    GD_TRY(launch_end("gd_reverse", st));
-    const size_t smg = smem_grads(s.Dk);
-    auto grads = gd_grads<T, NK>;
-    GD_TRY(allow_smem(grads, smg));
+    gd_reverse<W><<<dim3(s.Dv / W, s.B * s.H), 4 * W, sm, st>>>(
+        (const float*)a.q, (const float*)a.k, (const float*)a.dout, (const float*)(ws + L.rec),
+        (const float*)(ws + L.t), (const float*)(ws + L.P), (float*)a.dv, (float*)(ws + L.Y), (float*)(ws + L.dS), s.N, M,
+        s.Dk, s.Dv);
+    return launch_end("gd_reverse", st);
+}
+
+template <int NK>
+cudaError_t launch_grads(const BwdArgs& a, const la_shape& s, const Layout& L, char* ws, int M, cudaStream_t st) {
+    const size_t sm = smem_grads(s.Dk);
+    GD_TRY(allow_smem(gd_grads<NK>, sm));
     launch_begin("gd_grads", st);
-    grads<<<dim3(M, BH), kThreads, smg, st>>>((const T*)a.q, (const T*)a.k, (const T*)a.g, (const T*)a.dout, rec, X,
-                                              Y, S, dS, (T*)a.dq, (T*)a.dk, (T*)a.dg, (T*)a.dbeta, s.N, M, s.Dv);
+    gd_grads<NK><<<dim3(M, s.B * s.H), kThreads, sm, st>>>(
+        (const float*)a.q, (const float*)a.k, (const float*)a.g, (const float*)a.dout, (const float*)(ws + L.rec),
+        (const float*)(ws + L.X), (const float*)(ws + L.Y), (const float*)(ws + L.S), (const float*)(ws + L.dS),
+        (float*)a.dq, (float*)a.dk, (float*)a.dg, (float*)a.dbeta, s.N, M, s.Dv);
     return launch_end("gd_grads", st);
 }
 
@@ -563,21 +636,22 @@ Layout layout(const la_shape& s, bool bwd) {
         return at;
     };
     L.rec = take(chunks * kRec);
+    const int dk = tc_ok(s) ? tc_dim(s) : s.Dk, dv = tc_ok(s) ? tc_dim(s) : s.Dv;
     L.t = take((tc_ok(s) && bwd ? 3 : 2) * chunks * kC * kC);
     L.P = L.t + chunks * kC * kC * sizeof(float);
     if (bwd) {
-        L.X = take(chunks * kC * s.Dv);
+        L.X = take(chunks * kC * dv);
         const size_t half = tc_ok(s) ? 2 : 1;  // the states in bf16
-        L.Y = take(chunks * kC * s.Dv);
-        L.S = take(chunks * s.Dk * s.Dv / half);
-        L.dS = take(chunks * s.Dk * s.Dv / half);
+        L.Y = take(chunks * kC * dv);
+        L.S = take(chunks * dk * dv / half);
+        L.dS = take(chunks * dk * dv / half);
     }
     const int M = (s.N + kC - 1) / kC;
     L.segs = tc_ok(s) ? tc_segments(s, bwd) : 1;
     L.cps = (M + L.segs - 1) / L.segs;
     L.segs = (M + L.cps - 1) / L.cps;  // no empty segment
     if (L.segs > 1) {
-        const size_t seg = (size_t)s.B * s.H * L.segs * s.Dk * s.Dv;
+        const size_t seg = (size_t)s.B * s.H * L.segs * dk * dv;
         L.segB = take(seg);
         L.segM = take(seg);
         L.segS = take(seg);
@@ -590,29 +664,29 @@ Layout layout(const la_shape& s, bool bwd) {
     return L;
 }
 
-#define GD_DISPATCH(fn, ...)                                                             \
-    do {                                                                                 \
-        if (s.dtype == LA_BF16) {                                                        \
-            switch (s.Dk) {                                                              \
-                case 16: return fn<__nv_bfloat16, 1>(__VA_ARGS__);                       \
-                case 32: return fn<__nv_bfloat16, 2>(__VA_ARGS__);                       \
-                case 64: return fn<__nv_bfloat16, 4>(__VA_ARGS__);                       \
-                default: return fn<__nv_bfloat16, 8>(__VA_ARGS__);                       \
-            }                                                                            \
-        }                                                                                \
-        switch (s.Dk) {                                                                  \
-            case 16: return fn<float, 1>(__VA_ARGS__);                                   \
-            case 32: return fn<float, 2>(__VA_ARGS__);                                   \
-            case 64: return fn<float, 4>(__VA_ARGS__);                                   \
-            default: return fn<float, 8>(__VA_ARGS__);                                   \
-        }                                                                                \
-    } while (0)
-
 cudaError_t simt_fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) {
-    GD_DISPATCH(fwd_t, a, s, ws, st);
+    const int M = (s.N + kC - 1) / kC;
+    const Layout L = layout(s, false);
+    GD_TRY(prepare(a.q, a.k, a.g, a.beta, L, ws, s, M, st));
+    return states(a.q, a.k, a.v, a.S0, a.o, nullptr, nullptr, a.S, s, L, ws, M, st);
 }
+
 cudaError_t simt_bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) {
-    GD_DISPATCH(bwd_t, a, s, ws, st);
+    const int M = (s.N + kC - 1) / kC;
+    const Layout L = layout(s, true);
+    GD_TRY(prepare(a.q, a.k, a.g, a.beta, L, ws, s, M, st));
+    GD_TRY(states(a.q, a.k, a.v, nullptr, nullptr, (float*)(ws + L.X), (float*)(ws + L.S), nullptr, s, L, ws, M, st));
+    switch (slice(s)) {
+        case 16: GD_TRY(launch_reverse<16>(a, s, L, ws, M, st)); break;
+        case 32: GD_TRY(launch_reverse<32>(a, s, L, ws, M, st)); break;
+        default: GD_TRY(launch_reverse<64>(a, s, L, ws, M, st)); break;
+    }
+    switch (s.Dk) {
+        case 16: return launch_grads<1>(a, s, L, ws, M, st);
+        case 32: return launch_grads<2>(a, s, L, ws, M, st);
+        case 64: return launch_grads<4>(a, s, L, ws, M, st);
+        default: return launch_grads<8>(a, s, L, ws, M, st);
+    }
 }
 
 }  // namespace gd

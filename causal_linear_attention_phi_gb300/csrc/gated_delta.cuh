@@ -275,11 +275,12 @@ struct BwdArgs {
     const void *q, *k, *v, *g, *beta, *dout;
     void *dq, *dk, *dv, *dg, *dbeta;
 };
-// Any dtype and head size, on the CUDA cores.
+// fp32, any head size, on the CUDA cores.
 cudaError_t simt_fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st);
 cudaError_t simt_bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st);
-// bf16 heads with Dk = Dv = 64 or 128, on the tensor cores.
+// bf16, on the tensor cores: heads are padded on chip to 64 or 128 in both dimensions (tc_dim).
 bool tc_ok(const la_shape& s);
+int tc_dim(const la_shape& s);
 // Segments of a head for M chunks (a function of the sizes alone).
 int tc_segments(const la_shape& s, bool bwd);
 cudaError_t tc_fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st);

@@ -421,8 +421,9 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 const int d = map ? r : D == 64 ? r - D : -1;
                 S[x] = make_float2(c == d ? 1.f : 0.f, c + 1 == d ? 1.f : 0.f);
             } else {
-                const float* s0 = a.S0 + (((size_t)bh * a.P + p) * D + c) * D + r;
-                S[x] = a.S0 && r < D ? make_float2(s0[0], s0[D]) : make_float2(0.f, 0.f);
+                // the caller's state has the true sizes, the segments' the padded ones
+                const float* s0 = a.S0 + (((size_t)bh * a.P + p) * a.dk + c) * a.dv + r;
+                S[x] = a.S0 && r < a.dv && c < a.dk ? make_float2(s0[0], s0[a.dv]) : make_float2(0.f, 0.f);
             }
         }
         {
@@ -442,11 +443,11 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             tmem_ld_wait();
             arrive(&bar->o_free);
             const int t0 = (cbeg + j) * kC + kTok * h, n = a.N - t0;
-            __nv_bfloat16* o = a.o + ((size_t)bh * a.N + t0) * D + r;
-            if (r < D) {
+            __nv_bfloat16* o = a.o + ((size_t)bh * a.N + t0) * a.Dv + r;
+            if (r < a.Dv) {
 #pragma unroll
                 for (int x = 0; x < kTok; ++x)
-                    if (x < n) o[x * D] = __float2bfloat16_rn(__uint_as_float(w[x]) + __uint_as_float(w2[x]));
+                    if (x < n) o[x * a.Dv] = __float2bfloat16_rn(__uint_as_float(w[x]) + __uint_as_float(w2[x]));
             }
         };
         for (int i = 0; i < nloc; ++i) {
@@ -604,10 +605,12 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 else
                     a.segB[at + d * D + c] = x & 1 ? S[x / 2].y : S[x / 2].x;
             }
-        } else if (kMode == kOut && a.S_out && p == a.P - 1 && r < D) {
+        } else if (kMode == kOut && a.S_out && p == a.P - 1 && r < a.Dv) {
 #pragma unroll
-            for (int x = 0; x < kSc; ++x)
-                a.S_out[((size_t)bh * D + kSc * h + x) * D + r] = x & 1 ? S[x / 2].y : S[x / 2].x;
+            for (int x = 0; x < kSc; ++x) {
+                const int c = kSc * h + x;
+                if (c < a.Dk) a.S_out[((size_t)bh * a.Dk + c) * a.Dv + r] = x & 1 ? S[x / 2].y : S[x / 2].x;
+            }
         }
         tc_fence_before();
     }
@@ -638,7 +641,7 @@ struct JoinCfg {
 template <int D, bool kReverse, int kCols>
 __global__ void __launch_bounds__(JoinCfg<D, kCols>::threads)
 tc_gd_join(const float* __restrict__ B, const float* __restrict__ Mx, const float* __restrict__ first,
-           float* __restrict__ out, int P, int* err) {
+           float* __restrict__ out, int P, int Dk, int Dv, int* err) {
     using L = JoinCfg<D, kCols>;
     extern __shared__ __align__(128) uint8_t smem[];
     float* S = reinterpret_cast<float*>(smem + L::S);
@@ -670,7 +673,9 @@ tc_gd_join(const float* __restrict__ B, const float* __restrict__ Mx, const floa
     if (part == 0) {
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-            s[y] = !kReverse && first ? ld_f4(first + bh * rec + (row + y) * D + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+            s[y] = !kReverse && first && row + y < Dk && col < Dv  // the caller's state: true sizes
+                       ? ld_f4(first + (bh * Dk + row + y) * Dv + col)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
         load_b(0);
     }
     bool ok = true;
@@ -780,7 +785,7 @@ cudaError_t states(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
 }
 
 template <int D>
-cudaError_t join(const float* B, const float* Mx, const float* first, float* out, int BH, int P, bool reverse, int* err,
+cudaError_t join(const float* B, const float* Mx, const float* first, float* out, int BH, int P, int Dk, int Dv, bool reverse, int* err,
                  cudaStream_t st) {
     const bool wide = (long long)BH * (D / 16) > 152;
     auto kern = reverse ? (wide ? tc_gd_join<D, true, 32> : tc_gd_join<D, true, 16>)
@@ -791,7 +796,7 @@ cudaError_t join(const float* B, const float* Mx, const float* first, float* out
     launch_begin(name, st);
     const cudaError_t e =
         launch_pdl(kern, dim3(D / (wide ? 32 : 16), BH), dim3(wide ? JoinCfg<D, 32>::threads : JoinCfg<D, 16>::threads), smem,
-                   st, B, Mx, first, out, P, err);
+                   st, B, Mx, first, out, P, Dk, Dv, err);
     const cudaError_t e2 = launch_end(name, st);
     return e != cudaSuccess ? e : e2;
 }
@@ -799,7 +804,8 @@ cudaError_t join(const float* B, const float* Mx, const float* first, float* out
 #define GD_INSTANCE(D)                                                                                              \
     template cudaError_t states<D>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const StateArgs&,    \
                                    Mode, int, int, int*, cudaStream_t);                                            \
-    template cudaError_t join<D>(const float*, const float*, const float*, float*, int, int, bool, int*, cudaStream_t);
+    template cudaError_t join<D>(const float*, const float*, const float*, float*, int, int, int, int, bool, int*,     \
+                                 cudaStream_t);
 GD_INSTANCE(64)
 GD_INSTANCE(128)
 #undef GD_INSTANCE
@@ -812,8 +818,8 @@ template <int D>
 cudaError_t fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) {
     const int BH = s.B * s.H, M = (s.N + kC - 1) / kC;
     CUtensorMap tq, tk, tv;
-    if (!make_tmap_bf16_rows(&tq, a.q, BH, s.N, D, kC) || !make_tmap_bf16_rows(&tk, a.k, BH, s.N, D, kC) ||
-        !make_tmap_bf16_rows(&tv, a.v, BH, s.N, D, kC))
+    if (!make_tmap_bf16_rows(&tq, a.q, BH, s.N, s.Dk, kC) || !make_tmap_bf16_rows(&tk, a.k, BH, s.N, s.Dk, kC) ||
+        !make_tmap_bf16_rows(&tv, a.v, BH, s.N, s.Dv, kC))
         return cudaErrorInvalidValue;
     int* err = device_error_word();
     const Layout L = layout(s, false);
@@ -833,14 +839,19 @@ cudaError_t fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
         sa.segM = Mx;
         sa.nsum = L.segs - 1;
         GD_TRY(states<D>(tq, tk, tv, sa, kSum, BH, L.segs - 1, err, st));
-        GD_TRY(join<D>(B, Mx, a.S0, S, BH, L.segs, false, err, st));
+        GD_TRY(join<D>(B, Mx, a.S0, S, BH, L.segs, s.Dk, s.Dv, false, err, st));
         sa.S0 = S;
+        sa.dk = sa.dv = D;
     } else {
         sa.S0 = a.S0;
+        sa.dk = s.Dk;
+        sa.dv = s.Dv;
     }
     sa.S_out = a.S;
     sa.o = (__nv_bfloat16*)a.o;
     sa.N = s.N;
+    sa.Dk = s.Dk;
+    sa.Dv = s.Dv;
     return states<D>(tq, tk, tv, sa, kOut, BH, L.segs, err, st);
 }
 
@@ -854,15 +865,16 @@ int tc_segments(const la_shape& s, bool bwd) {
     const int BH = s.B * s.H, M = (s.N + kC - 1) / kC;
     const double main = bwd ? 3.8 + 4.6 : 3.2, sum = 2.6, reverse_sum = 2.8, launch = 6.0;
     auto waves = [](long long blocks) { return (double)((blocks + kSms - 1) / kSms); };
-    const long long slices = (long long)BH * (s.Dk / 16);
-    const double join = (s.Dk == 128 ? 1.9 : 0.8) * (slices > kSms ? 1.6 * waves(slices / 2) : 1.0);
+    const int D = tc_dim(s);
+    const long long slices = (long long)BH * (D / 16);
+    const double join = (D == 128 ? 1.9 : 0.8) * (slices > kSms ? 1.6 * waves(slices / 2) : 1.0);
     int best = 1;
     double best_t = waves(BH) * M * main;
     for (int P = 2; P <= M && P <= 64; ++P) {
         const int cps = (M + P - 1) / P;
         if ((M + cps - 1) / cps != P) continue;
         double t = waves((long long)BH * P) * cps * main + 2 * launch + (bwd ? 2 : 1) * P * join;
-        t += waves((long long)BH * (P - 1) * (s.Dk == 128 ? 2 : 1)) * cps * sum;
+        t += waves((long long)BH * (P - 1) * (D == 128 ? 2 : 1)) * cps * sum;
         if (bwd) t += waves((long long)BH * (P - 1)) * cps * reverse_sum + 2 * launch;
         if (t < 0.97 * best_t) {
             best_t = t;
@@ -872,10 +884,11 @@ int tc_segments(const la_shape& s, bool bwd) {
     return best;
 }
 
-bool tc_ok(const la_shape& s) { return s.dtype == LA_BF16 && s.Dk == s.Dv && (s.Dk == 64 || s.Dk == 128); }
+bool tc_ok(const la_shape& s) { return s.dtype == LA_BF16; }
+int tc_dim(const la_shape& s) { return s.Dk > 64 || s.Dv > 64 ? 128 : 64; }
 
 cudaError_t tc_fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) {
-    return s.Dk == 128 ? fwd<128>(a, s, ws, st) : fwd<64>(a, s, ws, st);
+    return tc_dim(s) == 128 ? fwd<128>(a, s, ws, st) : fwd<64>(a, s, ws, st);
 }
 
 }  // namespace gd

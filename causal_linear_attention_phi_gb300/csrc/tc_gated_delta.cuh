@@ -209,10 +209,11 @@ struct StateArgs {
     const float* recs;
     const uint8_t* mats;
     int mat_bytes;     // kMatsFwd or kMatsBwd
-    const float* S0;   // [BH][P] records: the states entering the segments; null: zero
+    const float* S0;   // [BH][P] records of dk x dv: the states entering the segments; null: zero
+    int dk, dv;
     float* S_out;      // kOut: [BH] records, the state after the last position, or null
-    __nv_bfloat16* o;  // kOut: [BH][N][D]
-    int N;
+    __nv_bfloat16* o;  // kOut: [BH][N][Dv]
+    int N, Dk, Dv;     // true sizes
     uint8_t *x_tiles, *s_tiles;   // kGrad
     float *segB, *segM;           // kSum: [BH][P] records
     int M, P, cps;                // chunks, segments, chunks of a segment
@@ -221,10 +222,10 @@ struct StateArgs {
 template <int D>
 cudaError_t states(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const StateArgs& a, Mode mode, int BH, int segments, int* err, cudaStream_t st);
-// Joins the segments' sums: out[p + 1] = B[p] + M[p] out[p] from out[0] = first (or zero); reverse: out[P - 1] = 0,
+// Joins the segments' sums: out[p + 1] = B[p] + M[p] out[p] from out[0] = first (or zero; Dk x Dv records); reverse: out[P - 1] = 0,
 // out[p - 1] = B[p] + M[p]^T out[p].
 template <int D>
-cudaError_t join(const float* B, const float* Mx, const float* first, float* out, int BH, int P, bool reverse, int* err,
+cudaError_t join(const float* B, const float* Mx, const float* first, float* out, int BH, int P, int Dk, int Dv, bool reverse, int* err,
                  cudaStream_t st);
 
 }  // namespace tcgd

@@ -58,7 +58,7 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dv,
               const float* __restrict__ recs, const uint8_t* __restrict__ mats, uint8_t* __restrict__ y_tiles,
               uint8_t* __restrict__ ds_tiles, const float* __restrict__ segdS, float* __restrict__ segB2, int M, int P,
-              int cps, int* err) {
+              int cps, int Dv, int* err) {
     using L = RevSmem<D>;
     using T = RTm<D>;
     constexpr int kSc = D / kHs;  // state columns of a thread
@@ -323,7 +323,8 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 named_barrier(1, 32 * kWarps);
                 if (ct == 0) {
 #pragma unroll
-                    for (int b = 0; b < D / 64; ++b) tma_store_3d(&tm_dv, out + b * kBlk, 64 * b, c * kC, bh);
+                    for (int b = 0; b < D / 64; ++b)
+                        if (64 * b < Dv) tma_store_3d(&tm_dv, out + b * kBlk, 64 * b, c * kC, bh);
                     bulk_store(y_tiles + at * L::ybytes, out + L::tile, L::ybytes);
                     bulk_commit();
                 }
@@ -408,7 +409,7 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dq,
             const __grid_constant__ CUtensorMap tm_dk, const float* __restrict__ recs, const uint8_t* __restrict__ x_tiles, const uint8_t* __restrict__ y_tiles,
             const uint8_t* __restrict__ s_tiles, const uint8_t* __restrict__ ds_tiles, __nv_bfloat16* __restrict__ dg,
-            __nv_bfloat16* __restrict__ dbeta, int N, int M, int total, int* err) {
+            __nv_bfloat16* __restrict__ dbeta, int N, int M, int total, int Dk, int* err) {
     using L = GradSmem<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -709,6 +710,7 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (ct == 0) {
 #pragma unroll
                 for (int b = 0; b < D / 64; ++b) {
+                    if (64 * b >= Dk) continue;
                     tma_store_3d(&tm_dq, base + L::out + b * kBlk, 64 * b, c0, bh);
                     tma_store_3d(&tm_dk, base + L::out + (D / 64 + b) * kBlk, 64 * b, c0, bh);
                 }
@@ -769,10 +771,10 @@ template <int D>
 cudaError_t bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) {
     const int BH = s.B * s.H, M = (s.N + kC - 1) / kC;
     CUtensorMap tq, tk, tv, tdo, tdq, tdk, tdv;
-    if (!make_tmap_bf16_rows(&tq, a.q, BH, s.N, D, kC) || !make_tmap_bf16_rows(&tk, a.k, BH, s.N, D, kC) ||
-        !make_tmap_bf16_rows(&tv, a.v, BH, s.N, D, kC) || !make_tmap_bf16_rows(&tdo, a.dout, BH, s.N, D, kC) ||
-        !make_tmap_bf16_rows(&tdq, a.dq, BH, s.N, D, kC) || !make_tmap_bf16_rows(&tdk, a.dk, BH, s.N, D, kC) ||
-        !make_tmap_bf16_rows(&tdv, a.dv, BH, s.N, D, kC))
+    if (!make_tmap_bf16_rows(&tq, a.q, BH, s.N, s.Dk, kC) || !make_tmap_bf16_rows(&tk, a.k, BH, s.N, s.Dk, kC) ||
+        !make_tmap_bf16_rows(&tv, a.v, BH, s.N, s.Dv, kC) || !make_tmap_bf16_rows(&tdo, a.dout, BH, s.N, s.Dv, kC) ||
+        !make_tmap_bf16_rows(&tdq, a.dq, BH, s.N, s.Dk, kC) || !make_tmap_bf16_rows(&tdk, a.dk, BH, s.N, s.Dk, kC) ||
+        !make_tmap_bf16_rows(&tdv, a.dv, BH, s.N, s.Dv, kC))
         return cudaErrorInvalidValue;
     int* err = device_error_word();
     const Layout L = layout(s, true);
@@ -796,7 +798,7 @@ cudaError_t bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
         launch_begin(name, st);
         const cudaError_t e =
             launch_pdl(kern, dim3(sums ? L.segs - 1 : L.segs, BH), dim3(kThreads), RevSmem<D>::bytes, st, tq, tk, tdo, tdv,
-                       (const float*)recs, (const uint8_t*)mats, Y, dS, segdS, segB2, M, L.segs, L.cps, err);
+                       (const float*)recs, (const uint8_t*)mats, Y, dS, segdS, segB2, M, L.segs, L.cps, s.Dv, err);
         const cudaError_t e2 = launch_end(name, st);
         return e != cudaSuccess ? e : e2;
     };
@@ -807,9 +809,10 @@ cudaError_t bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
         sa.nsum = L.segs - 1;  // the maps of all segments are wanted: the first for the states, the last for their gradients
         GD_TRY(states<D>(tq, tk, tv, sa, kSum, BH, L.segs, err, st));
         GD_TRY(reverse(true, nullptr, (float*)(ws + L.segB2)));
-        GD_TRY(join<D>(sa.segB, sa.segM, nullptr, (float*)(ws + L.segS), BH, L.segs, false, err, st));
-        GD_TRY(join<D>((float*)(ws + L.segB2), sa.segM, nullptr, (float*)(ws + L.segdS), BH, L.segs, true, err, st));
+        GD_TRY(join<D>(sa.segB, sa.segM, nullptr, (float*)(ws + L.segS), BH, L.segs, D, D, false, err, st));
+        GD_TRY(join<D>((float*)(ws + L.segB2), sa.segM, nullptr, (float*)(ws + L.segdS), BH, L.segs, D, D, true, err, st));
         sa.S0 = (float*)(ws + L.segS);
+        sa.dk = sa.dv = D;
         segdS = (float*)(ws + L.segdS);
     }
     GD_TRY(states<D>(tq, tk, tv, sa, kGrad, BH, L.segs, err, st));
@@ -819,7 +822,7 @@ cudaError_t bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
     const int total = BH * M;
     const cudaError_t e = launch_pdl(tc_gd_grads<D>, dim3(total < 152 ? total : 152), dim3(kThreads), GradSmem<D>::bytes, st, tq, tk, tdo, tdq, tdk,
                    (const float*)recs, (const uint8_t*)X, (const uint8_t*)Y,
-                   (const uint8_t*)S, (const uint8_t*)dS, (__nv_bfloat16*)a.dg, (__nv_bfloat16*)a.dbeta, s.N, M, total, err);
+                   (const uint8_t*)S, (const uint8_t*)dS, (__nv_bfloat16*)a.dg, (__nv_bfloat16*)a.dbeta, s.N, M, total, s.Dk, err);
     const cudaError_t e2 = launch_end("tc_gd_grads", st);
     return e != cudaSuccess ? e : e2;
 }
@@ -827,7 +830,7 @@ cudaError_t bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
 }  // namespace
 
 cudaError_t tc_bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) {
-    return s.Dk == 128 ? bwd<128>(a, s, ws, st) : bwd<64>(a, s, ws, st);
+    return tc_dim(s) == 128 ? bwd<128>(a, s, ws, st) : bwd<64>(a, s, ws, st);
 }
 
 }  // namespace gd

@@ -6,6 +6,7 @@
 // adjoint recurrence from the last chunk back, sliced alike: dv, Y and the gradient leaving every chunk) and
 // gd_grads (one block per chunk: dq, dk, dg, dbeta).  All arithmetic is fp32; sums of log decays fp64.
 #include "gated_delta.cuh"
+#include "sm100.cuh"
 
 namespace la {
 namespace gd {
@@ -27,8 +28,9 @@ struct Carve {
 
 // Rows [c0, c0 + n) of a [N][D] matrix as fp32 into dst[kC][D + 1]; the rows past n are 0.
 __device__ __forceinline__ void load_rows(float* dst, const float* __restrict__ src, int c0, int n, int D) {
+    const int lg = 31 - __clz(D);  // D is a power of two
     for (int i = threadIdx.x; i < kC * D; i += kThreads) {
-        const int r = i / D, d = i - r * D;
+        const int r = i >> lg, d = i & (D - 1);
         dst[r * (D + 1) + d] = r < n ? src[(size_t)(c0 + r) * D + d] : 0.f;
     }
 }
@@ -104,13 +106,14 @@ gd_prepare(const float* __restrict__ q, const float* __restrict__ k, const float
 // ------------------------------------------------------------------ products of the recurrences
 // Tiles in shared memory with rows of a multiple of 4 floats.  A thread forms 4 x 4 tiles, so that a multiply-add costs two
 // bytes of shared-memory reads (single columns of four rows cost five and were bound by them).
-// z[j] += sum_(x < K) a[(16 j) lda + x] b[x ldb + 0..3]
+// z[j] += sum_(x < K) a[(kStep j) lda + x] b[x ldb + 0..3]
+template <int kStep = 16>
 __device__ __forceinline__ void mac_rows(F4 (&z)[4], const float* a, int lda, const float* b, int ldb, int K) {
 #pragma unroll 2
     for (int x = 0; x < K; x += 4) {
         float4 av[4], bv[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) av[j] = ld_f4(a + 16 * j * lda + x);
+        for (int j = 0; j < 4; ++j) av[j] = ld_f4(a + kStep * j * lda + x);
 #pragma unroll
         for (int e = 0; e < 4; ++e) bv[e] = ld_f4(b + (x + e) * ldb);
 #pragma unroll
@@ -143,24 +146,36 @@ __device__ __forceinline__ F4 scaled(float m, const F4& z) {
 
 constexpr int kLc4 = kC + 4;  // row pitch of the 64 x 64 tiles
 
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool take) {  // zeros when not taken
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(dst)), "l"(src), "r"(take ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
 // Rows [c0, c0 + n) of a [N][D] matrix into dst, pitch D + 4; the rows past n are 0.
 template <int W>
-__device__ __forceinline__ void load_rows4(float* dst, const float* __restrict__ src, int c0, int n, int D) {
-    const int v = D / 4;
-    for (int i = threadIdx.x; i < kC * v; i += 4 * W) {
-        const int r = i / v, d = i - r * v;
-        const float4 x = r < n ? ld_f4(src + (size_t)(c0 + r) * D + 4 * d) : make_float4(0.f, 0.f, 0.f, 0.f);
-        *reinterpret_cast<float4*>(dst + r * (D + 4) + 4 * d) = x;
+__device__ __forceinline__ void copy_rows(float* dst, const float* __restrict__ src, int c0, int n, int D) {
+    const int lg = 29 - __clz(D);  // D / 4 is a power of two
+    for (int i = threadIdx.x; i < kC << lg; i += 4 * W) {
+        const int r = i >> lg, d = 4 * (i & (D / 4 - 1));
+        copy16(dst + r * (D + 4) + d, src + (size_t)(c0 + (r < n ? r : 0)) * D + d, r < n);
     }
 }
 template <int W>
-__device__ __forceinline__ void load_square4(float* dst, const float* __restrict__ src) {
-    for (int i = threadIdx.x; i < kC * kC / 4; i += 4 * W)
-        *reinterpret_cast<float4*>(dst + (i >> 4) * kLc4 + 4 * (i & 15)) = ld_f4(src + 4 * i);
+__device__ __forceinline__ void copy_square(float* dst, const float* __restrict__ src) {
+    for (int i = threadIdx.x; i < kC * kC / 4; i += 4 * W) copy16(dst + (i >> 4) * kLc4 + 4 * (i & 15), src + 4 * i, true);
+}
+template <int W>
+__device__ __forceinline__ void copy_rec(float* dst, const float* __restrict__ src) {
+    for (int i = threadIdx.x; i < kRec / 4; i += 4 * W) copy16(dst + 4 * i, src + 4 * i, true);
 }
 
 // ------------------------------------------------------------------ the recurrence over chunks
 // Block (slice, head): value columns [W slice, +W), 4 W threads.  o, Xs / Ss (the gradient's records) and S_out may be null.
+// K, which the last product of a chunk reads, has two buffers; Q, t and P of the next chunk are copied while the state moves on.
 template <int W>
 __global__ void __launch_bounds__(4 * W)
 gd_states(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v, const float* S0,
@@ -171,36 +186,53 @@ gd_states(const float* __restrict__ q, const float* __restrict__ k, const float*
     extern __shared__ __align__(16) float smem[];
     Carve sm{smem};
     const int ld = Dk + 4;
-    float* ks = sm.take(kC * ld);
+    float* k2 = sm.take(2 * kC * ld);
+    float* rec2 = sm.take(2 * kRec);
     float* qs = sm.take(kC * ld);
     float* tt = sm.take(kC * kLc4);
     float* PP = sm.take(kC * kLc4);
     float* S = sm.take(Dk * kLw);
     float* Rb = sm.take(kC * kLw);  // beta R, then tail u
     float* Ub = sm.take(kC * kLw);  // u
-    float* rec = sm.take(kRec);
     const int tid = threadIdx.x, rg = tid / (W / 4), c = 4 * (tid % (W / 4));
     const size_t bh = blockIdx.y;
     const int col = blockIdx.x * W + c;
     LA_DCHECK(col + 3 < Dv);
+    q += bh * N * Dk;
+    k += bh * N * Dk;
+    auto copy_k = [&](int m) {
+        copy_rows<W>(k2 + (m & 1) * kC * ld, k, m * kC, min(kC, N - m * kC), Dk);
+        copy_rec<W>(rec2 + (m & 1) * kRec, recs + (bh * M + m) * kRec);
+    };
+    auto copy_rest = [&](int m) {
+        copy_square<W>(tt, ts + (bh * M + m) * kC * kC);
+        if (o) {
+            copy_square<W>(PP, Ps + (bh * M + m) * kC * kC);
+            copy_rows<W>(qs, q, m * kC, min(kC, N - m * kC), Dk);
+        }
+    };
+    copy_k(0);
+    copy_rest(0);
+    copies_commit();
     for (int d = rg; d < Dk; d += 16)
         *reinterpret_cast<float4*>(S + d * kLw + c) =
             S0 ? ld_f4(S0 + (bh * Dk + d) * Dv + col) : make_float4(0.f, 0.f, 0.f, 0.f);
     for (int m = 0; m < M; ++m) {
         const int c0 = m * kC, n = min(kC, N - c0);
         const size_t at = bh * M + m;
-        __syncthreads();
-        load_rows4<W>(ks, k + bh * N * Dk, c0, n, Dk);
-        load_square4<W>(tt, ts + at * kC * kC);
-        for (int i = tid; i < kRec; i += 4 * W) rec[i] = recs[at * kRec + i];
-        if (o) {
-            load_rows4<W>(qs, q + bh * N * Dk, c0, n, Dk);
-            load_square4<W>(PP, Ps + at * kC * kC);
-        }
+        const float *ks = k2 + (m & 1) * kC * ld, *rec = rec2 + (m & 1) * kRec;
+        float4 vv[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            vv[j] = rg + 16 * j < n ? ld_f4(v + (bh * N + c0 + rg + 16 * j) * (size_t)Dv + col)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+        copies_wait<0>();
+        __syncthreads();  // the chunk's operands and the state are there; the other K has been read
+        if (m + 1 < M) copy_k(m + 1);
+        copies_commit();
         if (Ss)
             for (int d = rg; d < Dk; d += 16)
                 *reinterpret_cast<float4*>(Ss + (at * Dk + d) * Dv + col) = ld_f4(S + d * kLw + c);
-        __syncthreads();
         F4 x[4], w[4];
         zero(w);
         mac_rows(w, ks + rg * ld, ld, S + c, kLw, Dk);
@@ -208,13 +240,10 @@ gd_states(const float* __restrict__ q, const float* __restrict__ k, const float*
         for (int j = 0; j < 4; ++j) {
             const int r = rg + 16 * j;
             x[j] = scaled(-rec[kGam + r], w[j]);
-            if (r < n) {
-                const float4 vv = ld_f4(v + (bh * N + c0 + r) * (size_t)Dv + col);
-                x[j].a.x += vv.x;
-                x[j].a.y += vv.y;
-                x[j].b.x += vv.z;
-                x[j].b.y += vv.w;
-            }
+            x[j].a.x += vv[j].x;
+            x[j].a.y += vv[j].y;
+            x[j].b.x += vv[j].z;
+            x[j].b.y += vv[j].w;
             put4(Rb + r * kLw + c, x[j], rec[kBeta + r]);
         }
         __syncthreads();
@@ -239,8 +268,10 @@ gd_states(const float* __restrict__ q, const float* __restrict__ k, const float*
                 const int r = rg + 16 * j;
                 if (r < n) put4(o + (bh * N + c0 + r) * (size_t)Dv + col, w[j]);
             }
-            __syncthreads();  // the old slice has been read
+            __syncthreads();  // the old slice, Q and P have been read
         }
+        if (m + 1 < M) copy_rest(m + 1);
+        copies_commit();
         const float gc = rec[kGam + kC - 1];
         for (int g = rg; g < Dk / 4; g += 16) {
 #pragma unroll
@@ -257,6 +288,7 @@ gd_states(const float* __restrict__ q, const float* __restrict__ k, const float*
 }
 
 // ------------------------------------------------------------------ the adjoint recurrence, last chunk first
+// As above: K in two buffers, Q copied under the products before its own, t and P under the state's.
 template <int W>
 __global__ void __launch_bounds__(4 * W)
 gd_reverse(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ dout,
@@ -266,63 +298,66 @@ gd_reverse(const float* __restrict__ q, const float* __restrict__ k, const float
     extern __shared__ __align__(16) float smem[];
     Carve sm{smem};
     const int ld = Dk + 4;
-    float* ks = sm.take(kC * ld);
+    float* k2 = sm.take(2 * kC * ld);
+    float* rec2 = sm.take(2 * kRec);
     float* qs = sm.take(kC * ld);
     float* tt = sm.take(kC * kLc4);
     float* PP = sm.take(kC * kLc4);
     float* S = sm.take(Dk * kLw);   // this slice of dS'
     float* Db = sm.take(kC * kLw);  // dO, then gam dO
     float* Ub = sm.take(kC * kLw);  // beta dU, then -gam dR
-    float* rec = sm.take(kRec);
     const int tid = threadIdx.x, rg = tid / (W / 4), c = 4 * (tid % (W / 4));
     const size_t bh = blockIdx.y;
     const int col = blockIdx.x * W + c;
     LA_DCHECK(col + 3 < Dv);
+    q += bh * N * Dk;
+    k += bh * N * Dk;
+    auto copy_k = [&](int m) {
+        copy_rows<W>(k2 + (m & 1) * kC * ld, k, m * kC, min(kC, N - m * kC), Dk);
+        copy_rec<W>(rec2 + (m & 1) * kRec, recs + (bh * M + m) * kRec);
+    };
+    auto copy_squares = [&](int m) {
+        copy_square<W>(tt, ts + (bh * M + m) * kC * kC);
+        copy_square<W>(PP, Ps + (bh * M + m) * kC * kC);
+    };
+    copy_k(M - 1);
+    copy_squares(M - 1);
+    copies_commit();
     for (int d = rg; d < Dk; d += 16) *reinterpret_cast<float4*>(S + d * kLw + c) = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int m = M - 1; m >= 0; --m) {
         const int c0 = m * kC, n = min(kC, N - c0);
         const size_t at = bh * M + m;
-        __syncthreads();
-        load_rows4<W>(ks, k + bh * N * Dk, c0, n, Dk);
-        load_rows4<W>(qs, q + bh * N * Dk, c0, n, Dk);
-        load_square4<W>(tt, ts + at * kC * kC);
-        load_square4<W>(PP, Ps + at * kC * kC);
-        for (int i = tid; i < kRec; i += 4 * W) rec[i] = recs[at * kRec + i];
-        for (int r = rg; r < kC; r += 16)
-            *reinterpret_cast<float4*>(Db + r * kLw + c) =
-                r < n ? ld_f4(dout + (bh * N + c0 + r) * (size_t)Dv + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float *ks = k2 + (m & 1) * kC * ld, *rec = rec2 + (m & 1) * kRec;
+        float4 dd[4];  // rows 4 rg .. 4 rg + 3, here and below
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            dd[j] = 4 * rg + j < n ? ld_f4(dout + (bh * N + c0 + 4 * rg + j) * (size_t)Dv + col)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+        copies_wait<0>();
+        __syncthreads();  // the chunk's operands and the state are there; Q and the other K have been read
+        copy_rows<W>(qs, q, c0, n, Dk);
+        copies_commit();
+        if (m > 0) copy_k(m - 1);
+        copies_commit();
         for (int d = rg; d < Dk; d += 16)
             *reinterpret_cast<float4*>(dSs + (at * Dk + d) * Dv + col) = ld_f4(S + d * kLw + c);
-        __syncthreads();
-        // rows 4 rg .. 4 rg + 3 from here on
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<float4*>(Db + (4 * rg + j) * kLw + c) = dd[j];
         F4 y[4];
         zero(y);
-        {
-            const float* kr = ks + 4 * rg * ld;
-#pragma unroll 2
-            for (int x = 0; x < Dk; x += 4) {
-                float4 av[4], bv[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) av[j] = ld_f4(kr + j * ld + x);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) bv[e] = ld_f4(S + (x + e) * kLw + c);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    fma4(y[j], av[j].x, bv[0]);
-                    fma4(y[j], av[j].y, bv[1]);
-                    fma4(y[j], av[j].z, bv[2]);
-                    fma4(y[j], av[j].w, bv[3]);
-                }
-            }
-        }
+        mac_rows<1>(y, ks + 4 * rg * ld, ld, S + c, kLw, Dk);
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = scaled(rec[kTail + 4 * rg + j], y[j]);
+        __syncthreads();  // dO
         mac_cols(y, PP + 4 * rg, kLc4, Db + c, kLw, kC);
 #pragma unroll
         for (int j = 0; j < 4; ++j) put4(Ub + (4 * rg + j) * kLw + c, y[j], rec[kBeta + 4 * rg + j]);
         __syncthreads();
         mac_cols(y, tt + 4 * rg, kLc4, Ub + c, kLw, kC);
-        __syncthreads();  // Ub and Db have been read
+        copies_wait<1>();  // Q
+        __syncthreads();   // Ub, Db, t and P have been read
+        if (m > 0) copy_squares(m - 1);
+        copies_commit();
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int r = 4 * rg + j;
@@ -543,7 +578,7 @@ gd_grads(const float* __restrict__ q, const float* __restrict__ k, const float* 
 int f4(int n) { return (n + 3) / 4 * 4; }
 size_t smem_prepare(int Dk) { return 4 * (size_t)(2 * f4(kC * (Dk + 1)) + kC * kLd + kRec); }
 size_t smem_states(int Dk, int W) {
-    return 4 * (size_t)(2 * kC * (Dk + 4) + 2 * kC * kLc4 + Dk * (W + 4) + 2 * kC * (W + 4) + kRec);
+    return 4 * (size_t)(3 * kC * (Dk + 4) + 2 * kC * kLc4 + Dk * (W + 4) + 2 * kC * (W + 4) + 2 * kRec);
 }
 size_t smem_grads(int Dk) {
     return 4 * (size_t)(2 * f4(kC * (Dk + 1)) + 2 * f4(kC * kLc) + 3 * f4(kC * kLw) + 2 * f4(Dk * 17) + kRec +
@@ -573,11 +608,18 @@ cudaError_t prepare(const void* q, const void* k, const void* g, const void* bet
     return launch_end("gd_prepare", st);
 }
 
-// Value columns of a slice: wide ones read K, Q, t and P less often, narrow ones make more blocks where heads are few.
+// Value columns of a slice.  Shared memory leaves room for one block to an SM at Dk = 128; a chunk takes a block about the same
+// time with 16 or 32 columns (too few warps to fill the SM) and 1.55 times that with 64.  Measured, gd_states of Dk = Dv = 128:
+// 64 chunks of 16 heads 438, 436, 670 us with 16, 32, 64 columns, 32 chunks of 48 heads 653, 436, 339, of 64 heads 868, 438, 340.
 int slice(const la_shape& s) {
-    int w = s.Dv < 64 ? s.Dv : 64;
-    while (w > 16 && (long long)s.B * s.H * (s.Dv / w) < 152) w /= 2;
-    return w;
+    int best = 16;
+    double least = 1e30;
+    for (int w = 16; w <= 64 && w <= s.Dv; w *= 2) {
+        const long long blocks = (long long)s.B * s.H * (s.Dv / w);
+        const double t = (double)((blocks + 151) / 152) * (w == 64 ? 1.55 : w == 32 ? 1.02 : 1.0);
+        if (t < least) best = w, least = t;
+    }
+    return best;
 }
 
 template <int W>

@@ -277,7 +277,8 @@ la_status la_retention_step(const void* q, const void* k, const void* v, const f
  * may grow without bound).  g below -100 (-inf among them) is a decay of exactly 0: the state starts anew, so
  * sequences packed one after another are separated by a g of -inf at each one's first position.
  * Computed in chunks of 64 positions: inside a chunk the writes are solved for together (a triangular system),
- * the state is carried from chunk to chunk.
+ * the state is carried from chunk to chunk.  An infinity or NaN among the inputs therefore spoils its whole chunk and
+ * the positions after it (of its head; a later reset does not clear it), never another head's.
  * q, k: [B,H,N,Dk]; v, o: [B,H,N,Dv]; g, beta: [B,H,N], all in s.dtype; o written.  g and beta need the
  * alignment of their elements only.
  * S0: NULL, or a DEVICE fp32 [B,H,Dk,Dv]: the state before the first position.

@@ -15,7 +15,7 @@
 // F and E enter as hi + lo parts: dg is a difference of sums over them.  Lanes 0-63 hold E's rows, 64-127 F^T's.
 #include <cudaTypedefs.h>
 
-#include "tc_gated_delta.cuh"
+#include "tc_gated_delta_states.cuh"
 
 namespace la {
 namespace gd {
@@ -44,6 +44,15 @@ struct RevSmem {
     static_assert(bytes <= 232448, "shared memory");
 };
 
+struct ReverseArgs {
+    const float* recs;
+    const uint8_t* mats;
+    uint8_t *y_tiles, *ds_tiles;
+    const float* segdS;  // [BH][P]: the gradients of the segments' last states; null: zero
+    float* segB2;        // kSums: [BH][P]
+    int M, P, cps, Dv;
+};
+
 template <int D>
 struct RTm {
     static constexpr uint32_t SHi = 0, SLo = D / 2, A1 = D, A2 = D + 64, B = D + 128, G = D + 192, dS = D + 256;
@@ -53,12 +62,12 @@ struct RTm {
 
 // kSums: only the gradient that a segment adds to that of the state before it (segB2), from a zero gradient after it.
 template <int D, bool kSums>
-__global__ void __launch_bounds__(kThreads, 1)
-tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-              const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dv,
-              const float* __restrict__ recs, const uint8_t* __restrict__ mats, uint8_t* __restrict__ y_tiles,
-              uint8_t* __restrict__ ds_tiles, const float* __restrict__ segdS, float* __restrict__ segB2, int M, int P,
-              int cps, int Dv, int* err) {
+__device__ __forceinline__ void reverse_block(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_do,
+                                              const CUtensorMap& tm_dv, const ReverseArgs& a, int p, int bh, int* err) {
+    const float* __restrict__ recs = a.recs;
+    const uint8_t* __restrict__ mats = a.mats;
+    uint8_t *__restrict__ y_tiles = a.y_tiles, *__restrict__ ds_tiles = a.ds_tiles;
+    const int M = a.M, P = a.P, cps = a.cps, Dv = a.Dv;
     using L = RevSmem<D>;
     using T = RTm<D>;
     constexpr int kSc = D / kHs;  // state columns of a thread
@@ -67,8 +76,7 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     RBars* bar = reinterpret_cast<RBars*>(base + L::bars);
     uint32_t* slot = reinterpret_cast<uint32_t*>(base + L::slot);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int p = blockIdx.x + (kSums ? 1 : 0);  // the first segment's sum is not needed
-    const int bh = blockIdx.y, cbeg = p * cps, cend = min(M, cbeg + cps), nloc = cend - cbeg;
+    const int cbeg = p * cps, cend = min(M, cbeg + cps), nloc = cend - cbeg;
     LA_DCHECK(nloc >= 1);
     if (tid == 0) {
         mbar_init(&bar->full[0], 1);
@@ -204,8 +212,8 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         float2 S[kSc / 2];
 #pragma unroll
         for (int x = 0; x < kSc / 2; ++x) {
-            const float* s0 = segdS + (((size_t)bh * P + p) * D + kSc * h + 2 * x) * D + r;
-            S[x] = !kSums && segdS && r < D ? make_float2(s0[0], s0[D]) : make_float2(0.f, 0.f);
+            const float* s0 = a.segdS + (((size_t)bh * P + p) * D + kSc * h + 2 * x) * D + r;
+            S[x] = !kSums && a.segdS && r < D ? make_float2(s0[0], s0[D]) : make_float2(0.f, 0.f);
         }
         uint8_t* out = base + L::out;
         for (int i = 0; i < nloc; ++i) {
@@ -345,7 +353,7 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (kSums && r < D) {
 #pragma unroll
             for (int x = 0; x < kSc; ++x)
-                segB2[(((size_t)bh * P + p) * D + kSc * h + x) * D + r] = x & 1 ? S[x / 2].y : S[x / 2].x;
+                a.segB2[(((size_t)bh * P + p) * D + kSc * h + x) * D + r] = x & 1 ? S[x / 2].y : S[x / 2].x;
         }
         tc_fence_before();
     }
@@ -354,6 +362,31 @@ tc_gd_reverse(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// ------------------------------------------------------------------ both recurrences at once
+// They do not depend on each other: one grid of both fills the SMs better than two, and its last wave is shorter.  The
+// third grid dimension: 0 the adjoint one (the longer), then the forward one, and with kSums and D = 128 its maps.
+template <int D, bool kSums>
+struct SweepSmem {
+    static constexpr size_t fwd = FwdSmem<D, kSums ? kSum : kGrad>::bytes, rev = RevSmem<D>::bytes;
+    static constexpr size_t bytes = fwd > rev ? fwd : rev;
+};
+template <int D, bool kSums>
+__global__ void __launch_bounds__(kThreads, 1)
+tc_gd_sweeps(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+             const __grid_constant__ CUtensorMap tm_dv, const __grid_constant__ StateArgs a,
+             const __grid_constant__ ReverseArgs ra, int* err) {
+    const int p = blockIdx.x, bh = blockIdx.y;
+    if (blockIdx.z == 0) {
+        if (!kSums || p > 0)  // the first segment's sum is not needed
+            reverse_block<D, kSums>(tm_q, tm_k, tm_do, tm_dv, ra, p, bh, err);
+        return;
+    }
+    const bool map = kSums && blockIdx.z == 2;
+    if (kSums && D == 128 && !map && p >= a.P - 1) return;  // nor the last one's, but its map
+    states_block<D, kSums ? kSum : kGrad>(tm_q, tm_k, tm_v, a, p, bh, map, err);
 }
 
 // ------------------------------------------------------------------ dq, dk, dg, dbeta of a chunk
@@ -767,6 +800,18 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
 }
 
+template <int D, bool kSums>
+cudaError_t sweeps(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
+                   const CUtensorMap& tdv, const StateArgs& sa, const ReverseArgs& ra, dim3 grid, int* err, cudaStream_t st) {
+    GD_TRY(allow_smem(tc_gd_sweeps<D, kSums>, SweepSmem<D, kSums>::bytes));
+    const char* name = kSums ? "tc_gd_sweep_sums" : "tc_gd_sweeps";
+    launch_begin(name, st);
+    const cudaError_t e = launch_pdl(tc_gd_sweeps<D, kSums>, grid, dim3(kThreads), SweepSmem<D, kSums>::bytes, st, tq, tk, tv,
+                                     tdo, tdv, sa, ra, err);
+    const cudaError_t e2 = launch_end(name, st);
+    return e != cudaSuccess ? e : e2;
+}
+
 template <int D>
 cudaError_t bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) {
     const int BH = s.B * s.H, M = (s.N + kC - 1) / kC;
@@ -791,32 +836,27 @@ cudaError_t bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
     sa.M = M;
     sa.P = L.segs;
     sa.cps = L.cps;
-    auto reverse = [&](bool sums, const float* segdS, float* segB2) {
-        auto kern = sums ? tc_gd_reverse<D, true> : tc_gd_reverse<D, false>;
-        GD_TRY(allow_smem(kern, RevSmem<D>::bytes));
-        const char* name = sums ? "tc_gd_reverse_segments" : "tc_gd_reverse";
-        launch_begin(name, st);
-        const cudaError_t e =
-            launch_pdl(kern, dim3(sums ? L.segs - 1 : L.segs, BH), dim3(kThreads), RevSmem<D>::bytes, st, tq, tk, tdo, tdv,
-                       (const float*)recs, (const uint8_t*)mats, Y, dS, segdS, segB2, M, L.segs, L.cps, s.Dv, err);
-        const cudaError_t e2 = launch_end(name, st);
-        return e != cudaSuccess ? e : e2;
-    };
-    const float* segdS = nullptr;
+    ReverseArgs ra{};
+    ra.recs = recs;
+    ra.mats = mats;
+    ra.y_tiles = Y;
+    ra.ds_tiles = dS;
+    ra.M = M;
+    ra.P = L.segs;
+    ra.cps = L.cps;
+    ra.Dv = s.Dv;
     if (L.segs > 1) {
         sa.segB = (float*)(ws + L.segB);
         sa.segM = (float*)(ws + L.segM);
-        sa.nsum = L.segs - 1;  // the maps of all segments are wanted: the first for the states, the last for their gradients
-        GD_TRY(states<D>(tq, tk, tv, sa, kSum, BH, L.segs, err, st));
-        GD_TRY(reverse(true, nullptr, (float*)(ws + L.segB2)));
-        GD_TRY(join<D>(sa.segB, sa.segM, nullptr, (float*)(ws + L.segS), BH, L.segs, D, D, false, err, st));
-        GD_TRY(join<D>((float*)(ws + L.segB2), sa.segM, nullptr, (float*)(ws + L.segdS), BH, L.segs, D, D, true, err, st));
+        ra.segB2 = (float*)(ws + L.segB2);
+        GD_TRY((sweeps<D, true>(tq, tk, tv, tdo, tdv, sa, ra, dim3(L.segs, BH, D == 128 ? 3 : 2), err, st)));
+        GD_TRY(join<D>(sa.segB, sa.segM, nullptr, (float*)(ws + L.segS), ra.segB2, (float*)(ws + L.segdS), BH, L.segs, D, D,
+                       err, st));
         sa.S0 = (float*)(ws + L.segS);
         sa.dk = sa.dv = D;
-        segdS = (float*)(ws + L.segdS);
+        ra.segdS = (float*)(ws + L.segdS);
     }
-    GD_TRY(states<D>(tq, tk, tv, sa, kGrad, BH, L.segs, err, st));
-    GD_TRY(reverse(false, segdS, nullptr));
+    GD_TRY((sweeps<D, false>(tq, tk, tv, tdo, tdv, sa, ra, dim3(L.segs, BH, 2), err, st)));
     GD_TRY(allow_smem(tc_gd_grads<D>, GradSmem<D>::bytes));
     launch_begin("tc_gd_grads", st);
     const int total = BH * M;

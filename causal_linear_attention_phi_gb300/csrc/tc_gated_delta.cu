@@ -463,26 +463,52 @@ cudaError_t fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
 
 }  // namespace
 
-// More segments fill more of the 152 SMs and shorten the chain of chunks, but with P > 1 every segment but the last
-// is walked once more for its sum and once for its map (twice the blocks for D = 128), and the segments are joined one
-// after another.  The costs below are the measured microseconds of a chunk in each kernel; the gradient runs both
-// recurrences in one grid.
-int tc_segments(const la_shape& s, bool bwd) {
+// When the last of n1 blocks of t1 us and then n2 of t2 us ends, one block to each of 152 SMs, taken in order.
+static double finish(long long n1, double t1, long long n2, double t2) {
     constexpr int kSms = 152;
-    const int BH = s.B * s.H, M = (s.N + kC - 1) / kC, ways = bwd ? 2 : 1;
-    const double main = bwd ? 4.2 : 3.2, sum = bwd ? 2.7 : 2.6, launch = 6.0;
-    auto waves = [](long long blocks) { return (double)((blocks + kSms - 1) / kSms); };
-    const int D = tc_dim(s);
-    const long long slices = (long long)BH * (D / 16) * ways;
-    const double join = (D == 128 ? 1.9 : 0.8) * (slices > kSms ? 1.6 * waves(slices / 2) : 1.0);
+    // SMs in two groups of equal time
+    double at[2] = {(double)(n1 / kSms + 1) * t1, (double)(n1 / kSms) * t1};
+    const long long count[2] = {n1 % kSms, kSms - n1 % kSms};
+    if (const long long rounds = n2 / kSms - 2; rounds > 0) {
+        n2 -= rounds * kSms;
+        at[0] += rounds * t2;
+        at[1] += rounds * t2;
+    }
+    double end = count[0] ? at[0] : at[1];
+    while (n2 > 0) {
+        const int g = count[0] && at[0] <= at[1] ? 0 : 1;
+        at[g] += t2;
+        end = at[g] > end ? at[g] : end;
+        n2 -= count[g];
+    }
+    return end;
+}
+
+// More segments fill more of the SMs and shorten the chain of chunks, but with P > 1 every segment but the last
+// is walked once more for its sum and once for its map (twice the blocks for D = 128), and the segments are joined one
+// after another.  The costs are measured microseconds: of a chunk in each kernel, of a block's start, of a step of the
+// join.  Predicted and measured, B=2 H=16 N=32768 D=128 gradient without prepare and tc_gd_grads: P = 1 1.82 and 1.80 ms,
+// 2 1.71 and 1.69, 4 1.70 and 1.68, 7 1.59 and 1.52, 19 1.76 and 1.73.
+int tc_segments(const la_shape& s, bool bwd) {
+    const bool wide = tc_dim(s) == 128;
+    const long long BH = (long long)s.B * s.H, M = (s.N + kC - 1) / kC;
+    const double out = wide ? 2.6 : 1.9, sum = wide ? 2.2 : 1.45;                           // forward; out also kGrad's
+    const double rev = bwd ? (wide ? 3.55 : 2.75) : 0., rsum = bwd ? (wide ? 3.0 : 1.95) : 0.;  // adjoint
+    const double start = 4.0, launch = 4.0;
+    const long long ways = bwd ? 2 : 1, slices = BH * (wide ? 8 : 4) * ways;
+    const double step = (wide ? 3.4 : 1.1) * (slices > 152 ? 1.7 * (double)((slices / 2 + 151) / 152) : 1.0);
+    auto walk = [&](long long P, double cps) {  // of every segment
+        return finish(bwd ? BH * P : 0, cps * rev + start, BH * P, cps * out + start);
+    };
     int best = 1;
-    double best_t = waves((long long)BH * ways) * M * main;
+    double best_t = walk(1, (double)M);
     for (int P = 2; P <= M && P <= 64; ++P) {
-        const int cps = (M + P - 1) / P;
+        const long long cps = (M + P - 1) / P;
         if ((M + cps - 1) / cps != P) continue;
-        const double t = waves((long long)BH * P * ways) * cps * main + 2 * launch + P * join +
-                         waves((long long)BH * (P - 1) * (ways - 1 + (D == 128 ? 2 : 1))) * cps * sum;
-        if (t < 0.97 * best_t) {
+        const long long sums = (wide ? 2 : 1) * (P - 1) + (bwd ? 1 : 0);  // the gradient wants the last segment's map too
+        const double t = walk(P, (double)cps) + 2 * launch + (P - 1) * step +
+                         finish(bwd ? BH * (P - 1) : 0, cps * rsum + start, BH * sums, cps * sum + start);
+        if (t < 0.99 * best_t) {
             best_t = t;
             best = P;
         }

@@ -62,8 +62,7 @@ __device__ __forceinline__ void zero(float (&acc)[RT][CT]) {
 // ------------------------------------------------------------------ gates, t and P of every chunk
 __global__ void __launch_bounds__(kThreads)
 gd_prepare(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ g,
-           const float* __restrict__ beta,
-           float* __restrict__ recs, float* __restrict__ ts, float* __restrict__ Ps, int N, int M, int Dk) {
+           const float* __restrict__ beta, float* __restrict__ recs, float* __restrict__ ts, float* __restrict__ Ps, int N, int M, int Dk) {
     extern __shared__ __align__(16) float smem[];
     Carve sm{smem};
     float* ks = sm.take(kC * (Dk + 1));
@@ -390,8 +389,8 @@ __device__ __forceinline__ float row_sum(float x) {
 
 template <int NK>  // Dk = 16 NK
 __global__ void __launch_bounds__(kThreads)
-gd_grads(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ g, const float* __restrict__ dout,
-         const float* __restrict__ recs, const float* __restrict__ Xs, const float* __restrict__ Ys,
+gd_grads(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ g,
+         const float* __restrict__ dout, const float* __restrict__ recs, const float* __restrict__ Xs, const float* __restrict__ Ys,
          const float* __restrict__ Ss, const float* __restrict__ dSs, float* __restrict__ dq, float* __restrict__ dk,
          float* __restrict__ dg, float* __restrict__ dbeta, int N, int M, int Dv) {
     constexpr int Dk = 16 * NK;
@@ -608,9 +607,10 @@ cudaError_t prepare(const void* q, const void* k, const void* g, const void* bet
     return launch_end("gd_prepare", st);
 }
 
-// Value columns of a slice.  Shared memory leaves room for one block to an SM at Dk = 128; a chunk takes a block about the same
-// time with 16 or 32 columns (too few warps to fill the SM) and 1.55 times that with 64.  Measured, gd_states of Dk = Dv = 128:
-// 64 chunks of 16 heads 438, 436, 670 us with 16, 32, 64 columns, 32 chunks of 48 heads 653, 436, 339, of 64 heads 868, 438, 340.
+// Value columns of a slice.  Shared memory leaves room for one block to an SM at Dk = 128; a chunk takes a block about
+// the same time with 16 or 32 columns (too few warps to fill the SM) and 1.55 times that with 64.  Measured, gd_states of
+// Dk = Dv = 128: 64 chunks of 16 heads 438, 436, 670 us with 16, 32, 64 columns, 32 chunks of 48 heads 653, 436, 339, of
+// 64 heads 868, 438, 340.
 int slice(const la_shape& s) {
     int best = 16;
     double least = 1e30;

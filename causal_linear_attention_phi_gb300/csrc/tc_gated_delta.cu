@@ -1,5 +1,6 @@
-// tc_gated_delta.cu -- tensor-core (tcgen05 / TMEM / TMA) kernels of the gated delta rule for bf16 heads with
-// Dk = Dv = 128 or 64 (formulas in gated_delta.cuh), chunks of 64 positions.
+// tc_gated_delta.cu -- tensor-core (tcgen05 / TMEM / TMA) kernels of the gated delta rule for bf16 heads (formulas in
+// gated_delta.cuh), chunks of 64 positions.  Heads run at D = 64 or 128 in both dimensions, the smaller that holds
+// them: the columns past the true sizes lie outside the tensor maps, arrive as zeros and are not stored.
 //
 // tc_gd_prepare (one block per chunk): [Q; K] K^T as one 128 x 64 product, the decays applied, t solved for in fp32;
 // t and P go to the workspace as bf16 hi + lo tiles in the swizzled layout that the products read.
@@ -10,10 +11,14 @@
 //   Y^T  = S^T K^T                            R^T = V^T - gam Y^T          (a column is a position)
 //   X^T  = R^T + R^T (t beta)^T               (u = beta X)
 //   S^T <- gam_C S^T + (tail beta X)^T K      O^T = gam (S^T Q^T) + X^T (P beta)^T
-// The fp32 state stays in registers (half a row to a thread).  Inputs K, Q are bf16 already; what is formed
+// The fp32 state stays in registers (a quarter of a row to a thread).  Inputs K, Q are bf16 already; what is formed
 // here (S, R, X, t, P) enters the products as hi + lo bf16 parts, x = hi + lo to 2^-17, except the S of
 // S^T Q^T, which meets one rounding only (it adds 0.5e-3 to the 1.7e-3 of rounding o itself; with
 // single parts throughout, correlated keys lift o's error to 7e-3 and the state's to 4e-3).
+// Bound by its chain: a chunk's products depend on each other, and each costs its issue, 64 cycles or more a step and a
+// round trip through TMEM and registers.  Measured at D = 128: 2.6 us a chunk with outputs, 2.2 us for a segment's sum or
+// map (1.9 and 1.45 us at D = 64), against 0.9 us of products; so a sequence is cut into segments, walked at the
+// same time (tc_segments).
 //
 // Roles (576 threads): warp 0 issues TMA, warp 1 tcgen05.mma, warps 2-17 compute: warp w serves TMEM lanes
 // 32 (w % 4) .. +31 (value columns r) and, by its group of four, 16 positions and D / 4 state columns of them.
@@ -30,7 +35,8 @@ using namespace tcgd;
 
 // ------------------------------------------------------------------ t and P of every chunk
 // 128 threads, six blocks to an SM: the phases of a chunk are short and each ends in a barrier, so what counts is how many
-// chunks an SM has in hand (256 threads and four blocks: 0.82 ms at B=2 H=16 N=65536 D=128).
+// chunks an SM has in hand (256 threads and four blocks took 0.82 ms at B=2 H=16 N=65536 D=128 where this takes 0.60).
+// Bound by what shared memory returns to registers (its pipe is busy 83 % of the time) while t is solved for.
 constexpr int kPrepThreads = 128;
 struct PrepSmem {
     // offset 0: blocks of [Q rows 0-63; K rows 64-127] x 64 columns, then (once the product has read them) fp32 A, which
@@ -357,7 +363,8 @@ __device__ __forceinline__ void join_block(const float* __restrict__ B, const fl
 template <int D, int kCols>
 __global__ void __launch_bounds__(JoinCfg<D, kCols>::threads)
 tc_gd_join(const float* __restrict__ B, const float* __restrict__ Mx, const float* __restrict__ first,
-           float* __restrict__ out, const float* __restrict__ B2, float* __restrict__ out2, int P, int Dk, int Dv, int* err) {
+           float* __restrict__ out, const float* __restrict__ B2, float* __restrict__ out2, int P, int Dk, int Dv,
+           int* err) {
     if (blockIdx.z == 0)
         join_block<D, false, kCols>(B, Mx, first, out, P, Dk, Dv, err);
     else
@@ -386,8 +393,8 @@ template cudaError_t prepare<128>(const CUtensorMap&, const CUtensorMap&, const 
                                   const la_shape&, int, bool, int*, cudaStream_t);
 
 template <int D>
-cudaError_t join(const float* B, const float* Mx, const float* first, float* out, const float* B2, float* out2, int BH, int P,
-                 int Dk, int Dv, int* err, cudaStream_t st) {
+cudaError_t join(const float* B, const float* Mx, const float* first, float* out, const float* B2, float* out2, int BH,
+                 int P, int Dk, int Dv, int* err, cudaStream_t st) {
     const int ways = out2 ? 2 : 1;
     const bool wide = (long long)BH * (D / 16) * ways > 152;
     auto kern = wide ? tc_gd_join<D, 32> : tc_gd_join<D, 16>;

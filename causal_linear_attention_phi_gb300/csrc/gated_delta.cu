@@ -103,20 +103,21 @@ gd_prepare(const float* __restrict__ q, const float* __restrict__ k, const float
 }
 
 // ------------------------------------------------------------------ products of the recurrences
-// Tiles in shared memory with rows of a multiple of 4 floats.  A thread forms 4 x 4 tiles, so that a multiply-add costs two
-// bytes of shared-memory reads (single columns of four rows cost five and were bound by them).
+// Tiles in shared memory with rows of a multiple of 4 floats.  A thread forms tiles of kR rows by 4 columns: with 4 rows a
+// multiply-add costs two bytes of shared-memory reads, with 2 rows three (single columns of four rows cost five and
+// were bound by them).
 // z[j] += sum_(x < K) a[(kStep j) lda + x] b[x ldb + 0..3]
-template <int kStep = 16>
-__device__ __forceinline__ void mac_rows(F4 (&z)[4], const float* a, int lda, const float* b, int ldb, int K) {
+template <int kStep, int kR>
+__device__ __forceinline__ void mac_rows(F4 (&z)[kR], const float* a, int lda, const float* b, int ldb, int K) {
 #pragma unroll 2
     for (int x = 0; x < K; x += 4) {
-        float4 av[4], bv[4];
+        float4 av[kR], bv[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) av[j] = ld_f4(a + kStep * j * lda + x);
+        for (int j = 0; j < kR; ++j) av[j] = ld_f4(a + kStep * j * lda + x);
 #pragma unroll
         for (int e = 0; e < 4; ++e) bv[e] = ld_f4(b + (x + e) * ldb);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kR; ++j) {
             fma4(z[j], av[j].x, bv[0]);
             fma4(z[j], av[j].y, bv[1]);
             fma4(z[j], av[j].z, bv[2]);
@@ -124,20 +125,29 @@ __device__ __forceinline__ void mac_rows(F4 (&z)[4], const float* a, int lda, co
         }
     }
 }
-// z[j] += sum_(x < K) a[x lda + j] b[x ldb + 0..3]: four consecutive columns of a as rows
-__device__ __forceinline__ void mac_cols(F4 (&z)[4], const float* a, int lda, const float* b, int ldb, int K) {
+// z[j] += sum_(x < K) a[x lda + j] b[x ldb + 0..3]: kR consecutive columns of a as rows
+template <int kR>
+__device__ __forceinline__ void mac_cols(F4 (&z)[kR], const float* a, int lda, const float* b, int ldb, int K) {
 #pragma unroll 4
     for (int x = 0; x < K; ++x) {
-        const float4 av = ld_f4(a + x * lda), bv = ld_f4(b + x * ldb);
-        fma4(z[0], av.x, bv);
-        fma4(z[1], av.y, bv);
-        fma4(z[2], av.z, bv);
-        fma4(z[3], av.w, bv);
+        const float4 bv = ld_f4(b + x * ldb);
+        if constexpr (kR == 4) {
+            const float4 av = ld_f4(a + x * lda);
+            fma4(z[0], av.x, bv);
+            fma4(z[1], av.y, bv);
+            fma4(z[2], av.z, bv);
+            fma4(z[3], av.w, bv);
+        } else {
+            const float2 av = *reinterpret_cast<const float2*>(a + x * lda);
+            fma4(z[0], av.x, bv);
+            fma4(z[1], av.y, bv);
+        }
     }
 }
-__device__ __forceinline__ void zero(F4 (&z)[4]) {
+template <int kR>
+__device__ __forceinline__ void zero(F4 (&z)[kR]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) z[j].a = z[j].b = make_float2(0.f, 0.f);
+    for (int j = 0; j < kR; ++j) z[j].a = z[j].b = make_float2(0.f, 0.f);
 }
 __device__ __forceinline__ F4 scaled(float m, const F4& z) {
     return {make_float2(m * z.a.x, m * z.a.y), make_float2(m * z.b.x, m * z.b.y)};
@@ -155,33 +165,33 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 // Rows [c0, c0 + n) of a [N][D] matrix into dst, pitch D + 4; the rows past n are 0.
-template <int W>
+template <int kThr>
 __device__ __forceinline__ void copy_rows(float* dst, const float* __restrict__ src, int c0, int n, int D) {
     const int lg = 29 - __clz(D);  // D / 4 is a power of two
-    for (int i = threadIdx.x; i < kC << lg; i += 4 * W) {
+    for (int i = threadIdx.x; i < kC << lg; i += kThr) {
         const int r = i >> lg, d = 4 * (i & (D / 4 - 1));
         copy16(dst + r * (D + 4) + d, src + (size_t)(c0 + (r < n ? r : 0)) * D + d, r < n);
     }
 }
-template <int W>
+template <int kThr>
 __device__ __forceinline__ void copy_square(float* dst, const float* __restrict__ src) {
-    for (int i = threadIdx.x; i < kC * kC / 4; i += 4 * W) copy16(dst + (i >> 4) * kLc4 + 4 * (i & 15), src + 4 * i, true);
+    for (int i = threadIdx.x; i < kC * kC / 4; i += kThr) copy16(dst + (i >> 4) * kLc4 + 4 * (i & 15), src + 4 * i, true);
 }
-template <int W>
+template <int kThr>
 __device__ __forceinline__ void copy_rec(float* dst, const float* __restrict__ src) {
-    for (int i = threadIdx.x; i < kRec / 4; i += 4 * W) copy16(dst + 4 * i, src + 4 * i, true);
+    for (int i = threadIdx.x; i < kRec / 4; i += kThr) copy16(dst + 4 * i, src + 4 * i, true);
 }
 
 // ------------------------------------------------------------------ the recurrence over chunks
-// Block (slice, head): value columns [W slice, +W), 4 W threads.  o, Xs / Ss (the gradient's records) and S_out may be null.
+// Block (slice, head): value columns [W slice, +W), threads with kR x 4 elements of 64 rows each.  o, Xs / Ss (the gradient's records) and S_out may be null.
 // K, which the last product of a chunk reads, has two buffers; Q, t and P of the next chunk are copied while the state moves on.
-template <int W>
-__global__ void __launch_bounds__(4 * W)
+template <int W, int kR>
+__global__ void __launch_bounds__(16 * W / kR)
 gd_states(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v, const float* S0,
           const float* __restrict__ recs, const float* __restrict__ ts, const float* __restrict__ Ps,
           float* __restrict__ o, float* __restrict__ Xs, float* __restrict__ Ss, float* S_out, int N, int M, int Dk,
           int Dv) {
-    constexpr int kLw = W + 4;
+    constexpr int kLw = W + 4, kG = kC / kR, kThr = kG * W / 4;
     extern __shared__ __align__(16) float smem[];
     Carve sm{smem};
     const int ld = Dk + 4;
@@ -200,44 +210,44 @@ gd_states(const float* __restrict__ q, const float* __restrict__ k, const float*
     q += bh * N * Dk;
     k += bh * N * Dk;
     auto copy_k = [&](int m) {
-        copy_rows<W>(k2 + (m & 1) * kC * ld, k, m * kC, min(kC, N - m * kC), Dk);
-        copy_rec<W>(rec2 + (m & 1) * kRec, recs + (bh * M + m) * kRec);
+        copy_rows<kThr>(k2 + (m & 1) * kC * ld, k, m * kC, min(kC, N - m * kC), Dk);
+        copy_rec<kThr>(rec2 + (m & 1) * kRec, recs + (bh * M + m) * kRec);
     };
     auto copy_rest = [&](int m) {
-        copy_square<W>(tt, ts + (bh * M + m) * kC * kC);
+        copy_square<kThr>(tt, ts + (bh * M + m) * kC * kC);
         if (o) {
-            copy_square<W>(PP, Ps + (bh * M + m) * kC * kC);
-            copy_rows<W>(qs, q, m * kC, min(kC, N - m * kC), Dk);
+            copy_square<kThr>(PP, Ps + (bh * M + m) * kC * kC);
+            copy_rows<kThr>(qs, q, m * kC, min(kC, N - m * kC), Dk);
         }
     };
     copy_k(0);
     copy_rest(0);
     copies_commit();
-    for (int d = rg; d < Dk; d += 16)
+    for (int d = rg; d < Dk; d += kG)
         *reinterpret_cast<float4*>(S + d * kLw + c) =
             S0 ? ld_f4(S0 + (bh * Dk + d) * Dv + col) : make_float4(0.f, 0.f, 0.f, 0.f);
     for (int m = 0; m < M; ++m) {
         const int c0 = m * kC, n = min(kC, N - c0);
         const size_t at = bh * M + m;
         const float *ks = k2 + (m & 1) * kC * ld, *rec = rec2 + (m & 1) * kRec;
-        float4 vv[4];
+        float4 vv[kR];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            vv[j] = rg + 16 * j < n ? ld_f4(v + (bh * N + c0 + rg + 16 * j) * (size_t)Dv + col)
+        for (int j = 0; j < kR; ++j)
+            vv[j] = rg + kG * j < n ? ld_f4(v + (bh * N + c0 + rg + kG * j) * (size_t)Dv + col)
                                     : make_float4(0.f, 0.f, 0.f, 0.f);
         copies_wait<0>();
         __syncthreads();  // the chunk's operands and the state are there; the other K has been read
         if (m + 1 < M) copy_k(m + 1);
         copies_commit();
         if (Ss)
-            for (int d = rg; d < Dk; d += 16)
+            for (int d = rg; d < Dk; d += kG)
                 *reinterpret_cast<float4*>(Ss + (at * Dk + d) * Dv + col) = ld_f4(S + d * kLw + c);
-        F4 x[4], w[4];
+        F4 x[kR], w[kR];
         zero(w);
-        mac_rows(w, ks + rg * ld, ld, S + c, kLw, Dk);
+        mac_rows<kG, kR>(w, ks + rg * ld, ld, S + c, kLw, Dk);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = rg + 16 * j;
+        for (int j = 0; j < kR; ++j) {
+            const int r = rg + kG * j;
             x[j] = scaled(-rec[kGam + r], w[j]);
             x[j].a.x += vv[j].x;
             x[j].a.y += vv[j].y;
@@ -246,11 +256,11 @@ gd_states(const float* __restrict__ q, const float* __restrict__ k, const float*
             put4(Rb + r * kLw + c, x[j], rec[kBeta + r]);
         }
         __syncthreads();
-        mac_rows(x, tt + rg * kLc4, kLc4, Rb + c, kLw, kC);
+        mac_rows<kG, kR>(x, tt + rg * kLc4, kLc4, Rb + c, kLw, kC);
         __syncthreads();  // Rb has been read
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = rg + 16 * j;
+        for (int j = 0; j < kR; ++j) {
+            const int r = rg + kG * j;
             if (Xs) put4(Xs + (at * kC + r) * Dv + col, x[j]);
             put4(Ub + r * kLw + c, x[j], rec[kBeta + r]);
             put4(Rb + r * kLw + c, x[j], rec[kTb + r]);
@@ -258,13 +268,13 @@ gd_states(const float* __restrict__ q, const float* __restrict__ k, const float*
         __syncthreads();
         if (o) {
             zero(w);
-            mac_rows(w, qs + rg * ld, ld, S + c, kLw, Dk);
+            mac_rows<kG, kR>(w, qs + rg * ld, ld, S + c, kLw, Dk);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = scaled(rec[kGam + rg + 16 * j], w[j]);
-            mac_rows(w, PP + rg * kLc4, kLc4, Ub + c, kLw, kC);
+            for (int j = 0; j < kR; ++j) w[j] = scaled(rec[kGam + rg + kG * j], w[j]);
+            mac_rows<kG, kR>(w, PP + rg * kLc4, kLc4, Ub + c, kLw, kC);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = rg + 16 * j;
+            for (int j = 0; j < kR; ++j) {
+                const int r = rg + kG * j;
                 if (r < n) put4(o + (bh * N + c0 + r) * (size_t)Dv + col, w[j]);
             }
             __syncthreads();  // the old slice, Q and P have been read
@@ -272,28 +282,28 @@ gd_states(const float* __restrict__ q, const float* __restrict__ k, const float*
         if (m + 1 < M) copy_rest(m + 1);
         copies_commit();
         const float gc = rec[kGam + kC - 1];
-        for (int g = rg; g < Dk / 4; g += 16) {
+        for (int g = rg; g < Dk / kR; g += kG) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = scaled(gc, get4(S + (4 * g + j) * kLw + c));
-            mac_cols(w, ks + 4 * g, ld, Rb + c, kLw, kC);
+            for (int j = 0; j < kR; ++j) w[j] = scaled(gc, get4(S + (kR * g + j) * kLw + c));
+            mac_cols(w, ks + kR * g, ld, Rb + c, kLw, kC);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) put4(S + (4 * g + j) * kLw + c, w[j]);
+            for (int j = 0; j < kR; ++j) put4(S + (kR * g + j) * kLw + c, w[j]);
         }
     }
     __syncthreads();
     if (S_out)
-        for (int d = rg; d < Dk; d += 16)
+        for (int d = rg; d < Dk; d += kG)
             *reinterpret_cast<float4*>(S_out + (bh * Dk + d) * Dv + col) = ld_f4(S + d * kLw + c);
 }
 
 // ------------------------------------------------------------------ the adjoint recurrence, last chunk first
 // As above: K in two buffers, Q copied under the products before its own, t and P under the state's.
-template <int W>
-__global__ void __launch_bounds__(4 * W)
+template <int W, int kR>
+__global__ void __launch_bounds__(16 * W / kR)
 gd_reverse(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ dout,
            const float* __restrict__ recs, const float* __restrict__ ts, const float* __restrict__ Ps,
            float* __restrict__ dv, float* __restrict__ Ys, float* __restrict__ dSs, int N, int M, int Dk, int Dv) {
-    constexpr int kLw = W + 4;
+    constexpr int kLw = W + 4, kG = kC / kR, kThr = kG * W / 4;
     extern __shared__ __align__(16) float smem[];
     Carve sm{smem};
     const int ld = Dk + 4;
@@ -312,54 +322,54 @@ gd_reverse(const float* __restrict__ q, const float* __restrict__ k, const float
     q += bh * N * Dk;
     k += bh * N * Dk;
     auto copy_k = [&](int m) {
-        copy_rows<W>(k2 + (m & 1) * kC * ld, k, m * kC, min(kC, N - m * kC), Dk);
-        copy_rec<W>(rec2 + (m & 1) * kRec, recs + (bh * M + m) * kRec);
+        copy_rows<kThr>(k2 + (m & 1) * kC * ld, k, m * kC, min(kC, N - m * kC), Dk);
+        copy_rec<kThr>(rec2 + (m & 1) * kRec, recs + (bh * M + m) * kRec);
     };
     auto copy_squares = [&](int m) {
-        copy_square<W>(tt, ts + (bh * M + m) * kC * kC);
-        copy_square<W>(PP, Ps + (bh * M + m) * kC * kC);
+        copy_square<kThr>(tt, ts + (bh * M + m) * kC * kC);
+        copy_square<kThr>(PP, Ps + (bh * M + m) * kC * kC);
     };
     copy_k(M - 1);
     copy_squares(M - 1);
     copies_commit();
-    for (int d = rg; d < Dk; d += 16) *reinterpret_cast<float4*>(S + d * kLw + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int d = rg; d < Dk; d += kG) *reinterpret_cast<float4*>(S + d * kLw + c) = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int m = M - 1; m >= 0; --m) {
         const int c0 = m * kC, n = min(kC, N - c0);
         const size_t at = bh * M + m;
         const float *ks = k2 + (m & 1) * kC * ld, *rec = rec2 + (m & 1) * kRec;
-        float4 dd[4];  // rows 4 rg .. 4 rg + 3, here and below
+        float4 dd[kR];  // rows kR rg + j, here and below
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            dd[j] = 4 * rg + j < n ? ld_f4(dout + (bh * N + c0 + 4 * rg + j) * (size_t)Dv + col)
+        for (int j = 0; j < kR; ++j)
+            dd[j] = kR * rg + j < n ? ld_f4(dout + (bh * N + c0 + kR * rg + j) * (size_t)Dv + col)
                                    : make_float4(0.f, 0.f, 0.f, 0.f);
         copies_wait<0>();
         __syncthreads();  // the chunk's operands and the state are there; Q and the other K have been read
-        copy_rows<W>(qs, q, c0, n, Dk);
+        copy_rows<kThr>(qs, q, c0, n, Dk);
         copies_commit();
         if (m > 0) copy_k(m - 1);
         copies_commit();
-        for (int d = rg; d < Dk; d += 16)
+        for (int d = rg; d < Dk; d += kG)
             *reinterpret_cast<float4*>(dSs + (at * Dk + d) * Dv + col) = ld_f4(S + d * kLw + c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) *reinterpret_cast<float4*>(Db + (4 * rg + j) * kLw + c) = dd[j];
-        F4 y[4];
+        for (int j = 0; j < kR; ++j) *reinterpret_cast<float4*>(Db + (kR * rg + j) * kLw + c) = dd[j];
+        F4 y[kR];
         zero(y);
-        mac_rows<1>(y, ks + 4 * rg * ld, ld, S + c, kLw, Dk);
+        mac_rows<1, kR>(y, ks + kR * rg * ld, ld, S + c, kLw, Dk);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = scaled(rec[kTail + 4 * rg + j], y[j]);
+        for (int j = 0; j < kR; ++j) y[j] = scaled(rec[kTail + kR * rg + j], y[j]);
         __syncthreads();  // dO
-        mac_cols(y, PP + 4 * rg, kLc4, Db + c, kLw, kC);
+        mac_cols(y, PP + kR * rg, kLc4, Db + c, kLw, kC);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) put4(Ub + (4 * rg + j) * kLw + c, y[j], rec[kBeta + 4 * rg + j]);
+        for (int j = 0; j < kR; ++j) put4(Ub + (kR * rg + j) * kLw + c, y[j], rec[kBeta + kR * rg + j]);
         __syncthreads();
-        mac_cols(y, tt + 4 * rg, kLc4, Ub + c, kLw, kC);
+        mac_cols(y, tt + kR * rg, kLc4, Ub + c, kLw, kC);
         copies_wait<1>();  // Q
         __syncthreads();   // Ub, Db, t and P have been read
         if (m > 0) copy_squares(m - 1);
         copies_commit();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = 4 * rg + j;
+        for (int j = 0; j < kR; ++j) {
+            const int r = kR * rg + j;
             put4(Ys + (at * kC + r) * Dv + col, y[j]);
             if (r < n) put4(dv + (bh * N + c0 + r) * (size_t)Dv + col, y[j], rec[kBeta + r]);
             put4(Ub + r * kLw + c, y[j], rec[kBg + r]);
@@ -367,14 +377,14 @@ gd_reverse(const float* __restrict__ q, const float* __restrict__ k, const float
         }
         __syncthreads();
         const float gc = rec[kGam + kC - 1];
-        for (int g = rg; g < Dk / 4; g += 16) {
-            F4 s[4];
+        for (int g = rg; g < Dk / kR; g += kG) {
+            F4 s[kR];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[j] = scaled(gc, get4(S + (4 * g + j) * kLw + c));
-            mac_cols(s, qs + 4 * g, ld, Db + c, kLw, kC);
-            mac_cols(s, ks + 4 * g, ld, Ub + c, kLw, kC);
+            for (int j = 0; j < kR; ++j) s[j] = scaled(gc, get4(S + (kR * g + j) * kLw + c));
+            mac_cols(s, qs + kR * g, ld, Db + c, kLw, kC);
+            mac_cols(s, ks + kR * g, ld, Ub + c, kLw, kC);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) put4(S + (4 * g + j) * kLw + c, s[j]);
+            for (int j = 0; j < kR; ++j) put4(S + (kR * g + j) * kLw + c, s[j]);
         }
     }
 }
@@ -607,28 +617,27 @@ cudaError_t prepare(const void* q, const void* k, const void* g, const void* bet
     return launch_end("gd_prepare", st);
 }
 
-// Value columns of a slice.  Shared memory leaves room for one block to an SM at Dk = 128; a chunk takes a block about
-// the same time with 16 or 32 columns (too few warps to fill the SM) and 1.55 times that with 64.  Measured, gd_states of
-// Dk = Dv = 128: 64 chunks of 16 heads 438, 436, 670 us with 16, 32, 64 columns, 32 chunks of 48 heads 653, 436, 339, of
-// 64 heads 868, 438, 340.
+// Value columns of a slice.  Shared memory leaves room for one block to an SM at Dk = 128.  Measured microseconds of a chunk
+// there in gd_states (gd_reverse): 16 columns 5.6 (10.3) in tiles of 2 rows and 6.8 (11.0) of 4; 32 columns 8.2 (12.5)
+// and 6.8 (12.0); 64 columns 14.7 (23) and 10.6 (16.7).  16 columns are bound by latency, 64 by shared-memory reads.
 int slice(const la_shape& s) {
     int best = 16;
     double least = 1e30;
     for (int w = 16; w <= 64 && w <= s.Dv; w *= 2) {
         const long long blocks = (long long)s.B * s.H * (s.Dv / w);
-        const double t = (double)((blocks + 151) / 152) * (w == 64 ? 1.55 : w == 32 ? 1.02 : 1.0);
+        const double t = (double)((blocks + 151) / 152) * (w == 64 ? 1.75 : w == 32 ? 1.2 : 1.0);
         if (t < least) best = w, least = t;
     }
     return best;
 }
 
-template <int W>
+template <int W, int kR>
 cudaError_t launch_states(const void* q, const void* k, const void* v, const float* S0, void* o, float* X, float* S,
                           float* S_out, const la_shape& s, const Layout& L, char* ws, int M, cudaStream_t st) {
     const size_t sm = smem_states(s.Dk, W);
-    GD_TRY(allow_smem(gd_states<W>, sm));
+    GD_TRY((allow_smem(gd_states<W, kR>, sm)));
     launch_begin("gd_states", st);
-    gd_states<W><<<dim3(s.Dv / W, s.B * s.H), 4 * W, sm, st>>>(
+    gd_states<W, kR><<<dim3(s.Dv / W, s.B * s.H), 16 * W / kR, sm, st>>>(
         (const float*)q, (const float*)k, (const float*)v, S0, (const float*)(ws + L.rec), (const float*)(ws + L.t),
         (const float*)(ws + L.P), (float*)o, X, S, S_out, s.N, M, s.Dk, s.Dv);
     return launch_end("gd_states", st);
@@ -636,18 +645,18 @@ cudaError_t launch_states(const void* q, const void* k, const void* v, const flo
 cudaError_t states(const void* q, const void* k, const void* v, const float* S0, void* o, float* X, float* S,
                    float* S_out, const la_shape& s, const Layout& L, char* ws, int M, cudaStream_t st) {
     switch (slice(s)) {
-        case 16: return launch_states<16>(q, k, v, S0, o, X, S, S_out, s, L, ws, M, st);
-        case 32: return launch_states<32>(q, k, v, S0, o, X, S, S_out, s, L, ws, M, st);
-        default: return launch_states<64>(q, k, v, S0, o, X, S, S_out, s, L, ws, M, st);
+        case 16: return launch_states<16, 2>(q, k, v, S0, o, X, S, S_out, s, L, ws, M, st);
+        case 32: return launch_states<32, 4>(q, k, v, S0, o, X, S, S_out, s, L, ws, M, st);
+        default: return launch_states<64, 4>(q, k, v, S0, o, X, S, S_out, s, L, ws, M, st);
     }
 }
 
-template <int W>
+template <int W, int kR>
 cudaError_t launch_reverse(const BwdArgs& a, const la_shape& s, const Layout& L, char* ws, int M, cudaStream_t st) {
     const size_t sm = smem_states(s.Dk, W);
-    GD_TRY(allow_smem(gd_reverse<W>, sm));
+    GD_TRY((allow_smem(gd_reverse<W, kR>, sm)));
     launch_begin("gd_reverse", st);
-    gd_reverse<W><<<dim3(s.Dv / W, s.B * s.H), 4 * W, sm, st>>>(
+    gd_reverse<W, kR><<<dim3(s.Dv / W, s.B * s.H), 16 * W / kR, sm, st>>>(
         (const float*)a.q, (const float*)a.k, (const float*)a.dout, (const float*)(ws + L.rec),
         (const float*)(ws + L.t), (const float*)(ws + L.P), (float*)a.dv, (float*)(ws + L.Y), (float*)(ws + L.dS), s.N, M,
         s.Dk, s.Dv);
@@ -719,9 +728,9 @@ cudaError_t simt_bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t
     GD_TRY(prepare(a.q, a.k, a.g, a.beta, L, ws, s, M, st));
     GD_TRY(states(a.q, a.k, a.v, nullptr, nullptr, (float*)(ws + L.X), (float*)(ws + L.S), nullptr, s, L, ws, M, st));
     switch (slice(s)) {
-        case 16: GD_TRY(launch_reverse<16>(a, s, L, ws, M, st)); break;
-        case 32: GD_TRY(launch_reverse<32>(a, s, L, ws, M, st)); break;
-        default: GD_TRY(launch_reverse<64>(a, s, L, ws, M, st)); break;
+        case 16: GD_TRY((launch_reverse<16, 2>(a, s, L, ws, M, st))); break;
+        case 32: GD_TRY((launch_reverse<32, 4>(a, s, L, ws, M, st))); break;
+        default: GD_TRY((launch_reverse<64, 4>(a, s, L, ws, M, st))); break;
     }
     switch (s.Dk) {
         case 16: return launch_grads<1>(a, s, L, ws, M, st);

@@ -2,9 +2,11 @@
 //
 // Forward: gd_prepare (one block per chunk: gates, t, P) and gd_states (one block per head and slice of value
 // columns, which are independent of each other: it walks the chunks with its slice of S in shared memory and
-// writes o).  Gradient: gd_prepare, gd_states (X and the state entering every chunk), gd_reverse (the
-// adjoint recurrence from the last chunk back, sliced alike: dv, Y and the gradient leaving every chunk) and
+// writes o).  Gradient: gd_prepare, gd_sweeps (the forward recurrence for X and the state entering every chunk and,
+// beside it, the adjoint one from the last chunk back, sliced alike: dv, Y and the gradient leaving every chunk) and
 // gd_grads (one block per chunk: dq, dk, dg, dbeta).  All arithmetic is fp32; sums of log decays fp64.
+// Bound by what shared memory returns to registers and, where there are few heads, by the chain of a chunk's products:
+// B=2 H=32 N=2048 128 x 128 takes 0.74 ms forward (its operations 0.31 ms at 128 multiply-adds a clock and SM).
 #include "gated_delta.cuh"
 #include "sm100.cuh"
 
@@ -186,8 +188,8 @@ __device__ __forceinline__ void copy_rec(float* dst, const float* __restrict__ s
 // Block (slice, head): value columns [W slice, +W), threads with kR x 4 elements of 64 rows each.  o, Xs / Ss (the gradient's records) and S_out may be null.
 // K, which the last product of a chunk reads, has two buffers; Q, t and P of the next chunk are copied while the state moves on.
 template <int W, int kR>
-__global__ void __launch_bounds__(16 * W / kR)
-gd_states(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v, const float* S0,
+__device__ __forceinline__ void
+states_block(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v, const float* S0,
           const float* __restrict__ recs, const float* __restrict__ ts, const float* __restrict__ Ps,
           float* __restrict__ o, float* __restrict__ Xs, float* __restrict__ Ss, float* S_out, int N, int M, int Dk,
           int Dv) {
@@ -299,8 +301,8 @@ gd_states(const float* __restrict__ q, const float* __restrict__ k, const float*
 // ------------------------------------------------------------------ the adjoint recurrence, last chunk first
 // As above: K in two buffers, Q copied under the products before its own, t and P under the state's.
 template <int W, int kR>
-__global__ void __launch_bounds__(16 * W / kR)
-gd_reverse(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ dout,
+__device__ __forceinline__ void
+reverse_block(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ dout,
            const float* __restrict__ recs, const float* __restrict__ ts, const float* __restrict__ Ps,
            float* __restrict__ dv, float* __restrict__ Ys, float* __restrict__ dSs, int N, int M, int Dk, int Dv) {
     constexpr int kLw = W + 4, kG = kC / kR, kThr = kG * W / 4;
@@ -387,6 +389,28 @@ gd_reverse(const float* __restrict__ q, const float* __restrict__ k, const float
             for (int j = 0; j < kR; ++j) put4(S + (kR * g + j) * kLw + c, s[j]);
         }
     }
+}
+
+template <int W, int kR>
+__global__ void __launch_bounds__(16 * W / kR)
+gd_states(FwdArgs a, const float* __restrict__ recs, const float* __restrict__ ts, const float* __restrict__ Ps, int N,
+          int M, int Dk, int Dv) {
+    states_block<W, kR>((const float*)a.q, (const float*)a.k, (const float*)a.v, a.S0, recs, ts, Ps, (float*)a.o, nullptr,
+                        nullptr, a.S, N, M, Dk, Dv);
+}
+
+// The gradient's two recurrences do not depend on each other: one grid, the adjoint one (the longer) first.
+template <int W, int kR>
+__global__ void __launch_bounds__(16 * W / kR)
+gd_sweeps(BwdArgs a, const float* __restrict__ recs, const float* __restrict__ ts, const float* __restrict__ Ps,
+          float* __restrict__ X, float* __restrict__ Y, float* __restrict__ S, float* __restrict__ dS, int N, int M, int Dk,
+          int Dv) {
+    if (blockIdx.z == 0)
+        reverse_block<W, kR>((const float*)a.q, (const float*)a.k, (const float*)a.dout, recs, ts, Ps, (float*)a.dv, Y, dS,
+                             N, M, Dk, Dv);
+    else
+        states_block<W, kR>((const float*)a.q, (const float*)a.k, (const float*)a.v, nullptr, recs, ts, Ps, nullptr, X, S,
+                            nullptr, N, M, Dk, Dv);
 }
 
 // ------------------------------------------------------------------ dq, dk, dg, dbeta of one chunk
@@ -617,50 +641,40 @@ cudaError_t prepare(const void* q, const void* k, const void* g, const void* bet
     return launch_end("gd_prepare", st);
 }
 
-// Value columns of a slice.  Shared memory leaves room for one block to an SM at Dk = 128.  Measured microseconds of a chunk
-// there in gd_states (gd_reverse): 16 columns 5.6 (10.3) in tiles of 2 rows and 6.8 (11.0) of 4; 32 columns 8.2 (12.5)
-// and 6.8 (12.0); 64 columns 14.7 (23) and 10.6 (16.7).  16 columns are bound by latency, 64 by shared-memory reads.
-int slice(const la_shape& s) {
+// Value columns of a slice.  Shared memory leaves room for one block to an SM at Dk = 128.  Measured microseconds of a
+// chunk there, forward (adjoint) recurrence: 16 columns 5.6 (10.3) in tiles of 2 rows and 6.8 (11.0) of 4; 32 columns 8.2
+// (12.5) and 6.8 (12.0); 64 columns 14.7 (23) and 10.6 (16.7).  16 columns are bound by latency, 64 by shared-memory reads.
+int slice(const la_shape& s, bool bwd) {
+    static constexpr double fwd_us[] = {5.6, 6.8, 10.6}, rev_us[] = {10.3, 12.0, 16.7};
     int best = 16;
     double least = 1e30;
-    for (int w = 16; w <= 64 && w <= s.Dv; w *= 2) {
-        const long long blocks = (long long)s.B * s.H * (s.Dv / w);
-        const double t = (double)((blocks + 151) / 152) * (w == 64 ? 1.75 : w == 32 ? 1.2 : 1.0);
-        if (t < least) best = w, least = t;
+    for (int i = 0; i < 3 && (16 << i) <= s.Dv; ++i) {
+        const long long blocks = (long long)s.B * s.H * (s.Dv / (16 << i));
+        const double t = finish(bwd ? blocks : 0, rev_us[i], blocks, fwd_us[i]);
+        if (t < least) best = 16 << i, least = t;
     }
     return best;
 }
 
 template <int W, int kR>
-cudaError_t launch_states(const void* q, const void* k, const void* v, const float* S0, void* o, float* X, float* S,
-                          float* S_out, const la_shape& s, const Layout& L, char* ws, int M, cudaStream_t st) {
+cudaError_t launch_states(const FwdArgs& a, const la_shape& s, const Layout& L, char* ws, int M, cudaStream_t st) {
     const size_t sm = smem_states(s.Dk, W);
     GD_TRY((allow_smem(gd_states<W, kR>, sm)));
     launch_begin("gd_states", st);
     gd_states<W, kR><<<dim3(s.Dv / W, s.B * s.H), 16 * W / kR, sm, st>>>(
-        (const float*)q, (const float*)k, (const float*)v, S0, (const float*)(ws + L.rec), (const float*)(ws + L.t),
-        (const float*)(ws + L.P), (float*)o, X, S, S_out, s.N, M, s.Dk, s.Dv);
+        a, (const float*)(ws + L.rec), (const float*)(ws + L.t), (const float*)(ws + L.P), s.N, M, s.Dk, s.Dv);
     return launch_end("gd_states", st);
-}
-cudaError_t states(const void* q, const void* k, const void* v, const float* S0, void* o, float* X, float* S,
-                   float* S_out, const la_shape& s, const Layout& L, char* ws, int M, cudaStream_t st) {
-    switch (slice(s)) {
-        case 16: return launch_states<16, 2>(q, k, v, S0, o, X, S, S_out, s, L, ws, M, st);
-        case 32: return launch_states<32, 4>(q, k, v, S0, o, X, S, S_out, s, L, ws, M, st);
-        default: return launch_states<64, 4>(q, k, v, S0, o, X, S, S_out, s, L, ws, M, st);
-    }
 }
 
 template <int W, int kR>
-cudaError_t launch_reverse(const BwdArgs& a, const la_shape& s, const Layout& L, char* ws, int M, cudaStream_t st) {
+cudaError_t launch_sweeps(const BwdArgs& a, const la_shape& s, const Layout& L, char* ws, int M, cudaStream_t st) {
     const size_t sm = smem_states(s.Dk, W);
-    GD_TRY((allow_smem(gd_reverse<W, kR>, sm)));
-    launch_begin("gd_reverse", st);
-    gd_reverse<W, kR><<<dim3(s.Dv / W, s.B * s.H), 16 * W / kR, sm, st>>>(
-        (const float*)a.q, (const float*)a.k, (const float*)a.dout, (const float*)(ws + L.rec),
-        (const float*)(ws + L.t), (const float*)(ws + L.P), (float*)a.dv, (float*)(ws + L.Y), (float*)(ws + L.dS), s.N, M,
-        s.Dk, s.Dv);
-    return launch_end("gd_reverse", st);
+    GD_TRY((allow_smem(gd_sweeps<W, kR>, sm)));
+    launch_begin("gd_sweeps", st);
+    gd_sweeps<W, kR><<<dim3(s.Dv / W, s.B * s.H, 2), 16 * W / kR, sm, st>>>(
+        a, (const float*)(ws + L.rec), (const float*)(ws + L.t), (const float*)(ws + L.P), (float*)(ws + L.X),
+        (float*)(ws + L.Y), (float*)(ws + L.S), (float*)(ws + L.dS), s.N, M, s.Dk, s.Dv);
+    return launch_end("gd_sweeps", st);
 }
 
 template <int NK>
@@ -719,18 +733,21 @@ cudaError_t simt_fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t
     const int M = (s.N + kC - 1) / kC;
     const Layout L = layout(s, false);
     GD_TRY(prepare(a.q, a.k, a.g, a.beta, L, ws, s, M, st));
-    return states(a.q, a.k, a.v, a.S0, a.o, nullptr, nullptr, a.S, s, L, ws, M, st);
+    switch (slice(s, false)) {
+        case 16: return launch_states<16, 2>(a, s, L, ws, M, st);
+        case 32: return launch_states<32, 4>(a, s, L, ws, M, st);
+        default: return launch_states<64, 4>(a, s, L, ws, M, st);
+    }
 }
 
 cudaError_t simt_bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) {
     const int M = (s.N + kC - 1) / kC;
     const Layout L = layout(s, true);
     GD_TRY(prepare(a.q, a.k, a.g, a.beta, L, ws, s, M, st));
-    GD_TRY(states(a.q, a.k, a.v, nullptr, nullptr, (float*)(ws + L.X), (float*)(ws + L.S), nullptr, s, L, ws, M, st));
-    switch (slice(s)) {
-        case 16: GD_TRY((launch_reverse<16, 2>(a, s, L, ws, M, st))); break;
-        case 32: GD_TRY((launch_reverse<32, 4>(a, s, L, ws, M, st))); break;
-        default: GD_TRY((launch_reverse<64, 4>(a, s, L, ws, M, st))); break;
+    switch (slice(s, true)) {
+        case 16: GD_TRY((launch_sweeps<16, 2>(a, s, L, ws, M, st))); break;
+        case 32: GD_TRY((launch_sweeps<32, 4>(a, s, L, ws, M, st))); break;
+        default: GD_TRY((launch_sweeps<64, 4>(a, s, L, ws, M, st))); break;
     }
     switch (s.Dk) {
         case 16: return launch_grads<1>(a, s, L, ws, M, st);

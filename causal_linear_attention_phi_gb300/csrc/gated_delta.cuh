@@ -281,6 +281,8 @@ cudaError_t simt_bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t
 // bf16, on the tensor cores: heads are padded on chip to 64 or 128 in both dimensions (tc_dim).
 bool tc_ok(const la_shape& s);
 int tc_dim(const la_shape& s);
+// When the last of n1 blocks of t1 us and then n2 of t2 us ends, one block to each of 152 SMs, taken in order.
+double finish(long long n1, double t1, long long n2, double t2);
 // Segments of a head for M chunks (a function of the sizes alone).
 int tc_segments(const la_shape& s, bool bwd);
 cudaError_t tc_fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st);

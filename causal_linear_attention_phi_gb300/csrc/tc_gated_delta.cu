@@ -470,8 +470,7 @@ cudaError_t fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
 
 }  // namespace
 
-// When the last of n1 blocks of t1 us and then n2 of t2 us ends, one block to each of 152 SMs, taken in order.
-static double finish(long long n1, double t1, long long n2, double t2) {
+double finish(long long n1, double t1, long long n2, double t2) {
     constexpr int kSms = 152;
     // SMs in two groups of equal time
     double at[2] = {(double)(n1 / kSms + 1) * t1, (double)(n1 / kSms) * t1};

@@ -36,7 +36,7 @@ using namespace tcgd;
 // ------------------------------------------------------------------ t and P of every chunk
 // 128 threads, six blocks to an SM: the phases of a chunk are short and each ends in a barrier, so what counts is how many
 // chunks an SM has in hand (256 threads and four blocks took 0.82 ms at B=2 H=16 N=65536 D=128 where this takes 0.60).
-// Bound by what shared memory returns to registers (its pipe is busy 83 % of the time) while t is solved for.
+// Bound by what shared memory returns to registers (its data pipe is busy 62 % of the time) while t is solved for.
 constexpr int kPrepThreads = 128;
 struct PrepSmem {
     // offset 0: blocks of [Q rows 0-63; K rows 64-127] x 64 columns, then (once the product has read them) fp32 A, which

@@ -284,6 +284,8 @@ la_status la_retention_step(const void* q, const void* k, const void* v, const f
  * S0: NULL, or a DEVICE fp32 [B,H,Dk,Dv]: the state before the first position.
  * S: NULL, or a DEVICE fp32 [B,H,Dk,Dv] that receives the state after the last position (written; S0, or zero,
  *   for N = 0), from which la_gated_delta_step or another la_gated_delta_fwd continues.  It may be S0 itself.
+ * A state returned from a bf16 call is formed from operands in two bf16 parts: within 3e-6 of its largest element
+ * (fp32 calls: 5e-7).
  * Workspace: la_workspace_bytes(LA_OP_GATED_DELTA_FWD, s).
  */
 la_status la_gated_delta_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,

@@ -238,15 +238,15 @@ tc_gd_states(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 // out[p + 1] = B[p] + M[p] out[p], or in reverse out[p - 1] = B[p] + M[p]^T out[p].  A map (64 KB for D = 128) is copied to
 // shared memory while the previous one is applied.  A thread forms 2 rows x 4 columns with packed multiply-adds: per
 // four terms 6 vector loads from shared memory to 16 of those.
-// 16 columns to a block, with the terms of a product halved between two groups of threads, or 32 columns where that
-// many blocks would not be resident at once (a block's two maps fill most of an SM's shared memory).
+// 32 columns to a block, or 16 or 8 where so many blocks are resident at once (a block's two maps fill most of an SM's shared
+// memory), with the terms of a product split between two or four groups of threads: fewer columns read the map less often.
 template <int D, int kCols>
 struct JoinCfg {
     static constexpr int group = D / 2 * (kCols / 4), split = 32 / kCols, threads = group * split;
     static constexpr int map = D * D * 4;
     static constexpr int S = 2 * map;              // [D][kCols]
-    static constexpr int half = S + D * kCols * 4;  // the second group's sums
-    static constexpr int bars = half + (split > 1 ? D * kCols * 4 : 0);
+    static constexpr int half = S + D * kCols * 4;  // the other groups' sums
+    static constexpr int bars = half + (split - 1) * D * kCols * 4;
     static constexpr size_t bytes = bars + 32;
 };
 
@@ -340,19 +340,22 @@ __device__ __forceinline__ void join_block(const float* __restrict__ B, const fl
             }
         }
         if (L::split > 1) {
-            if (part == 1) {
+            if (part > 0) {
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
-                    half[y * L::group] = make_float4(acc[y].a.x, acc[y].a.y, acc[y].b.x, acc[y].b.y);
+                    half[(2 * (part - 1) + y) * L::group] = make_float4(acc[y].a.x, acc[y].a.y, acc[y].b.x, acc[y].b.y);
             }
-            __syncthreads();  // S and the map have been read, the second sums are there
+            __syncthreads();  // S and the map have been read, the other sums are there
         }
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
             s[y] = make_float4(acc[y].a.x, acc[y].a.y, acc[y].b.x, acc[y].b.y);
-            if (L::split > 1 && part == 0) {
-                const float4 h = half[y * L::group];
-                s[y] = make_float4(s[y].x + h.x, s[y].y + h.y, s[y].z + h.z, s[y].w + h.w);
+            if (part == 0) {
+#pragma unroll
+                for (int o = 0; o < L::split - 1; ++o) {
+                    const float4 h = half[(2 * o + y) * L::group];
+                    s[y] = make_float4(s[y].x + h.x, s[y].y + h.y, s[y].z + h.z, s[y].w + h.w);
+                }
             }
         }
         if (L::split == 1) __syncthreads();  // S and the map have been read
@@ -396,16 +399,18 @@ template <int D>
 cudaError_t join(const float* B, const float* Mx, const float* first, float* out, const float* B2, float* out2, int BH,
                  int P, int Dk, int Dv, int* err, cudaStream_t st) {
     const int ways = out2 ? 2 : 1;
-    const bool wide = (long long)BH * (D / 16) * ways > 152;
-    auto kern = wide ? tc_gd_join<D, 32> : tc_gd_join<D, 16>;
-    const size_t smem = wide ? JoinCfg<D, 32>::bytes : JoinCfg<D, 16>::bytes;
-    GD_TRY(allow_smem(kern, smem));
-    launch_begin("tc_gd_join", st);
-    const cudaError_t e = launch_pdl(kern, dim3(D / (wide ? 32 : 16), BH, ways),
-                                     dim3(wide ? JoinCfg<D, 32>::threads : JoinCfg<D, 16>::threads), smem, st, B, Mx, first,
-                                     out, B2, out2, P, Dk, Dv, err);
-    const cudaError_t e2 = launch_end("tc_gd_join", st);
-    return e != cudaSuccess ? e : e2;
+    auto go = [&](auto kern, int cols, int threads, size_t smem) {
+        GD_TRY(allow_smem(kern, smem));
+        launch_begin("tc_gd_join", st);
+        const cudaError_t e = launch_pdl(kern, dim3(D / cols, BH, ways), dim3(threads), smem, st, B, Mx, first, out, B2, out2,
+                                         P, Dk, Dv, err);
+        const cudaError_t e2 = launch_end("tc_gd_join", st);
+        return e != cudaSuccess ? e : e2;
+    };
+    const long long slices = (long long)BH * (D / 16) * ways;
+    if (2 * slices <= 152) return go(tc_gd_join<D, 8>, 8, JoinCfg<D, 8>::threads, JoinCfg<D, 8>::bytes);
+    if (slices <= 152) return go(tc_gd_join<D, 16>, 16, JoinCfg<D, 16>::threads, JoinCfg<D, 16>::bytes);
+    return go(tc_gd_join<D, 32>, 32, JoinCfg<D, 32>::threads, JoinCfg<D, 32>::bytes);
 }
 template cudaError_t join<64>(const float*, const float*, const float*, float*, const float*, float*, int, int, int, int,
                               int*, cudaStream_t);

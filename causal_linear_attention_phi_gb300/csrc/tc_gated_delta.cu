@@ -507,7 +507,8 @@ int tc_segments(const la_shape& s, bool bwd) {
     const double rev = bwd ? (wide ? 3.55 : 2.75) : 0., rsum = bwd ? (wide ? 3.0 : 1.95) : 0.;  // adjoint
     const double start = 4.0, launch = 4.0;
     const long long ways = bwd ? 2 : 1, slices = BH * (wide ? 8 : 4) * ways;
-    const double step = (wide ? 3.4 : 1.1) * (slices > 152 ? 1.7 * (double)((slices / 2 + 151) / 152) : 1.0);
+    const double step = 2 * slices <= 152 ? (wide ? 1.8 : 0.8)
+                                          : (wide ? 3.4 : 1.1) * (slices > 152 ? 1.7 * (double)((slices / 2 + 151) / 152) : 1.0);
     auto walk = [&](long long P, double cps) {  // of every segment
         return finish(bwd ? BH * P : 0, cps * rev + start, BH * P, cps * out + start);
     };

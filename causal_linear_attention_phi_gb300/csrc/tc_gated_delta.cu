@@ -35,7 +35,7 @@ using namespace tcgd;
 
 // ------------------------------------------------------------------ t and P of every chunk
 // 128 threads, six blocks to an SM: the phases of a chunk are short and each ends in a barrier, so what counts is how many
-// chunks an SM has in hand (256 threads and four blocks took 0.82 ms at B=2 H=16 N=65536 D=128 where this takes 0.60).
+// chunks an SM has in hand (at B=2 H=16 N=65536 D=128 0.49 ms; five blocks 0.60, four of 256 threads 0.82).
 // Bound by what shared memory returns to registers (its data pipe is busy 62 % of the time) while t is solved for.
 constexpr int kPrepThreads = 128;
 struct PrepSmem {
@@ -48,7 +48,8 @@ struct PrepSmem {
     static constexpr int total = bar + 32;
 };
 static_assert(PrepSmem::P >= kC * kLd * 4 && PrepSmem::rec >= 4 * kBlk, "regions");
-constexpr size_t kPrepBytes = PrepSmem::total + 1024;
+constexpr size_t kPrepBytes = PrepSmem::total;  // no slack for alignment: it would cost the sixth block
+static_assert(6 * (kPrepBytes + 1024) <= 233472, "six blocks to an SM");
 
 // w[x] (columns j0 .. j0 + 31 of row i) times the decay from j to i, 0 outside j <= last (kFull: all inside).
 template <bool kResets, bool kFull>
@@ -76,8 +77,11 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
 tc_gd_prepare(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __nv_bfloat16* __restrict__ g, const __nv_bfloat16* __restrict__ beta, float* __restrict__ recs,
               uint8_t* __restrict__ mats, int N, int M, int* err) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t base[];
+    if (smem_u32(base) & 1023) {  // the swizzled tiles need it
+        if (threadIdx.x == 0) atomicCAS(err, 0, (int)LA_ERR_BOUNDS);
+        return;
+    }
     float* rec = reinterpret_cast<float*>(base + PrepSmem::rec);
     uint64_t* bar = reinterpret_cast<uint64_t*>(base + PrepSmem::bar);  // loads, product
     uint32_t* slot = reinterpret_cast<uint32_t*>(bar + 2);

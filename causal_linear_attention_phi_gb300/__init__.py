@@ -76,6 +76,7 @@ def _declare(lib):
     lib.la_retention_step.argtypes = [_vp] * 6 + [Shape, _vp]
     lib.la_gated_delta_fwd.argtypes = [_vp] * 8 + [Shape, _vp, ctypes.c_size_t, _vp]
     lib.la_gated_delta_bwd.argtypes = [_vp] * 11 + [Shape, _vp, ctypes.c_size_t, _vp]
+    lib.la_gated_delta_bwd_with_state.argtypes = [_vp] * 14 + [Shape, _vp, ctypes.c_size_t, _vp]
     lib.la_gated_delta_step.argtypes = [_vp] * 7 + [Shape, _vp]
     lib.la_layer_norm_fwd.argtypes = [_vp] * 6 + [NormShape, ctypes.c_float, _vp]
     lib.la_layer_norm_workspace_bytes.argtypes = [NormShape]
@@ -86,8 +87,8 @@ def _declare(lib):
     for f in ("la_causal_step_host", "la_noncausal_fwd", "la_noncausal_bwd", "la_causal_fwd",
               "la_causal_fwd_with_state", "la_causal_bwd", "la_causal_bwd_after_fwd", "la_recurrent_step",
               "la_retention_fwd", "la_retention_step", "la_gated_delta_fwd", "la_gated_delta_bwd",
-              "la_gated_delta_step", "la_layer_norm_fwd", "la_layer_norm_bwd", "la_selftest_bounded_wait", "la_selftest_lookback_timeout",
-              "la_last_error", "la_causal_fwd_fused",
+              "la_gated_delta_bwd_with_state", "la_gated_delta_step", "la_layer_norm_fwd", "la_layer_norm_bwd",
+              "la_selftest_bounded_wait", "la_selftest_lookback_timeout", "la_last_error", "la_causal_fwd_fused",
               "la_clear_error", "la_timing_enable", "la_timing_reset"):
         getattr(lib, f).restype = ctypes.c_int
     lib.la_last_error.argtypes = []
@@ -437,8 +438,13 @@ def gated_delta_fwd(q, k, v, g, beta, S0=None, out=None, workspace=None, stream=
 
 
 def gated_delta_bwd(q, k, v, g, beta, dout, dq=None, dk=None, dv=None, dg=None, dbeta=None, workspace=None,
-                    stream=None):
-    """Gradients (dq, dk, dv, dg, dbeta) of gated_delta_fwd (from the zero state) for upstream gradient dout."""
+                    stream=None, S0=None, dS=None, return_dS0=False):
+    """Gradients (dq, dk, dv, dg, dbeta) of gated_delta_fwd for upstream gradient dout.
+
+    For a piece of a longer sequence: S0 is the state that the forward was given, dS the gradient of the state
+    that it returned (fp32 [B,H,Dk,Dv]; zero if None), and with return_dS0 the gradient of S0 is returned as well,
+    last: the dS of the piece before.
+    """
     lead, Dk, Dv, code = _delta_args(q, k, v, g, beta)
     if len(lead) != 3:
         raise ValueError("expected q, k [B,H,N,Dk] and v [B,H,N,Dv]")
@@ -451,10 +457,16 @@ def gated_delta_bwd(q, k, v, g, beta, dout, dq=None, dk=None, dv=None, dg=None, 
     dv = _result(dv, v, "dv")
     dg = _result(dg, g, "dg")
     dbeta = _result(dbeta, beta, "dbeta")
+    state = (lead[0], lead[1], Dk, Dv)
+    for t, what in ((S0, "S0"), (dS, "dS")):
+        if t is not None:
+            _state(t, state, what)
+    dS0 = torch.empty(state, dtype=torch.float32, device=q.device) if return_dS0 else None
     ws, nb = _workspace(OP_GATED_DELTA_BWD, s, q.device, workspace)
-    _check(library().la_gated_delta_bwd(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(dout), _p(dq), _p(dk), _p(dv), _p(dg),
-                                        _p(dbeta), s, _p(ws), nb, _stream_ptr(stream)), "la_gated_delta_bwd")
-    return dq, dk, dv, dg, dbeta
+    _check(library().la_gated_delta_bwd_with_state(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(S0), _p(dout), _p(dS), _p(dq),
+                                                   _p(dk), _p(dv), _p(dg), _p(dbeta), _p(dS0), s, _p(ws), nb,
+                                                   _stream_ptr(stream)), "la_gated_delta_bwd_with_state")
+    return (dq, dk, dv, dg, dbeta, dS0) if return_dS0 else (dq, dk, dv, dg, dbeta)
 
 
 def gated_delta_step(q, k, v, g, beta, S, out=None, stream=None):

@@ -680,24 +680,44 @@ la_status la_gated_delta_fwd(const void* q, const void* k, const void* v, const 
                        "gated delta forward");
 }
 
-la_status la_gated_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
-                             const void* dout, void* dq, void* dk, void* dv, void* dg, void* dbeta, la_shape s,
-                             void* ws, size_t ws_bytes, la_stream_t stream) {
+la_status la_gated_delta_bwd_with_state(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                                        const float* S0, const void* dout, const float* dS, void* dq, void* dk, void* dv,
+                                        void* dg, void* dbeta, float* dS0, la_shape s, void* ws, size_t ws_bytes,
+                                        la_stream_t stream) {
     t_detail.clear();
     LA_TRY(check_shape(s));
-    if (empty(s)) return LA_OK;
-    LA_TRY(check_bwd_args(q, k, v, dout, dq, dk, dv));
+    if (s.B == 0 || s.H == 0) return LA_OK;
+    if (s.N == 0 && !dS0) return LA_OK;
+    if (s.N > 0) LA_TRY(check_bwd_args(q, k, v, dout, dq, dk, dv));
+    LA_TRY(check_device());
+    if (S0) LA_TRY(check_ptr(S0, "S0"));
+    if (dS) LA_TRY(check_ptr(dS, "dS"));
+    if (dS0) LA_TRY(check_ptr(dS0, "dS0"));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (s.N == 0) {  // no position: the gradient passes through
+        const size_t bytes = (size_t)s.B * s.H * s.Dk * s.Dv * sizeof(float);
+        if (dS0 == dS) return LA_OK;
+        return cuda_status(dS ? cudaMemcpyAsync(dS0, dS, bytes, cudaMemcpyDeviceToDevice, st)
+                              : cudaMemsetAsync(dS0, 0, bytes, st),
+                           "state gradient copy");
+    }
     const uintptr_t elem = s.dtype == LA_BF16 ? 2 : 4;
     LA_TRY(check_ptr(g, "g", elem));
     LA_TRY(check_ptr(beta, "beta", elem));
     LA_TRY(check_ptr(dg, "dg", elem));
     LA_TRY(check_ptr(dbeta, "dbeta", elem));
     LA_TRY(check_ws(ws, ws_bytes, gd::layout(s, true).bytes));
-    const gd::BwdArgs a{q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta};
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const gd::BwdArgs a{q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta, S0, dS, dS0};
     return cuda_status(gd::tc_ok(s) ? gd::tc_bwd(a, s, static_cast<char*>(ws), st)
                                     : gd::simt_bwd(a, s, static_cast<char*>(ws), st),
                        "gated delta backward");
+}
+
+la_status la_gated_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                             const void* dout, void* dq, void* dk, void* dv, void* dg, void* dbeta, la_shape s,
+                             void* ws, size_t ws_bytes, la_stream_t stream) {
+    return la_gated_delta_bwd_with_state(q, k, v, g, beta, nullptr, dout, nullptr, dq, dk, dv, dg, dbeta, nullptr, s, ws,
+                                         ws_bytes, stream);
 }
 
 la_status la_gated_delta_step(const void* q, const void* k, const void* v, const void* g, const void* beta, float* S,

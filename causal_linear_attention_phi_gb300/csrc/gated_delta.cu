@@ -313,7 +313,8 @@ template <int W, int kR>
 __device__ __forceinline__ void
 reverse_block(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ dout,
            const float* __restrict__ recs, const float* __restrict__ ts, const float* __restrict__ Ps,
-           float* __restrict__ dv, float* __restrict__ Ys, float* __restrict__ dSs, int N, int M, int Dk, int Dv) {
+           float* __restrict__ dv, float* __restrict__ Ys, float* __restrict__ dSs, const float* __restrict__ dS,
+           float* __restrict__ dS0, int N, int M, int Dk, int Dv) {
     constexpr int kLw = W + 4, kG = kC / kR, kThr = kG * W / 4;
     extern __shared__ __align__(16) float smem[];
     Carve sm{smem};
@@ -343,7 +344,9 @@ reverse_block(const float* __restrict__ q, const float* __restrict__ k, const fl
     copy_k(M - 1);
     copy_squares(M - 1);
     copies_commit();
-    for (int d = rg; d < Dk; d += kG) *reinterpret_cast<float4*>(S + d * kLw + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int d = rg; d < Dk; d += kG)
+        *reinterpret_cast<float4*>(S + d * kLw + c) =
+            dS ? ld_f4(dS + (bh * Dk + d) * Dv + col) : make_float4(0.f, 0.f, 0.f, 0.f);
     for (int m = M - 1; m >= 0; --m) {
         const int c0 = m * kC, n = min(kC, N - c0);
         const size_t at = bh * M + m;
@@ -398,6 +401,10 @@ reverse_block(const float* __restrict__ q, const float* __restrict__ k, const fl
             for (int j = 0; j < kR; ++j) put4(S + (kR * g + j) * kLw + c, s[j]);
         }
     }
+    __syncthreads();
+    if (dS0)
+        for (int d = rg; d < Dk; d += kG)
+            *reinterpret_cast<float4*>(dS0 + (bh * Dk + d) * Dv + col) = ld_f4(S + d * kLw + c);
 }
 
 template <int W, int kR>
@@ -416,9 +423,9 @@ gd_sweeps(BwdArgs a, const float* __restrict__ recs, const float* __restrict__ t
           int Dv) {
     if (blockIdx.z == 0)
         reverse_block<W, kR>((const float*)a.q, (const float*)a.k, (const float*)a.dout, recs, ts, Ps, (float*)a.dv, Y, dS,
-                             N, M, Dk, Dv);
+                             a.dS, a.dS0, N, M, Dk, Dv);
     else
-        states_block<W, kR>((const float*)a.q, (const float*)a.k, (const float*)a.v, nullptr, recs, ts, Ps, nullptr, X, S,
+        states_block<W, kR>((const float*)a.q, (const float*)a.k, (const float*)a.v, a.S0, recs, ts, Ps, nullptr, X, S,
                             nullptr, N, M, Dk, Dv);
 }
 

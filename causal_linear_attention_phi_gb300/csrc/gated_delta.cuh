@@ -274,6 +274,8 @@ struct FwdArgs {
 struct BwdArgs {
     const void *q, *k, *v, *g, *beta, *dout;
     void *dq, *dk, *dv, *dg, *dbeta;
+    const float *S0, *dS;  // the state before the first position, the gradient of the one after the last; null: zero
+    float* dS0;            // null: not wanted
 };
 // fp32, any head size, on the CUDA cores.
 cudaError_t simt_fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st);

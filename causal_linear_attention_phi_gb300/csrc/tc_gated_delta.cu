@@ -289,7 +289,7 @@ __device__ __forceinline__ void join_block(const float* __restrict__ B, const fl
     if (part == 0) {
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-            s[y] = !kReverse && first && row + y < Dk && col < Dv  // the caller's state: true sizes
+            s[y] = first && row + y < Dk && col < Dv  // the caller's state or its gradient: true sizes
                        ? ld_f4(first + (bh * Dk + row + y) * Dv + col)
                        : make_float4(0.f, 0.f, 0.f, 0.f);
         load_b(0);
@@ -366,16 +366,16 @@ __device__ __forceinline__ void join_block(const float* __restrict__ B, const fl
     }
 }
 
-// The third grid dimension: 0 forwards, 1 in reverse (the gradient's, from zero).
+// The third grid dimension: 0 forwards, 1 in reverse (the gradient's).
 template <int D, int kCols>
 __global__ void __launch_bounds__(JoinCfg<D, kCols>::threads)
 tc_gd_join(const float* __restrict__ B, const float* __restrict__ Mx, const float* __restrict__ first,
-           float* __restrict__ out, const float* __restrict__ B2, float* __restrict__ out2, int P, int Dk, int Dv,
-           int* err) {
+           float* __restrict__ out, const float* __restrict__ B2, const float* __restrict__ first2,
+           float* __restrict__ out2, int P, int Dk, int Dv, int* err) {
     if (blockIdx.z == 0)
         join_block<D, false, kCols>(B, Mx, first, out, P, Dk, Dv, err);
     else
-        join_block<D, true, kCols>(B2, Mx, nullptr, out2, P, Dk, Dv, err);
+        join_block<D, true, kCols>(B2, Mx, first2, out2, P, Dk, Dv, err);
 }
 
 }  // namespace
@@ -400,14 +400,14 @@ template cudaError_t prepare<128>(const CUtensorMap&, const CUtensorMap&, const 
                                   const la_shape&, int, bool, int*, cudaStream_t);
 
 template <int D>
-cudaError_t join(const float* B, const float* Mx, const float* first, float* out, const float* B2, float* out2, int BH,
-                 int P, int Dk, int Dv, int* err, cudaStream_t st) {
+cudaError_t join(const float* B, const float* Mx, const float* first, float* out, const float* B2, const float* first2,
+                 float* out2, int BH, int P, int Dk, int Dv, int* err, cudaStream_t st) {
     const int ways = out2 ? 2 : 1;
     auto go = [&](auto kern, int cols, int threads, size_t smem) {
         GD_TRY(allow_smem(kern, smem));
         launch_begin("tc_gd_join", st);
-        const cudaError_t e = launch_pdl(kern, dim3(D / cols, BH, ways), dim3(threads), smem, st, B, Mx, first, out, B2, out2,
-                                         P, Dk, Dv, err);
+        const cudaError_t e = launch_pdl(kern, dim3(D / cols, BH, ways), dim3(threads), smem, st, B, Mx, first, out, B2, first2,
+                                         out2, P, Dk, Dv, err);
         const cudaError_t e2 = launch_end("tc_gd_join", st);
         return e != cudaSuccess ? e : e2;
     };
@@ -416,10 +416,10 @@ cudaError_t join(const float* B, const float* Mx, const float* first, float* out
     if (slices <= 152) return go(tc_gd_join<D, 16>, 16, JoinCfg<D, 16>::threads, JoinCfg<D, 16>::bytes);
     return go(tc_gd_join<D, 32>, 32, JoinCfg<D, 32>::threads, JoinCfg<D, 32>::bytes);
 }
-template cudaError_t join<64>(const float*, const float*, const float*, float*, const float*, float*, int, int, int, int,
-                              int*, cudaStream_t);
-template cudaError_t join<128>(const float*, const float*, const float*, float*, const float*, float*, int, int, int, int,
-                               int*, cudaStream_t);
+template cudaError_t join<64>(const float*, const float*, const float*, float*, const float*, const float*, float*, int,
+                              int, int, int, int*, cudaStream_t);
+template cudaError_t join<128>(const float*, const float*, const float*, float*, const float*, const float*, float*, int,
+                               int, int, int, int*, cudaStream_t);
 
 }  // namespace tcgd
 
@@ -461,7 +461,7 @@ cudaError_t fwd(const FwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
         sa.segB = B;
         sa.segM = Mx;
         GD_TRY((states<D, kSum>(tq, tk, tv, sa, dim3(L.segs - 1, BH, D == 128 ? 2 : 1), err, st)));
-        GD_TRY(join<D>(B, Mx, a.S0, S, nullptr, nullptr, BH, L.segs, s.Dk, s.Dv, err, st));
+        GD_TRY(join<D>(B, Mx, a.S0, S, nullptr, nullptr, nullptr, BH, L.segs, s.Dk, s.Dv, err, st));
         sa.S0 = S;
         sa.dk = sa.dv = D;
     } else {

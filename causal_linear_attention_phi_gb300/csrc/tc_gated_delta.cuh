@@ -218,11 +218,11 @@ struct StateArgs {
     float *segB, *segM;           // kSum: [BH][P] records
     int M, P, cps;                // chunks, segments, chunks of a segment
 };
-// Joins the segments' sums: out[p + 1] = B[p] + M[p] out[p] from out[0] = first (Dk x Dv records; null: zero) and, where
-// out2 is given, in reverse out2[p - 1] = B2[p] + M[p]^T out2[p] from out2[P - 1] = 0.
+// Joins the segments' sums: out[p + 1] = B[p] + M[p] out[p] from out[0] = first and, where out2 is given, in reverse
+// out2[p - 1] = B2[p] + M[p]^T out2[p] from out2[P - 1] = first2 (first, first2: Dk x Dv records; null: zero).
 template <int D>
-cudaError_t join(const float* B, const float* Mx, const float* first, float* out, const float* B2, float* out2, int BH,
-                 int P, int Dk, int Dv, int* err, cudaStream_t st);
+cudaError_t join(const float* B, const float* Mx, const float* first, float* out, const float* B2, const float* first2,
+                 float* out2, int BH, int P, int Dk, int Dv, int* err, cudaStream_t st);
 
 }  // namespace tcgd
 }  // namespace gd

@@ -52,9 +52,11 @@ struct ReverseArgs {
     const float* recs;
     const uint8_t* mats;
     uint8_t *y_tiles, *ds_tiles;
-    const float* segdS;  // [BH][P]: the gradients of the segments' last states; null: zero
+    const float* segdS;  // [BH][P] records of ek x ev: the gradients of the segments' last states; null: zero
+    int ek, ev;
     float* segB2;        // kSums: [BH][P]
-    int M, P, cps, Dv;
+    float* dS0;          // [BH] Dk x Dv: the gradient of the first state, or null
+    int M, P, cps, Dk, Dv;
 };
 
 template <int D>
@@ -216,8 +218,9 @@ __device__ __forceinline__ void reverse_block(const CUtensorMap& tm_q, const CUt
         float2 S[kSc / 2];
 #pragma unroll
         for (int x = 0; x < kSc / 2; ++x) {
-            const float* s0 = a.segdS + (((size_t)bh * P + p) * D + kSc * h + 2 * x) * D + r;
-            S[x] = !kSums && a.segdS && r < D ? make_float2(s0[0], s0[D]) : make_float2(0.f, 0.f);
+            const int c = kSc * h + 2 * x;
+            const float* s0 = a.segdS + (((size_t)bh * P + p) * a.ek + c) * a.ev + r;
+            S[x] = !kSums && a.segdS && r < a.ev && c < a.ek ? make_float2(s0[0], s0[a.ev]) : make_float2(0.f, 0.f);
         }
         uint8_t* out = base + L::out;
         for (int i = 0; i < nloc; ++i) {
@@ -358,6 +361,13 @@ __device__ __forceinline__ void reverse_block(const CUtensorMap& tm_q, const CUt
 #pragma unroll
             for (int x = 0; x < kSc; ++x)
                 a.segB2[(((size_t)bh * P + p) * D + kSc * h + x) * D + r] = x & 1 ? S[x / 2].y : S[x / 2].x;
+        }
+        if (!kSums && a.dS0 && p == 0 && r < a.Dv) {
+#pragma unroll
+            for (int x = 0; x < kSc; ++x) {
+                const int c = kSc * h + x;
+                if (c < a.Dk) a.dS0[((size_t)bh * a.Dk + c) * a.Dv + r] = x & 1 ? S[x / 2].y : S[x / 2].x;
+            }
         }
         tc_fence_before();
     }
@@ -849,17 +859,24 @@ cudaError_t bwd(const BwdArgs& a, const la_shape& s, char* ws, cudaStream_t st) 
     ra.M = M;
     ra.P = L.segs;
     ra.cps = L.cps;
-    ra.Dv = s.Dv;
+    ra.Dk = ra.ek = s.Dk;
+    ra.Dv = ra.ev = s.Dv;
+    ra.segdS = a.dS;
+    ra.dS0 = a.dS0;
+    sa.S0 = a.S0;
+    sa.dk = s.Dk;
+    sa.dv = s.Dv;
     if (L.segs > 1) {
         sa.segB = (float*)(ws + L.segB);
         sa.segM = (float*)(ws + L.segM);
         ra.segB2 = (float*)(ws + L.segB2);
         GD_TRY((sweeps<D, true>(tq, tk, tv, tdo, tdv, sa, ra, dim3(L.segs, BH, D == 128 ? 3 : 2), err, st)));
-        GD_TRY(join<D>(sa.segB, sa.segM, nullptr, (float*)(ws + L.segS), ra.segB2, (float*)(ws + L.segdS), BH, L.segs, D, D,
-                       err, st));
+        GD_TRY(join<D>(sa.segB, sa.segM, a.S0, (float*)(ws + L.segS), ra.segB2, a.dS, (float*)(ws + L.segdS), BH, L.segs,
+                       s.Dk, s.Dv, err, st));
         sa.S0 = (float*)(ws + L.segS);
         sa.dk = sa.dv = D;
         ra.segdS = (float*)(ws + L.segdS);
+        ra.ek = ra.ev = D;
     }
     GD_TRY((sweeps<D, false>(tq, tk, tv, tdo, tdv, sa, ra, dim3(L.segs, BH, 2), err, st)));
     GD_TRY(allow_smem(tc_gd_grads<D>, GradSmem<D>::bytes));

@@ -293,7 +293,7 @@ la_status la_gated_delta_fwd(const void* q, const void* k, const void* v, const 
                              void* ws, size_t ws_bytes, la_stream_t stream);
 
 /*
- * Gradient of la_gated_delta_fwd (from the zero state) for an upstream gradient dout = dL/do:
+ * Gradient of la_gated_delta_fwd from the zero state for an upstream gradient dout = dL/do:
  * dq, dk: [B,H,N,Dk]; dv: [B,H,N,Dv]; dg, dbeta: [B,H,N], all in s.dtype and written.  dg is the gradient with
  * respect to g (the log of the decay); it is 0 where g is below -100.  Everything is recomputed from the
  * inputs; the workspace holds one state and one state gradient for each chunk of 64 positions, so memory is linear in N.
@@ -302,6 +302,17 @@ la_status la_gated_delta_fwd(const void* q, const void* k, const void* v, const 
 la_status la_gated_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
                              const void* dout, void* dq, void* dk, void* dv, void* dg, void* dbeta, la_shape s,
                              void* ws, size_t ws_bytes, la_stream_t stream);
+
+/*
+ * The same for a sequence that starts from a state or hands one on (a piece of a longer one):
+ * S0: NULL (zero), or the state that la_gated_delta_fwd was given.  dS: NULL (zero), or dL/dS for the state S that
+ * it returned, the dS0 of the piece after this one.  dS0: NULL, or receives dL/dS0 (it may be dS).  All DEVICE fp32
+ * [B,H,Dk,Dv], 16-byte aligned.  For N = 0, dS0 = dS.  Same workspace.
+ */
+la_status la_gated_delta_bwd_with_state(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                                        const float* S0, const void* dout, const float* dS, void* dq, void* dk, void* dv,
+                                        void* dg, void* dbeta, float* dS0, la_shape s, void* ws, size_t ws_bytes,
+                                        la_stream_t stream);
 
 /*
  * One decode step of the gated delta rule for every head:

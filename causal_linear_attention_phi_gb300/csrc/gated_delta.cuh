@@ -178,28 +178,42 @@ __device__ __forceinline__ void acc_tile(F4 (&z)[4], const float* row, const flo
 // t_i = -(A_i + sum_(j<i) A_ij beta_j t_j), one column to a lane, the column in registers; then blocks are joined in
 // pairs, first to 32 and then to 64: t21 = -(I + t22 beta) A21 (I + beta t11), two small products each.  (Diagonal
 // blocks of 32 left all but two warps waiting for a chain of 31 rows.)
-// solve_diagonal: one warp, the two diagonal blocks of rows 32 w .. 32 w + 31, which it needs complete.
+// solve_diagonal: one warp, the two diagonal blocks of rows 32 w .. 32 w + 31, which it needs complete.  A row is loaded
+// while the one before it is solved, and takes the newest value last: a row then waits for one multiply-add.
 __device__ __forceinline__ void solve_diagonal(float* A, const float* beta, int w, int lane) {
     constexpr int kQ = kC / 4;
     const int b0 = 32 * w + (lane & 16), c = lane & 15;
     float y[kQ];  // beta_j t_j of this column
+    float4 row[kQ / 4];
+    float own, be;
+    auto load = [&](int r) {  // row r up to the diagonal, broadcast
+        const float* a = A + (b0 + r) * kLd + b0;
+#pragma unroll
+        for (int j = 0; j < r; j += 4) row[j / 4] = ld_f4(a + j);
+        own = a[c];
+        be = beta[b0 + r];
+    };
     y[0] = 0.f;
+    load(1);
 #pragma unroll
     for (int r = 1; r < kQ; ++r) {
-        float* a = A + (b0 + r) * kLd + b0;
-        float s0 = a[c], s1 = 0.f;
+        float s[4] = {own, 0.f, 0.f, 0.f};
+        float last = 0.f;
 #pragma unroll
-        for (int j = 0; j < r; j += 4) {
-            const float4 v = ld_f4(a + j);  // broadcast; zero from the diagonal on
-            s0 = fmaf(v.x, y[j], s0);
-            if (j + 1 < r) s1 = fmaf(v.y, y[j + 1], s1);
-            if (j + 2 < r) s0 = fmaf(v.z, y[j + 2], s0);
-            if (j + 3 < r) s1 = fmaf(v.w, y[j + 3], s1);
+        for (int j = 0; j < r; ++j) {
+            const float v = j % 4 == 0 ? row[j / 4].x : j % 4 == 1 ? row[j / 4].y : j % 4 == 2 ? row[j / 4].z : row[j / 4].w;
+            if (j < r - 1)
+                s[j & 3] = fmaf(v, y[j], s[j & 3]);
+            else
+                last = v;
         }
-        const float x = r > c ? -(s0 + s1) : 0.f;
+        const float b = be;
+        if (r + 1 < kQ) load(r + 1);
+        const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+        const float x = r > c ? -fmaf(last, y[r - 1], sum) : 0.f;
         __syncwarp();  // the row has been read
-        a[c] = x;
-        y[r] = beta[b0 + r] * x;
+        A[(b0 + r) * kLd + b0 + c] = x;
+        y[r] = b * x;
     }
 }
 

@@ -35,7 +35,7 @@ using namespace tcgd;
 
 // ------------------------------------------------------------------ t and P of every chunk
 // 128 threads, six blocks to an SM: the phases of a chunk are short and each ends in a barrier, so what counts is how many
-// chunks an SM has in hand (at B=2 H=16 N=65536 D=128 0.49 ms; five blocks 0.60, four of 256 threads 0.82).
+// chunks an SM has in hand (at B=2 H=16 N=65536 D=128 0.49 ms; with five blocks 0.60, four of 256 threads 0.82).
 // Shared memory's data pipe is the busiest unit (58 %): while t is solved for, loads cost the bytes they return.
 constexpr int kPrepThreads = 128;
 struct PrepSmem {

@@ -3,7 +3,9 @@
 A thin ctypes binding over the C ABI of ``libla.so`` (declared in
 ``include/la.h``).  It only marshals arguments: every step of the computation
 runs in the library's CUDA kernels.  PyTorch supplies device memory (outputs
-and the workspace come from its caching allocator) and the current stream.
+and the workspace come from its caching allocator) and the current stream.  A
+call with ``stream=`` runs on that stream and allocates there; ordering it after
+the work that made its inputs, and later work after it, is the caller's.
 There is no CPU fallback: if the library is not built, importing works but
 every call raises ``RuntimeError``.
 """
@@ -163,6 +165,47 @@ def _stream_ptr(stream=None) -> int:
     return int(torch.cuda.current_stream().cuda_stream)
 
 
+# What a call allocates comes from the pool of the stream that it runs on: the current stream, or the one given.  Memory of
+# the current stream's pool may still be in use by work queued there, which another stream does not wait for, and a
+# workspace dropped on return would be handed to the current stream's next tensor under the kernels that use it.
+def _elsewhere(stream):
+    """`stream` as a torch stream where it is another than the current one, else None."""
+    if stream is None or int(stream.cuda_stream) == _stream_ptr():
+        return None
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream.cuda_stream))
+
+
+def _scratch(nbytes, device, stream):
+    """Memory that only the call's kernels use."""
+    side = _elsewhere(stream)
+    if side is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(side):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _handed_out(make, stream):
+    """The tensor `make` allocates, which the caller gets: once the caller lets go of it, its memory waits for the current
+    stream too."""
+    side = _elsewhere(stream)
+    if side is None:
+        return make()
+    with torch.cuda.stream(side):
+        t = make()
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _new_like(t, stream):
+    if stream is None:
+        return torch.empty_like(t)
+    return _handed_out(lambda: torch.empty_like(t), stream)
+
+
+def _new_f32(shape, device, stream):
+    return _handed_out(lambda: torch.empty(shape, dtype=torch.float32, device=device), stream)
+
+
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None and t.numel() > 0 else ctypes.c_void_p(0)
 
@@ -184,7 +227,7 @@ def workspace_bytes(op: int, B: int, H: int, N: int, Dk: int, Dv: int, dtype: to
     return int(library().la_workspace_bytes(op, Shape(B, H, N, Dk, Dv, code)))
 
 
-def _workspace(op, s: Shape, device, workspace):
+def _workspace(op, s: Shape, device, workspace, stream):
     need = int(library().la_workspace_bytes(op, s))
     if workspace is not None:
         if not workspace.is_cuda:
@@ -192,7 +235,7 @@ def _workspace(op, s: Shape, device, workspace):
         return workspace, workspace.numel() * workspace.element_size()  # its real size: the library checks it
     if need == 0:
         return None, 0
-    return torch.empty(need, dtype=torch.uint8, device=device), need
+    return _scratch(need, device, stream), need
 
 
 def noncausal_fwd(q, k, v, out=None, workspace=None, stream=None):
@@ -200,8 +243,8 @@ def noncausal_fwd(q, k, v, out=None, workspace=None, stream=None):
     _need_cuda(q, k, v)
     s = _shape4(q, k, v)
     if out is None:
-        out = torch.empty_like(v)
-    ws, nb = _workspace(OP_NONCAUSAL_FWD, s, q.device, workspace)
+        out = _new_like(v, stream)
+    ws, nb = _workspace(OP_NONCAUSAL_FWD, s, q.device, workspace, stream)
     _check(library().la_noncausal_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), s, _ptr(ws), nb, _stream_ptr(stream)),
            "la_noncausal_fwd")
     return out
@@ -218,16 +261,16 @@ def causal_fwd(q, k, v, out=None, workspace=None, stream=None, return_state=Fals
     _need_cuda(q, k, v)
     s = _shape4(q, k, v)
     if out is None:
-        out = torch.empty_like(v)
-    ws, nb = _workspace(OP_CAUSAL_FWD, s, q.device, workspace)
+        out = _new_like(v, stream)
+    ws, nb = _workspace(OP_CAUSAL_FWD, s, q.device, workspace, stream)
     if not return_state:
         fn = library().la_causal_fwd_fused if one_launch else library().la_causal_fwd
         _check(fn(_ptr(q), _ptr(k), _ptr(v), _ptr(out), s, _ptr(ws), nb, _stream_ptr(stream)),
                "la_causal_fwd_fused" if one_launch else "la_causal_fwd")
         return out
     B, H, _, Dk = q.shape
-    S = torch.empty(B, H, Dk, v.shape[-1], dtype=torch.float32, device=q.device)
-    z = torch.empty(B, H, Dk, dtype=torch.float32, device=q.device)
+    S = _new_f32((B, H, Dk, v.shape[-1]), q.device, stream)
+    z = _new_f32((B, H, Dk), q.device, stream)
     _check(library().la_causal_fwd_with_state(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(S), _ptr(z), s, _ptr(ws),
                                               nb, _stream_ptr(stream)), "la_causal_fwd_with_state")
     return out, S, z
@@ -244,10 +287,10 @@ def causal_bwd(q, k, v, dout, dq=None, dk=None, dv=None, workspace=None, stream=
     s = _shape4(q, k, v)
     if dout.shape != v.shape or dout.dtype != v.dtype:
         raise ValueError("dout must match v in shape and dtype")
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    ws, nb = _workspace(OP_CAUSAL_BWD, s, q.device, workspace)
+    dq = _new_like(q, stream) if dq is None else dq
+    dk = _new_like(k, stream) if dk is None else dk
+    dv = _new_like(v, stream) if dv is None else dv
+    ws, nb = _workspace(OP_CAUSAL_BWD, s, q.device, workspace, stream)
     if fwd_workspace is None:
         _check(library().la_causal_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), s,
                                        _ptr(ws), nb, _stream_ptr(stream)), "la_causal_bwd")
@@ -267,10 +310,10 @@ def noncausal_bwd(q, k, v, dout, dq=None, dk=None, dv=None, workspace=None, stre
     s = _shape4(q, k, v)
     if dout.shape != v.shape or dout.dtype != v.dtype:
         raise ValueError("dout must match v in shape and dtype")
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    ws, nb = _workspace(OP_NONCAUSAL_BWD, s, q.device, workspace)
+    dq = _new_like(q, stream) if dq is None else dq
+    dk = _new_like(k, stream) if dk is None else dk
+    dv = _new_like(v, stream) if dv is None else dv
+    ws, nb = _workspace(OP_NONCAUSAL_BWD, s, q.device, workspace, stream)
     _check(library().la_noncausal_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), s,
                                       _ptr(ws), nb, _stream_ptr(stream)), "la_noncausal_bwd")
     return dq, dk, dv
@@ -298,7 +341,7 @@ def causal_step_host(q, k, v, dout, o, dq, dk, dv, group_heads=2, dev_buf=None, 
         raise ValueError("output and gradient shapes must match the inputs")
     need = int(library().la_host_step_bytes(s, group_heads))
     if dev_buf is None:
-        dev_buf = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", torch.cuda.current_device()))
+        dev_buf = _scratch(need, torch.device("cuda", torch.cuda.current_device()), stream)
     nb = dev_buf.numel() * dev_buf.element_size()
     _check(library().la_causal_step_host(_ptr(q), _ptr(k), _ptr(v), _ptr(dout), _ptr(o), _ptr(dq), _ptr(dk), _ptr(dv),
                                          s, group_heads, _ptr(dev_buf), nb, _stream_ptr(stream)),
@@ -316,7 +359,7 @@ def recurrent_step(q, k, v, S, z, out=None, stream=None):
     if S.dtype != torch.float32 or z.dtype != torch.float32 or S.shape != (B, H, Dk, Dv) or z.shape != (B, H, Dk):
         raise ValueError("S must be fp32 [B,H,Dk,Dv] and z fp32 [B,H,Dk]")
     if out is None:
-        out = torch.empty_like(v)
+        out = _new_like(v, stream)
     s = Shape(B, H, 1, Dk, Dv, _dtype_code(q))
     _check(library().la_recurrent_step(_ptr(q), _ptr(k), _ptr(v), _ptr(S), _ptr(z), _ptr(out), s, _stream_ptr(stream)),
            "la_recurrent_step")
@@ -341,12 +384,12 @@ def retention_fwd(q, k, v, gamma, out=None, workspace=None, stream=None, return_
     s = _shape4(q, k, v)
     _gamma(gamma, q.shape[1])
     if out is None:
-        out = torch.empty_like(v)
+        out = _new_like(v, stream)
     S = None
     if return_state:
         B, H, _, Dk = q.shape
-        S = torch.empty(B, H, Dk, v.shape[-1], dtype=torch.float32, device=q.device)
-    ws, nb = _workspace(OP_RETENTION_FWD, s, q.device, workspace)
+        S = _new_f32((B, H, Dk, v.shape[-1]), q.device, stream)
+    ws, nb = _workspace(OP_RETENTION_FWD, s, q.device, workspace, stream)
     _check(library().la_retention_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(gamma), _ptr(out), _ptr(S), s, _ptr(ws), nb,
                                       _stream_ptr(stream)), "la_retention_fwd")
     return (out, S) if return_state else out
@@ -363,7 +406,7 @@ def retention_step(q, k, v, gamma, S, out=None, stream=None):
     if S.dtype != torch.float32 or S.shape != (B, H, Dk, Dv):
         raise ValueError("S must be fp32 [B,H,Dk,Dv]")
     if out is None:
-        out = torch.empty_like(v)
+        out = _new_like(v, stream)
     s = Shape(B, H, 1, Dk, Dv, _dtype_code(q))
     _check(library().la_retention_step(_ptr(q), _ptr(k), _ptr(v), _ptr(gamma), _ptr(S), _ptr(out), s,
                                        _stream_ptr(stream)), "la_retention_step")
@@ -379,10 +422,10 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _result(t, like, what):
+def _result(t, like, what, stream):
     """A caller's output tensor, checked against what it receives; a new one if None."""
     if t is None:
-        return torch.empty_like(like)
+        return _new_like(like, stream)
     _need_cuda(t)
     if t.shape != like.shape or t.dtype != like.dtype:
         raise ValueError("%s must be %s of shape %s" % (what, like.dtype, tuple(like.shape)))
@@ -429,9 +472,9 @@ def gated_delta_fwd(q, k, v, g, beta, S0=None, out=None, workspace=None, stream=
     s = Shape(B, H, N, Dk, Dv, code)
     if S0 is not None:
         _state(S0, (B, H, Dk, Dv), "S0")
-    out = _result(out, v, "out")
-    S = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device) if return_state else None
-    ws, nb = _workspace(OP_GATED_DELTA_FWD, s, q.device, workspace)
+    out = _result(out, v, "out", stream)
+    S = _new_f32((B, H, Dk, Dv), q.device, stream) if return_state else None
+    ws, nb = _workspace(OP_GATED_DELTA_FWD, s, q.device, workspace, stream)
     _check(library().la_gated_delta_fwd(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(S0), _p(out), _p(S), s, _p(ws), nb,
                                         _stream_ptr(stream)), "la_gated_delta_fwd")
     return (out, S) if return_state else out
@@ -452,17 +495,17 @@ def gated_delta_bwd(q, k, v, g, beta, dout, dq=None, dk=None, dv=None, dg=None, 
     if dout.shape != v.shape or dout.dtype != v.dtype:
         raise ValueError("dout must match v in shape and dtype")
     s = Shape(*lead, Dk, Dv, code)
-    dq = _result(dq, q, "dq")
-    dk = _result(dk, k, "dk")
-    dv = _result(dv, v, "dv")
-    dg = _result(dg, g, "dg")
-    dbeta = _result(dbeta, beta, "dbeta")
+    dq = _result(dq, q, "dq", stream)
+    dk = _result(dk, k, "dk", stream)
+    dv = _result(dv, v, "dv", stream)
+    dg = _result(dg, g, "dg", stream)
+    dbeta = _result(dbeta, beta, "dbeta", stream)
     state = (lead[0], lead[1], Dk, Dv)
     for t, what in ((S0, "S0"), (dS, "dS")):
         if t is not None:
             _state(t, state, what)
-    dS0 = torch.empty(state, dtype=torch.float32, device=q.device) if return_dS0 else None
-    ws, nb = _workspace(OP_GATED_DELTA_BWD, s, q.device, workspace)
+    dS0 = _new_f32(state, q.device, stream) if return_dS0 else None
+    ws, nb = _workspace(OP_GATED_DELTA_BWD, s, q.device, workspace, stream)
     _check(library().la_gated_delta_bwd_with_state(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(S0), _p(dout), _p(dS), _p(dq),
                                                    _p(dk), _p(dv), _p(dg), _p(dbeta), _p(dS0), s, _p(ws), nb,
                                                    _stream_ptr(stream)), "la_gated_delta_bwd_with_state")
@@ -477,7 +520,7 @@ def gated_delta_step(q, k, v, g, beta, S, out=None, stream=None):
         raise ValueError("expected q, k [B,H,Dk] and v [B,H,Dv]")
     B, H = lead
     _state(S, (B, H, Dk, Dv), "S")
-    out = _result(out, v, "out")
+    out = _result(out, v, "out", stream)
     _check(library().la_gated_delta_step(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(S), _p(out),
                                          Shape(B, H, 1, Dk, Dv, code), _stream_ptr(stream)), "la_gated_delta_step")
     return out
@@ -508,11 +551,10 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, stream=None, r
     (y, mean, rstd): the fp32 statistics of shape x.shape[:-1] that layer_norm_bwd takes.
     """
     s = _norm_args(x, weight, bias)
-    out = _result(out, x, "out")
+    out = _result(out, x, "out", stream)
     mean = rstd = None
     if return_stats:
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        rstd = torch.empty_like(mean)
+        mean, rstd = (_new_f32(x.shape[:-1], x.device, stream) for _ in range(2))
     _check(library().la_layer_norm_fwd(_p(x), _p(weight), _p(bias), _p(out), _p(mean), _p(rstd), s, eps,
                                        _stream_ptr(stream)), "la_layer_norm_fwd")
     return (out, mean, rstd) if return_stats else out
@@ -534,19 +576,19 @@ def layer_norm_bwd(x, weight, mean, rstd, dout, dx=None, dweight=None, dbias=Non
     stats = x.shape[:-1]
     if mean.dtype != torch.float32 or rstd.dtype != torch.float32 or mean.shape != stats or rstd.shape != stats:
         raise ValueError("mean and rstd must be fp32 of shape x.shape[:-1]")
-    dx = _result(dx, x, "dx")
+    dx = _result(dx, x, "dx", stream)
     lib = library()
     ws, nb = None, 0
     if weight is not None:
-        dweight = _result(dweight, weight, "dweight")
-        dbias = _result(dbias, weight, "dbias")
+        dweight = _result(dweight, weight, "dweight", stream)
+        dbias = _result(dbias, weight, "dbias", stream)
         if workspace is not None:
             if not workspace.is_cuda:
                 raise ValueError("workspace must be a device tensor")
             ws, nb = workspace, workspace.numel() * workspace.element_size()
         else:
             nb = int(lib.la_layer_norm_workspace_bytes(s))
-            ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
+            ws = _scratch(nb, x.device, stream)
     else:
         dweight = dbias = None
     _check(lib.la_layer_norm_bwd(_p(x), _p(weight), _p(mean), _p(rstd), _p(dout), _p(dx), _p(dweight), _p(dbias), s,
@@ -567,8 +609,8 @@ def selftest_lookback_timeout(q, k, v, out=None, workspace=None, stream=None):
     _need_cuda(q, k, v)
     s = _shape4(q, k, v)
     if out is None:
-        out = torch.empty_like(v)
-    ws, nb = _workspace(OP_CAUSAL_FWD, s, q.device, workspace)
+        out = _new_like(v, stream)
+    ws, nb = _workspace(OP_CAUSAL_FWD, s, q.device, workspace, stream)
     _check(library().la_selftest_lookback_timeout(_ptr(q), _ptr(k), _ptr(v), _ptr(out), s, _ptr(ws), nb,
                                                   _stream_ptr(stream)), "la_selftest_lookback_timeout")
     return out

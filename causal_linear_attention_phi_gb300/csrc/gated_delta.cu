@@ -655,11 +655,6 @@ size_t smem_grads(int Dk) {
 }
 static_assert(kW == 16, "the staged state columns of gd_grads are one slice");
 
-template <typename K>
-cudaError_t allow_smem(K kern, size_t bytes) {
-    return cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 #define GD_TRY(x)                              \
     do {                                       \
         const cudaError_t _e = (x);            \
@@ -669,7 +664,7 @@ cudaError_t allow_smem(K kern, size_t bytes) {
 cudaError_t prepare(const void* q, const void* k, const void* g, const void* beta, const Layout& L, char* ws,
                     const la_shape& s, int M, cudaStream_t st) {
     const size_t sm = smem_prepare(s.Dk);
-    GD_TRY(allow_smem(gd_prepare, sm));
+    GD_TRY(allow_smem(gd_prepare, smem_prepare(kMaxHead)));
     launch_begin("gd_prepare", st);
     gd_prepare<<<dim3(M, s.B * s.H), kThreads, sm, st>>>((const float*)q, (const float*)k, (const float*)g,
                                                          (const float*)beta, (float*)(ws + L.rec), (float*)(ws + L.t),
@@ -695,7 +690,7 @@ int slice(const la_shape& s, bool bwd) {
 template <int W, int kR>
 cudaError_t launch_states(const FwdArgs& a, const la_shape& s, const Layout& L, char* ws, int M, cudaStream_t st) {
     const size_t sm = smem_states(s.Dk, W);
-    GD_TRY((allow_smem(gd_states<W, kR>, sm)));
+    GD_TRY((allow_smem(gd_states<W, kR>, smem_states(kMaxHead, W))));
     launch_begin("gd_states", st);
     gd_states<W, kR><<<dim3(s.Dv / W, s.B * s.H), 16 * W / kR, sm, st>>>(
         a, (const float*)(ws + L.rec), (const float*)(ws + L.t), (const float*)(ws + L.P), s.N, M, s.Dk, s.Dv);
@@ -705,7 +700,7 @@ cudaError_t launch_states(const FwdArgs& a, const la_shape& s, const Layout& L, 
 template <int W, int kR>
 cudaError_t launch_sweeps(const BwdArgs& a, const la_shape& s, const Layout& L, char* ws, int M, cudaStream_t st) {
     const size_t sm = smem_states(s.Dk, W);
-    GD_TRY((allow_smem(gd_sweeps<W, kR>, sm)));
+    GD_TRY((allow_smem(gd_sweeps<W, kR>, smem_states(kMaxHead, W))));
     launch_begin("gd_sweeps", st);
     gd_sweeps<W, kR><<<dim3(s.Dv / W, s.B * s.H, 2), 16 * W / kR, sm, st>>>(
         a, (const float*)(ws + L.rec), (const float*)(ws + L.t), (const float*)(ws + L.P), (float*)(ws + L.X),

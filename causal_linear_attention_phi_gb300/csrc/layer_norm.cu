@@ -655,14 +655,15 @@ Tiles tiles_of(long long rows, int C, int elem, int threads, int bytes) {
     t.pitch = (t.row * t.R + (vectors(C, elem) ? 0u : 30u) + 15u) & ~15u;  // up to 15 bytes at either end
     return t;
 }
+constexpr size_t kMostSmem = 225000;  // of a block; the rest of an SM's is left to static arrays
 int resident(size_t smem, int most) {  // blocks of an SM: by shared memory, at most `most` by registers
-    const long long per = 225000 / (long long)(smem + 1536);
+    const long long per = (long long)kMostSmem / (long long)(smem + 1536);
     return (int)(per < 1 ? 1 : per > most ? most : per);
 }
 constexpr int kFwdTile = 16384, kBwdTile = 16384;
 int bwd_tile(int C, int elem) { return !vectors(C, elem) && C <= 256 ? kBwdTile / 2 : kBwdTile; }  // four blocks to an SM
 int bwd_stages(const Tiles& t) {
-    const long long fit = 225000 / (2LL * t.pitch);
+    const long long fit = (long long)kMostSmem / (2LL * t.pitch);
     return (int)(fit < kBwdStages ? fit : kBwdStages);
 }
 
@@ -679,7 +680,7 @@ int bwd_blocks(const la_norm_shape& s) {
 namespace {
 template <typename K, typename... A>
 cudaError_t launch_tiles(const char* name, K kern, long long blocks, int block, size_t smem, cudaStream_t st, A... args) {
-    cudaError_t e = cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(kern, kMostSmem);
     if (e != cudaSuccess) return e;
     launch_begin(name, st);
     e = launch_pdl(kern, dim3((unsigned)blocks), dim3(block), smem, st, args...);

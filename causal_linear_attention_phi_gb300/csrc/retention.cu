@@ -466,8 +466,7 @@ cudaError_t retention_segment_sums(const void* k, const void* v, const float* ga
     auto run = [&](auto tag) {
         using T = decltype(tag);
         auto kern = retention_sums_kernel<T>;
-        if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
-            return;
+        if ((err = allow_smem(kern, smem_bytes_sums(kMaxHead, kMaxHead))) != cudaSuccess) return;
         launch_begin("retention_segment_sums", st);
         kern<<<grid, kThreads, smem, st>>>((const T*)k, (const T*)v, gamma, seg, s.H, s.N, s.Dk, s.Dv, p.nchunks,
                                            p.cps, p.P);
@@ -499,8 +498,7 @@ cudaError_t retention_out(const void* q, const void* k, const void* v, const flo
     auto run = [&](auto tag) {
         using T = decltype(tag);
         auto kern = retention_out_kernel<T>;
-        if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
-            return;
+        if ((err = allow_smem(kern, smem_bytes_out(kMaxHead, kMaxHead))) != cudaSuccess) return;
         launch_begin("retention_out", st);
         kern<<<grid, kThreads, smem, st>>>((const T*)q, (const T*)k, (const T*)v, gamma, (T*)o, seg, s.H, s.N, s.Dk,
                                            s.Dv, p.nchunks, p.cps, p.P);

@@ -709,12 +709,6 @@ size_t smem_bytes_bwd(int Dk, int Dv) {
            r((size_t)Dk * (Dv + 1)) + r(Dk) + r(kC) * 2;
 }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-    // Opt in to large dynamic shared memory (the attribute is per kernel and idempotent).
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 }  // namespace
 
 #define LA_DISPATCH_DTYPE(dt, T, ...)                 \
@@ -735,7 +729,7 @@ cudaError_t simt_segment_sums(const void* k, const void* v, float* seg, const la
     cudaError_t err = cudaSuccess;
     LA_DISPATCH_DTYPE(s.dtype, T, {
         auto kern = segment_sums_kernel<T>;
-        if ((err = allow_smem(kern, smem)) != cudaSuccess) return err;
+        if ((err = allow_smem(kern, smem_bytes_sums(kMaxHead, kMaxHead))) != cudaSuccess) return err;
         launch_begin("simt_segment_sums", st);
         kern<<<grid, kThreads, smem, st>>>((const T*)k, (const T*)v, seg, s.N, s.Dk, s.Dv, p.nchunks, p.cps, p.P);
         err = launch_end("simt_segment_sums", st);
@@ -783,7 +777,7 @@ cudaError_t simt_causal_fwd_out(const void* q, const void* k, const void* v, voi
     cudaError_t err = cudaSuccess;
     LA_DISPATCH_DTYPE(s.dtype, T, {
         auto kern = causal_fwd_out_kernel<T>;
-        if ((err = allow_smem(kern, smem)) != cudaSuccess) return err;
+        if ((err = allow_smem(kern, smem_floats_fwd(kMaxHead, kMaxHead))) != cudaSuccess) return err;
         launch_begin("simt_causal_fwd_out", st);
         kern<<<grid, kThreads, smem, st>>>((const T*)q, (const T*)k, (const T*)v, (T*)o, seg, s.N, s.Dk, s.Dv,
                                            p.nchunks, p.cps, p.P);
@@ -798,7 +792,7 @@ cudaError_t simt_noncausal_apply(const void* q, void* o, const float* totals, co
     cudaError_t err = cudaSuccess;
     LA_DISPATCH_DTYPE(s.dtype, T, {
         auto kern = noncausal_apply_kernel<T>;
-        if ((err = allow_smem(kern, smem)) != cudaSuccess) return err;
+        if ((err = allow_smem(kern, smem_bytes_apply(kMaxHead, kMaxHead))) != cudaSuccess) return err;
         launch_begin("simt_noncausal_apply", st);
         kern<<<grid, kThreads, smem, st>>>((const T*)q, (T*)o, totals, s.N, s.Dk, s.Dv);
         err = launch_end("simt_noncausal_apply", st);
@@ -814,7 +808,7 @@ cudaError_t simt_bwd_forward_sweep(const void* q, const void* k, const void* v, 
     cudaError_t err = cudaSuccess;
     LA_DISPATCH_DTYPE(s.dtype, T, {
         auto kern = causal ? bwd_forward_sweep_kernel<T, true> : bwd_forward_sweep_kernel<T, false>;
-        if ((err = allow_smem(kern, smem)) != cudaSuccess) return err;
+        if ((err = allow_smem(kern, smem_bytes_bwd(kMaxHead, kMaxHead))) != cudaSuccess) return err;
         launch_begin(causal ? "simt_bwd_forward_sweep" : "simt_noncausal_bwd_query", st);
         kern<<<grid, kThreads, smem, st>>>((const T*)q, (const T*)k, (const T*)v, (const T*)dout, (T*)dq, seg_S,
                                            seg_R, den_g, s.N, s.Dk, s.Dv, p.nchunks, p.cps, p.P);
@@ -831,7 +825,7 @@ cudaError_t simt_bwd_reverse_sweep(const void* q, const void* k, const void* v, 
     cudaError_t err = cudaSuccess;
     LA_DISPATCH_DTYPE(s.dtype, T, {
         auto kern = causal ? bwd_reverse_sweep_kernel<T, true> : bwd_reverse_sweep_kernel<T, false>;
-        if ((err = allow_smem(kern, smem)) != cudaSuccess) return err;
+        if ((err = allow_smem(kern, smem_bytes_bwd(kMaxHead, kMaxHead) + 256)) != cudaSuccess) return err;
         launch_begin(causal ? "simt_bwd_reverse_sweep" : "simt_noncausal_bwd_key", st);
         kern<<<grid, kThreads, smem, st>>>((const T*)q, (const T*)k, (const T*)v, (const T*)dout, (T*)dk, (T*)dv,
                                            seg_R, den_g, s.N, s.Dk, s.Dv, p.nchunks, p.cps, p.P);

@@ -186,10 +186,6 @@ __device__ __forceinline__ void col_put2(uint32_t col, int x, float a, float b) 
     col_put(col, x + 1, (uint16_t)(w >> 16));
 }
 
-template <typename K>
-cudaError_t allow_smem(K kern, size_t bytes) {
-    return cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
 #define GD_TRY(x)                         \
     do {                                  \
         const cudaError_t _e = (x);       \

@@ -115,12 +115,6 @@ __device__ __forceinline__ void group_sum(float (&x)[NV], float (*buf)[W8], int 
     }
 }
 
-// After a wait that ran out: wait once more, with the same limit, for the copies in flight (none is left behind).
-__device__ __noinline__ void drain(uint64_t* bar, int stages, long long issued, int* err) {
-    for (long long i = issued > stages ? issued - stages : 0; i < issued; ++i)
-        sm100::mbar_wait(bar + i % stages, (int)(i / stages) & 1, err, LA_ERR_TIMEOUT);
-}
-
 struct Tiles {
     long long rows, tiles;
     int C, R;       // R rows to a tile
@@ -218,7 +212,7 @@ ln_fwd_tiles(const T* x, const T* __restrict__ w, const T* __restrict__ b, T* y,
         __syncthreads();  // the tile has been read
         load(i + kFwdStages);
     }
-    if (!ok) drain(bar, kFwdStages, issued, err);
+    if (!ok) sm100::mbar_drain(bar, kFwdStages, issued, err, LA_ERR_TIMEOUT);
 }
 
 // The gradient: x and dy tiles; a thread keeps dw and db of its columns (VPT vectors) and, up to 16 elements, w.
@@ -337,7 +331,7 @@ ln_bwd_tiles(const T* x, const T* __restrict__ w, const float* __restrict__ mean
         load(i + stages);
         if (++s == stages) s = 0, phase ^= 1;
     }
-    if (!ok) drain(bar, stages, issued, err);
+    if (!ok) sm100::mbar_drain(bar, stages, issued, err, LA_ERR_TIMEOUT);
     if (!part) return;
     // the rows of a block joined in shared memory (the tiles are done with), then one record per block
     float* sums = reinterpret_cast<float*>(smem);
@@ -482,7 +476,7 @@ ln_fwd_elements(const T* x, const T* __restrict__ w, const T* __restrict__ b, T*
         load(i + kFwdStages, s);
         if (++s == kFwdStages) s = 0, phase ^= 1;
     }
-    if (!ok) drain(bar, kFwdStages, issued, err);
+    if (!ok) sm100::mbar_drain(bar, kFwdStages, issued, err, LA_ERR_TIMEOUT);
 }
 
 template <typename T, int VPT, int TPR>
@@ -571,7 +565,7 @@ ln_bwd_elements(const T* x, const T* __restrict__ w, const float* __restrict__ m
         load(i + stages, s);
         if (++s == stages) s = 0, phase ^= 1;
     }
-    if (!ok) drain(bar, stages, issued, err);
+    if (!ok) sm100::mbar_drain(bar, stages, issued, err, LA_ERR_TIMEOUT);
     if (!part) return;
     float* sums = reinterpret_cast<float*>(smem);
     float* p = part + (size_t)blockIdx.x * 2 * C;

@@ -275,8 +275,11 @@ __device__ __forceinline__ void join_block(const float* __restrict__ B, const fl
     pdl_enter();  // launched with programmatic dependent launch
     // the i-th map applied: segment i, or from the last one back
     auto seg = [&](int i) { return bh * P + (kReverse ? P - 1 - i : i); };
+    bool ok = true;
+    int issued = 0;
     auto load = [&](int i) {
-        if (tid != 0) return;
+        if (tid != 0 || !ok) return;
+        issued = i + 1;
         mbar_arrive_expect_tx(bar + (i & 1), D * D * 4);
         bulk_load(smem + (i & 1) * L::map, Mx + seg(i) * rec, D * D * 4, bar + (i & 1));
     };
@@ -294,7 +297,6 @@ __device__ __forceinline__ void join_block(const float* __restrict__ B, const fl
                        : make_float4(0.f, 0.f, 0.f, 0.f);
         load_b(0);
     }
-    bool ok = true;
     for (int i = 0; i < P; ++i) {
         F4 acc[2];
 #pragma unroll
@@ -364,6 +366,7 @@ __device__ __forceinline__ void join_block(const float* __restrict__ B, const fl
         }
         if (L::split == 1) __syncthreads();  // S and the map have been read
     }
+    if (!ok) mbar_drain(bar, 2, issued, err, LA_ERR_TIMEOUT);
 }
 
 // The third grid dimension: 0 forwards, 1 in reverse (the gradient's).

@@ -308,13 +308,14 @@ states_block(const float* __restrict__ q, const float* __restrict__ k, const flo
 }
 
 // ------------------------------------------------------------------ the adjoint recurrence, last chunk first
-// As above: K in two buffers, Q copied under the products before its own, t and P under the state's.
+// As above: K in two buffers, Q copied under the products before its own, t and P under the state's.  dS0 may be dS: a block
+// reads its slice before it writes it.
 template <int W, int kR>
 __device__ __forceinline__ void
 reverse_block(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ dout,
            const float* __restrict__ recs, const float* __restrict__ ts, const float* __restrict__ Ps,
-           float* __restrict__ dv, float* __restrict__ Ys, float* __restrict__ dSs, const float* __restrict__ dS,
-           float* __restrict__ dS0, int N, int M, int Dk, int Dv) {
+           float* __restrict__ dv, float* __restrict__ Ys, float* __restrict__ dSs, const float* dS, float* dS0, int N,
+           int M, int Dk, int Dv) {
     constexpr int kLw = W + 4, kG = kC / kR, kThr = kG * W / 4;
     extern __shared__ __align__(16) float smem[];
     Carve sm{smem};

@@ -45,3 +45,12 @@ def test_the_rule_sees_every_file_that_copies():
     copying = {n for n in FILES if re.search(r"\bmbar_arrive_expect_tx\(", code(text(n)))} - {"sm100.cuh"}
     seen = {n for n in copying if any(LEAVES_NONE.search(code(p)) for p in functions(text(n)))}
     assert copying == seen and len(copying) >= 8
+
+
+def test_states_that_may_be_one_buffer_are_not_restrict():
+    """la.h lets S be S0, dS0 be dS, y be x and dx be dy or x."""
+    for name, params in (("gated_delta.cu", r"(const float|float)\* __restrict__ (S0|S_out|dS0)\b|const float\* __restrict__ dS\b"),
+                         ("tc_gated_delta_states.cuh", r"__restrict__ (S0|S_out)\b"),
+                         ("tc_gated_delta_bwd.cu", r"__restrict__ (segdS|dS0|S0)\b"),
+                         ("layer_norm.cu", r"__restrict__ (x|y|dx|dy)\b")):
+        assert not re.search(params, code(text(name))), name

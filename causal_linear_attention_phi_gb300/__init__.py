@@ -568,7 +568,8 @@ def layer_norm_workspace_bytes(rows: int, C: int, dtype: torch.dtype) -> int:
 
 def layer_norm_bwd(x, weight, mean, rstd, dout, dx=None, dweight=None, dbias=None, workspace=None, stream=None):
     """Gradients (dx, dweight, dbias) of layer_norm_fwd for upstream gradient dout, from its
-    statistics.  With weight None there is no weight or bias: dweight and dbias are None."""
+    statistics.  With weight None (1), dweight and dbias are formed where the caller gives the
+    tensor that receives them ([C] of x's dtype; dbias for a norm with a bias alone), else None."""
     s = _norm_args(x, weight)
     _need_cuda(mean, rstd, dout)
     if dout.shape != x.shape or dout.dtype != x.dtype:
@@ -582,6 +583,14 @@ def layer_norm_bwd(x, weight, mean, rstd, dout, dx=None, dweight=None, dbias=Non
     if weight is not None:
         dweight = _result(dweight, weight, "dweight", stream)
         dbias = _result(dbias, weight, "dbias", stream)
+    else:
+        for t, what in ((dweight, "dweight"), (dbias, "dbias")):
+            if t is None:
+                continue
+            _need_cuda(t)
+            if t.shape != x.shape[-1:] or t.dtype != x.dtype:
+                raise ValueError("%s must be %s of shape %s" % (what, x.dtype, tuple(x.shape[-1:])))
+    if dweight is not None or dbias is not None:
         if workspace is not None:
             if not workspace.is_cuda:
                 raise ValueError("workspace must be a device tensor")
@@ -589,8 +598,6 @@ def layer_norm_bwd(x, weight, mean, rstd, dout, dx=None, dweight=None, dbias=Non
         else:
             nb = int(lib.la_layer_norm_workspace_bytes(s))
             ws = _scratch(nb, x.device, stream)
-    else:
-        dweight = dbias = None
     _check(lib.la_layer_norm_bwd(_p(x), _p(weight), _p(mean), _p(rstd), _p(dout), _p(dx), _p(dweight), _p(dbias), s,
                                  _p(ws), nb, _stream_ptr(stream)), "la_layer_norm_bwd")
     return dx, dweight, dbias

@@ -805,12 +805,12 @@ la_status la_last_error(void) {
     if (v == LA_ERR_BOUNDS) {
         unsigned site = 0;
         if (cudaMemcpyFromSymbol(&site, g_debug_site, sizeof(site)) == cudaSuccess) {
-            static const char* const kFiles[] = {"api.cu", "decode.cu", "gated_delta.cu", "gated_delta_step.cu",
-                                                 "gated_delta.cuh", "host_step.cu", "layer_norm.cu", "noalloc.cu",
-                                                 "retention.cu",
-                                                 "selftest.cu", "simt_kernels.cu", "tc_gated_delta.cu", "tc_gated_delta_bwd.cu", "tc_gated_delta.cuh", "tc_apply.cu", "tc_bwd.cu",
-                                                 "tc_fwd.cu", "tc_noncausal_bwd.cu", "tc_retention.cu",
-                                                 "la_internal.cuh", "simt_common.cuh", "tc_common.cuh", "sm100.cuh"};
+            static const char* const kFiles[] = {
+                "api.cu", "decode.cu", "gated_delta.cu", "gated_delta.cuh", "gated_delta_step.cu", "host_step.cu",
+                "la_internal.cuh", "layer_norm.cu", "layer_norm.cuh", "noalloc.cu", "retention.cu", "selftest.cu",
+                "simt_common.cuh", "simt_kernels.cu", "sm100.cuh", "tc_apply.cu", "tc_bwd.cu", "tc_common.cuh",
+                "tc_fwd.cu", "tc_gated_delta.cu", "tc_gated_delta.cuh", "tc_gated_delta_bwd.cu",
+                "tc_gated_delta_states.cuh", "tc_noncausal_bwd.cu", "tc_retention.cu"};
             const char* file = "unknown file";
             for (const char* f : kFiles)
                 if (dbg::file_tag(f) == (site >> 16)) file = f;

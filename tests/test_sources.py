@@ -54,3 +54,18 @@ def test_states_that_may_be_one_buffer_are_not_restrict():
                          ("tc_gated_delta_bwd.cu", r"__restrict__ (segdS|dS0|S0)\b"),
                          ("layer_norm.cu", r"__restrict__ (x|y|dx|dy)\b")):
         assert not re.search(params, code(text(name))), name
+
+
+def file_tag(name):
+    """dbg::file_tag in la_internal.cuh: FNV-1a of the base name, folded to 16 bits."""
+    h = 2166136261
+    for c in name.encode():
+        h = (h ^ c) * 16777619 & 0xFFFFFFFF
+    return (h ^ h >> 16) & 0xFFFF
+
+
+def test_a_failed_index_check_names_its_file():
+    """The debug build reports a check's site by a tag of its file: every source is in the list that names it, no two alike."""
+    listed = re.search(r"kFiles\[\] = \{(.*?)\}", text("api.cu"), re.S).group(1)
+    assert sorted(re.findall(r'"([^"]+)"', listed)) == FILES
+    assert len({file_tag(n) for n in FILES}) == len(FILES)

@@ -286,7 +286,7 @@ states_block(const float* __restrict__ q, const float* __restrict__ k, const flo
 #pragma unroll
             for (int j = 0; j < kR; ++j) {
                 const int r = rg + kG * j;
-                if (r < n) put4(o + (bh * N + c0 + r) * (size_t)Dv + col, w[j]);
+                if (r < n && LA_DCHECK(c0 + r < N)) put4(o + (bh * N + c0 + r) * (size_t)Dv + col, w[j]);
             }
             __syncthreads();  // the old slice, Q and P have been read
         }
@@ -386,7 +386,7 @@ reverse_block(const float* __restrict__ q, const float* __restrict__ k, const fl
         for (int j = 0; j < kR; ++j) {
             const int r = kR * rg + j;
             put4(Ys + (at * kC + r) * Dv + col, y[j]);
-            if (r < n) put4(dv + (bh * N + c0 + r) * (size_t)Dv + col, y[j], rec[kBeta + r]);
+            if (r < n && LA_DCHECK(c0 + r < N)) put4(dv + (bh * N + c0 + r) * (size_t)Dv + col, y[j], rec[kBeta + r]);
             put4(Ub + r * kLw + c, y[j], rec[kBg + r]);
             put4(Db + r * kLw + c, get4(Db + r * kLw + c), rec[kGam + r]);
         }
@@ -602,7 +602,7 @@ gd_grads(const float* __restrict__ q, const float* __restrict__ k, const float* 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = ty + 16 * i;
-        if (r >= n) continue;
+        if (r >= n || !LA_DCHECK(c0 + r < N)) continue;
 #pragma unroll
         for (int j = 0; j < NK; ++j) {
             dq[(bh * N + c0 + r) * (size_t)Dk + tx + 16 * j] = qi[i][j];

@@ -65,6 +65,7 @@ gd_step_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __rest
     const int h = blockIdx.x * C::kHeads + sub;
     if (h >= BH) return;  // a whole warp (kHeads > 1 only where a head is one warp)
     const int col = t % C::kCols * 4, grp = t / C::kCols;
+    LA_DCHECK(col + 3 < DV && grp + C::kGroups * (C::kRows - 1) < DK && sub < C::kHeads);
     float* Sh = S + (size_t)h * (DK * DV);
     float4 s[C::kRows];
 #pragma unroll

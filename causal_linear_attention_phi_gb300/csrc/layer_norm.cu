@@ -149,6 +149,7 @@ ln_fwd_tiles(const T* x, const T* __restrict__ w, const T* __restrict__ b, T* y,
         issued = i + 1;
         const int s = (int)(i % kFwdStages);
         const uint32_t bytes = rows_of(k) * tl.row;
+        LA_DCHECK(bytes <= tile && k * tl.R + rows_of(k) <= tl.rows);
         sm100::mbar_arrive_expect_tx(bar + s, bytes);
         bulk_load(smem + s * tile, reinterpret_cast<const uint8_t*>(x) + k * tile, bytes, bar + s);
     };
@@ -189,6 +190,7 @@ ln_fwd_tiles(const T* x, const T* __restrict__ w, const T* __restrict__ b, T* y,
             group_sum<TPR, 1>(a, buf[sub], sub, t, turn);
             const float rs = 1.f / sqrtf(fmaf(a[0], inv, eps));
             const long long row = k * tl.R + r;
+            if (in && !LA_DCHECK(row < tl.rows)) continue;
             if (in && t == 0) {
                 if (mean) mean[row] = mu;
                 if (rstd) rstd[row] = rs;
@@ -244,6 +246,7 @@ ln_bwd_tiles(const T* x, const T* __restrict__ w, const float* __restrict__ mean
         issued = i + 1;
         const int s = (int)(i % stages);
         const uint32_t bytes = rows_of(k) * tl.row;
+        LA_DCHECK(bytes <= tile && k * tl.R + rows_of(k) <= tl.rows);
         sm100::mbar_arrive_expect_tx(bar + s, 2 * bytes);
         bulk_load(smem + 2 * s * tile, reinterpret_cast<const uint8_t*>(x) + k * tile, bytes, bar + s);
         bulk_load(smem + (2 * s + 1) * tile, reinterpret_cast<const uint8_t*>(dy) + k * tile, bytes, bar + s);
@@ -286,6 +289,7 @@ ln_bwd_tiles(const T* x, const T* __restrict__ w, const float* __restrict__ mean
                 stats(k + gridDim.x, sub);
             if (TPR > 32 && !in) break;
             const long long row = k * tl.R + (in ? r : 0);
+            LA_DCHECK(row < tl.rows);
             const uint8_t* xr = smem + 2 * s * tile + (in ? r : 0) * tl.row;
             const uint8_t* dr = xr + tile;
             float2 s0 = both(0.f), s1 = s0;
@@ -379,6 +383,12 @@ struct Spans {
         if ((long long)threadIdx.x < left)
             reinterpret_cast<T*>(tile + bytes(k))[threadIdx.x] = x[at / (long long)sizeof(T) + threadIdx.x];
     }
+    // the copy stays in the rows and in the tile, and leaves out less than a vector
+    __device__ bool inside(long long k) const {
+        const long long from = start(k) - lead(k), end = start(k) + (long long)rows(k) * tl.row;
+        return from >= 0 && from + bytes(k) <= total && bytes(k) <= tl.pitch && end - from <= tl.pitch &&
+               (end <= from + bytes(k) || end - from - bytes(k) < 16);
+    }
     __device__ bool whole(long long k) const { return start(k) + (long long)rows(k) * tl.row <= (total & ~15LL); }
 };
 
@@ -405,6 +415,7 @@ ln_fwd_elements(const T* x, const T* __restrict__ w, const T* __restrict__ b, T*
         const long long k = blockIdx.x + i * gridDim.x;
         if (tid != 0 || k >= tl.tiles || !ok) return;
         issued = i + 1;
+        LA_DCHECK(sp.inside(k));
         sm100::mbar_arrive_expect_tx(bar + s, sp.bytes(k));
         if (sp.bytes(k))
             bulk_load(smem + s * tl.pitch, reinterpret_cast<const uint8_t*>(x) + sp.start(k) - sp.lead(k), sp.bytes(k), bar + s);
@@ -455,6 +466,7 @@ ln_fwd_elements(const T* x, const T* __restrict__ w, const T* __restrict__ b, T*
             group_sum<TPR, 1>(a, buf[sub], sub, t, turn);
             const float rs = 1.f / sqrtf(fmaf(a[0], inv, eps));
             const long long row = k * tl.R + r;
+            if (in && !LA_DCHECK(row < tl.rows)) continue;
             if (in && t == 0) {
                 if (mean) mean[row] = mu;
                 if (rstd) rstd[row] = rs;
@@ -504,6 +516,7 @@ ln_bwd_elements(const T* x, const T* __restrict__ w, const float* __restrict__ m
         issued = i + 1;
         const long long from = sp.start(k) - sp.lead(k);
         const uint32_t bytes = sp.bytes(k);
+        LA_DCHECK(sp.inside(k));
         sm100::mbar_arrive_expect_tx(bar + s, 2 * bytes);
         if (!bytes) return;
         bulk_load(smem + 2 * s * tl.pitch, reinterpret_cast<const uint8_t*>(x) + from, bytes, bar + s);
@@ -536,6 +549,7 @@ ln_bwd_elements(const T* x, const T* __restrict__ w, const float* __restrict__ m
             const bool in = r < n;
             if (TPR > 32 && !in) break;
             const long long row = k * tl.R + (in ? r : 0);
+            LA_DCHECK(row < tl.rows);
             const T *xr = xs + (in ? r : 0) * C, *gr = gs + (in ? r : 0) * C;
             const float mu = mean[row], rs = rstd[row];
             float a[2] = {0.f, 0.f};
@@ -605,7 +619,7 @@ ln_join_kernel(const float* __restrict__ part, T* __restrict__ dw, T* __restrict
     if (tx == 0 && col < 2 * C) {
         if (col < C) {
             if (dw) dw[col] = from_f32<T>(v);
-        } else if (db) {
+        } else if (db && LA_DCHECK(col - C < C)) {
             db[col - C] = from_f32<T>(v);
         }
     }

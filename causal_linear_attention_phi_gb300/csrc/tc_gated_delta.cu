@@ -266,6 +266,7 @@ __device__ __forceinline__ void join_block(const float* __restrict__ B, const fl
     const int row = 2 * (id / (kCols / 4)), c0 = 4 * (id % (kCols / 4)), col = blockIdx.x * kCols + c0;
     float4* half = reinterpret_cast<float4*>(smem + L::half) + id;
     const size_t bh = blockIdx.y, rec = (size_t)D * D;
+    LA_DCHECK(col + 3 < D && row + 1 < D && part < L::split);
     if (tid == 0) {
         mbar_init(bar, 1);
         mbar_init(bar + 1, 1);

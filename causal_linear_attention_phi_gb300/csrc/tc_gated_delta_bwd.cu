@@ -226,6 +226,7 @@ __device__ __forceinline__ void reverse_block(const CUtensorMap& tm_q, const CUt
         for (int i = 0; i < nloc; ++i) {
             const int s = i & 1, ph = i & 1, c = cend - 1 - i;
             const size_t at = (size_t)bh * M + c;
+            LA_DCHECK(c >= 0 && c < M && bh < (int)gridDim.y);
             uint8_t* sg = base + s * L::stage;
             const float* gates = reinterpret_cast<const float*>(sg + L::gates);
             auto gate = [&](int which, int x) { return get4(gates + which + kTok * h + x); };
@@ -616,6 +617,7 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const int ph = i & 1;
             const size_t at = (size_t)blockIdx.x + (size_t)gridDim.x * i;
             const int bh = (int)(at / M), c0 = (int)(at % M) * kC, n = min(kC, N - c0);
+            LA_DCHECK(at < (size_t)total && n >= 1);
             wait(&bar->a_full, ph);
             float kept = 0.f;  // <dS', S>
 #pragma unroll
@@ -794,7 +796,7 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int j = 2 * lane + e;
-                    if (j >= n) continue;
+                    if (j >= n || !LA_DCHECK(c0 + j < N)) continue;
                     const size_t pos = (size_t)bh * N + c0 + j;
                     // a reset is where the count of resets goes up
                     const bool reset = rec[kSeg + j] != (j > 0 ? rec[kSeg + j - 1] : 0.f);

@@ -233,7 +233,7 @@ __device__ __forceinline__ void states_block(const CUtensorMap& tm_q, const CUte
             auto put = [&](int stride) {
 #pragma unroll
                 for (int x = 0; x < kTok; ++x)
-                    if (x < n) o[x * stride] = __float2bfloat16_rn(__uint_as_float(w[x]) + __uint_as_float(w2[x]));
+                    if (x < n && LA_DCHECK(t0 + x < a.N)) o[x * stride] = __float2bfloat16_rn(__uint_as_float(w[x]) + __uint_as_float(w2[x]));
             };
             if (a.Dv == D) {
                 if (r < D) put(D);  // a constant, for immediate offsets
@@ -329,6 +329,7 @@ __device__ __forceinline__ void states_block(const CUtensorMap& tm_q, const CUte
                 named_barrier(1, 32 * kWarps);
                 if (ct == 0) {
                     const size_t at = (size_t)bh * M + cbeg + i;
+                    LA_DCHECK(cbeg + i < M && bh < (int)gridDim.y);
                     bulk_store(a.s_tiles + at * L::sbytes, base + L::out, L::sbytes);
                     bulk_store(a.x_tiles + at * L::xbytes, base + L::out + L::sbytes, L::xbytes);
                     bulk_commit();
@@ -386,6 +387,7 @@ __device__ __forceinline__ void states_block(const CUtensorMap& tm_q, const CUte
         if (kMode == kOut) output(nloc - 1);
         if (ct == 0) bulk_wait_all();
         if (kMode == kSum) {
+            LA_DCHECK(p < a.P && bh < (int)gridDim.y);
             const size_t at = ((size_t)bh * a.P + p) * (D * D);
             const int c = r & (D - 1);
 #pragma unroll
@@ -400,7 +402,7 @@ __device__ __forceinline__ void states_block(const CUtensorMap& tm_q, const CUte
 #pragma unroll
             for (int x = 0; x < kSc; ++x) {
                 const int c = kSc * h + x;
-                if (c < a.Dk) a.S_out[((size_t)bh * a.Dk + c) * a.Dv + r] = x & 1 ? S[x / 2].y : S[x / 2].x;
+                if (c < a.Dk && LA_DCHECK(bh < (int)gridDim.y)) a.S_out[((size_t)bh * a.Dk + c) * a.Dv + r] = x & 1 ? S[x / 2].y : S[x / 2].x;
             }
         }
         tc_fence_before();

@@ -203,6 +203,8 @@ def _new_like(t, stream):
 
 
 def _new_f32(shape, device, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=torch.float32, device=device)
     return _handed_out(lambda: torch.empty(shape, dtype=torch.float32, device=device), stream)
 
 
@@ -554,7 +556,8 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, stream=None, r
     out = _result(out, x, "out", stream)
     mean = rstd = None
     if return_stats:
-        mean, rstd = (_new_f32(x.shape[:-1], x.device, stream) for _ in range(2))
+        mean = _new_f32(x.shape[:-1], x.device, stream)
+        rstd = _new_like(mean, stream)
     _check(library().la_layer_norm_fwd(_p(x), _p(weight), _p(bias), _p(out), _p(mean), _p(rstd), s, eps,
                                        _stream_ptr(stream)), "la_layer_norm_fwd")
     return (out, mean, rstd) if return_stats else out

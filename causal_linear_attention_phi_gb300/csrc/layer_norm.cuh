@@ -6,7 +6,8 @@
 namespace la {
 namespace ln {
 
-constexpr int kMaxC = 16384;  // a row is held in the registers of at most 1024 threads, 16 elements each
+// Rows lie in shared memory, worked on by at most 512 threads; the gradient's keep dw and db of at most 32 columns each.
+constexpr int kMaxC = 16384;
 
 // Blocks of the gradient kernel, i.e. partial (dw, db) records of 2 C floats in the workspace.
 int bwd_blocks(const la_norm_shape& s);

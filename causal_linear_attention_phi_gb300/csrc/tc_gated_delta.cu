@@ -51,7 +51,8 @@ static_assert(PrepSmem::P >= kC * kLd * 4 && PrepSmem::rec >= 4 * kBlk, "regions
 constexpr size_t kPrepBytes = PrepSmem::total;  // no slack for alignment: it would cost the sixth block
 static_assert(6 * (kPrepBytes + 1024) <= 233472, "six blocks to an SM");
 
-// w[x] (columns j0 .. j0 + 31 of row i) times the decay from j to i, 0 outside j <= last (kFull: all inside).
+// w[x] (columns j0 .. j0 + 31 of row i) times the decay from j to i, 0 outside j <= last (kFull: all inside).  The decays are
+// ex2.approx (2^-22 relative) of differences in hi + lo: what they scale enters the products as two bf16 parts (2^-17).
 template <bool kResets, bool kFull>
 __device__ __forceinline__ void decay32(uint32_t (&w)[32], const float* rec, int i, int j0, int last) {
     const float seg = rec[kSeg + i];

@@ -8,7 +8,10 @@
 //   dS^T = gam_C dS'^T + (gam dO)^T Q - (beta gam Y)^T K
 // What is formed here enters the products as hi + lo bf16 parts, as in the forward kernel.  It writes dV and,
 // for tc_gd_grads, the tiles of Y^T [Dv rows x 64 positions], lo and hi, and of dS'^T [Dv rows x Dk], rounded to bf16
-// once like S (a relative error of 2^-9 of each term of the products with the states, none of which cancel by much).
+// once like S: a relative error of 2^-9 of each term of the products with the states (S Y^T takes Y's hi part alone, for the
+// same size of error).  In dq and dk these terms cancel by little.  dg is what they leave when they cancel: off by 5e-3 of its
+// largest for independent keys, more as keys coincide (0.4 with all keys within 0.05 of one direction, beta = 1 and no
+// decay; the fp32 path 2e-4).  A second part of S and dS' would add 64 KB to a chunk's tiles, for which shared memory has no room.
 //
 // tc_gd_grads (persistent blocks, a chunk at a time): with G = Y X^T, F^T = X dO^T, all products with 128 rows,
 //   F_ij = (dO_i . X_j) beta_j Gam_ij (i >= j),  E_ij = -beta_i beta_j Gam_ij G_ij (i > j),  dbeta_i = G_ii
@@ -766,7 +769,7 @@ tc_gd_grads(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 }
                 bulk_commit();
             }
-            if (warp == 3) {  // dg: the reverse cumulative sum, two positions to a lane (fp32: the result is bf16)
+            if (warp == 3) {  // dg: the reverse cumulative sum, two positions to a lane (fp32: the terms carry bf16 roundings)
                 float v[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {

@@ -808,8 +808,8 @@ la_status la_last_error(void) {
             static const char* const kFiles[] = {
                 "api.cu", "decode.cu", "gated_delta.cu", "gated_delta.cuh", "gated_delta_step.cu", "host_step.cu",
                 "la_internal.cuh", "layer_norm.cu", "layer_norm.cuh", "noalloc.cu", "retention.cu", "selftest.cu",
-                "simt_common.cuh", "simt_kernels.cu", "sm100.cuh", "tc_apply.cu", "tc_bwd.cu", "tc_common.cuh",
-                "tc_fwd.cu", "tc_gated_delta.cu", "tc_gated_delta.cuh", "tc_gated_delta_bwd.cu",
+                "shared_memory.cuh", "simt_common.cuh", "simt_kernels.cu", "sm100.cuh", "tc_apply.cu", "tc_bwd.cu",
+                "tc_common.cuh", "tc_fwd.cu", "tc_gated_delta.cu", "tc_gated_delta.cuh", "tc_gated_delta_bwd.cu",
                 "tc_gated_delta_states.cuh", "tc_noncausal_bwd.cu", "tc_retention.cu"};
             const char* file = "unknown file";
             for (const char* f : kFiles)

@@ -8,7 +8,7 @@
 // Bound by what shared memory returns to registers and, where there are few heads, by the chain of a chunk's products:
 // B=2 H=32 N=2048 128 x 128 takes 0.71 ms forward (its operations 0.30 ms at 128 multiply-adds a clock and SM).
 #include "gated_delta.cuh"
-#include "sm100.cuh"
+#include "shared_memory.cuh"
 
 namespace la {
 namespace gd {

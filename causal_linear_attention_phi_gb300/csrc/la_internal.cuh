@@ -139,15 +139,6 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
     return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
 }
 
-// Opts a kernel in to `most` bytes of dynamic shared memory: the most that any of its calls takes, not this call's.  The
-// limit belongs to the kernel and all host threads share it; set to a call's own size, a smaller call of another thread
-// could lower it between this thread's setting and its launch, which then fails.
-constexpr int kMaxHead = 128;  // the largest head size
-template <typename K>
-cudaError_t allow_smem(K kern, size_t most) {
-    return cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
-}
-
 // ------------------------------------------------------------------ launch bookkeeping
 // Every launch goes through launch_begin/launch_end so the optional per-kernel
 // timing (la_timing_enable) can bracket it with events on the launch stream.

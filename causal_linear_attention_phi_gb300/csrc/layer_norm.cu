@@ -12,7 +12,7 @@
 // Measured on one GB300, of the 6.79 TB/s a copy reaches: forward 131072 x 2048 bf16 178 us (0.89), gradient
 // 1048576 x 128 bf16 131 us (0.92), 32768 x 8192 bf16 320 us (0.74: 512 threads to a row, one block to an SM).
 #include "layer_norm.cuh"
-#include "sm100.cuh"
+#include "shared_memory.cuh"
 
 namespace la {
 namespace ln {
@@ -83,13 +83,6 @@ struct Pairs<float> {
 // (1048576 x 128; here 0.92).  What is left is the drain of the last tiles and the statistics.
 constexpr int kFwdStages = 2, kBwdStages = 3;
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            sm100::smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(sm100::smem_u32(bar))
-        : "memory");
-}
 // Sums of x over the TPR threads of a row, TPR <= 32 by shuffles, else over the row's warps by a barrier of its own
 // (id 1 + row of the block) and `buf` (two halves taken in turn).
 template <int TPR, int NV, int W8>
@@ -151,7 +144,7 @@ ln_fwd_tiles(const T* x, const T* __restrict__ w, const T* __restrict__ b, T* y,
         const uint32_t bytes = rows_of(k) * tl.row;
         LA_DCHECK(bytes <= tile && k * tl.R + rows_of(k) <= tl.rows);
         sm100::mbar_arrive_expect_tx(bar + s, bytes);
-        bulk_load(smem + s * tile, reinterpret_cast<const uint8_t*>(x) + k * tile, bytes, bar + s);
+        sm100::bulk_load(smem + s * tile, reinterpret_cast<const uint8_t*>(x) + k * tile, bytes, bar + s);
     };
     for (int i = 0; i < kFwdStages; ++i) load(i);
     const float inv = 1.f / (float)tl.C;
@@ -248,8 +241,8 @@ ln_bwd_tiles(const T* x, const T* __restrict__ w, const float* __restrict__ mean
         const uint32_t bytes = rows_of(k) * tl.row;
         LA_DCHECK(bytes <= tile && k * tl.R + rows_of(k) <= tl.rows);
         sm100::mbar_arrive_expect_tx(bar + s, 2 * bytes);
-        bulk_load(smem + 2 * s * tile, reinterpret_cast<const uint8_t*>(x) + k * tile, bytes, bar + s);
-        bulk_load(smem + (2 * s + 1) * tile, reinterpret_cast<const uint8_t*>(dy) + k * tile, bytes, bar + s);
+        sm100::bulk_load(smem + 2 * s * tile, reinterpret_cast<const uint8_t*>(x) + k * tile, bytes, bar + s);
+        sm100::bulk_load(smem + (2 * s + 1) * tile, reinterpret_cast<const uint8_t*>(dy) + k * tile, bytes, bar + s);
     };
     for (int i = 0; i < stages; ++i) load(i);
     float2 wv[kKeep ? VPT : 1][P::n], dw[VPT][P::n], db[VPT][P::n];
@@ -418,7 +411,7 @@ ln_fwd_elements(const T* x, const T* __restrict__ w, const T* __restrict__ b, T*
         LA_DCHECK(sp.inside(k));
         sm100::mbar_arrive_expect_tx(bar + s, sp.bytes(k));
         if (sp.bytes(k))
-            bulk_load(smem + s * tl.pitch, reinterpret_cast<const uint8_t*>(x) + sp.start(k) - sp.lead(k), sp.bytes(k), bar + s);
+            sm100::bulk_load(smem + s * tl.pitch, reinterpret_cast<const uint8_t*>(x) + sp.start(k) - sp.lead(k), sp.bytes(k), bar + s);
     };
     for (int i = 0; i < kFwdStages; ++i) load(i, i);
     float wv[kKeep ? VPT : 1], bv[kKeep ? VPT : 1];
@@ -519,8 +512,8 @@ ln_bwd_elements(const T* x, const T* __restrict__ w, const float* __restrict__ m
         LA_DCHECK(sp.inside(k));
         sm100::mbar_arrive_expect_tx(bar + s, 2 * bytes);
         if (!bytes) return;
-        bulk_load(smem + 2 * s * tl.pitch, reinterpret_cast<const uint8_t*>(x) + from, bytes, bar + s);
-        bulk_load(smem + (2 * s + 1) * tl.pitch, reinterpret_cast<const uint8_t*>(dy) + from, bytes, bar + s);
+        sm100::bulk_load(smem + 2 * s * tl.pitch, reinterpret_cast<const uint8_t*>(x) + from, bytes, bar + s);
+        sm100::bulk_load(smem + (2 * s + 1) * tl.pitch, reinterpret_cast<const uint8_t*>(dy) + from, bytes, bar + s);
     };
     for (int i = 0; i < stages; ++i) load(i, i);
     float wv[kKeep ? VPT : 1], dw[VPT], db[VPT];

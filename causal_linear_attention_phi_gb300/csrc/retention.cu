@@ -18,6 +18,7 @@
 // Powers gamma^m are formed by square-and-multiply in fp64 and rounded once to
 // fp32 (0^0 = 1, so gamma = 0 needs no special case); each CTA keeps a table of
 // gamma^0 .. gamma^C in shared memory.  Accumulation is fp32 throughout.
+#include "shared_memory.cuh"
 #include "simt_common.cuh"
 
 namespace la {

@@ -10,6 +10,7 @@
 // tile load"); rows past the end of the sequence hold zeros.
 #include <mutex>
 
+#include "shared_memory.cuh"
 #include "simt_common.cuh"
 
 namespace la {

@@ -76,14 +76,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
     return true;
 }
 
-// After a wait that ran out: for copies that the calling thread has issued to `stages` buffers in turn (the i-th completes
-// phase i / stages of barrier i % stages), waits once more, with the same limit, for those that may be in flight.  No block
-// leaves copies behind, which would land in the shared memory of the next one.
-inline __device__ __noinline__ void mbar_drain(uint64_t* bar, int stages, long long issued, int* err, int code) {
-    for (long long i = issued > stages ? issued - stages : 0; i < issued; ++i)
-        mbar_wait(bar + i % stages, (int)(i / stages) & 1, err, code);
-}
-
 // ------------------------------------------------------------------ flags in global memory
 // A flag written by one CTA and read by others: release store / acquire load at GPU scope.
 __device__ __forceinline__ void flag_release(unsigned* f, unsigned v) {

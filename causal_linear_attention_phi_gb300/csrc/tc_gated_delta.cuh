@@ -3,6 +3,7 @@
 #pragma once
 
 #include "gated_delta.cuh"
+#include "shared_memory.cuh"
 #include "tc_common.cuh"
 
 namespace la {
@@ -20,13 +21,6 @@ constexpr int kMatsFwd = 4 * kBlk, kMatsBwd = 6 * kBlk;  // bytes of a chunk
 constexpr int kFwdGates = 3 * kC * 4;  // gam, -gam, tail beta of the record
 constexpr int kRevGates = 6 * kC * 4;  // and tail, beta, -beta gam
 
-// Contiguous global -> shared copy (16-byte aligned, a multiple of 16 bytes).
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar))
-        : "memory");
-}
 // Contiguous shared -> global copy, tracked by the issuing thread's bulk groups.
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)

@@ -22,14 +22,16 @@ from . import build as _build
 __all__ = [
     "LaError", "noncausal_fwd", "noncausal_bwd", "causal_fwd", "causal_bwd", "causal_step_host", "host_step_bytes",
     "recurrent_step", "retention_fwd", "retention_step", "gated_delta_fwd", "gated_delta_bwd", "gated_delta_step",
+    "cross_fwd", "cross_bwd", "cross_apply", "cross_workspace_bytes",
     "layer_norm_fwd", "layer_norm_bwd", "layer_norm_workspace_bytes", "selftest_bounded_wait", "workspace_bytes",
     "last_error", "clear_error", "timing_enable", "timing_reset", "timing_read", "library", "version",
     "OP_NONCAUSAL_FWD", "OP_CAUSAL_FWD", "OP_CAUSAL_BWD", "OP_NONCAUSAL_BWD", "OP_RETENTION_FWD",
-    "OP_GATED_DELTA_FWD", "OP_GATED_DELTA_BWD",
+    "OP_GATED_DELTA_FWD", "OP_GATED_DELTA_BWD", "OP_CROSS_FWD", "OP_CROSS_BWD", "OP_CROSS_APPLY",
 ]
 
 OP_NONCAUSAL_FWD, OP_CAUSAL_FWD, OP_CAUSAL_BWD, OP_NONCAUSAL_BWD, OP_RETENTION_FWD = 0, 1, 2, 3, 4
 OP_GATED_DELTA_FWD, OP_GATED_DELTA_BWD = 5, 6
+OP_CROSS_FWD, OP_CROSS_BWD, OP_CROSS_APPLY = 7, 8, 9
 LA_F32, LA_BF16 = 0, 1
 _STATUS = {0: "LA_OK", 1: "LA_ERR_INVALID_ARG", 2: "LA_ERR_UNSUPPORTED", 3: "LA_ERR_WORKSPACE",
            4: "LA_ERR_CUDA", 5: "LA_ERR_TIMEOUT", 6: "LA_ERR_BOUNDS"}
@@ -57,6 +59,11 @@ class KernelTime(ctypes.Structure):
 
 _lib = None
 _lock = threading.Lock()
+class CrossShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("N", ctypes.c_int), ("M", ctypes.c_int),
+                ("Dk", ctypes.c_int), ("Dv", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
 _vp = ctypes.c_void_p
 
 
@@ -80,6 +87,11 @@ def _declare(lib):
     lib.la_gated_delta_bwd.argtypes = [_vp] * 11 + [Shape, _vp, ctypes.c_size_t, _vp]
     lib.la_gated_delta_bwd_with_state.argtypes = [_vp] * 14 + [Shape, _vp, ctypes.c_size_t, _vp]
     lib.la_gated_delta_step.argtypes = [_vp] * 7 + [Shape, _vp]
+    lib.la_cross_workspace_bytes.argtypes = [ctypes.c_int, CrossShape]
+    lib.la_cross_workspace_bytes.restype = ctypes.c_size_t
+    lib.la_cross_fwd.argtypes = [_vp] * 7 + [CrossShape, _vp, ctypes.c_size_t, _vp]
+    lib.la_cross_bwd.argtypes = [_vp] * 10 + [CrossShape, _vp, ctypes.c_size_t, _vp]
+    lib.la_cross_apply.argtypes = [_vp] * 4 + [CrossShape, _vp, ctypes.c_size_t, _vp]
     lib.la_layer_norm_fwd.argtypes = [_vp] * 6 + [NormShape, ctypes.c_float, _vp]
     lib.la_layer_norm_workspace_bytes.argtypes = [NormShape]
     lib.la_layer_norm_workspace_bytes.restype = ctypes.c_size_t
@@ -90,7 +102,7 @@ def _declare(lib):
               "la_causal_fwd_with_state", "la_causal_bwd", "la_causal_bwd_after_fwd", "la_recurrent_step",
               "la_retention_fwd", "la_retention_step", "la_gated_delta_fwd", "la_gated_delta_bwd",
               "la_gated_delta_bwd_with_state", "la_gated_delta_step", "la_layer_norm_fwd", "la_layer_norm_bwd",
-              "la_selftest_bounded_wait", "la_selftest_lookback_timeout", "la_last_error", "la_causal_fwd_fused",
+              "la_cross_fwd", "la_cross_bwd", "la_cross_apply", "la_selftest_bounded_wait", "la_selftest_lookback_timeout", "la_last_error", "la_causal_fwd_fused",
               "la_clear_error", "la_timing_enable", "la_timing_reset"):
         getattr(lib, f).restype = ctypes.c_int
     lib.la_last_error.argtypes = []
@@ -525,6 +537,117 @@ def gated_delta_step(q, k, v, g, beta, S, out=None, stream=None):
     out = _result(out, v, "out", stream)
     _check(library().la_gated_delta_step(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(S), _p(out),
                                          Shape(B, H, 1, Dk, Dv, code), _stream_ptr(stream)), "la_gated_delta_step")
+    return out
+
+
+def _cross_args(q, k, v, lengths):
+    """Checks the inputs of a cross attention call; returns its shape."""
+    _need_cuda(q, k, v)
+    qs, ks, vs, dt = q.shape, k.shape, v.shape, q.dtype
+    if len(qs) != 4 or len(ks) != 4 or len(vs) != 4 or ks[:3] != vs[:3] or ks[0] != qs[0] or ks[3] != qs[3]:
+        raise ValueError("expected q [B,H,N,Dk], k [B,Hk,M,Dk] and v [B,Hk,M,Dv]; got %s %s %s" %
+                         (tuple(qs), tuple(ks), tuple(vs)))
+    if k.dtype != dt or v.dtype != dt:
+        raise TypeError("q, k, v must share a dtype")
+    code = _DTYPE_CODE.get(dt)
+    if code is None:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dt)
+    if lengths is not None:
+        _need_cuda(lengths)
+        if lengths.dtype != torch.int32 or lengths.shape != qs[:1]:
+            raise ValueError("lengths must be int32 [B]")
+    return CrossShape(qs[0], qs[1], ks[1], qs[2], ks[2], qs[3], vs[3], code)
+
+
+def _cross_state(S, z, lead, Dk, Dv):
+    if (S is None) != (z is None):
+        raise ValueError("S and z go together")
+    if S is None:
+        return
+    _need_cuda(S, z)
+    if S.dtype != torch.float32 or z.dtype != torch.float32 or S.shape != (*lead, Dk, Dv) or z.shape != (*lead, Dk):
+        raise ValueError("S must be fp32 [B,Hk,Dk,Dv] and z fp32 [B,Hk,Dk]")
+
+
+def _cross_workspace(op, s, device, workspace, stream):
+    if workspace is not None:
+        if not workspace.is_cuda:
+            raise ValueError("workspace must be a device tensor")
+        return workspace, workspace.numel() * workspace.element_size()
+    need = int(library().la_cross_workspace_bytes(op, s))
+    return (_scratch(need, device, stream), need) if need else (None, 0)
+
+
+def cross_workspace_bytes(op: int, B: int, H: int, Hk: int, N: int, M: int, Dk: int, Dv: int, dtype: torch.dtype) -> int:
+    if dtype not in _DTYPE_CODE:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dtype)
+    return int(library().la_cross_workspace_bytes(op, CrossShape(B, H, Hk, N, M, Dk, Dv, _DTYPE_CODE[dtype])))
+
+
+def cross_fwd(q, k, v, lengths=None, out=None, workspace=None, stream=None, return_state=False):
+    """Cross attention: o_i = phi(q_i)^T S / phi(q_i)^T z with S = sum_j phi(k_j) v_j^T, z = sum_j phi(k_j).
+
+    q [B,H,N,Dk] attends to k [B,Hk,M,Dk], v [B,Hk,M,Dv] of another length; Hk divides H, and H / Hk heads of queries
+    share a head of keys.  lengths: int32 [B], the keys of each batch entry that count (all if None); what lies
+    behind them is not used.  A query that no key answers gets 0.  With return_state, returns (o, S, z): the
+    fp32 state that cross_apply (decoding) and cross_bwd take.
+    """
+    s = _cross_args(q, k, v, lengths)
+    if out is None:
+        out = _handed_out(lambda: q.new_empty((*q.shape[:3], s.Dv)), stream)
+    else:
+        _need_cuda(out)
+        if out.shape != (*q.shape[:3], s.Dv) or out.dtype != q.dtype:
+            raise ValueError("out must be %s of shape %s" % (q.dtype, (*q.shape[:3], s.Dv)))
+    S = z = None
+    if return_state:
+        S = _new_f32((s.B, s.Hk, s.Dk, s.Dv), q.device, stream)
+        z = _new_f32((s.B, s.Hk, s.Dk), q.device, stream)
+    ws, nb = _cross_workspace(OP_CROSS_FWD, s, q.device, workspace, stream)
+    _check(library().la_cross_fwd(_p(q), _p(k), _p(v), _p(lengths), _p(out), _p(S), _p(z), s, _p(ws), nb,
+                                  _stream_ptr(stream)), "la_cross_fwd")
+    return (out, S, z) if return_state else out
+
+
+def cross_bwd(q, k, v, dout, lengths=None, S=None, z=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of cross_fwd for upstream gradient dout [B,H,N,Dv]; those of shared heads of keys are summed
+    over the heads of queries, those behind the lengths are 0.  S, z: the state that cross_fwd returned for the same
+    k, v and lengths, summed again if None."""
+    s = _cross_args(q, k, v, lengths)
+    _need_cuda(dout)
+    if dout.shape != (*q.shape[:3], s.Dv) or dout.dtype != q.dtype:
+        raise ValueError("dout must be %s of shape %s" % (q.dtype, (*q.shape[:3], s.Dv)))
+    _cross_state(S, z, (s.B, s.Hk), s.Dk, s.Dv)
+    dq = _result(dq, q, "dq", stream)
+    dk = _result(dk, k, "dk", stream)
+    dv = _result(dv, v, "dv", stream)
+    ws, nb = _cross_workspace(OP_CROSS_BWD, s, q.device, workspace, stream)
+    _check(library().la_cross_bwd(_p(q), _p(k), _p(v), _p(lengths), _p(S), _p(z), _p(dout), _p(dq), _p(dk), _p(dv), s,
+                                  _p(ws), nb, _stream_ptr(stream)), "la_cross_bwd")
+    return dq, dk, dv
+
+
+def cross_apply(q, S, z, out=None, workspace=None, stream=None):
+    """Queries [B,H,N,Dk], or single tokens [B,H,Dk], to a kept state S [B,Hk,Dk,Dv], z [B,Hk,Dk] (fp32, not changed):
+    out = phi(q)^T S / phi(q)^T z, [B,H,N,Dv] or [B,H,Dv]."""
+    _need_cuda(q, S, z)
+    qs, ss = q.shape, S.shape
+    if len(qs) not in (3, 4) or len(ss) != 4 or ss[0] != qs[0] or ss[2] != qs[-1]:
+        raise ValueError("expected q [B,H,N,Dk] or [B,H,Dk] and S [B,Hk,Dk,Dv]; got %s %s" % (tuple(qs), tuple(ss)))
+    code = _DTYPE_CODE.get(q.dtype)
+    if code is None:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % q.dtype)
+    _cross_state(S, z, ss[:2], ss[2], ss[3])
+    s = CrossShape(qs[0], qs[1], ss[1], qs[2] if len(qs) == 4 else 1, 0, ss[2], ss[3], code)
+    want = (*qs[:-1], ss[3])
+    if out is None:
+        out = _handed_out(lambda: q.new_empty(want), stream)
+    else:
+        _need_cuda(out)
+        if out.shape != want or out.dtype != q.dtype:
+            raise ValueError("out must be %s of shape %s" % (q.dtype, want))
+    ws, nb = _cross_workspace(OP_CROSS_APPLY, s, q.device, workspace, stream)
+    _check(library().la_cross_apply(_p(q), _p(S), _p(z), _p(out), s, _p(ws), nb, _stream_ptr(stream)), "la_cross_apply")
     return out
 
 

@@ -9,6 +9,7 @@
 #include <string>
 #include <vector>
 
+#include "cross.cuh"
 #include "gated_delta.cuh"
 #include "la_internal.cuh"
 #include "layer_norm.cuh"
@@ -740,6 +741,117 @@ la_status la_gated_delta_step(const void* q, const void* k, const void* v, const
                        "gated delta step");
 }
 
+static la_status check_cross(const la_cross_shape& s) {
+    if (s.Hk < 0 || s.M < 0) return fail(LA_ERR_INVALID_ARG, "negative size Hk=%d M=%d", s.Hk, s.M);
+    LA_TRY(check_shape(la_shape{s.B, s.H, s.N, s.Dk, s.Dv, s.dtype}));
+    if (s.B == 0 || s.H == 0) return LA_OK;
+    if (s.Hk == 0 || s.H % s.Hk != 0) return fail(LA_ERR_INVALID_ARG, "H=%d is not a multiple of Hk=%d", s.H, s.Hk);
+    LA_TRY(check_shape(la_shape{s.B, s.Hk, s.M, s.Dk, s.Dv, s.dtype}));
+    if (cross::query_rows(s) >= 0x7FFFFFFFll - 128 || s.M >= 0x7FFFFFFF - 128)
+        return fail(LA_ERR_UNSUPPORTED, "too many rows to a head of keys (%lld queries, %d keys)", cross::query_rows(s), s.M);
+    return LA_OK;
+}
+
+static bool cross_few(const la_cross_shape& s) {
+    return !cross::tc_ok(s) ? cross::query_rows(s) <= 16 : cross::query_rows(s) <= 32;
+}
+
+size_t la_cross_workspace_bytes(int op, la_cross_shape s) {
+    if (op < LA_OP_CROSS_FWD || op > LA_OP_CROSS_APPLY) return 0;
+    if (check_cross(s) != LA_OK || s.B == 0 || s.H == 0) return 0;
+    if (op == LA_OP_CROSS_APPLY) return s.N == 0 || cross_few(s) || !cross::tc_ok(s) ? 0 : cross::tc_bytes(s, op);
+    if (s.M == 0 || (op == LA_OP_CROSS_BWD && s.N == 0)) return 0;
+    return cross::tc_ok(s) ? cross::tc_bytes(s, op) : cross::simt_bytes(s, op);
+}
+
+static la_status check_state(const float* S, const float* z) {
+    if (!S != !z) return fail(LA_ERR_INVALID_ARG, "S and z go together");
+    if (!S) return LA_OK;
+    LA_TRY(check_ptr(S, "S"));
+    return check_ptr(z, "z");
+}
+
+la_status la_cross_fwd(const void* q, const void* k, const void* v, const int* lens, void* o, float* S, float* z,
+                       la_cross_shape s, void* ws, size_t ws_bytes, la_stream_t stream) {
+    t_detail.clear();
+    LA_TRY(check_cross(s));
+    if (s.B == 0 || s.H == 0 || (s.N == 0 && !S && !z)) return LA_OK;
+    LA_TRY(check_device());
+    LA_TRY(check_state(S, z));
+    if (s.N > 0) LA_TRY(check_ptr(o, "o"));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (s.M == 0) {  // no key: nothing is answered, the state is zero
+        const size_t heads = (size_t)s.B * s.Hk, elem = s.dtype == LA_BF16 ? 2 : 4;
+        if (s.N > 0)
+            LA_TRY(cuda_status(cudaMemsetAsync(o, 0, (size_t)s.B * s.H * s.N * s.Dv * elem, st), "output clear"));
+        if (!S) return LA_OK;
+        LA_TRY(cuda_status(cudaMemsetAsync(S, 0, heads * s.Dk * s.Dv * sizeof(float), st), "state clear"));
+        return cuda_status(cudaMemsetAsync(z, 0, heads * s.Dk * sizeof(float), st), "state clear");
+    }
+    if (s.N > 0) LA_TRY(check_ptr(q, "q"));
+    LA_TRY(check_ptr(k, "k"));
+    LA_TRY(check_ptr(v, "v"));
+    if (lens) LA_TRY(check_ptr(lens, "lens", 4));
+    LA_TRY(check_ws(ws, ws_bytes, la_cross_workspace_bytes(LA_OP_CROSS_FWD, s)));
+    const cross::FwdArgs a{q, k, v, lens, o, S, z};
+    return cuda_status(cross::tc_ok(s) ? cross::tc_fwd(a, s, static_cast<char*>(ws), st)
+                                       : cross::simt_fwd(a, s, static_cast<char*>(ws), st),
+                       "cross attention forward");
+}
+
+la_status la_cross_bwd(const void* q, const void* k, const void* v, const int* lens, const float* S, const float* z,
+                       const void* dout, void* dq, void* dk, void* dv, la_cross_shape s, void* ws, size_t ws_bytes,
+                       la_stream_t stream) {
+    t_detail.clear();
+    LA_TRY(check_cross(s));
+    if (s.B == 0 || s.H == 0 || (s.N == 0 && s.M == 0)) return LA_OK;
+    LA_TRY(check_device());
+    LA_TRY(check_state(S, z));
+    if (s.N > 0) LA_TRY(check_ptr(dq, "dq"));
+    if (s.M > 0) {
+        LA_TRY(check_ptr(dk, "dk"));
+        LA_TRY(check_ptr(dv, "dv"));
+    }
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const size_t elem = s.dtype == LA_BF16 ? 2 : 4;
+    if (s.M == 0)  // no key: the outputs are 0 whatever the queries
+        return cuda_status(cudaMemsetAsync(dq, 0, (size_t)s.B * s.H * s.N * s.Dk * elem, st), "gradient clear");
+    if (s.N == 0) {  // no query: no gradient
+        const size_t rows = (size_t)s.B * s.Hk * s.M;
+        LA_TRY(cuda_status(cudaMemsetAsync(dk, 0, rows * s.Dk * elem, st), "gradient clear"));
+        return cuda_status(cudaMemsetAsync(dv, 0, rows * s.Dv * elem, st), "gradient clear");
+    }
+    LA_TRY(check_ptr(q, "q"));
+    LA_TRY(check_ptr(k, "k"));
+    LA_TRY(check_ptr(v, "v"));
+    LA_TRY(check_ptr(dout, "dout"));
+    if (lens) LA_TRY(check_ptr(lens, "lens", 4));
+    LA_TRY(check_ws(ws, ws_bytes, la_cross_workspace_bytes(LA_OP_CROSS_BWD, s)));
+    const cross::BwdArgs a{q, k, v, lens, S, z, dout, dq, dk, dv};
+    return cuda_status(cross::tc_ok(s) ? cross::tc_bwd(a, s, static_cast<char*>(ws), st)
+                                       : cross::simt_bwd(a, s, static_cast<char*>(ws), st),
+                       "cross attention backward");
+}
+
+la_status la_cross_apply(const void* q, const float* S, const float* z, void* o, la_cross_shape s, void* ws,
+                         size_t ws_bytes, la_stream_t stream) {
+    t_detail.clear();
+    s.M = 0;  // M is ignored
+    LA_TRY(check_cross(s));
+    if (s.B == 0 || s.H == 0 || s.N == 0) return LA_OK;
+    LA_TRY(check_device());
+    LA_TRY(check_ptr(q, "q"));
+    if (!S) return fail(LA_ERR_INVALID_ARG, "S is NULL");
+    LA_TRY(check_state(S, z));
+    LA_TRY(check_ptr(o, "o"));
+    LA_TRY(check_ws(ws, ws_bytes, la_cross_workspace_bytes(LA_OP_CROSS_APPLY, s)));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return cuda_status(cross_few(s)      ? cross::apply_few(q, S, z, o, s, st)
+                       : cross::tc_ok(s) ? cross::tc_apply(q, S, z, o, s, static_cast<char*>(ws), st)
+                                         : cross::simt_apply(q, S, z, o, s, st),
+                       "cross attention apply");
+}
+
 static la_status check_norm(const la_norm_shape& s) {
     if (s.rows < 0 || s.C < 1) return fail(LA_ERR_INVALID_ARG, "bad size rows=%lld C=%d", s.rows, s.C);
     if (s.dtype != LA_F32 && s.dtype != LA_BF16) return fail(LA_ERR_INVALID_ARG, "bad dtype %d", s.dtype);
@@ -806,7 +918,7 @@ la_status la_last_error(void) {
         unsigned site = 0;
         if (cudaMemcpyFromSymbol(&site, g_debug_site, sizeof(site)) == cudaSuccess) {
             static const char* const kFiles[] = {
-                "api.cu", "decode.cu", "gated_delta.cu", "gated_delta.cuh", "gated_delta_step.cu", "host_step.cu",
+                "api.cu", "cross.cuh", "cross_simt.cu", "cross_step.cu", "decode.cu", "gated_delta.cu", "gated_delta.cuh", "gated_delta_step.cu", "host_step.cu",
                 "la_internal.cuh", "layer_norm.cu", "layer_norm.cuh", "noalloc.cu", "retention.cu", "selftest.cu",
                 "shared_memory.cuh", "simt_common.cuh", "simt_kernels.cu", "sm100.cuh", "tc_apply.cu", "tc_bwd.cu",
                 "tc_common.cuh", "tc_fwd.cu", "tc_gated_delta.cu", "tc_gated_delta.cuh", "tc_gated_delta_bwd.cu",

@@ -1,0 +1,489 @@
+// cross_simt.cu -- CUDA-core kernels of cross attention, forward and gradient (fp32 inputs, where one bf16 or tf32 copy of
+// an operand is not exact enough).  Chunks of 64 rows; 256 threads seen as 16 x 16 (ty, tx), each with a register tile
+// of the chunk's product; operands are fp32 tiles in shared memory read in 16-byte vectors (rows broadcast, columns
+// 4 tx + 64 j conflict-free).  Sums are fp32; records of a head are added up in a fixed order.
+#include "cross.cuh"
+#include "shared_memory.cuh"
+
+namespace la {
+namespace cross {
+namespace {
+
+constexpr int kChunk = 64, kThreads = 256;
+
+// Column x of thread tx's W: quads of 4 at 64 j + 4 tx for W >= 4, else W neighbours.
+template <int W>
+__device__ __forceinline__ int col_of(int tx, int x) {
+    return W >= 4 ? 64 * (x >> 2) + 4 * tx + (x & 3) : W * tx + x;
+}
+template <int W>
+__device__ __forceinline__ void load_cols(const float* row, int tx, float (&v)[W]) {
+    if constexpr (W >= 4) {
+#pragma unroll
+        for (int j = 0; j < W / 4; ++j) {
+            const float4 f = *reinterpret_cast<const float4*>(row + 64 * j + 4 * tx);
+            v[4 * j] = f.x, v[4 * j + 1] = f.y, v[4 * j + 2] = f.z, v[4 * j + 3] = f.w;
+        }
+    } else if constexpr (W == 2) {
+        const float2 f = *reinterpret_cast<const float2*>(row + 2 * tx);
+        v[0] = f.x, v[1] = f.y;
+    } else {
+        v[0] = row[tx];
+    }
+}
+template <int W, typename T>
+__device__ __forceinline__ void store_cols(T* row, int tx, const float (&v)[W]) {
+#pragma unroll
+    for (int x = 0; x < W; ++x) row[col_of<W>(tx, x)] = from_f32<T>(v[x]);
+}
+template <int W>
+__device__ __forceinline__ void store_cols(float* row, int tx, const float (&v)[W]) {
+    if constexpr (W >= 4) {
+#pragma unroll
+        for (int j = 0; j < W / 4; ++j)
+            *reinterpret_cast<float4*>(row + 64 * j + 4 * tx) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    } else {
+#pragma unroll
+        for (int x = 0; x < W; ++x) row[W * tx + x] = v[x];
+    }
+}
+
+// Rows [0, n) of a chunk as fp32 (phi applied if asked), the rest of its 64 rows 0.  src: the chunk's first row.
+template <typename T, int D, bool kPhi>
+__device__ __forceinline__ void load_rows(float* dst, const T* __restrict__ src, int n) {
+    constexpr int V = 16 / (int)sizeof(T);
+#pragma unroll 4
+    for (int x = threadIdx.x; x < kChunk * D / V; x += kThreads) {
+        const bool in = x * V < n * D;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (in) w = reinterpret_cast<const uint4*>(src)[x];
+        const T* e = reinterpret_cast<const T*>(&w);
+        float f[V];
+#pragma unroll
+        for (int y = 0; y < V; ++y) {
+            f[y] = to_f32(e[y]);
+            if (kPhi) f[y] = in ? phi_f(f[y]) : 0.f;
+        }
+#pragma unroll
+        for (int y = 0; y < V; y += 4) *reinterpret_cast<float4*>(dst + x * V + y) = make_float4(f[y], f[y + 1], f[y + 2], f[y + 3]);
+    }
+}
+
+// acc[DA/16][DB/16] += A^T B over the 64 rows of two tiles: rows of acc follow col_of over ty.
+template <int DA, int DB>
+__device__ __forceinline__ void outer_sum(const float* a, const float* b, float (&acc)[DA / 16][DB / 16], int ty, int tx) {
+#pragma unroll 2
+    for (int p = 0; p < kChunk; ++p) {
+        float x[DA / 16], y[DB / 16];
+        load_cols<DA / 16>(a + p * DA, ty, x);
+        load_cols<DB / 16>(b + p * DB, tx, y);
+#pragma unroll
+        for (int i = 0; i < DA / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < DB / 16; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+    }
+}
+// out[4][DB/16] = rows 4 ty .. 4 ty + 3 of A [64][DA] times B [DA][DB].
+template <int DA, int DB>
+__device__ __forceinline__ void rows_times(const float* a, const float* b, float (&out)[4][DB / 16], int ty, int tx) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < DB / 16; ++j) out[i][j] = 0.f;
+#pragma unroll 2
+    for (int d = 0; d < DA; d += 4) {
+        float4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(a + (4 * ty + i) * DA + d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float y[DB / 16];
+            load_cols<DB / 16>(b + (d + e) * DB, tx, y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float xi = e == 0 ? x[i].x : e == 1 ? x[i].y : e == 2 ? x[i].z : x[i].w;
+#pragma unroll
+                for (int j = 0; j < DB / 16; ++j) out[i][j] = fmaf(xi, y[j], out[i][j]);
+            }
+        }
+    }
+}
+template <int DA, int DB>
+__device__ __forceinline__ void clear(float (&acc)[DA / 16][DB / 16]) {
+#pragma unroll
+    for (int i = 0; i < DA / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < DB / 16; ++j) acc[i][j] = 0.f;
+}
+// A record: [DK][DV] of the register tiles, then [DK] of threads 0 .. DK - 1.
+template <int DK, int DV>
+__device__ __forceinline__ void write_record(float* rec, const float (&acc)[DK / 16][DV / 16], float z, int ty, int tx) {
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i) store_cols<DV / 16>(rec + col_of<DK / 16>(ty, i) * DV, tx, acc[i]);
+    if (threadIdx.x < DK) rec[DK * DV + threadIdx.x] = z;
+}
+
+__device__ __forceinline__ Span shared_span(const Rows& r, int chunk, bool dead) {
+    __shared__ Span span;
+    if (threadIdx.x < 32) {
+        const Span s = span_of(r, chunk, dead, blockIdx.x, gridDim.x);
+        if (threadIdx.x == 0) span = s;
+    }
+    __syncthreads();
+    return span;
+}
+
+// ------------------------------------------------------------------ sums over the keys
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(kThreads)
+cross_sums_kernel(const T* __restrict__ k, const T* __restrict__ v, float* __restrict__ rec, Rows keys, int slots) {
+    extern __shared__ __align__(16) float sm[];
+    float *ks = sm, *vs = sm + kChunk * DK;
+    pdl_enter();  // launched with programmatic dependent launch
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float acc[DK / 16][DV / 16], z = 0.f;
+    clear<DK, DV>(acc);
+    for (Walk w(keys, kChunk, shared_span(keys, kChunk, false)); w.more(); w.next()) {
+        if (w.fresh) {
+            clear<DK, DV>(acc);
+            z = 0.f;
+        }
+        const size_t row = (size_t)w.bh * keys.M + w.row0();
+        LA_DCHECK(w.bh < keys.heads() && w.row0() + w.rows() <= keys.M && w.rows() > 0);
+        __syncthreads();
+        load_rows<T, DK, true>(ks, k + row * DK, w.rows());
+        load_rows<T, DV, false>(vs, v + row * DV, w.rows());
+        __syncthreads();
+        outer_sum<DK, DV>(ks, vs, acc, ty, tx);
+        if (threadIdx.x < DK)
+            for (int p = 0; p < kChunk; ++p) z += ks[p * DK + threadIdx.x];
+        if (w.last() && LA_DCHECK((int)blockIdx.x + w.bh < slots))
+            write_record<DK, DV>(rec + (size_t)(blockIdx.x + w.bh) * (DK * DV + DK), acc, z, ty, tx);
+    }
+}
+
+// ------------------------------------------------------------------ a head's records added up
+// E = Dk Dv + Dk floats to a record, the state's first; S and z get their parts.
+__global__ void __launch_bounds__(256)
+cross_join_kernel(const float* __restrict__ rec, float* __restrict__ S, float* __restrict__ z, Rows rows, int chunk,
+                  int ctas, int state, int dk) {
+    pdl_enter();  // launched with programmatic dependent launch
+    const int bh = blockIdx.x, E = state + dk, e4 = (blockIdx.y * 256 + threadIdx.x) * 4;
+    const Range g = records_of(rows, chunk, bh, ctas);
+    if (e4 >= E) return;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int c = g.first; c <= g.last; ++c) {
+        const float4 f = *reinterpret_cast<const float4*>(rec + (size_t)(c + bh) * E + e4);
+        a.x += f.x, a.y += f.y, a.z += f.z, a.w += f.w;
+    }
+    float* to = e4 < state ? S + (size_t)bh * state + e4 : z + (size_t)bh * dk + (e4 - state);
+    *reinterpret_cast<float4*>(to) = a;
+}
+
+// ------------------------------------------------------------------ queries
+// den of the 64 rows (4 threads to a row) as its inverse
+template <int DK>
+__device__ __forceinline__ void inverses(const float* ph, const float* zs, float* inv) {
+    const int r = threadIdx.x >> 2, part = threadIdx.x & 3;
+    float den = 0.f;
+#pragma unroll 4
+    for (int d = part; d < DK; d += 4) den = fmaf(ph[r * DK + d], zs[d], den);
+    den += __shfl_xor_sync(0xffffffffu, den, 1);
+    den += __shfl_xor_sync(0xffffffffu, den, 2);
+    if (part == 0) inv[r] = over(den);
+}
+
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(kThreads)
+cross_apply_kernel(const T* __restrict__ q, const float* __restrict__ S, const float* __restrict__ z, T* __restrict__ o,
+                   Rows rows) {
+    extern __shared__ __align__(16) float sm[];
+    float *Ss = sm, *ph = Ss + DK * DV, *zs = ph + kChunk * DK, *inv = zs + DK;
+    pdl_enter();  // launched with programmatic dependent launch
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    bool first = true;
+    for (Walk w(rows, kChunk, shared_span(rows, kChunk, false)); w.more(); w.next()) {
+        __syncthreads();
+        if (first || w.fresh) {
+            first = false;
+            for (int x = threadIdx.x; x < DK * DV / 4; x += kThreads)
+                reinterpret_cast<float4*>(Ss)[x] = reinterpret_cast<const float4*>(S + (size_t)w.bh * DK * DV)[x];
+            if (threadIdx.x < DK) zs[threadIdx.x] = z[(size_t)w.bh * DK + threadIdx.x];
+        }
+        const size_t row = (size_t)w.bh * rows.M + w.row0();
+        LA_DCHECK(w.bh < rows.heads() && w.row0() + w.rows() <= rows.M && w.rows() > 0);
+        load_rows<T, DK, true>(ph, q + row * DK, w.rows());
+        __syncthreads();
+        inverses<DK>(ph, zs, inv);
+        float out[4][DV / 16];
+        rows_times<DK, DV>(ph, Ss, out, ty, tx);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * ty + i;
+            if (r >= w.rows()) break;
+#pragma unroll
+            for (int j = 0; j < DV / 16; ++j) out[i][j] *= inv[r];
+            store_cols<DV / 16>(o + (row + r) * DV, tx, out[i]);
+        }
+    }
+}
+
+// dq and the head's records of (R, r).
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(kThreads)
+cross_query_kernel(const T* __restrict__ q, const T* __restrict__ dout, const float* __restrict__ S,
+                   const float* __restrict__ z, T* __restrict__ dq, float* __restrict__ rec, Rows rows, int slots) {
+    extern __shared__ __align__(16) float sm[];
+    float *St = sm, *ph = St + DK * DV, *ds = ph + kChunk * DK, *zs = ds + kChunk * DV, *inv = zs + DK, *wr = inv + kChunk;
+    pdl_enter();  // launched with programmatic dependent launch
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float R[DK / 16][DV / 16], rz = 0.f;
+    clear<DK, DV>(R);
+    bool first = true;
+    for (Walk w(rows, kChunk, shared_span(rows, kChunk, false)); w.more(); w.next()) {
+        __syncthreads();
+        if (first || w.fresh) {
+            first = false;
+            clear<DK, DV>(R);
+            rz = 0.f;
+            for (int x = threadIdx.x; x < DK * DV; x += kThreads)
+                St[x] = S[(size_t)w.bh * DK * DV + (x % DK) * DV + x / DK];  // transposed: [dv][dk]
+            if (threadIdx.x < DK) zs[threadIdx.x] = z[(size_t)w.bh * DK + threadIdx.x];
+        }
+        const size_t row = (size_t)w.bh * rows.M + w.row0();
+        LA_DCHECK(w.bh < rows.heads() && w.row0() + w.rows() <= rows.M && w.rows() > 0);
+        load_rows<T, DK, true>(ph, q + row * DK, w.rows());
+        load_rows<T, DV, false>(ds, dout + row * DV, w.rows());
+        __syncthreads();
+        inverses<DK>(ph, zs, inv);
+        __syncthreads();
+        float Y[4][DK / 16];
+        rows_times<DV, DK>(ds, St, Y, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * ty + i;
+            float p[DK / 16], zc[DK / 16], t = 0.f;
+            load_cols<DK / 16>(ph + r * DK, tx, p);
+            load_cols<DK / 16>(zs, tx, zc);
+#pragma unroll
+            for (int j = 0; j < DK / 16; ++j) {
+                Y[i][j] *= inv[r];
+                t = fmaf(p[j], Y[i][j], t);
+            }
+#pragma unroll
+            for (int x = 8; x > 0; x >>= 1) t += __shfl_xor_sync(0xffffffffu, t, x);  // over the 16 threads of the row
+            const float g = -t * inv[r];
+            if (tx == 0) wr[r] = -t;
+#pragma unroll
+            for (int j = 0; j < DK / 16; ++j) Y[i][j] = fmaf(g, zc[j], Y[i][j]) * dphi_from_phi(p[j]);
+            if (r < w.rows()) store_cols<DK / 16>(dq + (row + r) * DK, tx, Y[i]);
+        }
+        __syncthreads();
+        for (int x = threadIdx.x; x < kChunk * DK; x += kThreads) ph[x] *= inv[x / DK];
+        __syncthreads();
+        outer_sum<DK, DV>(ph, ds, R, ty, tx);
+        if (threadIdx.x < DK)
+            for (int p = 0; p < kChunk; ++p) rz = fmaf(ph[p * DK + threadIdx.x], wr[p], rz);
+        if (w.last() && LA_DCHECK((int)blockIdx.x + w.bh < slots))
+            write_record<DK, DV>(rec + (size_t)(blockIdx.x + w.bh) * (DK * DV + DK), R, rz, ty, tx);
+    }
+}
+
+// ------------------------------------------------------------------ gradients of the keys
+// The rows behind a head's length: dk = dv = 0.  Bytes [a, b) of a tensor of the head, 16-byte aligned.
+__device__ __forceinline__ void zero_bytes(void* p, size_t bytes, int tid, int threads) {
+    for (size_t x = tid; x < bytes / 16; x += threads) reinterpret_cast<uint4*>(p)[x] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(kThreads)
+cross_key_kernel(const T* __restrict__ k, const T* __restrict__ v, const float* __restrict__ R, const float* __restrict__ rz,
+                 T* __restrict__ dk, T* __restrict__ dv, Rows keys) {
+    extern __shared__ __align__(16) float sm[];
+    float *Rs = sm, *Rt = Rs + DK * DV, *ks = Rt + DK * DV, *vs = ks + kChunk * DK, *rs = vs + kChunk * DV;
+    pdl_enter();  // launched with programmatic dependent launch
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    bool first = true;
+    for (Walk w(keys, kChunk, shared_span(keys, kChunk, false)); w.more(); w.next()) {
+        __syncthreads();
+        if (first || w.fresh) {
+            first = false;
+            for (int x = threadIdx.x; x < DK * DV; x += kThreads) {
+                const float f = R[(size_t)w.bh * DK * DV + x];
+                Rs[x] = f;
+                Rt[(x % DV) * DK + x / DV] = f;
+            }
+            if (threadIdx.x < DK) rs[threadIdx.x] = rz[(size_t)w.bh * DK + threadIdx.x];
+        }
+        const size_t row = (size_t)w.bh * keys.M + w.row0();
+        LA_DCHECK(w.bh < keys.heads() && w.row0() + w.rows() <= keys.M && w.rows() > 0);
+        load_rows<T, DK, true>(ks, k + row * DK, w.rows());
+        load_rows<T, DV, false>(vs, v + row * DV, w.rows());
+        __syncthreads();
+        float out[4][DK / 16], ov[4][DV / 16], rc[DK / 16];
+        rows_times<DV, DK>(vs, Rt, out, ty, tx);
+        rows_times<DK, DV>(ks, Rs, ov, ty, tx);
+        load_cols<DK / 16>(rs, tx, rc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * ty + i;
+            float p[DK / 16];
+            load_cols<DK / 16>(ks + r * DK, tx, p);
+#pragma unroll
+            for (int j = 0; j < DK / 16; ++j) out[i][j] = (out[i][j] + rc[j]) * dphi_from_phi(p[j]);
+            if (r < w.rows()) {
+                store_cols<DK / 16>(dk + (row + r) * DK, tx, out[i]);
+                store_cols<DV / 16>(dv + (row + r) * DV, tx, ov[i]);
+            }
+        }
+    }
+}
+
+// The rows behind the lengths, [live, M) of every head.
+template <typename T>
+__global__ void __launch_bounds__(256)
+cross_clear_kernel(T* __restrict__ dk, T* __restrict__ dv, Rows keys, int Dk, int Dv) {
+    pdl_enter();  // launched with programmatic dependent launch
+    const int bh = blockIdx.y, live = keys.live(bh / keys.Hk);
+    const size_t row = (size_t)bh * keys.M + live, n = keys.M - live;
+    const int tid = blockIdx.x * 256 + threadIdx.x, all = gridDim.x * 256;
+    zero_bytes(dk + row * Dk, n * Dk * sizeof(T), tid, all);
+    zero_bytes(dv + row * Dv, n * Dv * sizeof(T), tid, all);
+}
+
+// ------------------------------------------------------------------ host
+// Blocks: a wave of the SMs or two, each with at least two chunks where there are that many.
+int blocks_for(long long heads, long long rows, int per_sm) {
+    const long long chunks = heads * ((rows + kChunk - 1) / kChunk), most = 152LL * per_sm;
+    const long long want = (chunks + 1) / 2;
+    return (int)(want < 1 ? 1 : want > most ? most : want);
+}
+int key_blocks(const la_cross_shape& s) { return blocks_for((long long)s.B * s.Hk, s.M, 2); }
+int query_blocks(const la_cross_shape& s) { return blocks_for((long long)s.B * s.Hk, query_rows(s), 1); }
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+struct Layout {
+    size_t rec, S, z, R, r, bytes;
+};
+Layout layout(const la_cross_shape& s, bool bwd) {
+    const size_t heads = (size_t)s.B * s.Hk, E = (size_t)s.Dk * s.Dv + s.Dk;
+    Layout l{};
+    size_t blocks = key_blocks(s);
+    if (bwd && (size_t)query_blocks(s) > blocks) blocks = query_blocks(s);
+    l.S = up((blocks + heads) * E * 4);  // the records first
+    l.z = l.S + up(heads * s.Dk * s.Dv * 4);
+    l.bytes = l.z + up(heads * s.Dk * 4);
+    if (bwd) {
+        l.R = l.bytes;
+        l.r = l.R + up(heads * s.Dk * s.Dv * 4);
+        l.bytes = l.r + up(heads * s.Dk * 4);
+    }
+    return l;
+}
+
+template <typename K, typename... A>
+cudaError_t run(const char* name, K kern, dim3 grid, size_t smem, cudaStream_t st, A... args) {
+    cudaError_t e = allow_smem(kern, smem);  // a kernel always takes the same
+    if (e != cudaSuccess) return e;
+    launch_begin(name, st);
+    e = launch_pdl(kern, grid, dim3(kThreads), smem, st, args...);
+    const cudaError_t e2 = launch_end(name, st);
+    return e != cudaSuccess ? e : e2;
+}
+#define CR_TRY(x)                            \
+    do {                                     \
+        const cudaError_t e_ = (x);          \
+        if (e_ != cudaSuccess) return e_;    \
+    } while (0)
+
+cudaError_t join(const float* rec, float* S, float* z, const Rows& rows, int ctas, const la_cross_shape& s, cudaStream_t st) {
+    const int E = s.Dk * s.Dv + s.Dk;
+    return run("cross_join", cross_join_kernel, dim3(rows.heads(), (E + 1023) / 1024), 0, st, rec, S, z, rows, kChunk, ctas,
+               s.Dk * s.Dv, s.Dk);
+}
+
+template <typename T, int DK, int DV>
+cudaError_t sums(const void* k, const void* v, const Rows& keys, float* rec, float* S, float* z, const la_cross_shape& s,
+                 cudaStream_t st) {
+    const int ctas = key_blocks(s);
+    CR_TRY(run("cross_sums", cross_sums_kernel<T, DK, DV>, dim3(ctas), kChunk * (DK + DV) * 4, st, (const T*)k, (const T*)v, rec,
+               keys, ctas + keys.heads()));
+    return join(rec, S, z, keys, ctas, s, st);
+}
+
+template <typename T, int DK, int DV>
+cudaError_t apply(const void* q, const float* S, const float* z, void* o, const la_cross_shape& s, cudaStream_t st) {
+    const Rows rows = grouped_queries(s);
+    return run("cross_apply", cross_apply_kernel<T, DK, DV>, dim3(blocks_for(rows.heads(), rows.M, 2)),
+               (DK * DV + kChunk * DK + DK + kChunk) * 4, st, (const T*)q, S, z, (T*)o, rows);
+}
+
+template <typename T, int DK, int DV>
+cudaError_t fwd_t(const FwdArgs& a, const la_cross_shape& s, char* ws, cudaStream_t st) {
+    const Layout l = layout(s, false);
+    float *S = a.S ? a.S : reinterpret_cast<float*>(ws + l.S), *z = a.z ? a.z : reinterpret_cast<float*>(ws + l.z);
+    CR_TRY((sums<T, DK, DV>(a.k, a.v, key_rows(s, a.lens), reinterpret_cast<float*>(ws), S, z, s, st)));
+    if (s.N == 0) return cudaSuccess;
+    return apply<T, DK, DV>(a.q, S, z, a.o, s, st);
+}
+
+template <typename T, int DK, int DV>
+cudaError_t bwd_t(const BwdArgs& a, const la_cross_shape& s, char* ws, cudaStream_t st) {
+    const Layout l = layout(s, true);
+    const Rows keys = key_rows(s, a.lens), rows = grouped_queries(s);
+    float *rec = reinterpret_cast<float*>(ws), *R = reinterpret_cast<float*>(ws + l.R), *r = reinterpret_cast<float*>(ws + l.r);
+    const float *S = a.S, *z = a.z;
+    if (!S) {
+        float *Sw = reinterpret_cast<float*>(ws + l.S), *zw = reinterpret_cast<float*>(ws + l.z);
+        CR_TRY((sums<T, DK, DV>(a.k, a.v, keys, rec, Sw, zw, s, st)));
+        S = Sw, z = zw;
+    }
+    const int qc = query_blocks(s);
+    CR_TRY(run("cross_query", cross_query_kernel<T, DK, DV>, dim3(qc), (DK * DV + kChunk * (DK + DV) + DK + 2 * kChunk) * 4, st,
+               (const T*)a.q, (const T*)a.dout, S, z, (T*)a.dq, rec, rows, qc + rows.heads()));
+    CR_TRY(join(rec, R, r, rows, qc, s, st));
+    CR_TRY(run("cross_key", cross_key_kernel<T, DK, DV>, dim3(blocks_for(keys.heads(), s.M, 1)),
+               (2 * DK * DV + kChunk * (DK + DV) + DK) * 4, st, (const T*)a.k, (const T*)a.v, R, r, (T*)a.dk, (T*)a.dv, keys));
+    if (!a.lens) return cudaSuccess;
+    return run("cross_clear", cross_clear_kernel<T>, dim3(8, keys.heads()), 0, st, (T*)a.dk, (T*)a.dv, keys, s.Dk, s.Dv);
+}
+
+#define LA_SIZES(F) F(16, 16) F(16, 32) F(16, 64) F(16, 128) F(32, 16) F(32, 32) F(32, 64) F(32, 128) \
+    F(64, 16) F(64, 32) F(64, 64) F(64, 128) F(128, 16) F(128, 32) F(128, 64) F(128, 128)
+
+}  // namespace
+
+bool tc_ok(const la_cross_shape&) { return false; }
+size_t tc_bytes(const la_cross_shape&, int) { return 0; }
+cudaError_t tc_fwd(const FwdArgs&, const la_cross_shape&, char*, cudaStream_t) { return cudaErrorInvalidValue; }
+cudaError_t tc_bwd(const BwdArgs&, const la_cross_shape&, char*, cudaStream_t) { return cudaErrorInvalidValue; }
+cudaError_t tc_apply(const void*, const float*, const float*, void*, const la_cross_shape&, char*, cudaStream_t) { return cudaErrorInvalidValue; }
+
+size_t simt_bytes(const la_cross_shape& s, int op) { return layout(s, op == LA_OP_CROSS_BWD).bytes; }
+
+cudaError_t simt_fwd(const FwdArgs& a, const la_cross_shape& s, char* ws, cudaStream_t st) {
+#define LA_GO(x, y) \
+    if (s.Dk == x && s.Dv == y) return s.dtype == LA_BF16 ? fwd_t<__nv_bfloat16, x, y>(a, s, ws, st) : fwd_t<float, x, y>(a, s, ws, st);
+    LA_SIZES(LA_GO)
+#undef LA_GO
+    return cudaErrorInvalidValue;
+}
+cudaError_t simt_bwd(const BwdArgs& a, const la_cross_shape& s, char* ws, cudaStream_t st) {
+#define LA_GO(x, y) \
+    if (s.Dk == x && s.Dv == y) return s.dtype == LA_BF16 ? bwd_t<__nv_bfloat16, x, y>(a, s, ws, st) : bwd_t<float, x, y>(a, s, ws, st);
+    LA_SIZES(LA_GO)
+#undef LA_GO
+    return cudaErrorInvalidValue;
+}
+cudaError_t simt_apply(const void* q, const float* S, const float* z, void* o, const la_cross_shape& s, cudaStream_t st) {
+#define LA_GO(x, y) \
+    if (s.Dk == x && s.Dv == y) return s.dtype == LA_BF16 ? apply<__nv_bfloat16, x, y>(q, S, z, o, s, st) : apply<float, x, y>(q, S, z, o, s, st);
+    LA_SIZES(LA_GO)
+#undef LA_GO
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace cross
+}  // namespace la

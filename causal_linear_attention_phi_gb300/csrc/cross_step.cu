@@ -1,0 +1,115 @@
+// cross_step.cu -- cross attention of a few queries to a kept state: out = phi(q)^T S / phi(q)^T z for the rows of
+// queries that share a head of keys (one token of each of its heads of queries, or a few tokens).
+//
+// Bound by memory: a state of Dk x Dv fp32 is read once, everything else is O(Dk + Dv) to a row.  A block owns a head:
+// its threads issue all loads of S before any arithmetic and keep S in registers (at most 16 16-byte vectors each),
+// so that every further row costs shared memory and arithmetic only.  Rows are taken kRows at a time: each thread
+// forms their partial sums over its rows of S, and the warps' sums are joined in shared memory in a fixed order.
+#include "cross.cuh"
+
+namespace la {
+namespace cross {
+namespace {
+
+template <int DK, int DV>
+struct Few {
+    static constexpr int kVecs = DK * DV / 4;
+    static constexpr int kThreads = kVecs / 8 < 32 ? 32 : kVecs / 8 > 256 ? 256 : kVecs / 8;
+    static constexpr int kWarps = kThreads / 32;
+    static constexpr int kCols = DV / 4;                 // 16-byte vectors of a row of S
+    static constexpr int kPer = kThreads / kCols;        // rows of S in one load of the block
+    static constexpr int kHeld = kVecs / kThreads;       // vectors held by a thread
+};
+
+template <typename T, int DK, int DV, int kRows>
+__global__ void __launch_bounds__(Few<DK, DV>::kThreads)
+cross_few_kernel(const T* __restrict__ q, const float* __restrict__ S, const float* __restrict__ z, T* __restrict__ o,
+                 int R) {
+    using F = Few<DK, DV>;
+    __shared__ float ph[kRows][DK];
+    __shared__ float part[F::kWarps][kRows][DV];
+    __shared__ float inv[kRows];
+    pdl_enter();  // launched with programmatic dependent launch
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int c4 = tid % F::kCols, r0 = tid / F::kCols;
+    const size_t bh = blockIdx.x;
+    const float* Sh = S + bh * DK * DV;
+    const float* zh = z + bh * DK;
+    float4 s[F::kHeld];
+#pragma unroll
+    for (int x = 0; x < F::kHeld; ++x)
+        s[x] = *reinterpret_cast<const float4*>(Sh + (size_t)(r0 + F::kPer * x) * DV + 4 * c4);
+    const T* qh = q + bh * R * DK;
+    T* oh = o + bh * R * DV;
+    for (int base = 0; base < R; base += kRows) {
+        const int n = min(kRows, R - base);
+        for (int x = tid; x < n * DK; x += F::kThreads) ph[x / DK][x % DK] = phi_f(to_f32(qh[(size_t)base * DK + x]));
+        __syncthreads();
+        for (int r = warp; r < n; r += F::kWarps) {
+            float den = 0.f;
+            for (int d = lane; d < DK; d += 32) den = fmaf(ph[r][d], zh[d], den);
+#pragma unroll
+            for (int y = 16; y > 0; y >>= 1) den += __shfl_xor_sync(0xffffffffu, den, y);
+            if (lane == 0) inv[r] = over(den);
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            if (r >= n) break;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int x = 0; x < F::kHeld; ++x) {
+                const float p = ph[r][r0 + F::kPer * x];
+                a.x = fmaf(p, s[x].x, a.x);
+                a.y = fmaf(p, s[x].y, a.y);
+                a.z = fmaf(p, s[x].z, a.z);
+                a.w = fmaf(p, s[x].w, a.w);
+            }
+#pragma unroll
+            for (int y = F::kCols; y < 32; y <<= 1) {  // lanes of the same columns
+                a.x += __shfl_xor_sync(0xffffffffu, a.x, y);
+                a.y += __shfl_xor_sync(0xffffffffu, a.y, y);
+                a.z += __shfl_xor_sync(0xffffffffu, a.z, y);
+                a.w += __shfl_xor_sync(0xffffffffu, a.w, y);
+            }
+            if (lane < F::kCols) *reinterpret_cast<float4*>(&part[warp][r][4 * c4]) = a;
+        }
+        __syncthreads();
+        for (int x = tid; x < n * DV; x += F::kThreads) {
+            float a = 0.f;
+#pragma unroll
+            for (int w = 0; w < F::kWarps; ++w) a += part[w][x / DV][x % DV];
+            if (LA_DCHECK(base + x / DV < R)) oh[(size_t)base * DV + x] = from_f32<T>(a * inv[x / DV]);
+        }
+        __syncthreads();  // before the next rows
+    }
+}
+
+template <typename T, int DK, int DV>
+cudaError_t go(const void* q, const float* S, const float* z, void* o, int heads, int R, cudaStream_t st) {
+    auto kern = R == 1 ? cross_few_kernel<T, DK, DV, 1> : cross_few_kernel<T, DK, DV, 4>;
+    launch_begin("cross_few", st);
+    const cudaError_t e = launch_pdl(kern, dim3(heads), dim3(Few<DK, DV>::kThreads), 0, st, (const T*)q, S, z, (T*)o, R);
+    const cudaError_t e2 = launch_end("cross_few", st);
+    return e != cudaSuccess ? e : e2;
+}
+
+template <typename T>
+cudaError_t pick(const void* q, const float* S, const float* z, void* o, const la_cross_shape& s, cudaStream_t st) {
+    const int heads = s.B * s.Hk, R = (int)query_rows(s);
+#define LA_FEW(a, b) \
+    if (s.Dk == a && s.Dv == b) return go<T, a, b>(q, S, z, o, heads, R, st);
+#define LA_FEW4(a) LA_FEW(a, 16) LA_FEW(a, 32) LA_FEW(a, 64) LA_FEW(a, 128)
+    LA_FEW4(16) LA_FEW4(32) LA_FEW4(64) LA_FEW4(128)
+#undef LA_FEW4
+#undef LA_FEW
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t apply_few(const void* q, const float* S, const float* z, void* o, const la_cross_shape& s, cudaStream_t st) {
+    return s.dtype == LA_BF16 ? pick<__nv_bfloat16>(q, S, z, o, s, st) : pick<float>(q, S, z, o, s, st);
+}
+
+}  // namespace cross
+}  // namespace la

@@ -73,7 +73,10 @@ typedef enum {
     LA_OP_NONCAUSAL_BWD = 3,
     LA_OP_RETENTION_FWD = 4,
     LA_OP_GATED_DELTA_FWD = 5,
-    LA_OP_GATED_DELTA_BWD = 6
+    LA_OP_GATED_DELTA_BWD = 6,
+    LA_OP_CROSS_FWD = 7,   /* the cross attention ops: la_cross_workspace_bytes */
+    LA_OP_CROSS_BWD = 8,
+    LA_OP_CROSS_APPLY = 9
 } la_op;
 
 /* Problem shape.  dtype is an la_dtype value. */
@@ -326,6 +329,56 @@ la_status la_gated_delta_bwd_with_state(const void* q, const void* k, const void
  */
 la_status la_gated_delta_step(const void* q, const void* k, const void* v, const void* g, const void* beta,
                               float* S, void* out, la_shape s, la_stream_t stream);
+
+/*
+ * Cross attention: the non-causal form for queries and keys of different lengths (a decoder attending to an
+ * encoder's positions), with memories padded to a common length and heads of keys shared by heads of queries.
+ *   o_i = phi(q_i)^T S / phi(q_i)^T z,  S = sum_{j < len_b} phi(k_j) v_j^T,  z = sum_{j < len_b} phi(k_j);
+ * query head h of H attends to key head h / (H / Hk) of Hk (Hk divides H).
+ * q: [B,H,N,Dk]; k: [B,Hk,M,Dk]; v: [B,Hk,M,Dv]; o: [B,H,N,Dv] in s.dtype; o written.
+ * lens: NULL (all M keys), or DEVICE int32 [B], 4-byte aligned: the keys of each batch entry that count.  Values are
+ *   taken as clamped to 0 .. M.  What lies behind a length is never used: it may hold infinities or NaN.
+ * A query whose normaliser is 0 (no key counts) gets an output of 0.
+ * S, z: both NULL, or DEVICE fp32 [B,Hk,Dk,Dv] and [B,Hk,Dk] that receive the state (written), from which
+ *   la_cross_apply answers further queries and la_cross_bwd takes it back.  o does not depend on whether they are given.
+ *   bf16 calls sum phi(k) in two bf16 parts (16 bits and a sign); products and sums are fp32.
+ * Sizes: Dk and Dv as above, B*H <= 65535, (H / Hk) * N < 2^31 - 128, elements of each tensor < 2^40.  N = 0 or
+ * M = 0 is allowed: without keys o, S and z are zero.
+ * Workspace: la_cross_workspace_bytes(LA_OP_CROSS_FWD, s).
+ */
+typedef struct {
+    int B, H, Hk, N, M, Dk, Dv;
+    int dtype;
+} la_cross_shape;
+
+size_t la_cross_workspace_bytes(int op, la_cross_shape s);
+la_status la_cross_fwd(const void* q, const void* k, const void* v, const int* lens, void* o, float* S, float* z,
+                       la_cross_shape s, void* ws, size_t ws_bytes, la_stream_t stream);
+
+/*
+ * Gradient of la_cross_fwd for an upstream gradient dout = dL/do.  With den_i = phi(q_i)^T z, y_i = S dout_i / den_i
+ * and t_i = phi(q_i)^T y_i:
+ *   dq_i = (y_i - t_i / den_i z) * phi'(q_i),
+ *   dk_j = (R v_j + r) * phi'(k_j),  dv_j = R^T phi(k_j)   for j < len_b, 0 behind the length,
+ *   R = sum_i phi(q_i) dout_i^T / den_i,  r = -sum_i phi(q_i) t_i / den_i  over the queries of all heads that share the keys.
+ * A query whose normaliser is 0 has a gradient of 0 and adds nothing.
+ * S, z: both NULL (summed again from k and v), or the state that la_cross_fwd returned for the same k, v and lens.
+ * q, dq: [B,H,N,Dk]; k, dk: [B,Hk,M,Dk]; v, dv: [B,Hk,M,Dv]; dout: [B,H,N,Dv]; dq, dk, dv written.
+ * A bf16 call enters S, R and phi(k) of the sums as two bf16 parts each (differences of large terms are left in dq
+ * and dk), phi(q) / den as one (two for Dk <= 64).
+ * Workspace: la_cross_workspace_bytes(LA_OP_CROSS_BWD, s).
+ */
+la_status la_cross_bwd(const void* q, const void* k, const void* v, const int* lens, const float* S, const float* z,
+                       const void* dout, void* dq, void* dk, void* dv, la_cross_shape s, void* ws, size_t ws_bytes,
+                       la_stream_t stream);
+
+/*
+ * Queries to a kept state (S, z), which is read, not changed: decoding, one token at a time (N = 1) or several.
+ * q: [B,H,N,Dk]; o: [B,H,N,Dv]; S: [B,Hk,Dk,Dv], z: [B,Hk,Dk] fp32.  s.M is ignored.
+ * Workspace: la_cross_workspace_bytes(LA_OP_CROSS_APPLY, s), which is 0 for a few queries.
+ */
+la_status la_cross_apply(const void* q, const float* S, const float* z, void* o, la_cross_shape s, void* ws,
+                         size_t ws_bytes, la_stream_t stream);
 
 /*
  * Layer norm over the last dimension of a dense [rows, C] array (the heads' outputs with C = Dv, or the model

@@ -23,7 +23,9 @@ __all__ = [
     "LaError", "noncausal_fwd", "noncausal_bwd", "causal_fwd", "causal_bwd", "causal_step_host", "host_step_bytes",
     "recurrent_step", "retention_fwd", "retention_step", "gated_delta_fwd", "gated_delta_bwd", "gated_delta_step",
     "cross_fwd", "cross_bwd", "cross_apply", "cross_workspace_bytes",
-    "layer_norm_fwd", "layer_norm_bwd", "layer_norm_workspace_bytes", "selftest_bounded_wait", "workspace_bytes",
+    "layer_norm_fwd", "layer_norm_bwd", "layer_norm_workspace_bytes",
+    "gated_norm_fwd", "gated_norm_bwd", "gated_norm_workspace_bytes", "residual_norm_fwd", "residual_norm_bwd",
+    "residual_norm_workspace_bytes", "selftest_bounded_wait", "workspace_bytes",
     "last_error", "clear_error", "timing_enable", "timing_reset", "timing_read", "library", "version",
     "OP_NONCAUSAL_FWD", "OP_CAUSAL_FWD", "OP_CAUSAL_BWD", "OP_NONCAUSAL_BWD", "OP_RETENTION_FWD",
     "OP_GATED_DELTA_FWD", "OP_GATED_DELTA_BWD", "OP_CROSS_FWD", "OP_CROSS_BWD", "OP_CROSS_APPLY",
@@ -64,6 +66,11 @@ class CrossShape(ctypes.Structure):
                 ("Dk", ctypes.c_int), ("Dv", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
+class HeadsShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("N", ctypes.c_int), ("D", ctypes.c_int),
+                ("dtype", ctypes.c_int)]
+
+
 _vp = ctypes.c_void_p
 
 
@@ -96,13 +103,22 @@ def _declare(lib):
     lib.la_layer_norm_workspace_bytes.argtypes = [NormShape]
     lib.la_layer_norm_workspace_bytes.restype = ctypes.c_size_t
     lib.la_layer_norm_bwd.argtypes = [_vp] * 8 + [NormShape, _vp, ctypes.c_size_t, _vp]
+    lib.la_gated_norm_fwd.argtypes = [_vp] * 4 + [HeadsShape, ctypes.c_int, ctypes.c_float, _vp]
+    lib.la_gated_norm_workspace_bytes.argtypes = [HeadsShape]
+    lib.la_gated_norm_workspace_bytes.restype = ctypes.c_size_t
+    lib.la_gated_norm_bwd.argtypes = [_vp] * 7 + [HeadsShape, ctypes.c_int, ctypes.c_float, _vp, ctypes.c_size_t, _vp]
+    lib.la_residual_norm_fwd.argtypes = [_vp] * 9 + [NormShape, ctypes.c_int, ctypes.c_float, _vp]
+    lib.la_residual_norm_workspace_bytes.argtypes = [NormShape]
+    lib.la_residual_norm_workspace_bytes.restype = ctypes.c_size_t
+    lib.la_residual_norm_bwd.argtypes = [_vp] * 13 + [NormShape, ctypes.c_int, _vp, ctypes.c_size_t, _vp]
     lib.la_selftest_bounded_wait.argtypes = [_vp]
     lib.la_selftest_lookback_timeout.argtypes = [_vp] * 4 + [Shape, _vp, ctypes.c_size_t, _vp]
     for f in ("la_causal_step_host", "la_noncausal_fwd", "la_noncausal_bwd", "la_causal_fwd",
               "la_causal_fwd_with_state", "la_causal_bwd", "la_causal_bwd_after_fwd", "la_recurrent_step",
               "la_retention_fwd", "la_retention_step", "la_gated_delta_fwd", "la_gated_delta_bwd",
               "la_gated_delta_bwd_with_state", "la_gated_delta_step", "la_layer_norm_fwd", "la_layer_norm_bwd",
-              "la_cross_fwd", "la_cross_bwd", "la_cross_apply", "la_selftest_bounded_wait", "la_selftest_lookback_timeout", "la_last_error", "la_causal_fwd_fused",
+              "la_cross_fwd", "la_cross_bwd", "la_cross_apply", "la_gated_norm_fwd", "la_gated_norm_bwd",
+              "la_residual_norm_fwd", "la_residual_norm_bwd", "la_selftest_bounded_wait", "la_selftest_lookback_timeout", "la_last_error", "la_causal_fwd_fused",
               "la_clear_error", "la_timing_enable", "la_timing_reset"):
         getattr(lib, f).restype = ctypes.c_int
     lib.la_last_error.argtypes = []
@@ -727,6 +743,152 @@ def layer_norm_bwd(x, weight, mean, rstd, dout, dx=None, dweight=None, dbias=Non
     _check(lib.la_layer_norm_bwd(_p(x), _p(weight), _p(mean), _p(rstd), _p(dout), _p(dx), _p(dweight), _p(dbias), s,
                                  _p(ws), nb, _stream_ptr(stream)), "la_layer_norm_bwd")
     return dx, dweight, dbias
+
+
+def _sums_workspace(need, device, workspace, stream):
+    """The workspace of a norm's sums over rows: the caller's, or one of need() bytes."""
+    if workspace is not None:
+        if not workspace.is_cuda:
+            raise ValueError("workspace must be a device tensor")
+        return workspace, workspace.numel() * workspace.element_size()
+    nb = int(need())
+    return (_scratch(nb, device, stream), nb) if nb else (None, 0)
+
+
+def _gated_args(o, gate, weight):
+    _need_cuda(o, gate)
+    os_, dt = o.shape, o.dtype
+    code = _DTYPE_CODE.get(dt)
+    if code is None:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dt)
+    if len(os_) != 4 or gate.dtype != dt or gate.shape not in ((os_[0], os_[2], os_[1] * os_[3]), (os_[0], os_[2], os_[1], os_[3])):
+        raise ValueError("expected o [B,H,N,D] and gate [B,N,H*D] or [B,N,H,D] of one dtype; got %s %s" %
+                         (tuple(os_), tuple(gate.shape)))
+    if weight is not None:
+        _need_cuda(weight)
+        if weight.shape != os_[3:] or weight.dtype != dt:
+            raise ValueError("weight must be [D] of the dtype of o")
+    return HeadsShape(os_[0], os_[1], os_[2], os_[3], code)
+
+
+def gated_norm_fwd(o, gate, weight=None, rms=False, eps=1e-5, out=None, stream=None):
+    """The norm of each head's output with its gate, heads merged: y[b,n,h] = norm(o[b,h,n]) weight silu(gate[b,n,h]).
+
+    o [B,H,N,D]; gate and the result [B,N,H*D] (or [B,N,H,D]); weight [D] of o's dtype, or None (1).  norm is layer
+    norm or, with rms, division by the root of the mean square.
+    """
+    s = _gated_args(o, gate, weight)
+    out = _result(out, gate, "out", stream)
+    _check(library().la_gated_norm_fwd(_p(o), _p(gate), _p(weight), _p(out), s, int(rms), eps, _stream_ptr(stream)),
+           "la_gated_norm_fwd")
+    return out
+
+
+def gated_norm_workspace_bytes(B: int, H: int, N: int, D: int, dtype: torch.dtype) -> int:
+    if dtype not in _DTYPE_CODE:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dtype)
+    return int(library().la_gated_norm_workspace_bytes(HeadsShape(B, H, N, D, _DTYPE_CODE[dtype])))
+
+
+def gated_norm_bwd(o, gate, weight, dout, rms=False, eps=1e-5, dx=None, dgate=None, dweight=None, workspace=None, stream=None):
+    """Gradients (of o, gate, weight) of gated_norm_fwd for upstream gradient dout.  With weight None (1) the last is formed
+    where the caller gives the tensor that receives it, else None."""
+    s = _gated_args(o, gate, weight)
+    _need_cuda(dout)
+    if dout.shape != gate.shape or dout.dtype != o.dtype:
+        raise ValueError("dout must match gate in shape and dtype")
+    dx = _result(dx, o, "dx", stream)
+    dgate = _result(dgate, gate, "dgate", stream)
+    if weight is not None:
+        dweight = _result(dweight, weight, "dweight", stream)
+    elif dweight is not None:
+        _need_cuda(dweight)
+        if dweight.shape != o.shape[3:] or dweight.dtype != o.dtype:
+            raise ValueError("dweight must be [D] of the dtype of o")
+    ws, nb = None, 0
+    if dweight is not None:
+        ws, nb = _sums_workspace(lambda: library().la_gated_norm_workspace_bytes(s), o.device, workspace, stream)
+    _check(library().la_gated_norm_bwd(_p(o), _p(gate), _p(weight), _p(dout), _p(dx), _p(dgate), _p(dweight), s, int(rms), eps,
+                                       _p(ws), nb, _stream_ptr(stream)), "la_gated_norm_bwd")
+    return dx, dgate, dweight
+
+
+def residual_norm_fwd(x, a, scale=None, weight=None, bias=None, rms=False, eps=1e-5, h=None, out=None, stream=None,
+                      return_stats=False):
+    """The residual sum and the norm after it: h = x + scale a, y = norm(h) weight + bias over the last dimension; returns (h, y).
+
+    scale, weight and bias are [C] of x's dtype, or None (1, 1 and 0); norm is layer norm or, with rms, division by the root of
+    the mean square.  With return_stats, returns (h, y, mean, rstd): the fp32 statistics of shape x.shape[:-1] that
+    residual_norm_bwd takes (mean is None with rms).
+    """
+    s = _norm_args(x, scale, weight, bias)
+    _need_cuda(a)
+    if a.shape != x.shape or a.dtype != x.dtype:
+        raise ValueError("a must match x in shape and dtype")
+    h = _result(h, x, "h", stream)
+    out = _result(out, x, "out", stream)
+    mean = rstd = None
+    if return_stats:
+        rstd = _new_f32(x.shape[:-1], x.device, stream)
+        mean = None if rms else _new_f32(x.shape[:-1], x.device, stream)
+    _check(library().la_residual_norm_fwd(_p(x), _p(a), _p(scale), _p(weight), _p(bias), _p(h), _p(out), _p(mean), _p(rstd), s,
+                                          int(rms), eps, _stream_ptr(stream)), "la_residual_norm_fwd")
+    return (h, out, mean, rstd) if return_stats else (h, out)
+
+
+def residual_norm_workspace_bytes(rows: int, C: int, dtype: torch.dtype) -> int:
+    if dtype not in _DTYPE_CODE:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dtype)
+    return int(library().la_residual_norm_workspace_bytes(NormShape(rows, C, _DTYPE_CODE[dtype])))
+
+
+def residual_norm_bwd(h, a, scale, weight, mean, rstd, dy, dh=None, rms=False, dx=None, da=None, dscale=None, dweight=None,
+                      dbias=None, workspace=None, stream=None):
+    """Gradients (dx, da, dscale, dweight, dbias) of residual_norm_fwd for the gradients dy of its norm and dh of its sum
+    (None: zero), from the sum h and the statistics.
+
+    Without a scale, da is dx itself (one tensor) and dscale None, and a may be None.  With weight None (1), dweight and dbias
+    are formed where the caller gives the tensor that receives them, else None.
+    """
+    s = _norm_args(h, scale, weight)
+    _need_cuda(rstd, dy)
+    if dy.shape != h.shape or dy.dtype != h.dtype:
+        raise ValueError("dy must match h in shape and dtype")
+    for t, what in ((dh, "dh"), (a, "a")):
+        if t is not None:
+            _need_cuda(t)
+            if t.shape != h.shape or t.dtype != h.dtype:
+                raise ValueError("%s must match h in shape and dtype" % what)
+    stats = h.shape[:-1]
+    if not rms:
+        _need_cuda(mean)
+    if rstd.dtype != torch.float32 or rstd.shape != stats or \
+            (not rms and (mean.dtype != torch.float32 or mean.shape != stats)):
+        raise ValueError("mean and rstd must be fp32 of shape h.shape[:-1]")
+    dx = _result(dx, h, "dx", stream)
+    if scale is not None:
+        if a is None:
+            raise ValueError("a is needed for the gradient of the scale")
+        da = _result(da, h, "da", stream)
+        dscale = _result(dscale, scale, "dscale", stream)
+    elif da is not None or dscale is not None:
+        raise ValueError("without a scale there is no dscale, and da is dx")
+    if weight is not None:
+        dweight = _result(dweight, weight, "dweight", stream)
+        dbias = _result(dbias, weight, "dbias", stream)
+    else:
+        for t, what in ((dweight, "dweight"), (dbias, "dbias")):
+            if t is not None:
+                _need_cuda(t)
+                if t.shape != h.shape[-1:] or t.dtype != h.dtype:
+                    raise ValueError("%s must be %s of shape %s" % (what, h.dtype, tuple(h.shape[-1:])))
+    ws, nb = None, 0
+    if dscale is not None or dweight is not None or dbias is not None:
+        ws, nb = _sums_workspace(lambda: library().la_residual_norm_workspace_bytes(s), h.device, workspace, stream)
+    _check(library().la_residual_norm_bwd(_p(h), _p(a), _p(scale), _p(weight), None if rms else _p(mean), _p(rstd), _p(dy),
+                                          _p(dh), _p(dx), _p(da), _p(dscale), _p(dweight), _p(dbias), s, int(rms), _p(ws), nb,
+                                          _stream_ptr(stream)), "la_residual_norm_bwd")
+    return dx, dx if scale is None else da, dscale, dweight, dbias
 
 
 def selftest_bounded_wait(stream=None):

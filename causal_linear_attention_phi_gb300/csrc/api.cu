@@ -9,6 +9,7 @@
 #include <string>
 #include <vector>
 
+#include "block_norm.cuh"
 #include "cross.cuh"
 #include "gated_delta.cuh"
 #include "la_internal.cuh"
@@ -909,6 +910,116 @@ la_status la_layer_norm_bwd(const void* x, const void* w, const float* mean, con
                        "layer norm backward");
 }
 
+static la_status check_heads(const la_heads_shape& s, float eps) {
+    LA_TRY(check_shape(la_shape{s.B, s.H, s.N, s.D, s.D, s.dtype}));
+    if (!(eps >= 0.f)) return fail(LA_ERR_INVALID_ARG, "eps must not be negative");
+    return LA_OK;
+}
+static bool no_rows(const la_heads_shape& s) { return s.B == 0 || s.H == 0 || s.N == 0; }
+static bn::Gated gated_of(const la_heads_shape& s, int rms, float eps) {
+    return bn::Gated{(long long)s.B * s.N, s.N, s.H, s.D, s.dtype, rms != 0, eps};
+}
+
+la_status la_gated_norm_fwd(const void* o, const void* gate, const void* w, void* y, la_heads_shape s, int rms, float eps,
+                            la_stream_t stream) {
+    t_detail.clear();
+    LA_TRY(check_heads(s, eps));
+    if (no_rows(s)) return LA_OK;
+    LA_TRY(check_device());
+    LA_TRY(check_ptr(o, "o"));
+    LA_TRY(check_ptr(gate, "gate"));
+    if (w) LA_TRY(check_ptr(w, "w"));
+    LA_TRY(check_ptr(y, "y"));
+    return cuda_status(bn::gated_fwd(o, gate, w, y, gated_of(s, rms, eps), reinterpret_cast<cudaStream_t>(stream)),
+                       "gated norm forward");
+}
+
+size_t la_gated_norm_workspace_bytes(la_heads_shape s) {
+    if (check_heads(s, 0.f) != LA_OK || no_rows(s)) return 0;
+    return align256(bn::gated_bwd_bytes(gated_of(s, 0, 0.f)));
+}
+
+la_status la_gated_norm_bwd(const void* o, const void* gate, const void* w, const void* dy, void* dx, void* dgate, void* dw,
+                            la_heads_shape s, int rms, float eps, void* ws, size_t ws_bytes, la_stream_t stream) {
+    t_detail.clear();
+    LA_TRY(check_heads(s, eps));
+    if (no_rows(s) && !dw) return LA_OK;
+    LA_TRY(check_device());
+    if (dw) LA_TRY(check_ptr(dw, "dw"));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (no_rows(s))  // a sum over no row
+        return cuda_status(cudaMemsetAsync(dw, 0, (size_t)s.D * (s.dtype == LA_BF16 ? 2 : 4), st), "gradient clear");
+    LA_TRY(check_ptr(o, "o"));
+    LA_TRY(check_ptr(gate, "gate"));
+    if (w) LA_TRY(check_ptr(w, "w"));
+    LA_TRY(check_ptr(dy, "dy"));
+    LA_TRY(check_ptr(dx, "dx"));
+    LA_TRY(check_ptr(dgate, "dgate"));
+    if (dw) LA_TRY(check_ws(ws, ws_bytes, la_gated_norm_workspace_bytes(s)));
+    return cuda_status(bn::gated_bwd(o, gate, w, dy, dx, dgate, dw, gated_of(s, rms, eps), static_cast<char*>(ws), st),
+                       "gated norm backward");
+}
+
+la_status la_residual_norm_fwd(const void* x, const void* a, const void* scale, const void* w, const void* b, void* h,
+                               void* y, float* mean, float* rstd, la_norm_shape s, int rms, float eps, la_stream_t stream) {
+    t_detail.clear();
+    LA_TRY(check_norm(s));
+    if (!(eps >= 0.f)) return fail(LA_ERR_INVALID_ARG, "eps must not be negative");
+    if (s.rows == 0) return LA_OK;
+    LA_TRY(check_device());
+    LA_TRY(check_ptr(x, "x"));
+    LA_TRY(check_ptr(a, "a"));
+    if (scale) LA_TRY(check_ptr(scale, "scale"));
+    if (w) LA_TRY(check_ptr(w, "w"));
+    if (b) LA_TRY(check_ptr(b, "b"));
+    LA_TRY(check_ptr(h, "h"));
+    LA_TRY(check_ptr(y, "y"));
+    if (h == y) return fail(LA_ERR_INVALID_ARG, "h and y are one buffer");
+    if (mean) LA_TRY(check_ptr(mean, "mean", 4));
+    if (rstd) LA_TRY(check_ptr(rstd, "rstd", 4));
+    const bn::ResidFwd f{x, a, scale, w, b, h, y, mean, rstd};
+    return cuda_status(bn::resid_fwd(f, s, rms != 0, eps, reinterpret_cast<cudaStream_t>(stream)), "residual norm forward");
+}
+
+size_t la_residual_norm_workspace_bytes(la_norm_shape s) {
+    if (check_norm(s) != LA_OK || s.rows == 0) return 0;
+    return align256(bn::resid_bwd_bytes(s));
+}
+
+la_status la_residual_norm_bwd(const void* h, const void* a, const void* scale, const void* w, const float* mean,
+                               const float* rstd, const void* dy, const void* dh, void* dx, void* da, void* dscale,
+                               void* dw, void* db, la_norm_shape s, int rms, void* ws, size_t ws_bytes, la_stream_t stream) {
+    t_detail.clear();
+    LA_TRY(check_norm(s));
+    const bool sums = dscale || dw || db;
+    if (s.rows == 0 && !sums) return LA_OK;
+    LA_TRY(check_device());
+    void* const outs[3] = {dscale, dw, db};
+    const char* const names[3] = {"dscale", "dw", "db"};
+    for (int i = 0; i < 3; ++i)
+        if (outs[i]) LA_TRY(check_ptr(outs[i], names[i]));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (s.rows == 0) {  // sums over no row
+        for (void* p : outs)
+            if (p) LA_TRY(cuda_status(cudaMemsetAsync(p, 0, (size_t)s.C * (s.dtype == LA_BF16 ? 2 : 4), st), "gradient clear"));
+        return LA_OK;
+    }
+    LA_TRY(check_ptr(h, "h"));
+    if (dscale) LA_TRY(check_ptr(a, "a"));
+    if (scale) LA_TRY(check_ptr(scale, "scale"));
+    if (w) LA_TRY(check_ptr(w, "w"));
+    if (!rms) LA_TRY(check_ptr(mean, "mean", 4));
+    LA_TRY(check_ptr(rstd, "rstd", 4));
+    LA_TRY(check_ptr(dy, "dy"));
+    if (dh) LA_TRY(check_ptr(dh, "dh"));
+    LA_TRY(check_ptr(dx, "dx"));
+    if (da) LA_TRY(check_ptr(da, "da"));
+    if (dx == da) return fail(LA_ERR_INVALID_ARG, "dx and da are one buffer");
+    if (sums) LA_TRY(check_ws(ws, ws_bytes, la_residual_norm_workspace_bytes(s)));
+    const bn::ResidBwd g{h, a, scale, w, mean, rstd, dy, dh, dx, da, dscale, dw, db};
+    return cuda_status(bn::resid_bwd(g, s, rms != 0, static_cast<char*>(ws), st), "residual norm backward");
+}
+
 la_status la_last_error(void) {
     int v = 0;
     if (cudaMemcpyFromSymbol(&v, g_error_word, sizeof(int)) != cudaSuccess)
@@ -918,8 +1029,8 @@ la_status la_last_error(void) {
         unsigned site = 0;
         if (cudaMemcpyFromSymbol(&site, g_debug_site, sizeof(site)) == cudaSuccess) {
             static const char* const kFiles[] = {
-                "api.cu", "cross.cuh", "cross_simt.cu", "cross_step.cu", "decode.cu", "gated_delta.cu", "gated_delta.cuh", "gated_delta_step.cu", "host_step.cu",
-                "la_internal.cuh", "layer_norm.cu", "layer_norm.cuh", "noalloc.cu", "retention.cu", "selftest.cu",
+                "api.cu", "block_norm.cu", "block_norm.cuh", "cross.cuh", "cross_simt.cu", "cross_step.cu", "decode.cu", "gated_delta.cu", "gated_delta.cuh", "gated_delta_step.cu", "host_step.cu",
+                "la_internal.cuh", "layer_norm.cu", "layer_norm.cuh", "noalloc.cu", "norm_common.cuh", "retention.cu", "selftest.cu",
                 "shared_memory.cuh", "simt_common.cuh", "simt_kernels.cu", "sm100.cuh", "tc_apply.cu", "tc_bwd.cu",
                 "tc_common.cuh", "tc_fwd.cu", "tc_gated_delta.cu", "tc_gated_delta.cuh", "tc_gated_delta_bwd.cu",
                 "tc_gated_delta_states.cuh", "tc_noncausal_bwd.cu", "tc_retention.cu"};

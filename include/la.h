@@ -410,6 +410,55 @@ la_status la_layer_norm_bwd(const void* x, const void* w, const float* mean, con
                             void* ws, size_t ws_bytes, la_stream_t stream);
 
 /*
+ * The norm after a block of heads, fused with its gate and with the merge of the heads:
+ *   y[b,n,h,:] = norm(o[b,h,n,:]) w * silu(gate[b,n,h,:]),  silu(x) = x / (1 + exp(-x)),
+ * norm over the D elements of a head: (x - mean) rstd, or with rms != 0 x rstd with rstd = 1 / sqrt(mean of x^2 + eps).
+ * o: [B,H,N,D]; gate, y: [B,N,H,D], i.e. [B,N,H*D]; w: [D], NULL for 1; all in s.dtype, 16-byte aligned.  y may be gate.
+ * D is 16, 32, 64 or 128, B*H <= 65535, B*H*N*D < 2^40.  No workspace.
+ */
+typedef struct {
+    int B, H, N, D;
+    int dtype;
+} la_heads_shape;
+
+la_status la_gated_norm_fwd(const void* o, const void* gate, const void* w, void* y, la_heads_shape s, int rms, float eps,
+                            la_stream_t stream);
+
+/*
+ * Its gradient for dy = dL/dy; the statistics are formed again from o.  dx = dL/do: [B,H,N,D]; dgate: [B,N,H,D]; dw: [D],
+ * NULL if not wanted; all in s.dtype and written (dw = 0 where there are no rows).  dx may be o, dgate may be gate or dy.
+ * Sums over rows are fp32 in a fixed order.  Workspace: la_gated_norm_workspace_bytes(s), needed where dw is wanted.
+ */
+size_t la_gated_norm_workspace_bytes(la_heads_shape s);
+la_status la_gated_norm_bwd(const void* o, const void* gate, const void* w, const void* dy, void* dx, void* dgate, void* dw,
+                            la_heads_shape s, int rms, float eps, void* ws, size_t ws_bytes, la_stream_t stream);
+
+/*
+ * The norm before a block, fused with the residual sum before it and its scale, over rows of a dense [rows, C] array:
+ *   h = x + scale * a,  y = norm(h) w + b
+ * with norm over the C elements of a row as above (layer norm, or rms != 0).  y is formed from h before h is rounded.
+ * x, a, h, y: [rows, C]; scale, w, b: [C], each may be NULL (1, 1 and 0); all in s.dtype, 16-byte aligned.  mean, rstd:
+ * NULL, or DEVICE fp32 [rows] that receive the statistics (mean: 0 with rms).  h may be x or a, y may be x or a, not both one.
+ * rows and C as for la_layer_norm_fwd.  No workspace.
+ */
+la_status la_residual_norm_fwd(const void* x, const void* a, const void* scale, const void* w, const void* b, void* h,
+                               void* y, float* mean, float* rstd, la_norm_shape s, int rms, float eps, la_stream_t stream);
+
+/*
+ * Its gradient for dy = dL/dy and dh = dL/dh (NULL: 0), from h and the saved statistics.  With n = (h - mean) rstd and d = dy w:
+ *   dx = dh + rstd (d - n mean(d n) - mean(d)),  da = scale * dx,  dscale = sum over rows of a * dx,
+ *   dw = sum over rows of dy n,  db = sum over rows of dy;   without the last mean and with n = h rstd where rms != 0.
+ * a is read for dscale only and may be NULL without it; mean is not read with rms.  da may be NULL (without a scale it is dx);
+ * dscale, dw, db: [C] in s.dtype, each may be NULL (not wanted).  dx may be h, dy or dh, da may be a, dy or dh, not both one.
+ * Sums over rows are fp32 in a fixed order; for rows = 0 they are zero.  Workspace: la_residual_norm_workspace_bytes(s),
+ * needed where one of them is wanted.
+ */
+size_t la_residual_norm_workspace_bytes(la_norm_shape s);
+la_status la_residual_norm_bwd(const void* h, const void* a, const void* scale, const void* w, const float* mean,
+                               const float* rstd, const void* dy, const void* dh, void* dx, void* da, void* dscale,
+                               void* dw, void* db, la_norm_shape s, int rms, void* ws, size_t ws_bytes, la_stream_t stream);
+
+/*
  * la_causal_fwd with no workspace argument: the same causal forward, with its
  * scratch (the per-segment states) in a 16 MiB device array that the library
  * owns.  The pages have no counterpart to this call; it exists for callers

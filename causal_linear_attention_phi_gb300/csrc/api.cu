@@ -1032,7 +1032,7 @@ la_status la_last_error(void) {
                 "api.cu", "block_norm.cu", "block_norm.cuh", "cross.cuh", "cross_simt.cu", "cross_step.cu", "decode.cu", "gated_delta.cu", "gated_delta.cuh", "gated_delta_step.cu", "host_step.cu",
                 "la_internal.cuh", "layer_norm.cu", "layer_norm.cuh", "noalloc.cu", "norm_common.cuh", "retention.cu", "selftest.cu",
                 "shared_memory.cuh", "simt_common.cuh", "simt_kernels.cu", "sm100.cuh", "tc_apply.cu", "tc_bwd.cu",
-                "tc_common.cuh", "tc_fwd.cu", "tc_gated_delta.cu", "tc_gated_delta.cuh", "tc_gated_delta_bwd.cu",
+                "tc_common.cuh", "tc_cross.cu", "tc_cross.cuh", "tc_cross_bwd.cu", "tc_fwd.cu", "tc_gated_delta.cu", "tc_gated_delta.cuh", "tc_gated_delta_bwd.cu",
                 "tc_gated_delta_states.cuh", "tc_noncausal_bwd.cu", "tc_retention.cu"};
             const char* file = "unknown file";
             for (const char* f : kFiles)

@@ -156,6 +156,8 @@ cudaError_t tc_fwd(const FwdArgs& a, const la_cross_shape& s, char* ws, cudaStre
 cudaError_t tc_bwd(const BwdArgs& a, const la_cross_shape& s, char* ws, cudaStream_t st);
 cudaError_t tc_apply(const void* q, const float* S, const float* z, void* o, const la_cross_shape& s, char* ws,
                      cudaStream_t st);
+// dk and dv of the rows behind the lengths, which are 0.
+cudaError_t clear_behind(void* dk, void* dv, const Rows& keys, const la_cross_shape& s, cudaStream_t st);
 // A few rows of queries to a state: each state is read once, into registers.
 cudaError_t apply_few(const void* q, const float* S, const float* z, void* o, const la_cross_shape& s, cudaStream_t st);
 

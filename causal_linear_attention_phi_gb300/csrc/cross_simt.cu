@@ -31,11 +31,6 @@ __device__ __forceinline__ void load_cols(const float* row, int tx, float (&v)[W
         v[0] = row[tx];
     }
 }
-template <int W, typename T>
-__device__ __forceinline__ void store_cols(T* row, int tx, const float (&v)[W]) {
-#pragma unroll
-    for (int x = 0; x < W; ++x) row[col_of<W>(tx, x)] = from_f32<T>(v[x]);
-}
 template <int W>
 __device__ __forceinline__ void store_cols(float* row, int tx, const float (&v)[W]) {
     if constexpr (W >= 4) {
@@ -48,24 +43,17 @@ __device__ __forceinline__ void store_cols(float* row, int tx, const float (&v)[
     }
 }
 
-// Rows [0, n) of a chunk as fp32 (phi applied if asked), the rest of its 64 rows 0.  src: the chunk's first row.
-template <typename T, int D, bool kPhi>
-__device__ __forceinline__ void load_rows(float* dst, const T* __restrict__ src, int n) {
-    constexpr int V = 16 / (int)sizeof(T);
+// Rows [0, n) of a chunk (phi applied if asked), the rest of its 64 rows 0.  src: the chunk's first row.
+template <int D, bool kPhi>
+__device__ __forceinline__ void load_rows(float* dst, const float* __restrict__ src, int n) {
 #pragma unroll 4
-    for (int x = threadIdx.x; x < kChunk * D / V; x += kThreads) {
-        const bool in = x * V < n * D;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (in) w = reinterpret_cast<const uint4*>(src)[x];
-        const T* e = reinterpret_cast<const T*>(&w);
-        float f[V];
-#pragma unroll
-        for (int y = 0; y < V; ++y) {
-            f[y] = to_f32(e[y]);
-            if (kPhi) f[y] = in ? phi_f(f[y]) : 0.f;
+    for (int x = threadIdx.x; x < kChunk * D / 4; x += kThreads) {
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (4 * x < n * D) {
+            f = reinterpret_cast<const float4*>(src)[x];
+            if (kPhi) f = make_float4(phi_f(f.x), phi_f(f.y), phi_f(f.z), phi_f(f.w));
         }
-#pragma unroll
-        for (int y = 0; y < V; y += 4) *reinterpret_cast<float4*>(dst + x * V + y) = make_float4(f[y], f[y + 1], f[y + 2], f[y + 3]);
+        reinterpret_cast<float4*>(dst)[x] = f;
     }
 }
 
@@ -134,9 +122,9 @@ __device__ __forceinline__ Span shared_span(const Rows& r, int chunk, bool dead)
 }
 
 // ------------------------------------------------------------------ sums over the keys
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads)
-cross_sums_kernel(const T* __restrict__ k, const T* __restrict__ v, float* __restrict__ rec, Rows keys, int slots) {
+cross_sums_kernel(const float* __restrict__ k, const float* __restrict__ v, float* __restrict__ rec, Rows keys, int slots) {
     extern __shared__ __align__(16) float sm[];
     float *ks = sm, *vs = sm + kChunk * DK;
     pdl_enter();  // launched with programmatic dependent launch
@@ -151,8 +139,8 @@ cross_sums_kernel(const T* __restrict__ k, const T* __restrict__ v, float* __res
         const size_t row = (size_t)w.bh * keys.M + w.row0();
         LA_DCHECK(w.bh < keys.heads() && w.row0() + w.rows() <= keys.M && w.rows() > 0);
         __syncthreads();
-        load_rows<T, DK, true>(ks, k + row * DK, w.rows());
-        load_rows<T, DV, false>(vs, v + row * DV, w.rows());
+        load_rows<DK, true>(ks, k + row * DK, w.rows());
+        load_rows<DV, false>(vs, v + row * DV, w.rows());
         __syncthreads();
         outer_sum<DK, DV>(ks, vs, acc, ty, tx);
         if (threadIdx.x < DK)
@@ -194,9 +182,9 @@ __device__ __forceinline__ void inverses(const float* ph, const float* zs, float
     if (part == 0) inv[r] = over(den);
 }
 
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads)
-cross_apply_kernel(const T* __restrict__ q, const float* __restrict__ S, const float* __restrict__ z, T* __restrict__ o,
+cross_apply_kernel(const float* __restrict__ q, const float* __restrict__ S, const float* __restrict__ z, float* __restrict__ o,
                    Rows rows) {
     extern __shared__ __align__(16) float sm[];
     float *Ss = sm, *ph = Ss + DK * DV, *zs = ph + kChunk * DK, *inv = zs + DK;
@@ -213,7 +201,7 @@ cross_apply_kernel(const T* __restrict__ q, const float* __restrict__ S, const f
         }
         const size_t row = (size_t)w.bh * rows.M + w.row0();
         LA_DCHECK(w.bh < rows.heads() && w.row0() + w.rows() <= rows.M && w.rows() > 0);
-        load_rows<T, DK, true>(ph, q + row * DK, w.rows());
+        load_rows<DK, true>(ph, q + row * DK, w.rows());
         __syncthreads();
         inverses<DK>(ph, zs, inv);
         float out[4][DV / 16];
@@ -231,10 +219,10 @@ cross_apply_kernel(const T* __restrict__ q, const float* __restrict__ S, const f
 }
 
 // dq and the head's records of (R, r).
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads)
-cross_query_kernel(const T* __restrict__ q, const T* __restrict__ dout, const float* __restrict__ S,
-                   const float* __restrict__ z, T* __restrict__ dq, float* __restrict__ rec, Rows rows, int slots) {
+cross_query_kernel(const float* __restrict__ q, const float* __restrict__ dout, const float* __restrict__ S,
+                   const float* __restrict__ z, float* __restrict__ dq, float* __restrict__ rec, Rows rows, int slots) {
     extern __shared__ __align__(16) float sm[];
     float *St = sm, *ph = St + DK * DV, *ds = ph + kChunk * DK, *zs = ds + kChunk * DV, *inv = zs + DK, *wr = inv + kChunk;
     pdl_enter();  // launched with programmatic dependent launch
@@ -254,8 +242,8 @@ cross_query_kernel(const T* __restrict__ q, const T* __restrict__ dout, const fl
         }
         const size_t row = (size_t)w.bh * rows.M + w.row0();
         LA_DCHECK(w.bh < rows.heads() && w.row0() + w.rows() <= rows.M && w.rows() > 0);
-        load_rows<T, DK, true>(ph, q + row * DK, w.rows());
-        load_rows<T, DV, false>(ds, dout + row * DV, w.rows());
+        load_rows<DK, true>(ph, q + row * DK, w.rows());
+        load_rows<DV, false>(ds, dout + row * DV, w.rows());
         __syncthreads();
         inverses<DK>(ph, zs, inv);
         __syncthreads();
@@ -292,15 +280,15 @@ cross_query_kernel(const T* __restrict__ q, const T* __restrict__ dout, const fl
 }
 
 // ------------------------------------------------------------------ gradients of the keys
-// The rows behind a head's length: dk = dv = 0.  Bytes [a, b) of a tensor of the head, 16-byte aligned.
+// `bytes` zero bytes, 16-byte aligned.
 __device__ __forceinline__ void zero_bytes(void* p, size_t bytes, int tid, int threads) {
     for (size_t x = tid; x < bytes / 16; x += threads) reinterpret_cast<uint4*>(p)[x] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads)
-cross_key_kernel(const T* __restrict__ k, const T* __restrict__ v, const float* __restrict__ R, const float* __restrict__ rz,
-                 T* __restrict__ dk, T* __restrict__ dv, Rows keys) {
+cross_key_kernel(const float* __restrict__ k, const float* __restrict__ v, const float* __restrict__ R, const float* __restrict__ rz,
+                 float* __restrict__ dk, float* __restrict__ dv, Rows keys) {
     extern __shared__ __align__(16) float sm[];
     float *Rs = sm, *Rt = Rs + DK * DV, *ks = Rt + DK * DV, *vs = ks + kChunk * DK, *rs = vs + kChunk * DV;
     pdl_enter();  // launched with programmatic dependent launch
@@ -319,8 +307,8 @@ cross_key_kernel(const T* __restrict__ k, const T* __restrict__ v, const float* 
         }
         const size_t row = (size_t)w.bh * keys.M + w.row0();
         LA_DCHECK(w.bh < keys.heads() && w.row0() + w.rows() <= keys.M && w.rows() > 0);
-        load_rows<T, DK, true>(ks, k + row * DK, w.rows());
-        load_rows<T, DV, false>(vs, v + row * DV, w.rows());
+        load_rows<DK, true>(ks, k + row * DK, w.rows());
+        load_rows<DV, false>(vs, v + row * DV, w.rows());
         __syncthreads();
         float out[4][DK / 16], ov[4][DV / 16], rc[DK / 16];
         rows_times<DV, DK>(vs, Rt, out, ty, tx);
@@ -341,16 +329,15 @@ cross_key_kernel(const T* __restrict__ k, const T* __restrict__ v, const float* 
     }
 }
 
-// The rows behind the lengths, [live, M) of every head.
-template <typename T>
+// The rows behind the lengths, [live, M) of every head; a row has k_bytes or v_bytes.
 __global__ void __launch_bounds__(256)
-cross_clear_kernel(T* __restrict__ dk, T* __restrict__ dv, Rows keys, int Dk, int Dv) {
+cross_clear_kernel(char* __restrict__ dk, char* __restrict__ dv, Rows keys, int k_bytes, int v_bytes) {
     pdl_enter();  // launched with programmatic dependent launch
     const int bh = blockIdx.y, live = keys.live(bh / keys.Hk);
     const size_t row = (size_t)bh * keys.M + live, n = keys.M - live;
     const int tid = blockIdx.x * 256 + threadIdx.x, all = gridDim.x * 256;
-    zero_bytes(dk + row * Dk, n * Dk * sizeof(T), tid, all);
-    zero_bytes(dv + row * Dv, n * Dv * sizeof(T), tid, all);
+    zero_bytes(dk + row * k_bytes, n * k_bytes, tid, all);
+    zero_bytes(dv + row * v_bytes, n * v_bytes, tid, all);
 }
 
 // ------------------------------------------------------------------ host
@@ -404,32 +391,32 @@ cudaError_t join(const float* rec, float* S, float* z, const Rows& rows, int cta
                s.Dk * s.Dv, s.Dk);
 }
 
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 cudaError_t sums(const void* k, const void* v, const Rows& keys, float* rec, float* S, float* z, const la_cross_shape& s,
                  cudaStream_t st) {
     const int ctas = key_blocks(s);
-    CR_TRY(run("cross_sums", cross_sums_kernel<T, DK, DV>, dim3(ctas), kChunk * (DK + DV) * 4, st, (const T*)k, (const T*)v, rec,
+    CR_TRY(run("cross_sums", cross_sums_kernel<DK, DV>, dim3(ctas), kChunk * (DK + DV) * 4, st, (const float*)k, (const float*)v, rec,
                keys, ctas + keys.heads()));
     return join(rec, S, z, keys, ctas, s, st);
 }
 
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 cudaError_t apply(const void* q, const float* S, const float* z, void* o, const la_cross_shape& s, cudaStream_t st) {
     const Rows rows = grouped_queries(s);
-    return run("cross_apply", cross_apply_kernel<T, DK, DV>, dim3(blocks_for(rows.heads(), rows.M, 2)),
-               (DK * DV + kChunk * DK + DK + kChunk) * 4, st, (const T*)q, S, z, (T*)o, rows);
+    return run("cross_apply", cross_apply_kernel<DK, DV>, dim3(blocks_for(rows.heads(), rows.M, 2)),
+               (DK * DV + kChunk * DK + DK + kChunk) * 4, st, (const float*)q, S, z, (float*)o, rows);
 }
 
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 cudaError_t fwd_t(const FwdArgs& a, const la_cross_shape& s, char* ws, cudaStream_t st) {
     const Layout l = layout(s, false);
     float *S = a.S ? a.S : reinterpret_cast<float*>(ws + l.S), *z = a.z ? a.z : reinterpret_cast<float*>(ws + l.z);
-    CR_TRY((sums<T, DK, DV>(a.k, a.v, key_rows(s, a.lens), reinterpret_cast<float*>(ws), S, z, s, st)));
+    CR_TRY((sums<DK, DV>(a.k, a.v, key_rows(s, a.lens), reinterpret_cast<float*>(ws), S, z, s, st)));
     if (s.N == 0) return cudaSuccess;
-    return apply<T, DK, DV>(a.q, S, z, a.o, s, st);
+    return apply<DK, DV>(a.q, S, z, a.o, s, st);
 }
 
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 cudaError_t bwd_t(const BwdArgs& a, const la_cross_shape& s, char* ws, cudaStream_t st) {
     const Layout l = layout(s, true);
     const Rows keys = key_rows(s, a.lens), rows = grouped_queries(s);
@@ -437,17 +424,16 @@ cudaError_t bwd_t(const BwdArgs& a, const la_cross_shape& s, char* ws, cudaStrea
     const float *S = a.S, *z = a.z;
     if (!S) {
         float *Sw = reinterpret_cast<float*>(ws + l.S), *zw = reinterpret_cast<float*>(ws + l.z);
-        CR_TRY((sums<T, DK, DV>(a.k, a.v, keys, rec, Sw, zw, s, st)));
+        CR_TRY((sums<DK, DV>(a.k, a.v, keys, rec, Sw, zw, s, st)));
         S = Sw, z = zw;
     }
     const int qc = query_blocks(s);
-    CR_TRY(run("cross_query", cross_query_kernel<T, DK, DV>, dim3(qc), (DK * DV + kChunk * (DK + DV) + DK + 2 * kChunk) * 4, st,
-               (const T*)a.q, (const T*)a.dout, S, z, (T*)a.dq, rec, rows, qc + rows.heads()));
+    CR_TRY(run("cross_query", cross_query_kernel<DK, DV>, dim3(qc), (DK * DV + kChunk * (DK + DV) + DK + 2 * kChunk) * 4, st,
+               (const float*)a.q, (const float*)a.dout, S, z, (float*)a.dq, rec, rows, qc + rows.heads()));
     CR_TRY(join(rec, R, r, rows, qc, s, st));
-    CR_TRY(run("cross_key", cross_key_kernel<T, DK, DV>, dim3(blocks_for(keys.heads(), s.M, 1)),
-               (2 * DK * DV + kChunk * (DK + DV) + DK) * 4, st, (const T*)a.k, (const T*)a.v, R, r, (T*)a.dk, (T*)a.dv, keys));
-    if (!a.lens) return cudaSuccess;
-    return run("cross_clear", cross_clear_kernel<T>, dim3(8, keys.heads()), 0, st, (T*)a.dk, (T*)a.dv, keys, s.Dk, s.Dv);
+    CR_TRY(run("cross_key", cross_key_kernel<DK, DV>, dim3(blocks_for(keys.heads(), s.M, 1)),
+               (2 * DK * DV + kChunk * (DK + DV) + DK) * 4, st, (const float*)a.k, (const float*)a.v, R, r, (float*)a.dk, (float*)a.dv, keys));
+    return a.lens ? clear_behind(a.dk, a.dv, keys, s, st) : cudaSuccess;
 }
 
 #define LA_SIZES(F) F(16, 16) F(16, 32) F(16, 64) F(16, 128) F(32, 16) F(32, 32) F(32, 64) F(32, 128) \
@@ -455,31 +441,30 @@ cudaError_t bwd_t(const BwdArgs& a, const la_cross_shape& s, char* ws, cudaStrea
 
 }  // namespace
 
-bool tc_ok(const la_cross_shape&) { return false; }
-size_t tc_bytes(const la_cross_shape&, int) { return 0; }
-cudaError_t tc_fwd(const FwdArgs&, const la_cross_shape&, char*, cudaStream_t) { return cudaErrorInvalidValue; }
-cudaError_t tc_bwd(const BwdArgs&, const la_cross_shape&, char*, cudaStream_t) { return cudaErrorInvalidValue; }
-cudaError_t tc_apply(const void*, const float*, const float*, void*, const la_cross_shape&, char*, cudaStream_t) { return cudaErrorInvalidValue; }
+cudaError_t clear_behind(void* dk, void* dv, const Rows& keys, const la_cross_shape& s, cudaStream_t st) {
+    const int elem = s.dtype == LA_BF16 ? 2 : 4;
+    return run("cross_clear", cross_clear_kernel, dim3(8, keys.heads()), 0, st, (char*)dk, (char*)dv, keys, s.Dk * elem, s.Dv * elem);
+}
 
 size_t simt_bytes(const la_cross_shape& s, int op) { return layout(s, op == LA_OP_CROSS_BWD).bytes; }
 
 cudaError_t simt_fwd(const FwdArgs& a, const la_cross_shape& s, char* ws, cudaStream_t st) {
 #define LA_GO(x, y) \
-    if (s.Dk == x && s.Dv == y) return s.dtype == LA_BF16 ? fwd_t<__nv_bfloat16, x, y>(a, s, ws, st) : fwd_t<float, x, y>(a, s, ws, st);
+    if (s.Dk == x && s.Dv == y) return fwd_t<x, y>(a, s, ws, st);
     LA_SIZES(LA_GO)
 #undef LA_GO
     return cudaErrorInvalidValue;
 }
 cudaError_t simt_bwd(const BwdArgs& a, const la_cross_shape& s, char* ws, cudaStream_t st) {
 #define LA_GO(x, y) \
-    if (s.Dk == x && s.Dv == y) return s.dtype == LA_BF16 ? bwd_t<__nv_bfloat16, x, y>(a, s, ws, st) : bwd_t<float, x, y>(a, s, ws, st);
+    if (s.Dk == x && s.Dv == y) return bwd_t<x, y>(a, s, ws, st);
     LA_SIZES(LA_GO)
 #undef LA_GO
     return cudaErrorInvalidValue;
 }
 cudaError_t simt_apply(const void* q, const float* S, const float* z, void* o, const la_cross_shape& s, cudaStream_t st) {
 #define LA_GO(x, y) \
-    if (s.Dk == x && s.Dv == y) return s.dtype == LA_BF16 ? apply<__nv_bfloat16, x, y>(q, S, z, o, s, st) : apply<float, x, y>(q, S, z, o, s, st);
+    if (s.Dk == x && s.Dv == y) return apply<x, y>(q, S, z, o, s, st);
     LA_SIZES(LA_GO)
 #undef LA_GO
     return cudaErrorInvalidValue;

@@ -1,0 +1,599 @@
+// tc_cross.cu -- tensor-core kernels of cross attention forward: the sums over the keys, their join, the queries' answers.
+//
+//   cross_sums_tc   S = phi(K)^T V and z = phi(K)^T 1 of each block's share of the keys      records
+//   cross_join_tc   a head's records added up in a fixed order                              image of (S, z)
+//   cross_apply_tc  o = phi(Q) S / (phi(Q) z)                                                outputs
+//
+// All three are bound by memory: a chunk of 128 rows of 128-wide q and o (or k and v) is 64 KB, 1.45 us of an SM's share of
+// the copy rate, against 0.35 us for its product.  What it takes to come near is loads in flight while the arithmetic of
+// earlier chunks goes on, so tiles come through rings of TMA stages, and two groups of four warps work on alternate
+// chunks, one waiting for its product while the other evaluates phi.  phi(k) enters the sums as two bf16 parts, so that S is
+// good to 2^-17 of its terms: dq in the gradient is a small difference of products with S.
+#include <cudaTypedefs.h>
+
+#include "tc_cross.cuh"
+
+namespace la {
+namespace cross {
+namespace {
+
+using tc::bf_hi;
+using tc::bf_lo;
+
+// ------------------------------------------------------------------ sums over the keys
+// A stage holds a chunk of 64 rows: K (phi's hi part in place), its lo part, V.  For KB = 1 hi and lo are the two 64-row
+// halves of one 128-row product; else they are two products.  Sums of a head alternate between two accumulators, so
+// that four warps write a head's record while the next head's sums are formed.
+constexpr int kSumThreads = 448;  // warp 0 TMA, 1 MMA, 2-9 two compute groups, 10-13 records
+
+template <int KB, int VB>
+struct SumSmem {
+    static constexpr int kTile = 8192;  // 64 rows of a block
+    static constexpr int kLo = KB * kTile, kV = 2 * KB * kTile, kStage = (2 * KB + VB) * kTile;
+    static constexpr int kStages = 196608 / kStage > 8 ? 8 : 196608 / kStage;
+    static constexpr int zpart = kStages * kStage;            // float[2][8][64 KB]
+    static constexpr int bars = zpart + 2 * 8 * 64 * KB * 4;
+    static constexpr int total = bars + 512;
+};
+
+template <int KB, int VB>
+__global__ void __launch_bounds__(kSumThreads, 1)
+cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, float* __restrict__ rec, Rows keys,
+              int Dk, int slots, int* err) {
+    using SM = SumSmem<KB, VB>;
+    constexpr int NS = SM::kStages, T = SM::kTile;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    struct Bars {
+        uint64_t full[8], ready[8], empty[8], acc_done[2], z_ready[2], flushed[2], final_mma;
+        uint32_t tmem;
+        Span span;
+    };
+    static_assert(sizeof(Bars) <= 512, "barriers");
+    Bars* bar = reinterpret_cast<Bars*>(smem + SM::bars);
+    LA_DCHECK((smem_u32(smem) & 1023) == 0);
+    float* zpart = reinterpret_cast<float*>(smem + SM::zpart);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 32) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&bar->full[s], 1);
+            mbar_init(&bar->ready[s], 128);
+            mbar_init(&bar->empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&bar->acc_done[a], 1);
+            mbar_init(&bar->z_ready[a], 8);
+            mbar_init(&bar->flushed[a], 128);
+        }
+        mbar_init(&bar->final_mma, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tmem_alloc(&bar->tmem, 128 * VB);
+        tmem_relinquish();
+    }
+    pdl_enter();  // launched with programmatic dependent launch
+    if (warp == 0) {
+        const Span sp = span_of(keys, kSumRows, false, blockIdx.x, gridDim.x);
+        if (lane == 0) bar->span = sp;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar->tmem;
+    Walk w(keys, kSumRows, bar->span);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            long long i = 0;
+            for (; w.more(); w.next(), ++i) {
+                const int s = (int)(i % NS);
+                if (!mbar_wait(&bar->empty[s], ((i / NS) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
+                uint8_t* st = smem + s * SM::kStage;
+                mbar_arrive_expect_tx(&bar->full[s], (KB + VB) * T);
+                check_copy(0, w.row0(), keys.M, w.bh, keys.heads());
+                for (int b = 0; b < KB; ++b) tma_load_3d(st + b * T, &tm_k, 64 * b, w.row0(), w.bh, &bar->full[s]);
+                for (int b = 0; b < VB; ++b) tma_load_3d(st + SM::kV + b * T, &tm_v, 64 * b, w.row0(), w.bh, &bar->full[s]);
+            }
+            mbar_drain(bar->full, NS, i, err, LA_ERR_TIMEOUT);  // no copy is left in flight
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t id = idesc_bf16_f32(128, 64 * VB, 1, 1);
+            long long i = 0;
+            int heads = 0;
+            bool first = true;
+            for (; w.more(); w.next(), ++i) {
+                const int s = (int)(i % NS), a = heads & 1;
+                if (!mbar_wait(&bar->ready[s], (i / NS) & 1, err, LA_ERR_TIMEOUT)) break;
+                if (first && !mbar_wait(&bar->flushed[a], ((heads >> 1) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem + s * SM::kStage), acc = tmem + 64 * VB * a;
+#pragma unroll
+                for (int kk = 0; kk < kSumRows / 16; ++kk) {
+                    mma_ss(acc, desc_mn(st, kk, T), desc_mn(st + SM::kV, kk, T), id, !first || kk > 0);
+                    if (KB == 2) mma_ss(acc, desc_mn(st + SM::kLo, kk, T), desc_mn(st + SM::kV, kk, T), id, 1);
+                }
+                mma_commit(&bar->empty[s]);
+                first = w.last();
+                if (first) {
+                    mma_commit(&bar->acc_done[a]);
+                    ++heads;
+                }
+            }
+            mma_commit(&bar->final_mma);  // every product is complete before the accumulators are given back
+            mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
+        }
+    } else if (warp < 10) {
+        const int group = (warp - 2) >> 2, ct = (tid - 64) & 127;
+        const int lc = (ct & 7) ^ ((ct >> 3) & 7), at = (ct >> 3) * 128 + (ct & 7) * 16;  // rows (ct >> 3) + 16 j
+        float zp[KB][8];
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) zp[b][e] = 0.f;
+        long long i = 0;
+        int heads = 0;
+        bool ok = true;
+        for (; w.more() && ok; w.next(), ++i) {
+            if ((i & 1) == group) {
+                const int s = (int)(i % NS), n = w.rows();
+                if (!(ok = warp_wait(&bar->full[s], (i / NS) & 1, err))) break;
+                uint8_t* st = smem + s * SM::kStage + at;
+#pragma unroll
+                for (int b = 0; b < KB; ++b) {
+                    const bool col = 64 * b + 8 * lc < Dk;
+                    uint4 x[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4*>(st + b * T + 2048 * j);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const bool in = col && (ct >> 3) + 16 * j < n;
+                        uint32_t* u = reinterpret_cast<uint32_t*>(&x[j]);
+                        uint4 l;
+                        uint32_t* ul = reinterpret_cast<uint32_t*>(&l);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float p0 = in ? phi_f(bf_lo(u[e])) : 0.f, p1 = in ? phi_f(bf_hi(u[e])) : 0.f;
+                            zp[b][2 * e] += p0;
+                            zp[b][2 * e + 1] += p1;
+                            split2(p0, p1, u[e], ul[e]);
+                        }
+                        *reinterpret_cast<uint4*>(st + b * T + 2048 * j) = x[j];
+                        *reinterpret_cast<uint4*>(st + SM::kLo + b * T + 2048 * j) = l;
+                    }
+                }
+                if (n < kSumRows) {  // what lies behind the length may be anything
+#pragma unroll
+                    for (int b = 0; b < VB; ++b)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if ((ct >> 3) + 16 * j >= n)
+                                *reinterpret_cast<uint4*>(st + SM::kV + b * T + 2048 * j) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&bar->ready[s]);
+            }
+            if (w.last()) {  // this group's part of the head's z: over the four lanes that share columns, by warp
+                const int a = heads & 1;
+                if (!(ok = warp_wait(&bar->flushed[a], ((heads >> 1) & 1) ^ 1, err))) break;
+                float* to = zpart + (a * 8 + warp - 2) * 64 * KB + 8 * lc;
+#pragma unroll
+                for (int b = 0; b < KB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float x = zp[b][e];
+                        x += __shfl_xor_sync(0xffffffffu, x, 9);
+                        x += __shfl_xor_sync(0xffffffffu, x, 18);
+                        if (lane < 8) to[64 * b + e] = x;
+                        zp[b][e] = 0.f;
+                    }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->z_ready[a]);
+                ++heads;
+            }
+        }
+    } else {
+        const int r = 32 * (warp & 3) + lane;
+        int heads = 0;
+        for (; w.more(); w.next()) {
+            if (!w.last()) continue;
+            const int a = heads & 1;
+            if (!warp_wait(&bar->acc_done[a], (heads >> 1) & 1, err) || !warp_wait(&bar->z_ready[a], (heads >> 1) & 1, err)) break;
+            tc_fence_after();
+            if (LA_DCHECK((int)blockIdx.x + w.bh < slots)) {
+                float* out = rec + (size_t)(blockIdx.x + w.bh) * record_floats(VB);
+                tc::tmem_row_to_global<64 * VB>(tmem + 64 * VB * a + ((uint32_t)(32 * (warp & 3)) << 16), out + (size_t)r * 64 * VB);
+                float z = 0.f;
+                if (r < 64 * KB)
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) z += zpart[(a * 8 + x) * 64 * KB + r];
+                out[128 * 64 * VB + r] = z;
+            }
+            tc_fence_before();
+            mbar_arrive(&bar->flushed[a]);
+            ++heads;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 128 * VB);
+    }
+}
+
+// ------------------------------------------------------------------ join
+// A head's records (or a caller's state) to its image.  8 threads share a 16-byte chunk of the image, taking every eighth record;
+// their sums are added in a fixed order.  The last block of a head does z.
+template <int KB, int VB>
+__global__ void __launch_bounds__(256)
+cross_join_tc(const float* __restrict__ rec, const float* __restrict__ S, const float* __restrict__ z, char* __restrict__ image,
+              float* __restrict__ S_out, float* __restrict__ z_out, Rows rows, int chunk, int ctas, int Dk, int Dv) {
+    constexpr int kChunks = 64 * KB * 8 * VB;
+    __shared__ float part[8][32][9];
+    pdl_enter();  // launched with programmatic dependent launch
+    const int bh = blockIdx.x, x = threadIdx.x & 31, lane8 = threadIdx.x >> 5;
+    const bool zs = blockIdx.y == kChunks / 32;
+    Range g{0, 0};
+    if (rec) g = records_of(rows, chunk, bh, ctas);
+    char* im = image + (size_t)bh * image_bytes(KB, VB);
+    if (zs) {
+        if (threadIdx.x < 64 * KB) {
+            const int d = threadIdx.x;
+            float a = 0.f;
+            if (!rec)
+                a = d < Dk ? z[(size_t)bh * Dk + d] : 0.f;
+            else
+                for (int c = g.first; c <= g.last; ++c) {
+                    const float* p = rec + (size_t)(c + bh) * record_floats(VB) + 128 * 64 * VB + d;
+                    a += KB == 1 ? p[0] + p[64] : p[0];
+                }
+            reinterpret_cast<float*>(im + 2 * image_part(KB, VB))[d] = a;
+            if (z_out && d < Dk) z_out[(size_t)bh * Dk + d] = a;
+        }
+        return;
+    }
+    // row d, columns c8 .. c8 + 7
+    const int at = blockIdx.y * 32 + x, d = at / (8 * VB), c8 = at % (8 * VB) * 8;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    auto add = [&](const float* p) {
+        const float4 f = *reinterpret_cast<const float4*>(p), h = *reinterpret_cast<const float4*>(p + 4);
+        v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w, v[4] += h.x, v[5] += h.y, v[6] += h.z, v[7] += h.w;
+    };
+    if (!rec) {
+        if (lane8 == 0 && d < Dk && c8 < Dv) add(S + ((size_t)bh * Dk + d) * Dv + c8);
+    } else {
+#pragma unroll 2
+        for (int c = g.first + lane8; c <= g.last; c += 8) {
+            const float* p = rec + (size_t)(c + bh) * record_floats(VB) + (size_t)d * 64 * VB + c8;
+            add(p);
+            if (KB == 1) add(p + 64 * 64 * VB);  // the sums of the lo parts
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) part[lane8][x][e] = v[e];
+        __syncthreads();
+        if (lane8 == 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[e] = 0.f;
+#pragma unroll
+                for (int l = 0; l < 8; ++l) v[e] += part[l][x][e];
+            }
+        }
+    }
+    if (lane8 != 0) return;
+    uint4 hi, lo;
+    split2(v[0], v[1], hi.x, lo.x);
+    split2(v[2], v[3], hi.y, lo.y);
+    split2(v[4], v[5], hi.z, lo.z);
+    split2(v[6], v[7], hi.w, lo.w);
+    const int off = (c8 >> 6) * (64 * KB * 128) + swz(d, c8 >> 3);
+    *reinterpret_cast<uint4*>(im + off) = hi;
+    *reinterpret_cast<uint4*>(im + image_part(KB, VB) + off) = lo;
+    if (S_out && d < Dk && c8 < Dv) {
+        float* to = S_out + ((size_t)bh * Dk + d) * Dv + c8;
+        *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+// ------------------------------------------------------------------ the queries' answers
+// A stage holds a chunk of 128 queries: phi(Q) in place for the product, then the outputs for their store.  A thread owns
+// a row.  S (its hi part) and z of the next head are copied while this head's chunks are worked on.
+constexpr int kApplyThreads = 352;  // warp 0 TMA loads, 1 MMA, 2-9 two compute groups, 10 TMA stores
+
+template <int KB, int VB>
+struct ApplySmem {
+    static constexpr int kTile = 16384;  // 128 rows of a block
+    static constexpr int kS = (int)image_part(KB, VB), kStage = (KB > VB ? KB : VB) * kTile;
+    static constexpr int kStages = (229376 - 2 * kS) / kStage > 6 ? 6 : (229376 - 2 * kS) / kStage;
+    static constexpr int S0 = kStages * kStage;     // two
+    static constexpr int z0 = S0 + 2 * kS;          // float[2][64 KB]
+    static constexpr int bars = z0 + 2 * 256 * KB;
+    static constexpr int total = bars + 512;
+};
+
+template <int KB, int VB>
+__global__ void __launch_bounds__(kApplyThreads, 1)
+cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_o, const char* __restrict__ image,
+               Rows rows, int* err) {
+    using SM = ApplySmem<KB, VB>;
+    constexpr int NS = SM::kStages, T = SM::kTile;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    struct Bars {
+        uint64_t full[6], empty[6], staged[6], s_full[2], s_empty[2], ready[2], done[2], final_mma;
+        uint32_t tmem;
+        Span span;
+    };
+    static_assert(sizeof(Bars) <= 512, "barriers");
+    Bars* bar = reinterpret_cast<Bars*>(smem + SM::bars);
+    LA_DCHECK((smem_u32(smem) & 1023) == 0);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 32) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&bar->full[s], 1);
+            mbar_init(&bar->empty[s], 1);
+            mbar_init(&bar->staged[s], 128);
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(&bar->s_full[g], 1);
+            mbar_init(&bar->s_empty[g], 1);
+            mbar_init(&bar->ready[g], 128);
+            mbar_init(&bar->done[g], 1);
+        }
+        mbar_init(&bar->final_mma, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_o);
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tmem_alloc(&bar->tmem, 128 * VB);
+        tmem_relinquish();
+    }
+    pdl_enter();  // launched with programmatic dependent launch
+    if (warp == 0) {
+        const Span sp = span_of(rows, kRowChunk, false, blockIdx.x, gridDim.x);
+        if (lane == 0) bar->span = sp;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar->tmem;
+    Walk w(rows, kRowChunk, bar->span);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            long long i = 0, heads = 0;
+            bool first = true;
+            for (; w.more(); w.next(), ++i) {
+                if (first) {
+                    const int h = (int)(heads & 1);
+                    if (!mbar_wait(&bar->s_empty[h], ((heads >> 1) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
+                    const char* im = image + (size_t)w.bh * image_bytes(KB, VB);
+                    mbar_arrive_expect_tx(&bar->s_full[h], SM::kS + 256 * KB);
+                    bulk_load(smem + SM::S0 + h * SM::kS, im, SM::kS, &bar->s_full[h]);
+                    bulk_load(smem + SM::z0 + h * 256 * KB, im + 2 * image_part(KB, VB), 256 * KB, &bar->s_full[h]);
+                    ++heads;
+                }
+                first = w.last();
+                const int s = (int)(i % NS);
+                if (!mbar_wait(&bar->empty[s], ((i / NS) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
+                mbar_arrive_expect_tx(&bar->full[s], KB * T);
+                check_copy(0, w.row0(), rows.M, w.bh, rows.heads());
+                for (int b = 0; b < KB; ++b) tma_load_3d(smem + s * SM::kStage + b * T, &tm_q, 64 * b, w.row0(), w.bh, &bar->full[s]);
+            }
+            mbar_drain(bar->full, NS, i, err, LA_ERR_TIMEOUT);  // no copy is left in flight
+            mbar_drain(bar->s_full, 2, heads, err, LA_ERR_TIMEOUT);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t id = idesc_bf16_f32(128, 64 * VB, 0, 1);
+            long long i = 0, heads = 0;
+            bool first = true;
+            for (; w.more(); w.next(), ++i) {
+                const int g = (int)(i & 1), s = (int)(i % NS);
+                if (first) ++heads;
+                const int h = (int)((heads - 1) & 1);
+                if (first && !mbar_wait(&bar->s_full[h], ((heads - 1) >> 1) & 1, err, LA_ERR_TIMEOUT)) break;
+                // phi(Q) is in place, and the group has read the outputs of its previous chunk
+                if (!mbar_wait(&bar->ready[g], (i >> 1) & 1, err, LA_ERR_TIMEOUT)) break;
+                tc_fence_after();
+                const uint32_t aQ = smem_u32(smem + s * SM::kStage), aS = smem_u32(smem + SM::S0 + h * SM::kS);
+#pragma unroll
+                for (int kk = 0; kk < 4 * KB; ++kk)
+                    mma_ss(tmem + 64 * VB * g, desc_k(aQ, kk, T), desc_mn(aS, kk, 8192 * KB), id, kk > 0);
+                mma_commit(&bar->done[g]);
+                first = w.last();
+                if (first) mma_commit(&bar->s_empty[h]);
+            }
+            mma_commit(&bar->final_mma);  // every product is complete before the accumulators are given back
+            mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
+        }
+    } else if (warp < 10) {
+        const int g = (warp - 2) >> 2, r = 32 * (warp & 3) + lane;
+        const uint32_t acc = tmem + 64 * VB * g + ((uint32_t)(32 * (warp & 3)) << 16);
+        long long i = 0, heads = 0;
+        bool first = true;
+        for (; w.more(); w.next(), ++i) {
+            if (first) ++heads;
+            first = w.last();
+            if ((i & 1) != g) continue;
+            const int s = (int)(i % NS), h = (int)((heads - 1) & 1);
+            uint8_t* st = smem + s * SM::kStage;
+            const float* zs = reinterpret_cast<const float*>(smem + SM::z0 + h * 256 * KB);
+            if (!warp_wait(&bar->s_full[h], ((heads - 1) >> 1) & 1, err) || !warp_wait(&bar->full[s], (i / NS) & 1, err)) break;
+            float den = 0.f;
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+#pragma unroll
+                for (int lc = 0; lc < 8; ++lc) {
+                    uint4* p = reinterpret_cast<uint4*>(st + b * T + swz(r, lc));
+                    uint4 x = *p;
+                    uint32_t* u = reinterpret_cast<uint32_t*>(&x);
+                    const float4 za = *reinterpret_cast<const float4*>(zs + 64 * b + 8 * lc);
+                    const float4 zb = *reinterpret_cast<const float4*>(zs + 64 * b + 8 * lc + 4);
+                    const float zv[8] = {za.x, za.y, za.z, za.w, zb.x, zb.y, zb.z, zb.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        u[e] = pack_bf16x2(phi_f(bf_lo(u[e])), phi_f(bf_hi(u[e])));
+                        den = fmaf(bf_lo(u[e]), zv[2 * e], den);  // of the rounded phi, as the product has it
+                        den = fmaf(bf_hi(u[e]), zv[2 * e + 1], den);
+                    }
+                    *p = x;
+                }
+            }
+            const float inv = over(den);
+            fence_proxy_async_smem();
+            tc_fence_before();
+            mbar_arrive(&bar->ready[g]);
+            if (!warp_wait(&bar->done[g], (i >> 1) & 1, err)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 2 * VB; ++b) {
+                uint32_t o[32];
+                tmem_ld32(acc + 32 * b, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint4 x;
+                    uint32_t* u = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        u[e] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]) * inv, __uint_as_float(o[8 * c + 2 * e + 1]) * inv);
+                    *reinterpret_cast<uint4*>(st + (b >> 1) * T + swz(r, 4 * (b & 1) + c)) = x;
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&bar->staged[s]);
+        }
+    } else if (lane == 0) {
+        // stores: a stage is empty once its outputs have been read
+        for (long long i = 0; w.more(); w.next(), ++i) {
+            const int s = (int)(i % NS);
+            if (!mbar_wait(&bar->staged[s], (i / NS) & 1, err, LA_ERR_TIMEOUT)) break;
+            check_copy(0, w.row0(), rows.M, w.bh, rows.heads());
+            for (int b = 0; b < VB; ++b) tma_store_3d(&tm_o, smem + s * SM::kStage + b * T, 64 * b, w.row0(), w.bh);
+            bulk_commit();
+            bulk_wait_read_all();
+            mbar_arrive(&bar->empty[s]);
+        }
+        bulk_wait_all();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 128 * VB);
+    }
+}
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+constexpr int kSms = 152;
+int ctas_for(long long heads, long long rows, int chunk, int least) {
+    const long long chunks = heads * ((rows + chunk - 1) / chunk), want = (chunks + least - 1) / least;
+    return (int)(want < 1 ? 1 : want > kSms ? kSms : want);
+}
+
+cudaError_t answers(const void* q, void* o, const char* image, const la_cross_shape& s, cudaStream_t st) {
+    const Rows rows = grouped_queries(s);
+    CUtensorMap tq, to;
+    if (!make_tmap_bf16_rows(&tq, q, rows.heads(), rows.M, s.Dk, kRowChunk) ||
+        !make_tmap_bf16_rows(&to, o, rows.heads(), rows.M, s.Dv, kRowChunk))
+        return cudaErrorInvalidValue;
+    const int ctas = ctas_for(rows.heads(), rows.M, kRowChunk, 1);
+    auto go = [&](auto kern, size_t smem) {
+        return tc_run("cross_apply_tc", kern, dim3(ctas), kApplyThreads, smem, st, tq, to, image, rows, device_error_word());
+    };
+    switch (2 * blocks64(s.Dk) + blocks64(s.Dv)) {
+        case 3: return go(cross_apply_tc<1, 1>, ApplySmem<1, 1>::total);
+        case 4: return go(cross_apply_tc<1, 2>, ApplySmem<1, 2>::total);
+        case 5: return go(cross_apply_tc<2, 1>, ApplySmem<2, 1>::total);
+        default: return go(cross_apply_tc<2, 2>, ApplySmem<2, 2>::total);
+    }
+}
+
+}  // namespace
+
+bool tc_ok(const la_cross_shape& s) { return s.dtype == LA_BF16; }
+
+TcLayout tc_layout(const la_cross_shape& s, int op) {
+    const int KB = blocks64(s.Dk), VB = blocks64(s.Dv);
+    const size_t heads = (size_t)s.B * s.Hk, image = up(heads * image_bytes(KB, VB)), rec = record_floats(VB) * 4;
+    TcLayout l{};
+    if (op != LA_OP_CROSS_APPLY) {
+        l.sum_ctas = ctas_for(heads, s.M, kSumRows, 2);
+        l.key_ctas = ctas_for(heads, s.M, kRowChunk, 1);
+        size_t most = l.sum_ctas;
+        if (op == LA_OP_CROSS_BWD) {
+            l.query_ctas = ctas_for(heads, query_rows(s), kRowChunk, 1);
+            if ((size_t)l.query_ctas > most) most = l.query_ctas;
+        }
+        l.bytes = up((most + heads) * rec);
+    }
+    l.S = l.bytes;
+    l.bytes += image;
+    if (op == LA_OP_CROSS_BWD) {
+        l.R = l.bytes;
+        l.bytes += image;
+    }
+    return l;
+}
+size_t tc_bytes(const la_cross_shape& s, int op) { return tc_layout(s, op).bytes; }
+
+cudaError_t tc_sums(const void* k, const void* v, const Rows& keys, float* rec, int ctas, const la_cross_shape& s, cudaStream_t st) {
+    CUtensorMap tk, tv;
+    if (!make_tmap_bf16_rows(&tk, k, keys.heads(), keys.M, s.Dk, kSumRows) ||
+        !make_tmap_bf16_rows(&tv, v, keys.heads(), keys.M, s.Dv, kSumRows))
+        return cudaErrorInvalidValue;
+    auto go = [&](auto kern, size_t smem) {
+        return tc_run("cross_sums_tc", kern, dim3(ctas), kSumThreads, smem, st, tk, tv, rec, keys, s.Dk, ctas + keys.heads(),
+                      device_error_word());
+    };
+    switch (2 * blocks64(s.Dk) + blocks64(s.Dv)) {
+        case 3: return go(cross_sums_tc<1, 1>, SumSmem<1, 1>::total);
+        case 4: return go(cross_sums_tc<1, 2>, SumSmem<1, 2>::total);
+        case 5: return go(cross_sums_tc<2, 1>, SumSmem<2, 1>::total);
+        default: return go(cross_sums_tc<2, 2>, SumSmem<2, 2>::total);
+    }
+}
+
+cudaError_t tc_join(const float* rec, const float* S, const float* z, char* image, float* S_out, float* z_out, const Rows& rows,
+                    int chunk, int ctas, const la_cross_shape& s, cudaStream_t st) {
+    const int KB = blocks64(s.Dk), VB = blocks64(s.Dv);
+    auto go = [&](auto kern) {
+        launch_begin("cross_join_tc", st);
+        const cudaError_t e = launch_pdl(kern, dim3(rows.heads(), 64 * KB * 8 * VB / 32 + 1), dim3(256), 0, st, rec, S, z, image, S_out,
+                                         z_out, rows, chunk, ctas, s.Dk, s.Dv);
+        const cudaError_t e2 = launch_end("cross_join_tc", st);
+        return e != cudaSuccess ? e : e2;
+    };
+    switch (2 * KB + VB) {
+        case 3: return go(cross_join_tc<1, 1>);
+        case 4: return go(cross_join_tc<1, 2>);
+        case 5: return go(cross_join_tc<2, 1>);
+        default: return go(cross_join_tc<2, 2>);
+    }
+}
+
+cudaError_t tc_fwd(const FwdArgs& a, const la_cross_shape& s, char* ws, cudaStream_t st) {
+    const TcLayout l = tc_layout(s, LA_OP_CROSS_FWD);
+    const Rows keys = key_rows(s, a.lens);
+    float* rec = reinterpret_cast<float*>(ws);
+    CR_TRY(tc_sums(a.k, a.v, keys, rec, l.sum_ctas, s, st));
+    CR_TRY(tc_join(rec, nullptr, nullptr, ws + l.S, a.S, a.z, keys, kSumRows, l.sum_ctas, s, st));
+    return s.N == 0 ? cudaSuccess : answers(a.q, a.o, ws + l.S, s, st);
+}
+
+cudaError_t tc_apply(const void* q, const float* S, const float* z, void* o, const la_cross_shape& s, char* ws, cudaStream_t st) {
+    CR_TRY(tc_join(nullptr, S, z, ws, nullptr, nullptr, grouped_queries(s), kRowChunk, 1, s, st));
+    return answers(q, o, ws, s, st);
+}
+
+}  // namespace cross
+}  // namespace la

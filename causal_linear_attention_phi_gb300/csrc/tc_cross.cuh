@@ -1,0 +1,89 @@
+// tc_cross.cuh -- shared pieces of the tensor-core (tcgen05 / TMEM / TMA) kernels of cross attention, bf16 heads.
+//
+// Heads are padded on chip to KB (keys) and VB (values) blocks of 64 columns by the tile copies, which fill what lies
+// outside a tensor with zeros.  A tile of `rows` rows is KB or VB blocks of rows x 128 bytes with the 128-byte
+// swizzle: 16-byte chunk lc of row r of a block sits at chunk lc ^ (r & 7).
+//
+// The state (S, z), and (R, r) of the gradient, pass between kernels as an image: S as two bf16 parts (hi, then lo =
+// S - hi), each a swizzled tile of 64 KB rows by VB blocks as the products' operands want it, then z as 64 KB floats; a
+// block brings it into shared memory with one copy.
+#pragma once
+
+#include <cuda.h>
+
+#include "cross.cuh"
+#include "shared_memory.cuh"
+#include "tc_common.cuh"
+
+namespace la {
+namespace cross {
+
+using namespace sm100;
+
+constexpr int kSumRows = 64;   // rows of a chunk of the sums
+constexpr int kRowChunk = 128; // rows of a chunk of the queries, and of the keys in the gradient
+
+constexpr size_t image_part(int KB, int VB) { return (size_t)KB * VB * 8192; }
+constexpr size_t image_bytes(int KB, int VB) { return 2 * image_part(KB, VB) + (size_t)KB * 256; }
+// A record of the sums: 128 accumulator rows of 64 VB floats, 128 floats of z (KB = 1: the upper 64 of either belong to the
+// lo parts and are added to the lower).
+constexpr size_t record_floats(int VB) { return (size_t)128 * 64 * VB + 128; }
+
+inline int blocks64(int d) { return d > 64 ? 2 : 1; }
+
+__device__ __forceinline__ int swz(int row, int lc) { return row * 128 + (((lc & 7) ^ (row & 7)) << 4); }
+// K-major operand, 16-element step kk: blocks of 64 elements are `block` bytes apart.
+__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int kk, uint32_t block) {
+    return smem_desc_sw128(tile + (kk >> 2) * block + (kk & 3) * 32, 16, 1024);
+}
+// MN-major operand, 16-row step kk: blocks of 64 M or N elements are `block` bytes apart.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int kk, uint32_t block) {
+    return smem_desc_sw128(tile + kk * 2048, block, 1024);
+}
+
+// A bounded wait whose outcome is the same for a whole warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* err) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, LA_ERR_TIMEOUT));
+}
+
+// Debug build: a tile copy of a [heads][rows][D] tensor.
+__device__ __forceinline__ void check_copy(int x, int row, int rows, int bh, int heads) {
+    LA_DCHECK((x == 0 || x == 64) && row >= 0 && row < rows && bh >= 0 && bh < heads);
+}
+
+// hi and lo bf16 parts of two floats.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16x2(a, b);
+    lo = pack_bf16x2(a - tc::bf_lo(hi), b - tc::bf_hi(hi));
+}
+
+// host
+struct TcLayout {
+    size_t rec, S, R, bytes;  // records; images of (S, z) and of (R, r)
+    int sum_ctas, query_ctas, key_ctas;
+};
+TcLayout tc_layout(const la_cross_shape& s, int op);
+
+// Records of the heads, or a caller's state, to images; with S_out the sums also as fp32 state.
+cudaError_t tc_join(const float* rec, const float* S, const float* z, char* image, float* S_out, float* z_out, const Rows& rows,
+                    int chunk, int ctas, const la_cross_shape& s, cudaStream_t st);
+cudaError_t tc_sums(const void* k, const void* v, const Rows& keys, float* rec, int ctas, const la_cross_shape& s, cudaStream_t st);
+
+// A kernel that takes nearly all of an SM's shared memory: opted in once for its one size.
+template <typename K, typename... A>
+cudaError_t tc_run(const char* name, K kern, dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+    cudaError_t e = allow_smem(kern, smem);
+    if (e != cudaSuccess) return e;
+    launch_begin(name, st);
+    e = launch_pdl(kern, grid, dim3(threads), smem, st, args...);
+    const cudaError_t e2 = launch_end(name, st);
+    return e != cudaSuccess ? e : e2;
+}
+#define CR_TRY(x)                            \
+    do {                                     \
+        const cudaError_t e_ = (x);          \
+        if (e_ != cudaSuccess) return e_;    \
+    } while (0)
+
+}  // namespace cross
+}  // namespace la

@@ -40,13 +40,13 @@ __device__ __forceinline__ long long chunks_before(const Rows& r, int b, int chu
 
 // A block's share of the work: its first chunk and how many it has.
 struct Span {
-    int bh, i;       // head, chunk of the head (among the live, or the dead ones)
-    long long left;  // chunks from there on
+    int bh, i;  // head, chunk of the head (among the live, or the dead ones)
+    int left;   // chunks from there on (fewer than 2^31: a tensor has fewer than 2^40 elements, a chunk at least 2^10)
 };
 __device__ __forceinline__ Span span_of(const Rows& r, int chunk, bool dead, int cta, int ctas) {  // a whole warp
     const long long total = chunks_before(r, r.B, chunk, dead) * r.Hk;
     long long from = total * cta / ctas;
-    Span s{0, 0, total * (cta + 1) / ctas - from};
+    Span s{0, 0, (int)(total * (cta + 1) / ctas - from)};
     if (s.left == 0) return s;
     int b = 0;
     if (!r.lens) {
@@ -82,8 +82,7 @@ __device__ __forceinline__ Span span_of(const Rows& r, int chunk, bool dead, int
 // The walk over a share.  `live` rows of the head; the chunk's rows are [i chunk, ...) (of the live ones).
 struct Walk {
     Rows r;
-    int chunk, bh, i, nch, live;
-    long long left;
+    int chunk, bh, i, nch, live, left;
     bool fresh;  // no chunk of this head has been taken before
     __device__ Walk(const Rows& rows, int chunk_, const Span& s)
         : r(rows), chunk(chunk_), bh(s.bh), i(s.i), nch(0), live(0), left(s.left), fresh(true) {

@@ -22,17 +22,20 @@ using tc::bf_lo;
 
 // ------------------------------------------------------------------ sums over the keys
 // A stage holds a chunk of 64 rows: K (phi's hi part in place), its lo part, V.  For KB = 1 hi and lo are the two 64-row
-// halves of one 128-row product; else they are two products.  Sums of a head alternate between two accumulators, so
-// that four warps write a head's record while the next head's sums are formed.
-constexpr int kSumThreads = 448;  // warp 0 TMA, 1 MMA, 2-9 two compute groups, 10-13 records
+// halves of one 128-row product; else they are two products.  An accumulator in tensor memory takes kPeriod chunks only:
+// the products add with truncation, half a unit in the last place each and always the same way (131,072 keys summed in one
+// accumulator to a block were 2e-5 off).  The compute warps then add it to sums of their own, in registers and rounded
+// to nearest, while the other accumulator takes the next period: a warp has 32 rows and a quarter of the columns.
+constexpr int kSumThreads = 576;  // warp 0 TMA, 1 MMA, 2-17 two compute groups of eight
+constexpr int kPeriod = 4;
 
 template <int KB, int VB>
 struct SumSmem {
     static constexpr int kTile = 8192;  // 64 rows of a block
     static constexpr int kLo = KB * kTile, kV = 2 * KB * kTile, kStage = (2 * KB + VB) * kTile;
     static constexpr int kStages = 196608 / kStage > 8 ? 8 : 196608 / kStage;
-    static constexpr int zpart = kStages * kStage;            // float[2][8][64 KB]
-    static constexpr int bars = zpart + 2 * 8 * 64 * KB * 4;
+    static constexpr int zpart = kStages * kStage;            // float[2][16][64 KB]
+    static constexpr int bars = zpart + 2 * 16 * 64 * KB * 4;
     static constexpr int total = bars + 512;
 };
 
@@ -44,7 +47,7 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     constexpr int NS = SM::kStages, T = SM::kTile;
     extern __shared__ __align__(1024) uint8_t smem[];
     struct Bars {
-        uint64_t full[8], ready[8], empty[8], acc_done[2], z_ready[2], flushed[2], final_mma;
+        uint64_t full[8], ready[8], empty[8], acc_done[2], flushed[2], z_ready[2], z_free[2], final_mma;
         uint32_t tmem;
         Span span;
     };
@@ -56,13 +59,14 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     if (tid == 32) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&bar->full[s], 1);
-            mbar_init(&bar->ready[s], 128);
+            mbar_init(&bar->ready[s], 256);
             mbar_init(&bar->empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&bar->acc_done[a], 1);
-            mbar_init(&bar->z_ready[a], 8);
-            mbar_init(&bar->flushed[a], 128);
+            mbar_init(&bar->flushed[a], 16);
+            mbar_init(&bar->z_ready[a], 16);
+            mbar_init(&bar->z_free[a], 4);
         }
         mbar_init(&bar->final_mma, 1);
         fence_mbar_init();
@@ -87,9 +91,9 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 
     if (warp == 0) {
         if (lane == 0) {
-            long long i = 0;
+            int i = 0;
             for (; w.more(); w.next(), ++i) {
-                const int s = (int)(i % NS);
+                const int s = i % NS;
                 if (!mbar_wait(&bar->empty[s], ((i / NS) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
                 uint8_t* st = smem + s * SM::kStage;
                 mbar_arrive_expect_tx(&bar->full[s], (KB + VB) * T);
@@ -102,118 +106,143 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     } else if (warp == 1) {
         if (lane == 0) {
             constexpr uint32_t id = idesc_bf16_f32(128, 64 * VB, 1, 1);
-            long long i = 0;
-            int heads = 0;
-            bool first = true;
+            int i = 0, period = 0;
+            int in = 0;  // chunks of the period so far
             for (; w.more(); w.next(), ++i) {
-                const int s = (int)(i % NS), a = heads & 1;
+                const int s = i % NS, a = period & 1;
                 if (!mbar_wait(&bar->ready[s], (i / NS) & 1, err, LA_ERR_TIMEOUT)) break;
-                if (first && !mbar_wait(&bar->flushed[a], ((heads >> 1) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
+                if (in == 0 && !mbar_wait(&bar->flushed[a], ((period >> 1) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
                 tc_fence_after();
                 const uint32_t st = smem_u32(smem + s * SM::kStage), acc = tmem + 64 * VB * a;
 #pragma unroll
                 for (int kk = 0; kk < kSumRows / 16; ++kk) {
-                    mma_ss(acc, desc_mn(st, kk, T), desc_mn(st + SM::kV, kk, T), id, !first || kk > 0);
+                    mma_ss(acc, desc_mn(st, kk, T), desc_mn(st + SM::kV, kk, T), id, in > 0 || kk > 0);
                     if (KB == 2) mma_ss(acc, desc_mn(st + SM::kLo, kk, T), desc_mn(st + SM::kV, kk, T), id, 1);
                 }
                 mma_commit(&bar->empty[s]);
-                first = w.last();
-                if (first) {
+                if (++in == kPeriod || w.last()) {
                     mma_commit(&bar->acc_done[a]);
-                    ++heads;
+                    ++period;
+                    in = 0;
                 }
             }
             mma_commit(&bar->final_mma);  // every product is complete before the accumulators are given back
             mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
         }
-    } else if (warp < 10) {
-        const int group = (warp - 2) >> 2, ct = (tid - 64) & 127;
-        const int lc = (ct & 7) ^ ((ct >> 3) & 7), at = (ct >> 3) * 128 + (ct & 7) * 16;  // rows (ct >> 3) + 16 j
-        float zp[KB][8];
+    } else {
+        const int cw = warp - 2, group = cw >> 3, ct = (tid - 64) & 255;
+        const int lc = (ct & 7) ^ ((ct >> 3) & 7), at = (ct >> 3) * 128 + (ct & 7) * 16;  // rows (ct >> 3) + 32 j
+        constexpr int kOwn = 16 * VB;  // columns of this warp's sums, of the rows 32 (warp % 4) ..
+        const int col0 = kOwn * (cw >> 2);
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        float zp[KB][8], sum[kOwn];
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int e = 0; e < 8; ++e) zp[b][e] = 0.f;
-        long long i = 0;
-        int heads = 0;
+#pragma unroll
+        for (int e = 0; e < kOwn; ++e) sum[e] = 0.f;
+        int i = 0, period = 0, flushed = 0, heads = 0;
+        int in = 0;
         bool ok = true;
+        auto flush = [&]() {  // the oldest period not yet added
+            const int a = flushed & 1;
+            ok = ok && warp_wait(&bar->acc_done[a], (flushed >> 1) & 1, err);
+            if (!ok) return;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < kOwn / 16; ++c) {
+                uint32_t x[16];
+                tmem_ld16(tmem + 64 * VB * a + col0 + 16 * c + lanes, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) sum[16 * c + e] += __uint_as_float(x[e]);
+            }
+            tc_fence_before();
+            if (lane == 0) mbar_arrive(&bar->flushed[a]);
+            ++flushed;
+        };
         for (; w.more() && ok; w.next(), ++i) {
             if ((i & 1) == group) {
-                const int s = (int)(i % NS), n = w.rows();
+                const int s = i % NS, n = w.rows();
                 if (!(ok = warp_wait(&bar->full[s], (i / NS) & 1, err))) break;
                 uint8_t* st = smem + s * SM::kStage + at;
+                uint4 x[KB][2];
+#pragma unroll
+                for (int b = 0; b < KB; ++b)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) x[b][j] = *reinterpret_cast<const uint4*>(st + b * T + 4096 * j);
 #pragma unroll
                 for (int b = 0; b < KB; ++b) {
                     const bool col = 64 * b + 8 * lc < Dk;
-                    uint4 x[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4*>(st + b * T + 2048 * j);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const bool in = col && (ct >> 3) + 16 * j < n;
-                        uint32_t* u = reinterpret_cast<uint32_t*>(&x[j]);
+                    for (int j = 0; j < 2; ++j) {
+                        const bool live = col && (ct >> 3) + 32 * j < n;
+                        uint32_t* u = reinterpret_cast<uint32_t*>(&x[b][j]);
                         uint4 l;
                         uint32_t* ul = reinterpret_cast<uint32_t*>(&l);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float p0 = in ? phi_f(bf_lo(u[e])) : 0.f, p1 = in ? phi_f(bf_hi(u[e])) : 0.f;
+                            const float p0 = live ? phi_f(bf_lo(u[e])) : 0.f, p1 = live ? phi_f(bf_hi(u[e])) : 0.f;
                             zp[b][2 * e] += p0;
                             zp[b][2 * e + 1] += p1;
                             split2(p0, p1, u[e], ul[e]);
                         }
-                        *reinterpret_cast<uint4*>(st + b * T + 2048 * j) = x[j];
-                        *reinterpret_cast<uint4*>(st + SM::kLo + b * T + 2048 * j) = l;
+                        *reinterpret_cast<uint4*>(st + b * T + 4096 * j) = x[b][j];
+                        *reinterpret_cast<uint4*>(st + SM::kLo + b * T + 4096 * j) = l;
                     }
                 }
                 if (n < kSumRows) {  // what lies behind the length may be anything
 #pragma unroll
                     for (int b = 0; b < VB; ++b)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if ((ct >> 3) + 16 * j >= n)
-                                *reinterpret_cast<uint4*>(st + SM::kV + b * T + 2048 * j) = make_uint4(0u, 0u, 0u, 0u);
+                        for (int j = 0; j < 2; ++j)
+                            if ((ct >> 3) + 32 * j >= n)
+                                *reinterpret_cast<uint4*>(st + SM::kV + b * T + 4096 * j) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&bar->ready[s]);
             }
-            if (w.last()) {  // this group's part of the head's z: over the four lanes that share columns, by warp
-                const int a = heads & 1;
-                if (!(ok = warp_wait(&bar->flushed[a], ((heads >> 1) & 1) ^ 1, err))) break;
-                float* to = zpart + (a * 8 + warp - 2) * 64 * KB + 8 * lc;
+            const bool last = w.last();
+            if (++in < kPeriod && !last) continue;
+            in = 0;
+            ++period;
+            while (ok && flushed < (last ? period : period - 1)) flush();
+            if (!last || !ok) continue;
+            // the head's record: this warp's sums, and z over the four lanes that share columns, then over the warps
+            const int a = heads & 1, r = 32 * (warp & 3) + lane;
+            if (!(ok = warp_wait(&bar->z_free[a], ((heads >> 1) & 1) ^ 1, err))) break;
+            float* to = zpart + (a * 16 + cw) * 64 * KB + 8 * lc;
 #pragma unroll
-                for (int b = 0; b < KB; ++b)
+            for (int b = 0; b < KB; ++b)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float x = zp[b][e];
-                        x += __shfl_xor_sync(0xffffffffu, x, 9);
-                        x += __shfl_xor_sync(0xffffffffu, x, 18);
-                        if (lane < 8) to[64 * b + e] = x;
-                        zp[b][e] = 0.f;
-                    }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->z_ready[a]);
-                ++heads;
+                for (int e = 0; e < 8; ++e) {
+                    float z = zp[b][e];
+                    z += __shfl_xor_sync(0xffffffffu, z, 9);
+                    z += __shfl_xor_sync(0xffffffffu, z, 18);
+                    if (lane < 8) to[64 * b + e] = z;
+                    zp[b][e] = 0.f;
+                }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar->z_ready[a]);
+            const bool slot = LA_DCHECK((int)blockIdx.x + w.bh < slots);
+            float* out = rec + (size_t)(blockIdx.x + w.bh) * record_floats(VB);
+#pragma unroll
+            for (int e = 0; e < kOwn; e += 4) {
+                if (slot) *reinterpret_cast<float4*>(out + (size_t)r * 64 * VB + col0 + e) = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+                sum[e] = sum[e + 1] = sum[e + 2] = sum[e + 3] = 0.f;
             }
-        }
-    } else {
-        const int r = 32 * (warp & 3) + lane;
-        int heads = 0;
-        for (; w.more(); w.next()) {
-            if (!w.last()) continue;
-            const int a = heads & 1;
-            if (!warp_wait(&bar->acc_done[a], (heads >> 1) & 1, err) || !warp_wait(&bar->z_ready[a], (heads >> 1) & 1, err)) break;
-            tc_fence_after();
-            if (LA_DCHECK((int)blockIdx.x + w.bh < slots)) {
-                float* out = rec + (size_t)(blockIdx.x + w.bh) * record_floats(VB);
-                tc::tmem_row_to_global<64 * VB>(tmem + 64 * VB * a + ((uint32_t)(32 * (warp & 3)) << 16), out + (size_t)r * 64 * VB);
+            if (cw < 4) {
+                if (!(ok = warp_wait(&bar->z_ready[a], (heads >> 1) & 1, err))) break;
+                const int c = 32 * cw + lane;
                 float z = 0.f;
-                if (r < 64 * KB)
+                if (c < 64 * KB)
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) z += zpart[(a * 8 + x) * 64 * KB + r];
-                out[128 * 64 * VB + r] = z;
+                    for (int x = 0; x < 16; ++x) z += zpart[(a * 16 + x) * 64 * KB + c];
+                if (slot) out[128 * 64 * VB + c] = z;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->z_free[a]);
             }
-            tc_fence_before();
-            mbar_arrive(&bar->flushed[a]);
             ++heads;
         }
     }
@@ -226,21 +255,20 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 }
 
 // ------------------------------------------------------------------ join
-// A head's records (or a caller's state) to its image.  8 threads share a 16-byte chunk of the image, taking every eighth record;
-// their sums are added in a fixed order.  The last block of a head does z.
-template <int KB, int VB>
+// A head's records (or a caller's state) to its image.  kLanes threads share a 16-byte chunk of the image, each taking every
+// kLanes-th record; their sums are added in a fixed order.  The last block of a head does z.
+template <int KB, int VB, int kLanes>
 __global__ void __launch_bounds__(256)
 cross_join_tc(const float* __restrict__ rec, const float* __restrict__ S, const float* __restrict__ z, char* __restrict__ image,
               float* __restrict__ S_out, float* __restrict__ z_out, Rows rows, int chunk, int ctas, int Dk, int Dv) {
-    constexpr int kChunks = 64 * KB * 8 * VB;
-    __shared__ float part[8][32][9];
+    constexpr int kChunks = 64 * KB * 8 * VB, kOwn = 256 / kLanes;
+    __shared__ float part[kLanes > 1 ? kLanes : 1][kLanes > 1 ? kOwn : 1][9];
     pdl_enter();  // launched with programmatic dependent launch
-    const int bh = blockIdx.x, x = threadIdx.x & 31, lane8 = threadIdx.x >> 5;
-    const bool zs = blockIdx.y == kChunks / 32;
+    const int bh = blockIdx.x, x = threadIdx.x % kOwn, lane = threadIdx.x / kOwn;
     Range g{0, 0};
     if (rec) g = records_of(rows, chunk, bh, ctas);
     char* im = image + (size_t)bh * image_bytes(KB, VB);
-    if (zs) {
+    if (blockIdx.y == kChunks / kOwn) {
         if (threadIdx.x < 64 * KB) {
             const int d = threadIdx.x;
             float a = 0.f;
@@ -257,7 +285,7 @@ cross_join_tc(const float* __restrict__ rec, const float* __restrict__ S, const 
         return;
     }
     // row d, columns c8 .. c8 + 7
-    const int at = blockIdx.y * 32 + x, d = at / (8 * VB), c8 = at % (8 * VB) * 8;
+    const int at = blockIdx.y * kOwn + x, d = at / (8 * VB), c8 = at % (8 * VB) * 8;
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 0.f;
@@ -266,27 +294,27 @@ cross_join_tc(const float* __restrict__ rec, const float* __restrict__ S, const 
         v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w, v[4] += h.x, v[5] += h.y, v[6] += h.z, v[7] += h.w;
     };
     if (!rec) {
-        if (lane8 == 0 && d < Dk && c8 < Dv) add(S + ((size_t)bh * Dk + d) * Dv + c8);
+        if (d < Dk && c8 < Dv) add(S + ((size_t)bh * Dk + d) * Dv + c8);
     } else {
-#pragma unroll 2
-        for (int c = g.first + lane8; c <= g.last; c += 8) {
+#pragma unroll 4
+        for (int c = g.first + lane; c <= g.last; c += kLanes) {
             const float* p = rec + (size_t)(c + bh) * record_floats(VB) + (size_t)d * 64 * VB + c8;
             add(p);
             if (KB == 1) add(p + 64 * 64 * VB);  // the sums of the lo parts
         }
+    }
+    if constexpr (kLanes > 1) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) part[lane8][x][e] = v[e];
+        for (int e = 0; e < 8; ++e) part[lane][x][e] = v[e];
         __syncthreads();
-        if (lane8 == 0) {
+        if (lane != 0) return;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[e] = 0.f;
+        for (int e = 0; e < 8; ++e) {
+            v[e] = 0.f;
 #pragma unroll
-                for (int l = 0; l < 8; ++l) v[e] += part[l][x][e];
-            }
+            for (int l = 0; l < kLanes; ++l) v[e] += part[l][x][e];
         }
     }
-    if (lane8 != 0) return;
     uint4 hi, lo;
     split2(v[0], v[1], hi.x, lo.x);
     split2(v[2], v[3], hi.y, lo.y);
@@ -369,11 +397,11 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 
     if (warp == 0) {
         if (lane == 0) {
-            long long i = 0, heads = 0;
+            int i = 0, heads = 0;
             bool first = true;
             for (; w.more(); w.next(), ++i) {
                 if (first) {
-                    const int h = (int)(heads & 1);
+                    const int h = heads & 1;
                     if (!mbar_wait(&bar->s_empty[h], ((heads >> 1) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
                     const char* im = image + (size_t)w.bh * image_bytes(KB, VB);
                     mbar_arrive_expect_tx(&bar->s_full[h], SM::kS + 256 * KB);
@@ -382,7 +410,7 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     ++heads;
                 }
                 first = w.last();
-                const int s = (int)(i % NS);
+                const int s = i % NS;
                 if (!mbar_wait(&bar->empty[s], ((i / NS) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
                 mbar_arrive_expect_tx(&bar->full[s], KB * T);
                 check_copy(0, w.row0(), rows.M, w.bh, rows.heads());
@@ -394,12 +422,12 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     } else if (warp == 1) {
         if (lane == 0) {
             constexpr uint32_t id = idesc_bf16_f32(128, 64 * VB, 0, 1);
-            long long i = 0, heads = 0;
+            int i = 0, heads = 0;
             bool first = true;
             for (; w.more(); w.next(), ++i) {
-                const int g = (int)(i & 1), s = (int)(i % NS);
+                const int g = i & 1, s = i % NS;
                 if (first) ++heads;
-                const int h = (int)((heads - 1) & 1);
+                const int h = (heads - 1) & 1;
                 if (first && !mbar_wait(&bar->s_full[h], ((heads - 1) >> 1) & 1, err, LA_ERR_TIMEOUT)) break;
                 // phi(Q) is in place, and the group has read the outputs of its previous chunk
                 if (!mbar_wait(&bar->ready[g], (i >> 1) & 1, err, LA_ERR_TIMEOUT)) break;
@@ -418,13 +446,13 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     } else if (warp < 10) {
         const int g = (warp - 2) >> 2, r = 32 * (warp & 3) + lane;
         const uint32_t acc = tmem + 64 * VB * g + ((uint32_t)(32 * (warp & 3)) << 16);
-        long long i = 0, heads = 0;
+        int i = 0, heads = 0;
         bool first = true;
         for (; w.more(); w.next(), ++i) {
             if (first) ++heads;
             first = w.last();
             if ((i & 1) != g) continue;
-            const int s = (int)(i % NS), h = (int)((heads - 1) & 1);
+            const int s = i % NS, h = (heads - 1) & 1;
             uint8_t* st = smem + s * SM::kStage;
             const float* zs = reinterpret_cast<const float*>(smem + SM::z0 + h * 256 * KB);
             if (!warp_wait(&bar->s_full[h], ((heads - 1) >> 1) & 1, err) || !warp_wait(&bar->full[s], (i / NS) & 1, err)) break;
@@ -474,8 +502,8 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
     } else if (lane == 0) {
         // stores: a stage is empty once its outputs have been read
-        for (long long i = 0; w.more(); w.next(), ++i) {
-            const int s = (int)(i % NS);
+        for (int i = 0; w.more(); w.next(), ++i) {
+            const int s = i % NS;
             if (!mbar_wait(&bar->staged[s], (i / NS) & 1, err, LA_ERR_TIMEOUT)) break;
             check_copy(0, w.row0(), rows.M, w.bh, rows.heads());
             for (int b = 0; b < VB; ++b) tma_store_3d(&tm_o, smem + s * SM::kStage + b * T, 64 * b, w.row0(), w.bh);
@@ -566,18 +594,20 @@ cudaError_t tc_sums(const void* k, const void* v, const Rows& keys, float* rec, 
 cudaError_t tc_join(const float* rec, const float* S, const float* z, char* image, float* S_out, float* z_out, const Rows& rows,
                     int chunk, int ctas, const la_cross_shape& s, cudaStream_t st) {
     const int KB = blocks64(s.Dk), VB = blocks64(s.Dv);
-    auto go = [&](auto kern) {
+    // few records to a head: a thread to a chunk; many (few heads): eight, with an eighth of the records each
+    const bool many = rec && ctas > 4 * rows.heads();
+    auto go = [&](auto kern, int own) {
         launch_begin("cross_join_tc", st);
-        const cudaError_t e = launch_pdl(kern, dim3(rows.heads(), 64 * KB * 8 * VB / 32 + 1), dim3(256), 0, st, rec, S, z, image, S_out,
+        const cudaError_t e = launch_pdl(kern, dim3(rows.heads(), 64 * KB * 8 * VB / own + 1), dim3(256), 0, st, rec, S, z, image, S_out,
                                          z_out, rows, chunk, ctas, s.Dk, s.Dv);
         const cudaError_t e2 = launch_end("cross_join_tc", st);
         return e != cudaSuccess ? e : e2;
     };
     switch (2 * KB + VB) {
-        case 3: return go(cross_join_tc<1, 1>);
-        case 4: return go(cross_join_tc<1, 2>);
-        case 5: return go(cross_join_tc<2, 1>);
-        default: return go(cross_join_tc<2, 2>);
+        case 3: return many ? go(cross_join_tc<1, 1, 8>, 32) : go(cross_join_tc<1, 1, 1>, 256);
+        case 4: return many ? go(cross_join_tc<1, 2, 8>, 32) : go(cross_join_tc<1, 2, 1>, 256);
+        case 5: return many ? go(cross_join_tc<2, 1, 8>, 32) : go(cross_join_tc<2, 1, 1>, 256);
+        default: return many ? go(cross_join_tc<2, 2, 8>, 32) : go(cross_join_tc<2, 2, 1>, 256);
     }
 }
 

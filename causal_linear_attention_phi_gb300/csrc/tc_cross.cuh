@@ -32,13 +32,14 @@ constexpr size_t record_floats(int VB) { return (size_t)128 * 64 * VB + 128; }
 inline int blocks64(int d) { return d > 64 ? 2 : 1; }
 
 __device__ __forceinline__ int swz(int row, int lc) { return row * 128 + (((lc & 7) ^ (row & 7)) << 4); }
+// Operand descriptors: a tile's first, and steps from it added to its address field (shared memory ends below the field's).
 // K-major operand, 16-element step kk: blocks of 64 elements are `block` bytes apart.
 __device__ __forceinline__ uint64_t desc_k(uint32_t tile, int kk, uint32_t block) {
-    return smem_desc_sw128(tile + (kk >> 2) * block + (kk & 3) * 32, 16, 1024);
+    return smem_desc_sw128(tile, 16, 1024) + (((kk >> 2) * block + (kk & 3) * 32) >> 4);
 }
 // MN-major operand, 16-row step kk: blocks of 64 M or N elements are `block` bytes apart.
 __device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int kk, uint32_t block) {
-    return smem_desc_sw128(tile + kk * 2048, block, 1024);
+    return smem_desc_sw128(tile, block, 1024) + ((kk * 2048) >> 4);
 }
 
 // A bounded wait whose outcome is the same for a whole warp.

@@ -12,17 +12,28 @@
 // chunks, a thread a row; outputs go back into the stage's tiles for their store.
 #include <cudaTypedefs.h>
 
+#include "norm_common.cuh"
 #include "tc_cross.cuh"
 
 namespace la {
 namespace cross {
 namespace {
 
+using norm::both;
+using norm::fma2;
+using norm::mul2;
+using norm::Pairs;
 using tc::bf_hi;
 using tc::bf_lo;
 
 constexpr int kThreads = 352;  // warp 0 TMA loads, 1 MMA, 2-9 two compute groups, 10 TMA stores
 constexpr int T = 16384;       // 128 rows of a block
+
+// A warpgroup gives registers back, or takes them, down or up to n a thread.
+template <int n>
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n)); }
+template <int n>
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n)); }
 
 // A row of a tile through f(first column, its 16 bytes as 4 words): f may change the words.
 template <int B, typename F>
@@ -42,6 +53,12 @@ __device__ __forceinline__ void row_words(const uint8_t* tile, int r, F f) {
 // 128-row product; for KB = 2 in a tile of its own, for which shared memory has no second.  t enters as the first two columns
 // (hi and lo) of a 16-column operand W, K-major, of whose rows only 8 are held: rows 8-15 of a block are read from the 1 KB
 // behind it (the other block's rows, or z and the barriers) and make columns of the result that nothing reads.
+//
+// The compute warps hold their row's phi in fp32 throughout (128 registers), which they get from the other warpgroup:
+// 384 threads of 168 registers are 128 of 80 and 256 of 208.  A chunk's phases, each overlapping the other group's:
+//   phi, den, X -> X^T dO may start;   Y -> t -> X^T t may start;   Y -> dq, which waits for X's tile.
+constexpr int kQueryThreads = 384;  // warp 0 TMA loads, 1 MMA, 2 TMA stores, 4-11 two compute groups
+
 template <int KB, int VB>
 struct QuerySmem {
     static constexpr int kLo = KB == 1 ? T : 0, kDo = (KB == 1 ? 2 : KB) * T, kStage = kDo + VB * T;
@@ -56,7 +73,7 @@ struct QuerySmem {
 };
 
 template <int KB, int VB>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kQueryThreads, 1)
 cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                const __grid_constant__ CUtensorMap tm_dq, const char* __restrict__ image, float* __restrict__ rec, Rows rows, int Dk,
                int slots, int* err) {
@@ -66,7 +83,8 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     constexpr uint32_t kCols = kW + 16 <= 256 ? 256 : 512;
     extern __shared__ __align__(1024) uint8_t smem[];
     struct Bars {
-        uint64_t full[4], empty[4], staged[4], s_full, s_empty, y_done[2], ready[2], r_done[2], x_free, r_flushed, final_mma;
+        uint64_t full[4], empty[4], staged[4], s_full, s_empty, y_done[2], y_free[2], x_ready[2], w_ready[2], r_done[2], x_free, r_flushed,
+            final_mma;
         uint32_t tmem;
         Span span;
     };
@@ -83,7 +101,9 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&bar->y_done[g], 1);
-            mbar_init(&bar->ready[g], 128);
+            mbar_init(&bar->y_free[g], 128);
+            mbar_init(&bar->x_ready[g], 128);
+            mbar_init(&bar->w_ready[g], 128);
             mbar_init(&bar->r_done[g], 1);
         }
         mbar_init(&bar->s_full, 1);
@@ -101,7 +121,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         tmem_alloc(&bar->tmem, kCols);
         tmem_relinquish();
     }
-    for (int x = tid; x < 2048 / 16; x += kThreads) reinterpret_cast<uint4*>(smem + SM::W)[x] = make_uint4(0u, 0u, 0u, 0u);
+    for (int x = tid; x < 2048 / 16; x += kQueryThreads) reinterpret_cast<uint4*>(smem + SM::W)[x] = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
     pdl_enter();  // launched with programmatic dependent launch
     if (warp == 0) {
@@ -114,12 +134,13 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     const uint32_t tmem = bar->tmem;
     Walk w(rows, kRowChunk, bar->span);
 
+    if (warp < 4) reg_dec<80>();
     if (warp == 0) {
         if (lane == 0) {
-            long long i = 0, heads = 0;
+            int i = 0, heads = 0;
             bool first = true;
             for (; w.more(); w.next(), ++i) {
-                const int s = (int)(i % NS);
+                const int s = i % NS;
                 if (!mbar_wait(&bar->empty[s], ((i / NS) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
                 uint8_t* st = smem + s * SM::kStage;
                 mbar_arrive_expect_tx(&bar->full[s], (KB + VB) * T);
@@ -148,14 +169,14 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                id_w = idesc_bf16_f32(128, 16, 1, 0);
             const uint32_t aS = smem_u32(smem + SM::S0), aSl = aS + (uint32_t)image_part(KB, VB), aW = smem_u32(smem + SM::W),
                            aX = smem_u32(smem + SM::X0);
-            bool ok = true;
-            long long yi = 0, heads = 0;
-            Walk wy = w;  // Y of a chunk is issued before X^T dO of the chunk before: dO is all it needs
-            bool y_first = true;
-            auto issue_y = [&]() {
-                const int g = (int)(yi & 1), s = (int)(yi % NS);
+            bool ok = true, y_first = true, first = true, r_first = true;
+            int yi = 0, ri = 0, heads = 0, flushes = 0;
+            Walk wy = w;
+            auto issue_y = [&]() {  // Y of chunk yi: dO is all it needs, so it runs a chunk ahead
+                const int g = yi & 1, s = yi % NS;
                 if (y_first) ok = ok && mbar_wait(&bar->s_full, heads++ & 1, err, LA_ERR_TIMEOUT);
-                ok = ok && mbar_wait(&bar->full[s], (yi / NS) & 1, err, LA_ERR_TIMEOUT);
+                ok = ok && mbar_wait(&bar->full[s], (yi / NS) & 1, err, LA_ERR_TIMEOUT) &&
+                     mbar_wait(&bar->y_free[g], ((yi >> 1) & 1) ^ 1, err, LA_ERR_TIMEOUT);
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t aD = smem_u32(smem + s * SM::kStage + SM::kDo), acc = tmem + kY + 64 * KB * g;
@@ -170,95 +191,115 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 wy.next();
                 ++yi;
             };
-            long long i = 0, flushes = 0;
-            bool first = true;
-            for (; w.more() && ok; w.next(), ++i) {
-                const int g = (int)(i & 1), s = (int)(i % NS);
-                while (ok && wy.more() && yi <= i) issue_y();
-                // the next chunk's Y (its group's previous chunk, i - 1, is through), unless it needs the next head's S, for
-                // which all of this head's chunks have to be through
-                if (ok && wy.more() && yi == i + 1 && !y_first) issue_y();
+            auto issue_r = [&]() {  // X^T t of chunk ri (of X's hi part for KB = 2: t is smaller than dO . v)
+                const int g = ri & 1, s = ri % NS;
+                ok = ok && mbar_wait(&bar->w_ready[g], (ri >> 1) & 1, err, LA_ERR_TIMEOUT);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem + s * SM::kStage);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) mma_ss(tmem + kW, desc_mn(st, kk, T), desc_k(aW, kk, 1024), id_w, !r_first || kk > 0);
+                mma_commit(&bar->r_done[g]);
+                r_first = false;
+                ++ri;
+            };
+            for (int i = 0; w.more() && ok; w.next(), ++i) {
+                const int g = i & 1, s = i % NS;
+                while (ok && yi <= i) issue_y();
+                ok = ok && mbar_wait(&bar->x_ready[g], (i >> 1) & 1, err, LA_ERR_TIMEOUT);
+                if (first && flushes > 0) ok = ok && mbar_wait(&bar->r_flushed, (flushes - 1) & 1, err, LA_ERR_TIMEOUT);
                 if (!ok) break;
-                if (!mbar_wait(&bar->ready[g], (i >> 1) & 1, err, LA_ERR_TIMEOUT)) break;
-                if (first && flushes > 0 && !mbar_wait(&bar->r_flushed, (flushes - 1) & 1, err, LA_ERR_TIMEOUT)) break;
                 tc_fence_after();
                 const uint32_t st = smem_u32(smem + s * SM::kStage), aD = st + SM::kDo;
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) {
-                    const uint64_t x = desc_mn(st, kk, T), d = desc_mn(aD, kk, T), t = desc_k(aW, kk, 1024);
-                    mma_ss(tmem + kR, x, d, id_r, !first || kk > 0);
-                    mma_ss(tmem + kW, x, t, id_w, !first || kk > 0);
-                    if (KB == 2) {
-                        const uint64_t xl = desc_mn(aX, kk, T);
-                        mma_ss(tmem + kR, xl, d, id_r, 1);
-                        mma_ss(tmem + kW, xl, t, id_w, 1);
-                    }
+                    mma_ss(tmem + kR, desc_mn(st, kk, T), desc_mn(aD, kk, T), id_r, !first || kk > 0);
+                    if (KB == 2) mma_ss(tmem + kR, desc_mn(aX, kk, T), desc_mn(aD, kk, T), id_r, 1);
                 }
                 mma_commit(&bar->x_free);
-                mma_commit(&bar->r_done[g]);
                 first = w.last();
-                if (first) ++flushes;
+                while (ok && ri < (first ? i + 1 : i)) issue_r();  // a head's are all issued before the next head begins
+                if (first) r_first = true, ++flushes;
+                if (ok && wy.more() && yi == i + 1 && !y_first) issue_y();  // unless it needs the next head's S
             }
             mma_commit(&bar->final_mma);  // every product is complete before the accumulators are given back
             mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
         }
-    } else if (warp < 10) {
-        const int g = (warp - 2) >> 2, r = 32 * (warp & 3) + lane;
+    } else if (warp == 2) {
+        if (lane == 0) {  // stores: a stage is empty once its dq has been read
+            for (int i = 0; w.more(); w.next(), ++i) {
+                const int s = i % NS;
+                if (!mbar_wait(&bar->staged[s], (i / NS) & 1, err, LA_ERR_TIMEOUT)) break;
+                check_copy(0, w.row0(), rows.M, w.bh, rows.heads());
+                for (int b = 0; b < KB; ++b) tma_store_3d(&tm_dq, smem + s * SM::kStage + b * T, 64 * b, w.row0(), w.bh);
+                bulk_commit();
+                bulk_wait_read_all();
+                mbar_arrive(&bar->empty[s]);
+            }
+            bulk_wait_all();
+        }
+    } else if (warp >= 4) {
+        reg_inc<208>();
+        const int g = (warp - 4) >> 2, r = 32 * (warp & 3) + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, acc = tmem + kY + 64 * KB * g + lanes;
-        long long i = 0, heads = 0;
+        int i = 0, heads = 0;
         bool first = true;
         for (; w.more(); w.next(), ++i) {
             if (first) ++heads;
             const bool last = first = w.last();
-            const bool mine = (i & 1) == g;
-            if (mine) {
-                const int s = (int)(i % NS);
+            if ((i & 1) == g) {
+                const int s = i % NS;
                 uint8_t* st = smem + s * SM::kStage;
                 if (!warp_wait(&bar->s_full, (heads - 1) & 1, err) || !warp_wait(&bar->full[s], (i / NS) & 1, err)) break;
-                // phi of the row, and its normaliser
-                float p[64 * KB], den = 0.f;
+                // phi of the row, its normaliser, X (rows behind the last query and padded columns, which hold phi(0): 0)
+                float2 p[32 * KB], s2 = both(0.f);
                 row_words<KB>(st, r, [&](int b, int lc, const uint32_t(&u)[4]) {
-                    const float4 za = *reinterpret_cast<const float4*>(zs + 64 * b + 8 * lc);
-                    const float4 zb = *reinterpret_cast<const float4*>(zs + 64 * b + 8 * lc + 4);
-                    const float zv[8] = {za.x, za.y, za.z, za.w, zb.x, zb.y, zb.z, zb.w};
+                    float2 zv[4];
+                    Pairs<float>::get(zs + 64 * b + 8 * lc, reinterpret_cast<float2(&)[2]>(zv[0]));
+                    Pairs<float>::get(zs + 64 * b + 8 * lc + 4, reinterpret_cast<float2(&)[2]>(zv[2]));
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float f = phi_f(e & 1 ? bf_hi(u[e >> 1]) : bf_lo(u[e >> 1]));
-                        p[64 * b + 8 * lc + e] = f;
-                        den = fmaf(f, zv[e], den);
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = make_float2(phi_f(bf_lo(u[e])), phi_f(bf_hi(u[e])));
+                        p[32 * b + 4 * lc + e] = f;
+                        s2 = fma2(f, zv[e], s2);
                     }
                 });
-                const float inv = over(den);
-                if (!warp_wait(&bar->y_done[g], (i >> 1) & 1, err)) break;
-                tc_fence_after();
-                float t = 0.f;
-#pragma unroll
-                for (int b = 0; b < 2 * KB; ++b) {
-                    uint32_t y[32];
-                    tmem_ld32(acc + 32 * b, y);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) t = fmaf(p[32 * b + e], __uint_as_float(y[e]), t);
-                }
-                t *= inv;
-                // X and t for the sums (rows behind the last query: 0), after the product that read the lo tile and W before
-                const float xi = r < w.rows() ? inv : 0.f;
-                if (i > 0 && !warp_wait(&bar->x_free, (i - 1) & 1, err)) break;
+                const float inv = over(s2.x + s2.y), xi = r < w.rows() ? inv : 0.f;
+                // KB = 2: the product that reads the lo tile of the chunk before is through
+                if (KB == 2 && i > 0 && !warp_wait(&bar->x_free, (i - 1) & 1, err)) break;
                 uint8_t* lo = KB == 2 ? smem + SM::X0 : st + SM::kLo;
 #pragma unroll
                 for (int b = 0; b < KB; ++b)
 #pragma unroll
                     for (int lc = 0; lc < 8; ++lc) {
                         uint4 h, l;
-                        const float* f = p + 64 * b + 8 * lc;
-                        const float k = 64 * b + 8 * lc < Dk ? xi : 0.f;  // padded columns hold phi(0)
-                        split2(f[0] * k, f[1] * k, h.x, l.x);
-                        split2(f[2] * k, f[3] * k, h.y, l.y);
-                        split2(f[4] * k, f[5] * k, h.z, l.z);
-                        split2(f[6] * k, f[7] * k, h.w, l.w);
+                        uint32_t *hw = reinterpret_cast<uint32_t*>(&h), *lw = reinterpret_cast<uint32_t*>(&l);
+                        const float2 k = both(64 * b + 8 * lc < Dk ? xi : 0.f);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 x = mul2(p[32 * b + 4 * lc + e], k);
+                            split2(x.x, x.y, hw[e], lw[e]);
+                        }
                         *reinterpret_cast<uint4*>(st + b * T + swz(r, lc)) = h;
                         *reinterpret_cast<uint4*>(lo + b * T + swz(r, lc)) = l;
                     }
+                fence_proxy_async_smem();
+                mbar_arrive(&bar->x_ready[g]);
+                // t = phi(q) . Y / den
+                if (!warp_wait(&bar->y_done[g], (i >> 1) & 1, err)) break;
+                tc_fence_after();
+                s2 = both(0.f);
+#pragma unroll
+                for (int b = 0; b < 2 * KB; ++b) {
+                    uint32_t y[32];
+                    tmem_ld32(acc + 32 * b, y);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        s2 = fma2(p[16 * b + e], make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), s2);
+                }
+                const float t = (s2.x + s2.y) * inv;
+                if (i > 0 && !warp_wait(&bar->r_done[(i - 1) & 1], ((i - 1) >> 1) & 1, err)) break;  // W is read
                 {
                     uint32_t th, tl;
                     split2(-t, 0.f, th, tl);
@@ -268,9 +309,9 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     *reinterpret_cast<uint16_t*>(at + swz(1, lc)) = (uint16_t)tl;
                 }
                 fence_proxy_async_smem();
-                tc_fence_before();
-                // dq while the sums are formed: the row is kept packed until its tile is free
-                const float gz = -t * inv;
+                mbar_arrive(&bar->w_ready[g]);
+                // dq, packed until the row's tile is free
+                const float2 gz = both(-t * inv), iv = both(inv);
                 uint32_t dq[32 * KB];
 #pragma unroll
                 for (int b = 0; b < 2 * KB; ++b) {
@@ -278,18 +319,21 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     tmem_ld32(acc + 32 * b, y);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 zv = *reinterpret_cast<const float4*>(zs + 32 * b + e);
-                        const float* f = p + 32 * b + e;
-                        dq[16 * b + e / 2] = pack_bf16x2(fmaf(gz, zv.x, __uint_as_float(y[e]) * inv) * dphi_from_phi(f[0]),
-                                                         fmaf(gz, zv.y, __uint_as_float(y[e + 1]) * inv) * dphi_from_phi(f[1]));
-                        dq[16 * b + e / 2 + 1] =
-                            pack_bf16x2(fmaf(gz, zv.z, __uint_as_float(y[e + 2]) * inv) * dphi_from_phi(f[2]),
-                                        fmaf(gz, zv.w, __uint_as_float(y[e + 3]) * inv) * dphi_from_phi(f[3]));
+                    for (int e = 0; e < 16; e += 2) {
+                        float2 zv[2];
+                        Pairs<float>::get(zs + 32 * b + 2 * e, zv);
+#pragma unroll
+                        for (int o = 0; o < 2; ++o) {
+                            const int c = 2 * (e + o);
+                            const float2 f = p[16 * b + e + o];
+                            const float2 d = mul2(fma2(gz, zv[o], mul2(iv, make_float2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])))),
+                                                  make_float2(dphi_from_phi(f.x), dphi_from_phi(f.y)));
+                            dq[16 * b + e + o] = pack_bf16x2(d.x, d.y);
+                        }
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(&bar->ready[g]);  // Y has been read, X and t are in place
+                mbar_arrive(&bar->y_free[g]);
                 if (!warp_wait(&bar->r_done[g], (i >> 1) & 1, err)) break;
 #pragma unroll
                 for (int b = 0; b < KB; ++b)
@@ -318,18 +362,6 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 if (lane == 0) mbar_arrive(&bar->s_empty);
             }
         }
-    } else if (lane == 0) {
-        // stores: a stage is empty once its dq has been read
-        for (long long i = 0; w.more(); w.next(), ++i) {
-            const int s = (int)(i % NS);
-            if (!mbar_wait(&bar->staged[s], (i / NS) & 1, err, LA_ERR_TIMEOUT)) break;
-            check_copy(0, w.row0(), rows.M, w.bh, rows.heads());
-            for (int b = 0; b < KB; ++b) tma_store_3d(&tm_dq, smem + s * SM::kStage + b * T, 64 * b, w.row0(), w.bh);
-            bulk_commit();
-            bulk_wait_read_all();
-            mbar_arrive(&bar->empty[s]);
-        }
-        bulk_wait_all();
     }
     tc_fence_before();
     __syncthreads();
@@ -340,11 +372,12 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 }
 
 // ------------------------------------------------------------------ key pass
-// A stage holds K (phi's bf16 copy in place, then dk) and V (then dv).  phi(K) enters dv's product rounded once: its errors
-// are independent from column to column of R, whose entries are not.  phi'(k) is formed from k itself.
+// A stage holds K (phi's bf16 copy in place) and V; then dv and, VB blocks on, dk.  V R^T starts as V lands, and its
+// epilogue runs beside phi(K) R where dk's place is not K's (KB <= VB).  phi(K) enters dv's product rounded once: its
+// errors are independent from column to column of R, whose entries are not.  phi'(k) is formed from k itself.
 template <int KB, int VB>
 struct KeySmem {
-    static constexpr int kV = KB * T, kStage = (KB + VB) * T, kR = 2 * (int)image_part(KB, VB);
+    static constexpr int kV = KB * T, kDk = VB * T, kStage = (KB + VB) * T, kR = 2 * (int)image_part(KB, VB);
     static constexpr int kStages = (229376 - kR) / kStage > 4 ? 4 : (229376 - kR) / kStage;
     static constexpr int R0 = kStages * kStage, r0 = R0 + kR, bars = r0 + 512, total = bars + 512;
     static_assert(kStages >= 2 && total <= 232448, "key pass: shared memory");
@@ -361,7 +394,7 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     constexpr uint32_t kCols = 2 * kSet <= 256 ? 256 : 512;
     extern __shared__ __align__(1024) uint8_t smem[];
     struct Bars {
-        uint64_t full[4], empty[4], staged[4], s_full, s_empty, ready[2], done[2], final_mma;
+        uint64_t full[4], empty[4], staged[4], s_full, s_empty, ready[2], k_done[2], v_done[2], acc_free[2], final_mma;
         uint32_t tmem;
         Span span;
     };
@@ -378,7 +411,9 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&bar->ready[g], 128);
-            mbar_init(&bar->done[g], 1);
+            mbar_init(&bar->k_done[g], 1);
+            mbar_init(&bar->v_done[g], 1);
+            mbar_init(&bar->acc_free[g], 128);
         }
         mbar_init(&bar->s_full, 1);
         mbar_init(&bar->s_empty, 9);  // the products and the eight compute warps (r)
@@ -407,10 +442,10 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
 
     if (warp == 0) {
         if (lane == 0) {
-            long long i = 0, heads = 0;
+            int i = 0, heads = 0;
             bool first = true;
             for (; w.more(); w.next(), ++i) {
-                const int s = (int)(i % NS);
+                const int s = i % NS;
                 if (!mbar_wait(&bar->empty[s], ((i / NS) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
                 uint8_t* st = smem + s * SM::kStage;
                 mbar_arrive_expect_tx(&bar->full[s], (KB + VB) * T);
@@ -437,28 +472,42 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         if (lane == 0) {
             constexpr uint32_t id_k = idesc_bf16_f32(128, 64 * KB, 0, 0), id_v = idesc_bf16_f32(128, 64 * VB, 0, 1);
             const uint32_t aR = smem_u32(smem + SM::R0), aRl = aR + (uint32_t)image_part(KB, VB);
-            long long i = 0, heads = 0;
-            bool first = true;
-            for (; w.more(); w.next(), ++i) {
-                const int g = (int)(i & 1), s = (int)(i % NS);
-                if (first && !mbar_wait(&bar->s_full, heads++ & 1, err, LA_ERR_TIMEOUT)) break;
-                // phi(K) is in place, and the group has read the products of its previous chunk
-                if (!mbar_wait(&bar->ready[g], (i >> 1) & 1, err, LA_ERR_TIMEOUT)) break;
+            int i = 0, vi = 0, heads = 0;
+            Walk wv = w;  // V R^T runs a chunk ahead
+            bool v_first = true, ok = true;
+            auto issue_k = [&]() {  // dK without r and phi' of chunk vi
+                const int g = vi & 1, s = vi % NS;
+                if (v_first) ok = ok && mbar_wait(&bar->s_full, heads++ & 1, err, LA_ERR_TIMEOUT);
+                ok = ok && mbar_wait(&bar->full[s], (vi / NS) & 1, err, LA_ERR_TIMEOUT) &&
+                     mbar_wait(&bar->acc_free[g], ((vi >> 1) & 1) ^ 1, err, LA_ERR_TIMEOUT);
+                if (!ok) return;
                 tc_fence_after();
-                const uint32_t aK = smem_u32(smem + s * SM::kStage), aV = aK + SM::kV, acc = tmem + kSet * g;
+                const uint32_t aV = smem_u32(smem + s * SM::kStage + SM::kV), acc = tmem + kSet * g;
 #pragma unroll
                 for (int kk = 0; kk < 4 * VB; ++kk) {
                     mma_ss(acc, desc_k(aV, kk, T), desc_k(aR, kk, 8192 * KB), id_k, kk > 0);
                     mma_ss(acc, desc_k(aV, kk, T), desc_k(aRl, kk, 8192 * KB), id_k, 1);
                 }
+                mma_commit(&bar->k_done[g]);
+                v_first = wv.last();
+                wv.next();
+                ++vi;
+            };
+            for (; w.more() && ok; w.next(), ++i) {
+                const int g = i & 1, s = i % NS;
+                while (ok && vi <= i) issue_k();
+                if (!ok || !mbar_wait(&bar->ready[g], (i >> 1) & 1, err, LA_ERR_TIMEOUT)) break;
+                tc_fence_after();
+                const uint32_t aK = smem_u32(smem + s * SM::kStage), acc = tmem + kSet * g + 64 * KB;
 #pragma unroll
                 for (int kk = 0; kk < 4 * KB; ++kk) {
-                    mma_ss(acc + 64 * KB, desc_k(aK, kk, T), desc_mn(aR, kk, 8192 * KB), id_v, kk > 0);
-                    mma_ss(acc + 64 * KB, desc_k(aK, kk, T), desc_mn(aRl, kk, 8192 * KB), id_v, 1);
+                    mma_ss(acc, desc_k(aK, kk, T), desc_mn(aR, kk, 8192 * KB), id_v, kk > 0);
+                    mma_ss(acc, desc_k(aK, kk, T), desc_mn(aRl, kk, 8192 * KB), id_v, 1);
                 }
-                mma_commit(&bar->done[g]);
-                first = w.last();
-                if (first) mma_commit(&bar->s_empty);
+                mma_commit(&bar->v_done[g]);
+                if (w.last()) mma_commit(&bar->s_empty);
+                // the next chunk's, unless it needs the next head's R, for which this head has to be through
+                if (wv.more() && vi == i + 1 && !v_first) issue_k();
             }
             mma_commit(&bar->final_mma);  // every product is complete before the accumulators are given back
             mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
@@ -466,13 +515,13 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     } else if (warp < 10) {
         const int g = (warp - 2) >> 2, r = 32 * (warp & 3) + lane;
         const uint32_t acc = tmem + kSet * g + ((uint32_t)(32 * (warp & 3)) << 16);
-        long long i = 0, heads = 0;
+        int i = 0, heads = 0;
         bool first = true;
         for (; w.more(); w.next(), ++i) {
             if (first) ++heads;
             const bool last = first = w.last();
             if ((i & 1) == g) {
-                const int s = (int)(i % NS);
+                const int s = i % NS;
                 const bool live = r < w.rows();
                 uint8_t* st = smem + s * SM::kStage;
                 if (!warp_wait(&bar->s_full, (heads - 1) & 1, err) || !warp_wait(&bar->full[s], (i / NS) & 1, err)) break;
@@ -488,9 +537,9 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                     *reinterpret_cast<uint4*>(st + b * T + swz(r, lc)) = x;
                 });
                 fence_proxy_async_smem();
-                tc_fence_before();
                 mbar_arrive(&bar->ready[g]);
-                if (!warp_wait(&bar->done[g], (i >> 1) & 1, err)) break;
+                if (KB > VB && !warp_wait(&bar->v_done[g], (i >> 1) & 1, err)) break;  // dk lies over phi(K)
+                if (!warp_wait(&bar->k_done[g], (i >> 1) & 1, err)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int b = 0; b < 2 * KB; ++b) {
@@ -513,9 +562,11 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                                                (__uint_as_float(y[8 * c + 2 * e + 1]) + rr[2 * e + 1]) * s1);
                         }
                         if (!live) x = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4*>(st + (b >> 1) * T + swz(r, 4 * (b & 1) + c)) = x;
+                        *reinterpret_cast<uint4*>(st + SM::kDk + (b >> 1) * T + swz(r, 4 * (b & 1) + c)) = x;
                     }
                 }
+                if (KB <= VB && !warp_wait(&bar->v_done[g], (i >> 1) & 1, err)) break;
+                tc_fence_after();
 #pragma unroll
                 for (int b = 0; b < 2 * VB; ++b) {
                     uint32_t y[32];
@@ -529,10 +580,12 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                         for (int e = 0; e < 4; ++e)
                             o[e] = pack_bf16x2(__uint_as_float(y[8 * c + 2 * e]), __uint_as_float(y[8 * c + 2 * e + 1]));
                         if (!live) x = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4*>(st + SM::kV + (b >> 1) * T + swz(r, 4 * (b & 1) + c)) = x;
+                        *reinterpret_cast<uint4*>(st + (b >> 1) * T + swz(r, 4 * (b & 1) + c)) = x;
                     }
                 }
                 fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(&bar->acc_free[g]);
                 mbar_arrive(&bar->staged[s]);
             }
             if (last) {  // r is no longer read
@@ -542,13 +595,13 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         }
     } else if (lane == 0) {
         // stores: a stage is empty once its outputs have been read
-        for (long long i = 0; w.more(); w.next(), ++i) {
-            const int s = (int)(i % NS);
+        for (int i = 0; w.more(); w.next(), ++i) {
+            const int s = i % NS;
             if (!mbar_wait(&bar->staged[s], (i / NS) & 1, err, LA_ERR_TIMEOUT)) break;
             const uint8_t* st = smem + s * SM::kStage;
             check_copy(0, w.row0(), keys.M, w.bh, keys.heads());
-            for (int b = 0; b < KB; ++b) tma_store_3d(&tm_dk, st + b * T, 64 * b, w.row0(), w.bh);
-            for (int b = 0; b < VB; ++b) tma_store_3d(&tm_dv, st + SM::kV + b * T, 64 * b, w.row0(), w.bh);
+            for (int b = 0; b < KB; ++b) tma_store_3d(&tm_dk, st + SM::kDk + b * T, 64 * b, w.row0(), w.bh);
+            for (int b = 0; b < VB; ++b) tma_store_3d(&tm_dv, st + b * T, 64 * b, w.row0(), w.bh);
             bulk_commit();
             bulk_wait_read_all();
             mbar_arrive(&bar->empty[s]);
@@ -586,7 +639,7 @@ cudaError_t tc_bwd(const BwdArgs& a, const la_cross_shape& s, char* ws, cudaStre
         return cudaErrorInvalidValue;
     int* err = device_error_word();
     auto go = [&](auto query, size_t qs, auto key, size_t ks) {
-        CR_TRY(tc_run("cross_query_tc", query, dim3(l.query_ctas), kThreads, qs, st, tq, td, tdq, (const char*)ws + l.S, rec, rows,
+        CR_TRY(tc_run("cross_query_tc", query, dim3(l.query_ctas), kQueryThreads, qs, st, tq, td, tdq, (const char*)ws + l.S, rec, rows,
                       s.Dk, l.query_ctas + rows.heads(), err));
         CR_TRY(tc_join(rec, nullptr, nullptr, ws + l.R, nullptr, nullptr, rows, kRowChunk, l.query_ctas, s, st));
         return tc_run("cross_key_tc", key, dim3(l.key_ctas), kThreads, ks, st, tk, tv, tdk, tdv, (const char*)ws + l.R, keys, err);

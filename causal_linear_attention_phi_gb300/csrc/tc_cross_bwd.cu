@@ -8,8 +8,8 @@
 // their products as they land, without a pass over them.  dq is a small difference of large terms (the keys' weights vary
 // little), so S enters as two bf16 parts and everything else of dq is fp32; dk keeps a rounding of X's and R's whole size, so R
 // is two parts, and X as well.  Bound by memory: a chunk of 128 rows, 128 wide, is 96 KB (query) or 128 KB (key), 2.2 and 2.9 us
-// of an SM's share of the copy rate, against 2 and 1.4 us for its products.  Two groups of four warps take alternate
-// chunks, a thread a row; outputs go back into the stage's tiles for their store.
+// of an SM's share of the copy rate, against 2 and 1.4 us for its products.  Two groups of eight warps take alternate
+// chunks, half a row to a thread; outputs go back into the stage's tiles for their store.
 #include <cudaTypedefs.h>
 
 #include "norm_common.cuh"
@@ -26,7 +26,6 @@ using norm::Pairs;
 using tc::bf_hi;
 using tc::bf_lo;
 
-constexpr int kThreads = 352;  // warp 0 TMA loads, 1 MMA, 2-9 two compute groups, 10 TMA stores
 constexpr int T = 16384;       // 128 rows of a block
 
 // A warpgroup gives registers back, or takes them, down or up to n a thread.
@@ -35,17 +34,33 @@ __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.al
 template <int n>
 __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n)); }
 
-// A row of a tile through f(first column, its 16 bytes as 4 words): f may change the words.
-template <int B, typename F>
-__device__ __forceinline__ void row_words(const uint8_t* tile, int r, F f) {
-#pragma unroll
-    for (int b = 0; b < B; ++b)
-#pragma unroll
-        for (int lc = 0; lc < 8; ++lc) {
-            const uint4 x = *reinterpret_cast<const uint4*>(tile + b * T + swz(r, lc));
-            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-            f(b, lc, u);
-        }
+// A float of each lane to a column of tensor memory, for another warp of the same lanes to read after a barrier.
+__device__ __forceinline__ void tmem_put(uint32_t taddr, float x) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(x)) : "memory");
+    tmem_st_wait();
+    tc_fence_before();
+}
+// The sum of two neighbouring columns.
+__device__ __forceinline__ float tmem_sum2(uint32_t taddr) {
+    uint32_t a, b;
+    tc_fence_after();
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(taddr));
+    tmem_ld_wait();
+    return __uint_as_float(a) + __uint_as_float(b);
+}
+
+// Whether v holds for both warps of a pair (barrier `id`, 64 threads); what either wrote to shared memory is then seen by both.
+__device__ __forceinline__ bool pair_all(int id, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, %2, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id)
+        : "memory");
+    return r != 0;
 }
 
 // ------------------------------------------------------------------ query pass
@@ -54,10 +69,12 @@ __device__ __forceinline__ void row_words(const uint8_t* tile, int r, F f) {
 // (hi and lo) of a 16-column operand W, K-major, of whose rows only 8 are held: rows 8-15 of a block are read from the 1 KB
 // behind it (the other block's rows, or z and the barriers) and make columns of the result that nothing reads.
 //
-// The compute warps hold their row's phi in fp32 throughout (128 registers), which they get from the other warpgroup:
-// 384 threads of 168 registers are 128 of 80 and 256 of 208.  A chunk's phases, each overlapping the other group's:
+// Two groups of eight warps; a thread holds half a row's phi in fp32 throughout, and the two threads of a row join their parts of
+// den and of t through tensor memory, shared memory being full (a whole row to a thread took 343 us where this takes 264 us: twice the code, of which the
+// instruction cache held half, and two warps to a scheduler).  Registers come from the other warpgroup: 640 threads of 96
+// are 128 of 56 and 512 of 104.  A chunk's phases, each overlapping the other group's:
 //   phi, den, X -> X^T dO may start;   Y -> t -> X^T t may start;   Y -> dq, which waits for X's tile.
-constexpr int kQueryThreads = 384;  // warp 0 TMA loads, 1 MMA, 2 TMA stores, 4-11 two compute groups
+constexpr int kQueryThreads = 640;  // warp 0 TMA loads, 1 MMA of Y and R, 2 TMA stores, 3 MMA of r, 4-19 two compute groups
 
 template <int KB, int VB>
 struct QuerySmem {
@@ -68,7 +85,8 @@ struct QuerySmem {
     static constexpr int W = X0 + kX;          // 2 blocks of 8 rows x 128 bytes
     static constexpr int z0 = W + 2048;        // float[64 KB]
     static constexpr int bars = z0 + 512;
-    static constexpr int total = bars + 512;   // W's last read ends here
+    static constexpr int total = bars + 512;
+    static_assert(total >= W + 2 * 1024 + 1024, "the product's last read of W ends in the block's shared memory");
     static_assert(kStages >= 2 && total <= 232448, "query pass: shared memory");
 };
 
@@ -79,12 +97,12 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                int slots, int* err) {
     using SM = QuerySmem<KB, VB>;
     constexpr int NS = SM::kStages;
-    constexpr uint32_t kY = 0, kR = 128 * KB, kW = kR + 64 * VB;  // TMEM: two Y, R, the columns of r
-    constexpr uint32_t kCols = kW + 16 <= 256 ? 256 : 512;
+    constexpr uint32_t kY = 0, kR = 128 * KB, kW = kR + 64 * VB, kX = kW + 16;  // TMEM: two Y, R, r's 16, the halves' sums
+    constexpr uint32_t kCols = kX + 8 <= 256 ? 256 : 512;
     extern __shared__ __align__(1024) uint8_t smem[];
     struct Bars {
         uint64_t full[4], empty[4], staged[4], s_full, s_empty, y_done[2], y_free[2], x_ready[2], w_ready[2], r_done[2], x_free, r_flushed,
-            final_mma;
+            final_mma, final_r;
         uint32_t tmem;
         Span span;
     };
@@ -97,20 +115,21 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         for (int s = 0; s < NS; ++s) {
             mbar_init(&bar->full[s], 1);
             mbar_init(&bar->empty[s], 1);
-            mbar_init(&bar->staged[s], 128);
+            mbar_init(&bar->staged[s], 256);
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&bar->y_done[g], 1);
-            mbar_init(&bar->y_free[g], 128);
-            mbar_init(&bar->x_ready[g], 128);
-            mbar_init(&bar->w_ready[g], 128);
-            mbar_init(&bar->r_done[g], 1);
+            mbar_init(&bar->y_free[g], 256);
+            mbar_init(&bar->x_ready[g], 256);
+            mbar_init(&bar->w_ready[g], 256);
+            mbar_init(&bar->r_done[g], 2);  // R's product and r's
         }
         mbar_init(&bar->s_full, 1);
-        mbar_init(&bar->s_empty, 9);  // the products and the eight compute warps (z)
+        mbar_init(&bar->s_empty, 17);  // the products and the compute warps (z)
         mbar_init(&bar->x_free, 1);
-        mbar_init(&bar->r_flushed, 128);
+        mbar_init(&bar->r_flushed, 256);
         mbar_init(&bar->final_mma, 1);
+        mbar_init(&bar->final_r, 1);
         fence_mbar_init();
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_do);
@@ -134,7 +153,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     const uint32_t tmem = bar->tmem;
     Walk w(rows, kRowChunk, bar->span);
 
-    if (warp < 4) reg_dec<80>();
+    if (warp < 4) reg_dec<56>();
     if (warp == 0) {
         if (lane == 0) {
             int i = 0, heads = 0;
@@ -165,12 +184,10 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            constexpr uint32_t id_y = idesc_bf16_f32(128, 64 * KB, 0, 0), id_r = idesc_bf16_f32(128, 64 * VB, 1, 1),
-                               id_w = idesc_bf16_f32(128, 16, 1, 0);
-            const uint32_t aS = smem_u32(smem + SM::S0), aSl = aS + (uint32_t)image_part(KB, VB), aW = smem_u32(smem + SM::W),
-                           aX = smem_u32(smem + SM::X0);
-            bool ok = true, y_first = true, first = true, r_first = true;
-            int yi = 0, ri = 0, heads = 0, flushes = 0;
+            constexpr uint32_t id_y = idesc_bf16_f32(128, 64 * KB, 0, 0), id_r = idesc_bf16_f32(128, 64 * VB, 1, 1);
+            const uint32_t aS = smem_u32(smem + SM::S0), aSl = aS + (uint32_t)image_part(KB, VB), aX = smem_u32(smem + SM::X0);
+            bool ok = true, y_first = true, first = true;
+            int yi = 0, heads = 0, flushes = 0;
             Walk wy = w;
             auto issue_y = [&]() {  // Y of chunk yi: dO is all it needs, so it runs a chunk ahead
                 const int g = yi & 1, s = yi % NS;
@@ -191,18 +208,6 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 wy.next();
                 ++yi;
             };
-            auto issue_r = [&]() {  // X^T t of chunk ri (of X's hi part for KB = 2: t is smaller than dO . v)
-                const int g = ri & 1, s = ri % NS;
-                ok = ok && mbar_wait(&bar->w_ready[g], (ri >> 1) & 1, err, LA_ERR_TIMEOUT);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t st = smem_u32(smem + s * SM::kStage);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk) mma_ss(tmem + kW, desc_mn(st, kk, T), desc_k(aW, kk, 1024), id_w, !r_first || kk > 0);
-                mma_commit(&bar->r_done[g]);
-                r_first = false;
-                ++ri;
-            };
             for (int i = 0; w.more() && ok; w.next(), ++i) {
                 const int g = i & 1, s = i % NS;
                 while (ok && yi <= i) issue_y();
@@ -217,13 +222,37 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     if (KB == 2) mma_ss(tmem + kR, desc_mn(aX, kk, T), desc_mn(aD, kk, T), id_r, 1);
                 }
                 mma_commit(&bar->x_free);
+                mma_commit(&bar->r_done[g]);
                 first = w.last();
-                while (ok && ri < (first ? i + 1 : i)) issue_r();  // a head's are all issued before the next head begins
-                if (first) r_first = true, ++flushes;
+                if (first) ++flushes;
                 if (ok && wy.more() && yi == i + 1 && !y_first) issue_y();  // unless it needs the next head's S
             }
             mma_commit(&bar->final_mma);  // every product is complete before the accumulators are given back
             mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
+        }
+    } else if (warp == 3) {
+        // r's products are ready later than R's, and their own thread's: behind one that waits for the other group's X they
+        // held each group back until the other had caught up (358 us of B=2 H=16 N=32768 128 x 128)
+        if (lane == 0) {
+            constexpr uint32_t id_w = idesc_bf16_f32(128, 16, 1, 0);
+            const uint32_t aW = smem_u32(smem + SM::W);
+            bool first = true;
+            int flushes = 0;
+            for (int i = 0; w.more(); w.next(), ++i) {
+                const int g = i & 1, s = i % NS;
+                if (!mbar_wait(&bar->w_ready[g], (i >> 1) & 1, err, LA_ERR_TIMEOUT)) break;
+                if (first && flushes > 0 && !mbar_wait(&bar->r_flushed, (flushes - 1) & 1, err, LA_ERR_TIMEOUT)) break;
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem + s * SM::kStage);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)  // X's hi part alone for KB = 2: t is smaller than dO . v
+                    mma_ss(tmem + kW, desc_mn(st, kk, T), desc_k(aW, kk, 1024), id_w, !first || kk > 0);
+                mma_commit(&bar->r_done[g]);
+                first = w.last();
+                if (first) ++flushes;
+            }
+            mma_commit(&bar->final_r);  // as above
+            mbar_wait(&bar->final_r, 0, err, LA_ERR_TIMEOUT);
         }
     } else if (warp == 2) {
         if (lane == 0) {  // stores: a stage is empty once its dq has been read
@@ -239,119 +268,124 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             bulk_wait_all();
         }
     } else if (warp >= 4) {
-        reg_inc<208>();
-        const int g = (warp - 4) >> 2, r = 32 * (warp & 3) + lane;
-        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, acc = tmem + kY + 64 * KB * g + lanes;
+        reg_inc<104>();
+        constexpr int kHalf = 32 * KB;  // columns of this thread: its half of row r
+        const int g = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, r = 32 * (warp & 3) + lane, pair = 1 + 4 * g + (warp & 3);
+        const int c0 = kHalf * half, blk = (c0 >> 6) * T, lc0 = (c0 >> 3) & 7;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, acc = tmem + kY + 64 * KB * g + c0 + lanes;
+        const uint32_t sums = tmem + kX + 4 * g + lanes;  // columns: den of either half, t of either half
         int i = 0, heads = 0;
-        bool first = true;
+        bool first = true, ok = true;
         for (; w.more(); w.next(), ++i) {
             if (first) ++heads;
             const bool last = first = w.last();
             if ((i & 1) == g) {
                 const int s = i % NS;
                 uint8_t* st = smem + s * SM::kStage;
-                if (!warp_wait(&bar->s_full, (heads - 1) & 1, err) || !warp_wait(&bar->full[s], (i / NS) & 1, err)) break;
-                // phi of the row, its normaliser, X (rows behind the last query and padded columns, which hold phi(0): 0)
-                float2 p[32 * KB], s2 = both(0.f);
-                row_words<KB>(st, r, [&](int b, int lc, const uint32_t(&u)[4]) {
+                ok = warp_wait(&bar->s_full, (heads - 1) & 1, err) && warp_wait(&bar->full[s], (i / NS) & 1, err);
+                // phi of the half row, its part of the normaliser
+                float2 p[kHalf / 2], s2 = both(0.f);
+#pragma unroll
+                for (int c = 0; c < kHalf / 8; ++c) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(st + blk + swz(r, lc0 + c));
+                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
                     float2 zv[4];
-                    Pairs<float>::get(zs + 64 * b + 8 * lc, reinterpret_cast<float2(&)[2]>(zv[0]));
-                    Pairs<float>::get(zs + 64 * b + 8 * lc + 4, reinterpret_cast<float2(&)[2]>(zv[2]));
+                    Pairs<float>::get(zs + c0 + 8 * c, reinterpret_cast<float2(&)[2]>(zv[0]));
+                    Pairs<float>::get(zs + c0 + 8 * c + 4, reinterpret_cast<float2(&)[2]>(zv[2]));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 f = make_float2(phi_f(bf_lo(u[e])), phi_f(bf_hi(u[e])));
-                        p[32 * b + 4 * lc + e] = f;
-                        s2 = fma2(f, zv[e], s2);
+                        p[4 * c + e] = make_float2(phi_f(bf_lo(u[e])), phi_f(bf_hi(u[e])));
+                        s2 = fma2(p[4 * c + e], zv[e], s2);
                     }
-                });
-                const float inv = over(s2.x + s2.y), xi = r < w.rows() ? inv : 0.f;
+                }
+                tmem_put(sums + half, s2.x + s2.y);
                 // KB = 2: the product that reads the lo tile of the chunk before is through
-                if (KB == 2 && i > 0 && !warp_wait(&bar->x_free, (i - 1) & 1, err)) break;
+                if (KB == 2 && i > 0) ok = ok && warp_wait(&bar->x_free, (i - 1) & 1, err);
+                if (!(ok = pair_all(pair, ok))) break;  // both halves are in
+                const float inv = over(tmem_sum2(sums)), xi = r < w.rows() ? inv : 0.f;
+                // X (rows behind the last query and padded columns, which hold phi(0): 0)
                 uint8_t* lo = KB == 2 ? smem + SM::X0 : st + SM::kLo;
 #pragma unroll
-                for (int b = 0; b < KB; ++b)
+                for (int c = 0; c < kHalf / 8; ++c) {
+                    uint4 h, l;
+                    uint32_t *hw = reinterpret_cast<uint32_t*>(&h), *lw = reinterpret_cast<uint32_t*>(&l);
+                    const float2 k = both(c0 + 8 * c < Dk ? xi : 0.f);
 #pragma unroll
-                    for (int lc = 0; lc < 8; ++lc) {
-                        uint4 h, l;
-                        uint32_t *hw = reinterpret_cast<uint32_t*>(&h), *lw = reinterpret_cast<uint32_t*>(&l);
-                        const float2 k = both(64 * b + 8 * lc < Dk ? xi : 0.f);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 x = mul2(p[32 * b + 4 * lc + e], k);
-                            split2(x.x, x.y, hw[e], lw[e]);
-                        }
-                        *reinterpret_cast<uint4*>(st + b * T + swz(r, lc)) = h;
-                        *reinterpret_cast<uint4*>(lo + b * T + swz(r, lc)) = l;
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 x = mul2(p[4 * c + e], k);
+                        split2(x.x, x.y, hw[e], lw[e]);
                     }
+                    *reinterpret_cast<uint4*>(st + blk + swz(r, lc0 + c)) = h;
+                    *reinterpret_cast<uint4*>(lo + blk + swz(r, lc0 + c)) = l;
+                }
                 fence_proxy_async_smem();
                 mbar_arrive(&bar->x_ready[g]);
                 // t = phi(q) . Y / den
-                if (!warp_wait(&bar->y_done[g], (i >> 1) & 1, err)) break;
+                ok = warp_wait(&bar->y_done[g], (i >> 1) & 1, err);
                 tc_fence_after();
                 s2 = both(0.f);
 #pragma unroll
                 for (int b = 0; b < 2 * KB; ++b) {
-                    uint32_t y[32];
-                    tmem_ld32(acc + 32 * b, y);
+                    uint32_t y[16];
+                    tmem_ld16(acc + 16 * b, y);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        s2 = fma2(p[16 * b + e], make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), s2);
+                    for (int e = 0; e < 8; ++e)
+                        s2 = fma2(p[8 * b + e], make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), s2);
                 }
-                const float t = (s2.x + s2.y) * inv;
-                if (i > 0 && !warp_wait(&bar->r_done[(i - 1) & 1], ((i - 1) >> 1) & 1, err)) break;  // W is read
-                {
+                tmem_put(sums + 2 + half, s2.x + s2.y);
+                if (i > 0) ok = ok && warp_wait(&bar->r_done[(i - 1) & 1], ((i - 1) >> 1) & 1, err);  // W has been read
+                if (!(ok = pair_all(pair, ok))) break;
+                const float t = tmem_sum2(sums + 2) * inv;
+                if (half == 0) {
                     uint32_t th, tl;
                     split2(-t, 0.f, th, tl);
                     uint8_t* at = smem + SM::W + (r >> 6) * 1024 + (r & 7) * 2;
                     const int lc = (r & 63) >> 3;  // rows 0 and 1 of the operand
                     *reinterpret_cast<uint16_t*>(at + swz(0, lc)) = (uint16_t)th;
                     *reinterpret_cast<uint16_t*>(at + swz(1, lc)) = (uint16_t)tl;
+                    fence_proxy_async_smem();
                 }
-                fence_proxy_async_smem();
                 mbar_arrive(&bar->w_ready[g]);
                 // dq, packed until the row's tile is free
                 const float2 gz = both(-t * inv), iv = both(inv);
-                uint32_t dq[32 * KB];
+                uint32_t dq[kHalf / 2];
 #pragma unroll
                 for (int b = 0; b < 2 * KB; ++b) {
-                    uint32_t y[32];
-                    tmem_ld32(acc + 32 * b, y);
+                    uint32_t y[16];
+                    tmem_ld16(acc + 16 * b, y);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
+                    for (int e = 0; e < 8; e += 2) {
                         float2 zv[2];
-                        Pairs<float>::get(zs + 32 * b + 2 * e, zv);
+                        Pairs<float>::get(zs + c0 + 16 * b + 2 * e, zv);
 #pragma unroll
                         for (int o = 0; o < 2; ++o) {
                             const int c = 2 * (e + o);
-                            const float2 f = p[16 * b + e + o];
+                            const float2 f = p[8 * b + e + o];
                             const float2 d = mul2(fma2(gz, zv[o], mul2(iv, make_float2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])))),
                                                   make_float2(dphi_from_phi(f.x), dphi_from_phi(f.y)));
-                            dq[16 * b + e + o] = pack_bf16x2(d.x, d.y);
+                            dq[8 * b + e + o] = pack_bf16x2(d.x, d.y);
                         }
                     }
                 }
                 tc_fence_before();
                 mbar_arrive(&bar->y_free[g]);
-                if (!warp_wait(&bar->r_done[g], (i >> 1) & 1, err)) break;
+                if (!(ok = pair_all(pair, warp_wait(&bar->r_done[g], (i >> 1) & 1, err)))) break;
 #pragma unroll
-                for (int b = 0; b < KB; ++b)
-#pragma unroll
-                    for (int lc = 0; lc < 8; ++lc)
-                        *reinterpret_cast<uint4*>(st + b * T + swz(r, lc)) =
-                            make_uint4(dq[32 * b + 4 * lc], dq[32 * b + 4 * lc + 1], dq[32 * b + 4 * lc + 2], dq[32 * b + 4 * lc + 3]);
+                for (int c = 0; c < kHalf / 8; ++c)
+                    *reinterpret_cast<uint4*>(st + blk + swz(r, lc0 + c)) = make_uint4(dq[4 * c], dq[4 * c + 1], dq[4 * c + 2], dq[4 * c + 3]);
                 fence_proxy_async_smem();
                 mbar_arrive(&bar->staged[s]);
                 if (last) {  // this head's sums
                     tc_fence_after();
                     if (LA_DCHECK((int)blockIdx.x + w.bh < slots)) {
                         float* out = rec + (size_t)(blockIdx.x + w.bh) * record_floats(VB);
-                        tc::tmem_row_to_global<64 * VB>(tmem + kR + lanes, out + (size_t)r * 64 * VB);
+                        tc::tmem_row_to_global<32 * VB>(tmem + kR + 32 * VB * half + lanes, out + (size_t)r * 64 * VB + 32 * VB * half);
                         uint32_t c[16];
                         tmem_ld16(tmem + kW + lanes, c);
                         tmem_ld_wait();
-                        out[128 * 64 * VB + r] = __uint_as_float(c[0]) + __uint_as_float(c[1]);
+                        if (half == 0) out[128 * 64 * VB + r] = __uint_as_float(c[0]) + __uint_as_float(c[1]);
                     }
                     tc_fence_before();
                     mbar_arrive(&bar->r_flushed);
@@ -375,6 +409,9 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 // A stage holds K (phi's bf16 copy in place) and V; then dv and, VB blocks on, dk.  V R^T starts as V lands, and its
 // epilogue runs beside phi(K) R where dk's place is not K's (KB <= VB).  phi(K) enters dv's product rounded once: its
 // errors are independent from column to column of R, whose entries are not.  phi'(k) is formed from k itself.
+// Two groups of eight warps, half a row to a thread.
+constexpr int kKeyThreads = 608;  // warp 0 TMA loads, 1 MMA, 2-17 two compute groups, 18 TMA stores
+
 template <int KB, int VB>
 struct KeySmem {
     static constexpr int kV = KB * T, kDk = VB * T, kStage = (KB + VB) * T, kR = 2 * (int)image_part(KB, VB);
@@ -384,7 +421,7 @@ struct KeySmem {
 };
 
 template <int KB, int VB>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kKeyThreads, 1)
 cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
              const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv, const char* __restrict__ image,
              Rows keys, int* err) {
@@ -407,16 +444,16 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         for (int s = 0; s < NS; ++s) {
             mbar_init(&bar->full[s], 1);
             mbar_init(&bar->empty[s], 1);
-            mbar_init(&bar->staged[s], 128);
+            mbar_init(&bar->staged[s], 256);
         }
         for (int g = 0; g < 2; ++g) {
-            mbar_init(&bar->ready[g], 128);
+            mbar_init(&bar->ready[g], 256);
             mbar_init(&bar->k_done[g], 1);
             mbar_init(&bar->v_done[g], 1);
-            mbar_init(&bar->acc_free[g], 128);
+            mbar_init(&bar->acc_free[g], 256);
         }
         mbar_init(&bar->s_full, 1);
-        mbar_init(&bar->s_empty, 9);  // the products and the eight compute warps (r)
+        mbar_init(&bar->s_empty, 17);  // the products and the compute warps (r)
         mbar_init(&bar->final_mma, 1);
         fence_mbar_init();
         tma_prefetch_desc(&tm_k);
@@ -512,8 +549,10 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             mma_commit(&bar->final_mma);  // every product is complete before the accumulators are given back
             mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
         }
-    } else if (warp < 10) {
-        const int g = (warp - 2) >> 2, r = 32 * (warp & 3) + lane;
+    } else if (warp < 18) {
+        constexpr int kHalfK = 32 * KB, kHalfV = 32 * VB;  // columns of this thread: its half of row r
+        const int g = (warp - 2) >> 3, half = ((warp - 2) >> 2) & 1, r = 32 * (warp & 3) + lane;
+        const int ck = kHalfK * half, cv = kHalfV * half;
         const uint32_t acc = tmem + kSet * g + ((uint32_t)(32 * (warp & 3)) << 16);
         int i = 0, heads = 0;
         bool first = true;
@@ -525,52 +564,52 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                 const bool live = r < w.rows();
                 uint8_t* st = smem + s * SM::kStage;
                 if (!warp_wait(&bar->s_full, (heads - 1) & 1, err) || !warp_wait(&bar->full[s], (i / NS) & 1, err)) break;
-                uint32_t k[32 * KB];
-                row_words<KB>(st, r, [&](int b, int lc, const uint32_t(&u)[4]) {
-                    uint4 x;
+                uint4 k[kHalfK / 8];
+#pragma unroll
+                for (int c = 0; c < kHalfK / 8; ++c) {
+                    uint4* at = reinterpret_cast<uint4*>(st + (ck >> 6) * T + swz(r, ((ck >> 3) & 7) + c));
+                    uint4 x = k[c] = *at;
                     uint32_t* p = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        k[32 * b + 4 * lc + e] = u[e];
-                        p[e] = pack_bf16x2(phi_f(bf_lo(u[e])), phi_f(bf_hi(u[e])));
-                    }
-                    *reinterpret_cast<uint4*>(st + b * T + swz(r, lc)) = x;
-                });
+                    for (int e = 0; e < 4; ++e) p[e] = pack_bf16x2(phi_f(bf_lo(p[e])), phi_f(bf_hi(p[e])));
+                    *at = x;
+                }
                 fence_proxy_async_smem();
                 mbar_arrive(&bar->ready[g]);
                 if (KB > VB && !warp_wait(&bar->v_done[g], (i >> 1) & 1, err)) break;  // dk lies over phi(K)
                 if (!warp_wait(&bar->k_done[g], (i >> 1) & 1, err)) break;
                 tc_fence_after();
 #pragma unroll
-                for (int b = 0; b < 2 * KB; ++b) {
+                for (int b = 0; b < kHalfK / 32; ++b) {
                     uint32_t y[32];
-                    tmem_ld32(acc + 32 * b, y);
+                    tmem_ld32(acc + ck + 32 * b, y);
                     tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint4 x;
                         uint32_t* o = reinterpret_cast<uint32_t*>(&x);
-                        const float4 ra = *reinterpret_cast<const float4*>(rs + 32 * b + 8 * c);
-                        const float4 rb = *reinterpret_cast<const float4*>(rs + 32 * b + 8 * c + 4);
-                        const float rr[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
+                        const uint32_t* kw = reinterpret_cast<const uint32_t*>(&k[4 * b + c]);
+                        float2 rr[4];
+                        Pairs<float>::get(rs + ck + 32 * b + 8 * c, reinterpret_cast<float2(&)[2]>(rr[0]));
+                        Pairs<float>::get(rs + ck + 32 * b + 8 * c + 4, reinterpret_cast<float2(&)[2]>(rr[2]));
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const uint32_t kw = k[16 * b + 4 * c + e];
-                            const float s0 = ex2_approx(fminf(bf_lo(kw), 0.f) * 1.4426950408889634f);
-                            const float s1 = ex2_approx(fminf(bf_hi(kw), 0.f) * 1.4426950408889634f);
-                            o[e] = pack_bf16x2((__uint_as_float(y[8 * c + 2 * e]) + rr[2 * e]) * s0,
-                                               (__uint_as_float(y[8 * c + 2 * e + 1]) + rr[2 * e + 1]) * s1);
+                            const float2 slope = make_float2(ex2_approx(fminf(bf_lo(kw[e]), 0.f) * 1.4426950408889634f),
+                                                             ex2_approx(fminf(bf_hi(kw[e]), 0.f) * 1.4426950408889634f));
+                            const float2 d = mul2(norm::add2(make_float2(__uint_as_float(y[8 * c + 2 * e]), __uint_as_float(y[8 * c + 2 * e + 1])),
+                                                             rr[e]), slope);
+                            o[e] = pack_bf16x2(d.x, d.y);
                         }
                         if (!live) x = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4*>(st + SM::kDk + (b >> 1) * T + swz(r, 4 * (b & 1) + c)) = x;
+                        *reinterpret_cast<uint4*>(st + SM::kDk + ((ck + 32 * b) >> 6) * T + swz(r, (((ck + 32 * b) >> 3) & 7) + c)) = x;
                     }
                 }
                 if (KB <= VB && !warp_wait(&bar->v_done[g], (i >> 1) & 1, err)) break;
                 tc_fence_after();
 #pragma unroll
-                for (int b = 0; b < 2 * VB; ++b) {
+                for (int b = 0; b < kHalfV / 32; ++b) {
                     uint32_t y[32];
-                    tmem_ld32(acc + 64 * KB + 32 * b, y);
+                    tmem_ld32(acc + 64 * KB + cv + 32 * b, y);
                     tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -580,7 +619,7 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                         for (int e = 0; e < 4; ++e)
                             o[e] = pack_bf16x2(__uint_as_float(y[8 * c + 2 * e]), __uint_as_float(y[8 * c + 2 * e + 1]));
                         if (!live) x = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4*>(st + (b >> 1) * T + swz(r, 4 * (b & 1) + c)) = x;
+                        *reinterpret_cast<uint4*>(st + ((cv + 32 * b) >> 6) * T + swz(r, (((cv + 32 * b) >> 3) & 7) + c)) = x;
                     }
                 }
                 fence_proxy_async_smem();
@@ -642,7 +681,7 @@ cudaError_t tc_bwd(const BwdArgs& a, const la_cross_shape& s, char* ws, cudaStre
         CR_TRY(tc_run("cross_query_tc", query, dim3(l.query_ctas), kQueryThreads, qs, st, tq, td, tdq, (const char*)ws + l.S, rec, rows,
                       s.Dk, l.query_ctas + rows.heads(), err));
         CR_TRY(tc_join(rec, nullptr, nullptr, ws + l.R, nullptr, nullptr, rows, kRowChunk, l.query_ctas, s, st));
-        return tc_run("cross_key_tc", key, dim3(l.key_ctas), kThreads, ks, st, tk, tv, tdk, tdv, (const char*)ws + l.R, keys, err);
+        return tc_run("cross_key_tc", key, dim3(l.key_ctas), kKeyThreads, ks, st, tk, tv, tdk, tdv, (const char*)ws + l.R, keys, err);
     };
     cudaError_t e;
     switch (2 * blocks64(s.Dk) + blocks64(s.Dv)) {

@@ -17,9 +17,6 @@ namespace la {
 namespace cross {
 namespace {
 
-using tc::bf_hi;
-using tc::bf_lo;
-
 // ------------------------------------------------------------------ sums over the keys
 // A stage holds a chunk of 64 rows: K (phi's hi part in place), its lo part, V.  For KB = 1 hi and lo are the two 64-row
 // halves of one 128-row product; else they are two products.  An accumulator in tensor memory takes kPeriod chunks only:
@@ -135,11 +132,12 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         constexpr int kOwn = 16 * VB;  // columns of this warp's sums, of the rows 32 (warp % 4) ..
         const int col0 = kOwn * (cw >> 2);
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        float zp[KB][8], sum[kOwn];
+        float2 zp[KB][4];
+        float sum[kOwn];
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) zp[b][e] = 0.f;
+            for (int e = 0; e < 4; ++e) zp[b][e] = norm::both(0.f);
 #pragma unroll
         for (int e = 0; e < kOwn; ++e) sum[e] = 0.f;
         int i = 0, period = 0, flushed = 0, heads = 0;
@@ -183,10 +181,9 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         uint32_t* ul = reinterpret_cast<uint32_t*>(&l);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float p0 = live ? phi_f(bf_lo(u[e])) : 0.f, p1 = live ? phi_f(bf_hi(u[e])) : 0.f;
-                            zp[b][2 * e] += p0;
-                            zp[b][2 * e + 1] += p1;
-                            split2(p0, p1, u[e], ul[e]);
+                            const float2 p = live ? phi2(unpack2(u[e])) : norm::both(0.f);
+                            zp[b][e] = norm::add2(zp[b][e], p);
+                            split2(p, u[e], ul[e]);
                         }
                         *reinterpret_cast<uint4*>(st + b * T + 4096 * j) = x[b][j];
                         *reinterpret_cast<uint4*>(st + SM::kLo + b * T + 4096 * j) = l;
@@ -217,11 +214,11 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             for (int b = 0; b < KB; ++b)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    float z = zp[b][e];
+                    float z = e & 1 ? zp[b][e >> 1].y : zp[b][e >> 1].x;
                     z += __shfl_xor_sync(0xffffffffu, z, 9);
                     z += __shfl_xor_sync(0xffffffffu, z, 18);
                     if (lane < 8) to[64 * b + e] = z;
-                    zp[b][e] = 0.f;
+                    if (e & 1) zp[b][e >> 1] = norm::both(0.f);
                 }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar->z_ready[a]);
@@ -316,10 +313,10 @@ cross_join_tc(const float* __restrict__ rec, const float* __restrict__ S, const 
         }
     }
     uint4 hi, lo;
-    split2(v[0], v[1], hi.x, lo.x);
-    split2(v[2], v[3], hi.y, lo.y);
-    split2(v[4], v[5], hi.z, lo.z);
-    split2(v[6], v[7], hi.w, lo.w);
+    split2(make_float2(v[0], v[1]), hi.x, lo.x);
+    split2(make_float2(v[2], v[3]), hi.y, lo.y);
+    split2(make_float2(v[4], v[5]), hi.z, lo.z);
+    split2(make_float2(v[6], v[7]), hi.w, lo.w);
     const int off = (c8 >> 6) * (64 * KB * 128) + swz(d, c8 >> 3);
     *reinterpret_cast<uint4*>(im + off) = hi;
     *reinterpret_cast<uint4*>(im + image_part(KB, VB) + off) = lo;
@@ -456,7 +453,7 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             uint8_t* st = smem + s * SM::kStage;
             const float* zs = reinterpret_cast<const float*>(smem + SM::z0 + h * 256 * KB);
             if (!warp_wait(&bar->s_full[h], ((heads - 1) >> 1) & 1, err) || !warp_wait(&bar->full[s], (i / NS) & 1, err)) break;
-            float den = 0.f;
+            float2 den = norm::both(0.f);
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
 #pragma unroll
@@ -464,19 +461,18 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     uint4* p = reinterpret_cast<uint4*>(st + b * T + swz(r, lc));
                     uint4 x = *p;
                     uint32_t* u = reinterpret_cast<uint32_t*>(&x);
-                    const float4 za = *reinterpret_cast<const float4*>(zs + 64 * b + 8 * lc);
-                    const float4 zb = *reinterpret_cast<const float4*>(zs + 64 * b + 8 * lc + 4);
-                    const float zv[8] = {za.x, za.y, za.z, za.w, zb.x, zb.y, zb.z, zb.w};
+                    float2 zv[4];
+                    norm::Pairs<float>::get(zs + 64 * b + 8 * lc, reinterpret_cast<float2(&)[2]>(zv[0]));
+                    norm::Pairs<float>::get(zs + 64 * b + 8 * lc + 4, reinterpret_cast<float2(&)[2]>(zv[2]));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        u[e] = pack_bf16x2(phi_f(bf_lo(u[e])), phi_f(bf_hi(u[e])));
-                        den = fmaf(bf_lo(u[e]), zv[2 * e], den);  // of the rounded phi, as the product has it
-                        den = fmaf(bf_hi(u[e]), zv[2 * e + 1], den);
+                        u[e] = pack2(phi2(unpack2(u[e])));
+                        den = norm::fma2(unpack2(u[e]), zv[e], den);  // of the rounded phi, as the product has it
                     }
                     *p = x;
                 }
             }
-            const float inv = over(den);
+            const float2 inv = norm::both(over(den.x + den.y));
             fence_proxy_async_smem();
             tc_fence_before();
             mbar_arrive(&bar->ready[g]);
@@ -493,7 +489,7 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     uint32_t* u = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        u[e] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]) * inv, __uint_as_float(o[8 * c + 2 * e + 1]) * inv);
+                        u[e] = pack2(norm::mul2(make_float2(__uint_as_float(o[8 * c + 2 * e]), __uint_as_float(o[8 * c + 2 * e + 1])), inv));
                     *reinterpret_cast<uint4*>(st + (b >> 1) * T + swz(r, 4 * (b & 1) + c)) = x;
                 }
             }

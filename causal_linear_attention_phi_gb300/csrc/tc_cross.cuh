@@ -12,6 +12,7 @@
 #include <cuda.h>
 
 #include "cross.cuh"
+#include "norm_common.cuh"
 #include "shared_memory.cuh"
 #include "tc_common.cuh"
 
@@ -52,10 +53,17 @@ __device__ __forceinline__ void check_copy(int x, int row, int rows, int bh, int
     LA_DCHECK((x == 0 || x == 64) && row >= 0 && row < rows && bh >= 0 && bh < heads);
 }
 
+// phi of two values, as phi_f, with the product and the sum of both in one instruction each.
+__device__ __forceinline__ float2 phi2(float2 x) {
+    const float2 t = norm::mul2(make_float2(fminf(x.x, 0.f), fminf(x.y, 0.f)), norm::both(1.4426950408889634f));
+    return norm::add2(make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)), make_float2(ex2_approx(t.x), ex2_approx(t.y)));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(tc::bf_lo(w), tc::bf_hi(w)); }
+__device__ __forceinline__ uint32_t pack2(float2 x) { return pack_bf16x2(x.x, x.y); }
 // hi and lo bf16 parts of two floats.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = pack_bf16x2(a, b);
-    lo = pack_bf16x2(a - tc::bf_lo(hi), b - tc::bf_hi(hi));
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+    hi = pack2(x);
+    lo = pack2(norm::fma2(unpack2(hi), norm::both(-1.f), x));
 }
 
 // host

@@ -6,13 +6,12 @@
 //
 // t needs no product of its own: dO . (phi(q) S) is phi(q) . (S dO), the row sum that the epilogue of Y forms.  dO and V enter
 // their products as they land, without a pass over them.  dq is a small difference of large terms (the keys' weights vary
-// little), so S enters as two bf16 parts and everything else of dq is fp32; dk keeps a rounding of X's and R's whole size, so R
-// is two parts, and X as well.  Bound by memory: a chunk of 128 rows, 128 wide, is 96 KB (query) or 128 KB (key), 2.2 and 2.9 us
-// of an SM's share of the copy rate, against 2 and 1.4 us for its products.  Two groups of eight warps take alternate
+// little), so S enters as two bf16 parts and everything else of dq is fp32; dk keeps a rounding of X's and of R's whole size: R is two parts,
+// X one (see below).  Bound by memory: a chunk of 128 rows, 128 wide, is 96 KB (query) or 128 KB (key), 2.2 and 2.9 us
+// of an SM's share of the copy rate, against 1.4 us for its products.  Two groups of eight warps take alternate
 // chunks, half a row to a thread; outputs go back into the stage's tiles for their store.
 #include <cudaTypedefs.h>
 
-#include "norm_common.cuh"
 #include "tc_cross.cuh"
 
 namespace la {
@@ -64,25 +63,27 @@ __device__ __forceinline__ bool pair_all(int id, bool v) {
 }
 
 // ------------------------------------------------------------------ query pass
-// A stage holds Q (then X's hi part, then dq) and dO.  X's lo part: for KB = 1 in the stage, the second 64-row half of one
-// 128-row product; for KB = 2 in a tile of its own, for which shared memory has no second.  t enters as the first two columns
+// A stage holds Q (then X) and dO; dq has a tile of its own, so a stage is free as soon as its products are through.  X is rounded
+// once for KB = 2: dk is then 1.4 times as far off as its own rounding makes it (a second part would double the product
+// and its reads of shared memory, which is what bounds this kernel: 280 us instead of 190 at B=2 H=16 N=32768).  For KB = 1 a lo part fills the
+// second 64-row half of the 128-row product for nothing.  t enters as the first two columns
 // (hi and lo) of a 16-column operand W, K-major, of whose rows only 8 are held: rows 8-15 of a block are read from the 1 KB
 // behind it (the other block's rows, or z and the barriers) and make columns of the result that nothing reads.
 //
 // Two groups of eight warps; a thread holds half a row's phi in fp32 throughout, and the two threads of a row join their parts of
-// den and of t through tensor memory, shared memory being full (a whole row to a thread took 343 us where this takes 264 us: twice the code, of which the
+// den and of t through tensor memory, shared memory being full (a whole row to a thread took 343 us where this took 264: twice the code, of which the
 // instruction cache held half, and two warps to a scheduler).  Registers come from the other warpgroup: 640 threads of 96
 // are 128 of 56 and 512 of 104.  A chunk's phases, each overlapping the other group's:
-//   phi, den, X -> X^T dO may start;   Y -> t -> X^T t may start;   Y -> dq, which waits for X's tile.
+//   phi, den, X -> X^T dO may start;   Y -> t -> X^T t may start;   Y -> dq.
 constexpr int kQueryThreads = 640;  // warp 0 TMA loads, 1 MMA of Y and R, 2 TMA stores, 3 MMA of r, 4-19 two compute groups
 
 template <int KB, int VB>
 struct QuerySmem {
-    static constexpr int kLo = KB == 1 ? T : 0, kDo = (KB == 1 ? 2 : KB) * T, kStage = kDo + VB * T;
-    static constexpr int kS = 2 * (int)image_part(KB, VB), kX = KB == 2 ? KB * T : 0;
-    static constexpr int kStages = (229376 - kS - kX) / kStage > 4 ? 4 : (229376 - kS - kX) / kStage;
-    static constexpr int S0 = kStages * kStage, X0 = S0 + kS;
-    static constexpr int W = X0 + kX;          // 2 blocks of 8 rows x 128 bytes
+    static constexpr int kLo = T, kDo = 2 * T, kStage = kDo + VB * T;  // Q: two blocks, or X's parts
+    static constexpr int kS = 2 * (int)image_part(KB, VB), kOut = KB * T;
+    static constexpr int kStages = (229376 - kS - kOut) / kStage > 4 ? 4 : (229376 - kS - kOut) / kStage;
+    static constexpr int S0 = kStages * kStage, O0 = S0 + kS;
+    static constexpr int W = O0 + kOut;        // 2 blocks of 8 rows x 128 bytes
     static constexpr int z0 = W + 2048;        // float[64 KB]
     static constexpr int bars = z0 + 512;
     static constexpr int total = bars + 512;
@@ -101,7 +102,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     constexpr uint32_t kCols = kX + 8 <= 256 ? 256 : 512;
     extern __shared__ __align__(1024) uint8_t smem[];
     struct Bars {
-        uint64_t full[4], empty[4], staged[4], s_full, s_empty, y_done[2], y_free[2], x_ready[2], w_ready[2], r_done[2], x_free, r_flushed,
+        uint64_t full[4], empty[4], staged, out_free, s_full, s_empty, y_done[2], y_free[2], x_ready[2], w_ready[2], r_done[2], r_flushed,
             final_mma, final_r;
         uint32_t tmem;
         Span span;
@@ -114,9 +115,10 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     if (tid == 32) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&bar->full[s], 1);
-            mbar_init(&bar->empty[s], 1);
-            mbar_init(&bar->staged[s], 256);
+            mbar_init(&bar->empty[s], 2);  // R's product and r's
         }
+        mbar_init(&bar->staged, 256);
+        mbar_init(&bar->out_free, 1);
         for (int g = 0; g < 2; ++g) {
             mbar_init(&bar->y_done[g], 1);
             mbar_init(&bar->y_free[g], 256);
@@ -126,7 +128,6 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         mbar_init(&bar->s_full, 1);
         mbar_init(&bar->s_empty, 17);  // the products and the compute warps (z)
-        mbar_init(&bar->x_free, 1);
         mbar_init(&bar->r_flushed, 256);
         mbar_init(&bar->final_mma, 1);
         mbar_init(&bar->final_r, 1);
@@ -164,8 +165,8 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 uint8_t* st = smem + s * SM::kStage;
                 mbar_arrive_expect_tx(&bar->full[s], (KB + VB) * T);
                 check_copy(0, w.row0(), rows.M, w.bh, rows.heads());
-                for (int b = 0; b < VB; ++b) tma_load_3d(st + SM::kDo + b * T, &tm_do, 64 * b, w.row0(), w.bh, &bar->full[s]);
                 for (int b = 0; b < KB; ++b) tma_load_3d(st + b * T, &tm_q, 64 * b, w.row0(), w.bh, &bar->full[s]);
+                for (int b = 0; b < VB; ++b) tma_load_3d(st + SM::kDo + b * T, &tm_do, 64 * b, w.row0(), w.bh, &bar->full[s]);
                 if (first) {  // after the chunk's own tiles: those need no wait for the head before
                     if (!mbar_wait(&bar->s_empty, (heads & 1) ^ 1, err, LA_ERR_TIMEOUT)) {
                         ++i;
@@ -185,7 +186,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     } else if (warp == 1) {
         if (lane == 0) {
             constexpr uint32_t id_y = idesc_bf16_f32(128, 64 * KB, 0, 0), id_r = idesc_bf16_f32(128, 64 * VB, 1, 1);
-            const uint32_t aS = smem_u32(smem + SM::S0), aSl = aS + (uint32_t)image_part(KB, VB), aX = smem_u32(smem + SM::X0);
+            const uint32_t aS = smem_u32(smem + SM::S0), aSl = aS + (uint32_t)image_part(KB, VB);
             bool ok = true, y_first = true, first = true;
             int yi = 0, heads = 0, flushes = 0;
             Walk wy = w;
@@ -217,12 +218,10 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 tc_fence_after();
                 const uint32_t st = smem_u32(smem + s * SM::kStage), aD = st + SM::kDo;
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
+                for (int kk = 0; kk < 8; ++kk)
                     mma_ss(tmem + kR, desc_mn(st, kk, T), desc_mn(aD, kk, T), id_r, !first || kk > 0);
-                    if (KB == 2) mma_ss(tmem + kR, desc_mn(aX, kk, T), desc_mn(aD, kk, T), id_r, 1);
-                }
-                mma_commit(&bar->x_free);
                 mma_commit(&bar->r_done[g]);
+                mma_commit(&bar->empty[s]);
                 first = w.last();
                 if (first) ++flushes;
                 if (ok && wy.more() && yi == i + 1 && !y_first) issue_y();  // unless it needs the next head's S
@@ -245,9 +244,10 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 tc_fence_after();
                 const uint32_t st = smem_u32(smem + s * SM::kStage);
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)  // X's hi part alone for KB = 2: t is smaller than dO . v
+                for (int kk = 0; kk < 8; ++kk)
                     mma_ss(tmem + kW, desc_mn(st, kk, T), desc_k(aW, kk, 1024), id_w, !first || kk > 0);
                 mma_commit(&bar->r_done[g]);
+                mma_commit(&bar->empty[s]);
                 first = w.last();
                 if (first) ++flushes;
             }
@@ -255,15 +255,14 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             mbar_wait(&bar->final_r, 0, err, LA_ERR_TIMEOUT);
         }
     } else if (warp == 2) {
-        if (lane == 0) {  // stores: a stage is empty once its dq has been read
+        if (lane == 0) {  // stores
             for (int i = 0; w.more(); w.next(), ++i) {
-                const int s = i % NS;
-                if (!mbar_wait(&bar->staged[s], (i / NS) & 1, err, LA_ERR_TIMEOUT)) break;
+                if (!mbar_wait(&bar->staged, i & 1, err, LA_ERR_TIMEOUT)) break;
                 check_copy(0, w.row0(), rows.M, w.bh, rows.heads());
-                for (int b = 0; b < KB; ++b) tma_store_3d(&tm_dq, smem + s * SM::kStage + b * T, 64 * b, w.row0(), w.bh);
+                for (int b = 0; b < KB; ++b) tma_store_3d(&tm_dq, smem + SM::O0 + b * T, 64 * b, w.row0(), w.bh);
                 bulk_commit();
                 bulk_wait_read_all();
-                mbar_arrive(&bar->empty[s]);
+                mbar_arrive(&bar->out_free);
             }
             bulk_wait_all();
         }
@@ -294,17 +293,14 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     Pairs<float>::get(zs + c0 + 8 * c + 4, reinterpret_cast<float2(&)[2]>(zv[2]));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        p[4 * c + e] = make_float2(phi_f(bf_lo(u[e])), phi_f(bf_hi(u[e])));
+                        p[4 * c + e] = phi2(unpack2(u[e]));
                         s2 = fma2(p[4 * c + e], zv[e], s2);
                     }
                 }
                 tmem_put(sums + half, s2.x + s2.y);
-                // KB = 2: the product that reads the lo tile of the chunk before is through
-                if (KB == 2 && i > 0) ok = ok && warp_wait(&bar->x_free, (i - 1) & 1, err);
                 if (!(ok = pair_all(pair, ok))) break;  // both halves are in
                 const float inv = over(tmem_sum2(sums)), xi = r < w.rows() ? inv : 0.f;
                 // X (rows behind the last query and padded columns, which hold phi(0): 0)
-                uint8_t* lo = KB == 2 ? smem + SM::X0 : st + SM::kLo;
 #pragma unroll
                 for (int c = 0; c < kHalf / 8; ++c) {
                     uint4 h, l;
@@ -312,11 +308,13 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const float2 k = both(c0 + 8 * c < Dk ? xi : 0.f);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 x = mul2(p[4 * c + e], k);
-                        split2(x.x, x.y, hw[e], lw[e]);
+                        if (KB == 1)
+                            split2(mul2(p[4 * c + e], k), hw[e], lw[e]);
+                        else
+                            hw[e] = pack2(mul2(p[4 * c + e], k));
                     }
                     *reinterpret_cast<uint4*>(st + blk + swz(r, lc0 + c)) = h;
-                    *reinterpret_cast<uint4*>(lo + blk + swz(r, lc0 + c)) = l;
+                    if (KB == 1) *reinterpret_cast<uint4*>(st + SM::kLo + swz(r, lc0 + c)) = l;
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&bar->x_ready[g]);
@@ -339,7 +337,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const float t = tmem_sum2(sums + 2) * inv;
                 if (half == 0) {
                     uint32_t th, tl;
-                    split2(-t, 0.f, th, tl);
+                    split2(make_float2(-t, 0.f), th, tl);
                     uint8_t* at = smem + SM::W + (r >> 6) * 1024 + (r & 7) * 2;
                     const int lc = (r & 63) >> 3;  // rows 0 and 1 of the operand
                     *reinterpret_cast<uint16_t*>(at + swz(0, lc)) = (uint16_t)th;
@@ -347,7 +345,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     fence_proxy_async_smem();
                 }
                 mbar_arrive(&bar->w_ready[g]);
-                // dq, packed until the row's tile is free
+                // dq, packed until the tile of outputs is free
                 const float2 gz = both(-t * inv), iv = both(inv);
                 uint32_t dq[kHalf / 2];
 #pragma unroll
@@ -365,18 +363,20 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                             const float2 f = p[8 * b + e + o];
                             const float2 d = mul2(fma2(gz, zv[o], mul2(iv, make_float2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])))),
                                                   make_float2(dphi_from_phi(f.x), dphi_from_phi(f.y)));
-                            dq[8 * b + e + o] = pack_bf16x2(d.x, d.y);
+                            dq[8 * b + e + o] = pack2(d);
                         }
                     }
                 }
                 tc_fence_before();
                 mbar_arrive(&bar->y_free[g]);
-                if (!(ok = pair_all(pair, warp_wait(&bar->r_done[g], (i >> 1) & 1, err)))) break;
+                // the tile of outputs is free once the chunk before has been stored
+                if (!(ok = pair_all(pair, i == 0 || warp_wait(&bar->out_free, (i - 1) & 1, err)))) break;
 #pragma unroll
                 for (int c = 0; c < kHalf / 8; ++c)
-                    *reinterpret_cast<uint4*>(st + blk + swz(r, lc0 + c)) = make_uint4(dq[4 * c], dq[4 * c + 1], dq[4 * c + 2], dq[4 * c + 3]);
+                    *reinterpret_cast<uint4*>(smem + SM::O0 + blk + swz(r, lc0 + c)) = make_uint4(dq[4 * c], dq[4 * c + 1], dq[4 * c + 2], dq[4 * c + 3]);
                 fence_proxy_async_smem();
-                mbar_arrive(&bar->staged[s]);
+                mbar_arrive(&bar->staged);
+                if (last && !(ok = pair_all(pair, warp_wait(&bar->r_done[g], (i >> 1) & 1, err)))) break;
                 if (last) {  // this head's sums
                     tc_fence_after();
                     if (LA_DCHECK((int)blockIdx.x + w.bh < slots)) {
@@ -571,7 +571,7 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                     uint4 x = k[c] = *at;
                     uint32_t* p = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) p[e] = pack_bf16x2(phi_f(bf_lo(p[e])), phi_f(bf_hi(p[e])));
+                    for (int e = 0; e < 4; ++e) p[e] = pack2(phi2(unpack2(p[e])));
                     *at = x;
                 }
                 fence_proxy_async_smem();
@@ -594,11 +594,12 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                         Pairs<float>::get(rs + ck + 32 * b + 8 * c + 4, reinterpret_cast<float2(&)[2]>(rr[2]));
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float2 slope = make_float2(ex2_approx(fminf(bf_lo(kw[e]), 0.f) * 1.4426950408889634f),
-                                                             ex2_approx(fminf(bf_hi(kw[e]), 0.f) * 1.4426950408889634f));
+                            const float2 low = mul2(make_float2(fminf(bf_lo(kw[e]), 0.f), fminf(bf_hi(kw[e]), 0.f)),
+                                                    both(1.4426950408889634f));
+                            const float2 slope = make_float2(ex2_approx(low.x), ex2_approx(low.y));
                             const float2 d = mul2(norm::add2(make_float2(__uint_as_float(y[8 * c + 2 * e]), __uint_as_float(y[8 * c + 2 * e + 1])),
                                                              rr[e]), slope);
-                            o[e] = pack_bf16x2(d.x, d.y);
+                            o[e] = pack2(d);
                         }
                         if (!live) x = make_uint4(0u, 0u, 0u, 0u);
                         *reinterpret_cast<uint4*>(st + SM::kDk + ((ck + 32 * b) >> 6) * T + swz(r, (((ck + 32 * b) >> 3) & 7) + c)) = x;

@@ -40,6 +40,7 @@ __device__ __forceinline__ float rcp(float x) {  // 1 ulp
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
 __device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2_approx(-1.4426950408889634f * x)); }
 
 template <int L>
@@ -53,7 +54,12 @@ __device__ __forceinline__ float lanes_sum(float x) {
 // A row is a head at a position; rows are numbered as the gate has them, position by position.  L lanes own a row, 16 bytes
 // each, so the gate's side is contiguous and the heads' side comes in whole rows.  A block takes kU rows to a lane group
 // at a time and issues all their loads before any arithmetic.
-constexpr int kBlock = 256, kU = 4;
+constexpr int kBlock = 256;
+constexpr int kFwdU = 4;
+// The gradient of bf16 rows: two rows at a time and four blocks to an SM (four and two: 488 us instead of 435 for B=2 H=16 N=65536
+// D=128); fp32 rows, half as long to a lane, are better off with four (203 us instead of 230 for N=16384 D=128).
+template <typename T>
+constexpr int bwd_u() { return sizeof(T) == 2 ? 2 : 4; }
 
 struct GatedRows {
     long long rows;       // B N H
@@ -82,32 +88,32 @@ struct Place {
 
 // norm's statistics of a row held by L lanes: v becomes x - mean; returns rstd.
 template <int L, int n>
-__device__ __forceinline__ float centre(float (&v)[n], float inv_d, bool rms, float eps) {
+__device__ __forceinline__ float centre(float2 (&v)[n], float inv_d, bool rms, float eps) {
     if (!rms) {
-        float s = 0.f;
+        float2 s = v[0];
 #pragma unroll
-        for (int e = 0; e < n; ++e) s += v[e];
-        const float mu = lanes_sum<L>(s) * inv_d;
+        for (int e = 1; e < n; ++e) s = add2(s, v[e]);
+        const float2 mu = both(-lanes_sum<L>(s.x + s.y) * inv_d);
 #pragma unroll
-        for (int e = 0; e < n; ++e) v[e] -= mu;
+        for (int e = 0; e < n; ++e) v[e] = add2(v[e], mu);
     }
-    float s = 0.f;
+    float2 s = mul2(v[0], v[0]);
 #pragma unroll
-    for (int e = 0; e < n; ++e) s = fmaf(v[e], v[e], s);
-    return 1.f / sqrtf(fmaf(lanes_sum<L>(s), inv_d, eps));
+    for (int e = 1; e < n; ++e) s = fma2(v[e], v[e], s);
+    return 1.f / sqrtf(fmaf(lanes_sum<L>(s.x + s.y), inv_d, eps));
 }
 
 template <typename T, int L>
-__global__ void __launch_bounds__(kBlock)
+__global__ void __launch_bounds__(kBlock, 4)
 gated_fwd_kernel(const T* o, const T* gate, const T* __restrict__ w, T* y, GatedRows g, int rms, float eps) {
     using V = Vec<T>;
-    constexpr int kRows = kBlock / L, D = L * V::n;
+    constexpr int kRows = kBlock / L, D = L * V::n, kP = V::n / 2, kU = kFwdU;
     pdl_enter();  // launched with programmatic dependent launch
     const int lane = threadIdx.x % L, sub = threadIdx.x / L;
-    float wv[V::n];
+    float2 wv[kP];
 #pragma unroll
-    for (int e = 0; e < V::n; ++e) wv[e] = 1.f;
-    if (w) V::load(w + lane * V::n, wv);
+    for (int e = 0; e < kP; ++e) wv[e] = both(1.f);
+    if (w) Pairs<T>::get(w + lane * V::n, wv);
     for (long long f0 = (long long)blockIdx.x * (kRows * kU); f0 < g.rows; f0 += (long long)gridDim.x * (kRows * kU)) {
         const Place at = Place::of(g, f0);
         uint4 xo[kU], xg[kU];
@@ -124,31 +130,35 @@ gated_fwd_kernel(const T* o, const T* gate, const T* __restrict__ w, T* y, Gated
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int l = u * kRows + sub;
-            float v[V::n], s[V::n];
-            V::get(xo[u], v);
+            float2 v[kP];
+            float x[V::n], s[V::n];
+            Pairs<T>::get(&xo[u], v);
             V::get(xg[u], s);
             const float rs = centre<L>(v, 1.f / D, rms, eps);
 #pragma unroll
-            for (int e = 0; e < V::n; ++e) v[e] = v[e] * rs * wv[e] * (s[e] * sigmoid(s[e]));
-            if (f0 + l < g.rows) V::put(y + (f0 + l) * D + lane * V::n, v);
+            for (int e = 0; e < V::n; ++e) {
+                const float n = (e & 1 ? v[e >> 1].y : v[e >> 1].x) * rs, wt = e & 1 ? wv[e >> 1].y : wv[e >> 1].x;
+                x[e] = n * wt * (s[e] * sigmoid(s[e]));
+            }
+            if (f0 + l < g.rows) V::put(y + (f0 + l) * D + lane * V::n, x);
         }
     }
 }
 
 // part: [blocks][D]
 template <typename T, int L>
-__global__ void __launch_bounds__(kBlock)
+__global__ void __launch_bounds__(kBlock, sizeof(T) == 2 ? 4 : 2)
 gated_bwd_kernel(const T* o, const T* gate, const T* __restrict__ w, const T* dy, T* dout, T* dgate,
                  float* __restrict__ part, GatedRows g, int rms, float eps) {
     using V = Vec<T>;
-    constexpr int kRows = kBlock / L, D = L * V::n;
+    constexpr int kRows = kBlock / L, D = L * V::n, kP = V::n / 2, kU = bwd_u<T>();
     __shared__ float sums[kRows][D];
     pdl_enter();  // launched with programmatic dependent launch
     const int lane = threadIdx.x % L, sub = threadIdx.x / L;
-    float wv[V::n], dw[V::n];
+    float2 wv[kP], dw[kP];
 #pragma unroll
-    for (int e = 0; e < V::n; ++e) wv[e] = 1.f, dw[e] = 0.f;
-    if (w) V::load(w + lane * V::n, wv);
+    for (int e = 0; e < kP; ++e) wv[e] = both(1.f), dw[e] = both(0.f);
+    if (w) Pairs<T>::get(w + lane * V::n, wv);
     for (long long f0 = (long long)blockIdx.x * (kRows * kU); f0 < g.rows; f0 += (long long)gridDim.x * (kRows * kU)) {
         const Place at = Place::of(g, f0);
         uint4 xo[kU], xg[kU], xd[kU];
@@ -169,35 +179,36 @@ gated_bwd_kernel(const T* o, const T* gate, const T* __restrict__ w, const T* dy
         for (int u = 0; u < kU; ++u) {
             const int l = u * kRows + sub;
             const bool in = f0 + l < g.rows;
-            float v[V::n], s[V::n], d[V::n];
-            V::get(xo[u], v);
-            V::get(xg[u], s);
-            V::get(xd[u], d);
-            const float rs = centre<L>(v, 1.f / D, rms, eps);
-            float m0 = 0.f, m1 = 0.f;
+            float2 v[kP], s[kP], d[kP];
+            Pairs<T>::get(&xo[u], v);
+            Pairs<T>::get(&xg[u], s);
+            Pairs<T>::get(&xd[u], d);
+            const float rstd = centre<L>(v, 1.f / D, rms, eps);  // every lane takes part
+            const float rs = in ? rstd : 0.f;                    // rows behind the last add nothing
+            float2 m0 = both(0.f), m1 = both(0.f);
 #pragma unroll
-            for (int e = 0; e < V::n; ++e) {
-                const float sg = sigmoid(s[e]), silu = s[e] * sg;
-                v[e] *= rs;
-                const float dn = d[e] * v[e];  // d(w silu)
-                if (in) dw[e] = fmaf(dn, silu, dw[e]);
-                s[e] = dn * wv[e] * fmaf(silu, 1.f - sg, sg);  // dgate: silu' = sg + silu (1 - sg)
-                d[e] *= silu * wv[e];
-                m0 += d[e];
-                m1 = fmaf(d[e], v[e], m1);
+            for (int e = 0; e < kP; ++e) {
+                const float2 t = mul2(s[e], both(-1.4426950408889634f)), q = add2(make_float2(ex2_approx(t.x), ex2_approx(t.y)), both(1.f));
+                const float2 sg = make_float2(rcp(q.x), rcp(q.y)), silu = mul2(s[e], sg);
+                v[e] = mul2(v[e], both(rs));
+                const float2 dn = mul2(d[e], v[e]);  // d(w silu)
+                dw[e] = fma2(dn, silu, dw[e]);
+                s[e] = mul2(mul2(dn, wv[e]), fma2(silu, fma2(sg, both(-1.f), both(1.f)), sg));  // dgate: silu' = sg + silu (1 - sg)
+                d[e] = mul2(d[e], mul2(silu, wv[e]));
+                m1 = fma2(d[e], v[e], m1);
+                if (!rms) m0 = add2(m0, d[e]);
             }
-            m1 = lanes_sum<L>(m1) * (1.f / D);
-            m0 = rms ? 0.f : lanes_sum<L>(m0) * (1.f / D);
+            const float2 k1 = both(-lanes_sum<L>(m1.x + m1.y) * (1.f / D)), k0 = both(rms ? 0.f : -lanes_sum<L>(m0.x + m0.y) * (1.f / D));
 #pragma unroll
-            for (int e = 0; e < V::n; ++e) d[e] = rs * (d[e] - fmaf(v[e], m1, m0));
+            for (int e = 0; e < kP; ++e) d[e] = mul2(both(rs), fma2(v[e], k1, add2(d[e], k0)));
             if (!in) continue;
-            V::put(dgate + (f0 + l) * D + lane * V::n, s);
-            V::put(dout + r[u] * D + lane * V::n, d);
+            Pairs<T>::put(dgate + (f0 + l) * D + lane * V::n, s);
+            Pairs<T>::put(dout + r[u] * D + lane * V::n, d);
         }
     }
     if (!part) return;
 #pragma unroll
-    for (int e = 0; e < V::n; ++e) sums[sub][lane * V::n + e] = dw[e];
+    for (int e = 0; e < kP; ++e) *reinterpret_cast<float2*>(&sums[sub][lane * V::n + 2 * e]) = dw[e];
     __syncthreads();
     for (int c = threadIdx.x; c < D; c += kBlock) {
         float a = 0.f;
@@ -355,12 +366,13 @@ resid_fwd_tiles(const T* x, const T* a, const T* __restrict__ scale, const T* __
 
 // The arrays of the gradient in a stage: h, dy, then dh and a where there are any.
 template <typename T, int VPT, int TPR>
-__global__ void __launch_bounds__(block_of<TPR>())
+__global__ void __launch_bounds__(block_of<TPR>(), TPR > kBlock ? 1 : 2)
 resid_bwd_tiles(const T* h, const T* a, const T* __restrict__ scale, const T* __restrict__ w, const float* __restrict__ mean,
                 const float* __restrict__ rstd, const T* dy, const T* dh, T* dx, T* da, float* __restrict__ part, Tiles tl,
                 int rms, int* err) {
     using V = Vec<T>;
-    constexpr int kThr = block_of<TPR>(), kRows = kThr / TPR;
+    constexpr int kThr = block_of<TPR>(), kRows = kThr / TPR, kP = V::n / 2;
+    constexpr bool kKeep = VPT * V::n <= 16;  // n and d in registers between the passes, else formed again
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t bar[kMostStages];
     __shared__ float buf[kRows][4][TPR > 256 ? 16 : 8];
@@ -389,11 +401,11 @@ resid_bwd_tiles(const T* h, const T* a, const T* __restrict__ scale, const T* __
         if (a) sm100::bulk_load(to + at_a, reinterpret_cast<const uint8_t*>(a) + k * tile, bytes, bar + s);
     };
     for (int i = 0; i < stages; ++i) load(i, i);
-    float dw[VPT][V::n], db[VPT][V::n], ds[VPT][V::n];
+    float2 dw[VPT][kP], db[VPT][kP], ds[VPT][kP];
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
-        for (int e = 0; e < V::n; ++e) dw[j][e] = db[j][e] = ds[j][e] = 0.f;
+        for (int e = 0; e < kP; ++e) dw[j][e] = db[j][e] = ds[j][e] = both(0.f);
     const float inv = 1.f / (float)tl.C;
     float mu_next = 0.f, rs_next = 0.f;  // the statistics of this thread's next row, loaded a turn ahead
     auto stats = [&](long long k, int r) {
@@ -421,59 +433,62 @@ resid_bwd_tiles(const T* h, const T* a, const T* __restrict__ scale, const T* __
             const long long row = k * tl.R + (in ? r : 0);
             LA_DCHECK(row < tl.rows);
             const uint8_t* hr = smem + s * set + (in ? r : 0) * tl.row;
-            float sum[2] = {0.f, 0.f};
+            float2 n[kKeep ? VPT : 1][kP], d[kKeep ? VPT : 1][kP], s0 = both(0.f), s1 = s0;
+            auto normed = [&](int j, float2 (&g)[kP]) {  // n and d of vector j, g = dy
+                const int c = t + TPR * j, q = kKeep ? j : 0;
+                Pairs<T>::get(hr + 16 * c, n[q]);
+                Pairs<T>::get(hr + tile + 16 * c, g);
+                if (w) Pairs<T>::get(reinterpret_cast<const uint4*>(w) + c, d[q]);
+#pragma unroll
+                for (int e = 0; e < kP; ++e) {
+                    n[q][e] = mul2(add2(n[q][e], both(-mu)), both(rs));
+                    d[q][e] = w ? mul2(g[e], d[q][e]) : g[e];
+                }
+            };
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int c = t + TPR * j;
-                if (!in || c >= nv) continue;
-                float v[V::n], g[V::n], wv[V::n];
-                V::load(hr + 16 * c, v);
-                V::load(hr + tile + 16 * c, g);
-                if (w) V::load(reinterpret_cast<const uint4*>(w) + c, wv);
+                if (!in || t + TPR * j >= nv) continue;
+                const int q = kKeep ? j : 0;
+                float2 g[kP];
+                normed(j, g);
 #pragma unroll
-                for (int e = 0; e < V::n; ++e) {
-                    const float nn = __fmul_rn(v[e] - mu, rs), d = w ? __fmul_rn(g[e], wv[e]) : g[e];
-                    sum[0] += d;
-                    sum[1] = fmaf(d, nn, sum[1]);
-                    dw[j][e] = fmaf(g[e], nn, dw[j][e]);
-                    db[j][e] += g[e];
+                for (int e = 0; e < kP; ++e) {
+                    s0 = add2(s0, d[q][e]);
+                    s1 = fma2(d[q][e], n[q][e], s1);
+                    dw[j][e] = fma2(g[e], n[q][e], dw[j][e]);
+                    db[j][e] = add2(db[j][e], g[e]);
                 }
             }
+            float sum[2] = {s0.x + s0.y, s1.x + s1.y};
             group_sum<TPR, 2>(sum, buf[sub], sub, t, turn);
             if (!in) continue;
-            const float m0 = rms ? 0.f : __fmul_rn(sum[0], inv), m1 = __fmul_rn(sum[1], inv);
+            const float2 m0 = both(rms ? 0.f : -__fmul_rn(sum[0], inv)), m1 = both(-__fmul_rn(sum[1], inv));
             uint8_t *ox = reinterpret_cast<uint8_t*>(dx) + row * tl.row, *oa = reinterpret_cast<uint8_t*>(da) + row * tl.row;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int c = t + TPR * j;
+                const int c = t + TPR * j, q = kKeep ? j : 0;
                 if (c >= nv) continue;
-                float v[V::n], g[V::n], x[V::n];
-                V::load(hr + 16 * c, v);
-                V::load(hr + tile + 16 * c, g);
-                if (w) {
-                    V::load(reinterpret_cast<const uint4*>(w) + c, x);
+                float2 g[kP], x[kP];
+                if (!kKeep) normed(j, g);
+                if (dh) Pairs<T>::get(hr + at_dh + 16 * c, x);
 #pragma unroll
-                    for (int e = 0; e < V::n; ++e) g[e] = __fmul_rn(g[e], x[e]);
+                for (int e = 0; e < kP; ++e) {
+                    g[e] = fma2(n[q][e], m1, add2(d[q][e], m0));
+                    g[e] = dh ? fma2(both(rs), g[e], x[e]) : mul2(both(rs), g[e]);
                 }
-                if (dh) V::load(hr + at_dh + 16 * c, x);
-#pragma unroll
-                for (int e = 0; e < V::n; ++e) {
-                    const float nn = __fmul_rn(v[e] - mu, rs);
-                    g[e] = fmaf(rs, fmaf(-nn, m1, g[e] - m0), dh ? x[e] : 0.f);
-                }
-                V::put(ox + 16 * c, g);
+                Pairs<T>::put(ox + 16 * c, g);
                 if (a) {
-                    V::load(hr + at_a + 16 * c, x);
+                    Pairs<T>::get(hr + at_a + 16 * c, x);
 #pragma unroll
-                    for (int e = 0; e < V::n; ++e) ds[j][e] = fmaf(x[e], g[e], ds[j][e]);
+                    for (int e = 0; e < kP; ++e) ds[j][e] = fma2(x[e], g[e], ds[j][e]);
                 }
                 if (da) {
                     if (scale) {
-                        V::load(reinterpret_cast<const uint4*>(scale) + c, x);
+                        Pairs<T>::get(reinterpret_cast<const uint4*>(scale) + c, x);
 #pragma unroll
-                        for (int e = 0; e < V::n; ++e) g[e] *= x[e];
+                        for (int e = 0; e < kP; ++e) g[e] = mul2(g[e], x[e]);
                     }
-                    V::put(oa + 16 * c, g);
+                    Pairs<T>::put(oa + 16 * c, g);
                 }
             }
         }
@@ -495,8 +510,8 @@ resid_bwd_tiles(const T* h, const T* a, const T* __restrict__ scale, const T* __
             const int c = t + TPR * j;
             if (c >= nv) continue;
 #pragma unroll
-            for (int e = 0; e < V::n; ++e)
-                sums[sub * tl.C + c * V::n + e] = which == 0 ? dw[j][e] : which == 1 ? db[j][e] : ds[j][e];
+            for (int e = 0; e < kP; ++e)
+                *reinterpret_cast<float2*>(sums + sub * tl.C + c * V::n + 2 * e) = which == 0 ? dw[j][e] : which == 1 ? db[j][e] : ds[j][e];
         }
         __syncthreads();
         for (int c = tid; c < tl.C; c += kThr) {
@@ -560,11 +575,11 @@ resid_fwd_elements(const T* x, const T* a, const T* __restrict__ scale, const T*
 }
 
 template <typename T, int VPT, int TPR>
-__global__ void __launch_bounds__(block_of<TPR>())
+__global__ void __launch_bounds__(block_of<TPR>(), TPR > kBlock ? 1 : 5)
 resid_bwd_elements(const T* h, const T* a, const T* __restrict__ scale, const T* __restrict__ w, const float* __restrict__ mean,
                    const float* __restrict__ rstd, const T* dy, const T* dh, T* dx, T* da, float* __restrict__ part,
                    long long rows, int C, int rms) {
-    constexpr int kThr = block_of<TPR>(), kRows = kThr / TPR;
+    constexpr int kThr = block_of<TPR>(), kRows = kThr / TPR, kAhead = VPT <= 8 ? VPT : 8;
     extern __shared__ float sums[];  // [kRows][C], where a block has several rows
     __shared__ float buf[kRows][4][TPR > 256 ? 16 : 8];
     pdl_enter();  // launched with programmatic dependent launch
@@ -579,15 +594,28 @@ resid_bwd_elements(const T* h, const T* a, const T* __restrict__ scale, const T*
         if (TPR > 32 && !in) break;
         const long long row = in ? r0 + sub : r0, at = row * C;
         const float mu = rms ? 0.f : mean[row], rs = rstd[row];
-        float n[VPT], d[VPT], sum[2] = {0.f, 0.f};
+        // what a row needs is loaded together, before any use or store (the outputs may lie in the inputs' arrays)
+        float n[VPT], d[VPT], xh[kAhead], xa[kAhead], sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = t + TPR * j;
-            n[j] = d[j] = 0.f;
-            if (!in || c >= C) continue;
-            const float g = to_f32(dy[at + c]);
-            n[j] = __fmul_rn(to_f32(h[at + c]) - mu, rs);
-            d[j] = w ? __fmul_rn(g, to_f32(w[c])) : g;
+            const bool here = in && t + TPR * j < C;
+            n[j] = here ? to_f32(h[at + t + TPR * j]) : mu;
+            d[j] = here ? to_f32(dy[at + t + TPR * j]) : 0.f;
+        }
+        auto fetch = [&](int j0) {
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int c = t + TPR * (j0 + j);
+                xh[j] = in && c < C && dh ? to_f32(dh[at + c]) : 0.f;
+                xa[j] = in && c < C && a ? to_f32(a[at + c]) : 0.f;
+            }
+        };
+        fetch(0);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const float g = d[j];
+            n[j] = __fmul_rn(n[j] - mu, rs);
+            if (w && t + TPR * j < C) d[j] = __fmul_rn(g, to_f32(w[t + TPR * j]));
             sum[0] += d[j];
             sum[1] = fmaf(d[j], n[j], sum[1]);
             dw[j] = fmaf(g, n[j], dw[j]);
@@ -597,13 +625,17 @@ resid_bwd_elements(const T* h, const T* a, const T* __restrict__ scale, const T*
         if (!in) continue;
         const float m0 = rms ? 0.f : __fmul_rn(sum[0], inv), m1 = __fmul_rn(sum[1], inv);
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int c = t + TPR * j;
-            if (c >= C || !LA_DCHECK(at + c < rows * C)) continue;
-            const float g = fmaf(rs, fmaf(-n[j], m1, d[j] - m0), dh ? to_f32(dh[at + c]) : 0.f);
-            if (a) ds[j] = fmaf(to_f32(a[at + c]), g, ds[j]);
-            dx[at + c] = from_f32<T>(g);
-            if (da) da[at + c] = from_f32<T>(scale ? to_f32(scale[c]) * g : g);
+        for (int j0 = 0; j0 < VPT; j0 += kAhead) {
+            if (j0 > 0) fetch(j0);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int j = j0 + k, c = t + TPR * j;
+                if (c >= C || !LA_DCHECK(at + c < rows * C)) continue;
+                const float g = fmaf(rs, fmaf(-n[j], m1, d[j] - m0), xh[k]);
+                ds[j] = fmaf(xa[k], g, ds[j]);
+                dx[at + c] = from_f32<T>(g);
+                if (da) da[at + c] = from_f32<T>(scale ? to_f32(scale[c]) * g : g);
+            }
         }
     }
     if (!part) return;
@@ -645,22 +677,24 @@ GatedRows rows_of(const Gated& g) {
     r.magic = (unsigned)((0x100000000ull + g.H - 1) / g.H);
     return r;
 }
-int gated_blocks(const Gated& g, int per_sm) {
-    const long long rows = g.positions * g.H, at_once = (long long)kU * kBlock / (g.D * elem_of(g.dtype) / 16);
+int gated_blocks(const Gated& g, int u, int per_sm) {
+    const long long rows = g.positions * g.H, at_once = (long long)u * kBlock / (g.D * elem_of(g.dtype) / 16);
     const long long tiles = (rows + at_once - 1) / at_once, most = 152LL * per_sm;
     return (int)(tiles < most ? tiles : most);
 }
-constexpr int kGatedFwdPerSm = 8, kGatedBwdPerSm = 4;
+constexpr int kGatedFwdPerSm = 8;
+// The gradient's blocks (and records): a wave of the SMs.
+int gated_bwd_blocks(const Gated& g) { return g.dtype == LA_BF16 ? gated_blocks(g, bwd_u<__nv_bfloat16>(), 4) : gated_blocks(g, bwd_u<float>(), 2); }
 
 template <typename T, int L>
 cudaError_t gated_fwd_l(const void* o, const void* gate, const void* w, void* y, const Gated& g, cudaStream_t st) {
-    return run("gated_fwd", gated_fwd_kernel<T, L>, gated_blocks(g, kGatedFwdPerSm), kBlock, 0, st, (const T*)o, (const T*)gate,
+    return run("gated_fwd", gated_fwd_kernel<T, L>, gated_blocks(g, kFwdU, kGatedFwdPerSm), kBlock, 0, st, (const T*)o, (const T*)gate,
                (const T*)w, (T*)y, rows_of(g), g.rms, g.eps);
 }
 template <typename T, int L>
 cudaError_t gated_bwd_l(const void* o, const void* gate, const void* w, const void* dy, void* dout, void* dgate, void* dw,
                         const Gated& g, float* part, cudaStream_t st) {
-    const int blocks = gated_blocks(g, kGatedBwdPerSm);
+    const int blocks = gated_bwd_blocks(g);
     const cudaError_t e = run("gated_bwd", gated_bwd_kernel<T, L>, blocks, kBlock, 0, st, (const T*)o, (const T*)gate,
                               (const T*)w, (const T*)dy, (T*)dout, (T*)dgate, part, rows_of(g), g.rms, g.eps);
     if (e != cudaSuccess || !part) return e;
@@ -668,9 +702,15 @@ cudaError_t gated_bwd_l(const void* o, const void* gate, const void* w, const vo
                blocks, g.D, 1, g.D);
 }
 
-int row_threads(int C) {  // at most 16 elements to a thread, 32 of the widest rows
+// Elements to a thread: 8 forward, 16 in the gradient (whose threads hold three sums to an element; 8 took 297 us instead of 267 for
+// 65536 x 2048 bf16, where the forward takes 353 us instead of 370 for 131072 x 2048); up to 32 of the widest rows.
+constexpr int kFwdElems = 8, kBwdElems = 16;
+// Rows that vectors do not divide: 65536 x 1001 bf16 takes 137 us forward with 16 (154 with 8), the gradient 263 us with 4 and five
+// blocks to an SM (444 with 8 and three, 820 with 16 and two: its loads wait for one another, so many short rows it is).
+constexpr int kFwdSingles = 16, kBwdSingles = 4;
+int row_threads(int C, int elems) {
     int t = 8;
-    while (t < 512 && t * 16 < C) t *= 2;
+    while (t < 512 && t * elems < C) t *= 2;
     return t;
 }
 int block_for(int threads) { return threads > kBlock ? threads : kBlock; }
@@ -681,9 +721,9 @@ bool bwd_streams(const la_norm_shape& s) {
     return vectors(s.C, elem_of(s.dtype)) && (size_t)4 * s.C * elem_of(s.dtype) <= kMostSmem;
 }
 // A tile of about `bytes` to an array, fewer rows where there are few, a multiple of the rows worked on at a time.
-Tiles tiles_of(const la_norm_shape& s, int arrays, int bytes) {
+Tiles tiles_of(const la_norm_shape& s, int elems, int arrays, int bytes, int stages) {
     Tiles t{};
-    const int elem = elem_of(s.dtype), threads = row_threads(s.C), at_once = block_for(threads) / threads;
+    const int elem = elem_of(s.dtype), threads = row_threads(s.C, elems), at_once = block_for(threads) / threads;
     t.rows = s.rows;
     t.C = s.C;
     t.row = (uint32_t)s.C * elem;
@@ -693,55 +733,56 @@ Tiles tiles_of(const la_norm_shape& s, int arrays, int bytes) {
     if (t.R < at_once) t.R = at_once;
     t.tiles = (s.rows + t.R - 1) / t.R;
     const long long fit = (long long)kMostSmem / ((long long)arrays * t.R * t.row);
-    t.stages = (int)(fit < kMostStages ? fit : kMostStages);
+    t.stages = (int)(fit < stages ? fit : stages);
     return t;
 }
 int resident(size_t smem, int most) {
     const long long per = (long long)kMostSmem / (long long)(smem + 1536);
     return (int)(per < 1 ? 1 : per > most ? most : per);
 }
-constexpr int kFwdTile = 8192, kBwdTile = 8192;
+constexpr int kFwdTile = 8192, kBwdTile = 8192, kFwdStages = 3, kBwdStages = 2, kElementsPerSm = 5;
 // Blocks of the gradient, i.e. its records of 3 C floats: the same whether or not there are a and dh.
 int bwd_blocks(const la_norm_shape& s) {
-    const int threads = row_threads(s.C);
     if (!bwd_streams(s)) {
-        const int at_once = block_for(threads) / threads;
-        const long long tiles = (s.rows + at_once - 1) / at_once, most = 152LL * (threads > 256 ? 1 : 2);
+        const int threads = row_threads(s.C, kBwdSingles), at_once = block_for(threads) / threads;
+        const long long tiles = (s.rows + at_once - 1) / at_once, most = 152LL * (threads > 256 ? 1 : kElementsPerSm);
         return (int)(tiles < most ? tiles : most);
     }
-    const Tiles t = tiles_of(s, 4, kBwdTile);
+    const int threads = row_threads(s.C, kBwdElems);
+    const Tiles t = tiles_of(s, kBwdElems, 4, kBwdTile, kBwdStages);
     const long long most = 152LL * resident((size_t)4 * t.stages * t.R * t.row, threads > 256 ? 1 : 2);
     return (int)(t.tiles < most ? t.tiles : most);
 }
 
-// Calls f with the (elements to a thread) / kPer and threads to a row of a size.
-#define LA_ROW_SIZES(go, per)                                      \
-    switch (row_threads(s.C)) {                                    \
-        case 8: return go(16 / (per), 8);                          \
-        case 16: return go(16 / (per), 16);                        \
-        case 32: return go(16 / (per), 32);                        \
-        case 64: return go(16 / (per), 64);                        \
-        case 128: return go(16 / (per), 128);                      \
-        case 256: return go(16 / (per), 256);                      \
-        default:                                                   \
-            if (s.C <= 512 * 16) return go(16 / (per), 512);       \
-            return go(32 / (per), 512);                            \
+// Calls go with (elements to a thread) / per and threads to a row of a size.
+#define LA_ROW_SIZES(go, elems, per)                                   \
+    switch (row_threads(s.C, elems)) {                                 \
+        case 8: return go(elems / (per), 8);                           \
+        case 16: return go(elems / (per), 16);                         \
+        case 32: return go(elems / (per), 32);                         \
+        case 64: return go(elems / (per), 64);                         \
+        case 128: return go(elems / (per), 128);                       \
+        case 256: return go(elems / (per), 256);                       \
+        default:                                                       \
+            if (s.C <= 512 * elems) return go(elems / (per), 512);     \
+            if (s.C <= 512 * 16) return go(16 / (per), 512);           \
+            return go(32 / (per), 512);                                \
     }
 
 template <typename T>
 cudaError_t resid_fwd_t(const ResidFwd& a, const la_norm_shape& s, bool rms, float eps, cudaStream_t st) {
     constexpr int V = 16 / (int)sizeof(T);
-    const int threads = row_threads(s.C), block = block_for(threads);
+    const int threads = row_threads(s.C, vectors(s.C, sizeof(T)) ? kFwdElems : kFwdSingles), block = block_for(threads);
     if (!vectors(s.C, sizeof(T))) {
         const long long tiles = (s.rows + block / threads - 1) / (block / threads), most = 152LL * 16;
         const long long blocks = tiles < most ? tiles : most;
 #define LA_GO(vpt, tpr)                                                                                                    \
     run("resid_fwd", resid_fwd_elements<T, vpt, tpr>, blocks, block, 0, st, (const T*)a.x, (const T*)a.a, (const T*)a.scale, \
         (const T*)a.w, (const T*)a.b, (T*)a.h, (T*)a.y, a.mean, a.rstd, s.rows, s.C, (int)rms, eps)
-        LA_ROW_SIZES(LA_GO, 1)
+        LA_ROW_SIZES(LA_GO, kFwdSingles, 1)
 #undef LA_GO
     }
-    const Tiles t = tiles_of(s, 2, kFwdTile);
+    const Tiles t = tiles_of(s, kFwdElems, 2, kFwdTile, kFwdStages);
     const size_t smem = (size_t)2 * t.stages * t.R * t.row;
     const long long all = 152LL * resident(smem, 4), blocks = t.tiles < all ? t.tiles : all;
     auto go = [&](auto kern) {
@@ -751,24 +792,24 @@ cudaError_t resid_fwd_t(const ResidFwd& a, const la_norm_shape& s, bool rms, flo
                    (const T*)a.b, (T*)a.h, (T*)a.y, a.mean, a.rstd, t, (int)rms, eps, device_error_word());
     };
 #define LA_GO(vpt, tpr) go(resid_fwd_tiles<T, vpt, tpr>)
-    LA_ROW_SIZES(LA_GO, V)
+    LA_ROW_SIZES(LA_GO, kFwdElems, V)
 #undef LA_GO
 }
 
 template <typename T>
 cudaError_t resid_bwd_t(const ResidBwd& a, const la_norm_shape& s, bool rms, float* part, cudaStream_t st) {
     constexpr int V = 16 / (int)sizeof(T);
-    const int threads = row_threads(s.C), block = block_for(threads), blocks = bwd_blocks(s);
+    const int threads = row_threads(s.C, bwd_streams(s) ? kBwdElems : kBwdSingles), block = block_for(threads), blocks = bwd_blocks(s);
     const size_t sums = block > threads ? (size_t)(block / threads) * s.C * 4 : 0;
     if (!bwd_streams(s)) {
 #define LA_GO(vpt, tpr)                                                                                                       \
     run("resid_bwd", resid_bwd_elements<T, vpt, tpr>, blocks, block, sums, st, (const T*)a.h, (const T*)a.a, (const T*)a.scale, \
         (const T*)a.w, a.mean, a.rstd, (const T*)a.dy, (const T*)a.dh, (T*)a.dx, (T*)a.da, part, s.rows, s.C, (int)rms)
-        LA_ROW_SIZES(LA_GO, 1)
+        LA_ROW_SIZES(LA_GO, kBwdSingles, 1)
 #undef LA_GO
     }
     const int arrays = 2 + (a.dh ? 1 : 0) + (a.a ? 1 : 0);
-    const Tiles t = tiles_of(s, 4, kBwdTile);  // of four arrays: the blocks do not depend on which are there
+    const Tiles t = tiles_of(s, kBwdElems, 4, kBwdTile, kBwdStages);  // of four arrays: the blocks do not depend on which are there
     size_t smem = (size_t)arrays * t.stages * t.R * t.row;
     const size_t one = (size_t)(block / threads) * s.C * 4;
     if (smem < one) smem = one;
@@ -779,13 +820,13 @@ cudaError_t resid_bwd_t(const ResidBwd& a, const la_norm_shape& s, bool rms, flo
                    a.mean, a.rstd, (const T*)a.dy, (const T*)a.dh, (T*)a.dx, (T*)a.da, part, t, (int)rms, device_error_word());
     };
 #define LA_GO(vpt, tpr) go(resid_bwd_tiles<T, vpt, tpr>)
-    LA_ROW_SIZES(LA_GO, V)
+    LA_ROW_SIZES(LA_GO, kBwdElems, V)
 #undef LA_GO
 }
 
 }  // namespace
 
-size_t gated_bwd_bytes(const Gated& g) { return (size_t)gated_blocks(g, kGatedBwdPerSm) * g.D * 4; }
+size_t gated_bwd_bytes(const Gated& g) { return (size_t)gated_bwd_blocks(g) * g.D * 4; }
 
 // The lanes of a row: 16 bytes each.
 #define LA_HEADS(go)                                                                                  \

@@ -1,8 +1,8 @@
 // cross_step.cu -- cross attention of a few queries to a kept state: out = phi(q)^T S / phi(q)^T z for the rows of
 // queries that share a head of keys (one token of each of its heads of queries, or a few tokens).
 //
-// Bound by memory: a state of Dk x Dv fp32 is read once, everything else is O(Dk + Dv) to a row.  A block owns a head:
-// its threads issue all loads of S before any arithmetic and keep S in registers (at most 16 16-byte vectors each),
+// Bound by memory: a state of Dk x Dv fp32 is read once, everything else is O(Dk + Dv) to a row.  A block owns a head, or 64 columns of
+// one (32 KB: five blocks to an SM take over from one another more evenly than two with 64 KB): its threads issue all loads of S before any arithmetic and keep S in registers (at most 16 16-byte vectors each),
 // so that every further row costs shared memory and arithmetic only.  Rows are taken kRows at a time: each thread
 // forms their partial sums over its rows of S, and the warps' sums are joined in shared memory in a fixed order.
 #include "cross.cuh"
@@ -11,6 +11,7 @@ namespace la {
 namespace cross {
 namespace {
 
+// DV: the columns of a block.
 template <int DK, int DV>
 struct Few {
     static constexpr int kVecs = DK * DV / 4;
@@ -24,7 +25,7 @@ struct Few {
 template <typename T, int DK, int DV, int kRows>
 __global__ void __launch_bounds__(Few<DK, DV>::kThreads)
 cross_few_kernel(const T* __restrict__ q, const float* __restrict__ S, const float* __restrict__ z, T* __restrict__ o,
-                 int R) {
+                 int R, int pitch) {
     using F = Few<DK, DV>;
     __shared__ float ph[kRows][DK];
     __shared__ float part[F::kWarps][kRows][DV];
@@ -33,14 +34,14 @@ cross_few_kernel(const T* __restrict__ q, const float* __restrict__ S, const flo
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c4 = tid % F::kCols, r0 = tid / F::kCols;
     const size_t bh = blockIdx.x;
-    const float* Sh = S + bh * DK * DV;
+    const float* Sh = S + bh * DK * pitch + blockIdx.y * DV;
     const float* zh = z + bh * DK;
     float4 s[F::kHeld];
 #pragma unroll
     for (int x = 0; x < F::kHeld; ++x)
-        s[x] = *reinterpret_cast<const float4*>(Sh + (size_t)(r0 + F::kPer * x) * DV + 4 * c4);
+        s[x] = *reinterpret_cast<const float4*>(Sh + (size_t)(r0 + F::kPer * x) * pitch + 4 * c4);
     const T* qh = q + bh * R * DK;
-    T* oh = o + bh * R * DV;
+    T* oh = o + bh * R * pitch + blockIdx.y * DV;
     for (int base = 0; base < R; base += kRows) {
         const int n = min(kRows, R - base);
         for (int x = tid; x < n * DK; x += F::kThreads) ph[x / DK][x % DK] = phi_f(to_f32(qh[(size_t)base * DK + x]));
@@ -78,7 +79,7 @@ cross_few_kernel(const T* __restrict__ q, const float* __restrict__ S, const flo
             float a = 0.f;
 #pragma unroll
             for (int w = 0; w < F::kWarps; ++w) a += part[w][x / DV][x % DV];
-            if (LA_DCHECK(base + x / DV < R)) oh[(size_t)base * DV + x] = from_f32<T>(a * inv[x / DV]);
+            if (LA_DCHECK(base + x / DV < R)) oh[(size_t)(base + x / DV) * pitch + x % DV] = from_f32<T>(a * inv[x / DV]);
         }
         __syncthreads();  // before the next rows
     }
@@ -86,9 +87,12 @@ cross_few_kernel(const T* __restrict__ q, const float* __restrict__ S, const flo
 
 template <typename T, int DK, int DV>
 cudaError_t go(const void* q, const float* S, const float* z, void* o, int heads, int R, cudaStream_t st) {
-    auto kern = R == 1 ? cross_few_kernel<T, DK, DV, 1> : cross_few_kernel<T, DK, DV, 4>;
+    constexpr int kCols = DV < 64 ? DV : 64;
+    auto kern = R == 1   ? cross_few_kernel<T, DK, kCols, 1>
+                : R == 2 ? cross_few_kernel<T, DK, kCols, 2>
+                         : cross_few_kernel<T, DK, kCols, 4>;
     launch_begin("cross_few", st);
-    const cudaError_t e = launch_pdl(kern, dim3(heads), dim3(Few<DK, DV>::kThreads), 0, st, (const T*)q, S, z, (T*)o, R);
+    const cudaError_t e = launch_pdl(kern, dim3(heads, DV / kCols), dim3(Few<DK, kCols>::kThreads), 0, st, (const T*)q, S, z, (T*)o, R, DV);
     const cudaError_t e2 = launch_end("cross_few", st);
     return e != cudaSuccess ? e : e2;
 }

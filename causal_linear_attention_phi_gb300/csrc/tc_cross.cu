@@ -18,8 +18,9 @@ namespace cross {
 namespace {
 
 // ------------------------------------------------------------------ sums over the keys
-// A stage holds a chunk of 64 rows: K (phi's hi part in place), its lo part, V.  For KB = 1 hi and lo are the two 64-row
-// halves of one 128-row product; else they are two products.  An accumulator in tensor memory takes kPeriod chunks only:
+// A stage holds a chunk of 64 rows: K (phi's hi part in place) and V.  phi's lo part: for KB = 1 in the stage, hi and lo being the
+// two 64-row halves of one 128-row product; for KB = 2 in a ring of its own, held only while the products run, which leaves
+// room for a fifth stage.  An accumulator in tensor memory takes kPeriod chunks only:
 // the products add with truncation, half a unit in the last place each and always the same way (131,072 keys summed in one
 // accumulator to a block were 2e-5 off).  The compute warps then add it to sums of their own, in registers and rounded
 // to nearest, while the other accumulator takes the next period: a warp has 32 rows and a quarter of the columns.
@@ -29,9 +30,11 @@ constexpr int kPeriod = 4;
 template <int KB, int VB>
 struct SumSmem {
     static constexpr int kTile = 8192;  // 64 rows of a block
-    static constexpr int kLo = KB * kTile, kV = 2 * KB * kTile, kStage = (2 * KB + VB) * kTile;
-    static constexpr int kStages = 196608 / kStage > 8 ? 8 : 196608 / kStage;
-    static constexpr int zpart = kStages * kStage;            // float[2][16][64 KB]
+    static constexpr int kV = 2 * kTile, kStage = kV + VB * kTile;  // K: two blocks, or phi's parts
+    static constexpr int kLos = KB == 2 ? 3 : 0, kRoom = 212992 - kLos * 2 * kTile;
+    static constexpr int kStages = kRoom / kStage > 8 ? 8 : kRoom / kStage;
+    static constexpr int lo0 = kStages * kStage;
+    static constexpr int zpart = lo0 + kLos * 2 * kTile;      // float[2][16][64 KB]
     static constexpr int bars = zpart + 2 * 16 * 64 * KB * 4;
     static constexpr int total = bars + 512;
 };
@@ -41,10 +44,10 @@ __global__ void __launch_bounds__(kSumThreads, 1)
 cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, float* __restrict__ rec, Rows keys,
               int Dk, int slots, int* err) {
     using SM = SumSmem<KB, VB>;
-    constexpr int NS = SM::kStages, T = SM::kTile;
+    constexpr int NS = SM::kStages, T = SM::kTile, kLos = KB == 2 ? SM::kLos : 1;
     extern __shared__ __align__(1024) uint8_t smem[];
     struct Bars {
-        uint64_t full[8], ready[8], empty[8], acc_done[2], flushed[2], z_ready[2], z_free[2], final_mma;
+        uint64_t full[8], ready[8], empty[8], lo_free[3], acc_done[2], flushed[2], z_ready[2], z_free[2], final_mma;
         uint32_t tmem;
         Span span;
     };
@@ -56,9 +59,10 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     if (tid == 32) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&bar->full[s], 1);
-            mbar_init(&bar->ready[s], 256);
+            mbar_init(&bar->ready[s], 8);
             mbar_init(&bar->empty[s], 1);
         }
+        for (int l = 0; l < SM::kLos; ++l) mbar_init(&bar->lo_free[l], 1);
         for (int a = 0; a < 2; ++a) {
             mbar_init(&bar->acc_done[a], 1);
             mbar_init(&bar->flushed[a], 16);
@@ -103,6 +107,7 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     } else if (warp == 1) {
         if (lane == 0) {
             constexpr uint32_t id = idesc_bf16_f32(128, 64 * VB, 1, 1);
+            const uint32_t lo = smem_u32(smem + SM::lo0);
             int i = 0, period = 0;
             int in = 0;  // chunks of the period so far
             for (; w.more(); w.next(), ++i) {
@@ -114,9 +119,10 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 #pragma unroll
                 for (int kk = 0; kk < kSumRows / 16; ++kk) {
                     mma_ss(acc, desc_mn(st, kk, T), desc_mn(st + SM::kV, kk, T), id, in > 0 || kk > 0);
-                    if (KB == 2) mma_ss(acc, desc_mn(st + SM::kLo, kk, T), desc_mn(st + SM::kV, kk, T), id, 1);
+                    if (KB == 2) mma_ss(acc, desc_mn(lo + i % kLos * 2 * T, kk, T), desc_mn(st + SM::kV, kk, T), id, 1);
                 }
                 mma_commit(&bar->empty[s]);
+                if (KB == 2) mma_commit(&bar->lo_free[i % kLos]);
                 if (++in == kPeriod || w.last()) {
                     mma_commit(&bar->acc_done[a]);
                     ++period;
@@ -157,14 +163,17 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 for (int e = 0; e < 16; ++e) sum[16 * c + e] += __uint_as_float(x[e]);
             }
             tc_fence_before();
-            if (lane == 0) mbar_arrive(&bar->flushed[a]);
+            warp_arrive(&bar->flushed[a]);
             ++flushed;
         };
         for (; w.more() && ok; w.next(), ++i) {
             if ((i & 1) == group) {
                 const int s = i % NS, n = w.rows();
                 if (!(ok = warp_wait(&bar->full[s], (i / NS) & 1, err))) break;
+                if (KB == 2 && !(ok = warp_wait(&bar->lo_free[i % kLos], ((i / kLos) & 1) ^ 1, err))) break;
                 uint8_t* st = smem + s * SM::kStage + at;
+                uint8_t* lo = KB == 2 ? smem + SM::lo0 + i % kLos * 2 * T + at : st + T;
+                const bool whole = n == kSumRows && (Dk & 63) == 0;
                 uint4 x[KB][2];
 #pragma unroll
                 for (int b = 0; b < KB; ++b)
@@ -175,7 +184,7 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     const bool col = 64 * b + 8 * lc < Dk;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const bool live = col && (ct >> 3) + 32 * j < n;
+                        const bool live = whole || (col && (ct >> 3) + 32 * j < n);
                         uint32_t* u = reinterpret_cast<uint32_t*>(&x[b][j]);
                         uint4 l;
                         uint32_t* ul = reinterpret_cast<uint32_t*>(&l);
@@ -186,7 +195,7 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                             split2(p, u[e], ul[e]);
                         }
                         *reinterpret_cast<uint4*>(st + b * T + 4096 * j) = x[b][j];
-                        *reinterpret_cast<uint4*>(st + SM::kLo + b * T + 4096 * j) = l;
+                        *reinterpret_cast<uint4*>(lo + b * T + 4096 * j) = l;
                     }
                 }
                 if (n < kSumRows) {  // what lies behind the length may be anything
@@ -198,7 +207,7 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                                 *reinterpret_cast<uint4*>(st + SM::kV + b * T + 4096 * j) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(&bar->ready[s]);
+                warp_arrive(&bar->ready[s]);
             }
             const bool last = w.last();
             if (++in < kPeriod && !last) continue;
@@ -220,8 +229,7 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     if (lane < 8) to[64 * b + e] = z;
                     if (e & 1) zp[b][e >> 1] = norm::both(0.f);
                 }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar->z_ready[a]);
+            warp_arrive(&bar->z_ready[a]);
             const bool slot = LA_DCHECK((int)blockIdx.x + w.bh < slots);
             float* out = rec + (size_t)(blockIdx.x + w.bh) * record_floats(VB);
 #pragma unroll
@@ -237,8 +245,7 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 #pragma unroll
                     for (int x = 0; x < 16; ++x) z += zpart[(a * 16 + x) * 64 * KB + c];
                 if (slot) out[128 * 64 * VB + c] = z;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->z_free[a]);
+                warp_arrive(&bar->z_free[a]);
             }
             ++heads;
         }
@@ -363,12 +370,12 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         for (int s = 0; s < NS; ++s) {
             mbar_init(&bar->full[s], 1);
             mbar_init(&bar->empty[s], 1);
-            mbar_init(&bar->staged[s], 128);
+            mbar_init(&bar->staged[s], 4);
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&bar->s_full[g], 1);
             mbar_init(&bar->s_empty[g], 1);
-            mbar_init(&bar->ready[g], 128);
+            mbar_init(&bar->ready[g], 4);
             mbar_init(&bar->done[g], 1);
         }
         mbar_init(&bar->final_mma, 1);
@@ -475,7 +482,7 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const float2 inv = norm::both(over(den.x + den.y));
             fence_proxy_async_smem();
             tc_fence_before();
-            mbar_arrive(&bar->ready[g]);
+            warp_arrive(&bar->ready[g]);
             if (!warp_wait(&bar->done[g], (i >> 1) & 1, err)) break;
             tc_fence_after();
 #pragma unroll
@@ -494,7 +501,7 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
             }
             fence_proxy_async_smem();
-            mbar_arrive(&bar->staged[s]);
+            warp_arrive(&bar->staged[s]);
         }
     } else if (lane == 0) {
         // stores: a stage is empty once its outputs have been read

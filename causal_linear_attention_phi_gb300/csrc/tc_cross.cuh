@@ -48,6 +48,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* e
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, LA_ERR_TIMEOUT));
 }
 
+// One arrival for a warp, after all its lanes have got here (32 arrivals of lanes are 32 turns at the barrier's word).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // Debug build: a tile copy of a [heads][rows][D] tensor.
 __device__ __forceinline__ void check_copy(int x, int row, int rows, int bh, int heads) {
     LA_DCHECK((x == 0 || x == 64) && row >= 0 && row < rows && bh >= 0 && bh < heads);

@@ -117,18 +117,18 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             mbar_init(&bar->full[s], 1);
             mbar_init(&bar->empty[s], 2);  // R's product and r's
         }
-        mbar_init(&bar->staged, 256);
+        mbar_init(&bar->staged, 8);
         mbar_init(&bar->out_free, 1);
         for (int g = 0; g < 2; ++g) {
             mbar_init(&bar->y_done[g], 1);
-            mbar_init(&bar->y_free[g], 256);
-            mbar_init(&bar->x_ready[g], 256);
-            mbar_init(&bar->w_ready[g], 256);
+            mbar_init(&bar->y_free[g], 8);
+            mbar_init(&bar->x_ready[g], 8);
+            mbar_init(&bar->w_ready[g], 8);
             mbar_init(&bar->r_done[g], 2);  // R's product and r's
         }
         mbar_init(&bar->s_full, 1);
         mbar_init(&bar->s_empty, 17);  // the products and the compute warps (z)
-        mbar_init(&bar->r_flushed, 256);
+        mbar_init(&bar->r_flushed, 8);
         mbar_init(&bar->final_mma, 1);
         mbar_init(&bar->final_r, 1);
         fence_mbar_init();
@@ -317,7 +317,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     if (KB == 1) *reinterpret_cast<uint4*>(st + SM::kLo + swz(r, lc0 + c)) = l;
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(&bar->x_ready[g]);
+                warp_arrive(&bar->x_ready[g]);
                 // t = phi(q) . Y / den
                 ok = warp_wait(&bar->y_done[g], (i >> 1) & 1, err);
                 tc_fence_after();
@@ -344,7 +344,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     *reinterpret_cast<uint16_t*>(at + swz(1, lc)) = (uint16_t)tl;
                     fence_proxy_async_smem();
                 }
-                mbar_arrive(&bar->w_ready[g]);
+                warp_arrive(&bar->w_ready[g]);
                 // dq, packed until the tile of outputs is free
                 const float2 gz = both(-t * inv), iv = both(inv);
                 uint32_t dq[kHalf / 2];
@@ -368,14 +368,14 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(&bar->y_free[g]);
+                warp_arrive(&bar->y_free[g]);
                 // the tile of outputs is free once the chunk before has been stored
                 if (!(ok = pair_all(pair, i == 0 || warp_wait(&bar->out_free, (i - 1) & 1, err)))) break;
 #pragma unroll
                 for (int c = 0; c < kHalf / 8; ++c)
                     *reinterpret_cast<uint4*>(smem + SM::O0 + blk + swz(r, lc0 + c)) = make_uint4(dq[4 * c], dq[4 * c + 1], dq[4 * c + 2], dq[4 * c + 3]);
                 fence_proxy_async_smem();
-                mbar_arrive(&bar->staged);
+                warp_arrive(&bar->staged);
                 if (last && !(ok = pair_all(pair, warp_wait(&bar->r_done[g], (i >> 1) & 1, err)))) break;
                 if (last) {  // this head's sums
                     tc_fence_after();
@@ -388,12 +388,11 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         if (half == 0) out[128 * 64 * VB + r] = __uint_as_float(c[0]) + __uint_as_float(c[1]);
                     }
                     tc_fence_before();
-                    mbar_arrive(&bar->r_flushed);
+                    warp_arrive(&bar->r_flushed);
                 }
             }
             if (last) {  // z is no longer read
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->s_empty);
+                warp_arrive(&bar->s_empty);
             }
         }
     }
@@ -444,13 +443,13 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         for (int s = 0; s < NS; ++s) {
             mbar_init(&bar->full[s], 1);
             mbar_init(&bar->empty[s], 1);
-            mbar_init(&bar->staged[s], 256);
+            mbar_init(&bar->staged[s], 8);
         }
         for (int g = 0; g < 2; ++g) {
-            mbar_init(&bar->ready[g], 256);
+            mbar_init(&bar->ready[g], 8);
             mbar_init(&bar->k_done[g], 1);
             mbar_init(&bar->v_done[g], 1);
-            mbar_init(&bar->acc_free[g], 256);
+            mbar_init(&bar->acc_free[g], 8);
         }
         mbar_init(&bar->s_full, 1);
         mbar_init(&bar->s_empty, 17);  // the products and the compute warps (r)
@@ -575,7 +574,7 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                     *at = x;
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(&bar->ready[g]);
+                warp_arrive(&bar->ready[g]);
                 if (KB > VB && !warp_wait(&bar->v_done[g], (i >> 1) & 1, err)) break;  // dk lies over phi(K)
                 if (!warp_wait(&bar->k_done[g], (i >> 1) & 1, err)) break;
                 tc_fence_after();
@@ -625,12 +624,11 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(&bar->acc_free[g]);
-                mbar_arrive(&bar->staged[s]);
+                warp_arrive(&bar->acc_free[g]);
+                warp_arrive(&bar->staged[s]);
             }
             if (last) {  // r is no longer read
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->s_empty);
+                warp_arrive(&bar->s_empty);
             }
         }
     } else if (lane == 0) {

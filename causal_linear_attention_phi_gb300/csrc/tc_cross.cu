@@ -105,17 +105,18 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             mbar_drain(bar->full, NS, i, err, LA_ERR_TIMEOUT);  // no copy is left in flight
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t id = idesc_bf16_f32(128, 64 * VB, 1, 1);
-            const uint32_t lo = smem_u32(smem + SM::lo0);
-            int i = 0, period = 0;
-            int in = 0;  // chunks of the period so far
-            for (; w.more(); w.next(), ++i) {
-                const int s = i % NS, a = period & 1;
-                if (!mbar_wait(&bar->ready[s], (i / NS) & 1, err, LA_ERR_TIMEOUT)) break;
-                if (in == 0 && !mbar_wait(&bar->flushed[a], ((period >> 1) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
-                tc_fence_after();
-                const uint32_t st = smem_u32(smem + s * SM::kStage), acc = tmem + 64 * VB * a;
+        constexpr uint32_t id = idesc_bf16_f32(128, 64 * VB, 1, 1);
+        const uint32_t lo = smem_u32(smem + SM::lo0), t0 = uniform(tmem);
+        const int n = uniform(w.left);
+        int period = 0, in = 0;  // chunks of the period so far
+        for (int i = 0; i < n; ++i, w.next()) {
+            const int s = i % NS, a = period & 1;
+            if (!warp_wait(&bar->ready[s], (i / NS) & 1, err)) break;
+            if (in == 0 && !warp_wait(&bar->flushed[a], ((period >> 1) & 1) ^ 1, err)) break;
+            tc_fence_after();
+            const bool close = uniform(in + 1 == kPeriod || w.last());
+            if (elect_one()) {
+                const uint32_t st = smem_u32(smem + s * SM::kStage), acc = t0 + 64 * VB * a;
 #pragma unroll
                 for (int kk = 0; kk < kSumRows / 16; ++kk) {
                     mma_ss(acc, desc_mn(st, kk, T), desc_mn(st + SM::kV, kk, T), id, in > 0 || kk > 0);
@@ -123,15 +124,17 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 }
                 mma_commit(&bar->empty[s]);
                 if (KB == 2) mma_commit(&bar->lo_free[i % kLos]);
-                if (++in == kPeriod || w.last()) {
-                    mma_commit(&bar->acc_done[a]);
-                    ++period;
-                    in = 0;
-                }
+                if (close) mma_commit(&bar->acc_done[a]);
             }
+            __syncwarp();
+            ++in;
+            if (close) in = 0, ++period;
+        }
+        if (elect_one()) {
             mma_commit(&bar->final_mma);  // every product is complete before the accumulators are given back
             mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
         }
+        __syncwarp();
     } else {
         const int cw = warp - 2, group = cw >> 3, ct = (tid - 64) & 255;
         const int lc = (ct & 7) ^ ((ct >> 3) & 7), at = (ct >> 3) * 128 + (ct & 7) * 16;  // rows (ct >> 3) + 32 j
@@ -424,29 +427,35 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             mbar_drain(bar->s_full, 2, heads, err, LA_ERR_TIMEOUT);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t id = idesc_bf16_f32(128, 64 * VB, 0, 1);
-            int i = 0, heads = 0;
-            bool first = true;
-            for (; w.more(); w.next(), ++i) {
-                const int g = i & 1, s = i % NS;
-                if (first) ++heads;
-                const int h = (heads - 1) & 1;
-                if (first && !mbar_wait(&bar->s_full[h], ((heads - 1) >> 1) & 1, err, LA_ERR_TIMEOUT)) break;
-                // phi(Q) is in place, and the group has read the outputs of its previous chunk
-                if (!mbar_wait(&bar->ready[g], (i >> 1) & 1, err, LA_ERR_TIMEOUT)) break;
-                tc_fence_after();
+        constexpr uint32_t id = idesc_bf16_f32(128, 64 * VB, 0, 1);
+        const uint32_t t0 = uniform(tmem);
+        const int n = uniform(w.left);
+        int heads = 0;
+        bool first = true;
+        for (int i = 0; i < n; ++i, w.next()) {
+            const int g = i & 1, s = i % NS;
+            if (first) ++heads;
+            const int h = (heads - 1) & 1;
+            if (first && !warp_wait(&bar->s_full[h], ((heads - 1) >> 1) & 1, err)) break;
+            // phi(Q) is in place, and the group has read the outputs of its previous chunk
+            if (!warp_wait(&bar->ready[g], (i >> 1) & 1, err)) break;
+            tc_fence_after();
+            first = uniform(w.last());
+            if (elect_one()) {
                 const uint32_t aQ = smem_u32(smem + s * SM::kStage), aS = smem_u32(smem + SM::S0 + h * SM::kS);
 #pragma unroll
                 for (int kk = 0; kk < 4 * KB; ++kk)
-                    mma_ss(tmem + 64 * VB * g, desc_k(aQ, kk, T), desc_mn(aS, kk, 8192 * KB), id, kk > 0);
+                    mma_ss(t0 + 64 * VB * g, desc_k(aQ, kk, T), desc_mn(aS, kk, 8192 * KB), id, kk > 0);
                 mma_commit(&bar->done[g]);
-                first = w.last();
                 if (first) mma_commit(&bar->s_empty[h]);
             }
+            __syncwarp();
+        }
+        if (elect_one()) {
             mma_commit(&bar->final_mma);  // every product is complete before the accumulators are given back
             mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
         }
+        __syncwarp();
     } else if (warp < 10) {
         const int g = (warp - 2) >> 2, r = 32 * (warp & 3) + lane;
         const uint32_t acc = tmem + 64 * VB * g + ((uint32_t)(32 * (warp & 3)) << 16);

@@ -54,6 +54,20 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
+// The products are issued by one thread, but a whole warp goes through the loop around them: operands of tcgen05.mma are
+// uniform registers, which code that one lane runs alone has to fill one by one before each product (about 130 cycles a
+// product, which bound all four kernels).  `uniform` tells the compiler that all lanes hold the same value.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // Debug build: a tile copy of a [heads][rows][D] tensor.
 __device__ __forceinline__ void check_copy(int x, int row, int rows, int bh, int heads) {
     LA_DCHECK((x == 0 || x == 64) && row >= 0 && row < rows && bh >= 0 && bh < heads);

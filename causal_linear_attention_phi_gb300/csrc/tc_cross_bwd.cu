@@ -184,76 +184,89 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             mbar_drain(&bar->s_full, 1, heads, err, LA_ERR_TIMEOUT);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t id_y = idesc_bf16_f32(128, 64 * KB, 0, 0), id_r = idesc_bf16_f32(128, 64 * VB, 1, 1);
-            const uint32_t aS = smem_u32(smem + SM::S0), aSl = aS + (uint32_t)image_part(KB, VB);
-            bool ok = true, y_first = true, first = true;
-            int yi = 0, heads = 0, flushes = 0;
-            Walk wy = w;
-            auto issue_y = [&]() {  // Y of chunk yi: dO is all it needs, so it runs a chunk ahead
-                const int g = yi & 1, s = yi % NS;
-                if (y_first) ok = ok && mbar_wait(&bar->s_full, heads++ & 1, err, LA_ERR_TIMEOUT);
-                ok = ok && mbar_wait(&bar->full[s], (yi / NS) & 1, err, LA_ERR_TIMEOUT) &&
-                     mbar_wait(&bar->y_free[g], ((yi >> 1) & 1) ^ 1, err, LA_ERR_TIMEOUT);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t aD = smem_u32(smem + s * SM::kStage + SM::kDo), acc = tmem + kY + 64 * KB * g;
+        constexpr uint32_t id_y = idesc_bf16_f32(128, 64 * KB, 0, 0), id_r = idesc_bf16_f32(128, 64 * VB, 1, 1);
+        const uint32_t aS = smem_u32(smem + SM::S0), aSl = aS + (uint32_t)image_part(KB, VB), t0 = uniform(tmem);
+        const int n = uniform(w.left);
+        bool ok = true, y_first = true, first = true;
+        int yi = 0, heads = 0, flushes = 0;
+        Walk wy = w;
+        auto issue_y = [&]() {  // Y of chunk yi: dO is all it needs, so it runs a chunk ahead
+            const int g = yi & 1, s = yi % NS;
+            if (y_first) ok = ok && warp_wait(&bar->s_full, heads++ & 1, err);
+            ok = ok && warp_wait(&bar->full[s], (yi / NS) & 1, err) && warp_wait(&bar->y_free[g], ((yi >> 1) & 1) ^ 1, err);
+            if (!ok) return;
+            tc_fence_after();
+            y_first = uniform(wy.last());
+            if (elect_one()) {
+                const uint32_t aD = smem_u32(smem + s * SM::kStage + SM::kDo), acc = t0 + kY + 64 * KB * g;
 #pragma unroll
                 for (int kk = 0; kk < 4 * VB; ++kk) {
                     mma_ss(acc, desc_k(aD, kk, T), desc_k(aS, kk, 8192 * KB), id_y, kk > 0);
                     mma_ss(acc, desc_k(aD, kk, T), desc_k(aSl, kk, 8192 * KB), id_y, 1);
                 }
                 mma_commit(&bar->y_done[g]);
-                y_first = wy.last();
                 if (y_first) mma_commit(&bar->s_empty);
-                wy.next();
-                ++yi;
-            };
-            for (int i = 0; w.more() && ok; w.next(), ++i) {
-                const int g = i & 1, s = i % NS;
-                while (ok && yi <= i) issue_y();
-                ok = ok && mbar_wait(&bar->x_ready[g], (i >> 1) & 1, err, LA_ERR_TIMEOUT);
-                if (first && flushes > 0) ok = ok && mbar_wait(&bar->r_flushed, (flushes - 1) & 1, err, LA_ERR_TIMEOUT);
-                if (!ok) break;
-                tc_fence_after();
+            }
+            __syncwarp();
+            wy.next();
+            ++yi;
+        };
+        for (int i = 0; i < n && ok; ++i, w.next()) {
+            const int g = i & 1, s = i % NS;
+            if (yi <= i) issue_y();
+            ok = ok && warp_wait(&bar->x_ready[g], (i >> 1) & 1, err);
+            if (first && flushes > 0) ok = ok && warp_wait(&bar->r_flushed, (flushes - 1) & 1, err);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
                 const uint32_t st = smem_u32(smem + s * SM::kStage), aD = st + SM::kDo;
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    mma_ss(tmem + kR, desc_mn(st, kk, T), desc_mn(aD, kk, T), id_r, !first || kk > 0);
+                    mma_ss(t0 + kR, desc_mn(st, kk, T), desc_mn(aD, kk, T), id_r, !first || kk > 0);
                 mma_commit(&bar->r_done[g]);
                 mma_commit(&bar->empty[s]);
-                first = w.last();
-                if (first) ++flushes;
-                if (ok && wy.more() && yi == i + 1 && !y_first) issue_y();  // unless it needs the next head's S
             }
+            __syncwarp();
+            first = uniform(w.last());
+            if (first) ++flushes;
+            // the next chunk's Y (its group's previous chunk, i - 1, is through), unless it needs the next head's S, for
+            // which all of this head's chunks have to be through
+            if (i + 1 < n && yi == i + 1 && !y_first) issue_y();
+        }
+        if (elect_one()) {
             mma_commit(&bar->final_mma);  // every product is complete before the accumulators are given back
             mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
         }
+        __syncwarp();
     } else if (warp == 3) {
         // r's products are ready later than R's, and their own thread's: behind one that waits for the other group's X they
         // held each group back until the other had caught up (358 us of B=2 H=16 N=32768 128 x 128)
-        if (lane == 0) {
-            constexpr uint32_t id_w = idesc_bf16_f32(128, 16, 1, 0);
-            const uint32_t aW = smem_u32(smem + SM::W);
-            bool first = true;
-            int flushes = 0;
-            for (int i = 0; w.more(); w.next(), ++i) {
-                const int g = i & 1, s = i % NS;
-                if (!mbar_wait(&bar->w_ready[g], (i >> 1) & 1, err, LA_ERR_TIMEOUT)) break;
-                if (first && flushes > 0 && !mbar_wait(&bar->r_flushed, (flushes - 1) & 1, err, LA_ERR_TIMEOUT)) break;
-                tc_fence_after();
+        constexpr uint32_t id_w = idesc_bf16_f32(128, 16, 1, 0);
+        const uint32_t aW = smem_u32(smem + SM::W), t0 = uniform(tmem);
+        const int n = uniform(w.left);
+        bool first = true;
+        int flushes = 0;
+        for (int i = 0; i < n; ++i, w.next()) {
+            const int g = i & 1, s = i % NS;
+            if (!warp_wait(&bar->w_ready[g], (i >> 1) & 1, err)) break;
+            if (first && flushes > 0 && !warp_wait(&bar->r_flushed, (flushes - 1) & 1, err)) break;
+            tc_fence_after();
+            if (elect_one()) {
                 const uint32_t st = smem_u32(smem + s * SM::kStage);
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ss(tmem + kW, desc_mn(st, kk, T), desc_k(aW, kk, 1024), id_w, !first || kk > 0);
+                for (int kk = 0; kk < 8; ++kk) mma_ss(t0 + kW, desc_mn(st, kk, T), desc_k(aW, kk, 1024), id_w, !first || kk > 0);
                 mma_commit(&bar->r_done[g]);
                 mma_commit(&bar->empty[s]);
-                first = w.last();
-                if (first) ++flushes;
             }
+            __syncwarp();
+            first = uniform(w.last());
+            if (first) ++flushes;
+        }
+        if (elect_one()) {
             mma_commit(&bar->final_r);  // as above
             mbar_wait(&bar->final_r, 0, err, LA_ERR_TIMEOUT);
         }
+        __syncwarp();
     } else if (warp == 2) {
         if (lane == 0) {  // stores
             for (int i = 0; w.more(); w.next(), ++i) {
@@ -505,49 +518,57 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             mbar_drain(&bar->s_full, 1, heads, err, LA_ERR_TIMEOUT);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t id_k = idesc_bf16_f32(128, 64 * KB, 0, 0), id_v = idesc_bf16_f32(128, 64 * VB, 0, 1);
-            const uint32_t aR = smem_u32(smem + SM::R0), aRl = aR + (uint32_t)image_part(KB, VB);
-            int i = 0, vi = 0, heads = 0;
-            Walk wv = w;  // V R^T runs a chunk ahead
-            bool v_first = true, ok = true;
-            auto issue_k = [&]() {  // dK without r and phi' of chunk vi
-                const int g = vi & 1, s = vi % NS;
-                if (v_first) ok = ok && mbar_wait(&bar->s_full, heads++ & 1, err, LA_ERR_TIMEOUT);
-                ok = ok && mbar_wait(&bar->full[s], (vi / NS) & 1, err, LA_ERR_TIMEOUT) &&
-                     mbar_wait(&bar->acc_free[g], ((vi >> 1) & 1) ^ 1, err, LA_ERR_TIMEOUT);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t aV = smem_u32(smem + s * SM::kStage + SM::kV), acc = tmem + kSet * g;
+        constexpr uint32_t id_k = idesc_bf16_f32(128, 64 * KB, 0, 0), id_v = idesc_bf16_f32(128, 64 * VB, 0, 1);
+        const uint32_t aR = smem_u32(smem + SM::R0), aRl = aR + (uint32_t)image_part(KB, VB), t0 = uniform(tmem);
+        const int n = uniform(w.left);
+        int vi = 0, heads = 0;
+        Walk wv = w;  // V R^T runs a chunk ahead
+        bool v_first = true, ok = true;
+        auto issue_k = [&]() {  // dK without r and phi' of chunk vi
+            const int g = vi & 1, s = vi % NS;
+            if (v_first) ok = ok && warp_wait(&bar->s_full, heads++ & 1, err);
+            ok = ok && warp_wait(&bar->full[s], (vi / NS) & 1, err) && warp_wait(&bar->acc_free[g], ((vi >> 1) & 1) ^ 1, err);
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t aV = smem_u32(smem + s * SM::kStage + SM::kV), acc = t0 + kSet * g;
 #pragma unroll
                 for (int kk = 0; kk < 4 * VB; ++kk) {
                     mma_ss(acc, desc_k(aV, kk, T), desc_k(aR, kk, 8192 * KB), id_k, kk > 0);
                     mma_ss(acc, desc_k(aV, kk, T), desc_k(aRl, kk, 8192 * KB), id_k, 1);
                 }
                 mma_commit(&bar->k_done[g]);
-                v_first = wv.last();
-                wv.next();
-                ++vi;
-            };
-            for (; w.more() && ok; w.next(), ++i) {
-                const int g = i & 1, s = i % NS;
-                while (ok && vi <= i) issue_k();
-                if (!ok || !mbar_wait(&bar->ready[g], (i >> 1) & 1, err, LA_ERR_TIMEOUT)) break;
-                tc_fence_after();
-                const uint32_t aK = smem_u32(smem + s * SM::kStage), acc = tmem + kSet * g + 64 * KB;
+            }
+            __syncwarp();
+            v_first = uniform(wv.last());
+            wv.next();
+            ++vi;
+        };
+        for (int i = 0; i < n && ok; ++i, w.next()) {
+            const int g = i & 1, s = i % NS;
+            if (vi <= i) issue_k();
+            if (!ok || !warp_wait(&bar->ready[g], (i >> 1) & 1, err)) break;
+            tc_fence_after();
+            const bool last = uniform(w.last());
+            if (elect_one()) {
+                const uint32_t aK = smem_u32(smem + s * SM::kStage), acc = t0 + kSet * g + 64 * KB;
 #pragma unroll
                 for (int kk = 0; kk < 4 * KB; ++kk) {
                     mma_ss(acc, desc_k(aK, kk, T), desc_mn(aR, kk, 8192 * KB), id_v, kk > 0);
                     mma_ss(acc, desc_k(aK, kk, T), desc_mn(aRl, kk, 8192 * KB), id_v, 1);
                 }
                 mma_commit(&bar->v_done[g]);
-                if (w.last()) mma_commit(&bar->s_empty);
-                // the next chunk's, unless it needs the next head's R, for which this head has to be through
-                if (wv.more() && vi == i + 1 && !v_first) issue_k();
+                if (last) mma_commit(&bar->s_empty);
             }
+            __syncwarp();
+            // the next chunk's, unless it needs the next head's R, for which this head has to be through
+            if (i + 1 < n && vi == i + 1 && !v_first) issue_k();
+        }
+        if (elect_one()) {
             mma_commit(&bar->final_mma);  // every product is complete before the accumulators are given back
             mbar_wait(&bar->final_mma, 0, err, LA_ERR_TIMEOUT);
         }
+        __syncwarp();
     } else if (warp < 18) {
         constexpr int kHalfK = 32 * KB, kHalfV = 32 * VB;  // columns of this thread: its half of row r
         const int g = (warp - 2) >> 3, half = ((warp - 2) >> 2) & 1, r = 32 * (warp & 3) + lane;

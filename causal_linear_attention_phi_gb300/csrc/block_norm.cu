@@ -231,8 +231,8 @@ columns_join_kernel(const float* __restrict__ part, Outs out, int blocks, int C,
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx, all = K * C;
     float v = 0.f;
     if (c < all) {
-#pragma unroll 4
-        for (int i = ty; i < blocks; i += 32) v += part[(size_t)i * pitch + c];
+#pragma unroll 10
+        for (int i = ty; i < blocks; i += 32) v += part[(size_t)i * pitch + c];  // in that order; the loads of ten go together
     }
     s[ty][tx] = v;
     __syncthreads();

@@ -1,7 +1,8 @@
 // cross.cuh -- cross attention: shapes, the split of its work over blocks, and the host launchers of its kernels.
 //
 // Work is a flat list of chunks of rows, head after head; a head of keys has as many as its batch entry's length asks
-// for.  Block c of `ctas` takes the chunks [total c / ctas, total (c + 1) / ctas), so that every block has the same share
+// for.  Of `ctas` blocks as many work as there are chunks, each with one at least (a block without any would leave a gap
+// in a head's records); block c of those takes the chunks [total c / ctas, total (c + 1) / ctas), so that every block has the same share
 // whatever the lengths are, and writes one record for each head that it meets.  Walking on, a block comes to a new (block,
 // head) pair whenever either number grows, so block + head numbers the records without gaps that overlap.
 #pragma once
@@ -45,9 +46,10 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const Rows& r, int chunk, bool dead, int cta, int ctas) {  // a whole warp
     const long long total = chunks_before(r, r.B, chunk, dead) * r.Hk;
+    if (total < ctas) ctas = (int)total;
+    if (cta >= ctas) return Span{0, 0, 0};
     long long from = total * cta / ctas;
     Span s{0, 0, (int)(total * (cta + 1) / ctas - from)};
-    if (s.left == 0) return s;
     int b = 0;
     if (!r.lens) {
         const long long n = (long long)r.chunks(0, chunk, dead) * r.Hk;
@@ -118,6 +120,7 @@ __device__ __forceinline__ Range records_of(const Rows& r, int chunk, int bh, in
     const int b = bh / r.Hk;
     const long long n = r.chunks(b, chunk, false), total = chunks_before(r, r.B, chunk, false) * r.Hk;
     if (n == 0) return Range{1, 0};
+    if (total < ctas) ctas = (int)total;
     const long long from = chunks_before(r, b, chunk, false) * r.Hk + (bh - b * r.Hk) * n;
     // the block of chunk f is the largest c with floor(total c / ctas) <= f
     return Range{(int)(((from + 1) * ctas - 1) / total), (int)(((from + n) * ctas - 1) / total)};
@@ -155,8 +158,6 @@ cudaError_t tc_fwd(const FwdArgs& a, const la_cross_shape& s, char* ws, cudaStre
 cudaError_t tc_bwd(const BwdArgs& a, const la_cross_shape& s, char* ws, cudaStream_t st);
 cudaError_t tc_apply(const void* q, const float* S, const float* z, void* o, const la_cross_shape& s, char* ws,
                      cudaStream_t st);
-// dk and dv of the rows behind the lengths, which are 0.
-cudaError_t clear_behind(void* dk, void* dv, const Rows& keys, const la_cross_shape& s, cudaStream_t st);
 // A few rows of queries to a state: each state is read once, into registers.
 cudaError_t apply_few(const void* q, const float* S, const float* z, void* o, const la_cross_shape& s, cudaStream_t st);
 

@@ -151,20 +151,36 @@ cross_sums_kernel(const float* __restrict__ k, const float* __restrict__ v, floa
 }
 
 // ------------------------------------------------------------------ a head's records added up
-// E = Dk Dv + Dk floats to a record, the state's first; S and z get their parts.
+// E = Dk Dv + Dk floats to a record, the state's first; S and z get their parts.  kLanes threads share four floats, each taking
+// every kLanes-th record; their sums are added in a fixed order.
+template <int kLanes>
 __global__ void __launch_bounds__(256)
 cross_join_kernel(const float* __restrict__ rec, float* __restrict__ S, float* __restrict__ z, Rows rows, int chunk,
                   int ctas, int state, int dk) {
+    constexpr int kOwn = 256 / kLanes;
+    __shared__ float4 part[kLanes][kOwn];
     pdl_enter();  // launched with programmatic dependent launch
-    const int bh = blockIdx.x, E = state + dk, e4 = (blockIdx.y * 256 + threadIdx.x) * 4;
+    const int bh = blockIdx.x, x = threadIdx.x % kOwn, lane = threadIdx.x / kOwn, E = state + dk, e4 = (blockIdx.y * kOwn + x) * 4;
     const Range g = records_of(rows, chunk, bh, ctas);
-    if (e4 >= E) return;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (e4 < E) {
 #pragma unroll 8
-    for (int c = g.first; c <= g.last; ++c) {
-        const float4 f = *reinterpret_cast<const float4*>(rec + (size_t)(c + bh) * E + e4);
-        a.x += f.x, a.y += f.y, a.z += f.z, a.w += f.w;
+        for (int c = g.first + lane; c <= g.last; c += kLanes) {
+            const float4 f = *reinterpret_cast<const float4*>(rec + (size_t)(c + bh) * E + e4);
+            a.x += f.x, a.y += f.y, a.z += f.z, a.w += f.w;
+        }
     }
+    if (kLanes > 1) {
+        part[lane][x] = a;
+        __syncthreads();
+        if (lane != 0) return;
+#pragma unroll
+        for (int l = 1; l < kLanes; ++l) {
+            const float4 f = part[l][x];
+            a.x += f.x, a.y += f.y, a.z += f.z, a.w += f.w;
+        }
+    }
+    if (e4 >= E) return;
     float* to = e4 < state ? S + (size_t)bh * state + e4 : z + (size_t)bh * dk + (e4 - state);
     *reinterpret_cast<float4*>(to) = a;
 }
@@ -341,11 +357,10 @@ cross_clear_kernel(char* __restrict__ dk, char* __restrict__ dv, Rows keys, int 
 }
 
 // ------------------------------------------------------------------ host
-// Blocks: a wave of the SMs or two, each with at least two chunks where there are that many.
+// Blocks: a wave of the SMs or two, or one to a chunk.
 int blocks_for(long long heads, long long rows, int per_sm) {
     const long long chunks = heads * ((rows + kChunk - 1) / kChunk), most = 152LL * per_sm;
-    const long long want = (chunks + 1) / 2;
-    return (int)(want < 1 ? 1 : want > most ? most : want);
+    return (int)(chunks < most ? chunks : most);
 }
 int key_blocks(const la_cross_shape& s) { return blocks_for((long long)s.B * s.Hk, s.M, 2); }
 int query_blocks(const la_cross_shape& s) { return blocks_for((long long)s.B * s.Hk, query_rows(s), 1); }
@@ -387,8 +402,11 @@ cudaError_t run(const char* name, K kern, dim3 grid, size_t smem, cudaStream_t s
 
 cudaError_t join(const float* rec, float* S, float* z, const Rows& rows, int ctas, const la_cross_shape& s, cudaStream_t st) {
     const int E = s.Dk * s.Dv + s.Dk;
-    return run("cross_join", cross_join_kernel, dim3(rows.heads(), (E + 1023) / 1024), 0, st, rec, S, z, rows, kChunk, ctas,
-               s.Dk * s.Dv, s.Dk);
+    auto go = [&](auto kern, int own) {
+        return run("cross_join", kern, dim3(rows.heads(), (E + 4 * own - 1) / (4 * own)), 0, st, rec, S, z, rows, kChunk, ctas,
+                   s.Dk * s.Dv, s.Dk);
+    };
+    return ctas > 4 * rows.heads() ? go(cross_join_kernel<8>, 32) : go(cross_join_kernel<1>, 256);
 }
 
 template <int DK, int DV>
@@ -433,18 +451,14 @@ cudaError_t bwd_t(const BwdArgs& a, const la_cross_shape& s, char* ws, cudaStrea
     CR_TRY(join(rec, R, r, rows, qc, s, st));
     CR_TRY(run("cross_key", cross_key_kernel<DK, DV>, dim3(blocks_for(keys.heads(), s.M, 1)),
                (2 * DK * DV + kChunk * (DK + DV) + DK) * 4, st, (const float*)a.k, (const float*)a.v, R, r, (float*)a.dk, (float*)a.dv, keys));
-    return a.lens ? clear_behind(a.dk, a.dv, keys, s, st) : cudaSuccess;
+    if (!a.lens) return cudaSuccess;
+    return run("cross_clear", cross_clear_kernel, dim3(8, keys.heads()), 0, st, (char*)a.dk, (char*)a.dv, keys, 4 * s.Dk, 4 * s.Dv);
 }
 
 #define LA_SIZES(F) F(16, 16) F(16, 32) F(16, 64) F(16, 128) F(32, 16) F(32, 32) F(32, 64) F(32, 128) \
     F(64, 16) F(64, 32) F(64, 64) F(64, 128) F(128, 16) F(128, 32) F(128, 64) F(128, 128)
 
 }  // namespace
-
-cudaError_t clear_behind(void* dk, void* dv, const Rows& keys, const la_cross_shape& s, cudaStream_t st) {
-    const int elem = s.dtype == LA_BF16 ? 2 : 4;
-    return run("cross_clear", cross_clear_kernel, dim3(8, keys.heads()), 0, st, (char*)dk, (char*)dv, keys, s.Dk * elem, s.Dv * elem);
-}
 
 size_t simt_bytes(const la_cross_shape& s, int op) { return layout(s, op == LA_OP_CROSS_BWD).bytes; }
 

@@ -29,26 +29,43 @@ cross_few_kernel(const T* __restrict__ q, const float* __restrict__ S, const flo
     using F = Few<DK, DV>;
     __shared__ float ph[kRows][DK];
     __shared__ float part[F::kWarps][kRows][DV];
-    __shared__ float inv[kRows];
+    __shared__ float inv[kRows], zs[DK];
     pdl_enter();  // launched with programmatic dependent launch
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c4 = tid % F::kCols, r0 = tid / F::kCols;
-    const size_t bh = blockIdx.x;
-    const float* Sh = S + bh * DK * pitch + blockIdx.y * DV;
+    const size_t bh = blockIdx.y;
+    const float* Sh = S + bh * DK * pitch + blockIdx.x * DV;
     const float* zh = z + bh * DK;
     float4 s[F::kHeld];
 #pragma unroll
     for (int x = 0; x < F::kHeld; ++x)
         s[x] = *reinterpret_cast<const float4*>(Sh + (size_t)(r0 + F::kPer * x) * pitch + 4 * c4);
+    // z and the first rows of q are on their way together with S: loads one after another were three latencies to a block
+    constexpr int kZ = (DK + F::kThreads - 1) / F::kThreads, kQ = (kRows * DK + F::kThreads - 1) / F::kThreads;
     const T* qh = q + bh * R * DK;
-    T* oh = o + bh * R * pitch + blockIdx.y * DV;
+    float zr[kZ], qr[kQ];
+    auto fetch_q = [&](int base) {
+        const int all = min(kRows, R - base) * DK;
+#pragma unroll
+        for (int x = 0; x < kQ; ++x) qr[x] = tid + x * F::kThreads < all ? to_f32(qh[(size_t)base * DK + tid + x * F::kThreads]) : 0.f;
+    };
+    fetch_q(0);
+#pragma unroll
+    for (int x = 0; x < kZ; ++x) zr[x] = tid + x * F::kThreads < DK ? zh[tid + x * F::kThreads] : 0.f;
+#pragma unroll
+    for (int x = 0; x < kZ; ++x)
+        if (tid + x * F::kThreads < DK) zs[tid + x * F::kThreads] = zr[x];
+    T* oh = o + bh * R * pitch + blockIdx.x * DV;
     for (int base = 0; base < R; base += kRows) {
         const int n = min(kRows, R - base);
-        for (int x = tid; x < n * DK; x += F::kThreads) ph[x / DK][x % DK] = phi_f(to_f32(qh[(size_t)base * DK + x]));
+#pragma unroll
+        for (int x = 0; x < kQ; ++x)
+            if (tid + x * F::kThreads < n * DK) (&ph[0][0])[tid + x * F::kThreads] = phi_f(qr[x]);
         __syncthreads();
+        if (base + kRows < R) fetch_q(base + kRows);
         for (int r = warp; r < n; r += F::kWarps) {
             float den = 0.f;
-            for (int d = lane; d < DK; d += 32) den = fmaf(ph[r][d], zh[d], den);
+            for (int d = lane; d < DK; d += 32) den = fmaf(ph[r][d], zs[d], den);
 #pragma unroll
             for (int y = 16; y > 0; y >>= 1) den += __shfl_xor_sync(0xffffffffu, den, y);
             if (lane == 0) inv[r] = over(den);
@@ -92,7 +109,7 @@ cudaError_t go(const void* q, const float* S, const float* z, void* o, int heads
                 : R == 2 ? cross_few_kernel<T, DK, kCols, 2>
                          : cross_few_kernel<T, DK, kCols, 4>;
     launch_begin("cross_few", st);
-    const cudaError_t e = launch_pdl(kern, dim3(heads, DV / kCols), dim3(Few<DK, kCols>::kThreads), 0, st, (const T*)q, S, z, (T*)o, R, DV);
+    const cudaError_t e = launch_pdl(kern, dim3(DV / kCols, heads), dim3(Few<DK, kCols>::kThreads), 0, st, (const T*)q, S, z, (T*)o, R, DV);
     const cudaError_t e2 = launch_end("cross_few", st);
     return e != cudaSuccess ? e : e2;
 }

@@ -19,8 +19,7 @@ namespace {
 
 // ------------------------------------------------------------------ sums over the keys
 // A stage holds a chunk of 64 rows: K (phi's hi part in place) and V.  phi's lo part: for KB = 1 in the stage, hi and lo being the
-// two 64-row halves of one 128-row product; for KB = 2 in a ring of its own, held only while the products run, which leaves
-// room for a fifth stage.  An accumulator in tensor memory takes kPeriod chunks only:
+// two 64-row halves of one 128-row product; for KB = 2 in a ring of its own, held only while the products run.  An accumulator in tensor memory takes kPeriod chunks only:
 // the products add with truncation, half a unit in the last place each and always the same way (131,072 keys summed in one
 // accumulator to a block were 2e-5 off).  The compute warps then add it to sums of their own, in registers and rounded
 // to nearest, while the other accumulator takes the next period: a warp has 32 rows and a quarter of the columns.
@@ -32,7 +31,7 @@ struct SumSmem {
     static constexpr int kTile = 8192;  // 64 rows of a block
     static constexpr int kV = 2 * kTile, kStage = kV + VB * kTile;  // K: two blocks, or phi's parts
     static constexpr int kLos = KB == 2 ? 3 : 0, kRoom = 212992 - kLos * 2 * kTile;
-    static constexpr int kStages = kRoom / kStage > 8 ? 8 : kRoom / kStage;
+    static constexpr int kStages = even_stages(kRoom / kStage, 8);
     static constexpr int lo0 = kStages * kStage;
     static constexpr int zpart = lo0 + kLos * 2 * kTile;      // float[2][16][64 KB]
     static constexpr int bars = zpart + 2 * 16 * 64 * KB * 4;
@@ -282,6 +281,7 @@ cross_join_tc(const float* __restrict__ rec, const float* __restrict__ S, const 
             if (!rec)
                 a = d < Dk ? z[(size_t)bh * Dk + d] : 0.f;
             else
+#pragma unroll 4
                 for (int c = g.first; c <= g.last; ++c) {
                     const float* p = rec + (size_t)(c + bh) * record_floats(VB) + 128 * 64 * VB + d;
                     a += KB == 1 ? p[0] + p[64] : p[0];
@@ -346,7 +346,7 @@ template <int KB, int VB>
 struct ApplySmem {
     static constexpr int kTile = 16384;  // 128 rows of a block
     static constexpr int kS = (int)image_part(KB, VB), kStage = (KB > VB ? KB : VB) * kTile;
-    static constexpr int kStages = (229376 - 2 * kS) / kStage > 6 ? 6 : (229376 - 2 * kS) / kStage;
+    static constexpr int kStages = even_stages((229376 - 2 * kS) / kStage, 6);
     static constexpr int S0 = kStages * kStage;     // two
     static constexpr int z0 = S0 + 2 * kS;          // float[2][64 KB]
     static constexpr int bars = z0 + 2 * 256 * KB;
@@ -462,13 +462,15 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         int i = 0, heads = 0;
         bool first = true;
         for (; w.more(); w.next(), ++i) {
-            if (first) ++heads;
+            const int h = (first ? heads : heads - 1) & 1;
+            // every head's, whether or not it has a chunk of this group: a wait that skips a phase can be let through by the one before
+            if (first && !warp_wait(&bar->s_full[h], (heads++ >> 1) & 1, err)) break;
             first = w.last();
             if ((i & 1) != g) continue;
-            const int s = i % NS, h = (heads - 1) & 1;
+            const int s = i % NS;
             uint8_t* st = smem + s * SM::kStage;
             const float* zs = reinterpret_cast<const float*>(smem + SM::z0 + h * 256 * KB);
-            if (!warp_wait(&bar->s_full[h], ((heads - 1) >> 1) & 1, err) || !warp_wait(&bar->full[s], (i / NS) & 1, err)) break;
+            if (!warp_wait(&bar->full[s], (i / NS) & 1, err)) break;
             float2 den = norm::both(0.f);
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
@@ -535,9 +537,9 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 constexpr int kSms = 152;
-int ctas_for(long long heads, long long rows, int chunk, int least) {
-    const long long chunks = heads * ((rows + chunk - 1) / chunk), want = (chunks + least - 1) / least;
-    return (int)(want < 1 ? 1 : want > kSms ? kSms : want);
+int ctas_for(long long heads, long long rows, int chunk) {  // a block to an SM, or to a chunk
+    const long long chunks = heads * ((rows + chunk - 1) / chunk);
+    return (int)(chunks < kSms ? chunks : kSms);
 }
 
 cudaError_t answers(const void* q, void* o, const char* image, const la_cross_shape& s, cudaStream_t st) {
@@ -546,7 +548,7 @@ cudaError_t answers(const void* q, void* o, const char* image, const la_cross_sh
     if (!make_tmap_bf16_rows(&tq, q, rows.heads(), rows.M, s.Dk, kRowChunk) ||
         !make_tmap_bf16_rows(&to, o, rows.heads(), rows.M, s.Dv, kRowChunk))
         return cudaErrorInvalidValue;
-    const int ctas = ctas_for(rows.heads(), rows.M, kRowChunk, 1);
+    const int ctas = ctas_for(rows.heads(), rows.M, kRowChunk);
     auto go = [&](auto kern, size_t smem) {
         return tc_run("cross_apply_tc", kern, dim3(ctas), kApplyThreads, smem, st, tq, to, image, rows, device_error_word());
     };
@@ -567,11 +569,11 @@ TcLayout tc_layout(const la_cross_shape& s, int op) {
     const size_t heads = (size_t)s.B * s.Hk, image = up(heads * image_bytes(KB, VB)), rec = record_floats(VB) * 4;
     TcLayout l{};
     if (op != LA_OP_CROSS_APPLY) {
-        l.sum_ctas = ctas_for(heads, s.M, kSumRows, 2);
-        l.key_ctas = ctas_for(heads, s.M, kRowChunk, 1);
+        l.sum_ctas = ctas_for(heads, s.M, kSumRows);
+        l.key_ctas = ctas_for(heads, s.M, kRowChunk);
         size_t most = l.sum_ctas;
         if (op == LA_OP_CROSS_BWD) {
-            l.query_ctas = ctas_for(heads, query_rows(s), kRowChunk, 1);
+            l.query_ctas = ctas_for(heads, query_rows(s), kRowChunk);
             if ((size_t)l.query_ctas > most) most = l.query_ctas;
         }
         l.bytes = up((most + heads) * rec);

@@ -30,6 +30,10 @@ constexpr size_t image_bytes(int KB, int VB) { return 2 * image_part(KB, VB) + (
 // lo parts and are added to the lower).
 constexpr size_t record_floats(int VB) { return (size_t)128 * 64 * VB + 128; }
 
+// Stages of a ring that two groups take in turn: an even number, so that a stage is always the same group's, which then waits
+// for each of its phases (a wait that skips one can be let through by the phase before).
+constexpr int even_stages(int fit, int most) { return (fit < most ? fit : most) / 2 * 2; }
+
 inline int blocks64(int d) { return d > 64 ? 2 : 1; }
 
 __device__ __forceinline__ int swz(int row, int lc) { return row * 128 + (((lc & 7) ^ (row & 7)) << 4); }

@@ -81,7 +81,7 @@ template <int KB, int VB>
 struct QuerySmem {
     static constexpr int kLo = T, kDo = 2 * T, kStage = kDo + VB * T;  // Q: two blocks, or X's parts
     static constexpr int kS = 2 * (int)image_part(KB, VB), kOut = KB * T;
-    static constexpr int kStages = (229376 - kS - kOut) / kStage > 4 ? 4 : (229376 - kS - kOut) / kStage;
+    static constexpr int kStages = even_stages((229376 - kS - kOut) / kStage, 4);
     static constexpr int S0 = kStages * kStage, O0 = S0 + kS;
     static constexpr int W = O0 + kOut;        // 2 blocks of 8 rows x 128 bytes
     static constexpr int z0 = W + 2048;        // float[64 KB]
@@ -102,8 +102,8 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     constexpr uint32_t kCols = kX + 8 <= 256 ? 256 : 512;
     extern __shared__ __align__(1024) uint8_t smem[];
     struct Bars {
-        uint64_t full[4], empty[4], staged, out_free, s_full, s_empty, y_done[2], y_free[2], x_ready[2], w_ready[2], r_done[2], r_flushed,
-            final_mma, final_r;
+        uint64_t full[4], empty[4], staged, out_free[2], s_full, s_empty, y_done[2], y_free[2], x_ready[2], w_ready[2], r_done[2], sums_done,
+            r_flushed, final_mma, final_r;
         uint32_t tmem;
         Span span;
     };
@@ -118,16 +118,17 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             mbar_init(&bar->empty[s], 2);  // R's product and r's
         }
         mbar_init(&bar->staged, 8);
-        mbar_init(&bar->out_free, 1);
         for (int g = 0; g < 2; ++g) {
             mbar_init(&bar->y_done[g], 1);
             mbar_init(&bar->y_free[g], 8);
             mbar_init(&bar->x_ready[g], 8);
             mbar_init(&bar->w_ready[g], 8);
-            mbar_init(&bar->r_done[g], 2);  // R's product and r's
+            mbar_init(&bar->r_done[g], 1);
+            mbar_init(&bar->out_free[g], 1);
         }
         mbar_init(&bar->s_full, 1);
         mbar_init(&bar->s_empty, 17);  // the products and the compute warps (z)
+        mbar_init(&bar->sums_done, 2);  // a head's last products of R and of r
         mbar_init(&bar->r_flushed, 8);
         mbar_init(&bar->final_mma, 1);
         mbar_init(&bar->final_r, 1);
@@ -218,16 +219,17 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (first && flushes > 0) ok = ok && warp_wait(&bar->r_flushed, (flushes - 1) & 1, err);
             if (!ok) break;
             tc_fence_after();
+            const bool last = uniform(w.last());
             if (elect_one()) {
                 const uint32_t st = smem_u32(smem + s * SM::kStage), aD = st + SM::kDo;
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                     mma_ss(t0 + kR, desc_mn(st, kk, T), desc_mn(aD, kk, T), id_r, !first || kk > 0);
-                mma_commit(&bar->r_done[g]);
                 mma_commit(&bar->empty[s]);
+                if (last) mma_commit(&bar->sums_done);
             }
             __syncwarp();
-            first = uniform(w.last());
+            first = last;
             if (first) ++flushes;
             // the next chunk's Y (its group's previous chunk, i - 1, is through), unless it needs the next head's S, for
             // which all of this head's chunks have to be through
@@ -251,15 +253,17 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (!warp_wait(&bar->w_ready[g], (i >> 1) & 1, err)) break;
             if (first && flushes > 0 && !warp_wait(&bar->r_flushed, (flushes - 1) & 1, err)) break;
             tc_fence_after();
+            const bool last = uniform(w.last());
             if (elect_one()) {
                 const uint32_t st = smem_u32(smem + s * SM::kStage);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) mma_ss(t0 + kW, desc_mn(st, kk, T), desc_k(aW, kk, 1024), id_w, !first || kk > 0);
-                mma_commit(&bar->r_done[g]);
                 mma_commit(&bar->empty[s]);
+                if (last) mma_commit(&bar->sums_done);
+                mma_commit(&bar->r_done[g]);
             }
             __syncwarp();
-            first = uniform(w.last());
+            first = last;
             if (first) ++flushes;
         }
         if (elect_one()) {
@@ -275,7 +279,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 for (int b = 0; b < KB; ++b) tma_store_3d(&tm_dq, smem + SM::O0 + b * T, 64 * b, w.row0(), w.bh);
                 bulk_commit();
                 bulk_wait_read_all();
-                mbar_arrive(&bar->out_free);
+                mbar_arrive(&bar->out_free[i & 1]);
             }
             bulk_wait_all();
         }
@@ -289,12 +293,13 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         int i = 0, heads = 0;
         bool first = true, ok = true;
         for (; w.more(); w.next(), ++i) {
-            if (first) ++heads;
+            // every head's, whether or not it has a chunk of this group
+            if (first) ok = warp_wait(&bar->s_full, heads++ & 1, err);
             const bool last = first = w.last();
             if ((i & 1) == g) {
                 const int s = i % NS;
                 uint8_t* st = smem + s * SM::kStage;
-                ok = warp_wait(&bar->s_full, (heads - 1) & 1, err) && warp_wait(&bar->full[s], (i / NS) & 1, err);
+                ok = ok && warp_wait(&bar->full[s], (i / NS) & 1, err);
                 // phi of the half row, its part of the normaliser
                 float2 p[kHalf / 2], s2 = both(0.f);
 #pragma unroll
@@ -383,13 +388,14 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 tc_fence_before();
                 warp_arrive(&bar->y_free[g]);
                 // the tile of outputs is free once the chunk before has been stored
-                if (!(ok = pair_all(pair, i == 0 || warp_wait(&bar->out_free, (i - 1) & 1, err)))) break;
+                if (!(ok = pair_all(pair, i == 0 || warp_wait(&bar->out_free[(i - 1) & 1], ((i - 1) >> 1) & 1, err)))) break;
 #pragma unroll
                 for (int c = 0; c < kHalf / 8; ++c)
                     *reinterpret_cast<uint4*>(smem + SM::O0 + blk + swz(r, lc0 + c)) = make_uint4(dq[4 * c], dq[4 * c + 1], dq[4 * c + 2], dq[4 * c + 3]);
                 fence_proxy_async_smem();
                 warp_arrive(&bar->staged);
-                if (last && !(ok = pair_all(pair, warp_wait(&bar->r_done[g], (i >> 1) & 1, err)))) break;
+                // (phases that this group has skipped are complete: this head's S waited for every warp to be through with the last)
+                if (last && !(ok = pair_all(pair, warp_wait(&bar->sums_done, (heads - 1) & 1, err)))) break;
                 if (last) {  // this head's sums
                     tc_fence_after();
                     if (LA_DCHECK((int)blockIdx.x + w.bh < slots)) {
@@ -422,12 +428,12 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 // epilogue runs beside phi(K) R where dk's place is not K's (KB <= VB).  phi(K) enters dv's product rounded once: its
 // errors are independent from column to column of R, whose entries are not.  phi'(k) is formed from k itself.
 // Two groups of eight warps, half a row to a thread.
-constexpr int kKeyThreads = 608;  // warp 0 TMA loads, 1 MMA, 2-17 two compute groups, 18 TMA stores
+constexpr int kKeyThreads = 640;  // warp 0 TMA loads, 1 MMA, 2-17 two compute groups, 18 TMA stores, 19 zeros behind the lengths
 
 template <int KB, int VB>
 struct KeySmem {
     static constexpr int kV = KB * T, kDk = VB * T, kStage = (KB + VB) * T, kR = 2 * (int)image_part(KB, VB);
-    static constexpr int kStages = (229376 - kR) / kStage > 4 ? 4 : (229376 - kR) / kStage;
+    static constexpr int kStages = even_stages((229376 - kR) / kStage, 4);
     static constexpr int R0 = kStages * kStage, r0 = R0 + kR, bars = r0 + 512, total = bars + 512;
     static_assert(kStages >= 2 && total <= 232448, "key pass: shared memory");
 };
@@ -436,7 +442,7 @@ template <int KB, int VB>
 __global__ void __launch_bounds__(kKeyThreads, 1)
 cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
              const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv, const char* __restrict__ image,
-             Rows keys, int* err) {
+             uint4* dk, uint4* dv, Rows keys, int Dk, int Dv, int* err) {
     using SM = KeySmem<KB, VB>;
     constexpr int NS = SM::kStages;
     constexpr uint32_t kSet = 64 * (KB + VB);  // TMEM of a group: dK without r and phi', then dV
@@ -577,13 +583,14 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         int i = 0, heads = 0;
         bool first = true;
         for (; w.more(); w.next(), ++i) {
-            if (first) ++heads;
+            // every head's, whether or not it has a chunk of this group
+            if (first && !warp_wait(&bar->s_full, heads++ & 1, err)) break;
             const bool last = first = w.last();
             if ((i & 1) == g) {
                 const int s = i % NS;
                 const bool live = r < w.rows();
                 uint8_t* st = smem + s * SM::kStage;
-                if (!warp_wait(&bar->s_full, (heads - 1) & 1, err) || !warp_wait(&bar->full[s], (i / NS) & 1, err)) break;
+                if (!warp_wait(&bar->full[s], (i / NS) & 1, err)) break;
                 uint4 k[kHalfK / 8];
 #pragma unroll
                 for (int c = 0; c < kHalfK / 8; ++c) {
@@ -652,6 +659,23 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                 warp_arrive(&bar->s_empty);
             }
         }
+    } else if (warp == 19) {
+        // the chunks behind the lengths (rows behind one inside a chunk are the compute warps'): this block's share of them
+        if (keys.lens) {
+            Span d = span_of(keys, kRowChunk, true, blockIdx.x, gridDim.x);
+            for (; d.left > 0; --d.left) {
+                const int b = d.bh / keys.Hk, row = ((keys.live(b) + kRowChunk - 1) / kRowChunk + d.i) * kRowChunk;
+                const int n = min(kRowChunk, keys.M - row);
+                const size_t at = (size_t)d.bh * keys.M + row;
+                LA_DCHECK(d.bh < keys.heads() && n > 0);
+                for (int x = lane; x < n * Dk / 8; x += 32) dk[at * Dk / 8 + x] = make_uint4(0u, 0u, 0u, 0u);
+                for (int x = lane; x < n * Dv / 8; x += 32) dv[at * Dv / 8 + x] = make_uint4(0u, 0u, 0u, 0u);
+                if (d.left == 1 || ++d.i < keys.chunks(b, kRowChunk, true)) continue;
+                d.i = 0;
+                do ++d.bh;  // ends: another chunk is left
+                while (keys.chunks(d.bh / keys.Hk, kRowChunk, true) == 0);
+            }
+        }
     } else if (lane == 0) {
         // stores: a stage is empty once its outputs have been read
         for (int i = 0; w.more(); w.next(), ++i) {
@@ -701,7 +725,8 @@ cudaError_t tc_bwd(const BwdArgs& a, const la_cross_shape& s, char* ws, cudaStre
         CR_TRY(tc_run("cross_query_tc", query, dim3(l.query_ctas), kQueryThreads, qs, st, tq, td, tdq, (const char*)ws + l.S, rec, rows,
                       s.Dk, l.query_ctas + rows.heads(), err));
         CR_TRY(tc_join(rec, nullptr, nullptr, ws + l.R, nullptr, nullptr, rows, kRowChunk, l.query_ctas, s, st));
-        return tc_run("cross_key_tc", key, dim3(l.key_ctas), kKeyThreads, ks, st, tk, tv, tdk, tdv, (const char*)ws + l.R, keys, err);
+        return tc_run("cross_key_tc", key, dim3(l.key_ctas), kKeyThreads, ks, st, tk, tv, tdk, tdv, (const char*)ws + l.R, (uint4*)a.dk, (uint4*)a.dv,
+                      keys, s.Dk, s.Dv, err);
     };
     cudaError_t e;
     switch (2 * blocks64(s.Dk) + blocks64(s.Dv)) {
@@ -710,8 +735,7 @@ cudaError_t tc_bwd(const BwdArgs& a, const la_cross_shape& s, char* ws, cudaStre
         case 5: e = go(cross_query_tc<2, 1>, QuerySmem<2, 1>::total, cross_key_tc<2, 1>, KeySmem<2, 1>::total); break;
         default: e = go(cross_query_tc<2, 2>, QuerySmem<2, 2>::total, cross_key_tc<2, 2>, KeySmem<2, 2>::total); break;
     }
-    if (e != cudaSuccess || !a.lens) return e;
-    return clear_behind(a.dk, a.dv, keys, s, st);
+    return e;
 }
 
 }  // namespace cross

@@ -239,3 +239,33 @@ def test_underflowing_normaliser(la):
     assert not la.cross_fwd(q, k, v).any()
     for g in la.cross_bwd(q, k, v, torch.ones(1, 1, 3, 16, device=DEV)):
         assert not g.any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lengths", [[0, 0, 900, 0], [1, 0, 0, 64], [900, 1, 1, 1], [0, 65, 0, 0]])
+def test_few_live_chunks(la, dtype, lengths):
+    """Lengths that leave fewer chunks than a padded batch has blocks, in workspaces full of NaN: every sum read was written."""
+    q, k, v, do = R.make(4, 2, 2, 37, 900, 64, 64, dtype, seed=len(lengths), lengths=lengths, behind=0.0)
+    x, g, n = dev(q, k, v), do.to(DEV), torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    nan = lambda op: torch.full((la.cross_workspace_bytes(op, 4, 2, 2, 37, 900, 64, 64, dtype) // 4,), float("nan"), device=DEV)
+    got = la.cross_fwd(*x, lengths=n, return_state=True, workspace=nan(la.OP_CROSS_FWD))
+    check_fwd(got, q, k, v, lengths)
+    check_bwd(la.cross_bwd(*x, g, lengths=n, workspace=nan(la.OP_CROSS_BWD)), q, k, v, do, lengths)
+    check_bwd(la.cross_bwd(*x, g, lengths=n, S=got[1], z=got[2], workspace=nan(la.OP_CROSS_BWD)), q, k, v, do, lengths)
+
+
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 64), (128, 64), (64, 128)])
+def test_heads_of_one_and_two_chunks(la, Dk, Dv):
+    """More heads than blocks, of one, two and three chunks: every chunk meets its own head's state, call after call."""
+    for N, M in ((100, 120), (130, 260), (300, 100)):
+        B, H = 40, 16
+        q, k, v, do = R.make(B, H, H, N, M, Dk, Dv, BF16, seed=N)
+        x, g = dev(q, k, v), do.to(DEV)
+        first = la.cross_fwd(*x, return_state=True) + la.cross_bwd(*x, g)
+        for _ in range(6):
+            again = la.cross_fwd(*x, return_state=True) + la.cross_bwd(*x, g)
+            assert all(torch.equal(a, b) for a, b in zip(again, first))
+        for b in (0, 17, B - 1):
+            one = [t[b:b + 1] for t in (q, k, v)]
+            check_fwd([t[b:b + 1] for t in first[:3]], *one, None)
+            check_bwd([t[b:b + 1] for t in first[3:]], *one, do[b:b + 1], None)

@@ -3,6 +3,7 @@
 // of the chunk's product; operands are fp32 tiles in shared memory read in 16-byte vectors (rows broadcast, columns
 // 4 tx + 64 j conflict-free).  Sums are fp32; records of a head are added up in a fixed order.
 #include "cross.cuh"
+#include "norm_common.cuh"
 #include "shared_memory.cuh"
 
 namespace la {
@@ -57,6 +58,19 @@ __device__ __forceinline__ void load_rows(float* dst, const float* __restrict__ 
     }
 }
 
+// acc[] += x y[]: two columns to an instruction where there are two.
+template <int W>
+__device__ __forceinline__ void axpy(float x, const float (&y)[W], float (&acc)[W]) {
+    if constexpr (W % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < W; j += 2) {
+            const float2 d = norm::fma2(norm::both(x), make_float2(y[j], y[j + 1]), make_float2(acc[j], acc[j + 1]));
+            acc[j] = d.x, acc[j + 1] = d.y;
+        }
+    } else {
+        acc[0] = fmaf(x, y[0], acc[0]);
+    }
+}
 // acc[DA/16][DB/16] += A^T B over the 64 rows of two tiles: rows of acc follow col_of over ty.
 template <int DA, int DB>
 __device__ __forceinline__ void outer_sum(const float* a, const float* b, float (&acc)[DA / 16][DB / 16], int ty, int tx) {
@@ -66,9 +80,7 @@ __device__ __forceinline__ void outer_sum(const float* a, const float* b, float 
         load_cols<DA / 16>(a + p * DA, ty, x);
         load_cols<DB / 16>(b + p * DB, tx, y);
 #pragma unroll
-        for (int i = 0; i < DA / 16; ++i)
-#pragma unroll
-            for (int j = 0; j < DB / 16; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+        for (int i = 0; i < DA / 16; ++i) axpy(x[i], y, acc[i]);
     }
 }
 // out[4][DB/16] = rows 4 ty .. 4 ty + 3 of A [64][DA] times B [DA][DB].
@@ -88,11 +100,7 @@ __device__ __forceinline__ void rows_times(const float* a, const float* b, float
             float y[DB / 16];
             load_cols<DB / 16>(b + (d + e) * DB, tx, y);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float xi = e == 0 ? x[i].x : e == 1 ? x[i].y : e == 2 ? x[i].z : x[i].w;
-#pragma unroll
-                for (int j = 0; j < DB / 16; ++j) out[i][j] = fmaf(xi, y[j], out[i][j]);
-            }
+            for (int i = 0; i < 4; ++i) axpy(e == 0 ? x[i].x : e == 1 ? x[i].y : e == 2 ? x[i].z : x[i].w, y, out[i]);
         }
     }
 }

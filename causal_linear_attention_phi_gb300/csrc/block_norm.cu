@@ -152,7 +152,7 @@ gated_bwd_kernel(const T* o, const T* gate, const T* __restrict__ w, const T* dy
                  float* __restrict__ part, GatedRows g, int rms, float eps) {
     using V = Vec<T>;
     constexpr int kRows = kBlock / L, D = L * V::n, kP = V::n / 2, kU = bwd_u<T>();
-    __shared__ float sums[kRows][D];
+    __shared__ __align__(16) float sums[kRows][D];
     pdl_enter();  // launched with programmatic dependent launch
     const int lane = threadIdx.x % L, sub = threadIdx.x / L;
     float2 wv[kP], dw[kP];

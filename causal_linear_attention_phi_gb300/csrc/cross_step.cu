@@ -28,7 +28,7 @@ cross_few_kernel(const T* __restrict__ q, const float* __restrict__ S, const flo
                  int R, int pitch) {
     using F = Few<DK, DV>;
     __shared__ float ph[kRows][DK];
-    __shared__ float part[F::kWarps][kRows][DV];
+    __shared__ __align__(16) float part[F::kWarps][kRows][DV];
     __shared__ float inv[kRows], zs[DK];
     pdl_enter();  // launched with programmatic dependent launch
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

@@ -339,26 +339,32 @@ cross_join_tc(const float* __restrict__ rec, const float* __restrict__ S, const 
 
 // ------------------------------------------------------------------ the queries' answers
 // A stage holds a chunk of 128 queries: phi(Q) in place for the product, then the outputs for their store.  A thread owns
-// a row.  S (its hi part) and z of the next head are copied while this head's chunks are worked on.
+// a row.  S (its hi part) and z of the next head are copied while this head's chunks are worked on.  One part of phi(q) and of S
+// is enough for an S that was summed from keys: its rows are alike, so that their roundings and phi's average out over the
+// columns of a head (o is as far off as its own rounding).  A caller's state may be any: kExact forms
+// phi_hi S_hi + phi_hi S_lo + phi_lo S_hi (independent entries: 1.8 times as far off without).
 constexpr int kApplyThreads = 352;  // warp 0 TMA loads, 1 MMA, 2-9 two compute groups, 10 TMA stores
 
-template <int KB, int VB>
+template <int KB, int VB, bool kExact>
 struct ApplySmem {
     static constexpr int kTile = 16384;  // 128 rows of a block
-    static constexpr int kS = (int)image_part(KB, VB), kStage = (KB > VB ? KB : VB) * kTile;
-    static constexpr int kStages = even_stages((229376 - 2 * kS) / kStage, 6);
-    static constexpr int S0 = kStages * kStage;     // two
-    static constexpr int z0 = S0 + 2 * kS;          // float[2][64 KB]
-    static constexpr int bars = z0 + 2 * 256 * KB;
+    static constexpr int kBufs = kExact ? 1 : 2;  // of S
+    static constexpr int kS = (kExact ? 2 : 1) * (int)image_part(KB, VB);
+    static constexpr int kLo = (KB > VB ? KB : VB) * kTile, kStage = kLo + (kExact ? KB * kTile : 0);
+    static constexpr int kStages = even_stages((229376 - kBufs * kS) / kStage, 6);
+    static constexpr int S0 = kStages * kStage;
+    static constexpr int z0 = S0 + kBufs * kS;      // float[kBufs][64 KB]
+    static constexpr int bars = z0 + kBufs * 256 * KB;
     static constexpr int total = bars + 512;
+    static_assert(kStages >= 2 && total <= 232448, "apply: shared memory");
 };
 
-template <int KB, int VB>
+template <int KB, int VB, bool kExact>
 __global__ void __launch_bounds__(kApplyThreads, 1)
 cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_o, const char* __restrict__ image,
                Rows rows, int* err) {
-    using SM = ApplySmem<KB, VB>;
-    constexpr int NS = SM::kStages, T = SM::kTile;
+    using SM = ApplySmem<KB, VB, kExact>;
+    constexpr int NS = SM::kStages, T = SM::kTile, NB = SM::kBufs;
     extern __shared__ __align__(1024) uint8_t smem[];
     struct Bars {
         uint64_t full[6], empty[6], staged[6], s_full[2], s_empty[2], ready[2], done[2], final_mma;
@@ -408,8 +414,8 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             bool first = true;
             for (; w.more(); w.next(), ++i) {
                 if (first) {
-                    const int h = heads & 1;
-                    if (!mbar_wait(&bar->s_empty[h], ((heads >> 1) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
+                    const int h = heads % NB;
+                    if (!mbar_wait(&bar->s_empty[h], ((heads / NB) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
                     const char* im = image + (size_t)w.bh * image_bytes(KB, VB);
                     mbar_arrive_expect_tx(&bar->s_full[h], SM::kS + 256 * KB);
                     bulk_load(smem + SM::S0 + h * SM::kS, im, SM::kS, &bar->s_full[h]);
@@ -424,7 +430,7 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 for (int b = 0; b < KB; ++b) tma_load_3d(smem + s * SM::kStage + b * T, &tm_q, 64 * b, w.row0(), w.bh, &bar->full[s]);
             }
             mbar_drain(bar->full, NS, i, err, LA_ERR_TIMEOUT);  // no copy is left in flight
-            mbar_drain(bar->s_full, 2, heads, err, LA_ERR_TIMEOUT);
+            mbar_drain(bar->s_full, NB, heads, err, LA_ERR_TIMEOUT);
         }
     } else if (warp == 1) {
         constexpr uint32_t id = idesc_bf16_f32(128, 64 * VB, 0, 1);
@@ -435,8 +441,8 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         for (int i = 0; i < n; ++i, w.next()) {
             const int g = i & 1, s = i % NS;
             if (first) ++heads;
-            const int h = (heads - 1) & 1;
-            if (first && !warp_wait(&bar->s_full[h], ((heads - 1) >> 1) & 1, err)) break;
+            const int h = (heads - 1) % NB;
+            if (first && !warp_wait(&bar->s_full[h], ((heads - 1) / NB) & 1, err)) break;
             // phi(Q) is in place, and the group has read the outputs of its previous chunk
             if (!warp_wait(&bar->ready[g], (i >> 1) & 1, err)) break;
             tc_fence_after();
@@ -444,8 +450,13 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (elect_one()) {
                 const uint32_t aQ = smem_u32(smem + s * SM::kStage), aS = smem_u32(smem + SM::S0 + h * SM::kS);
 #pragma unroll
-                for (int kk = 0; kk < 4 * KB; ++kk)
+                for (int kk = 0; kk < 4 * KB; ++kk) {
                     mma_ss(t0 + 64 * VB * g, desc_k(aQ, kk, T), desc_mn(aS, kk, 8192 * KB), id, kk > 0);
+                    if (kExact) {
+                        mma_ss(t0 + 64 * VB * g, desc_k(aQ, kk, T), desc_mn(aS + (uint32_t)image_part(KB, VB), kk, 8192 * KB), id, 1);
+                        mma_ss(t0 + 64 * VB * g, desc_k(aQ + SM::kLo, kk, T), desc_mn(aS, kk, 8192 * KB), id, 1);
+                    }
+                }
                 mma_commit(&bar->done[g]);
                 if (first) mma_commit(&bar->s_empty[h]);
             }
@@ -462,9 +473,9 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         int i = 0, heads = 0;
         bool first = true;
         for (; w.more(); w.next(), ++i) {
-            const int h = (first ? heads : heads - 1) & 1;
+            const int h = (first ? heads : heads - 1) % NB;
             // every head's, whether or not it has a chunk of this group: a wait that skips a phase can be let through by the one before
-            if (first && !warp_wait(&bar->s_full[h], (heads++ >> 1) & 1, err)) break;
+            if (first && !warp_wait(&bar->s_full[h], (heads++ / NB) & 1, err)) break;
             first = w.last();
             if ((i & 1) != g) continue;
             const int s = i % NS;
@@ -478,16 +489,23 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 for (int lc = 0; lc < 8; ++lc) {
                     uint4* p = reinterpret_cast<uint4*>(st + b * T + swz(r, lc));
                     uint4 x = *p;
-                    uint32_t* u = reinterpret_cast<uint32_t*>(&x);
+                    uint32_t *u = reinterpret_cast<uint32_t*>(&x), l[4];
                     float2 zv[4];
                     norm::Pairs<float>::get(zs + 64 * b + 8 * lc, reinterpret_cast<float2(&)[2]>(zv[0]));
                     norm::Pairs<float>::get(zs + 64 * b + 8 * lc + 4, reinterpret_cast<float2(&)[2]>(zv[2]));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        u[e] = pack2(phi2(unpack2(u[e])));
-                        den = norm::fma2(unpack2(u[e]), zv[e], den);  // of the rounded phi, as the product has it
+                        const float2 f = phi2(unpack2(u[e]));
+                        if (kExact) {
+                            split2(f, u[e], l[e]);
+                            den = norm::fma2(f, zv[e], den);
+                        } else {
+                            u[e] = pack2(f);
+                            den = norm::fma2(unpack2(u[e]), zv[e], den);  // of the rounded phi, as the product has it
+                        }
                     }
                     *p = x;
+                    if (kExact) *reinterpret_cast<uint4*>(st + SM::kLo + b * T + swz(r, lc)) = make_uint4(l[0], l[1], l[2], l[3]);
                 }
             }
             const float2 inv = norm::both(over(den.x + den.y));
@@ -542,7 +560,7 @@ int ctas_for(long long heads, long long rows, int chunk) {  // a block to an SM,
     return (int)(chunks < kSms ? chunks : kSms);
 }
 
-cudaError_t answers(const void* q, void* o, const char* image, const la_cross_shape& s, cudaStream_t st) {
+cudaError_t answers(const void* q, void* o, const char* image, bool exact, const la_cross_shape& s, cudaStream_t st) {
     const Rows rows = grouped_queries(s);
     CUtensorMap tq, to;
     if (!make_tmap_bf16_rows(&tq, q, rows.heads(), rows.M, s.Dk, kRowChunk) ||
@@ -552,12 +570,15 @@ cudaError_t answers(const void* q, void* o, const char* image, const la_cross_sh
     auto go = [&](auto kern, size_t smem) {
         return tc_run("cross_apply_tc", kern, dim3(ctas), kApplyThreads, smem, st, tq, to, image, rows, device_error_word());
     };
+#define LA_GO(KB, VB) \
+    exact ? go(cross_apply_tc<KB, VB, true>, ApplySmem<KB, VB, true>::total) : go(cross_apply_tc<KB, VB, false>, ApplySmem<KB, VB, false>::total)
     switch (2 * blocks64(s.Dk) + blocks64(s.Dv)) {
-        case 3: return go(cross_apply_tc<1, 1>, ApplySmem<1, 1>::total);
-        case 4: return go(cross_apply_tc<1, 2>, ApplySmem<1, 2>::total);
-        case 5: return go(cross_apply_tc<2, 1>, ApplySmem<2, 1>::total);
-        default: return go(cross_apply_tc<2, 2>, ApplySmem<2, 2>::total);
+        case 3: return LA_GO(1, 1);
+        case 4: return LA_GO(1, 2);
+        case 5: return LA_GO(2, 1);
+        default: return LA_GO(2, 2);
     }
+#undef LA_GO
 }
 
 }  // namespace
@@ -631,12 +652,12 @@ cudaError_t tc_fwd(const FwdArgs& a, const la_cross_shape& s, char* ws, cudaStre
     float* rec = reinterpret_cast<float*>(ws);
     CR_TRY(tc_sums(a.k, a.v, keys, rec, l.sum_ctas, s, st));
     CR_TRY(tc_join(rec, nullptr, nullptr, ws + l.S, a.S, a.z, keys, kSumRows, l.sum_ctas, s, st));
-    return s.N == 0 ? cudaSuccess : answers(a.q, a.o, ws + l.S, s, st);
+    return s.N == 0 ? cudaSuccess : answers(a.q, a.o, ws + l.S, false, s, st);
 }
 
 cudaError_t tc_apply(const void* q, const float* S, const float* z, void* o, const la_cross_shape& s, char* ws, cudaStream_t st) {
     CR_TRY(tc_join(nullptr, S, z, ws, nullptr, nullptr, grouped_queries(s), kRowChunk, 1, s, st));
-    return answers(q, o, ws, s, st);
+    return answers(q, o, ws, true, s, st);
 }
 
 }  // namespace cross

@@ -374,7 +374,8 @@ la_status la_cross_bwd(const void* q, const void* k, const void* v, const int* l
 
 /*
  * Queries to a kept state (S, z), which is read, not changed: decoding, one token at a time (N = 1) or several.
- * q: [B,H,N,Dk]; o: [B,H,N,Dv]; S: [B,Hk,Dk,Dv], z: [B,Hk,Dk] fp32.  s.M is ignored.
+ * q: [B,H,N,Dk]; o: [B,H,N,Dv]; S: [B,Hk,Dk,Dv], z: [B,Hk,Dk] fp32.  s.M is ignored.  S may hold any values: a bf16 call
+ * multiplies in fp32, or with phi(q) and S in two bf16 parts each.
  * Workspace: la_cross_workspace_bytes(LA_OP_CROSS_APPLY, s), which is 0 for a few queries.
  */
 la_status la_cross_apply(const void* q, const float* S, const float* z, void* o, la_cross_shape s, void* ws,

@@ -33,6 +33,9 @@ __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.al
 template <int n>
 __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n)); }
 
+// Wait until all but this thread's last committed store have finished reading shared memory.
+__device__ __forceinline__ void bulk_wait_read_all_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+
 // A float of each lane to a column of tensor memory, for another warp of the same lanes to read after a barrier.
 __device__ __forceinline__ void tmem_put(uint32_t taddr, float x) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(x)) : "memory");
@@ -424,17 +427,19 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 }
 
 // ------------------------------------------------------------------ key pass
-// A stage holds K (phi's bf16 copy in place) and V; then dv and, VB blocks on, dk.  V R^T starts as V lands, and its
-// epilogue runs beside phi(K) R where dk's place is not K's (KB <= VB).  phi(K) enters dv's product rounded once: its
-// errors are independent from column to column of R, whose entries are not.  phi'(k) is formed from k itself.
+// K and V have rings of their own, as they are free at different times: K (phi's bf16 copy in place) once its product is
+// through, V, whose product starts as it lands, once dk (KB > VB: dv) has been stored from its place; the other output has a
+// tile of its own.  With both outputs stored from one stage's tiles a stage waited 2,400 cycles for its stores and then
+// 6,500 for its loads, of 14,000 in all (190 us of B=2 H=16 N=32768 128 x 128; now 183).  phi(K) enters dv's product
+// rounded once: its errors are independent from column to column of R, whose entries are not.  phi'(k) is formed from k itself.
 // Two groups of eight warps, half a row to a thread.
 constexpr int kKeyThreads = 640;  // warp 0 TMA loads, 1 MMA, 2-17 two compute groups, 18 TMA stores, 19 zeros behind the lengths
 
 template <int KB, int VB>
 struct KeySmem {
-    static constexpr int kV = KB * T, kDk = VB * T, kStage = (KB + VB) * T, kR = 2 * (int)image_part(KB, VB);
-    static constexpr int kStages = even_stages((229376 - kR) / kStage, 4);
-    static constexpr int R0 = kStages * kStage, r0 = R0 + kR, bars = r0 + 512, total = bars + 512;
+    static constexpr int kK = KB * T, kV = VB * T, kOut = KB <= VB ? kV : kK, kR = 2 * (int)image_part(KB, VB);
+    static constexpr int kStages = even_stages((229376 - kR - kOut) / (kK + kV), 4);
+    static constexpr int V0 = kStages * kK, O0 = V0 + kStages * kV, R0 = O0 + kOut, r0 = R0 + kR, bars = r0 + 512, total = bars + 512;
     static_assert(kStages >= 2 && total <= 232448, "key pass: shared memory");
 };
 
@@ -449,7 +454,8 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     constexpr uint32_t kCols = 2 * kSet <= 256 ? 256 : 512;
     extern __shared__ __align__(1024) uint8_t smem[];
     struct Bars {
-        uint64_t full[4], empty[4], staged[4], s_full, s_empty, ready[2], k_done[2], v_done[2], acc_free[2], final_mma;
+        uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], dk_staged[2], dv_staged[2], out_free[2], s_full, s_empty, ready[2], k_done[2], v_done[2],
+            acc_free[2], final_mma;
         uint32_t tmem;
         Span span;
     };
@@ -460,15 +466,19 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     LA_DCHECK((smem_u32(smem) & 1023) == 0);
     if (tid == 32) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&bar->full[s], 1);
-            mbar_init(&bar->empty[s], 1);
-            mbar_init(&bar->staged[s], 8);
+            mbar_init(&bar->k_full[s], 1);
+            mbar_init(&bar->k_empty[s], 1);
+            mbar_init(&bar->v_full[s], 1);
+            mbar_init(&bar->v_empty[s], 1);
         }
         for (int g = 0; g < 2; ++g) {
+            mbar_init(&bar->dk_staged[g], 8);
+            mbar_init(&bar->dv_staged[g], 8);
             mbar_init(&bar->ready[g], 8);
             mbar_init(&bar->k_done[g], 1);
             mbar_init(&bar->v_done[g], 1);
             mbar_init(&bar->acc_free[g], 8);
+            mbar_init(&bar->out_free[g], 1);
         }
         mbar_init(&bar->s_full, 1);
         mbar_init(&bar->s_empty, 17);  // the products and the compute warps (r)
@@ -501,12 +511,17 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             bool first = true;
             for (; w.more(); w.next(), ++i) {
                 const int s = i % NS;
-                if (!mbar_wait(&bar->empty[s], ((i / NS) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
-                uint8_t* st = smem + s * SM::kStage;
-                mbar_arrive_expect_tx(&bar->full[s], (KB + VB) * T);
                 check_copy(0, w.row0(), keys.M, w.bh, keys.heads());
-                for (int b = 0; b < KB; ++b) tma_load_3d(st + b * T, &tm_k, 64 * b, w.row0(), w.bh, &bar->full[s]);
-                for (int b = 0; b < VB; ++b) tma_load_3d(st + SM::kV + b * T, &tm_v, 64 * b, w.row0(), w.bh, &bar->full[s]);
+                if (!mbar_wait(&bar->v_empty[s], ((i / NS) & 1) ^ 1, err, LA_ERR_TIMEOUT)) break;
+                mbar_arrive_expect_tx(&bar->v_full[s], VB * T);
+                for (int b = 0; b < VB; ++b)
+                    tma_load_3d(smem + SM::V0 + s * SM::kV + b * T, &tm_v, 64 * b, w.row0(), w.bh, &bar->v_full[s]);
+                if (!mbar_wait(&bar->k_empty[s], ((i / NS) & 1) ^ 1, err, LA_ERR_TIMEOUT)) {
+                    mbar_drain(bar->v_full, NS, i + 1, err, LA_ERR_TIMEOUT);
+                    break;
+                }
+                mbar_arrive_expect_tx(&bar->k_full[s], KB * T);
+                for (int b = 0; b < KB; ++b) tma_load_3d(smem + s * SM::kK + b * T, &tm_k, 64 * b, w.row0(), w.bh, &bar->k_full[s]);
                 if (first) {  // after the chunk's own tiles: those need no wait for the head before
                     if (!mbar_wait(&bar->s_empty, (heads & 1) ^ 1, err, LA_ERR_TIMEOUT)) {
                         ++i;
@@ -520,7 +535,8 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                 }
                 first = w.last();
             }
-            mbar_drain(bar->full, NS, i, err, LA_ERR_TIMEOUT);  // no copy is left in flight
+            mbar_drain(bar->v_full, NS, i, err, LA_ERR_TIMEOUT);  // no copy is left in flight
+            mbar_drain(bar->k_full, NS, i, err, LA_ERR_TIMEOUT);
             mbar_drain(&bar->s_full, 1, heads, err, LA_ERR_TIMEOUT);
         }
     } else if (warp == 1) {
@@ -533,11 +549,11 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         auto issue_k = [&]() {  // dK without r and phi' of chunk vi
             const int g = vi & 1, s = vi % NS;
             if (v_first) ok = ok && warp_wait(&bar->s_full, heads++ & 1, err);
-            ok = ok && warp_wait(&bar->full[s], (vi / NS) & 1, err) && warp_wait(&bar->acc_free[g], ((vi >> 1) & 1) ^ 1, err);
+            ok = ok && warp_wait(&bar->v_full[s], (vi / NS) & 1, err) && warp_wait(&bar->acc_free[g], ((vi >> 1) & 1) ^ 1, err);
             if (!ok) return;
             tc_fence_after();
             if (elect_one()) {
-                const uint32_t aV = smem_u32(smem + s * SM::kStage + SM::kV), acc = t0 + kSet * g;
+                const uint32_t aV = smem_u32(smem + SM::V0 + s * SM::kV), acc = t0 + kSet * g;
 #pragma unroll
                 for (int kk = 0; kk < 4 * VB; ++kk) {
                     mma_ss(acc, desc_k(aV, kk, T), desc_k(aR, kk, 8192 * KB), id_k, kk > 0);
@@ -557,13 +573,14 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             tc_fence_after();
             const bool last = uniform(w.last());
             if (elect_one()) {
-                const uint32_t aK = smem_u32(smem + s * SM::kStage), acc = t0 + kSet * g + 64 * KB;
+                const uint32_t aK = smem_u32(smem + s * SM::kK), acc = t0 + kSet * g + 64 * KB;
 #pragma unroll
                 for (int kk = 0; kk < 4 * KB; ++kk) {
                     mma_ss(acc, desc_k(aK, kk, T), desc_mn(aR, kk, 8192 * KB), id_v, kk > 0);
                     mma_ss(acc, desc_k(aK, kk, T), desc_mn(aRl, kk, 8192 * KB), id_v, 1);
                 }
                 mma_commit(&bar->v_done[g]);
+                mma_commit(&bar->k_empty[s]);
                 if (last) mma_commit(&bar->s_empty);
             }
             __syncwarp();
@@ -589,8 +606,9 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             if ((i & 1) == g) {
                 const int s = i % NS;
                 const bool live = r < w.rows();
-                uint8_t* st = smem + s * SM::kStage;
-                if (!warp_wait(&bar->full[s], (i / NS) & 1, err)) break;
+                uint8_t *st = smem + s * SM::kK, *own = smem + SM::V0 + s * SM::kV, *out = smem + SM::O0;
+                uint8_t *to_k = KB <= VB ? own : out, *to_v = KB <= VB ? out : own;
+                if (!warp_wait(&bar->k_full[s], (i / NS) & 1, err)) break;
                 uint4 k[kHalfK / 8];
 #pragma unroll
                 for (int c = 0; c < kHalfK / 8; ++c) {
@@ -603,8 +621,9 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                 }
                 fence_proxy_async_smem();
                 warp_arrive(&bar->ready[g]);
-                if (KB > VB && !warp_wait(&bar->v_done[g], (i >> 1) & 1, err)) break;  // dk lies over phi(K)
                 if (!warp_wait(&bar->k_done[g], (i >> 1) & 1, err)) break;
+                // the tile of outputs is free once the chunk before has been stored from it
+                if (KB > VB && i > 0 && !warp_wait(&bar->out_free[(i - 1) & 1], ((i - 1) >> 1) & 1, err)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int b = 0; b < kHalfK / 32; ++b) {
@@ -629,10 +648,13 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                             o[e] = pack2(d);
                         }
                         if (!live) x = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4*>(st + SM::kDk + ((ck + 32 * b) >> 6) * T + swz(r, (((ck + 32 * b) >> 3) & 7) + c)) = x;
+                        *reinterpret_cast<uint4*>(to_k + ((ck + 32 * b) >> 6) * T + swz(r, (((ck + 32 * b) >> 3) & 7) + c)) = x;
                     }
                 }
-                if (KB <= VB && !warp_wait(&bar->v_done[g], (i >> 1) & 1, err)) break;
+                fence_proxy_async_smem();
+                warp_arrive(&bar->dk_staged[g]);
+                if (!warp_wait(&bar->v_done[g], (i >> 1) & 1, err)) break;
+                if (KB <= VB && i > 0 && !warp_wait(&bar->out_free[(i - 1) & 1], ((i - 1) >> 1) & 1, err)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int b = 0; b < kHalfV / 32; ++b) {
@@ -647,13 +669,13 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                         for (int e = 0; e < 4; ++e)
                             o[e] = pack_bf16x2(__uint_as_float(y[8 * c + 2 * e]), __uint_as_float(y[8 * c + 2 * e + 1]));
                         if (!live) x = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4*>(st + ((cv + 32 * b) >> 6) * T + swz(r, (((cv + 32 * b) >> 3) & 7) + c)) = x;
+                        *reinterpret_cast<uint4*>(to_v + ((cv + 32 * b) >> 6) * T + swz(r, (((cv + 32 * b) >> 3) & 7) + c)) = x;
                     }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 warp_arrive(&bar->acc_free[g]);
-                warp_arrive(&bar->staged[s]);
+                warp_arrive(&bar->dv_staged[g]);
             }
             if (last) {  // r is no longer read
                 warp_arrive(&bar->s_empty);
@@ -677,17 +699,21 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             }
         }
     } else if (lane == 0) {
-        // stores: a stage is empty once its outputs have been read
-        for (int i = 0; w.more(); w.next(), ++i) {
+        for (int i = 0; w.more(); w.next(), ++i) {  // stores: a tile is free once its output has been read
             const int s = i % NS;
-            if (!mbar_wait(&bar->staged[s], (i / NS) & 1, err, LA_ERR_TIMEOUT)) break;
-            const uint8_t* st = smem + s * SM::kStage;
+            const uint8_t *own = smem + SM::V0 + s * SM::kV, *out = smem + SM::O0;
+            const uint8_t *of_k = KB <= VB ? own : out, *of_v = KB <= VB ? out : own;
             check_copy(0, w.row0(), keys.M, w.bh, keys.heads());
-            for (int b = 0; b < KB; ++b) tma_store_3d(&tm_dk, st + SM::kDk + b * T, 64 * b, w.row0(), w.bh);
-            for (int b = 0; b < VB; ++b) tma_store_3d(&tm_dv, st + b * T, 64 * b, w.row0(), w.bh);
+            if (!mbar_wait(&bar->dk_staged[i & 1], (i >> 1) & 1, err, LA_ERR_TIMEOUT)) break;
+            for (int b = 0; b < KB; ++b) tma_store_3d(&tm_dk, of_k + b * T, 64 * b, w.row0(), w.bh);
             bulk_commit();
+            if (!mbar_wait(&bar->dv_staged[i & 1], (i >> 1) & 1, err, LA_ERR_TIMEOUT)) break;
+            for (int b = 0; b < VB; ++b) tma_store_3d(&tm_dv, of_v + b * T, 64 * b, w.row0(), w.bh);
+            bulk_commit();
+            bulk_wait_read_all_but_one();
+            mbar_arrive(KB <= VB ? &bar->v_empty[s] : &bar->out_free[i & 1]);
             bulk_wait_read_all();
-            mbar_arrive(&bar->empty[s]);
+            mbar_arrive(KB <= VB ? &bar->out_free[i & 1] : &bar->v_empty[s]);
         }
         bulk_wait_all();
     }

@@ -6,9 +6,11 @@
 //
 // All three are bound by memory: a chunk of 128 rows of 128-wide q and o (or k and v) is 64 KB, 1.45 us of an SM's share of
 // the copy rate, against 0.35 us for its product.  What it takes to come near is loads in flight while the arithmetic of
-// earlier chunks goes on, so tiles come through rings of TMA stages, and two groups of four warps work on alternate
-// chunks, one waiting for its product while the other evaluates phi.  phi(k) enters the sums as two bf16 parts, so that S is
-// good to 2^-17 of its terms: dq in the gradient is a small difference of products with S.
+// earlier chunks goes on, so tiles come through rings of TMA stages, and two groups of warps (eight each in the sums, four in
+// the answers) work on alternate chunks, one waiting for its product while the other evaluates phi.  phi(k) enters the sums
+// as two bf16 parts, so that S is good to 2^-17 of its terms: dq in the gradient is a small difference of products with S.
+// Measured, of the 6.79 TB/s a copy reaches: sums over 8 heads of 131,071 keys 112 us (0.71), answers to 2,097,152 queries
+// of 16 heads 165 us (0.96), both 128 x 128.
 #include <cudaTypedefs.h>
 
 #include "tc_cross.cuh"
@@ -19,8 +21,8 @@ namespace {
 
 // ------------------------------------------------------------------ sums over the keys
 // A stage holds a chunk of 64 rows: K (phi's hi part in place) and V.  phi's lo part: for KB = 1 in the stage, hi and lo being the
-// two 64-row halves of one 128-row product; for KB = 2 in a ring of its own, held only while the products run.  An accumulator in tensor memory takes kPeriod chunks only:
-// the products add with truncation, half a unit in the last place each and always the same way (131,072 keys summed in one
+// two 64-row halves of one 128-row product; for KB = 2 in a ring of its own, held only while the products run.  An accumulator
+// in tensor memory takes kPeriod chunks only: the products add with truncation, half a unit in the last place each and always the same way (131,072 keys summed in one
 // accumulator to a block were 2e-5 off).  The compute warps then add it to sums of their own, in registers and rounded
 // to nearest, while the other accumulator takes the next period: a warp has 32 rows and a quarter of the columns.
 constexpr int kSumThreads = 576;  // warp 0 TMA, 1 MMA, 2-17 two compute groups of eight

@@ -6,10 +6,11 @@
 //
 // t needs no product of its own: dO . (phi(q) S) is phi(q) . (S dO), the row sum that the epilogue of Y forms.  dO and V enter
 // their products as they land, without a pass over them.  dq is a small difference of large terms (the keys' weights vary
-// little), so S enters as two bf16 parts and everything else of dq is fp32; dk keeps a rounding of X's and of R's whole size: R is two parts,
-// X one (see below).  Bound by memory: a chunk of 128 rows, 128 wide, is 96 KB (query) or 128 KB (key), 2.2 and 2.9 us
-// of an SM's share of the copy rate, against 1.4 us for its products.  Two groups of eight warps take alternate
-// chunks, half a row to a thread; outputs go back into the stage's tiles for their store.
+// little), so S enters as two bf16 parts and everything else of dq is fp32; dk keeps a rounding of X's and of R's whole size:
+// R is two parts, X one (see below).  Bound by memory, then by what passes through shared memory: a chunk of 128 rows, 128
+// wide, is 96 KB (query) or 128 KB (key), 2.2 and 2.9 us of an SM's share of the copy rate, and its products, copies and
+// epilogues move four times that between shared memory and the rest.  Two groups of eight warps take alternate chunks, half
+// a row to a thread.  Measured at B=2 H=16 N=M=32768 128 x 128: query pass 160 us (0.74 of the copy rate), key pass 183 (0.86).
 #include <cudaTypedefs.h>
 
 #include "tc_cross.cuh"
@@ -74,9 +75,9 @@ __device__ __forceinline__ bool pair_all(int id, bool v) {
 // behind it (the other block's rows, or z and the barriers) and make columns of the result that nothing reads.
 //
 // Two groups of eight warps; a thread holds half a row's phi in fp32 throughout, and the two threads of a row join their parts of
-// den and of t through tensor memory, shared memory being full (a whole row to a thread took 343 us where this took 264: twice the code, of which the
-// instruction cache held half, and two warps to a scheduler).  Registers come from the other warpgroup: 640 threads of 96
-// are 128 of 56 and 512 of 104.  A chunk's phases, each overlapping the other group's:
+// den and of t through tensor memory, shared memory being full (a whole row to a thread took 343 us where this took 264:
+// twice the code, of which the instruction cache held half, and two warps to a scheduler).  Registers come from the other
+// warpgroup: 640 threads of 96 are 128 of 56 and 512 of 104.  A chunk's phases, each overlapping the other group's:
 //   phi, den, X -> X^T dO may start;   Y -> t -> X^T t may start;   Y -> dq.
 constexpr int kQueryThreads = 640;  // warp 0 TMA loads, 1 MMA of Y and R, 2 TMA stores, 3 MMA of r, 4-19 two compute groups
 

@@ -236,6 +236,13 @@ def _new_f32(shape, device, stream):
     return _handed_out(lambda: torch.empty(shape, dtype=torch.float32, device=device), stream)
 
 
+def _new(shape, like, stream):
+    """A tensor of another shape, of the type and on the device of `like`."""
+    if stream is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    return _handed_out(lambda: torch.empty(shape, dtype=like.dtype, device=like.device), stream)
+
+
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None and t.numel() > 0 else ctypes.c_void_p(0)
 
@@ -610,7 +617,7 @@ def cross_fwd(q, k, v, lengths=None, out=None, workspace=None, stream=None, retu
     """
     s = _cross_args(q, k, v, lengths)
     if out is None:
-        out = _handed_out(lambda: q.new_empty((*q.shape[:3], s.Dv)), stream)
+        out = _new((*q.shape[:3], s.Dv), q, stream)
     else:
         _need_cuda(out)
         if out.shape != (*q.shape[:3], s.Dv) or out.dtype != q.dtype:
@@ -657,7 +664,7 @@ def cross_apply(q, S, z, out=None, workspace=None, stream=None):
     s = CrossShape(qs[0], qs[1], ss[1], qs[2] if len(qs) == 4 else 1, 0, ss[2], ss[3], code)
     want = (*qs[:-1], ss[3])
     if out is None:
-        out = _handed_out(lambda: q.new_empty(want), stream)
+        out = _new(want, q, stream)
     else:
         _need_cuda(out)
         if out.shape != want or out.dtype != q.dtype:

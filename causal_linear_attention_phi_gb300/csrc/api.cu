@@ -258,7 +258,16 @@ la_status check_device() {
         g_cc_ok[dev] = ok;
         if (ok < 0) return fail(LA_ERR_UNSUPPORTED, "device %d is sm_%d%d; the library is compiled for sm_103a", dev, major, minor);
     }
-    return ok > 0 ? LA_OK : fail(LA_ERR_UNSUPPORTED, "device is not sm_103");
+    if (ok < 0) return fail(LA_ERR_UNSUPPORTED, "device is not sm_103");
+    // A host thread that has not used the device yet has no context, and tensor maps are encoded by a driver call, which
+    // fails without one.  This runtime call, legal in a capture too, gives the thread the context that its launches would.
+    thread_local int ready = -1;
+    if (ready != dev) {
+        void* p = nullptr;
+        if (cudaGetSymbolAddress(&p, g_error_word) != cudaSuccess) return fail(LA_ERR_CUDA, "cannot use device %d", dev);
+        ready = dev;
+    }
+    return LA_OK;
 }
 
 // A tensor argument must be a 16-byte aligned (`align`) pointer to device (or

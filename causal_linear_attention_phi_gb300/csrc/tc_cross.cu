@@ -27,6 +27,7 @@ namespace {
 // to nearest, while the other accumulator takes the next period: a warp has 32 rows and a quarter of the columns.
 constexpr int kSumThreads = 576;  // warp 0 TMA, 1 MMA, 2-17 two compute groups of eight
 constexpr int kPeriod = 4;
+constexpr uint32_t kNone = 0xff80ff80u;  // -inf, -inf
 
 template <int KB, int VB>
 struct SumSmem {
@@ -177,24 +178,29 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 if (KB == 2 && !(ok = warp_wait(&bar->lo_free[i % kLos], ((i / kLos) & 1) ^ 1, err))) break;
                 uint8_t* st = smem + s * SM::kStage + at;
                 uint8_t* lo = KB == 2 ? smem + SM::lo0 + i % kLos * 2 * T + at : st + T;
-                const bool whole = n == kSumRows && (Dk & 63) == 0;
                 uint4 x[KB][2];
 #pragma unroll
                 for (int b = 0; b < KB; ++b)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) x[b][j] = *reinterpret_cast<const uint4*>(st + b * T + 4096 * j);
+                if (n < kSumRows || (Dk & 63) != 0) {  // phi(-inf) is 0; masked here, the loop below has no branch
+#pragma unroll
+                    for (int b = 0; b < KB; ++b)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if (64 * b + 8 * lc >= Dk || (ct >> 3) + 32 * j >= n)
+                                x[b][j] = make_uint4(kNone, kNone, kNone, kNone);
+                }
 #pragma unroll
                 for (int b = 0; b < KB; ++b) {
-                    const bool col = 64 * b + 8 * lc < Dk;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const bool live = whole || (col && (ct >> 3) + 32 * j < n);
                         uint32_t* u = reinterpret_cast<uint32_t*>(&x[b][j]);
                         uint4 l;
                         uint32_t* ul = reinterpret_cast<uint32_t*>(&l);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float2 p = live ? phi2(unpack2(u[e])) : norm::both(0.f);
+                            const float2 p = phi2(unpack2(u[e]));
                             zp[b][e] = norm::add2(zp[b][e], p);
                             split2(p, u[e], ul[e]);
                         }

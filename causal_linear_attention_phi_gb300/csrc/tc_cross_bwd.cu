@@ -106,7 +106,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     constexpr uint32_t kCols = kX + 8 <= 256 ? 256 : 512;
     extern __shared__ __align__(1024) uint8_t smem[];
     struct Bars {
-        uint64_t full[4], empty[4], staged, out_free[2], s_full, s_empty, y_done[2], y_free[2], x_ready[2], w_ready[2], r_done[2], sums_done,
+        uint64_t full[4], empty[4], staged, out_free[2], s_full, s_empty, y_done[2], y_free[2], x_ready[4], w_ready[2], r_done[2], sums_done,
             r_flushed, final_mma, final_r;
         uint32_t tmem;
         Span span;
@@ -120,12 +120,12 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         for (int s = 0; s < NS; ++s) {
             mbar_init(&bar->full[s], 1);
             mbar_init(&bar->empty[s], 2);  // R's product and r's
+            mbar_init(&bar->x_ready[s], 8);  // a stage's: a group may be a chunk ahead of R's products where the ring has four
         }
         mbar_init(&bar->staged, 8);
         for (int g = 0; g < 2; ++g) {
             mbar_init(&bar->y_done[g], 1);
             mbar_init(&bar->y_free[g], 8);
-            mbar_init(&bar->x_ready[g], 8);
             mbar_init(&bar->w_ready[g], 8);
             mbar_init(&bar->r_done[g], 1);
             mbar_init(&bar->out_free[g], 1);
@@ -217,9 +217,9 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             ++yi;
         };
         for (int i = 0; i < n && ok; ++i, w.next()) {
-            const int g = i & 1, s = i % NS;
+            const int s = i % NS;
             if (yi <= i) issue_y();
-            ok = ok && warp_wait(&bar->x_ready[g], (i >> 1) & 1, err);
+            ok = ok && warp_wait(&bar->x_ready[s], (i / NS) & 1, err);
             if (first && flushes > 0) ok = ok && warp_wait(&bar->r_flushed, (flushes - 1) & 1, err);
             if (!ok) break;
             tc_fence_after();
@@ -339,7 +339,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     if (KB == 1) *reinterpret_cast<uint4*>(st + SM::kLo + swz(r, lc0 + c)) = l;
                 }
                 fence_proxy_async_smem();
-                warp_arrive(&bar->x_ready[g]);
+                warp_arrive(&bar->x_ready[s]);
                 // t = phi(q) . Y / den
                 ok = warp_wait(&bar->y_done[g], (i >> 1) & 1, err);
                 tc_fence_after();
@@ -455,7 +455,7 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     constexpr uint32_t kCols = 2 * kSet <= 256 ? 256 : 512;
     extern __shared__ __align__(1024) uint8_t smem[];
     struct Bars {
-        uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], dk_staged[2], dv_staged[2], out_free[2], s_full, s_empty, ready[2], k_done[2], v_done[2],
+        uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], dk_staged[4], dv_staged[2], out_free[2], s_full, s_empty, ready[2], k_done[2], v_done[2],
             acc_free[2], final_mma;
         uint32_t tmem;
         Span span;
@@ -471,9 +471,9 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             mbar_init(&bar->k_empty[s], 1);
             mbar_init(&bar->v_full[s], 1);
             mbar_init(&bar->v_empty[s], 1);
+            mbar_init(&bar->dk_staged[s], 8);  // a stage's: a group may be a chunk ahead of the stores where the ring has four
         }
         for (int g = 0; g < 2; ++g) {
-            mbar_init(&bar->dk_staged[g], 8);
             mbar_init(&bar->dv_staged[g], 8);
             mbar_init(&bar->ready[g], 8);
             mbar_init(&bar->k_done[g], 1);
@@ -653,7 +653,7 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                     }
                 }
                 fence_proxy_async_smem();
-                warp_arrive(&bar->dk_staged[g]);
+                warp_arrive(&bar->dk_staged[s]);
                 if (!warp_wait(&bar->v_done[g], (i >> 1) & 1, err)) break;
                 if (KB <= VB && i > 0 && !warp_wait(&bar->out_free[(i - 1) & 1], ((i - 1) >> 1) & 1, err)) break;
                 tc_fence_after();
@@ -705,7 +705,7 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             const uint8_t *own = smem + SM::V0 + s * SM::kV, *out = smem + SM::O0;
             const uint8_t *of_k = KB <= VB ? own : out, *of_v = KB <= VB ? out : own;
             check_copy(0, w.row0(), keys.M, w.bh, keys.heads());
-            if (!mbar_wait(&bar->dk_staged[i & 1], (i >> 1) & 1, err, LA_ERR_TIMEOUT)) break;
+            if (!mbar_wait(&bar->dk_staged[s], (i / NS) & 1, err, LA_ERR_TIMEOUT)) break;
             for (int b = 0; b < KB; ++b) tma_store_3d(&tm_dk, of_k + b * T, 64 * b, w.row0(), w.bh);
             bulk_commit();
             if (!mbar_wait(&bar->dv_staged[i & 1], (i >> 1) & 1, err, LA_ERR_TIMEOUT)) break;

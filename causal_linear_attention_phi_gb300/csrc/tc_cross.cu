@@ -124,8 +124,8 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     mma_ss(acc, desc_mn(st, kk, T), desc_mn(st + SM::kV, kk, T), id, in > 0 || kk > 0);
                     if (KB == 2) mma_ss(acc, desc_mn(lo + i % kLos * 2 * T, kk, T), desc_mn(st + SM::kV, kk, T), id, 1);
                 }
+                if (KB == 2) mma_commit(&bar->lo_free[i % kLos]);  // before empty: see the wait for it
                 mma_commit(&bar->empty[s]);
-                if (KB == 2) mma_commit(&bar->lo_free[i % kLos]);
                 if (close) mma_commit(&bar->acc_done[a]);
             }
             __syncwarp();
@@ -175,6 +175,8 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             if ((i & 1) == group) {
                 const int s = i % NS, n = w.rows();
                 if (!(ok = warp_wait(&bar->full[s], (i / NS) & 1, err))) break;
+                // (this group has skipped the slot's phase before; it is complete, as full is, which waited for chunk i - NS or later)
+                static_assert(NS <= 2 * kLos || KB == 1, "the slot's release before the last is older than this stage's");
                 if (KB == 2 && !(ok = warp_wait(&bar->lo_free[i % kLos], ((i / kLos) & 1) ^ 1, err))) break;
                 uint8_t* st = smem + s * SM::kStage + at;
                 uint8_t* lo = KB == 2 ? smem + SM::lo0 + i % kLos * 2 * T + at : st + T;
@@ -391,7 +393,7 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&bar->s_full[g], 1);
-            mbar_init(&bar->s_empty[g], 1);
+            mbar_init(&bar->s_empty[g], 9);  // the products and the compute warps
             mbar_init(&bar->ready[g], 4);
             mbar_init(&bar->done[g], 1);
         }
@@ -482,10 +484,14 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         bool first = true;
         for (; w.more(); w.next(), ++i) {
             const int h = (first ? heads : heads - 1) % NB;
-            // every head's, whether or not it has a chunk of this group: a wait that skips a phase can be let through by the one before
+            // every head's, whether or not it has a chunk of this group: a wait that skips a phase can be let through by the one
+            // before, and one that the next phase overtakes does not end, so each warp also says when it is through with a head
             if (first && !warp_wait(&bar->s_full[h], (heads++ / NB) & 1, err)) break;
             first = w.last();
-            if ((i & 1) != g) continue;
+            if ((i & 1) != g) {
+                if (first) warp_arrive(&bar->s_empty[h]);
+                continue;
+            }
             const int s = i % NS;
             uint8_t* st = smem + s * SM::kStage;
             const float* zs = reinterpret_cast<const float*>(smem + SM::z0 + h * 256 * KB);
@@ -520,6 +526,7 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(&bar->ready[g]);
+            if (first) warp_arrive(&bar->s_empty[h]);  // z has been read
             if (!warp_wait(&bar->done[g], (i >> 1) & 1, err)) break;
             tc_fence_after();
 #pragma unroll

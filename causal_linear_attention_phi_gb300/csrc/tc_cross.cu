@@ -9,7 +9,7 @@
 // earlier chunks goes on, so tiles come through rings of TMA stages, and two groups of warps (eight each in the sums, four in
 // the answers) work on alternate chunks, one waiting for its product while the other evaluates phi.  phi(k) enters the sums
 // as two bf16 parts, so that S is good to 2^-17 of its terms: dq in the gradient is a small difference of products with S.
-// Measured, of the 6.79 TB/s a copy reaches: sums over 8 heads of 131,071 keys 112 us (0.71), answers to 2,097,152 queries
+// Measured, of the 6.79 TB/s a copy reaches: sums over 8 heads of 131,071 keys 107 us (0.74), answers to 2,097,152 queries
 // of 16 heads 165 us (0.96), both 128 x 128.
 #include <cudaTypedefs.h>
 
@@ -202,7 +202,7 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         uint32_t* ul = reinterpret_cast<uint32_t*>(&l);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float2 p = phi2(unpack2(u[e]));
+                            const float2 p = phi2(u[e]);
                             zp[b][e] = norm::add2(zp[b][e], p);
                             split2(p, u[e], ul[e]);
                         }
@@ -509,7 +509,7 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     norm::Pairs<float>::get(zs + 64 * b + 8 * lc + 4, reinterpret_cast<float2(&)[2]>(zv[2]));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 f = phi2(unpack2(u[e]));
+                        const float2 f = phi2(u[e]);
                         if (kExact) {
                             split2(f, u[e], l[e]);
                             den = norm::fma2(f, zv[e], den);

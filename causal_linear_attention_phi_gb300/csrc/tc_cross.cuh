@@ -77,12 +77,23 @@ __device__ __forceinline__ void check_copy(int x, int row, int rows, int bh, int
     LA_DCHECK((x == 0 || x == 64) && row >= 0 && row < rows && bh >= 0 && bh < heads);
 }
 
-// phi of two values, as phi_f, with the product and the sum of both in one instruction each.
-__device__ __forceinline__ float2 phi2(float2 x) {
-    const float2 t = norm::mul2(make_float2(fminf(x.x, 0.f), fminf(x.y, 0.f)), norm::both(1.4426950408889634f));
-    return norm::add2(make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)), make_float2(ex2_approx(t.x), ex2_approx(t.y)));
-}
 __device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(tc::bf_lo(w), tc::bf_hi(w)); }
+// phi of a pair of bf16, as phi_f: the bounds by 0 are exact in bf16, both in one instruction, and the upper one is added as it
+// is, without conversion (sums over 128 x 64 heads 54.0 us with bounds in fp32, 52.7 so; bounds and conversions share a pipe).
+__device__ __forceinline__ float2 phi2(uint32_t w) {
+    uint32_t low, high;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(low) : "r"(w), "r"(0u));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(high) : "r"(w), "r"(0u));
+    const float2 t = norm::mul2(unpack2(low), norm::both(1.4426950408889634f));
+    float2 p;
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "add.f32.bf16 %0, l, %3;\n\t"
+        "add.f32.bf16 %1, h, %4;\n\t}"
+        : "=f"(p.x), "=f"(p.y)
+        : "r"(high), "f"(ex2_approx(t.x)), "f"(ex2_approx(t.y)));
+    return p;
+}
 __device__ __forceinline__ uint32_t pack2(float2 x) { return pack_bf16x2(x.x, x.y); }
 // hi and lo bf16 parts of two floats.
 __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {

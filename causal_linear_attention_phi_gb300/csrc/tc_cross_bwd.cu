@@ -10,7 +10,7 @@
 // R is two parts, X one (see below).  Bound by memory, then by what passes through shared memory: a chunk of 128 rows, 128
 // wide, is 96 KB (query) or 128 KB (key), 2.2 and 2.9 us of an SM's share of the copy rate, and its products, copies and
 // epilogues move four times that between shared memory and the rest.  Two groups of eight warps take alternate chunks, half
-// a row to a thread.  Measured at B=2 H=16 N=M=32768 128 x 128: query pass 160 us (0.74 of the copy rate), key pass 183 (0.86).
+// a row to a thread.  Measured at B=2 H=16 N=M=32768 128 x 128: query pass 161 us (0.74 of the copy rate), key pass 168 (0.94).
 #include <cudaTypedefs.h>
 
 #include "tc_cross.cuh"
@@ -315,7 +315,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     Pairs<float>::get(zs + c0 + 8 * c + 4, reinterpret_cast<float2(&)[2]>(zv[2]));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        p[4 * c + e] = phi2(unpack2(u[e]));
+                        p[4 * c + e] = phi2(u[e]);
                         s2 = fma2(p[4 * c + e], zv[e], s2);
                     }
                 }
@@ -431,7 +431,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 // K and V have rings of their own, as they are free at different times: K (phi's bf16 copy in place) once its product is
 // through, V, whose product starts as it lands, once dk (KB > VB: dv) has been stored from its place; the other output has a
 // tile of its own.  With both outputs stored from one stage's tiles a stage waited 2,400 cycles for its stores and then
-// 6,500 for its loads, of 14,000 in all (190 us of B=2 H=16 N=32768 128 x 128; now 183).  phi(K) enters dv's product
+// 6,500 for its loads, of 14,000 in all (190 us of B=2 H=16 N=32768 128 x 128 instead of 183).  phi(K) enters dv's product
 // rounded once: its errors are independent from column to column of R, whose entries are not.  phi'(k) is formed from k itself.
 // Two groups of eight warps, half a row to a thread.
 constexpr int kKeyThreads = 640;  // warp 0 TMA loads, 1 MMA, 2-17 two compute groups, 18 TMA stores, 19 zeros behind the lengths
@@ -617,7 +617,7 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                     uint4 x = k[c] = *at;
                     uint32_t* p = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) p[e] = pack2(phi2(unpack2(p[e])));
+                    for (int e = 0; e < 4; ++e) p[e] = pack2(phi2(p[e]));
                     *at = x;
                 }
                 fence_proxy_async_smem();
@@ -641,6 +641,8 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                         Pairs<float>::get(rs + ck + 32 * b + 8 * c + 4, reinterpret_cast<float2(&)[2]>(rr[2]));
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
+                            // formed again, and not as phi2 forms it: the compiler would keep phi2's exponentials, 64
+                            // registers (184 us of B=2 H=16 N=32768 128 x 128 then, 168 so)
                             const float2 low = mul2(make_float2(fminf(bf_lo(kw[e]), 0.f), fminf(bf_hi(kw[e]), 0.f)),
                                                     both(1.4426950408889634f));
                             const float2 slope = make_float2(ex2_approx(low.x), ex2_approx(low.y));

@@ -71,6 +71,8 @@ CASES = [
     (1, 1, 1, 1, 1, 16, 16, F32, None), (1, 2, 2, 17, 64, 16, 16, F32, None), (2, 4, 2, 65, 63, 32, 16, F32, [63, 5]),
     (1, 2, 1, 130, 129, 16, 128, F32, None), (3, 2, 2, 70, 200, 64, 64, F32, [0, 200, 131]),
     (2, 2, 2, 64, 300, 128, 128, F32, [300, 1]), (1, 8, 2, 33, 1000, 128, 32, F32, None), (40, 2, 1, 3, 70, 32, 64, F32, None),
+    (2, 8, 2, 16, 64, 128, 128, F32, [64, 0]), (3, 4, 4, 64, 33, 32, 128, F32, [1, 33, -2]), (2, 4, 2, 33, 64, 64, 32, F32, [64, 63]),
+    (300, 2, 1, 5, 7, 16, 64, F32, None),
     (1, 1, 1, 1, 1, 64, 64, BF16, None), (1, 1, 1, 128, 128, 128, 128, BF16, None), (2, 2, 2, 127, 129, 128, 128, BF16, [129, 64]),
     (2, 4, 2, 200, 63, 64, 64, BF16, [63, 62]), (3, 4, 1, 100, 257, 128, 64, BF16, [0, 257, 128]),
     (1, 2, 2, 300, 700, 64, 128, BF16, None), (2, 2, 1, 77, 190, 32, 16, BF16, [65, 190]), (1, 3, 3, 140, 65, 16, 128, BF16, None),
@@ -172,7 +174,7 @@ def test_refusals(la):
         la.cross_apply(r(2, 4, 8, 32), S, z)
     short = torch.empty(256, dtype=torch.uint8, device=DEV)
     with pytest.raises(la.LaError) as e:
-        la.cross_fwd(q, k, v, workspace=short)
+        la.cross_fwd(q, r(2, 2, 70, 16), r(2, 2, 70, 32), workspace=short)
     assert e.value.status == 3
     assert la.last_error() == 0
 

@@ -12,6 +12,7 @@
 // Measured, of the 6.79 TB/s a copy reaches: sums over 8 heads of 131,071 keys 107 us (0.74), answers to 2,097,152 queries
 // of 16 heads 165 us (0.96), both 128 x 128.
 #include <cudaTypedefs.h>
+#include <float.h>
 
 #include "tc_cross.cuh"
 
@@ -202,9 +203,8 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         uint32_t* ul = reinterpret_cast<uint32_t*>(&l);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float2 p = phi2(u[e]);
-                            zp[b][e] = norm::add2(zp[b][e], p);
-                            split2(p, u[e], ul[e]);
+                            split2(phi2(u[e]), u[e], ul[e]);
+                            zp[b][e] = norm::add2(zp[b][e], norm::add2(unpack2(u[e]), unpack2(ul[e])));
                         }
                         *reinterpret_cast<uint4*>(st + b * T + 4096 * j) = x[b][j];
                         *reinterpret_cast<uint4*>(lo + b * T + 4096 * j) = l;
@@ -272,58 +272,91 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 
 // ------------------------------------------------------------------ join
 // A head's records (or a caller's state) to its image.  kLanes threads share a 16-byte chunk of the image, each taking every
-// kLanes-th record; their sums are added in a fixed order.  The last block of a head does z.
-template <int KB, int VB, int kLanes>
+// kLanes-th record; their sums are added in a fixed order.  The thread of a row's first chunk adds up the row's z, or r.
+//
+// Centred images are the gradient's.  dq = (Y - t z) / den and dk = R v + r are small where the values are alike, and what cancels
+// there, the part of v that all keys have in common, would leave the rounding of S to 16 bits behind.  For any vector c
+//   S' = S - z c^T,  Y' = S' dO,  t' = phi(q) . Y' / den = t - c . dO,  dq = (Y' - t' z) / den phi'(q),
+//   r' = -sum x t',  r = r' - R c,
+// so with c a weighted mean of values, c = S[d,:] / z[d] of the head's first record (one row, of its largest z), the common part
+// is gone before anything is rounded to bf16.  c is kept in the image for the join of (R, r), which subtracts R c with R as the
+// products have it.  c only has to be the same wherever it is used; one that is not finite counts as 0.  (With S itself one key
+// left 10 times the residue that fp32 leaves, and values of 250 times their spread a dq 1.5e-2 off.)
+template <int KB, int VB>
+__device__ __forceinline__ float record_z(const float* p, int d) {
+    p += 128 * 64 * VB + d;
+    return KB == 1 ? p[0] + p[64] : p[0];
+}
+
+template <int KB, int VB, int kLanes, int kMode>
 __global__ void __launch_bounds__(256)
 cross_join_tc(const float* __restrict__ rec, const float* __restrict__ S, const float* __restrict__ z, char* __restrict__ image,
-              float* __restrict__ S_out, float* __restrict__ z_out, Rows rows, int chunk, int ctas, int Dk, int Dv) {
-    constexpr int kChunks = 64 * KB * 8 * VB, kOwn = 256 / kLanes;
+              const char* __restrict__ centre, float* __restrict__ S_out, float* __restrict__ z_out, Rows rows, int chunk, int ctas,
+              int Dk, int Dv) {
+    constexpr int kRow = 8 * VB, kOwn = 256 / kLanes;  // 16-byte chunks of a row; of a block
     __shared__ float part[kLanes > 1 ? kLanes : 1][kLanes > 1 ? kOwn : 1][9];
+    __shared__ float top_z[2 * KB];  // each warp's largest
+    __shared__ int top_d[2 * KB];
     pdl_enter();  // launched with programmatic dependent launch
     const int bh = blockIdx.x, x = threadIdx.x % kOwn, lane = threadIdx.x / kOwn;
     Range g{0, 0};
     if (rec) g = records_of(rows, chunk, bh, ctas);
     char* im = image + (size_t)bh * image_bytes(KB, VB);
-    if (blockIdx.y == kChunks / kOwn) {
-        if (threadIdx.x < 64 * KB) {
-            const int d = threadIdx.x;
-            float a = 0.f;
-            if (!rec)
-                a = d < Dk ? z[(size_t)bh * Dk + d] : 0.f;
-            else
-#pragma unroll 4
-                for (int c = g.first; c <= g.last; ++c) {
-                    const float* p = rec + (size_t)(c + bh) * record_floats(VB) + 128 * 64 * VB + d;
-                    a += KB == 1 ? p[0] + p[64] : p[0];
-                }
-            reinterpret_cast<float*>(im + 2 * image_part(KB, VB))[d] = a;
-            if (z_out && d < Dk) z_out[(size_t)bh * Dk + d] = a;
-        }
-        return;
-    }
     // row d, columns c8 .. c8 + 7
-    const int at = blockIdx.y * kOwn + x, d = at / (8 * VB), c8 = at % (8 * VB) * 8;
-    float v[8];
+    const int at = blockIdx.y * kOwn + x, d = at / kRow, c8 = at % kRow * 8;
+    float v[8], c[8], zs = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
-    auto add = [&](const float* p) {
+    for (int e = 0; e < 8; ++e) v[e] = c[e] = 0.f;
+    auto add = [&](const float* p, float (&to)[8]) {
         const float4 f = *reinterpret_cast<const float4*>(p), h = *reinterpret_cast<const float4*>(p + 4);
-        v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w, v[4] += h.x, v[5] += h.y, v[6] += h.z, v[7] += h.w;
+        to[0] += f.x, to[1] += f.y, to[2] += f.z, to[3] += f.w, to[4] += h.x, to[5] += h.y, to[6] += h.z, to[7] += h.w;
     };
+    auto add_row = [&](const float* p, int row, float (&to)[8]) {  // of a record
+        p += (size_t)row * 64 * VB + c8;
+        add(p, to);
+        if (KB == 1) add(p + 64 * 64 * VB, to);  // the sums of the lo parts
+    };
+    // kCentred: z of the first record, from which its largest is chosen once the sums below are under way
+    const float* first = rec + (size_t)(g.first + bh) * record_floats(VB);
+    const bool keys = !rec || g.first <= g.last;
+    float tz = 0.f;
+    int td = threadIdx.x;
+    if (kMode == kCentred && keys && td < 64 * KB) {
+        if (rec)
+            tz = record_z<KB, VB>(first, td);
+        else if (td < Dk)
+            tz = z[(size_t)bh * Dk + td];
+    }
+    const bool with_z = kMode == kCentred || c8 == 0;
     if (!rec) {
-        if (d < Dk && c8 < Dv) add(S + ((size_t)bh * Dk + d) * Dv + c8);
+        if (d < Dk) {
+            if (c8 < Dv) add(S + ((size_t)bh * Dk + d) * Dv + c8, v);
+            if (with_z) zs = z[(size_t)bh * Dk + d];
+        }
     } else {
 #pragma unroll 4
-        for (int c = g.first + lane; c <= g.last; c += kLanes) {
-            const float* p = rec + (size_t)(c + bh) * record_floats(VB) + (size_t)d * 64 * VB + c8;
-            add(p);
-            if (KB == 1) add(p + 64 * 64 * VB);  // the sums of the lo parts
+        for (int i = g.first + lane; i <= g.last; i += kLanes) {
+            const float* p = rec + (size_t)(i + bh) * record_floats(VB);
+            add_row(p, d, v);
+            if (with_z) zs += record_z<KB, VB>(p, d);
         }
     }
-    if constexpr (kLanes > 1) {
+    if (kMode == kCentred && threadIdx.x < 64 * KB) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float oz = __shfl_xor_sync(0xffffffffu, tz, o);
+            const int od = __shfl_xor_sync(0xffffffffu, td, o);
+            if (oz > tz || (oz == tz && od < td)) tz = oz, td = od;
+        }
+        if ((threadIdx.x & 31) == 0) top_z[threadIdx.x >> 5] = tz, top_d[threadIdx.x >> 5] = td;
+    }
+    if (kLanes > 1) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) part[lane][x][e] = v[e];
-        __syncthreads();
+        part[lane][x][8] = zs;
+    }
+    if (kMode == kCentred || kLanes > 1) __syncthreads();
+    if constexpr (kLanes > 1) {
         if (lane != 0) return;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -331,19 +364,58 @@ cross_join_tc(const float* __restrict__ rec, const float* __restrict__ S, const 
 #pragma unroll
             for (int l = 0; l < kLanes; ++l) v[e] += part[l][x][e];
         }
+        zs = 0.f;
+#pragma unroll
+        for (int l = 0; l < kLanes; ++l) zs += part[l][x][8];
     }
-    uint4 hi, lo;
-    split2(make_float2(v[0], v[1]), hi.x, lo.x);
-    split2(make_float2(v[2], v[3]), hi.y, lo.y);
-    split2(make_float2(v[4], v[5]), hi.z, lo.z);
-    split2(make_float2(v[6], v[7]), hi.w, lo.w);
-    const int off = (c8 >> 6) * (64 * KB * 128) + swz(d, c8 >> 3);
-    *reinterpret_cast<uint4*>(im + off) = hi;
-    *reinterpret_cast<uint4*>(im + image_part(KB, VB) + off) = lo;
     if (S_out && d < Dk && c8 < Dv) {
         float* to = S_out + ((size_t)bh * Dk + d) * Dv + c8;
         *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
         *reinterpret_cast<float4*>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    if constexpr (kMode == kCentred) {
+        tz = top_z[0], td = top_d[0];
+#pragma unroll
+        for (int w = 1; w < 2 * KB; ++w)
+            if (top_z[w] > tz) tz = top_z[w], td = top_d[w];
+        if (tz >= FLT_MIN && tz <= FLT_MAX) {  // else no key, or one of infinity: c stays 0
+            if (rec)
+                add_row(first, td, c);
+            else if (c8 < Dv)
+                add(S + ((size_t)bh * Dk + td) * Dv + c8, c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                c[e] /= tz;
+                if (!(fabsf(c[e]) <= FLT_MAX)) c[e] = 0.f;
+                v[e] = fmaf(-zs, c[e], v[e]);
+            }
+        }
+    }
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split2(make_float2(v[2 * e], v[2 * e + 1]), hi[e], lo[e]);
+    const int off = (c8 >> 6) * (64 * KB * 128) + swz(d, c8 >> 3);
+    *reinterpret_cast<uint4*>(im + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(im + image_part(KB, VB) + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if constexpr (kMode == kGradSums) {  // r = r' - R c
+        const float* cs = image_centre(centre + (size_t)bh * image_bytes(KB, VB), KB, VB) + c8;
+        float2 dot = norm::both(0.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            dot = norm::fma2(norm::add2(unpack2(hi[e]), unpack2(lo[e])), *reinterpret_cast<const float2*>(cs + 2 * e), dot);
+        float s = dot.x + dot.y;
+#pragma unroll
+        for (int o = kRow / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        zs -= s;
+    }
+    if (c8 == 0) {
+        reinterpret_cast<float*>(im + 2 * image_part(KB, VB))[d] = zs;
+        if (z_out && d < Dk) z_out[(size_t)bh * Dk + d] = zs;
+    }
+    if (kMode == kCentred && d == 0) {
+        float* to = image_centre(im, KB, VB) + c8;
+        *reinterpret_cast<float4*>(to) = make_float4(c[0], c[1], c[2], c[3]);
+        *reinterpret_cast<float4*>(to + 4) = make_float4(c[4], c[5], c[6], c[7]);
     }
 }
 
@@ -641,24 +713,29 @@ cudaError_t tc_sums(const void* k, const void* v, const Rows& keys, float* rec, 
     }
 }
 
-cudaError_t tc_join(const float* rec, const float* S, const float* z, char* image, float* S_out, float* z_out, const Rows& rows,
-                    int chunk, int ctas, const la_cross_shape& s, cudaStream_t st) {
+cudaError_t tc_join(JoinMode mode, const float* rec, const float* S, const float* z, char* image, const char* centre, float* S_out,
+                    float* z_out, const Rows& rows, int chunk, int ctas, const la_cross_shape& s, cudaStream_t st) {
     const int KB = blocks64(s.Dk), VB = blocks64(s.Dv);
     // few records to a head: a thread to a chunk; many (few heads): eight, with an eighth of the records each
     const bool many = rec && ctas > 4 * rows.heads();
     auto go = [&](auto kern, int own) {
         launch_begin("cross_join_tc", st);
-        const cudaError_t e = launch_pdl(kern, dim3(rows.heads(), 64 * KB * 8 * VB / own + 1), dim3(256), 0, st, rec, S, z, image, S_out,
-                                         z_out, rows, chunk, ctas, s.Dk, s.Dv);
+        const cudaError_t e = launch_pdl(kern, dim3(rows.heads(), 64 * KB * 8 * VB / own), dim3(256), 0, st, rec, S, z, image, centre,
+                                         S_out, z_out, rows, chunk, ctas, s.Dk, s.Dv);
         const cudaError_t e2 = launch_end("cross_join_tc", st);
         return e != cudaSuccess ? e : e2;
     };
+#define LA_MODES(KB, VB, lanes)                                                        \
+    (mode == kState     ? go(cross_join_tc<KB, VB, lanes, kState>, 256 / (lanes))      \
+     : mode == kCentred ? go(cross_join_tc<KB, VB, lanes, kCentred>, 256 / (lanes))    \
+                        : go(cross_join_tc<KB, VB, lanes, kGradSums>, 256 / (lanes)))
     switch (2 * KB + VB) {
-        case 3: return many ? go(cross_join_tc<1, 1, 8>, 32) : go(cross_join_tc<1, 1, 1>, 256);
-        case 4: return many ? go(cross_join_tc<1, 2, 8>, 32) : go(cross_join_tc<1, 2, 1>, 256);
-        case 5: return many ? go(cross_join_tc<2, 1, 8>, 32) : go(cross_join_tc<2, 1, 1>, 256);
-        default: return many ? go(cross_join_tc<2, 2, 8>, 32) : go(cross_join_tc<2, 2, 1>, 256);
+        case 3: return many ? LA_MODES(1, 1, 8) : LA_MODES(1, 1, 1);
+        case 4: return many ? LA_MODES(1, 2, 8) : LA_MODES(1, 2, 1);
+        case 5: return many ? LA_MODES(2, 1, 8) : LA_MODES(2, 1, 1);
+        default: return many ? LA_MODES(2, 2, 8) : LA_MODES(2, 2, 1);
     }
+#undef LA_MODES
 }
 
 cudaError_t tc_fwd(const FwdArgs& a, const la_cross_shape& s, char* ws, cudaStream_t st) {
@@ -666,12 +743,12 @@ cudaError_t tc_fwd(const FwdArgs& a, const la_cross_shape& s, char* ws, cudaStre
     const Rows keys = key_rows(s, a.lens);
     float* rec = reinterpret_cast<float*>(ws);
     CR_TRY(tc_sums(a.k, a.v, keys, rec, l.sum_ctas, s, st));
-    CR_TRY(tc_join(rec, nullptr, nullptr, ws + l.S, a.S, a.z, keys, kSumRows, l.sum_ctas, s, st));
+    CR_TRY(tc_join(kState, rec, nullptr, nullptr, ws + l.S, nullptr, a.S, a.z, keys, kSumRows, l.sum_ctas, s, st));
     return s.N == 0 ? cudaSuccess : answers(a.q, a.o, ws + l.S, false, s, st);
 }
 
 cudaError_t tc_apply(const void* q, const float* S, const float* z, void* o, const la_cross_shape& s, char* ws, cudaStream_t st) {
-    CR_TRY(tc_join(nullptr, S, z, ws, nullptr, nullptr, grouped_queries(s), kRowChunk, 1, s, st));
+    CR_TRY(tc_join(kState, nullptr, S, z, ws, nullptr, nullptr, nullptr, grouped_queries(s), kRowChunk, 1, s, st));
     return answers(q, o, ws, true, s, st);
 }
 

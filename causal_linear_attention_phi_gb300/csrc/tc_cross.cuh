@@ -6,10 +6,12 @@
 //
 // The state (S, z), and (R, r) of the gradient, pass between kernels as an image: S as two bf16 parts (hi, then lo =
 // S - hi), each a swizzled tile of 64 KB rows by VB blocks as the products' operands want it, then z as 64 KB floats; a
-// block brings it into shared memory with one copy.
+// block brings it into shared memory with one copy.  Behind them 64 VB floats: what a centred image has taken out of S.
 #pragma once
 
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "cross.cuh"
 #include "norm_common.cuh"
@@ -25,7 +27,14 @@ constexpr int kSumRows = 64;   // rows of a chunk of the sums
 constexpr int kRowChunk = 128; // rows of a chunk of the queries, and of the keys in the gradient
 
 constexpr size_t image_part(int KB, int VB) { return (size_t)KB * VB * 8192; }
-constexpr size_t image_bytes(int KB, int VB) { return 2 * image_part(KB, VB) + (size_t)KB * 256; }
+constexpr size_t image_bytes(int KB, int VB) { return 2 * image_part(KB, VB) + (size_t)(KB + VB) * 256; }
+#ifdef __CUDACC__
+template <typename C>  // char or const char
+__device__ __forceinline__ auto image_centre(C* image, int KB, int VB) {
+    using F = std::conditional_t<std::is_const_v<C>, const float, float>;
+    return reinterpret_cast<F*>(image + 2 * image_part(KB, VB) + (size_t)KB * 256);
+}
+#endif
 // A record of the sums: 128 accumulator rows of 64 VB floats, 128 floats of z (KB = 1: the upper 64 of either belong to the
 // lo parts and are added to the lower).
 constexpr size_t record_floats(int VB) { return (size_t)128 * 64 * VB + 128; }
@@ -108,9 +117,11 @@ struct TcLayout {
 };
 TcLayout tc_layout(const la_cross_shape& s, int op);
 
-// Records of the heads, or a caller's state, to images; with S_out the sums also as fp32 state.
-cudaError_t tc_join(const float* rec, const float* S, const float* z, char* image, float* S_out, float* z_out, const Rows& rows,
-                    int chunk, int ctas, const la_cross_shape& s, cudaStream_t st);
+// Records of the heads, or a caller's state, to images; with S_out the sums also as fp32 state.  kState: the forward's, (S, z) as
+// they are; kCentred: the gradient's; kGradSums: (R, r) of sums formed with the centred images `centre`.
+enum JoinMode { kState, kCentred, kGradSums };
+cudaError_t tc_join(JoinMode mode, const float* rec, const float* S, const float* z, char* image, const char* centre, float* S_out,
+                    float* z_out, const Rows& rows, int chunk, int ctas, const la_cross_shape& s, cudaStream_t st);
 cudaError_t tc_sums(const void* k, const void* v, const Rows& keys, float* rec, int ctas, const la_cross_shape& s, cudaStream_t st);
 
 // A kernel that takes nearly all of an SM's shared memory: opted in once for its one size.

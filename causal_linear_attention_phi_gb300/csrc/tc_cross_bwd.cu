@@ -6,8 +6,8 @@
 //
 // t needs no product of its own: dO . (phi(q) S) is phi(q) . (S dO), the row sum that the epilogue of Y forms.  dO and V enter
 // their products as they land, without a pass over them.  dq is a small difference of large terms (the keys' weights vary
-// little), so S enters as two bf16 parts and everything else of dq is fp32; dk keeps a rounding of X's and of R's whole size:
-// R is two parts, X one (see below).  Bound by memory, then by what passes through shared memory: a chunk of 128 rows, 128
+// little), so S enters centred (cross_join_tc; t, r and Y are those of the centred S) and as two bf16 parts, and everything else
+// of dq is fp32; dk keeps a rounding of X's and of R's whole size: R is two parts, X one (see below).  Bound by memory, then by what passes through shared memory: a chunk of 128 rows, 128
 // wide, is 96 KB (query) or 128 KB (key), 2.2 and 2.9 us of an SM's share of the copy rate, and its products, copies and
 // epilogues move four times that between shared memory and the rest.  Two groups of eight warps take alternate chunks, half
 // a row to a thread.  Measured at B=2 H=16 N=M=32768 128 x 128: query pass 161 us (0.74 of the copy rate), key pass 168 (0.94).
@@ -735,10 +735,10 @@ cudaError_t tc_bwd(const BwdArgs& a, const la_cross_shape& s, char* ws, cudaStre
     const Rows keys = key_rows(s, a.lens), rows = grouped_queries(s);
     float* rec = reinterpret_cast<float*>(ws);
     if (a.S) {
-        CR_TRY(tc_join(nullptr, a.S, a.z, ws + l.S, nullptr, nullptr, keys, kSumRows, 1, s, st));
+        CR_TRY(tc_join(kCentred, nullptr, a.S, a.z, ws + l.S, nullptr, nullptr, nullptr, keys, kSumRows, 1, s, st));
     } else {
         CR_TRY(tc_sums(a.k, a.v, keys, rec, l.sum_ctas, s, st));
-        CR_TRY(tc_join(rec, nullptr, nullptr, ws + l.S, nullptr, nullptr, keys, kSumRows, l.sum_ctas, s, st));
+        CR_TRY(tc_join(kCentred, rec, nullptr, nullptr, ws + l.S, nullptr, nullptr, nullptr, keys, kSumRows, l.sum_ctas, s, st));
     }
     CUtensorMap tq, td, tdq, tk, tv, tdk, tdv;
     if (!make_tmap_bf16_rows(&tq, a.q, rows.heads(), rows.M, s.Dk, kRowChunk) ||
@@ -753,7 +753,7 @@ cudaError_t tc_bwd(const BwdArgs& a, const la_cross_shape& s, char* ws, cudaStre
     auto go = [&](auto query, size_t qs, auto key, size_t ks) {
         CR_TRY(tc_run("cross_query_tc", query, dim3(l.query_ctas), kQueryThreads, qs, st, tq, td, tdq, (const char*)ws + l.S, rec, rows,
                       s.Dk, l.query_ctas + rows.heads(), err));
-        CR_TRY(tc_join(rec, nullptr, nullptr, ws + l.R, nullptr, nullptr, rows, kRowChunk, l.query_ctas, s, st));
+        CR_TRY(tc_join(kGradSums, rec, nullptr, nullptr, ws + l.R, ws + l.S, nullptr, nullptr, rows, kRowChunk, l.query_ctas, s, st));
         return tc_run("cross_key_tc", key, dim3(l.key_ctas), kKeyThreads, ks, st, tk, tv, tdk, tdv, (const char*)ws + l.R, (uint4*)a.dk, (uint4*)a.dv,
                       keys, s.Dk, s.Dv, err);
     };

@@ -341,7 +341,7 @@ la_status la_gated_delta_step(const void* q, const void* k, const void* v, const
  * A query whose normaliser is 0 (no key counts) gets an output of 0.
  * S, z: both NULL, or DEVICE fp32 [B,Hk,Dk,Dv] and [B,Hk,Dk] that receive the state (written), from which
  *   la_cross_apply answers further queries and la_cross_bwd takes it back.  o does not depend on whether they are given.
- *   bf16 calls sum phi(k) in two bf16 parts (16 bits and a sign); products and sums are fp32.
+ *   bf16 calls sum phi(k) in two bf16 parts (16 bits and a sign), the same in S and in z; products and sums are fp32.
  * Outputs are buffers of their own (here and in the two calls below).
  * Sizes: Dk and Dv as above, B*H <= 65535, (H / Hk) * N < 2^31 - 128, elements of each tensor < 2^40.  N = 0 or
  * M = 0 is allowed: without keys o, S and z are zero.
@@ -366,7 +366,8 @@ la_status la_cross_fwd(const void* q, const void* k, const void* v, const int* l
  * S, z: both NULL (summed again from k and v), or the state that la_cross_fwd returned for the same k, v and lens.
  * q, dq: [B,H,N,Dk]; k, dk: [B,Hk,M,Dk]; v, dv: [B,Hk,M,Dv]; dout: [B,H,N,Dv]; dq, dk, dv written.
  * A bf16 call enters S, R and phi(k) of the sums as two bf16 parts each (differences of large terms are left in dq
- * and dk), phi(q) / den as one (two for Dk <= 64).
+ * and dk), phi(q) / den as one (two for Dk <= 64).  What the values of a head have in common, which drops out of dq and dk,
+ * is taken out of S in fp32 first: with one key that counts both are 0 to fp32's roundings.
  * Workspace: la_cross_workspace_bytes(LA_OP_CROSS_BWD, s).
  */
 la_status la_cross_bwd(const void* q, const void* k, const void* v, const int* lens, const float* S, const float* z,

@@ -126,6 +126,19 @@ __device__ __forceinline__ Range records_of(const Rows& r, int chunk, int bh, in
     return Range{(int)(((from + 1) * ctas - 1) / total), (int)(((from + n) * ctas - 1) / total)};
 }
 
+// phi_f and dphi_from_phi, but a NaN stays one (fminf and fmaxf take the other operand: phi would be 1).
+__device__ __forceinline__ float min_nan(float x, float y) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ float phi_of(float x) {
+    float high;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(high) : "f"(x), "f"(0.f));
+    return high + ex2_approx(min_nan(x, 0.f) * 1.4426950408889634f);
+}
+__device__ __forceinline__ float slope_of(float phi) { return min_nan(phi, 1.f); }
+
 // 1 / den, and 0 for a query that no key answers.
 __device__ __forceinline__ float over(float den) { return den == 0.f ? 0.f : 1.f / den; }
 #endif

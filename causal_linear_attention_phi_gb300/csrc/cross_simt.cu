@@ -52,7 +52,7 @@ __device__ __forceinline__ void load_rows(float* dst, const float* __restrict__ 
         float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
         if (4 * x < n * D) {
             f = reinterpret_cast<const float4*>(src)[x];
-            if (kPhi) f = make_float4(phi_f(f.x), phi_f(f.y), phi_f(f.z), phi_f(f.w));
+            if (kPhi) f = make_float4(phi_of(f.x), phi_of(f.y), phi_of(f.z), phi_of(f.w));
         }
         reinterpret_cast<float4*>(dst)[x] = f;
     }
@@ -337,7 +337,7 @@ cross_query_kernel(const float* __restrict__ q, const float* __restrict__ dout, 
             const float g = -t * inv[r];
             if (tx == 0) wr[r] = -t;
 #pragma unroll
-            for (int j = 0; j < DK / 16; ++j) Y[i][j] = fmaf(g, zc[j], Y[i][j]) * dphi_from_phi(p[j]);
+            for (int j = 0; j < DK / 16; ++j) Y[i][j] = fmaf(g, zc[j], Y[i][j]) * slope_of(p[j]);
             if (r < w.rows()) store_cols<DK / 16>(dq + (row + r) * DK, tx, Y[i]);
         }
         __syncthreads();
@@ -392,7 +392,7 @@ cross_key_kernel(const float* __restrict__ k, const float* __restrict__ v, const
             float p[DK / 16];
             load_cols<DK / 16>(ks + r * DK, tx, p);
 #pragma unroll
-            for (int j = 0; j < DK / 16; ++j) out[i][j] = (out[i][j] + rc[j]) * dphi_from_phi(p[j]);
+            for (int j = 0; j < DK / 16; ++j) out[i][j] = (out[i][j] + rc[j]) * slope_of(p[j]);
             if (r < w.rows()) {
                 store_cols<DK / 16>(dk + (row + r) * DK, tx, out[i]);
                 store_cols<DV / 16>(dv + (row + r) * DV, tx, ov[i]);

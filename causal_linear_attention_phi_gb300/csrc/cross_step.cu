@@ -60,7 +60,7 @@ cross_few_kernel(const T* __restrict__ q, const float* __restrict__ S, const flo
         const int n = min(kRows, R - base);
 #pragma unroll
         for (int x = 0; x < kQ; ++x)
-            if (tid + x * F::kThreads < n * DK) (&ph[0][0])[tid + x * F::kThreads] = phi_f(qr[x]);
+            if (tid + x * F::kThreads < n * DK) (&ph[0][0])[tid + x * F::kThreads] = phi_of(qr[x]);
         __syncthreads();
         if (base + kRows < R) fetch_q(base + kRows);
         for (int r = warp; r < n; r += F::kWarps) {

@@ -384,7 +384,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                             const int c = 2 * (e + o);
                             const float2 f = p[8 * b + e + o];
                             const float2 d = mul2(fma2(gz, zv[o], mul2(iv, make_float2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])))),
-                                                  make_float2(dphi_from_phi(f.x), dphi_from_phi(f.y)));
+                                                  make_float2(slope_of(f.x), slope_of(f.y)));
                             dq[8 * b + e + o] = pack2(d);
                         }
                     }
@@ -643,7 +643,7 @@ cross_key_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                         for (int e = 0; e < 4; ++e) {
                             // formed again, and not as phi2 forms it: the compiler would keep phi2's exponentials, 64
                             // registers (184 us of B=2 H=16 N=32768 128 x 128 then, 168 so)
-                            const float2 low = mul2(make_float2(fminf(bf_lo(kw[e]), 0.f), fminf(bf_hi(kw[e]), 0.f)),
+                            const float2 low = mul2(make_float2(min_nan(bf_lo(kw[e]), 0.f), min_nan(bf_hi(kw[e]), 0.f)),
                                                     both(1.4426950408889634f));
                             const float2 slope = make_float2(ex2_approx(low.x), ex2_approx(low.y));
                             const float2 d = mul2(norm::add2(make_float2(__uint_as_float(y[8 * c + 2 * e]), __uint_as_float(y[8 * c + 2 * e + 1])),

@@ -338,6 +338,8 @@ la_status la_gated_delta_step(const void* q, const void* k, const void* v, const
  * q: [B,H,N,Dk]; k: [B,Hk,M,Dk]; v: [B,Hk,M,Dv]; o: [B,H,N,Dv] in s.dtype; o written.
  * lens: NULL (all M keys), or DEVICE int32 [B], 4-byte aligned: the keys of each batch entry that count.  Values are
  *   taken as clamped to 0 .. M.  What lies behind a length is never used: it may hold infinities or NaN.
+ *   A NaN that counts stays one: in k it makes its row of the state and its head's outputs NaN, in q its query's output,
+ *   and either the gradients of its head.
  * A query whose normaliser is 0 (no key counts) gets an output of 0.
  * S, z: both NULL, or DEVICE fp32 [B,Hk,Dk,Dv] and [B,Hk,Dk] that receive the state (written), from which
  *   la_cross_apply answers further queries and la_cross_bwd takes it back.  o does not depend on whether they are given.

@@ -74,12 +74,49 @@ __device__ __forceinline__ bool pair_all(int id, bool v) {
 // (hi and lo) of a 16-column operand W, K-major, of whose rows only 8 are held: rows 8-15 of a block are read from the 1 KB
 // behind it (the other block's rows, or z and the barriers) and make columns of the result that nothing reads.
 //
+// R and r stay in tensor memory for kPeriod chunks of a head only, as additions there are cut off (cross_sums_tc): then they are
+// added to the block's record of the head, in fp32 and rounded to nearest.  No registers are free for them; the record is in L2.
+// (131,072 queries in one accumulator: dk and dv 7e-4 short.  B=2 H=16 Hk=4 N=65536 M=131071 128 x 128: 497 us with a period of 32
+// chunks, 473 of 64, 464 without one; B=2 H=16 N=32768: 351, 337, 337.)
+//
 // Two groups of eight warps; a thread holds half a row's phi in fp32 throughout, and the two threads of a row join their parts of
 // den and of t through tensor memory, shared memory being full (a whole row to a thread took 343 us where this took 264:
 // twice the code, of which the instruction cache held half, and two warps to a scheduler).  Registers come from the other
 // warpgroup: 640 threads of 96 are 128 of 56 and 512 of 104.  A chunk's phases, each overlapping the other group's:
 //   phi, den, X -> X^T dO may start;   Y -> t -> X^T t may start;   Y -> dq.
 constexpr int kQueryThreads = 640;  // warp 0 TMA loads, 1 MMA of Y and R, 2 TMA stores, 3 MMA of r, 4-19 two compute groups
+constexpr int kPeriod = 64;
+
+// A walk's periods: where the accumulators of R and r are closed, the last chunk of a head or kPeriod chunks of it.
+struct Period {
+    int in = 0;  // chunks of the period so far
+    __device__ bool close(const Walk& w) {  // whether chunk w ends its period; once for each chunk, in turn
+        const bool c = w.last() || ++in == kPeriod;
+        if (c) in = 0;
+        return c;
+    }
+};
+
+// kCols fp32 columns of a row from tensor memory, written to the row of a record or added to it.
+template <int kCols>
+__device__ __forceinline__ void tmem_row_to_record(uint32_t taddr, float* dst, bool add) {
+#pragma unroll
+    for (int b = 0; b < kCols / 16; ++b) {
+        uint32_t w[16];
+        tmem_ld16(taddr + 16 * b, w);
+        tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 16; x += 4) {
+            float4* to = reinterpret_cast<float4*>(dst + 16 * b + x);
+            float4 f = make_float4(__uint_as_float(w[x]), __uint_as_float(w[x + 1]), __uint_as_float(w[x + 2]), __uint_as_float(w[x + 3]));
+            if (add) {
+                const float4 was = *to;
+                f.x += was.x, f.y += was.y, f.z += was.z, f.w += was.w;
+            }
+            *to = f;
+        }
+    }
+}
 
 template <int KB, int VB>
 struct QuerySmem {
@@ -98,7 +135,7 @@ struct QuerySmem {
 template <int KB, int VB>
 __global__ void __launch_bounds__(kQueryThreads, 1)
 cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-               const __grid_constant__ CUtensorMap tm_dq, const char* __restrict__ image, float* __restrict__ rec, Rows rows, int Dk,
+               const __grid_constant__ CUtensorMap tm_dq, const char* __restrict__ image, float* rec, Rows rows, int Dk,
                int slots, int* err) {
     using SM = QuerySmem<KB, VB>;
     constexpr int NS = SM::kStages;
@@ -132,7 +169,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         mbar_init(&bar->s_full, 1);
         mbar_init(&bar->s_empty, 17);  // the products and the compute warps (z)
-        mbar_init(&bar->sums_done, 2);  // a head's last products of R and of r
+        mbar_init(&bar->sums_done, 2);  // a period's last products of R and of r
         mbar_init(&bar->r_flushed, 8);
         mbar_init(&bar->final_mma, 1);
         mbar_init(&bar->final_r, 1);
@@ -195,6 +232,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         bool ok = true, y_first = true, first = true;
         int yi = 0, heads = 0, flushes = 0;
         Walk wy = w;
+        Period period;
         auto issue_y = [&]() {  // Y of chunk yi: dO is all it needs, so it runs a chunk ahead
             const int g = yi & 1, s = yi % NS;
             if (y_first) ok = ok && warp_wait(&bar->s_full, heads++ & 1, err);
@@ -223,17 +261,17 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (first && flushes > 0) ok = ok && warp_wait(&bar->r_flushed, (flushes - 1) & 1, err);
             if (!ok) break;
             tc_fence_after();
-            const bool last = uniform(w.last());
+            const bool close = uniform(period.close(w));
             if (elect_one()) {
                 const uint32_t st = smem_u32(smem + s * SM::kStage), aD = st + SM::kDo;
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                     mma_ss(t0 + kR, desc_mn(st, kk, T), desc_mn(aD, kk, T), id_r, !first || kk > 0);
                 mma_commit(&bar->empty[s]);
-                if (last) mma_commit(&bar->sums_done);
+                if (close) mma_commit(&bar->sums_done);
             }
             __syncwarp();
-            first = last;
+            first = close;
             if (first) ++flushes;
             // the next chunk's Y (its group's previous chunk, i - 1, is through), unless it needs the next head's S, for
             // which all of this head's chunks have to be through
@@ -252,22 +290,23 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int n = uniform(w.left);
         bool first = true;
         int flushes = 0;
+        Period period;
         for (int i = 0; i < n; ++i, w.next()) {
             const int g = i & 1, s = i % NS;
             if (!warp_wait(&bar->w_ready[g], (i >> 1) & 1, err)) break;
             if (first && flushes > 0 && !warp_wait(&bar->r_flushed, (flushes - 1) & 1, err)) break;
             tc_fence_after();
-            const bool last = uniform(w.last());
+            const bool close = uniform(period.close(w));
             if (elect_one()) {
                 const uint32_t st = smem_u32(smem + s * SM::kStage);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) mma_ss(t0 + kW, desc_mn(st, kk, T), desc_k(aW, kk, 1024), id_w, !first || kk > 0);
                 mma_commit(&bar->empty[s]);
-                if (last) mma_commit(&bar->sums_done);
+                if (close) mma_commit(&bar->sums_done);
                 mma_commit(&bar->r_done[g]);
             }
             __syncwarp();
-            first = last;
+            first = close;
             if (first) ++flushes;
         }
         if (elect_one()) {
@@ -294,12 +333,13 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int c0 = kHalf * half, blk = (c0 >> 6) * T, lc0 = (c0 >> 3) & 7;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, acc = tmem + kY + 64 * KB * g + c0 + lanes;
         const uint32_t sums = tmem + kX + 4 * g + lanes;  // columns: den of either half, t of either half
-        int i = 0, heads = 0;
-        bool first = true, ok = true;
+        int i = 0, heads = 0, flushes = 0;
+        bool first = true, ok = true, begun = false;  // begun: the record holds periods of this head
+        Period period;
         for (; w.more(); w.next(), ++i) {
             // every head's, whether or not it has a chunk of this group
             if (first) ok = warp_wait(&bar->s_full, heads++ & 1, err);
-            const bool last = first = w.last();
+            const bool last = first = w.last(), close = period.close(w);
             if ((i & 1) == g) {
                 const int s = i % NS;
                 uint8_t* st = smem + s * SM::kStage;
@@ -398,22 +438,30 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     *reinterpret_cast<uint4*>(smem + SM::O0 + blk + swz(r, lc0 + c)) = make_uint4(dq[4 * c], dq[4 * c + 1], dq[4 * c + 2], dq[4 * c + 3]);
                 fence_proxy_async_smem();
                 warp_arrive(&bar->staged);
-                // (phases that this group has skipped are complete: this head's S waited for every warp to be through with the last)
-                if (last && !(ok = pair_all(pair, warp_wait(&bar->sums_done, (heads - 1) & 1, err)))) break;
-                if (last) {  // this head's sums
+                if (close) {  // the sums of this period
+                    // The period before may be the other group's, whose additions to the record have to be in.  (Phases that this
+                    // group has skipped are complete: those of earlier heads, as this head's S waited for every warp to be through
+                    // with them; of this head, r_flushed's before the last, as R of the chunk before this one, whose products
+                    // were issued before this chunk's Y, waited for it; sums_done's, as the last of r_flushed follows them.)
+                    const bool in = !begun || warp_wait(&bar->r_flushed, (flushes - 1) & 1, err);
+                    if (!(ok = pair_all(pair, in && warp_wait(&bar->sums_done, flushes & 1, err)))) break;
                     tc_fence_after();
                     if (LA_DCHECK((int)blockIdx.x + w.bh < slots)) {
                         float* out = rec + (size_t)(blockIdx.x + w.bh) * record_floats(VB);
-                        tc::tmem_row_to_global<32 * VB>(tmem + kR + 32 * VB * half + lanes, out + (size_t)r * 64 * VB + 32 * VB * half);
+                        tmem_row_to_record<32 * VB>(tmem + kR + 32 * VB * half + lanes, out + (size_t)r * 64 * VB + 32 * VB * half, begun);
                         uint32_t c[16];
                         tmem_ld16(tmem + kW + lanes, c);
                         tmem_ld_wait();
-                        if (half == 0) out[128 * 64 * VB + r] = __uint_as_float(c[0]) + __uint_as_float(c[1]);
+                        if (half == 0) {
+                            float* to = out + 128 * 64 * VB + r;
+                            *to = (begun ? *to : 0.f) + (__uint_as_float(c[0]) + __uint_as_float(c[1]));
+                        }
                     }
                     tc_fence_before();
                     warp_arrive(&bar->r_flushed);
                 }
             }
+            if (close) ++flushes, begun = !last;
             if (last) {  // z is no longer read
                 warp_arrive(&bar->s_empty);
             }

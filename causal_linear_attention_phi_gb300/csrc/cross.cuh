@@ -7,6 +7,8 @@
 // head) pair whenever either number grows, so block + head numbers the records without gaps that overlap.
 #pragma once
 
+#include <float.h>
+
 #include "la_internal.cuh"
 
 namespace la {
@@ -139,8 +141,9 @@ __device__ __forceinline__ float phi_of(float x) {
 }
 __device__ __forceinline__ float slope_of(float phi) { return min_nan(phi, 1.f); }
 
-// 1 / den, and 0 for a query that no key answers.
-__device__ __forceinline__ float over(float den) { return den == 0.f ? 0.f : 1.f / den; }
+// 1 / den, and 0 for a query that no key answers: whose normaliser is 0, or below the normal numbers (phi is 0 there too; the
+// inverse would overflow, and one such query with it dk and dv of its head).
+__device__ __forceinline__ float over(float den) { return fabsf(den) < FLT_MIN ? 0.f : 1.f / den; }
 #endif
 
 inline long long query_rows(const la_cross_shape& s) { return (long long)(s.H / s.Hk) * s.N; }

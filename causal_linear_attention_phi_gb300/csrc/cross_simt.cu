@@ -355,15 +355,13 @@ cross_query_kernel(const float* __restrict__ q, const float* __restrict__ dout, 
             load_cols<DK / 16>(zs, tx, zc);
 #pragma unroll
             for (int j = 0; j < DK / 16; ++j) {
-                Y[i][j] *= inv[r];
-                t = fmaf(p[j], Y[i][j], t);
+                t = fmaf(p[j], Y[i][j] * inv[r], t);
             }
 #pragma unroll
             for (int x = 8; x > 0; x >>= 1) t += __shfl_xor_sync(0xffffffffu, t, x);  // over the 16 threads of the row
-            const float g = -t * inv[r];
             if (tx == 0) wr[r] = -t;
 #pragma unroll
-            for (int j = 0; j < DK / 16; ++j) Y[i][j] = fmaf(g, zc[j], Y[i][j]) * slope_of(p[j]);
+            for (int j = 0; j < DK / 16; ++j) Y[i][j] = fmaf(-t, zc[j], Y[i][j]) * (inv[r] * slope_of(p[j]));  // t / den could overflow
             if (r < w.rows()) store_cols<DK / 16>(dq + (row + r) * DK, tx, Y[i]);
         }
         __syncthreads();

@@ -12,7 +12,6 @@
 // Measured, of the 6.79 TB/s a copy reaches: sums over 8 heads of 131,071 keys 107 us (0.74), answers to 2,097,152 queries
 // of 16 heads 165 us (0.96), both 128 x 128.
 #include <cudaTypedefs.h>
-#include <float.h>
 
 #include "tc_cross.cuh"
 

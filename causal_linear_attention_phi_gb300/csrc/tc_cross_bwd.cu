@@ -408,7 +408,7 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
                 warp_arrive(&bar->w_ready[g]);
                 // dq, packed until the tile of outputs is free
-                const float2 gz = both(-t * inv), iv = both(inv);
+                const float2 mt = both(-t), iv = both(inv);  // t / den could overflow, inv phi' does not
                 uint32_t dq[kHalf / 2];
 #pragma unroll
                 for (int b = 0; b < 2 * KB; ++b) {
@@ -423,8 +423,8 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         for (int o = 0; o < 2; ++o) {
                             const int c = 2 * (e + o);
                             const float2 f = p[8 * b + e + o];
-                            const float2 d = mul2(fma2(gz, zv[o], mul2(iv, make_float2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])))),
-                                                  make_float2(slope_of(f.x), slope_of(f.y)));
+                            const float2 d = mul2(fma2(mt, zv[o], make_float2(__uint_as_float(y[c]), __uint_as_float(y[c + 1]))),
+                                                  mul2(iv, make_float2(slope_of(f.x), slope_of(f.y))));
                             dq[8 * b + e + o] = pack2(d);
                         }
                     }

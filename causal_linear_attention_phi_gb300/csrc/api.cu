@@ -762,12 +762,19 @@ static la_status check_cross(const la_cross_shape& s) {
     return LA_OK;
 }
 
+// Without heads of queries the keys still have a state and gradients: one head of no queries to each.
+static la_cross_shape without_queries(la_cross_shape s) {
+    if (s.H == 0 && s.Hk > 0) s.H = s.Hk, s.N = 0;
+    return s;
+}
+
 static bool cross_few(const la_cross_shape& s) {
     return !cross::tc_ok(s) ? cross::query_rows(s) <= 16 : cross::query_rows(s) <= 32;
 }
 
 size_t la_cross_workspace_bytes(int op, la_cross_shape s) {
     if (op < LA_OP_CROSS_FWD || op > LA_OP_CROSS_APPLY) return 0;
+    s = without_queries(s);
     if (check_cross(s) != LA_OK || s.B == 0 || s.H == 0) return 0;
     if (op == LA_OP_CROSS_APPLY) return s.N == 0 || cross_few(s) || !cross::tc_ok(s) ? 0 : cross::tc_bytes(s, op);
     if (s.M == 0 || (op == LA_OP_CROSS_BWD && s.N == 0)) return 0;
@@ -784,6 +791,7 @@ static la_status check_state(const float* S, const float* z) {
 la_status la_cross_fwd(const void* q, const void* k, const void* v, const int* lens, void* o, float* S, float* z,
                        la_cross_shape s, void* ws, size_t ws_bytes, la_stream_t stream) {
     t_detail.clear();
+    s = without_queries(s);
     LA_TRY(check_cross(s));
     if (s.B == 0 || s.H == 0 || (s.N == 0 && !S && !z)) return LA_OK;
     LA_TRY(check_device());
@@ -813,6 +821,7 @@ la_status la_cross_bwd(const void* q, const void* k, const void* v, const int* l
                        const void* dout, void* dq, void* dk, void* dv, la_cross_shape s, void* ws, size_t ws_bytes,
                        la_stream_t stream) {
     t_detail.clear();
+    s = without_queries(s);
     LA_TRY(check_cross(s));
     if (s.B == 0 || s.H == 0 || (s.N == 0 && s.M == 0)) return LA_OK;
     LA_TRY(check_device());

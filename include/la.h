@@ -345,8 +345,8 @@ la_status la_gated_delta_step(const void* q, const void* k, const void* v, const
  *   la_cross_apply answers further queries and la_cross_bwd takes it back.  o does not depend on whether they are given.
  *   bf16 calls sum phi(k) in two bf16 parts (16 bits and a sign), the same in S and in z; products and sums are fp32.
  * Outputs are buffers of their own (here and in the two calls below).
- * Sizes: Dk and Dv as above, B*H <= 65535, (H / Hk) * N < 2^31 - 128, elements of each tensor < 2^40.  N = 0 or
- * M = 0 is allowed: without keys o, S and z are zero.
+ * Sizes: Dk and Dv as above, B*H <= 65535, (H / Hk) * N < 2^31 - 128, elements of each tensor < 2^40.  N = 0, H = 0
+ * or M = 0 is allowed: without keys o, S and z are zero.
  * Workspace: la_cross_workspace_bytes(LA_OP_CROSS_FWD, s).
  */
 typedef struct {

@@ -141,6 +141,8 @@ __device__ __forceinline__ float phi_of(float x) {
 }
 __device__ __forceinline__ float slope_of(float phi) { return min_nan(phi, 1.f); }
 
+// A head without keys is one whose z is 0 in every entry: its queries get 0 whatever they hold (0 times a NaN or infinity is not 0).
+
 // 1 / den, and 0 for a query that no key answers: whose normaliser is 0, or below the normal numbers (phi is 0 there too; the
 // inverse would overflow, and one such query with it dk and dv of its head).
 __device__ __forceinline__ float over(float den) { return fabsf(den) < FLT_MIN ? 0.f : 1.f / den; }

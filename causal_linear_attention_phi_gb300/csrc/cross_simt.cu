@@ -233,6 +233,14 @@ __device__ __forceinline__ void inverses(const float* ph, const float* zs, float
     if (part == 0) inv[r] = over(den);
 }
 
+// z of a head to shared memory; whether it has keys.  The whole block.
+template <int DK>
+__device__ __forceinline__ bool load_z(float* zs, const float* __restrict__ z) {
+    const float own = threadIdx.x < DK ? z[threadIdx.x] : 0.f;
+    if (threadIdx.x < DK) zs[threadIdx.x] = own;
+    return __syncthreads_or(own != 0.f);
+}
+
 template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads)
 cross_apply_kernel(const float* __restrict__ q, const float* __restrict__ S, const float* __restrict__ z, float* __restrict__ o,
@@ -241,14 +249,14 @@ cross_apply_kernel(const float* __restrict__ q, const float* __restrict__ S, con
     float *Ss = sm, *ph = Ss + DK * DV, *zs = ph + kChunk * DK, *inv = zs + DK;
     pdl_enter();  // launched with programmatic dependent launch
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    bool first = true;
+    bool first = true, alive = false;
     for (Walk w(rows, kChunk, shared_span(rows, kChunk, false)); w.more(); w.next()) {
         __syncthreads();
         if (first || w.fresh) {
             first = false;
             for (int x = threadIdx.x; x < DK * DV / 4; x += kThreads)
                 reinterpret_cast<float4*>(Ss)[x] = reinterpret_cast<const float4*>(S + (size_t)w.bh * DK * DV)[x];
-            if (threadIdx.x < DK) zs[threadIdx.x] = z[(size_t)w.bh * DK + threadIdx.x];
+            alive = load_z<DK>(zs, z + (size_t)w.bh * DK);
         }
         const size_t row = (size_t)w.bh * rows.M + w.row0();
         LA_DCHECK(w.bh < rows.heads() && w.row0() + w.rows() <= rows.M && w.rows() > 0);
@@ -263,7 +271,7 @@ cross_apply_kernel(const float* __restrict__ q, const float* __restrict__ S, con
             const int r = 4 * ty + i;
             if (r >= w.rows()) break;
 #pragma unroll
-            for (int j = 0; j < DV / 16; ++j) out[i][j] *= inv[r];
+            for (int j = 0; j < DV / 16; ++j) out[i][j] = alive ? out[i][j] * inv[r] : 0.f;
             store_cols<DV / 16>(o + (row + r) * DV, tx, out[i]);
         }
     }
@@ -296,7 +304,7 @@ cross_head_kernel(const float* __restrict__ q, const float* __restrict__ k, cons
     if (threadIdx.x < DK)
         for (int p = 0; p < kChunk; ++p) zc += ks[p * DK + threadIdx.x];
     write_record<DK, DV>(Ss, acc, zc, ty, tx);  // S, and z behind it
-    __syncthreads();
+    const bool alive = __syncthreads_or(zc != 0.f);
     if (S) {
         for (int x = threadIdx.x; x < DK * DV / 4; x += kThreads)
             reinterpret_cast<float4*>(S + (size_t)blockIdx.x * DK * DV)[x] = reinterpret_cast<const float4*>(Ss)[x];
@@ -312,7 +320,7 @@ cross_head_kernel(const float* __restrict__ q, const float* __restrict__ k, cons
         const int r = 4 * ty + i;
         if (r >= queries) break;
 #pragma unroll
-        for (int j = 0; j < DV / 16; ++j) out[i][j] *= inv[r];
+        for (int j = 0; j < DV / 16; ++j) out[i][j] = alive ? out[i][j] * inv[r] : 0.f;
         store_cols<DV / 16>(o + (row + r) * DV, tx, out[i]);
     }
 }
@@ -329,14 +337,14 @@ cross_query_kernel(const float* __restrict__ q, const float* __restrict__ dout, 
     float R[DK / 16][DV / 16], rz = 0.f;
     clear<DK, DV>(R);
     int in = 0;  // chunks of the period so far
-    bool first = true, begun = false;  // begun: the record holds periods of this head
+    bool first = true, alive = false, begun = false;  // begun: the record holds periods of this head
     for (Walk w(rows, kChunk, shared_span(rows, kChunk, false)); w.more(); w.next()) {
         __syncthreads();
         if (first || w.fresh) {
             first = false;
             for (int x = threadIdx.x; x < DK * DV; x += kThreads)
                 St[x] = S[(size_t)w.bh * DK * DV + (x % DK) * DV + x / DK];  // transposed: [dv][dk]
-            if (threadIdx.x < DK) zs[threadIdx.x] = z[(size_t)w.bh * DK + threadIdx.x];
+            alive = load_z<DK>(zs, z + (size_t)w.bh * DK);
         }
         const size_t row = (size_t)w.bh * rows.M + w.row0();
         LA_DCHECK(w.bh < rows.heads() && w.row0() + w.rows() <= rows.M && w.rows() > 0);
@@ -361,7 +369,8 @@ cross_query_kernel(const float* __restrict__ q, const float* __restrict__ dout, 
             for (int x = 8; x > 0; x >>= 1) t += __shfl_xor_sync(0xffffffffu, t, x);  // over the 16 threads of the row
             if (tx == 0) wr[r] = -t;
 #pragma unroll
-            for (int j = 0; j < DK / 16; ++j) Y[i][j] = fmaf(-t, zc[j], Y[i][j]) * (inv[r] * slope_of(p[j]));  // t / den could overflow
+            for (int j = 0; j < DK / 16; ++j)   // t / den could overflow
+                Y[i][j] = alive ? fmaf(-t, zc[j], Y[i][j]) * (inv[r] * slope_of(p[j])) : 0.f;
             if (r < w.rows()) store_cols<DK / 16>(dq + (row + r) * DK, tx, Y[i]);
         }
         __syncthreads();

@@ -52,16 +52,19 @@ cross_few_kernel(const T* __restrict__ q, const float* __restrict__ S, const flo
     fetch_q(0);
 #pragma unroll
     for (int x = 0; x < kZ; ++x) zr[x] = tid + x * F::kThreads < DK ? zh[tid + x * F::kThreads] : 0.f;
+    bool keys = false;  // this thread's z, then the head's
 #pragma unroll
-    for (int x = 0; x < kZ; ++x)
+    for (int x = 0; x < kZ; ++x) {
         if (tid + x * F::kThreads < DK) zs[tid + x * F::kThreads] = zr[x];
+        keys = keys || zr[x] != 0.f;
+    }
     T* oh = o + bh * R * pitch + blockIdx.x * DV;
     for (int base = 0; base < R; base += kRows) {
         const int n = min(kRows, R - base);
 #pragma unroll
         for (int x = 0; x < kQ; ++x)
             if (tid + x * F::kThreads < n * DK) (&ph[0][0])[tid + x * F::kThreads] = phi_of(qr[x]);
-        __syncthreads();
+        keys = __syncthreads_or(keys);
         if (base + kRows < R) fetch_q(base + kRows);
         for (int r = warp; r < n; r += F::kWarps) {
             float den = 0.f;
@@ -96,7 +99,7 @@ cross_few_kernel(const T* __restrict__ q, const float* __restrict__ S, const flo
             float a = 0.f;
 #pragma unroll
             for (int w = 0; w < F::kWarps; ++w) a += part[w][x / DV][x % DV];
-            if (LA_DCHECK(base + x / DV < R)) oh[(size_t)(base + x / DV) * pitch + x % DV] = from_f32<T>(a * inv[x / DV]);
+            if (LA_DCHECK(base + x / DV < R)) oh[(size_t)(base + x / DV) * pitch + x % DV] = from_f32<T>(keys ? a * inv[x / DV] : 0.f);
         }
         __syncthreads();  // before the next rows
     }

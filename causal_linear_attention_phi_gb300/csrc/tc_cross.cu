@@ -552,12 +552,16 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int g = (warp - 2) >> 2, r = 32 * (warp & 3) + lane;
         const uint32_t acc = tmem + 64 * VB * g + ((uint32_t)(32 * (warp & 3)) << 16);
         int i = 0, heads = 0;
-        bool first = true;
+        bool first = true, alive = true;
         for (; w.more(); w.next(), ++i) {
             const int h = (first ? heads : heads - 1) % NB;
+            const float* zs = reinterpret_cast<const float*>(smem + SM::z0 + h * 256 * KB);
             // every head's, whether or not it has a chunk of this group: a wait that skips a phase can be let through by the one
             // before, and one that the next phase overtakes does not end, so each warp also says when it is through with a head
-            if (first && !warp_wait(&bar->s_full[h], (heads++ / NB) & 1, err)) break;
+            if (first) {
+                if (!warp_wait(&bar->s_full[h], (heads++ / NB) & 1, err)) break;
+                alive = any_key<KB>(zs);
+            }
             first = w.last();
             if ((i & 1) != g) {
                 if (first) warp_arrive(&bar->s_empty[h]);
@@ -565,7 +569,6 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             const int s = i % NS;
             uint8_t* st = smem + s * SM::kStage;
-            const float* zs = reinterpret_cast<const float*>(smem + SM::z0 + h * 256 * KB);
             if (!warp_wait(&bar->full[s], (i / NS) & 1, err)) break;
             float2 den = norm::both(0.f);
 #pragma unroll
@@ -612,6 +615,7 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         u[e] = pack2(norm::mul2(make_float2(__uint_as_float(o[8 * c + 2 * e]), __uint_as_float(o[8 * c + 2 * e + 1])), inv));
+                    if (!alive) x = make_uint4(0u, 0u, 0u, 0u);
                     *reinterpret_cast<uint4*>(st + (b >> 1) * T + swz(r, 4 * (b & 1) + c)) = x;
                 }
             }

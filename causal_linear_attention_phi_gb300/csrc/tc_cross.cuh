@@ -86,6 +86,15 @@ __device__ __forceinline__ void check_copy(int x, int row, int rows, int bh, int
     LA_DCHECK((x == 0 || x == 64) && row >= 0 && row < rows && bh >= 0 && bh < heads);
 }
 
+// Whether a head has keys, from its z in shared memory.  A whole warp.
+template <int KB>
+__device__ __forceinline__ bool any_key(const float* zs) {
+    bool some = false;
+#pragma unroll
+    for (int x = 0; x < 2 * KB; ++x) some = some || zs[32 * x + (threadIdx.x & 31)] != 0.f;
+    return __any_sync(0xffffffffu, some);
+}
+
 __device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(tc::bf_lo(w), tc::bf_hi(w)); }
 // phi of a pair of bf16, as phi_of: the bounds by 0 are exact in bf16, both in one instruction, and the upper one is added as it
 // is, without conversion (sums over 128 x 64 heads 54.0 us with bounds in fp32, 52.7 so; bounds and conversions share a pipe).

@@ -433,9 +433,11 @@ cross_query_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 warp_arrive(&bar->y_free[g]);
                 // the tile of outputs is free once the chunk before has been stored
                 if (!(ok = pair_all(pair, i == 0 || warp_wait(&bar->out_free[(i - 1) & 1], ((i - 1) >> 1) & 1, err)))) break;
+                const bool alive = any_key<KB>(zs);  // asked here: kept over the chunk it is a register too many (473 us to 487)
 #pragma unroll
                 for (int c = 0; c < kHalf / 8; ++c)
-                    *reinterpret_cast<uint4*>(smem + SM::O0 + blk + swz(r, lc0 + c)) = make_uint4(dq[4 * c], dq[4 * c + 1], dq[4 * c + 2], dq[4 * c + 3]);
+                    *reinterpret_cast<uint4*>(smem + SM::O0 + blk + swz(r, lc0 + c)) =
+                        alive ? make_uint4(dq[4 * c], dq[4 * c + 1], dq[4 * c + 2], dq[4 * c + 3]) : make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
                 warp_arrive(&bar->staged);
                 if (close) {  // the sums of this period

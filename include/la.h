@@ -340,7 +340,7 @@ la_status la_gated_delta_step(const void* q, const void* k, const void* v, const
  *   taken as clamped to 0 .. M.  What lies behind a length is never used: it may hold infinities or NaN.
  *   A NaN that counts stays one: in k it makes its row of the state and its head's outputs NaN, in q its query's output,
  *   and either the gradients of its head.
- * A query whose normaliser is 0 (no key counts), or less than 2^-126, gets an output of 0.
+ * A query whose normaliser is 0, or less than 2^-126, gets an output of 0; where no key counts it may hold anything.
  * S, z: both NULL, or DEVICE fp32 [B,Hk,Dk,Dv] and [B,Hk,Dk] that receive the state (written), from which
  *   la_cross_apply answers further queries and la_cross_bwd takes it back.  o does not depend on whether they are given.
  *   bf16 calls sum phi(k) in two bf16 parts (16 bits and a sign), the same in S and in z; products and sums are fp32.
@@ -364,7 +364,8 @@ la_status la_cross_fwd(const void* q, const void* k, const void* v, const int* l
  *   dq_i = (y_i - t_i / den_i z) * phi'(q_i),
  *   dk_j = (R v_j + r) * phi'(k_j),  dv_j = R^T phi(k_j)   for j < len_b, 0 behind the length,
  *   R = sum_i phi(q_i) dout_i^T / den_i,  r = -sum_i phi(q_i) t_i / den_i  over the queries of all heads that share the keys.
- * A query whose normaliser is 0, or less than 2^-126, has a gradient of 0 and adds nothing.
+ * A query whose normaliser is 0, or less than 2^-126, has a gradient of 0 and adds nothing; where no key counts it and
+ * its row of dout may hold anything.
  * S, z: both NULL (summed again from k and v), or the state that la_cross_fwd returned for the same k, v and lens.
  * q, dq: [B,H,N,Dk]; k, dk: [B,Hk,M,Dk]; v, dv: [B,Hk,M,Dv]; dout: [B,H,N,Dv]; dq, dk, dv written.
  * A bf16 call enters S, R and phi(k) of the sums as two bf16 parts each (differences of large terms are left in dq

@@ -768,6 +768,10 @@ static la_cross_shape without_queries(la_cross_shape s) {
     return s;
 }
 
+// Few rows to a state: a block keeps its part of the state in registers and each row costs arithmetic; more: tiles of rows, the state in
+// shared memory.  Both sides, of 64 and of 4096 states, us: bf16 128 x 128, 16 rows 13 and 122 against 15 and 199, 32 rows 20 and
+// 217 against 15 and 198; 64 x 64, 32 rows 17 and 73 against 13 and 90; fp32 128 x 128, 16 rows 11 and 113 against 20 and 247, 32 rows 15
+// and 201 against 20 and 260.  Small heads turn earlier: fp32 16 x 16, 17 rows of 2 states 13 against 9.
 static bool cross_few(const la_cross_shape& s) {
     return !cross::tc_ok(s) ? cross::query_rows(s) <= 16 : cross::query_rows(s) <= 32;
 }

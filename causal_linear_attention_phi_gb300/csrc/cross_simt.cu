@@ -498,7 +498,9 @@ cudaError_t join(const float* rec, float* S, float* z, const Rows& rows, int cta
         return run("cross_join", kern, dim3(rows.heads(), (E + 4 * own - 1) / (4 * own)), 0, st, rec, S, z, rows, kChunk, ctas,
                    s.Dk * s.Dv, s.Dk);
     };
-    return ctas > 4 * rows.heads() ? go(cross_join_kernel<8>, 32) : go(cross_join_kernel<1>, 256);
+    // forward of N = M = 65536 / heads with one lane and with eight, us: 64 x 64, 2 heads 81 and 71, 8 73 and 71, 16 71 and 79, 48 71 and
+    // 78; 128 x 128, 2 heads 160 and 149, 8 150 and 150, 16 149 and 152, 48 152 and 160
+    return ctas > 24 * rows.heads() ? go(cross_join_kernel<8>, 32) : go(cross_join_kernel<1>, 256);
 }
 
 template <int DK, int DV>

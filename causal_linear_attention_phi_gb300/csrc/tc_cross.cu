@@ -719,7 +719,9 @@ cudaError_t tc_sums(const void* k, const void* v, const Rows& keys, float* rec, 
 cudaError_t tc_join(JoinMode mode, const float* rec, const float* S, const float* z, char* image, const char* centre, float* S_out,
                     float* z_out, const Rows& rows, int chunk, int ctas, const la_cross_shape& s, cudaStream_t st) {
     const int KB = blocks64(s.Dk), VB = blocks64(s.Dv);
-    // few records to a head: a thread to a chunk; many (few heads): eight, with an eighth of the records each
+    // few records to a head: a thread to a chunk; many (few heads): eight, with an eighth of the records each.  Gradients of N = M =
+    // 262144 / heads with one and with eight, us: 64 x 64, 8 heads 132 and 91, 32 105 and 93, 76 89 and 91, 152 89 and 98; 128 x 128, 8
+    // heads 167 and 144, 32 161 and 162, 38 147 and 153, 152 148 and 194.
     const bool many = rec && ctas > 4 * rows.heads();
     auto go = [&](auto kern, int own) {
         launch_begin("cross_join_tc", st);

@@ -30,6 +30,7 @@ cross_few_kernel(const T* __restrict__ q, const float* __restrict__ S, const flo
     __shared__ float ph[kRows][DK];
     __shared__ __align__(16) float part[F::kWarps][kRows][DV];
     __shared__ float inv[kRows], zs[DK];
+    __shared__ bool keys[kRows];
     pdl_enter();  // launched with programmatic dependent launch
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c4 = tid % F::kCols, r0 = tid / F::kCols;
@@ -52,26 +53,28 @@ cross_few_kernel(const T* __restrict__ q, const float* __restrict__ S, const flo
     fetch_q(0);
 #pragma unroll
     for (int x = 0; x < kZ; ++x) zr[x] = tid + x * F::kThreads < DK ? zh[tid + x * F::kThreads] : 0.f;
-    bool keys = false;  // this thread's z, then the head's
 #pragma unroll
-    for (int x = 0; x < kZ; ++x) {
+    for (int x = 0; x < kZ; ++x)
         if (tid + x * F::kThreads < DK) zs[tid + x * F::kThreads] = zr[x];
-        keys = keys || zr[x] != 0.f;
-    }
     T* oh = o + bh * R * pitch + blockIdx.x * DV;
     for (int base = 0; base < R; base += kRows) {
         const int n = min(kRows, R - base);
 #pragma unroll
         for (int x = 0; x < kQ; ++x)
             if (tid + x * F::kThreads < n * DK) (&ph[0][0])[tid + x * F::kThreads] = phi_of(qr[x]);
-        keys = __syncthreads_or(keys);
+        __syncthreads();
         if (base + kRows < R) fetch_q(base + kRows);
         for (int r = warp; r < n; r += F::kWarps) {
             float den = 0.f;
-            for (int d = lane; d < DK; d += 32) den = fmaf(ph[r][d], zs[d], den);
+            bool some = false;
+            for (int d = lane; d < DK; d += 32) {
+                den = fmaf(ph[r][d], zs[d], den);
+                some = some || zs[d] != 0.f;
+            }
 #pragma unroll
             for (int y = 16; y > 0; y >>= 1) den += __shfl_xor_sync(0xffffffffu, den, y);
-            if (lane == 0) inv[r] = over(den);
+            some = __any_sync(0xffffffffu, some);  // the head has keys
+            if (lane == 0) inv[r] = over(den), keys[r] = some;
         }
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
@@ -99,7 +102,7 @@ cross_few_kernel(const T* __restrict__ q, const float* __restrict__ S, const flo
             float a = 0.f;
 #pragma unroll
             for (int w = 0; w < F::kWarps; ++w) a += part[w][x / DV][x % DV];
-            if (LA_DCHECK(base + x / DV < R)) oh[(size_t)(base + x / DV) * pitch + x % DV] = from_f32<T>(keys ? a * inv[x / DV] : 0.f);
+            if (LA_DCHECK(base + x / DV < R)) oh[(size_t)(base + x / DV) * pitch + x % DV] = from_f32<T>(keys[x / DV] ? a * inv[x / DV] : 0.f);
         }
         __syncthreads();  // before the next rows
     }

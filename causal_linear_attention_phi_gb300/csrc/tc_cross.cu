@@ -277,10 +277,12 @@ cross_sums_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 // there, the part of v that all keys have in common, would leave the rounding of S to 16 bits behind.  For any vector c
 //   S' = S - z c^T,  Y' = S' dO,  t' = phi(q) . Y' / den = t - c . dO,  dq = (Y' - t' z) / den phi'(q),
 //   r' = -sum x t',  r = r' - R c,
-// so with c a weighted mean of values, c = S[d,:] / z[d] of the head's first record (one row, of its largest z), the common part
-// is gone before anything is rounded to bf16.  c is kept in the image for the join of (R, r), which subtracts R c with R as the
-// products have it.  c only has to be the same wherever it is used; one that is not finite counts as 0.  (With S itself one key
-// left 10 times the residue that fp32 leaves, and values of 250 times their spread a dq 1.5e-2 off.)
+// so with c a weighted mean of the head's values, c = S[d,:] / z[d] for one row d, the common part is gone before anything is rounded
+// to bf16.  c is kept in the image for the join of (R, r), which subtracts R c with R as the products have it.  It only has to be
+// the same wherever it is used; one that is not finite counts as 0.  d is a row of no extreme z, the second largest of four: the
+// largest may be a single key's, the smallest a few keys'.  (With S itself one key left 10 times the residue that fp32 leaves,
+// and values of 250 times their spread a dq 1.5e-2 off; with the mean of the first record alone, 131,072 values that grow along the
+// keys a dq 5.9e-3 off instead of 1.7e-3.)
 template <int KB, int VB>
 __device__ __forceinline__ float record_z(const float* p, int d) {
     p += 128 * 64 * VB + d;
@@ -293,9 +295,9 @@ cross_join_tc(const float* __restrict__ rec, const float* __restrict__ S, const 
               const char* __restrict__ centre, float* __restrict__ S_out, float* __restrict__ z_out, Rows rows, int chunk, int ctas,
               int Dk, int Dv) {
     constexpr int kRow = 8 * VB, kOwn = 256 / kLanes;  // 16-byte chunks of a row; of a block
-    __shared__ float part[kLanes > 1 ? kLanes : 1][kLanes > 1 ? kOwn : 1][9];
-    __shared__ float top_z[2 * KB];  // each warp's largest
-    __shared__ int top_d[2 * KB];
+    constexpr bool kC = kMode == kCentred;
+    constexpr int kParts = kC ? 19 : 9;  // v, z, and c, its z; odd
+    __shared__ float part[kLanes > 1 ? kLanes : 1][kLanes > 1 ? kOwn : 1][kParts];
     pdl_enter();  // launched with programmatic dependent launch
     const int bh = blockIdx.x, x = threadIdx.x % kOwn, lane = threadIdx.x / kOwn;
     Range g{0, 0};
@@ -303,7 +305,7 @@ cross_join_tc(const float* __restrict__ rec, const float* __restrict__ S, const 
     char* im = image + (size_t)bh * image_bytes(KB, VB);
     // row d, columns c8 .. c8 + 7
     const int at = blockIdx.y * kOwn + x, d = at / kRow, c8 = at % kRow * 8;
-    float v[8], c[8], zs = 0.f;
+    float v[8], c[8], zs = 0.f, zc = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = c[e] = 0.f;
     auto add = [&](const float* p, float (&to)[8]) {
@@ -315,22 +317,31 @@ cross_join_tc(const float* __restrict__ rec, const float* __restrict__ S, const 
         add(p, to);
         if (KB == 1) add(p + 64 * 64 * VB, to);  // the sums of the lo parts
     };
-    // kCentred: z of the first record, from which its largest is chosen once the sums below are under way
-    const float* first = rec + (size_t)(g.first + bh) * record_floats(VB);
-    const bool keys = !rec || g.first <= g.last;
-    float tz = 0.f;
-    int td = threadIdx.x;
-    if (kMode == kCentred && keys && td < 64 * KB) {
-        if (rec)
-            tz = record_z<KB, VB>(first, td);
-        else if (td < Dk)
-            tz = z[(size_t)bh * Dk + td];
+    int dc = 0;  // the row of c: of four, by the first record's z, the second largest
+    if (kC && (!rec || g.first <= g.last)) {
+        const float* zf = rec ? rec + (size_t)(g.first + bh) * record_floats(VB) : z + (size_t)bh * Dk;
+        float most = -1.f, next = -1.f;
+        int top = 0;
+#pragma unroll
+        for (int i = 1; i < 8; i += 2) {
+            const int r = Dk / 8 * i;
+            const float f = rec ? record_z<KB, VB>(zf, r) : zf[r];
+            if (f > most)
+                next = most, dc = top, most = f, top = r;
+            else if (f > next)
+                next = f, dc = r;
+        }
     }
-    const bool with_z = kMode == kCentred || c8 == 0;
+    const bool with_z = kC || c8 == 0;
     if (!rec) {
+        const float* Sh = S + (size_t)bh * Dk * Dv + c8;
         if (d < Dk) {
-            if (c8 < Dv) add(S + ((size_t)bh * Dk + d) * Dv + c8, v);
+            if (c8 < Dv) add(Sh + (size_t)d * Dv, v);
             if (with_z) zs = z[(size_t)bh * Dk + d];
+        }
+        if (kC) {
+            if (c8 < Dv) add(Sh + (size_t)dc * Dv, c);
+            zc = z[(size_t)bh * Dk + dc];
         }
     } else {
 #pragma unroll 4
@@ -338,56 +349,48 @@ cross_join_tc(const float* __restrict__ rec, const float* __restrict__ S, const 
             const float* p = rec + (size_t)(i + bh) * record_floats(VB);
             add_row(p, d, v);
             if (with_z) zs += record_z<KB, VB>(p, d);
+            if (kC) {
+                add_row(p, dc, c);
+                zc += record_z<KB, VB>(p, dc);
+            }
         }
     }
-    if (kMode == kCentred && threadIdx.x < 64 * KB) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float oz = __shfl_xor_sync(0xffffffffu, tz, o);
-            const int od = __shfl_xor_sync(0xffffffffu, td, o);
-            if (oz > tz || (oz == tz && od < td)) tz = oz, td = od;
-        }
-        if ((threadIdx.x & 31) == 0) top_z[threadIdx.x >> 5] = tz, top_d[threadIdx.x >> 5] = td;
-    }
-    if (kLanes > 1) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) part[lane][x][e] = v[e];
-        part[lane][x][8] = zs;
-    }
-    if (kMode == kCentred || kLanes > 1) __syncthreads();
     if constexpr (kLanes > 1) {
-        if (lane != 0) return;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            v[e] = 0.f;
-#pragma unroll
-            for (int l = 0; l < kLanes; ++l) v[e] += part[l][x][e];
+            part[lane][x][e] = v[e];
+            if (kC) part[lane][x][9 + e] = c[e];
         }
-        zs = 0.f;
+        part[lane][x][8] = zs;
+        if (kC) part[lane][x][17] = zc;
+        __syncthreads();
+        if (lane != 0) return;
+        auto total = [&](int e) {
+            float s = 0.f;
 #pragma unroll
-        for (int l = 0; l < kLanes; ++l) zs += part[l][x][8];
+            for (int l = 0; l < kLanes; ++l) s += part[l][x][e];
+            return s;
+        };
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            v[e] = total(e);
+            if (kC) c[e] = total(9 + e);
+        }
+        zs = total(8);
+        if (kC) zc = total(17);
     }
     if (S_out && d < Dk && c8 < Dv) {
         float* to = S_out + ((size_t)bh * Dk + d) * Dv + c8;
         *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
         *reinterpret_cast<float4*>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
     }
-    if constexpr (kMode == kCentred) {
-        tz = top_z[0], td = top_d[0];
+    if constexpr (kC) {
+        const bool use = zc >= FLT_MIN && zc <= FLT_MAX;  // else no key, or one of infinity
 #pragma unroll
-        for (int w = 1; w < 2 * KB; ++w)
-            if (top_z[w] > tz) tz = top_z[w], td = top_d[w];
-        if (tz >= FLT_MIN && tz <= FLT_MAX) {  // else no key, or one of infinity: c stays 0
-            if (rec)
-                add_row(first, td, c);
-            else if (c8 < Dv)
-                add(S + ((size_t)bh * Dk + td) * Dv + c8, c);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                c[e] /= tz;
-                if (!(fabsf(c[e]) <= FLT_MAX)) c[e] = 0.f;
-                v[e] = fmaf(-zs, c[e], v[e]);
-            }
+        for (int e = 0; e < 8; ++e) {
+            c[e] /= zc;
+            if (!use || !(fabsf(c[e]) <= FLT_MAX)) c[e] = 0.f;
+            v[e] = fmaf(-zs, c[e], v[e]);
         }
     }
     uint32_t hi[4], lo[4];
@@ -411,7 +414,7 @@ cross_join_tc(const float* __restrict__ rec, const float* __restrict__ S, const 
         reinterpret_cast<float*>(im + 2 * image_part(KB, VB))[d] = zs;
         if (z_out && d < Dk) z_out[(size_t)bh * Dk + d] = zs;
     }
-    if (kMode == kCentred && d == 0) {
+    if (kC && d == 0) {
         float* to = image_centre(im, KB, VB) + c8;
         *reinterpret_cast<float4*>(to) = make_float4(c[0], c[1], c[2], c[3]);
         *reinterpret_cast<float4*>(to + 4) = make_float4(c[4], c[5], c[6], c[7]);

@@ -77,3 +77,16 @@ def test_offset_values(la, B, H, Hk, N, M, lengths, Dk, Dv, kept):
     for what, i, part in (("dq", 0, BU), ("dk", 1, (4 if Dk > 64 else 1) * BU), ("dv", 2, 3 * BU)):
         own, off = np.linalg.norm(plain[i] - ref[i]), np.linalg.norm(got[i] - ref[i])
         assert off <= part * np.linalg.norm(ref[i]) + 2 * own, "%s: %.2e off, fp32 %.2e" % (what, off / np.linalg.norm(ref[i]), own / np.linalg.norm(ref[i]))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_that_grow_along_the_keys(la, D):
+    """Many keys whose values are in order: their mean, which is taken out of S, is that of all of them.  What is left of S is two
+    bf16 parts, 2^-16 of it at most; dq is of the order of 1 / sqrt(M) of S without its mean, so 2^-16 * sqrt(131072) = 2^-7.5 in the worst case and a
+    small part of that over the independent roundings of a row; half a step of dq itself bounds both."""
+    q, k, v, do = R.make(1, 1, 1, 64, 131072, D, D, BF16, seed=D)
+    v = v.sort(2)[0]
+    ref = R.bwd(q, k, v, do)[0][0]
+    for kept in (False, True):
+        dq = gradients(la, q, k, v, do, None, kept)[0]
+        assert np.linalg.norm(dq - ref) <= BU * np.linalg.norm(ref), np.linalg.norm(dq - ref) / np.linalg.norm(ref)

@@ -61,6 +61,8 @@ class KernelTime(ctypes.Structure):
 
 _lib = None
 _lock = threading.Lock()
+
+
 class CrossShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("N", ctypes.c_int), ("M", ctypes.c_int),
                 ("Dk", ctypes.c_int), ("Dv", ctypes.c_int), ("dtype", ctypes.c_int)]

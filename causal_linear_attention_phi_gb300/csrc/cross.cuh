@@ -148,6 +148,14 @@ __device__ __forceinline__ float slope_of(float phi) { return min_nan(phi, 1.f);
 __device__ __forceinline__ float over(float den) { return fabsf(den) < FLT_MIN ? 0.f : 1.f / den; }
 #endif
 
+constexpr int kSms = 152;
+inline size_t up(size_t x) { return (x + 255) / 256 * 256; }  // a workspace region's bytes
+#define CR_TRY(x)                            \
+    do {                                     \
+        const cudaError_t e_ = (x);          \
+        if (e_ != cudaSuccess) return e_;    \
+    } while (0)
+
 inline long long query_rows(const la_cross_shape& s) { return (long long)(s.H / s.Hk) * s.N; }
 inline Rows key_rows(const la_cross_shape& s, const int* lens) { return Rows{lens, s.B, s.Hk, s.M}; }
 inline Rows grouped_queries(const la_cross_shape& s) { return Rows{nullptr, s.B * s.Hk, 1, (int)query_rows(s)}; }

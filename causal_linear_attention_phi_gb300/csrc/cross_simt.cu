@@ -1,5 +1,5 @@
-// cross_simt.cu -- CUDA-core kernels of cross attention, forward and gradient (fp32 inputs, where one bf16 or tf32 copy of
-// an operand is not exact enough).  Chunks of 64 rows; 256 threads seen as 16 x 16 (ty, tx), each with a register tile
+// cross_simt.cu -- CUDA-core kernels of cross attention, forward and gradient (fp32 inputs: one bf16 or tf32 copy of an
+// operand is not exact enough; three bf16 parts and six products would be, and are not built).  Chunks of 64 rows; 256 threads seen as 16 x 16 (ty, tx), each with a register tile
 // of the chunk's product; operands are fp32 tiles in shared memory read in 16-byte vectors (rows broadcast, columns
 // 4 tx + 64 j conflict-free).  Sums are fp32; records of a head are added up in a fixed order.
 #include "cross.cuh"
@@ -451,13 +451,12 @@ cross_clear_kernel(char* __restrict__ dk, char* __restrict__ dv, Rows keys, int 
 // ------------------------------------------------------------------ host
 // Blocks: a wave of the SMs or two, or one to a chunk.
 int blocks_for(long long heads, long long rows, int per_sm) {
-    const long long chunks = heads * ((rows + kChunk - 1) / kChunk), most = 152LL * per_sm;
+    const long long chunks = heads * ((rows + kChunk - 1) / kChunk), most = (long long)kSms * per_sm;
     return (int)(chunks < most ? chunks : most);
 }
 int key_blocks(const la_cross_shape& s) { return blocks_for((long long)s.B * s.Hk, s.M, 2); }
 int query_blocks(const la_cross_shape& s) { return blocks_for((long long)s.B * s.Hk, query_rows(s), 1); }
 
-size_t up(size_t x) { return (x + 255) / 256 * 256; }
 struct Layout {
     size_t rec, S, z, R, r, bytes;
 };
@@ -486,11 +485,6 @@ cudaError_t run(const char* name, K kern, dim3 grid, size_t smem, cudaStream_t s
     const cudaError_t e2 = launch_end(name, st);
     return e != cudaSuccess ? e : e2;
 }
-#define CR_TRY(x)                            \
-    do {                                     \
-        const cudaError_t e_ = (x);          \
-        if (e_ != cudaSuccess) return e_;    \
-    } while (0)
 
 cudaError_t join(const float* rec, float* S, float* z, const Rows& rows, int ctas, const la_cross_shape& s, cudaStream_t st) {
     const int E = s.Dk * s.Dv + s.Dk;

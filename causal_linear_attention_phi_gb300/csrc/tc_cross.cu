@@ -8,8 +8,9 @@
 // the copy rate, against 0.35 us for its product.  What it takes to come near is loads in flight while the arithmetic of
 // earlier chunks goes on, so tiles come through rings of TMA stages, and two groups of warps (eight each in the sums, four in
 // the answers) work on alternate chunks, one waiting for its product while the other evaluates phi.  phi(k) enters the sums
-// as two bf16 parts, so that S is good to 2^-17 of its terms: dq in the gradient is a small difference of products with S.
-// Measured, of the 6.79 TB/s a copy reaches: sums over 8 heads of 131,071 keys 107 us (0.74), answers to 2,097,152 queries
+// as two bf16 parts, so that S is good to 2^-17 of its terms: dq in the gradient is a small difference of products with S.  z adds
+// the same parts, so that the two are sums of one phi.
+// Measured, of the 6.79 TB/s a copy reaches: sums over 8 heads of 131,071 keys 105 us (0.75), answers to 2,097,152 queries
 // of 16 heads 165 us (0.96), both 128 x 128.
 #include <cudaTypedefs.h>
 
@@ -425,7 +426,7 @@ cross_join_tc(const float* __restrict__ rec, const float* __restrict__ S, const 
 // A stage holds a chunk of 128 queries: phi(Q) in place for the product, then the outputs for their store.  A thread owns
 // a row.  S (its hi part) and z of the next head are copied while this head's chunks are worked on.  One part of phi(q) and of S
 // is enough for an S that was summed from keys: its rows are alike, so that their roundings and phi's average out over the
-// columns of a head (o is as far off as its own rounding).  A caller's state may be any: kExact forms
+// columns of a head (o is as far off as its own rounding, 1.6 times that where one key outweighs the others).  A caller's state may be any: kExact forms
 // phi_hi S_hi + phi_hi S_lo + phi_lo S_hi (independent entries: 1.8 times as far off without).
 constexpr int kApplyThreads = 352;  // warp 0 TMA loads, 1 MMA, 2-9 two compute groups, 10 TMA stores
 
@@ -646,8 +647,6 @@ cross_apply_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     }
 }
 
-size_t up(size_t x) { return (x + 255) / 256 * 256; }
-constexpr int kSms = 152;
 int ctas_for(long long heads, long long rows, int chunk) {  // a block to an SM, or to a chunk
     const long long chunks = heads * ((rows + chunk - 1) / chunk);
     return (int)(chunks < kSms ? chunks : kSms);

@@ -143,11 +143,6 @@ cudaError_t tc_run(const char* name, K kern, dim3 grid, int threads, size_t smem
     const cudaError_t e2 = launch_end(name, st);
     return e != cudaSuccess ? e : e2;
 }
-#define CR_TRY(x)                            \
-    do {                                     \
-        const cudaError_t e_ = (x);          \
-        if (e_ != cudaSuccess) return e_;    \
-    } while (0)
 
 }  // namespace cross
 }  // namespace la

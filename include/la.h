@@ -343,7 +343,8 @@ la_status la_gated_delta_step(const void* q, const void* k, const void* v, const
  * A query whose normaliser is 0, or less than 2^-126, gets an output of 0; where no key counts it may hold anything.
  * S, z: both NULL, or DEVICE fp32 [B,Hk,Dk,Dv] and [B,Hk,Dk] that receive the state (written), from which
  *   la_cross_apply answers further queries and la_cross_bwd takes it back.  o does not depend on whether they are given.
- *   bf16 calls sum phi(k) in two bf16 parts (16 bits and a sign), the same in S and in z; products and sums are fp32.
+ *   bf16 calls sum phi(k) in two bf16 parts (16 bits and a sign), the same in S and in z; products and sums are fp32.  For o
+ *   they round phi(q) and S once.
  * Outputs are buffers of their own (here and in the two calls below).
  * Sizes: Dk and Dv as above, B*H <= 65535, (H / Hk) * N < 2^31 - 128, elements of each tensor < 2^40.  N = 0, H = 0
  * or M = 0 is allowed: without keys o, S and z are zero.

@@ -340,7 +340,7 @@ la_status la_gated_delta_step(const void* q, const void* k, const void* v, const
  *   taken as clamped to 0 .. M.  What lies behind a length is never used: it may hold infinities or NaN.
  *   A NaN that counts stays one: in k it makes its row of the state and its head's outputs NaN, in q its query's output,
  *   and either the gradients of its head.
- * A query whose normaliser is 0, or less than 2^-126, gets an output of 0; where no key counts it may hold anything.
+ * A query whose normaliser is 0, or below 2^-126 in magnitude, gets an output of 0; where no key counts it may hold anything.
  * S, z: both NULL, or DEVICE fp32 [B,Hk,Dk,Dv] and [B,Hk,Dk] that receive the state (written), from which
  *   la_cross_apply answers further queries and la_cross_bwd takes it back.  o does not depend on whether they are given.
  *   bf16 calls sum phi(k) in two bf16 parts (16 bits and a sign), the same in S and in z; products and sums are fp32.  For o
@@ -365,7 +365,7 @@ la_status la_cross_fwd(const void* q, const void* k, const void* v, const int* l
  *   dq_i = (y_i - t_i / den_i z) * phi'(q_i),
  *   dk_j = (R v_j + r) * phi'(k_j),  dv_j = R^T phi(k_j)   for j < len_b, 0 behind the length,
  *   R = sum_i phi(q_i) dout_i^T / den_i,  r = -sum_i phi(q_i) t_i / den_i  over the queries of all heads that share the keys.
- * A query whose normaliser is 0, or less than 2^-126, has a gradient of 0 and adds nothing; where no key counts it and
+ * A query whose normaliser is 0, or below 2^-126, has a gradient of 0 and adds nothing; where no key counts it and
  * its row of dout may hold anything.
  * S, z: both NULL (summed again from k and v), or the state that la_cross_fwd returned for the same k, v and lens.
  * q, dq: [B,H,N,Dk]; k, dk: [B,Hk,M,Dk]; v, dv: [B,Hk,M,Dv]; dout: [B,H,N,Dv]; dq, dk, dv written.
@@ -381,7 +381,8 @@ la_status la_cross_bwd(const void* q, const void* k, const void* v, const int* l
 /*
  * Queries to a kept state (S, z), which is read, not changed: decoding, one token at a time (N = 1) or several.
  * q: [B,H,N,Dk]; o: [B,H,N,Dv]; S: [B,Hk,Dk,Dv], z: [B,Hk,Dk] fp32.  s.M is ignored.  S may hold any values: a bf16 call
- * multiplies in fp32, or with phi(q) and S in two bf16 parts each.
+ * multiplies in fp32, or with phi(q) and S in two bf16 parts each.  Normalisers count as in la_cross_fwd (a z of 0 in every
+ * entry is that of no key).
  * Workspace: la_cross_workspace_bytes(LA_OP_CROSS_APPLY, s), which is 0 for a few queries.
  */
 la_status la_cross_apply(const void* q, const float* S, const float* z, void* o, la_cross_shape s, void* ws,
